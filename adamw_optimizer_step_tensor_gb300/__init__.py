@@ -6,6 +6,8 @@ it checks dtypes, devices and contiguity, builds the ``adamw_tensor`` list
 and keeps the tensors alive for the plan's lifetime.  Every step of the
 update runs in the library's CUDA kernels; there is no CPU fallback -- if the
 library is missing, importing ``_capi``'s functions raises.
+``FusedTokenLoss`` and ``FusedLayerNorm`` (operators.py) are the losses and the
+layer norm whose gradients the step consumes.
 """
 
 from __future__ import annotations
@@ -19,7 +21,10 @@ from ._capi import (  # noqa: F401
     adamw_plan_destroy,
     adamw_plan_info, adamw_plan_status, adamw_q8_default_maps, adamw_q8_dequant, adamw_q8_quant,
     adamw_q8_set_maps, adamw_step, adamw_step_amp, adamw_step_noalloc, adamw_step_noalloc_status,
-    adamw_wait_selftest,
+    adamw_wait_selftest, adamw_grad_norm, adamw_clip_grads, adamw_loss_plan_create,
+    adamw_loss_plan_destroy, adamw_token_logps, adamw_policy_loss, adamw_preference_loss,
+    adamw_layer_norm_plan_create, adamw_layer_norm_plan_destroy, adamw_layer_norm_forward,
+    adamw_layer_norm_backward,
 )
 
 MODES = {"fp32": _capi.MODE_FP32, "bf16_rem": _capi.MODE_BF16_REM, "q8": _capi.MODE_Q8,
@@ -134,6 +139,19 @@ class FusedAdamW:
     def check_nonfinite(self, found_inf, stream=None) -> None:
         adamw_check_nonfinite(self.plan, _ptr(found_inf), _stream(stream))
 
+    def grad_norm(self, norm, *, max_norm=float("inf"), grad_scale=None, clip_scale=None,
+                  found_inf=None, stream=None) -> None:
+        """Writes the global norm of the (unscaled) grads to ``norm``; the scale that
+        clips them to ``max_norm`` to ``clip_scale`` -- hand it to any step as its
+        ``grad_scale``, or to ``clip_grads`` -- and 1 to ``found_inf`` if the norm is
+        not finite.  float32 CUDA scalar tensors."""
+        adamw_grad_norm(self.plan, max_norm, _ptr(grad_scale), _ptr(norm), _ptr(clip_scale),
+                        _ptr(found_inf), _stream(stream))
+
+    def clip_grads(self, clip_scale, stream=None) -> None:
+        """Divides the plan's grads by ``clip_scale`` in place."""
+        adamw_clip_grads(self.plan, _ptr(clip_scale), _stream(stream))
+
     def step(self, lr, step, *, betas=(0.9, 0.999), eps=1e-8, grad_scale=None, found_inf=None,
              stream=None) -> None:
         """lr: float32 CUDA scalar tensor; step: int32 CUDA scalar (completed steps)."""
@@ -186,3 +204,11 @@ class FusedAdamW:
             self.close()
         except Exception:
             pass
+
+
+def __getattr__(name):
+    # operators.py imports torch; the ctypes binding alone does not need it
+    if name in ("FusedTokenLoss", "FusedLayerNorm"):
+        from . import operators
+        return getattr(operators, name)
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -47,7 +47,63 @@ class adamw_tensor(ctypes.Structure):
     ]
 
 
+class adamw_logits(ctypes.Structure):
+    _fields_ = [
+        ("logits", _vp),
+        ("labels", _vp),
+        ("rows", ctypes.c_int64),
+        ("row_stride", ctypes.c_int64),
+        ("vocab", ctypes.c_int32),
+        ("label_bytes", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("temperature", ctypes.c_float),
+    ]
+
+
+class adamw_policy(ctypes.Structure):
+    _fields_ = [
+        ("weights", _vp),
+        ("advantages", _vp),
+        ("old_logps", _vp),
+        ("ref_logps", _vp),
+        ("clip_low", ctypes.c_float),
+        ("clip_high", ctypes.c_float),
+        ("kl_coef", ctypes.c_float),
+        ("grad_scale_dev", _vp),
+    ]
+
+
+class adamw_preference(ctypes.Structure):
+    _fields_ = [
+        ("weights", _vp),
+        ("ref_logps", _vp),
+        ("seq_starts", _vp),
+        ("n_pairs", ctypes.c_int32),
+        ("beta", ctypes.c_float),
+        ("label_smoothing", ctypes.c_float),
+        ("grad_scale_dev", _vp),
+    ]
+
+
 _SIGNATURES = {
+    "adamw_grad_norm": (ctypes.c_int, [_vp, ctypes.c_float, _vp, _vp, _vp, _vp, _vp]),
+    "adamw_clip_grads": (ctypes.c_int, [_vp, _vp, _vp]),
+    "adamw_loss_plan_create": (ctypes.c_int, [ctypes.c_int64, ctypes.c_int32, ctypes.POINTER(_vp)]),
+    "adamw_loss_plan_destroy": (ctypes.c_int, [_vp]),
+    "adamw_token_logps": (ctypes.c_int, [_vp, ctypes.POINTER(adamw_logits), _vp, _vp, _vp]),
+    "adamw_policy_loss": (ctypes.c_int, [_vp, ctypes.POINTER(adamw_logits), ctypes.POINTER(adamw_policy),
+                                         _vp, _vp, _vp, ctypes.c_int64, _vp]),
+    "adamw_preference_loss": (ctypes.c_int, [_vp, ctypes.POINTER(adamw_logits),
+                                             ctypes.POINTER(adamw_preference), _vp, _vp, _vp, _vp,
+                                             ctypes.c_int64, _vp]),
+    "adamw_layer_norm_plan_create": (ctypes.c_int, [ctypes.c_int32, ctypes.c_float, ctypes.POINTER(_vp)]),
+    "adamw_layer_norm_plan_destroy": (ctypes.c_int, [_vp]),
+    "adamw_layer_norm_forward": (ctypes.c_int, [_vp, ctypes.c_int, ctypes.c_int, ctypes.c_int64, _vp,
+                                                ctypes.c_int64, _vp, _vp, _vp, ctypes.c_int64, _vp, _vp,
+                                                _vp]),
+    "adamw_layer_norm_backward": (ctypes.c_int, [_vp, ctypes.c_int, ctypes.c_int, ctypes.c_int64, _vp,
+                                                 ctypes.c_int64, _vp, ctypes.c_int64, _vp, _vp, _vp, _vp,
+                                                 ctypes.c_int64, _vp, _vp, _vp]),
     "adamw_plan_create": (ctypes.c_int, [ctypes.POINTER(adamw_tensor), ctypes.c_int32, ctypes.c_int,
                                          ctypes.c_int, ctypes.POINTER(_vp)]),
     "adamw_mini_plan_create": (ctypes.c_int, [ctypes.POINTER(adamw_tensor), ctypes.POINTER(ctypes.c_int64),
@@ -290,3 +346,65 @@ def adamw_q4_dequant(plan: int, which: int, codes: int, absmax: int, out: int, n
 def adamw_q4_quant(plan: int, which: int, x: int, codes: int, absmax: int, n: int,
                    stream: int | None) -> None:
     _check(load().adamw_q4_quant(plan, which, x, codes, absmax, n, stream))
+
+
+def adamw_grad_norm(plan: int, max_norm: float, grad_scale_dev: int | None, norm_dev: int,
+                    clip_scale_dev: int | None, found_inf_dev: int | None, stream: int | None) -> None:
+    _check(load().adamw_grad_norm(plan, max_norm, grad_scale_dev, norm_dev, clip_scale_dev,
+                                  found_inf_dev, stream))
+
+
+def adamw_clip_grads(plan: int, clip_scale_dev: int, stream: int | None) -> None:
+    _check(load().adamw_clip_grads(plan, clip_scale_dev, stream))
+
+
+def adamw_loss_plan_create(max_rows: int, max_pairs: int) -> int:
+    out = _vp()
+    _check(load().adamw_loss_plan_create(max_rows, max_pairs, ctypes.byref(out)))
+    return out.value
+
+
+def adamw_loss_plan_destroy(plan: int) -> None:
+    _check(load().adamw_loss_plan_destroy(plan))
+
+
+def adamw_token_logps(plan: int, z: adamw_logits, logps: int, lse: int | None,
+                      stream: int | None) -> None:
+    _check(load().adamw_token_logps(plan, z, logps, lse, stream))
+
+
+def adamw_policy_loss(plan: int, z: adamw_logits, p: adamw_policy, stats: int, logps: int,
+                      dlogits: int | None, dlogits_stride: int, stream: int | None) -> None:
+    _check(load().adamw_policy_loss(plan, z, p, stats, logps, dlogits, dlogits_stride, stream))
+
+
+def adamw_preference_loss(plan: int, z: adamw_logits, p: adamw_preference, stats: int, rewards: int,
+                          logps: int, dlogits: int | None, dlogits_stride: int,
+                          stream: int | None) -> None:
+    _check(load().adamw_preference_loss(plan, z, p, stats, rewards, logps, dlogits, dlogits_stride,
+                                        stream))
+
+
+def adamw_layer_norm_plan_create(width: int, eps: float) -> int:
+    out = _vp()
+    _check(load().adamw_layer_norm_plan_create(width, eps, ctypes.byref(out)))
+    return out.value
+
+
+def adamw_layer_norm_plan_destroy(plan: int) -> None:
+    _check(load().adamw_layer_norm_plan_destroy(plan))
+
+
+def adamw_layer_norm_forward(plan: int, dtype: int, weight_dtype: int, rows: int, x: int, x_stride: int,
+                             weight: int | None, bias: int | None, y: int, y_stride: int, mean: int,
+                             rstd: int, stream: int | None) -> None:
+    _check(load().adamw_layer_norm_forward(plan, dtype, weight_dtype, rows, x, x_stride, weight, bias, y,
+                                           y_stride, mean, rstd, stream))
+
+
+def adamw_layer_norm_backward(plan: int, dtype: int, weight_dtype: int, rows: int, dy: int,
+                              dy_stride: int, x: int, x_stride: int, weight: int | None, mean: int,
+                              rstd: int, dx: int, dx_stride: int, dweight: int | None,
+                              dbias: int | None, stream: int | None) -> None:
+    _check(load().adamw_layer_norm_backward(plan, dtype, weight_dtype, rows, dy, dy_stride, x, x_stride,
+                                            weight, mean, rstd, dx, dx_stride, dweight, dbias, stream))

@@ -9,6 +9,7 @@
 #include <vector>
 
 #include "entry_checks.h"
+#include "plan.h"
 
 namespace adamw {
 void default_maps(float smap[256], float umap[256]);
@@ -24,55 +25,11 @@ int zero_code_of(const float* value, int n);
 
 using namespace adamw;
 
-struct adamw_plan {
-  int device = -1;
-  adamw_mode mode = ADAMW_MODE_FP32;
-  adamw_dtype gdt = ADAMW_F32;
-  int32_t n_tensors = 0;
-  int64_t total_numel = 0;
-  int64_t n_chunks = 0;
-  int grid = 1;
-  int block_threads = kThreads;   // threads per CTA of the step kernel
-  int grid_check = 1;
-  TensorDesc* d_tensors = nullptr;
-  Chunk* d_chunks = nullptr;
-  StepScratch* d_scratch = nullptr;
-  QTables* d_qt = nullptr;
-  int refine = 1;              // Q8: thresholds per bucket lookup of the current maps
-  bool bulk = false;           // launch the bulk-staged step kernel
-  // fused check + step (adamw_step_amp): its own chunk table, sized for its own
-  // co-resident grid (fp32 and bf16+remainder plans only)
-  Chunk* d_chunks_fused = nullptr;
-  int64_t n_chunks_fused = 0;
-  int grid_fused = 0;
-  bool has_slow = false;       // every tensor carries an AdEMAMix slow EMA
-  bool has_v = true;           // every tensor carries exp_avg_sq (false: Lion-only plan)
-  int grid_sqrt_div = 1;       // grid of the RMSprop / Adagrad kernels (2 CTAs per SM)
-  // Adam-mini plans (adamw_mini_plan_create): blocks sharing one v
-  bool mini = false;
-  int64_t n_blocks = 0, n_red = 0;
-  int grid_red = 1;
-  // plans small enough to sit in shared memory whole (small_kernels.cu): the
-  // tensor table as kernel parameters, one piece of one tensor per CTA
-  bool small = false;
-  bool small_fused = false;    // adamw_step_amp takes the fused small path too
-  SmallArgs small_args{};
-  int small_grid = 0;
-  int small_smem = 0;
-  int small_smem_fused = 0;
-  MiniBlock* d_blocks = nullptr;
-  int32_t* d_chunk_blk = nullptr;
-  int64_t* d_red_chunks = nullptr;
-  double* d_partial = nullptr;
-  uint32_t* d_arrived = nullptr;
-  float* d_blk_r = nullptr;
-};
-
 namespace {
-
 thread_local std::string g_err;
+}  // namespace
 
-adamw_status fail(adamw_status st, const char* fmt, ...) {
+adamw_status adamw::fail(adamw_status st, const char* fmt, ...) {
   char buf[512];
   va_list ap;
   va_start(ap, fmt);
@@ -82,11 +39,21 @@ adamw_status fail(adamw_status st, const char* fmt, ...) {
   return st;
 }
 
-adamw_status cuda_fail(cudaError_t e, const char* what) {
+adamw_status adamw::cuda_fail(cudaError_t e, const char* what) {
   return fail(ADAMW_ECUDA, "%s: %s (%s)", what, cudaGetErrorName(e), cudaGetErrorString(e));
 }
 
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+adamw_status adamw::check_current_device(int device, const char* what) {
+  int dev = -1;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+  if (dev != device)
+    return fail(ADAMW_EINVAL, "%s was created on device %d but device %d is current", what, device,
+                dev);
+  return ADAMW_OK;
+}
+
+namespace {
 
 size_t dtype_size(adamw_dtype d) { return d == ADAMW_F32 ? 4 : 2; }
 
@@ -115,18 +82,11 @@ void free_plan(adamw_plan* p) {
   cudaFree(p->d_partial);
   cudaFree(p->d_arrived);
   cudaFree(p->d_blk_r);
+  cudaFree(p->d_norm);
   delete p;
 }
 
-adamw_status check_device(const adamw_plan* p) {
-  int dev = -1;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
-  if (dev != p->device)
-    return fail(ADAMW_EINVAL, "plan was created on device %d but device %d is current",
-                p->device, dev);
-  return ADAMW_OK;
-}
+adamw_status check_device(const adamw_plan* p) { return check_current_device(p->device, "plan"); }
 
 // Checks every step entry point shares: the plan, then the run-time scalars.
 adamw_status check_step(const adamw_plan* plan, const float* lr_dev, const int32_t* step_dev,
@@ -420,6 +380,15 @@ static adamw_status create_plan(const adamw_tensor* tensors, int32_t n_tensors, 
     return cuda_fail(e, "upload chunk table");
   if ((e = cudaMemset(p->d_scratch, 0, sizeof(StepScratch))) != cudaSuccess)
     return cuda_fail(e, "clear step scratch");
+  // the gradient norm: one float64 partial sum per CTA, then the ticket word
+  p->grid_norm = static_cast<int>(p->n_chunks < kNormCtasPerSm * static_cast<int64_t>(sms)
+                                      ? (p->n_chunks > 0 ? p->n_chunks : 1)
+                                      : kNormCtasPerSm * static_cast<int64_t>(sms));
+  const size_t norm_bytes = static_cast<size_t>(p->grid_norm + 1) * sizeof(double);
+  if ((e = cudaMalloc(&p->d_norm, norm_bytes)) != cudaSuccess)
+    return fail(ADAMW_ENOMEM, "cudaMalloc(norm partial sums): %s", cudaGetErrorString(e));
+  if ((e = cudaMemset(p->d_norm, 0, norm_bytes)) != cudaSuccess)
+    return cuda_fail(e, "clear norm partial sums");
   if (v_block) {
     p->mini = true;
     p->n_blocks = static_cast<int64_t>(blocks.size());

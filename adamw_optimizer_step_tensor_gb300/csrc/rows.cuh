@@ -1,0 +1,75 @@
+// rows.cuh -- device pieces shared by the row kernels (token_loss.cu,
+// layer_norm.cu): element types and the fixed-order sum across a grid's CTAs.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <cstdint>
+#include <type_traits>
+
+namespace adamw {
+namespace {
+
+constexpr uint32_t kFull = 0xFFFFFFFFu;
+
+__device__ __forceinline__ float to_f32(float x) { return x; }
+__device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
+
+// Rounds once, to nearest even.
+template <typename T>
+__device__ __forceinline__ T from_f32(float x) {
+  if constexpr (std::is_same<T, float>::value) return x;
+  else if constexpr (std::is_same<T, __half>::value) return __float2half_rn(x);
+  else return __float2bfloat16_rn(x);
+}
+
+// Sum over the CTA's threads, the same value in every thread.
+template <int THREADS>
+__device__ __forceinline__ float block_sum(float x, float* s_warp) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(kFull, x, o);
+  if (THREADS == 32) return x;
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) s_warp[threadIdx.x >> 5] = x;
+  __syncthreads();
+  float t = 0.0f;
+#pragma unroll
+  for (int i = 0; i < THREADS / 32; ++i) t += s_warp[i];
+  return t;
+}
+
+// Every CTA leaves four float64 sums; the last one to finish adds them in CTA
+// order (the same bits whatever the order of arrival) and returns true with
+// the totals in `out`, for its thread 0.  Call with the CTA's sums in thread 0.
+__device__ __forceinline__ bool last_cta_sums(const double (&mine)[4], double* partial,
+                                              uint32_t* ticket, double (&out)[4]) {
+  bool last = false;
+  if (threadIdx.x == 0) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) partial[4 * blockIdx.x + i] = mine[i];
+    __threadfence();
+    last = atomicAdd(ticket, 1u) == gridDim.x - 1;
+  }
+  if (!__syncthreads_or(last)) return false;
+  __threadfence();
+  if (threadIdx.x < 32) {
+    double t[4] = {0.0, 0.0, 0.0, 0.0};
+    for (unsigned c = threadIdx.x; c < gridDim.x; c += 32) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) t[i] += __ldcg(partial + 4 * c + i);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) t[i] += __shfl_xor_sync(kFull, t[i], o);
+      out[i] = t[i];
+    }
+    if (threadIdx.x == 0) atomicExch(ticket, 0u);
+  }
+  return threadIdx.x == 0;
+}
+
+}  // namespace
+}  // namespace adamw

@@ -1,0 +1,247 @@
+"""Losses on token log-probabilities, and layer norm, with torch tensors in place of raw pointers.
+
+``FusedTokenLoss`` scores tokens, and gives the clipped policy loss and the
+preference loss with the gradient of the logits.  ``FusedLayerNorm`` is layer
+norm forward and backward with the gradients of its weight and bias.  Both hold
+a plan of the library (its workspace) on the current device, check their
+arguments and launch on the current stream or ``stream``; all arithmetic runs in
+the library's CUDA kernels.
+"""
+
+from __future__ import annotations
+
+import torch
+
+from . import _capi
+
+_DTYPES = {torch.float32: _capi.F32, torch.float16: _capi.F16, torch.bfloat16: _capi.BF16}
+_LABEL_BYTES = {torch.int32: 4, torch.int64: 8}
+
+
+def _stream(stream):
+    if stream is None:
+        return torch.cuda.current_stream().cuda_stream
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
+
+
+def _rows(name, t, dtype=None, shape=None):
+    """Checks a matrix of rows (the last axis contiguous) and returns its row stride."""
+    if not t.is_cuda or t.dim() != 2:
+        raise ValueError(f"{name} must be a CUDA matrix")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    rows, width = t.shape
+    if width > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must be contiguous along its last axis")
+    if rows < 2:
+        return width
+    stride = t.stride(0)
+    if stride < width:
+        raise ValueError(f"{name} has overlapping rows")
+    return stride
+
+
+def _vector(name, t, n, dtype=torch.float32):
+    """Address of a contiguous CUDA vector of n elements; None stays None."""
+    if t is None:
+        return None
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_cuda or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA tensor of {n} elements")
+    return t.data_ptr()
+
+
+class _Plan:
+    _destroy = None
+
+    def close(self) -> None:
+        if getattr(self, "plan", None):
+            self._destroy(self.plan)
+            self.plan = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class FusedTokenLoss(_Plan):
+    """Losses on the log-probability of one token per row of logits.
+
+    ``max_rows`` rows per call at most; ``max_pairs`` pairs for ``preference``.
+    logits [rows, vocab] float32, float16 or bfloat16, any row stride; labels
+    int32 or int64 [rows], a label outside [0, vocab) (such as -100) marks a row
+    that counts for nothing; per-row inputs and outputs float32 [rows].
+    """
+
+    _destroy = staticmethod(_capi.adamw_loss_plan_destroy)
+
+    def __init__(self, max_rows: int, max_pairs: int = 0):
+        self.plan = _capi.adamw_loss_plan_create(int(max_rows), int(max_pairs))
+        self._z = _capi.adamw_logits()
+        self._policy = _capi.adamw_policy()
+        self._preference = _capi.adamw_preference()
+
+    def _logits(self, logits, labels, temperature):
+        if logits.dtype not in _DTYPES:
+            raise TypeError(f"unsupported logits dtype {logits.dtype}")
+        if labels.dtype not in _LABEL_BYTES:
+            raise TypeError(f"labels must be int32 or int64, got {labels.dtype}")
+        z = self._z
+        z.row_stride = _rows("logits", logits)
+        z.rows, z.vocab = logits.shape
+        z.labels = _vector("labels", labels, logits.shape[0], labels.dtype)
+        z.logits = logits.data_ptr()
+        z.label_bytes = _LABEL_BYTES[labels.dtype]
+        z.dtype = _DTYPES[logits.dtype]
+        z.temperature = temperature
+        return z
+
+    @staticmethod
+    def _gradient(logits, dlogits, backward):
+        if not backward:
+            return None, None, 0
+        if dlogits is None:
+            dlogits = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+        return dlogits, dlogits.data_ptr(), _rows("dlogits", dlogits, logits.dtype, logits.shape)
+
+    def logps(self, logits, labels, *, temperature=1.0, logps=None, lse=None, stream=None):
+        """(logps, lse) of every row: the log-probability of its token and the log of its sum of
+        exponentials, 0 where the row has no token."""
+        z = self._logits(logits, labels, temperature)
+        n = logits.shape[0]
+        if logps is None:
+            logps = torch.empty(n, dtype=torch.float32, device=logits.device)
+        if lse is None:
+            lse = torch.empty(n, dtype=torch.float32, device=logits.device)
+        _capi.adamw_token_logps(self.plan, z, _vector("logps", logps, n), _vector("lse", lse, n),
+                                _stream(stream))
+        return logps, lse
+
+    def policy(self, logits, labels, weights, advantages, old_logps=None, ref_logps=None, *,
+               clip=(0.2, 0.2), kl_coef=0.0, temperature=1.0, grad_scale=None, backward=True,
+               stats=None, logps=None, dlogits=None, stream=None):
+        """Clipped policy loss with a KL term: (stats, logps, dlogits).
+
+        stats float32 [4]: the loss (sum of weights times rows' terms), its policy part, the KL
+        sum, the weight of the clipped rows.  ``weights`` is the mask already divided by whatever
+        the mean runs over.  dlogits (None when ``backward`` is false) is the gradient of
+        stats[0], times ``grad_scale``; it may be given, also as the logits themselves.
+        """
+        z = self._logits(logits, labels, temperature)
+        n = logits.shape[0]
+        p = self._policy
+        p.weights = _vector("weights", weights, n)
+        p.advantages = _vector("advantages", advantages, n)
+        p.old_logps = _vector("old_logps", old_logps, n)
+        p.ref_logps = _vector("ref_logps", ref_logps, n)
+        p.clip_low, p.clip_high = clip
+        p.kl_coef = kl_coef
+        p.grad_scale_dev = _vector("grad_scale", grad_scale, 1)
+        if stats is None:
+            stats = torch.empty(4, dtype=torch.float32, device=logits.device)
+        if logps is None:
+            logps = torch.empty(n, dtype=torch.float32, device=logits.device)
+        dlogits, at, stride = self._gradient(logits, dlogits, backward)
+        _capi.adamw_policy_loss(self.plan, z, p, _vector("stats", stats, 4), _vector("logps", logps, n),
+                                at, stride, _stream(stream))
+        return stats, logps, dlogits
+
+    def preference(self, logits, labels, weights, ref_logps, seq_starts, *, beta=0.1,
+                   label_smoothing=0.0, temperature=1.0, grad_scale=None, backward=True, stats=None,
+                   rewards=None, logps=None, dlogits=None, stream=None):
+        """Preference loss over pairs of sequences: (stats, rewards, logps, dlogits).
+
+        seq_starts int32 [2 pairs + 1] (on the device): sequence s is rows seq_starts[s] to
+        seq_starts[s + 1] - 1; the chosen ones first, then the rejected ones in the same order.
+        ``weights`` (or None) weighs a row in its sequence's sum.  stats float32 [4]: the loss,
+        the share of pairs with the chosen one ahead, mean chosen and mean rejected reward;
+        rewards float32 [2 pairs].
+        """
+        z = self._logits(logits, labels, temperature)
+        n = logits.shape[0]
+        pairs = (seq_starts.numel() - 1) // 2
+        p = self._preference
+        p.weights = _vector("weights", weights, n)
+        p.ref_logps = _vector("ref_logps", ref_logps, n)
+        p.seq_starts = _vector("seq_starts", seq_starts, 2 * pairs + 1, torch.int32)
+        p.n_pairs = pairs
+        p.beta = beta
+        p.label_smoothing = label_smoothing
+        p.grad_scale_dev = _vector("grad_scale", grad_scale, 1)
+        if stats is None:
+            stats = torch.empty(4, dtype=torch.float32, device=logits.device)
+        if rewards is None:
+            rewards = torch.empty(2 * pairs, dtype=torch.float32, device=logits.device)
+        if logps is None:
+            logps = torch.empty(n, dtype=torch.float32, device=logits.device)
+        dlogits, at, stride = self._gradient(logits, dlogits, backward)
+        _capi.adamw_preference_loss(self.plan, z, p, _vector("stats", stats, 4),
+                                    _vector("rewards", rewards, 2 * pairs), _vector("logps", logps, n),
+                                    at, stride, _stream(stream))
+        return stats, rewards, logps, dlogits
+
+
+class FusedLayerNorm(_Plan):
+    """Layer norm over rows of ``width`` elements.
+
+    Rows [rows, width] float32, float16 or bfloat16, any row stride; weight and bias
+    float32 or of the rows' dtype, or None; mean and rstd float32 [rows].
+    """
+
+    _destroy = staticmethod(_capi.adamw_layer_norm_plan_destroy)
+
+    def __init__(self, width: int, eps: float = 1e-5):
+        self.plan = _capi.adamw_layer_norm_plan_create(int(width), float(eps))
+        self.width = int(width)
+
+    def _check(self, x, weight):
+        if x.dtype not in _DTYPES:
+            raise TypeError(f"unsupported dtype {x.dtype}")
+        if weight is not None and weight.dtype not in (torch.float32, x.dtype):
+            raise TypeError(f"the weight must be float32 or {x.dtype}, got {weight.dtype}")
+        stride = _rows("x", x)
+        if x.shape[1] != self.width:
+            raise ValueError(f"x must have {self.width} columns, got {x.shape[1]}")
+        return stride, (x.dtype if weight is None else weight.dtype)
+
+    def forward(self, x, weight=None, bias=None, *, y=None, mean=None, rstd=None, stream=None):
+        """(y, mean, rstd)"""
+        stride, wdt = self._check(x, weight if weight is not None else bias)
+        n = x.shape[0]
+        if y is None:
+            y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        if mean is None:
+            mean = torch.empty(n, dtype=torch.float32, device=x.device)
+        if rstd is None:
+            rstd = torch.empty(n, dtype=torch.float32, device=x.device)
+        _capi.adamw_layer_norm_forward(
+            self.plan, _DTYPES[x.dtype], _DTYPES[wdt], n, x.data_ptr(), stride,
+            _vector("weight", weight, self.width, wdt), _vector("bias", bias, self.width, wdt),
+            y.data_ptr(), _rows("y", y, x.dtype, x.shape), _vector("mean", mean, n),
+            _vector("rstd", rstd, n), _stream(stream))
+        return y, mean, rstd
+
+    def backward(self, dy, x, weight, mean, rstd, *, dx=None, dweight=None, dbias=None, stream=None):
+        """(dx, dweight, dbias) from the forward pass's x, mean and rstd; the weight's and bias's
+        gradients in the weight's dtype (the rows' when the weight is None)."""
+        stride, wdt = self._check(x, weight)
+        n = x.shape[0]
+        if dx is None:
+            dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        if dweight is None:
+            dweight = torch.empty(self.width, dtype=wdt, device=x.device)
+        if dbias is None:
+            dbias = torch.empty(self.width, dtype=wdt, device=x.device)
+        _capi.adamw_layer_norm_backward(
+            self.plan, _DTYPES[x.dtype], _DTYPES[wdt], n, dy.data_ptr(),
+            _rows("dy", dy, x.dtype, x.shape), x.data_ptr(), stride,
+            _vector("weight", weight, self.width, wdt), _vector("mean", mean, n),
+            _vector("rstd", rstd, n), dx.data_ptr(), _rows("dx", dx, x.dtype, x.shape),
+            _vector("dweight", dweight, self.width, wdt), _vector("dbias", dbias, self.width, wdt),
+            _stream(stream))
+        return dx, dweight, dbias

@@ -480,6 +480,161 @@ adamw_status adamw_q8_dequant(const adamw_plan* plan, int32_t which, const uint8
 adamw_status adamw_q8_quant(const adamw_plan* plan, int32_t which, const float* x,
                             uint8_t* codes, float* absmax, int64_t n, void* stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * Operators around the step: the gradient norm and clip between the backward
+ * pass and the step, the losses that start the backward pass, and layer norm
+ * with the gradients of its weight and bias.  The conventions at the top of
+ * this file hold: caller-owned tensors, host-side validation, stream-ordered
+ * work, no allocation outside the *_plan_create calls.  Sums, softmax
+ * statistics and norms are float32 or wider; results do not depend on the
+ * order in which CTAs run.
+ * ---------------------------------------------------------------------------
+ */
+
+/*
+ * Global gradient norm over every tensor of the plan (any mode; only the grads
+ * are read), in one launch:
+ *     norm       = sqrt(sum (g_raw / scale)^2)       scale = *grad_scale_dev or 1
+ *     coef       = min(1, max_norm / (norm + 1e-6))
+ *     clip_scale = scale / coef        (scale itself where coef is 1)
+ * *norm_dev is required; clip_scale_dev and found_inf_dev may be NULL.  Passing
+ * clip_scale_dev as a step's grad_scale_dev makes that step a clipped one: it
+ * multiplies every grad by 1 / clip_scale, with no extra pass.  *found_inf_dev
+ * is 1.0f when norm is not finite (a non-finite grad, or a norm past the
+ * float32 range), else 0.0f.  A NaN norm gives a NaN clip_scale, an infinite
+ * one an infinite clip_scale; pass found_inf_dev to the step to skip both.
+ * max_norm > 0; INFINITY never clips.  Squares are summed in float32 in short
+ * runs (in float64 where a run leaves float32's range) and then in float64,
+ * in a fixed order.  A plan's norm calls must not overlap one another.
+ */
+adamw_status adamw_grad_norm(adamw_plan* plan, float max_norm, const float* grad_scale_dev,
+                             float* norm_dev, float* clip_scale_dev, float* found_inf_dev,
+                             void* stream);
+
+/* Writes g <- g * (1 / *clip_scale_dev) over the plan's grads in place, rounded
+ * once to their type (a clip_scale of 1 leaves every byte alone): for callers
+ * that read the clipped grads themselves. */
+adamw_status adamw_clip_grads(adamw_plan* plan, const float* clip_scale_dev, void* stream);
+
+/* Rows of logits and one token per row. */
+typedef struct {
+  const void* logits;     /* dtype [rows][row_stride], the first vocab of each row used */
+  const void* labels;     /* int32 or int64 [rows]; a label outside [0, vocab) marks a
+                             row without a token: it is not read and counts for nothing */
+  int64_t rows;           /* 0 .. the plan's max_rows                         */
+  int64_t row_stride;     /* elements, >= vocab                                */
+  int32_t vocab;          /* >= 1                                              */
+  int32_t label_bytes;    /* 4 or 8                                            */
+  int32_t dtype;          /* adamw_dtype of the logits and their gradient      */
+  float temperature;      /* > 0: the distribution is softmax(logits / temperature) */
+} adamw_logits;
+
+/* Workspace of the token losses: per-row statistics of up to max_rows rows when
+ * max_pairs > 0 (the preference loss), and the CTAs' partial sums.  Synchronous
+ * (allocates and clears device memory).  max_pairs at most 4096.  Calls on one
+ * plan must not overlap one another. */
+typedef struct adamw_loss_plan adamw_loss_plan;
+adamw_status adamw_loss_plan_create(int64_t max_rows, int32_t max_pairs, adamw_loss_plan** out);
+/* Frees a loss plan (NULL is allowed).  Synchronises with the device first. */
+adamw_status adamw_loss_plan_destroy(adamw_loss_plan* plan);
+
+/*
+ * logps[t] = log softmax(logits[t] / temperature)[labels[t]] and, if lse is not
+ * NULL, lse[t] = log sum exp(logits[t] / temperature); both 0 for rows without
+ * a token.  -inf logits are entries of probability 0; a NaN or +inf logit, or a
+ * row of -inf alone, makes the row's outputs NaN.
+ */
+adamw_status adamw_token_logps(adamw_loss_plan* plan, const adamw_logits* z, float* logps,
+                               float* lse, void* stream);
+
+/* Per-row inputs of the policy loss, float32 [rows] each. */
+typedef struct {
+  const float* weights;         /* weight of each row's term (a mask already divided by
+                                   whatever the mean runs over); rows of weight 0 are
+                                   not read and get a zero gradient              */
+  const float* advantages;
+  const float* old_logps;       /* of the policy that sampled; NULL: ratio 1      */
+  const float* ref_logps;       /* of the reference policy; NULL: no KL term      */
+  float clip_low, clip_high;    /* the ratio is clipped to [1 - low, 1 + high]    */
+  float kl_coef;                /* >= 0                                           */
+  const float* grad_scale_dev;  /* NULL, or device fp32 loss scale of dlogits     */
+} adamw_policy;
+
+/*
+ * Clipped policy loss with a KL term, forward and (dlogits != NULL) backward:
+ *     r_t = exp(logp_t - old_t),   x_t = ref_t - logp_t
+ *     L_t = -min(r_t A_t, clip(r_t, 1 - low, 1 + high) A_t) + kl_coef (e^x_t - x_t - 1)
+ *     stats = { sum w L, sum w (policy part), sum w (e^x - x - 1), sum of w where clipped }
+ *     dlogits = grad_scale * d stats[0] / d logits, every entry of every row,
+ * rounded once to the logits' type.  logps [rows] as adamw_token_logps, 0 for
+ * rows of weight 0 too.  dlogits may be the logits themselves (same stride).
+ */
+adamw_status adamw_policy_loss(adamw_loss_plan* plan, const adamw_logits* z, const adamw_policy* p,
+                               float* stats, float* logps, void* dlogits, int64_t dlogits_stride,
+                               void* stream);
+
+/* Inputs of the preference loss. */
+typedef struct {
+  const float* weights;         /* [rows] or NULL (1): weight of a row in its sequence's sum */
+  const float* ref_logps;       /* [rows], of the reference policy                */
+  const int32_t* seq_starts;    /* device [2 n_pairs + 1], ascending: sequence s is rows
+                                   seq_starts[s] .. seq_starts[s + 1] - 1; the first
+                                   n_pairs are the chosen ones, the rest the rejected
+                                   ones in the same order                         */
+  int32_t n_pairs;              /* 1 .. the plan's max_pairs                       */
+  float beta;                   /* > 0                                            */
+  float label_smoothing;        /* [0, 0.5)                                       */
+  const float* grad_scale_dev;  /* NULL, or device fp32 loss scale of dlogits     */
+} adamw_preference;
+
+/*
+ * Preference loss over pairs of sequences, from their log ratios:
+ *     R_s = beta * sum over the rows of s of w_t (logp_t - ref_t)
+ *     d_i = R_i - R_{n_pairs + i}
+ *     L   = mean_i of -(1 - smoothing) log sigmoid(d_i) - smoothing log sigmoid(-d_i)
+ *     stats = { L, share of pairs with d > 0, mean chosen R, mean rejected R }
+ * rewards [2 n_pairs] = R; logps and dlogits as adamw_policy_loss.  Rows of no
+ * sequence, of weight 0 or without a token get a zero gradient.
+ */
+adamw_status adamw_preference_loss(adamw_loss_plan* plan, const adamw_logits* z,
+                                   const adamw_preference* p, float* stats, float* rewards,
+                                   float* logps, void* dlogits, int64_t dlogits_stride,
+                                   void* stream);
+
+/* Workspace of layer norm over rows of `width` elements: the partial sums of the
+ * weight's and bias's gradients.  Synchronous.  eps finite and >= 0.  Calls on
+ * one plan must not overlap one another. */
+typedef struct adamw_layer_norm_plan adamw_layer_norm_plan;
+adamw_status adamw_layer_norm_plan_create(int32_t width, float eps, adamw_layer_norm_plan** out);
+/* Frees a layer norm plan (NULL is allowed).  Synchronises with the device first. */
+adamw_status adamw_layer_norm_plan_destroy(adamw_layer_norm_plan* plan);
+
+/*
+ * y = (x - mean) rstd * weight + bias per row, rstd = 1 / sqrt(var + eps) with
+ * the variance over width elements.  Row strides in elements, >= width.  weight
+ * and bias are float32 or of the rows' dtype (EUNSUPPORTED otherwise) and may
+ * be NULL (1 and 0).  mean, rstd: float32 [rows].  y may be x.
+ */
+adamw_status adamw_layer_norm_forward(adamw_layer_norm_plan* plan, adamw_dtype dtype,
+                                      adamw_dtype weight_dtype, int64_t rows, const void* x,
+                                      int64_t x_stride, const void* weight, const void* bias,
+                                      void* y, int64_t y_stride, float* mean, float* rstd,
+                                      void* stream);
+
+/*
+ * dx = rstd (w dy - mean(w dy) - xhat mean(w dy xhat)),  dweight = sum over rows
+ * of dy xhat,  dbias = sum over rows of dy, from the forward pass's mean and
+ * rstd.  dweight and dbias are of the weight's dtype, written (not added to),
+ * and may be NULL.  dx may be dy (same stride).
+ */
+adamw_status adamw_layer_norm_backward(adamw_layer_norm_plan* plan, adamw_dtype dtype,
+                                       adamw_dtype weight_dtype, int64_t rows, const void* dy,
+                                       int64_t dy_stride, const void* x, int64_t x_stride,
+                                       const void* weight, const float* mean, const float* rstd,
+                                       void* dx, int64_t dx_stride, void* dweight, void* dbias,
+                                       void* stream);
+
 /* Message for the calling thread's last non-OK status ("" if none). */
 const char* adamw_last_error(void);
 
