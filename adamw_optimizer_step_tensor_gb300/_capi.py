@@ -90,6 +90,7 @@ _SIGNATURES = {
     "adamw_clip_grads": (ctypes.c_int, [_vp, _vp, _vp]),
     "adamw_loss_plan_create": (ctypes.c_int, [ctypes.c_int64, ctypes.c_int32, ctypes.POINTER(_vp)]),
     "adamw_loss_plan_destroy": (ctypes.c_int, [_vp]),
+    "adamw_loss_plan_status": (ctypes.c_int, [_vp, ctypes.POINTER(ctypes.c_uint32)]),
     "adamw_token_logps": (ctypes.c_int, [_vp, ctypes.POINTER(adamw_logits), _vp, _vp, _vp]),
     "adamw_policy_loss": (ctypes.c_int, [_vp, ctypes.POINTER(adamw_logits), ctypes.POINTER(adamw_policy),
                                          _vp, _vp, _vp, ctypes.c_int64, _vp]),
@@ -366,6 +367,13 @@ def adamw_loss_plan_create(max_rows: int, max_pairs: int) -> int:
 
 def adamw_loss_plan_destroy(plan: int) -> None:
     _check(load().adamw_loss_plan_destroy(plan))
+
+
+def adamw_loss_plan_status(plan: int) -> int:
+    """Fault bits of a loss plan's row kernels; raises AdamWError (ETIMEOUT) if set."""
+    bits = ctypes.c_uint32()
+    _check(load().adamw_loss_plan_status(plan, ctypes.byref(bits)))
+    return bits.value
 
 
 def adamw_token_logps(plan: int, z: adamw_logits, logps: int, lse: int | None,

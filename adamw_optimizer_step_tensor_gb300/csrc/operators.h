@@ -44,8 +44,7 @@ struct LossArgs {
   const float* old_logps;      // policy; null: the row's own (ratio 1)
   const float* ref_logps;      // policy: null without the KL term; preference: required
   const float* grad_scale;     // may be null
-  float k, k_lo;               // log2(e) / temperature = k + k_lo
-  double k64;
+  float k, k_lo;               // log2(e) / temperature = k + k_lo, k_lo > 0
   float inv_temp;
   float clip_lo, clip_hi;      // 1 - low, 1 + high
   float kl_coef;
@@ -57,14 +56,20 @@ struct LossArgs {
   float* stats;                // [4]
   float* rewards;              // preference: [2 * pairs]
   // plan-owned
-  float2* row_stat;            // preference: per row (reference c, sum of 2^(z k - c))
-  float* row_coef;             // preference: per row d loss / d logp
+  float2* row_stat;            // per row (reference c, sum of 2^(z k - c))
+  float* row_coef;             // per row d loss / d logp
   double* partial;             // [4 per CTA]
   uint32_t* ticket;            // 0 between launches
+  uint32_t* fault;             // nonzero: a bounded wait gave up (bit per site)
 };
 constexpr int kLossMaxCtas = 4096;   // partial sums the plan holds
-cudaError_t launch_token_loss(adamw_dtype dt, LossKind kind, const LossArgs& a, int sms,
-                              cudaStream_t s);
+struct LossLimits {
+  int sms;
+  int clusters[4];             // clusters of 1, 2, 4, 8 CTAs resident at once
+};
+cudaError_t prepare_token_loss(int sms, LossLimits* lim);
+cudaError_t launch_token_loss(adamw_dtype dt, LossKind kind, const LossArgs& a,
+                              const LossLimits& lim, cudaStream_t s);
 
 // ---- layer norm (layer_norm.cu)
 struct LayerNormArgs {

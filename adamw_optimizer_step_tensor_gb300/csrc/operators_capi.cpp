@@ -12,12 +12,12 @@ using namespace adamw;
 
 struct adamw_loss_plan {
   int device = -1;
-  int sms = 0;
+  LossLimits limits{};
   int64_t max_rows = 0;
   int32_t max_pairs = 0;
-  float2* d_stat = nullptr;      // preference: per row
+  float2* d_stat = nullptr;
   float* d_coef = nullptr;
-  double* d_partial = nullptr;   // kLossMaxCtas x 4 sums, then the ticket
+  double* d_partial = nullptr;   // kLossMaxCtas x 4 sums, then the ticket and the fault word
 };
 
 struct adamw_layer_norm_plan {
@@ -101,14 +101,17 @@ adamw_status loss_args(const adamw_loss_plan* plan, const adamw_logits* z, float
   a->rows = z->rows;
   const double inv = 1.0 / static_cast<double>(z->temperature);
   a->inv_temp = static_cast<float>(inv);
-  a->k64 = 1.4426950408889634074 * inv;
-  a->k = static_cast<float>(a->k64);
-  a->k_lo = static_cast<float>(a->k64 - a->k);
+  // k rounded down and k_lo > 0, so that -inf k + (-inf) k_lo stays -inf
+  const double k = 1.4426950408889634074 * inv;
+  a->k = static_cast<float>(k);
+  if (a->k > k) a->k = std::nextafterf(a->k, 0.0f);
+  a->k_lo = std::fmax(static_cast<float>(k - a->k), 1e-30f);
   a->logps = logps;
   a->row_stat = plan->d_stat;
   a->row_coef = plan->d_coef;
   a->partial = plan->d_partial;
   a->ticket = reinterpret_cast<uint32_t*>(plan->d_partial + 4 * kLossMaxCtas);
+  a->fault = a->ticket + 1;
   return ADAMW_OK;
 }
 
@@ -204,12 +207,13 @@ adamw_status adamw_loss_plan_create(int64_t max_rows, int32_t max_pairs, adamw_l
                                                                  free_loss_plan);
   if (!p) return fail(ADAMW_ENOMEM, "out of host memory");
   p->device = device;
-  p->sms = sms;
   p->max_rows = max_rows;
   p->max_pairs = max_pairs;
   const size_t sums = (4 * kLossMaxCtas + 1) * sizeof(double);
-  cudaError_t e = cudaMalloc(&p->d_partial, sums);
-  if (e == cudaSuccess && max_pairs > 0 && max_rows > 0) {
+  cudaError_t e = prepare_token_loss(sms, &p->limits);
+  if (e != cudaSuccess) return cuda_fail(e, "prepare the token loss kernels");
+  e = cudaMalloc(&p->d_partial, sums);
+  if (e == cudaSuccess && max_rows > 0) {
     e = cudaMalloc(&p->d_stat, static_cast<size_t>(max_rows) * sizeof(float2));
     if (e == cudaSuccess) e = cudaMalloc(&p->d_coef, static_cast<size_t>(max_rows) * sizeof(float));
   }
@@ -218,6 +222,22 @@ adamw_status adamw_loss_plan_create(int64_t max_rows, int32_t max_pairs, adamw_l
       (e = cudaStreamSynchronize(cudaStreamLegacy)) != cudaSuccess)
     return cuda_fail(e, "clear the loss plan");
   *out = p.release();
+  return ADAMW_OK;
+}
+
+adamw_status adamw_loss_plan_status(const adamw_loss_plan* plan, uint32_t* fault_bits) {
+  if (!plan) return fail(ADAMW_EINVAL, "plan is NULL");
+  adamw_status st = check_current_device(plan->device, "plan");
+  if (st != ADAMW_OK) return st;
+  cudaError_t e = cudaDeviceSynchronize();
+  uint32_t bits = 0;
+  if (e == cudaSuccess)
+    e = cudaMemcpy(&bits, reinterpret_cast<uint32_t*>(plan->d_partial + 4 * kLossMaxCtas) + 1,
+                   sizeof bits, cudaMemcpyDeviceToHost);
+  if (e != cudaSuccess) return cuda_fail(e, "read fault word");
+  if (fault_bits) *fault_bits = bits;
+  if (bits != 0)
+    return fail(ADAMW_ETIMEOUT, "a bounded wait of a token loss gave up (fault bits 0x%x)", bits);
   return ADAMW_OK;
 }
 
@@ -231,8 +251,8 @@ adamw_status adamw_token_logps(adamw_loss_plan* plan, const adamw_logits* z, flo
   if (!aligned(lse, 4)) return fail(ADAMW_EALIGN, "lse is not 4-byte aligned");
   a.lse = lse;
   if ((st = check_current_device(plan->device, "plan")) != ADAMW_OK || z->rows == 0) return st;
-  cudaError_t e = launch_token_loss(static_cast<adamw_dtype>(z->dtype), kLossLogps, a, plan->sms,
-                                    static_cast<cudaStream_t>(stream));
+  cudaError_t e = launch_token_loss(static_cast<adamw_dtype>(z->dtype), kLossLogps, a,
+                                    plan->limits, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? ADAMW_OK : cuda_fail(e, "launch token log-probabilities");
 }
 
@@ -264,8 +284,8 @@ adamw_status adamw_policy_loss(adamw_loss_plan* plan, const adamw_logits* z, con
   a.kl_coef = p->kl_coef;
   a.stats = stats;
   if ((st = check_current_device(plan->device, "plan")) != ADAMW_OK) return st;
-  cudaError_t e = launch_token_loss(static_cast<adamw_dtype>(z->dtype), kLossPolicy, a, plan->sms,
-                                    static_cast<cudaStream_t>(stream));
+  cudaError_t e = launch_token_loss(static_cast<adamw_dtype>(z->dtype), kLossPolicy, a,
+                                    plan->limits, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? ADAMW_OK : cuda_fail(e, "launch policy loss");
 }
 
@@ -300,8 +320,8 @@ adamw_status adamw_preference_loss(adamw_loss_plan* plan, const adamw_logits* z,
   a.stats = stats;
   a.rewards = rewards;
   if ((st = check_current_device(plan->device, "plan")) != ADAMW_OK) return st;
-  cudaError_t e = launch_token_loss(static_cast<adamw_dtype>(z->dtype), kLossPrefer, a, plan->sms,
-                                    static_cast<cudaStream_t>(stream));
+  cudaError_t e = launch_token_loss(static_cast<adamw_dtype>(z->dtype), kLossPrefer, a,
+                                    plan->limits, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? ADAMW_OK : cuda_fail(e, "launch preference loss");
 }
 

@@ -40,23 +40,25 @@ __device__ __forceinline__ float block_sum(float x, float* s_warp) {
   return t;
 }
 
-// Every CTA leaves four float64 sums; the last one to finish adds them in CTA
-// order (the same bits whatever the order of arrival) and returns true with
-// the totals in `out`, for its thread 0.  Call with the CTA's sums in thread 0.
+// CTA `me` of `ctas` leaves four float64 sums (its thread 0's `mine`); the last
+// one to arrive adds them in CTA order (the same bits whatever the order of
+// arrival) and returns true with the totals in `out`, in its thread 0.  Called
+// by every thread of those CTAs.
 __device__ __forceinline__ bool last_cta_sums(const double (&mine)[4], double* partial,
-                                              uint32_t* ticket, double (&out)[4]) {
+                                              uint32_t* ticket, unsigned me, unsigned ctas,
+                                              double (&out)[4]) {
   bool last = false;
   if (threadIdx.x == 0) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) partial[4 * blockIdx.x + i] = mine[i];
+    for (int i = 0; i < 4; ++i) partial[4 * me + i] = mine[i];
     __threadfence();
-    last = atomicAdd(ticket, 1u) == gridDim.x - 1;
+    last = atomicAdd(ticket, 1u) == ctas - 1;
   }
   if (!__syncthreads_or(last)) return false;
   __threadfence();
   if (threadIdx.x < 32) {
     double t[4] = {0.0, 0.0, 0.0, 0.0};
-    for (unsigned c = threadIdx.x; c < gridDim.x; c += 32) {
+    for (unsigned c = threadIdx.x; c < ctas; c += 32) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) t[i] += __ldcg(partial + 4 * c + i);
     }

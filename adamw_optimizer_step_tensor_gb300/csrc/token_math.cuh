@@ -1,0 +1,214 @@
+// token_math.cuh -- arithmetic shared by the token-loss kernels.
+//
+// With z = logits / T, y the row's token, w its weight:
+//   logp   = z_y - log sum_j exp z_j
+//   dlogits_j = (d loss / d logp) * (1{j = y} - softmax(z)_j) / T
+// Everything runs in base 2: with k = log2(e) / T, a_j = z_j k - c for a running
+// reference c (the largest z k seen), S = sum_j 2^a_j, and
+// logp = (z_y k - c - log2 S) * ln 2.  An fma rounds relative to the small
+// difference, so large logits lose nothing, and the softmax is 2^a_j / S.
+// Errors with the same sign for every token would add up over the tokens of a
+// sequence, whose log ratios nearly cancel, so four of them are kept out: k is
+// two float32 (k + k_lo); c is an integer (the ceiling of the largest z k), so
+// moving a sum to another reference multiplies it by an exact power of two;
+// log2 S takes back the mean error of the hardware's 2^x; and exponentials are
+// summed in runs of 8 or 16 before they join a long sum, which would round the
+// small ones away.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <cstdint>
+#include <type_traits>
+
+#include "operators.h"
+#include "rows.cuh"
+
+namespace adamw {
+namespace {
+
+constexpr float kLn2 = 0.69314718055994530942f;
+constexpr float kLowest = -3.40282347e38f;
+
+// ex2.approx is exact at integers and elsewhere low by 4.9e-8 on average,
+// whatever the fraction (measured on GB300 over 4 M arguments in [-17, 0); the
+// spread around that is 3e-8): in log2 S that is 7.1e-8.
+constexpr float kExp2Bias = 7.1e-8f;
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ float arg(const LossArgs& a, float z, float c) {
+  return fmaf(z, a.k_lo, fmaf(z, a.k, -c));
+}
+// The same for a gradient entry: 16-bit gradients do not see k_lo.
+template <typename T>
+__device__ __forceinline__ float grad_arg(const LossArgs& a, float z, float c) {
+  return std::is_same<T, float>::value ? arg(a, z, c) : fmaf(z, a.k, -c);
+}
+
+// Integer reference c and S = sum 2^(z k - c).
+struct RowSum {
+  float c, s;
+  __device__ __forceinline__ void raise(float zk) {
+    if (zk > c) {
+      const float hi = ceilf(zk);
+      s *= exp2_fast(c - hi);
+      c = hi;
+    }
+  }
+  __device__ __forceinline__ void join(float c2, float s2) {
+    const float hi = fmaxf(c, c2);
+    s = s * exp2_fast(c - hi) + s2 * exp2_fast(c2 - hi);
+    c = hi;
+  }
+  __device__ __forceinline__ void join_warp() {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+      join(__shfl_xor_sync(kFull, c, o), __shfl_xor_sync(kFull, s, o));
+  }
+};
+
+// c + log2 S as an integer plus a small rest, so that a difference to z_y k
+// rounds relative to the difference.
+struct Log2Sum {
+  float whole, rest;
+};
+__device__ __forceinline__ Log2Sum log2_sum(const RowSum& r) {
+  if (!(r.s >= 1.17549435e-38f && r.s <= 3.40282347e38f)) return {r.c, log2f(r.s)};
+  const uint32_t b = __float_as_uint(r.s);
+  const float f = __uint_as_float((b & 0x007FFFFFu) | 0x3F800000u);     // [1, 2)
+  const float e = static_cast<float>(static_cast<int>(b >> 23) - 127);
+  return {r.c + e, log2f(f) + kExp2Bias};
+}
+__device__ __forceinline__ float logp_of(const LossArgs& a, float zy, const Log2Sum& l) {
+  return (fmaf(zy, a.k, -l.whole) + fmaf(zy, a.k_lo, -l.rest)) * kLn2;
+}
+__device__ __forceinline__ float lse_of(const Log2Sum& l) { return (l.whole + l.rest) * kLn2; }
+
+__device__ __forceinline__ int64_t label_of(const LossArgs& a, int64_t t) {
+  return a.labels64 ? static_cast<const int64_t*>(a.labels)[t]
+                    : static_cast<const int32_t*>(a.labels)[t];
+}
+
+// Inputs of one row's policy term.
+struct PolicyRow {
+  float w, adv, old, ref;
+};
+// What one row adds to the policy loss, and d loss / d logp.
+struct PolicyTerm {
+  float policy, kl, clipped, slope;
+};
+__device__ __forceinline__ PolicyTerm policy_term(const LossArgs& a, const PolicyRow& in,
+                                                  float logp) {
+  const float ratio = a.old_logps != nullptr ? expf(logp - in.old) : 1.0f;
+  const float bound = fminf(fmaxf(ratio, a.clip_lo), a.clip_hi);
+  const bool cut = bound * in.adv < ratio * in.adv;
+  PolicyTerm r;
+  r.policy = -in.w * ((cut ? bound : ratio) * in.adv);
+  r.clipped = cut ? in.w : 0.0f;
+  r.slope = cut ? 0.0f : -in.adv * ratio;
+  r.kl = 0.0f;
+  if (a.ref_logps != nullptr) {
+    const float x = in.ref - logp;
+    const float e = expm1f(x);
+    r.kl = in.w * (e - x);
+    r.slope = fmaf(-a.kl_coef, e, r.slope);
+  }
+  r.slope *= in.w;
+  return r;
+}
+
+// ---- 16-byte words of a row: 8 or 4 elements
+template <typename T> constexpr int kPerWord = 16 / sizeof(T);
+
+template <typename T>
+__device__ __forceinline__ void unpack(const uint4& w, float (&x)[kPerWord<T>]) {
+  const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (sizeof(T) == 4) {
+      x[i] = __uint_as_float(v[i]);
+    } else if constexpr (std::is_same<T, __half>::value) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&v[i]));
+      x[2 * i] = f.x;
+      x[2 * i + 1] = f.y;
+    } else {
+      x[2 * i] = __uint_as_float(v[i] << 16);
+      x[2 * i + 1] = __uint_as_float(v[i] & 0xFFFF0000u);
+    }
+  }
+}
+template <typename T>
+__device__ __forceinline__ uint4 pack(const float (&x)[kPerWord<T>]) {
+  uint32_t v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (sizeof(T) == 4) {
+      v[i] = __float_as_uint(x[i]);
+    } else if constexpr (std::is_same<T, __half>::value) {
+      const __half2 h = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
+      v[i] = *reinterpret_cast<const uint32_t*>(&h);
+    } else {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+      v[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+  }
+  return make_uint4(v[0], v[1], v[2], v[3]);
+}
+
+// The largest element of a word, NaN ignored (16-bit types two at a time).
+template <typename T>
+__device__ __forceinline__ float word_max(const uint4& w) {
+  if constexpr (sizeof(T) == 4) {
+    return fmaxf(fmaxf(__uint_as_float(w.x), __uint_as_float(w.y)),
+                 fmaxf(__uint_as_float(w.z), __uint_as_float(w.w)));
+  } else if constexpr (std::is_same<T, __half>::value) {
+    const __half2* h = reinterpret_cast<const __half2*>(&w);
+    const float2 f = __half22float2(__hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3])));
+    return fmaxf(f.x, f.y);
+  } else {
+    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&w);
+    const float2 f = __bfloat1622float2(__hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3])));
+    return fmaxf(f.x, f.y);
+  }
+}
+
+// Adds a word's exponentials to the row's sum.
+template <typename T>
+__device__ __forceinline__ void add_word(const LossArgs& a, const uint4& w, RowSum& r) {
+  r.raise(word_max<T>(w) * a.k);
+  float x[kPerWord<T>];
+  unpack<T>(w, x);
+  float t[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (sizeof(T) == 4) t[i] = exp2_fast(arg(a, x[i], r.c));
+    else t[i] = exp2_fast(arg(a, x[2 * i], r.c)) + exp2_fast(arg(a, x[2 * i + 1], r.c));
+  }
+  r.s += (t[0] + t[1]) + (t[2] + t[3]);
+}
+
+// The gradient of a word's logits: 2^a_j * f, plus coef at the token's place
+// (`at`, outside [0, elements) when the token is elsewhere).
+template <typename T>
+__device__ __forceinline__ uint4 grad_word(const LossArgs& a, const uint4& w, float c, float f,
+                                           float coef, int at) {
+  float x[kPerWord<T>];
+  unpack<T>(w, x);
+#pragma unroll
+  for (int i = 0; i < kPerWord<T>; ++i) x[i] = exp2_fast(grad_arg<T>(a, x[i], c)) * f;
+  if (static_cast<unsigned>(at) < kPerWord<T>) {
+#pragma unroll
+    for (int i = 0; i < kPerWord<T>; ++i)
+      if (i == at) x[i] += coef;
+  }
+  return pack<T>(x);
+}
+
+}  // namespace
+}  // namespace adamw

@@ -86,6 +86,10 @@ class FusedTokenLoss(_Plan):
         self._policy = _capi.adamw_policy()
         self._preference = _capi.adamw_preference()
 
+    def status(self) -> int:
+        """Device-side fault bits (0 = healthy); raises AdamWError if a bounded wait gave up."""
+        return _capi.adamw_loss_plan_status(self.plan)
+
     def _logits(self, logits, labels, temperature):
         if logits.dtype not in _DTYPES:
             raise TypeError(f"unsupported logits dtype {logits.dtype}")

@@ -530,12 +530,15 @@ typedef struct {
   float temperature;      /* > 0: the distribution is softmax(logits / temperature) */
 } adamw_logits;
 
-/* Workspace of the token losses: per-row statistics of up to max_rows rows when
- * max_pairs > 0 (the preference loss), and the CTAs' partial sums.  Synchronous
- * (allocates and clears device memory).  max_pairs at most 4096.  Calls on one
- * plan must not overlap one another. */
+/* Workspace of the token losses: per-row statistics of up to max_rows rows and
+ * the CTAs' partial sums.  max_pairs (at most 4096) bounds the preference loss's
+ * pairs.  Synchronous (allocates and clears device memory).  Calls on one plan
+ * must not overlap one another. */
 typedef struct adamw_loss_plan adamw_loss_plan;
 adamw_status adamw_loss_plan_create(int64_t max_rows, int32_t max_pairs, adamw_loss_plan** out);
+/* Device-side health, as adamw_plan_status: every wait of the row kernels is
+ * bounded (2 s); one that gave up left its call's outputs incomplete. */
+adamw_status adamw_loss_plan_status(const adamw_loss_plan* plan, uint32_t* fault_bits);
 /* Frees a loss plan (NULL is allowed).  Synchronises with the device first. */
 adamw_status adamw_loss_plan_destroy(adamw_loss_plan* plan);
 
@@ -543,7 +546,7 @@ adamw_status adamw_loss_plan_destroy(adamw_loss_plan* plan);
  * logps[t] = log softmax(logits[t] / temperature)[labels[t]] and, if lse is not
  * NULL, lse[t] = log sum exp(logits[t] / temperature); both 0 for rows without
  * a token.  -inf logits are entries of probability 0; a NaN or +inf logit, or a
- * row of -inf alone, makes the row's outputs NaN.
+ * row of -inf alone, makes the row's log-probability (and gradient) NaN.
  */
 adamw_status adamw_token_logps(adamw_loss_plan* plan, const adamw_logits* z, float* logps,
                                float* lse, void* stream);

@@ -248,6 +248,35 @@ def test_logps(rows, vocab, dtype):
     assert np.all(np.abs(wide(lse) - wl) <= lp_tol(wl, vocab))
 
 
+def test_probability_zero_at_any_temperature():
+    """-inf stays probability 0 whatever the sign of the rounding of 1 / temperature."""
+    def edit(z, y, w, rng):
+        hit = rng.random(z.shape) < 0.3
+        hit[np.arange(len(y)), y] = False
+        z[hit] = -np.inf
+    for vocab in (300, 20_011):
+        for temperature in (0.3, 0.5, 0.7, 0.9, 1.1, 1.3, 2.0, 3.0):
+            b = Batch(4, vocab, torch.float32, edit=edit, masked=0.0)
+            check_policy(b, temperature=float(f32(temperature)))
+
+
+def test_plan_status_is_clear():
+    b = Batch(30, 40_003, torch.bfloat16)
+    adv, old, ref = b.policy_inputs()
+    loss = FusedTokenLoss(30, 1)
+    loss.policy(b.logits, b.labels, b.w, adv, old, ref)
+    loss.preference(b.logits, b.labels, None, ref, dev(np.array([0, 9, 30], np.int32)))
+    assert loss.status() == 0
+
+
+@pytest.mark.parametrize("dtype,vocab", [(torch.bfloat16, 300_007), (torch.float32, 430_001), (torch.bfloat16, 860_003)])
+def test_very_large_vocabularies(dtype, vocab):
+    """Rows of more slots than one CTA's, and rows that do not fit a cluster's shared memory."""
+    b = Batch(5, vocab, dtype, masked=0.2)
+    check_policy(b)
+    check_preference(b, np.array([0, 2, 5], np.int32))
+
+
 def test_large_logits():
     """Logits of several hundred: the softmax depends on differences alone."""
     for vocab in (500, 30_000):
