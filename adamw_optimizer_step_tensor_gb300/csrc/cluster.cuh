@@ -55,10 +55,11 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity
     if (global_ns() - t0 > kWaitLimitNs) return false;
   return true;
 }
-// Waits until all but the newest bulk store of this thread have read their
+// Waits until all but the N newest bulk stores of this thread have read their
 // shared source.
-__device__ __forceinline__ void bulk_wait_read_all_but_one() {
-  asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+template <int N>
+__device__ __forceinline__ void bulk_wait_read_but() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
 }
 
 }  // namespace

@@ -82,6 +82,7 @@ adamw_status loss_args(const adamw_loss_plan* plan, const adamw_logits* z, float
     return fail(ADAMW_EINVAL, "%lld rows, but the plan was made for %lld", (long long)z->rows,
                 (long long)plan->max_rows);
   if (z->vocab < 1) return fail(ADAMW_EINVAL, "vocab < 1");
+  if (z->vocab > (1 << 30)) return fail(ADAMW_EUNSUPPORTED, "vocab is more than 2^30");
   if (z->row_stride < z->vocab) return fail(ADAMW_EINVAL, "row_stride is less than vocab");
   if (!(z->temperature > 0.0f) || !std::isfinite(z->temperature))
     return fail(ADAMW_EINVAL, "temperature must be finite and > 0");

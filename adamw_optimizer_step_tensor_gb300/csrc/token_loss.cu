@@ -3,19 +3,24 @@
 //
 // One cluster of C CTAs (C = 1, 2, 4, 8) works through rows of logits; each CTA
 // has its share of every row pass through a ring of shared-memory slots:
-//   producer (one thread)   bulk copies (TMA engine) of 16 KB pieces into free
-//                           slots; for gradients, bulk copies of finished
-//                           slots out to dlogits
+//   loader (one thread)     bulk copies (TMA engine) of 16 KB pieces into free
+//                           slots
 //   scheduler (one warp)    walks the rows' labels and weights ahead of the
 //                           others, deals live rows (and the rows that only
 //                           need zeros) out to the clusters in turn, and hands
 //                           each of its cluster's rows on with everything the
 //                           row's arithmetic reads from memory
-//   consumers (16 warps)    sum the exponentials of a row's pieces, join the
-//                           sum over the cluster, and turn the same pieces,
-//                           still in shared memory, into gradients in place
-// A policy-loss row is so read once and its gradient written once.  What bounds
-// it is DRAM: 4 bytes per 16-bit logit against about 11 instructions.
+//   summing warps           sum the exponentials of a row's pieces
+//   finisher (one warp)     joins the sums over the CTA and the cluster, and
+//                           turns them into the row's outputs and slope
+//   gradient warps          turn the same pieces, still in shared memory, into
+//                           gradients in place
+//   storer (one thread)     bulk copies of finished slots out to dlogits; a slot
+//                           is free once its copy has read it
+// A policy-loss row is so read once and its gradient written once.  Summing and
+// gradient warps are apart so that the next row is summed while one row's sum
+// is joined and differentiated; with one set of warps for both, every row paid
+// the join's latency and 8192 rows of 128,256 bf16 logits took 727 us.
 #include <cmath>
 
 #include "cluster.cuh"
@@ -27,13 +32,19 @@ namespace {
 constexpr int kSlotBytes = 16384;
 constexpr int kSlots = 13;
 constexpr int kSlotWords = kSlotBytes / 16;
-constexpr int kConsumers = 16;                  // warps
-constexpr int kConsumerThreads = kConsumers * 32;
-constexpr int kRingThreads = kConsumerThreads + 64;
+constexpr int kWorkers = 16;                    // summing and gradient warps together
+constexpr int kFirstWorker = 4;                 // after loader, scheduler, finisher, storer
+constexpr int kRingThreads = (kFirstWorker + kWorkers) * 32;
 constexpr int kQueue = 8;                       // rows handed on ahead
-constexpr int kPending = 16;                    // rows with slots in flight, at most kSlots
+// Cluster-wide sums under way: a finisher is through with sum n only after the
+// others have taken it up, and they do that after they are through with n - 1,
+// so two places are enough.
+constexpr int kJoins = 2;
+constexpr int kStoresOut = 3;                   // copies out whose slots may be awaited later
 constexpr int kMaxCluster = 8;
-constexpr int kRowsPerLane = 4;                 // rows the scheduler looks at per lane and step
+constexpr int kRowsPerLane = 8;                 // rows the scheduler looks at per lane and step
+constexpr int kBatch = 4;                       // rows whose inputs it fetches together
+constexpr int kSharePieces = 4;                 // of a row that waits for its sum, at most
 
 // What a launch does with each live row.
 enum Pass {
@@ -50,29 +61,47 @@ __host__ __device__ constexpr bool policy_pass(int pass) {
   return pass == kPassPolicy || pass == kPassPolicyGrad;
 }
 
+__host__ __device__ constexpr bool sums(int pass) { return pass != kPassGrad; }
+// Warps of either kind; a pass with one kind gives it all of them.
+__host__ __device__ constexpr int sum_warps(int pass) {
+  return !sums(pass) ? 0 : (writes_gradient(pass) ? kWorkers / 2 : kWorkers);
+}
+__host__ __device__ constexpr int grad_warps(int pass) { return kWorkers - sum_warps(pass); }
+
 enum RowKind { kRowLive, kRowZero, kRowStop };
-struct QueueRow {
+// A row's inputs, one per scheduler lane: its elements off the 16-byte grid (the
+// first ones on lanes 0.., the last ones on lanes 8..), then
+enum Input {
+  kInToken = 16,                          // the token's logit
+  kInWeight, kInAdvantage, kInOld, kInRef,
+  kInReference, kInSum, kInSlope,         // kPassGrad
+  kInputs
+};
+struct DealtRow {
   int64_t row;
   int32_t kind;
   int32_t y;                  // the row's token
-  float zy;
-  PolicyRow policy;
-  float c, s, slope;          // kPassGrad
-  float edge[16];             // the row's first and last elements off the 16-byte grid
+};
+struct QueueRow : DealtRow {
+  float in[kInputs];
 };
 
 struct RingShared {
   alignas(128) unsigned char slot[kSlots][kSlotBytes];
   QueueRow queue[kQueue];
-  float2 part[2][kMaxCluster * kConsumers];     // (c, s) of every consumer warp of the cluster
+  DealtRow dealt[kBatch + 32 * kRowsPerLane];   // this cluster's next rows, scheduler only
+  float2 part[kQueue][kWorkers];          // (c, s) of every summing warp
+  float2 cross[kJoins][kMaxCluster];      // (c, s) of every CTA of the cluster
   struct {
-    unsigned char* dst;
-    int32_t words, pad;
-  } pending[kPending];
+    float c, f, coef, pad;
+  } result[kQueue];                       // what the gradient warps need of a row
   uint64_t full[kSlots];      // a slot's copy has landed
-  uint64_t done[kSlots];      // the consumers are through with a slot
+  uint64_t done[kSlots];      // a slot's gradients are in place
+  uint64_t empty[kSlots];     // a slot may be filled again
   uint64_t queue_full[kQueue], queue_empty[kQueue];
-  uint64_t joined[2];         // the cluster's partial sums are in `part`
+  uint64_t summed[kQueue];    // a row's `part` is complete
+  uint64_t joined[kJoins];    // a row's `cross` is complete
+  uint64_t ready[kQueue];     // a row's `result` is there
   uint32_t gave_up;
 };
 
@@ -100,7 +129,8 @@ struct RowShare {
     head = static_cast<int>((lo16 - lo) / sizeof(T));
     tail = static_cast<int>((hi - hi16) / sizeof(T));
     const int64_t all = static_cast<int64_t>((hi16 - lo16) / 16);
-    const int64_t per = ((all + ranks - 1) / ranks + 7) / 8 * 8;
+    // ranks is a power of two; shares start on 128-byte steps of the words
+    const int64_t per = (((all + ranks - 1) >> (__ffs(ranks) - 1)) + 7) & ~static_cast<int64_t>(7);
     const int64_t from = min(per * rank, all);
     words = static_cast<int>(min(per, all - from));
     pieces = (words + kSlotWords - 1) / kSlotWords;
@@ -112,13 +142,41 @@ struct RowShare {
   }
 };
 
+// The element off the 16-byte grid that lane `lane` looks after, or -1: the
+// row's first elements on lanes 0.., its last on lanes 8...
+template <typename T>
+__device__ __forceinline__ int ragged_element(const RowShare<T>& share, int vocab, int lane) {
+  if (lane < 8) return lane < share.head ? lane : -1;
+  return lane < 16 && lane - 8 < share.tail ? vocab - share.tail + lane - 8 : -1;
+}
+
 // ---- scheduler
 
-template <int PASS>
-__device__ __forceinline__ bool row_live(const LossArgs& a, int64_t t) {
-  if (PASS == kPassGrad) return a.row_coef[t] != 0.0f;
-  const int64_t y = label_of(a, t);
-  return y >= 0 && y < a.vocab && (a.weights == nullptr || a.weights[t] != 0.0f);
+// Lane `lane`'s input of a row.
+template <typename T, int PASS>
+__device__ __forceinline__ float row_input(const LossArgs& a, const DealtRow& d, int lane,
+                                           uint32_t rank, uint32_t ranks) {
+  const T* const z = static_cast<const T*>(a.logits) + d.row * a.stride;
+  const float* from = nullptr;
+  if (lane <= kInToken) {
+    const RowShare<T> share(z, a.vocab, rank, ranks);
+    const int e = lane == kInToken ? (PASS != kPassGrad ? d.y : -1)
+                                   : ragged_element(share, a.vocab, lane);
+    return e >= 0 ? to_f32(z[e]) : 0.0f;
+  }
+  if (policy_pass(PASS)) {
+    if (lane == kInWeight) from = a.weights;
+    if (lane == kInAdvantage) from = a.advantages;
+    if (lane == kInOld) from = a.old_logps;
+    if (lane == kInRef) from = a.ref_logps;
+  }
+  if (PASS == kPassGrad) {
+    const float2 st = a.row_stat[d.row];
+    if (lane == kInReference) return st.x;
+    if (lane == kInSum) return st.y;
+    if (lane == kInSlope) from = a.row_coef;
+  }
+  return from != nullptr ? from[d.row] : 0.0f;
 }
 
 template <typename T, int PASS>
@@ -126,350 +184,378 @@ __device__ void schedule(const LossArgs& a, RingShared& sh) {
   const uint32_t rank = cluster_rank(), ranks = cluster_size();
   const uint32_t me = blockIdx.x / ranks, clusters = gridDim.x / ranks;
   const int lane = threadIdx.x & 31;
-  uint32_t sent = 0;
   uint32_t live_turn = 0, zero_turn = 0;       // whose turn the next live / zero row is
-  auto send = [&](int64_t row, int kind) -> bool {
-    QueueRow& q = sh.queue[sent % kQueue];
-    if (sent >= kQueue &&
-        !mbar_wait(&sh.queue_empty[sent % kQueue], (sent / kQueue - 1) & 1u)) return false;
-    if (kind == kRowLive) {
-      const T* const z = static_cast<const T*>(a.logits) + row * a.stride;
-      const RowShare<T> share(z, a.vocab, rank, ranks);
-      const int64_t y = label_of(a, row);
-      if (lane < 8) {
-        if (lane < share.head) q.edge[lane] = to_f32(z[lane]);
-      } else if (lane < 16) {
-        if (lane - 8 < share.tail) q.edge[lane] = to_f32(z[a.vocab - share.tail + lane - 8]);
-      } else if (lane == 16) {
-        if (PASS != kPassGrad) q.zy = to_f32(z[y]);
-      } else if (lane == 17) {
-        if (policy_pass(PASS)) {
-          q.policy.w = a.weights[row];
-          q.policy.adv = a.advantages[row];
-          q.policy.old = a.old_logps != nullptr ? a.old_logps[row] : 0.0f;
-          q.policy.ref = a.ref_logps != nullptr ? a.ref_logps[row] : 0.0f;
-        }
-        if (PASS == kPassGrad) {
-          const float2 st = a.row_stat[row];
-          q.c = st.x;
-          q.s = st.y;
-          q.slope = a.row_coef[row];
-        }
+  uint32_t sent = 0;
+  int64_t base = 0;                            // rows looked at
+  int held = 0, next = 0;                      // rows in sh.dealt, and the first not sent yet
+  for (;;) {
+    if (next == held) next = held = 0;
+    while (held - next < kBatch && held <= kBatch && base < a.rows) {
+      int64_t y[kRowsPerLane];
+      bool live[kRowsPerLane];
+#pragma unroll
+      for (int u = 0; u < kRowsPerLane; ++u) {
+        const int64_t i = base + 32 * u + lane;
+        // gradients of known rows run from the last row to the first: the pass
+        // before ended there, so the end of the logits is still in L2
+        const int64_t t = PASS == kPassGrad ? a.rows - 1 - i : i;
+        const bool in = i < a.rows;
+        y[u] = in ? label_of(a, t) : -1;
+        if (PASS == kPassGrad) live[u] = in && a.row_coef[t] != 0.0f;
+        else live[u] = in && (a.weights == nullptr || a.weights[t] != 0.0f);
       }
-      if (lane == 0) q.y = static_cast<int32_t>(y);
-    }
-    if (lane == 0) {
-      q.row = row;
-      q.kind = kind;
-    }
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&sh.queue_full[sent % kQueue]);
-    ++sent;
-    return true;
-  };
-  bool ok = true;
-  for (int64_t base = 0; ok && base < a.rows; base += 32 * kRowsPerLane) {
-    bool live[kRowsPerLane];
 #pragma unroll
-    for (int u = 0; u < kRowsPerLane; ++u) {
-      const int64_t i = base + 32 * u + lane;
-      // gradients of known rows run from the last row to the first: the pass
-      // before ended there, so the end of the logits is still in L2
-      const int64_t t = PASS == kPassGrad ? a.rows - 1 - i : i;
-      live[u] = i < a.rows && row_live<PASS>(a, t);
-    }
-#pragma unroll
-    for (int u = 0; u < kRowsPerLane; ++u) {
-      const int64_t i = base + 32 * u + lane;
-      const uint32_t in = __ballot_sync(kFull, i < a.rows);
-      const uint32_t on = __ballot_sync(kFull, live[u]);
-      const uint32_t off = in & ~on;
-      const uint32_t before = (1u << lane) - 1u;
-      const uint32_t turn = live[u] ? (live_turn + __popc(on & before)) % clusters
-                                    : (zero_turn + __popc(off & before)) % clusters;
-      uint32_t mine = __ballot_sync(kFull, i < a.rows && turn == me);
-      live_turn = (live_turn + __popc(on)) % clusters;
-      zero_turn = (zero_turn + __popc(off)) % clusters;
-      while (ok && mine != 0u) {
-        const int l = __ffs(mine) - 1;
-        mine &= mine - 1u;
-        const int64_t r = base + 32 * u + l;
-        const int64_t t = PASS == kPassGrad ? a.rows - 1 - r : r;
-        const bool is_live = (on >> l) & 1u;
-        if (rank == 0 && lane == 0) {
+      for (int u = 0; u < kRowsPerLane; ++u) {
+        const int64_t i = base + 32 * u + lane;
+        const int64_t t = PASS == kPassGrad ? a.rows - 1 - i : i;
+        const bool is_live = live[u] && y[u] >= 0 && y[u] < a.vocab;
+        const uint32_t on = __ballot_sync(kFull, is_live);
+        const uint32_t off = __ballot_sync(kFull, i < a.rows && !is_live);
+        const uint32_t before = (1u << lane) - 1u;
+        const uint32_t turn = is_live ? (live_turn + __popc(on & before)) % clusters
+                                      : (zero_turn + __popc(off & before)) % clusters;
+        const bool mine = i < a.rows && turn == me;
+        live_turn = (live_turn + __popc(on)) % clusters;
+        zero_turn = (zero_turn + __popc(off)) % clusters;
+        if (mine && rank == 0) {
           if (PASS == kPassPrefer) a.row_coef[t] = 0.0f;
           if (PASS != kPassGrad && !is_live) {
             a.logps[t] = 0.0f;
             if (a.lse != nullptr) a.lse[t] = 0.0f;
           }
         }
-        if (is_live) ok = send(t, kRowLive);
-        else if (writes_gradient(PASS)) ok = send(t, kRowZero);
+        const bool send = mine && (is_live || writes_gradient(PASS));
+        const uint32_t sends = __ballot_sync(kFull, send);
+        if (send)
+          sh.dealt[held + __popc(sends & before)] = {t, is_live ? kRowLive : kRowZero,
+                                                     static_cast<int32_t>(y[u])};
+        held += __popc(sends);
       }
+      base += 32 * kRowsPerLane;
+      __syncwarp();
     }
+    const int n = min(kBatch, held - next);
+    float in[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i)
+      in[i] = i < n && sh.dealt[next + i].kind == kRowLive
+                  ? row_input<T, PASS>(a, sh.dealt[next + i], lane, rank, ranks)
+                  : 0.0f;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      if (i > n || (i == n && n != 0)) break;
+      // with nothing left, one last row says so
+      const DealtRow d = n == 0 ? DealtRow{0, kRowStop, 0} : sh.dealt[next + i];
+      const uint32_t q = sent % kQueue;
+      if (sent >= kQueue && !mbar_wait(&sh.queue_empty[q], (sent / kQueue - 1) & 1u)) {
+        atomicOr(&sh.gave_up, 1u);
+        return;
+      }
+      if (lane < kInputs) sh.queue[q].in[lane] = in[i];
+      if (lane == 0) static_cast<DealtRow&>(sh.queue[q]) = d;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.queue_full[q]);
+      ++sent;
+      if (n == 0) return;
+    }
+    next += n;
+    __syncwarp();
   }
-  if (ok) ok = send(0, kRowStop);
-  if (!ok && lane == 0) atomicOr(&sh.gave_up, 1u);
 }
 
-// ---- producer
+// ---- loader and storer
 
-template <typename T, int PASS>
-__device__ void produce(const LossArgs& a, RingShared& sh, bool bulk_out) {
+// Waits for the next row of the queue; false if the wait gave up.
+__device__ __forceinline__ bool take_row(RingShared& sh, uint32_t n, uint32_t site) {
+  if (mbar_wait(&sh.queue_full[n % kQueue], (n / kQueue) & 1u)) return true;
+  atomicOr(&sh.gave_up, site);
+  return false;
+}
+
+template <typename T>
+__device__ void load_rows(const LossArgs& a, RingShared& sh) {
   const uint32_t rank = cluster_rank(), ranks = cluster_size();
-  constexpr bool kGrad = writes_gradient(PASS);
-  uint32_t loads = 0, freed = 0;           // slot uses issued / whose slot may be refilled
-  uint32_t stores = 0;
-  uint32_t taken = 0;                      // queue rows taken
-  uint32_t rows_in = 0, rows_out = 0;      // pending rows
-  int piece = 0, pieces = 0, out_piece = 0;
-  const unsigned char* src = nullptr;
-  int words = 0;
-  bool more = true, ok = true;
-  while (ok) {
-    // fill every free slot; wait for a row only when nothing is left to drain
-    while (more && (!kGrad || loads - freed < kSlots)) {
-      if (piece == pieces) {
-        uint64_t* const bar = &sh.queue_full[taken % kQueue];
-        const uint32_t parity = (taken / kQueue) & 1u;
-        if (!mbar_try_wait(bar, parity)) {
-          if (kGrad && stores != loads) break;
-          if (!mbar_wait(bar, parity)) {
-            ok = false;
-            break;
-          }
-        }
-        const QueueRow& q = sh.queue[taken % kQueue];
-        const int kind = q.kind;
-        const int64_t row = q.row;
-        mbar_arrive(&sh.queue_empty[taken % kQueue]);
-        ++taken;
-        if (kind == kRowStop) {
-          more = false;
-          break;
-        }
-        if (kind == kRowZero) continue;
-        const RowShare<T> share(static_cast<const T*>(a.logits) + row * a.stride, a.vocab, rank,
-                                ranks);
-        if (share.pieces == 0) continue;
-        src = share.base;
-        words = share.words;
-        pieces = share.pieces;
-        piece = 0;
-        if (kGrad) {
-          auto& p = sh.pending[rows_in % kPending];
-          p.dst = reinterpret_cast<unsigned char*>(static_cast<T*>(a.dlogits) + row * a.dstride +
-                                                   share.first);
-          p.words = words;
-          ++rows_in;
-        }
-      }
-      const int s = loads % kSlots;
-      if (!kGrad && loads >= kSlots &&
-          !mbar_wait(&sh.done[s], (loads / kSlots - 1) & 1u)) {
+  uint32_t use = 0;
+  bool ok = true;
+  for (uint32_t n = 0; ok && (ok = take_row(sh, n, 2u)); ++n) {
+    const int64_t row = sh.queue[n % kQueue].row;
+    const int kind = sh.queue[n % kQueue].kind;
+    mbar_arrive(&sh.queue_empty[n % kQueue]);
+    if (kind == kRowStop) break;
+    if (kind == kRowZero) continue;
+    const RowShare<T> share(static_cast<const T*>(a.logits) + row * a.stride, a.vocab, rank, ranks);
+    for (int j = 0; j < share.pieces; ++j, ++use) {
+      const uint32_t s = use % kSlots;
+      if (use >= kSlots && !mbar_wait(&sh.empty[s], (use / kSlots - 1) & 1u)) {
+        atomicOr(&sh.gave_up, 2u);
         ok = false;
         break;
       }
-      const uint32_t bytes = 16u * min(kSlotWords, words - piece * kSlotWords);
+      const uint32_t bytes = 16u * share.piece_words(j);
       mbar_expect_tx(&sh.full[s], bytes);
-      bulk_g2s(sh.slot[s], src + static_cast<int64_t>(piece) * kSlotBytes, bytes, &sh.full[s]);
-      ++loads;
-      ++piece;
-    }
-    if (!ok) break;
-    if (!kGrad) break;                     // every row has been issued
-    if (stores == loads) {
-      if (!more) break;
-      continue;
-    }
-    if (piece < pieces && rows_in - rows_out == 1 && freed < stores) {
-      // the consumers wait for the rest of this row, which may need the slot
-      // whose copy out was left running
-      bulk_wait_read_all();
-      freed = stores;
-      continue;
-    }
-    const int s = stores % kSlots;
-    if (!mbar_wait(&sh.done[s], (stores / kSlots) & 1u)) {
-      ok = false;
-      break;
-    }
-    const auto& p = sh.pending[rows_out % kPending];
-    if (bulk_out) {
-      bulk_s2g(p.dst + static_cast<int64_t>(out_piece) * kSlotBytes, sh.slot[s],
-               16u * min(kSlotWords, p.words - out_piece * kSlotWords));
-      bulk_commit();
-    }
-    ++stores;
-    if ((++out_piece) * kSlotWords >= p.words) {
-      out_piece = 0;
-      ++rows_out;
-    }
-    if (bulk_out) {
-      bulk_wait_read_all_but_one();
-      freed = stores - 1;
-    } else {
-      freed = stores;
+      bulk_g2s(sh.slot[s], share.base + static_cast<int64_t>(j) * kSlotBytes, bytes, &sh.full[s]);
     }
   }
-  if (!ok) {
-    atomicOr(&sh.gave_up, 2u);
-    // copies in flight land before the CTA may leave
-    for (uint32_t u = loads > kSlots ? loads - kSlots : 0; u < loads; ++u)
+  // after a wait that gave up, the copies in flight land before the CTA may leave
+  if (!ok)
+    for (uint32_t u = use > kSlots ? use - kSlots : 0; u < use; ++u)
       mbar_wait(&sh.full[u % kSlots], (u / kSlots) & 1u);
+}
+
+template <typename T>
+__device__ void store_rows(const LossArgs& a, RingShared& sh, bool bulk_out) {
+  const uint32_t rank = cluster_rank(), ranks = cluster_size();
+  uint32_t stores = 0, released = 0;
+  auto release_to = [&](uint32_t upto) {
+    for (; released < upto; ++released) mbar_arrive(&sh.empty[released % kSlots]);
+  };
+  // Waits on `bar`; where it is not ready at once, the copies still out are
+  // awaited first, so that nobody waits for a slot that this thread holds back.
+  auto await = [&](uint64_t* bar, uint32_t parity) -> bool {
+    if (mbar_try_wait(bar, parity)) return true;
+    bulk_wait_read_all();
+    release_to(stores);
+    if (mbar_wait(bar, parity)) return true;
+    atomicOr(&sh.gave_up, 512u);
+    return false;
+  };
+  for (uint32_t n = 0; await(&sh.queue_full[n % kQueue], (n / kQueue) & 1u); ++n) {
+    const int64_t row = sh.queue[n % kQueue].row;
+    const int kind = sh.queue[n % kQueue].kind;
+    mbar_arrive(&sh.queue_empty[n % kQueue]);
+    if (kind == kRowStop) break;
+    if (kind == kRowZero) continue;
+    const RowShare<T> share(static_cast<const T*>(a.logits) + row * a.stride, a.vocab, rank, ranks);
+    unsigned char* const out = reinterpret_cast<unsigned char*>(static_cast<T*>(a.dlogits) +
+                                                                row * a.dstride + share.first);
+    bool ok = true;
+    for (int j = 0; ok && j < share.pieces; ++j) {
+      const uint32_t s = stores % kSlots;
+      if (!(ok = await(&sh.done[s], (stores / kSlots) & 1u))) break;
+      if (bulk_out) {
+        bulk_s2g(out + static_cast<int64_t>(j) * kSlotBytes, sh.slot[s], 16u * share.piece_words(j));
+        bulk_commit();
+      }
+      ++stores;
+      if (stores - released > kStoresOut) {
+        bulk_wait_read_but<kStoresOut>();
+        release_to(stores - kStoresOut);
+      }
+    }
+    if (!ok) break;
   }
   bulk_wait_all();
 }
 
-// ---- consumers
+// ---- workers
+
+__device__ __forceinline__ void leave_row(RingShared& sh, uint32_t n) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(&sh.queue_empty[n % kQueue]);
+}
 
 template <typename T, int PASS>
-__device__ void consume(const LossArgs& a, RingShared& sh, bool bulk_out, double (&acc)[4]) {
+__device__ void sum_rows(const LossArgs& a, RingShared& sh, int warp) {
+  constexpr int kThreadsHere = sum_warps(PASS) * 32;
+  constexpr int kEach = kSlotWords / kThreadsHere;       // words per thread and full piece
+  constexpr int kRun = kEach < 2 ? kEach : 2;            // words summed together
   const uint32_t rank = cluster_rank(), ranks = cluster_size();
-  const int tid = threadIdx.x - 64, lane = tid & 31, warp = tid >> 5;
-  const float out_scale = a.inv_temp * (a.grad_scale != nullptr ? *a.grad_scale : 1.0f);
-  uint32_t use = 0, sums = 0;
-  for (uint32_t n = 0;; ++n) {
-    if (!mbar_wait(&sh.queue_full[n % kQueue], (n / kQueue) & 1u)) {
-      if (lane == 0) atomicOr(&sh.gave_up, 4u);
-      return;
-    }
+  const int lane = threadIdx.x & 31, tid = warp * 32 + lane;
+  uint32_t use = 0;
+  for (uint32_t n = 0; take_row(sh, n, 4u); ++n) {
     const QueueRow& q = sh.queue[n % kQueue];
-    const int64_t row = q.row;
     if (q.kind == kRowStop) return;
-    if (q.kind == kRowZero) {
-      T* const dz = static_cast<T*>(a.dlogits) + row * a.dstride;
-      const RowShare<T> share(dz, a.vocab, rank, ranks);
-      uint4* const out = reinterpret_cast<uint4*>(const_cast<unsigned char*>(share.base));
-      for (int i = tid; i < share.words; i += kConsumerThreads) out[i] = make_uint4(0, 0, 0, 0);
-      if (rank == 0 && tid < share.head) dz[tid] = from_f32<T>(0.0f);
-      if (rank == 0 && tid < share.tail) dz[a.vocab - 1 - tid] = from_f32<T>(0.0f);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.queue_empty[n % kQueue]);
-      continue;
-    }
-    const T* const z = static_cast<const T*>(a.logits) + row * a.stride;
-    const RowShare<T> share(z, a.vocab, rank, ranks);
-    // the ragged element this thread looks after: rank 0's first warp has them all
-    const bool ragged = rank == 0 && warp == 0 &&
-                        (lane < 8 ? lane < share.head : (lane < 16 && lane - 8 < share.tail));
-    RowSum r{kLowest, 0.0f};
-    float slope, logp = 0.0f, lse = 0.0f;
-    if (PASS != kPassGrad) {
-      for (int j = 0; j < share.pieces; ++j) {
-        const uint32_t u = use + j;
-        if (!mbar_wait(&sh.full[u % kSlots], (u / kSlots) & 1u)) {
-          if (lane == 0) atomicOr(&sh.gave_up, 8u);
+    if (q.kind == kRowLive) {
+      const RowShare<T> share(static_cast<const T*>(a.logits) + q.row * a.stride, a.vocab, rank,
+                              ranks);
+      RowSum r{kLowest, 0.0f};
+      for (int j = 0; j < share.pieces; ++j, ++use) {
+        const uint32_t slot = use % kSlots;
+        if (!mbar_wait(&sh.full[slot], (use / kSlots) & 1u)) {
+          atomicOr(&sh.gave_up, 8u);
           return;
         }
-        const uint4* const w = reinterpret_cast<const uint4*>(sh.slot[u % kSlots]);
+        const uint4* const w = reinterpret_cast<const uint4*>(sh.slot[slot]) + tid;
         const int words = share.piece_words(j);
         if (words == kSlotWords) {
 #pragma unroll
-          for (int i = 0; i < kSlotWords / kConsumerThreads; ++i)
-            add_word<T>(a, w[tid + i * kConsumerThreads], r);
+          for (int i = 0; i < kEach; i += kRun) {
+            uint4 v[kRun];
+#pragma unroll
+            for (int m = 0; m < kRun; ++m) v[m] = w[(i + m) * kThreadsHere];
+            add_words<T, kRun>(a, v, r);
+          }
         } else {
-          for (int i = tid; i < words; i += kConsumerThreads) add_word<T>(a, w[i], r);
+          for (int i = 0; tid + i < words; i += kThreadsHere) {
+            const uint4 v[1] = {w[i]};
+            add_words<T, 1>(a, v, r);
+          }
         }
         if (!writes_gradient(PASS)) {
           __syncwarp();
-          if (lane == 0) mbar_arrive(&sh.done[u % kSlots]);
+          if (lane == 0) mbar_arrive(&sh.empty[slot]);
         }
       }
-      if (ragged) {
-        const float x = q.edge[lane];
+      if (rank == 0 && warp == 0 && ragged_element(share, a.vocab, lane) >= 0) {
+        const float x = q.in[lane];
         r.raise(x * a.k);
         r.s += exp2_fast(arg(a, x, r.c));
       }
-      // join over the warp, then over all warps of the cluster: every warp
-      // leaves its pair in every CTA
-      r.join_warp();
-      float2* const part = sh.part[sums & 1u];
-      uint64_t* const bar = &sh.joined[sums & 1u];
-      if (lane < static_cast<int>(ranks)) {
-        cluster_store2(cluster_map(&part[rank * kConsumers + warp], lane), r.c, r.s);
-        cluster_arrive(cluster_map(bar, lane));
+      r.join_lanes();
+      if (lane == 0) {
+        sh.part[n % kQueue][warp] = make_float2(r.c, r.s);
+        mbar_arrive(&sh.summed[n % kQueue]);
       }
-      if (!mbar_wait_cluster(bar, (sums >> 1) & 1u)) {
-        if (lane == 0) atomicOr(&sh.gave_up, 16u);
+    } else if (lane == 0) {
+      mbar_arrive(&sh.summed[n % kQueue]);               // keeps the phases in step
+    }
+    leave_row(sh, n);
+  }
+}
+
+template <typename T, int PASS>
+__device__ void finish_rows(const LossArgs& a, RingShared& sh, double (&acc)[4]) {
+  const uint32_t rank = cluster_rank(), ranks = cluster_size();
+  const int lane = threadIdx.x & 31;
+  const float out_scale = a.inv_temp * (a.grad_scale != nullptr ? *a.grad_scale : 1.0f);
+  uint32_t joins = 0;
+  for (uint32_t n = 0; take_row(sh, n, 16u); ++n) {
+    const QueueRow& q = sh.queue[n % kQueue];
+    const int64_t row = q.row;
+    if (q.kind == kRowStop) return;
+    const int e = n % kQueue;
+    if (q.kind == kRowLive) {
+      if (!mbar_wait(&sh.summed[e], (n / kQueue) & 1u)) {
+        atomicOr(&sh.gave_up, 32u);
         return;
       }
-      ++sums;
-      r = RowSum{kLowest, 0.0f};
-      for (int i = lane; i < static_cast<int>(ranks) * kConsumers; i += 32)
-        r.join(part[i].x, part[i].y);
-      r.join_warp();
-      const Log2Sum l = log2_sum(r);
-      logp = logp_of(a, q.zy, l);
-      lse = lse_of(l);
-      if (policy_pass(PASS)) {
-        const PolicyTerm p = policy_term(a, q.policy, logp);
-        slope = p.slope;
-        if (tid == 0) {
-          acc[1] += p.policy;
-          acc[2] += p.kl;
-          acc[3] += p.clipped;
+      RowSum r{kLowest, 0.0f};
+      if (lane < sum_warps(PASS)) r = RowSum{sh.part[e][lane].x, sh.part[e][lane].y};
+      r.join_lanes<sum_warps(PASS)>();
+      if (ranks > 1) {
+        r = RowSum{__shfl_sync(kFull, r.c, 0), __shfl_sync(kFull, r.s, 0)};
+        const int b = joins % kJoins;
+        if (lane < static_cast<int>(ranks)) {
+          cluster_store2(cluster_map(&sh.cross[b][rank], lane), r.c, r.s);
+          cluster_arrive(cluster_map(&sh.joined[b], lane));
         }
-      }
-      if (rank == 0 && tid == 0) {
-        a.logps[row] = logp;
-        if (a.lse != nullptr) a.lse[row] = lse;
-        if (PASS == kPassPrefer || PASS == kPassPolicy) {
-          if (a.row_stat != nullptr) a.row_stat[row] = make_float2(r.c, r.s);
-          if (PASS == kPassPolicy && a.row_coef != nullptr) a.row_coef[row] = slope;
-        }
-      }
-    } else {
-      r.c = q.c;
-      r.s = q.s;
-      slope = q.slope;
-    }
-    if (writes_gradient(PASS)) {
-      const float coef = slope * out_scale;
-      const float f = -coef / r.s;
-      T* const dz = static_cast<T*>(a.dlogits) + row * a.dstride;
-      for (int j = 0; j < share.pieces; ++j) {
-        const uint32_t u = use + j;
-        if (PASS == kPassGrad && !mbar_wait(&sh.full[u % kSlots], (u / kSlots) & 1u)) {
-          if (lane == 0) atomicOr(&sh.gave_up, 8u);
+        if (!mbar_wait_cluster(&sh.joined[b], (joins / kJoins) & 1u)) {
+          atomicOr(&sh.gave_up, 64u);
           return;
         }
-        uint4* const w = reinterpret_cast<uint4*>(sh.slot[u % kSlots]);
-        const int words = share.piece_words(j);
-        // the token's place relative to the piece's first element
-        const int64_t first = share.first + static_cast<int64_t>(j) * kSlotWords * kPerWord<T>;
-        const int at = static_cast<int>(max(min(q.y - first, (int64_t)INT32_MAX), (int64_t)-1));
-        auto one = [&](int i) {
-          const int rel = at < 0 ? -1 : at - i * kPerWord<T>;
-          const uint4 d = grad_word<T>(a, w[i], r.c, f, coef, rel);
-          if (bulk_out) {
-            w[i] = d;
-          } else {
-            const T* const e = reinterpret_cast<const T*>(&d);
-#pragma unroll
-            for (int m = 0; m < kPerWord<T>; ++m) dz[first + i * kPerWord<T> + m] = e[m];
-          }
-        };
-        if (words == kSlotWords) {
-#pragma unroll
-          for (int i = 0; i < kSlotWords / kConsumerThreads; ++i) one(tid + i * kConsumerThreads);
-        } else {
-          for (int i = tid; i < words; i += kConsumerThreads) one(i);
-        }
-        if (bulk_out) fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.done[u % kSlots]);
+        ++joins;
+        r = RowSum{kLowest, 0.0f};
+        if (lane < static_cast<int>(ranks)) r = RowSum{sh.cross[b][lane].x, sh.cross[b][lane].y};
+        r.join_lanes<kMaxCluster>();
       }
-      if (ragged) {
-        const int e = lane < 8 ? lane : a.vocab - share.tail + lane - 8;
-        float d = exp2_fast(grad_arg<T>(a, q.edge[lane], r.c)) * f;
-        if (e == q.y) d += coef;
-        dz[e] = from_f32<T>(d);
+      const Log2Sum l = log2_sum(r);
+      const float logp = logp_of(a, q.in[kInToken], l);
+      float slope = 0.0f;
+      if (policy_pass(PASS)) {
+        const PolicyTerm p = policy_term(a, {q.in[kInWeight], q.in[kInAdvantage], q.in[kInOld], q.in[kInRef]}, logp);
+        slope = p.slope;
+        acc[1] += p.policy;
+        acc[2] += p.kl;
+        acc[3] += p.clipped;
+      }
+      if (lane == 0) {
+        if (writes_gradient(PASS)) {
+          const float coef = slope * out_scale;
+          sh.result[e] = {r.c, -coef / r.s, coef, 0.0f};
+        }
+        if (rank == 0) {
+          a.logps[row] = logp;
+          if (a.lse != nullptr) a.lse[row] = lse_of(l);
+          if ((PASS == kPassPrefer || PASS == kPassPolicy) && a.row_stat != nullptr) {
+            a.row_stat[row] = make_float2(r.c, r.s);
+            if (PASS == kPassPolicy) a.row_coef[row] = slope;
+          }
+        }
       }
     }
-    use += share.pieces;
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&sh.queue_empty[n % kQueue]);
+    if (writes_gradient(PASS) && lane == 0) mbar_arrive(&sh.ready[e]);
+    leave_row(sh, n);
+  }
+}
+
+template <typename T, int PASS>
+__device__ void grad_rows(const LossArgs& a, RingShared& sh, int warp, bool bulk_out) {
+  constexpr int kThreadsHere = grad_warps(PASS) * 32;
+  constexpr int kEach = kSlotWords / (kThreadsHere > 0 ? kThreadsHere : 1);
+  const uint32_t rank = cluster_rank(), ranks = cluster_size();
+  const int lane = threadIdx.x & 31, tid = warp * 32 + lane;
+  const float out_scale = a.inv_temp * (a.grad_scale != nullptr ? *a.grad_scale : 1.0f);
+  uint32_t use = 0;
+  for (uint32_t n = 0; take_row(sh, n, 128u); ++n) {
+    const QueueRow& q = sh.queue[n % kQueue];
+    if (q.kind == kRowStop) return;
+    const int e = n % kQueue;
+    T* const dz = static_cast<T*>(a.dlogits) + q.row * a.dstride;
+    if (sums(PASS) && !mbar_wait(&sh.ready[e], (n / kQueue) & 1u)) {
+      atomicOr(&sh.gave_up, 256u);
+      return;
+    }
+    if (q.kind == kRowZero) {
+      const RowShare<T> share(dz, a.vocab, rank, ranks);
+      uint4* const out = reinterpret_cast<uint4*>(const_cast<unsigned char*>(share.base));
+      for (int i = tid; i < share.words; i += kThreadsHere) out[i] = make_uint4(0, 0, 0, 0);
+      if (rank == 0 && tid < share.head) dz[tid] = from_f32<T>(0.0f);
+      if (rank == 0 && tid < share.tail) dz[a.vocab - 1 - tid] = from_f32<T>(0.0f);
+      leave_row(sh, n);
+      continue;
+    }
+    const RowShare<T> share(static_cast<const T*>(a.logits) + q.row * a.stride, a.vocab, rank,
+                            ranks);
+    float c, f, coef;
+    if (sums(PASS)) {
+      c = sh.result[e].c;
+      f = sh.result[e].f;
+      coef = sh.result[e].coef;
+    } else {
+      c = q.in[kInReference];
+      coef = q.in[kInSlope] * out_scale;
+      f = -coef / q.in[kInSum];
+    }
+    // the token's place relative to this thread's first word
+    const int64_t from = share.first + tid * kPerWord<T>;
+    const int at = static_cast<int>(q.y - from);            // vocab is at most 2^30
+    for (int j = 0; j < share.pieces; ++j, ++use) {
+      const uint32_t slot = use % kSlots;
+      if (!sums(PASS) && !mbar_wait(&sh.full[slot], (use / kSlots) & 1u)) {
+        atomicOr(&sh.gave_up, 8u);
+        return;
+      }
+      uint4* const w = reinterpret_cast<uint4*>(sh.slot[slot]) + tid;
+      const int words = share.piece_words(j);
+      const int at_piece = at - j * (kSlotWords * kPerWord<T>);
+      auto one = [&](int i) {
+        const uint4 d = grad_word<T>(a, w[i], c, f, coef, at_piece - i * kPerWord<T>);
+        if (bulk_out) {
+          w[i] = d;
+        } else {
+          const T* const el = reinterpret_cast<const T*>(&d);
+          T* const out = dz + from + (static_cast<int64_t>(j) * kSlotWords + i) * kPerWord<T>;
+#pragma unroll
+          for (int m = 0; m < kPerWord<T>; ++m) out[m] = el[m];
+        }
+      };
+      if (words == kSlotWords) {
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) one(i * kThreadsHere);
+      } else {
+        for (int i = 0; tid + i < words; i += kThreadsHere) one(i);
+      }
+      if (bulk_out) fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.done[slot]);
+    }
+    const int el = rank == 0 && warp == 0 ? ragged_element(share, a.vocab, lane) : -1;
+    if (el >= 0) {
+      float d = exp2_fast(grad_arg<T>(a, q.in[lane], c)) * f;
+      if (el == q.y) d += coef;
+      dz[el] = from_f32<T>(d);
+    }
+    leave_row(sh, n);
   }
 }
 
@@ -481,31 +567,44 @@ __global__ void __launch_bounds__(kRingThreads, 1) ring_kernel(const LossArgs a,
   if (threadIdx.x == 0) {
     for (int i = 0; i < kSlots; ++i) {
       mbar_init(&sh.full[i], 1);
-      mbar_init(&sh.done[i], kConsumers);
+      mbar_init(&sh.done[i], grad_warps(PASS) > 0 ? grad_warps(PASS) : 1);
+      mbar_init(&sh.empty[i], writes_gradient(PASS) ? 1 : sum_warps(PASS));
     }
     for (int i = 0; i < kQueue; ++i) {
       mbar_init(&sh.queue_full[i], 1);
-      mbar_init(&sh.queue_empty[i], kConsumers + 1);
+      // the loader, the workers and, where there are any, finisher and storer
+      mbar_init(&sh.queue_empty[i],
+                1 + kWorkers + (sums(PASS) ? 1 : 0) + (writes_gradient(PASS) ? 1 : 0));
+      mbar_init(&sh.summed[i], sums(PASS) ? sum_warps(PASS) : 1);
+      mbar_init(&sh.ready[i], 1);
     }
-    for (int i = 0; i < 2; ++i) mbar_init(&sh.joined[i], kConsumers * ranks);
+    for (int i = 0; i < kJoins; ++i) mbar_init(&sh.joined[i], ranks);
     sh.gave_up = 0u;
     fence_mbar_init();
   }
   cluster_sync();
   double acc[4] = {0.0, 0.0, 0.0, 0.0};
-  if (threadIdx.x < 32) {
-    if (threadIdx.x == 0) produce<T, PASS>(a, sh, bulk_out != 0);
-  } else if (threadIdx.x < 64) {
+  const int warp = threadIdx.x >> 5;
+  if (warp == 0) {
+    if (threadIdx.x == 0) load_rows<T>(a, sh);
+  } else if (warp == 1) {
     schedule<T, PASS>(a, sh);
+  } else if (warp == 2) {
+    if constexpr (sums(PASS)) finish_rows<T, PASS>(a, sh, acc);
+  } else if (warp == 3) {
+    if (writes_gradient(PASS) && (threadIdx.x & 31) == 0) store_rows<T>(a, sh, bulk_out != 0);
+  } else if (warp - kFirstWorker < sum_warps(PASS)) {
+    if constexpr (sums(PASS)) sum_rows<T, PASS>(a, sh, warp - kFirstWorker);
   } else {
-    consume<T, PASS>(a, sh, bulk_out != 0, acc);
+    if constexpr (writes_gradient(PASS))
+      grad_rows<T, PASS>(a, sh, warp - kFirstWorker - sum_warps(PASS), bulk_out != 0);
   }
   __syncwarp();
   // no CTA leaves while another may still write to its shared memory
   cluster_sync();
   if (threadIdx.x == 0 && sh.gave_up != 0u) atomicOr(a.fault, sh.gave_up);
   if (policy_pass(PASS) && cluster_rank() == 0) {
-    // the sums sit in the first consumer thread
+    // the sums sit in the finisher
     __shared__ double s_acc[4];
     if (threadIdx.x == 64)
       for (int i = 0; i < 4; ++i) s_acc[i] = acc[i];
@@ -622,14 +721,14 @@ cudaLaunchConfig_t ring_config(int clusters, int size, cudaStream_t s, cudaLaunc
   return c;
 }
 
-// CTAs per row.  A gradient pass keeps a CTA's share of the row in the ring
-// until the row's sum is known and wants room beside it to fetch the next row:
-// at most 8 of the 13 slots.  With fewer rows than half the clusters, the rows
-// are cut finer, down to one slot per CTA.
+// CTAs per row.  Where a share of the row waits in the ring for the row's sum,
+// room beside it for the next rows is worth more CTAs per row: at most
+// kSharePieces of the kSlots.  With fewer rows than half the clusters, rows are
+// cut finer, down to one slot per CTA.
 int cluster_for(int pass, int64_t rows, int64_t row_bytes, int sms) {
   int size = 1;
   if (pass == kPassPolicyGrad)
-    while (size < kMaxCluster && row_bytes > 8LL * kSlotBytes * size) size *= 2;
+    while (size < kMaxCluster && row_bytes > 1LL * kSharePieces * kSlotBytes * size) size *= 2;
   while (size < kMaxCluster && rows * size * 2 <= sms && row_bytes > kSlotBytes * size) size *= 2;
   return size;
 }

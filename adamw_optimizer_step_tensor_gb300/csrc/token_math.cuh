@@ -51,6 +51,34 @@ __device__ __forceinline__ float grad_arg(const LossArgs& a, float z, float c) {
   return std::is_same<T, float>::value ? arg(a, z, c) : fmaf(z, a.k, -c);
 }
 
+// Two float32 operations per instruction.
+__device__ __forceinline__ float2 fma2(float2 x, float2 y, float2 z) {
+  float2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<unsigned long long&>(r))
+      : "l"(reinterpret_cast<const unsigned long long&>(x)),
+        "l"(reinterpret_cast<const unsigned long long&>(y)),
+        "l"(reinterpret_cast<const unsigned long long&>(z)));
+  return r;
+}
+__device__ __forceinline__ float2 add2(float2 x, float2 y) {
+  float2 r;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<unsigned long long&>(r))
+      : "l"(reinterpret_cast<const unsigned long long&>(x)),
+        "l"(reinterpret_cast<const unsigned long long&>(y)));
+  return r;
+}
+__device__ __forceinline__ float2 mul2(float2 x, float2 y) {
+  float2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<unsigned long long&>(r))
+      : "l"(reinterpret_cast<const unsigned long long&>(x)),
+        "l"(reinterpret_cast<const unsigned long long&>(y)));
+  return r;
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
 // Integer reference c and S = sum 2^(z k - c).
 struct RowSum {
   float c, s;
@@ -66,9 +94,10 @@ struct RowSum {
     s = s * exp2_fast(c - hi) + s2 * exp2_fast(c2 - hi);
     c = hi;
   }
-  __device__ __forceinline__ void join_warp() {
+  template <int LANES = 32>
+  __device__ __forceinline__ void join_lanes() {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
+    for (int o = LANES / 2; o > 0; o >>= 1)
       join(__shfl_xor_sync(kFull, c, o), __shfl_xor_sync(kFull, s, o));
   }
 };
@@ -123,74 +152,82 @@ __device__ __forceinline__ PolicyTerm policy_term(const LossArgs& a, const Polic
   return r;
 }
 
-// ---- 16-byte words of a row: 8 or 4 elements
+// ---- 16-byte words of a row: 8 or 4 elements, in pairs
 template <typename T> constexpr int kPerWord = 16 / sizeof(T);
 
 template <typename T>
-__device__ __forceinline__ void unpack(const uint4& w, float (&x)[kPerWord<T>]) {
+__device__ __forceinline__ void unpack(const uint4& w, float2 (&x)[kPerWord<T> / 2]) {
   const uint32_t v[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if constexpr (sizeof(T) == 4) {
-      x[i] = __uint_as_float(v[i]);
-    } else if constexpr (std::is_same<T, __half>::value) {
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&v[i]));
-      x[2 * i] = f.x;
-      x[2 * i + 1] = f.y;
-    } else {
-      x[2 * i] = __uint_as_float(v[i] << 16);
-      x[2 * i + 1] = __uint_as_float(v[i] & 0xFFFF0000u);
-    }
-  }
-}
-template <typename T>
-__device__ __forceinline__ uint4 pack(const float (&x)[kPerWord<T>]) {
-  uint32_t v[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if constexpr (sizeof(T) == 4) {
-      v[i] = __float_as_uint(x[i]);
-    } else if constexpr (std::is_same<T, __half>::value) {
-      const __half2 h = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
-      v[i] = *reinterpret_cast<const uint32_t*>(&h);
-    } else {
-      const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-      v[i] = *reinterpret_cast<const uint32_t*>(&h);
-    }
-  }
-  return make_uint4(v[0], v[1], v[2], v[3]);
-}
-
-// The largest element of a word, NaN ignored (16-bit types two at a time).
-template <typename T>
-__device__ __forceinline__ float word_max(const uint4& w) {
   if constexpr (sizeof(T) == 4) {
-    return fmaxf(fmaxf(__uint_as_float(w.x), __uint_as_float(w.y)),
-                 fmaxf(__uint_as_float(w.z), __uint_as_float(w.w)));
-  } else if constexpr (std::is_same<T, __half>::value) {
-    const __half2* h = reinterpret_cast<const __half2*>(&w);
-    const float2 f = __half22float2(__hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3])));
-    return fmaxf(f.x, f.y);
+    x[0] = make_float2(__uint_as_float(v[0]), __uint_as_float(v[1]));
+    x[1] = make_float2(__uint_as_float(v[2]), __uint_as_float(v[3]));
   } else {
-    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&w);
-    const float2 f = __bfloat1622float2(__hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3])));
-    return fmaxf(f.x, f.y);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (std::is_same<T, __half>::value)
+        x[i] = __half22float2(*reinterpret_cast<const __half2*>(&v[i]));
+      else
+        x[i] = make_float2(__uint_as_float(v[i] << 16), __uint_as_float(v[i] & 0xFFFF0000u));
+    }
+  }
+}
+template <typename T>
+__device__ __forceinline__ uint4 pack(const float2 (&x)[kPerWord<T> / 2]) {
+  if constexpr (sizeof(T) == 4) {
+    return make_uint4(__float_as_uint(x[0].x), __float_as_uint(x[0].y), __float_as_uint(x[1].x),
+                      __float_as_uint(x[1].y));
+  } else {
+    uint32_t v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (std::is_same<T, __half>::value) {
+        const __half2 h = __float22half2_rn(x[i]);
+        v[i] = *reinterpret_cast<const uint32_t*>(&h);
+      } else {
+        const __nv_bfloat162 h = __float22bfloat162_rn(x[i]);
+        v[i] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+    }
+    return make_uint4(v[0], v[1], v[2], v[3]);
   }
 }
 
-// Adds a word's exponentials to the row's sum.
-template <typename T>
-__device__ __forceinline__ void add_word(const LossArgs& a, const uint4& w, RowSum& r) {
-  r.raise(word_max<T>(w) * a.k);
-  float x[kPerWord<T>];
-  unpack<T>(w, x);
-  float t[4];
+// The largest element of N words, NaN ignored (16-bit types two at a time).
+template <typename T, int N>
+__device__ __forceinline__ float words_max(const uint4 (&w)[N]) {
+  if constexpr (sizeof(T) == 4) {
+    float m = kLowest;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if constexpr (sizeof(T) == 4) t[i] = exp2_fast(arg(a, x[i], r.c));
-    else t[i] = exp2_fast(arg(a, x[2 * i], r.c)) + exp2_fast(arg(a, x[2 * i + 1], r.c));
+    for (int i = 0; i < N; ++i)
+      m = fmaxf(m, fmaxf(fmaxf(__uint_as_float(w[i].x), __uint_as_float(w[i].y)),
+                         fmaxf(__uint_as_float(w[i].z), __uint_as_float(w[i].w))));
+    return m;
+  } else {
+    using T2 = typename std::conditional<std::is_same<T, __half>::value, __half2, __nv_bfloat162>::type;
+    T2 m = reinterpret_cast<const T2*>(&w[0])[0];
+#pragma unroll
+    for (int i = 1; i < 4 * N; ++i) m = __hmax2(m, reinterpret_cast<const T2*>(&w[i / 4])[i % 4]);
+    return fmaxf(to_f32(m.x), to_f32(m.y));
   }
-  r.s += (t[0] + t[1]) + (t[2] + t[3]);
+}
+
+// Adds the exponentials of N words to the row's sum.
+template <typename T, int N>
+__device__ __forceinline__ void add_words(const LossArgs& a, const uint4 (&w)[N], RowSum& r) {
+  r.raise(words_max<T, N>(w) * a.k);
+  const float2 k = both(a.k), k_lo = both(a.k_lo), c = both(-r.c);
+  float2 t = make_float2(0.0f, 0.0f);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    float2 x[kPerWord<T> / 2];
+    unpack<T>(w[i], x);
+#pragma unroll
+    for (int j = 0; j < kPerWord<T> / 2; ++j) {
+      const float2 e = fma2(x[j], k_lo, fma2(x[j], k, c));
+      t = add2(t, make_float2(exp2_fast(e.x), exp2_fast(e.y)));
+    }
+  }
+  r.s += t.x + t.y;
 }
 
 // The gradient of a word's logits: 2^a_j * f, plus coef at the token's place
@@ -198,14 +235,20 @@ __device__ __forceinline__ void add_word(const LossArgs& a, const uint4& w, RowS
 template <typename T>
 __device__ __forceinline__ uint4 grad_word(const LossArgs& a, const uint4& w, float c, float f,
                                            float coef, int at) {
-  float x[kPerWord<T>];
+  float2 x[kPerWord<T> / 2];
   unpack<T>(w, x);
 #pragma unroll
-  for (int i = 0; i < kPerWord<T>; ++i) x[i] = exp2_fast(grad_arg<T>(a, x[i], c)) * f;
+  for (int j = 0; j < kPerWord<T> / 2; ++j) {
+    float2 e = fma2(x[j], both(a.k), both(-c));
+    if (std::is_same<T, float>::value) e = fma2(x[j], both(a.k_lo), e);
+    x[j] = mul2(make_float2(exp2_fast(e.x), exp2_fast(e.y)), both(f));
+  }
   if (static_cast<unsigned>(at) < kPerWord<T>) {
 #pragma unroll
-    for (int i = 0; i < kPerWord<T>; ++i)
-      if (i == at) x[i] += coef;
+    for (int j = 0; j < kPerWord<T> / 2; ++j) {
+      if (2 * j == at) x[j].x += coef;
+      if (2 * j + 1 == at) x[j].y += coef;
+    }
   }
   return pack<T>(x);
 }

@@ -524,7 +524,7 @@ typedef struct {
                              row without a token: it is not read and counts for nothing */
   int64_t rows;           /* 0 .. the plan's max_rows                         */
   int64_t row_stride;     /* elements, >= vocab                                */
-  int32_t vocab;          /* >= 1                                              */
+  int32_t vocab;          /* 1 .. 2^30 (EUNSUPPORTED above)                    */
   int32_t label_bytes;    /* 4 or 8                                            */
   int32_t dtype;          /* adamw_dtype of the logits and their gradient      */
   float temperature;      /* > 0: the distribution is softmax(logits / temperature) */
