@@ -21,7 +21,7 @@ OUT = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT, "libadamw.so")
 SOURCES = ["capi.cpp", "qmap.cpp", "step_kernels.cu", "bulk_kernels.cu", "small_kernels.cu",
            "aux_kernels.cu", "noalloc.cu", "mini_kernels.cu", "q4_kernels.cu", "operators_capi.cpp",
-           "grad_norm.cu", "token_loss.cu", "layer_norm.cu"]
+           "grad_norm.cu", "token_loss.cu", "token_loss_small.cu", "layer_norm.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

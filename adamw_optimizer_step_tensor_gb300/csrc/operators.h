@@ -66,6 +66,7 @@ constexpr int kLossMaxCtas = 4096;   // partial sums the plan holds
 struct LossLimits {
   int sms;
   int clusters[4];             // clusters of 1, 2, 4, 8 CTAs resident at once
+  int small_ctas[3][4];        // per adamw_dtype: resident CTAs of the small-vocabulary kernels
 };
 cudaError_t prepare_token_loss(int sms, LossLimits* lim);
 cudaError_t launch_token_loss(adamw_dtype dt, LossKind kind, const LossArgs& a,

@@ -24,18 +24,18 @@
 #include <cmath>
 
 #include "cluster.cuh"
-#include "token_math.cuh"
+#include "token_rows.cuh"
 
 namespace adamw {
 namespace {
 
-constexpr int kSlotBytes = 16384;
+constexpr int kSlotWords = kPieceWords;
+constexpr int kSlotBytes = kSlotWords * 16;
 constexpr int kSlots = 13;
-constexpr int kSlotWords = kSlotBytes / 16;
 constexpr int kWorkers = 16;                    // summing and gradient warps together
 constexpr int kFirstWorker = 4;                 // after loader, scheduler, finisher, storer
 constexpr int kRingThreads = (kFirstWorker + kWorkers) * 32;
-constexpr int kQueue = 8;                       // rows handed on ahead
+constexpr int kQueue = 16;                      // rows handed on ahead
 // Cluster-wide sums under way: a finisher is through with sum n only after the
 // others have taken it up, and they do that after they are through with n - 1,
 // so two places are enough.
@@ -44,24 +44,8 @@ constexpr int kStoresOut = 3;                   // copies out whose slots may be
 constexpr int kMaxCluster = 8;
 constexpr int kRowsPerLane = 8;                 // rows the scheduler looks at per lane and step
 constexpr int kBatch = 4;                       // rows whose inputs it fetches together
-constexpr int kSharePieces = 4;                 // of a row that waits for its sum, at most
+constexpr int kSharePieces = 7;                 // of a row that waits for its sum, at most
 
-// What a launch does with each live row.
-enum Pass {
-  kPassLogps,        // log-probabilities
-  kPassPolicy,       // and the policy term
-  kPassPolicyGrad,   // and the gradient
-  kPassPrefer,       // log-probabilities, reference and sum kept for kPassGrad
-  kPassGrad          // gradients of rows whose reference, sum and slope are known
-};
-__host__ __device__ constexpr bool writes_gradient(int pass) {
-  return pass == kPassPolicyGrad || pass == kPassGrad;
-}
-__host__ __device__ constexpr bool policy_pass(int pass) {
-  return pass == kPassPolicy || pass == kPassPolicyGrad;
-}
-
-__host__ __device__ constexpr bool sums(int pass) { return pass != kPassGrad; }
 // Warps of either kind; a pass with one kind gives it all of them.
 __host__ __device__ constexpr int sum_warps(int pass) {
   return !sums(pass) ? 0 : (writes_gradient(pass) ? kWorkers / 2 : kWorkers);
@@ -105,51 +89,6 @@ struct RingShared {
   uint32_t gave_up;
 };
 
-// A row of logits as this CTA sees it: elements off the 16-byte grid at either
-// end, and its share of the 16-byte words between.
-template <typename T>
-struct RowShare {
-  const unsigned char* base;  // the CTA's first word
-  int64_t first;              // the element that word starts with
-  int head, tail;             // ragged elements of the whole row
-  int words, pieces;
-  __device__ __forceinline__ RowShare(const T* z, int vocab, uint32_t rank, uint32_t ranks) {
-    const uintptr_t lo = reinterpret_cast<uintptr_t>(z);
-    const uintptr_t hi = lo + static_cast<uintptr_t>(vocab) * sizeof(T);
-    const uintptr_t lo16 = (lo + 15) & ~static_cast<uintptr_t>(15);
-    const uintptr_t hi16 = hi & ~static_cast<uintptr_t>(15);
-    if (lo16 >= hi16) {       // no whole word: every element is ragged (at most 14)
-      head = hi <= lo16 ? vocab : static_cast<int>((lo16 - lo) / sizeof(T));
-      tail = vocab - head;
-      words = pieces = 0;
-      base = nullptr;
-      first = 0;
-      return;
-    }
-    head = static_cast<int>((lo16 - lo) / sizeof(T));
-    tail = static_cast<int>((hi - hi16) / sizeof(T));
-    const int64_t all = static_cast<int64_t>((hi16 - lo16) / 16);
-    // ranks is a power of two; shares start on 128-byte steps of the words
-    const int64_t per = (((all + ranks - 1) >> (__ffs(ranks) - 1)) + 7) & ~static_cast<int64_t>(7);
-    const int64_t from = min(per * rank, all);
-    words = static_cast<int>(min(per, all - from));
-    pieces = (words + kSlotWords - 1) / kSlotWords;
-    base = reinterpret_cast<const unsigned char*>(lo16) + from * 16;
-    first = head + from * kPerWord<T>;
-  }
-  __device__ __forceinline__ int piece_words(int j) const {
-    return min(kSlotWords, words - j * kSlotWords);
-  }
-};
-
-// The element off the 16-byte grid that lane `lane` looks after, or -1: the
-// row's first elements on lanes 0.., its last on lanes 8...
-template <typename T>
-__device__ __forceinline__ int ragged_element(const RowShare<T>& share, int vocab, int lane) {
-  if (lane < 8) return lane < share.head ? lane : -1;
-  return lane < 16 && lane - 8 < share.tail ? vocab - share.tail + lane - 8 : -1;
-}
-
 // ---- scheduler
 
 // Lane `lane`'s input of a row.
@@ -188,27 +127,39 @@ __device__ void schedule(const LossArgs& a, RingShared& sh) {
   uint32_t sent = 0;
   int64_t base = 0;                            // rows looked at
   int held = 0, next = 0;                      // rows in sh.dealt, and the first not sent yet
+  // labels and weights of the next step's rows, on their way while this step's
+  // rows are dealt
+  int64_t ahead_y[kRowsPerLane];
+  float ahead_w[kRowsPerLane];
+  auto look = [&](int64_t at) {
+    const float* const weights = PASS == kPassGrad ? a.row_coef : a.weights;
+#pragma unroll
+    for (int u = 0; u < kRowsPerLane; ++u) {
+      const int64_t i = at + 32 * u + lane;
+      // gradients of known rows run from the last row to the first: the pass
+      // before ended there, so the end of the logits is still in L2
+      const int64_t t = PASS == kPassGrad ? a.rows - 1 - i : i;
+      ahead_y[u] = i < a.rows ? label_of(a, t) : -1;
+      ahead_w[u] = i < a.rows && weights != nullptr ? weights[t] : 1.0f;
+    }
+  };
+  look(0);
   for (;;) {
     if (next == held) next = held = 0;
     while (held - next < kBatch && held <= kBatch && base < a.rows) {
       int64_t y[kRowsPerLane];
-      bool live[kRowsPerLane];
+      float w[kRowsPerLane];
 #pragma unroll
       for (int u = 0; u < kRowsPerLane; ++u) {
-        const int64_t i = base + 32 * u + lane;
-        // gradients of known rows run from the last row to the first: the pass
-        // before ended there, so the end of the logits is still in L2
-        const int64_t t = PASS == kPassGrad ? a.rows - 1 - i : i;
-        const bool in = i < a.rows;
-        y[u] = in ? label_of(a, t) : -1;
-        if (PASS == kPassGrad) live[u] = in && a.row_coef[t] != 0.0f;
-        else live[u] = in && (a.weights == nullptr || a.weights[t] != 0.0f);
+        y[u] = ahead_y[u];
+        w[u] = ahead_w[u];
       }
+      look(base + 32 * kRowsPerLane);
 #pragma unroll
       for (int u = 0; u < kRowsPerLane; ++u) {
         const int64_t i = base + 32 * u + lane;
         const int64_t t = PASS == kPassGrad ? a.rows - 1 - i : i;
-        const bool is_live = live[u] && y[u] >= 0 && y[u] < a.vocab;
+        const bool is_live = w[u] != 0.0f && y[u] >= 0 && y[u] < a.vocab;
         const uint32_t on = __ballot_sync(kFull, is_live);
         const uint32_t off = __ballot_sync(kFull, i < a.rows && !is_live);
         const uint32_t before = (1u << lane) - 1u;
@@ -649,8 +600,8 @@ __device__ double sequence_sum(const LossArgs& a, int64_t lo, int64_t hi, double
 }
 
 // -log sigmoid(d)
-__device__ __forceinline__ double minus_log_sigmoid(double d) {
-  return log1p(exp(-fabs(d))) + fmax(-d, 0.0);
+__device__ __forceinline__ float minus_log_sigmoid(float d) {
+  return log1pf(expf(-fabsf(d))) + fmaxf(-d, 0.0f);
 }
 
 // One CTA per pair: both sequences' rewards, the pair's loss, and
@@ -667,11 +618,12 @@ __global__ void __launch_bounds__(kPairThreads) pair_kernel(const LossArgs a) {
     hi[side] = min(max(static_cast<int64_t>(a.starts[s + 1]), lo[side]), a.rows);
     sum[side] = sequence_sum(a, lo[side], hi[side], s_warp);
   }
-  const double beta = a.beta, e = a.smoothing;
-  const double chosen = beta * sum[0], rejected = beta * sum[1], d = chosen - rejected;
+  const double beta = a.beta, chosen = beta * sum[0], rejected = beta * sum[1];
+  const float e = a.smoothing, d = static_cast<float>(chosen - rejected);
   // d loss / d d = e - sigmoid(-d), over the pairs' mean
-  const double sig = d >= 0.0 ? exp(-d) / (1.0 + exp(-d)) : 1.0 / (1.0 + exp(d));
-  const float slope = static_cast<float>((e - sig) * beta / a.pairs);
+  const float t = expf(-fabsf(d));
+  const float sig = d >= 0.0f ? t / (1.0f + t) : 1.0f / (1.0f + t);
+  const float slope = (e - sig) * a.beta / static_cast<float>(a.pairs);
   if (threadIdx.x == 0) {
     a.rewards[p] = static_cast<float>(chosen);
     a.rewards[p + a.pairs] = static_cast<float>(rejected);
@@ -682,8 +634,8 @@ __global__ void __launch_bounds__(kPairThreads) pair_kernel(const LossArgs a) {
       float w;
       if (pref_live(a, t, w)) a.row_coef[t] = w * (side == 0 ? slope : -slope);
     }
-  const double mine[4] = {(1.0 - e) * minus_log_sigmoid(d) + e * minus_log_sigmoid(-d),
-                          d > 0.0 ? 1.0 : 0.0, chosen, rejected};
+  const double mine[4] = {(1.0f - e) * minus_log_sigmoid(d) + e * minus_log_sigmoid(-d),
+                          d > 0.0f ? 1.0 : 0.0, chosen, rejected};
   double out[4];
   if (last_cta_sums(mine, a.partial, a.ticket, blockIdx.x, gridDim.x, out))
     for (int i = 0; i < 4; ++i) a.stats[i] = static_cast<float>(out[i] / a.pairs);
@@ -733,20 +685,29 @@ int cluster_for(int pass, int64_t rows, int64_t row_bytes, int sms) {
   return size;
 }
 
+template <typename T>
+constexpr int dtype_index() {
+  return std::is_same<T, float>::value ? ADAMW_F32
+                                       : (std::is_same<T, __half>::value ? ADAMW_F16 : ADAMW_BF16);
+}
+
 template <typename T, int PASS>
-cudaError_t launch_ring(const LossArgs& a, const LossLimits& lim, cudaStream_t s) {
-  const int size = cluster_for(PASS, a.rows, static_cast<int64_t>(a.vocab) * sizeof(T), lim.sms);
-  int most = lim.clusters[size == 1 ? 0 : size == 2 ? 1 : size == 4 ? 2 : 3];
-  const int clusters = static_cast<int>(a.rows < 1 ? 1 : (a.rows < most ? a.rows : most));
-  // the bulk copies out need every gradient row at its logits' offset from the
-  // 16-byte grid
-  const bool bulk_out =
+cudaError_t launch_pass(const LossArgs& a, const LossLimits& lim, cudaStream_t s) {
+  // the wide stores and bulk copies out need every gradient row at its logits'
+  // offset from the 16-byte grid
+  const bool same_grid =
       a.dlogits != nullptr &&
       ((reinterpret_cast<uintptr_t>(a.dlogits) - reinterpret_cast<uintptr_t>(a.logits)) % 16 == 0) &&
       (((a.dstride - a.stride) * static_cast<int64_t>(sizeof(T))) % 16 == 0);
+  if (a.vocab <= kSmallVocabBytes / static_cast<int>(sizeof(T)))
+    return launch_small_vocab<T>(static_cast<Pass>(PASS), a, same_grid,
+                                 lim.small_ctas[dtype_index<T>()], s);
+  const int size = cluster_for(PASS, a.rows, static_cast<int64_t>(a.vocab) * sizeof(T), lim.sms);
+  int most = lim.clusters[size == 1 ? 0 : size == 2 ? 1 : size == 4 ? 2 : 3];
+  const int clusters = static_cast<int>(a.rows < 1 ? 1 : (a.rows < most ? a.rows : most));
   cudaLaunchAttribute attr;
   const cudaLaunchConfig_t c = ring_config(clusters, size, s, &attr);
-  return cudaLaunchKernelEx(&c, ring_kernel<T, PASS>, a, bulk_out ? 1 : 0);
+  return cudaLaunchKernelEx(&c, ring_kernel<T, PASS>, a, same_grid ? 1 : 0);
 }
 
 template <typename T>
@@ -754,26 +715,26 @@ cudaError_t launch_typed(LossKind kind, LossArgs a, const LossLimits& lim, cudaS
   const int64_t row_bytes = static_cast<int64_t>(a.vocab) * sizeof(T);
   cudaError_t e;
   switch (kind) {
-    case kLossLogps: return launch_ring<T, kPassLogps>(a, lim, s);
+    case kLossLogps: return launch_pass<T, kPassLogps>(a, lim, s);
     case kLossPolicy:
       if (a.dlogits == nullptr) {
         a.row_stat = nullptr;
         a.row_coef = nullptr;
-        return launch_ring<T, kPassPolicy>(a, lim, s);
+        return launch_pass<T, kPassPolicy>(a, lim, s);
       }
       // a share must fit the ring whole
       if (row_bytes <= static_cast<int64_t>(kSlots - 1) * kSlotBytes * kMaxCluster)
-        return launch_ring<T, kPassPolicyGrad>(a, lim, s);
+        return launch_pass<T, kPassPolicyGrad>(a, lim, s);
       e = cudaMemsetAsync(a.row_coef, 0, a.rows * sizeof(float), s);
-      if (e == cudaSuccess) e = launch_ring<T, kPassPolicy>(a, lim, s);
-      if (e == cudaSuccess && a.rows > 0) e = launch_ring<T, kPassGrad>(a, lim, s);
+      if (e == cudaSuccess) e = launch_pass<T, kPassPolicy>(a, lim, s);
+      if (e == cudaSuccess && a.rows > 0) e = launch_pass<T, kPassGrad>(a, lim, s);
       return e;
     case kLossPrefer:
-      e = launch_ring<T, kPassPrefer>(a, lim, s);
+      e = launch_pass<T, kPassPrefer>(a, lim, s);
       if (e != cudaSuccess) return e;
       pair_kernel<<<a.pairs, kPairThreads, 0, s>>>(a);
       if ((e = cudaGetLastError()) != cudaSuccess) return e;
-      if (a.dlogits != nullptr && a.rows > 0) e = launch_ring<T, kPassGrad>(a, lim, s);
+      if (a.dlogits != nullptr && a.rows > 0) e = launch_pass<T, kPassGrad>(a, lim, s);
       return e;
   }
   return cudaErrorInvalidValue;
@@ -785,6 +746,9 @@ cudaError_t prepare_token_loss(int sms, LossLimits* lim) {
   cudaError_t e = prepare_typed<float>();
   if (e == cudaSuccess) e = prepare_typed<__half>();
   if (e == cudaSuccess) e = prepare_typed<__nv_bfloat16>();
+  if (e == cudaSuccess) e = prepare_small_vocab<float>(sms, lim->small_ctas[ADAMW_F32]);
+  if (e == cudaSuccess) e = prepare_small_vocab<__half>(sms, lim->small_ctas[ADAMW_F16]);
+  if (e == cudaSuccess) e = prepare_small_vocab<__nv_bfloat16>(sms, lim->small_ctas[ADAMW_BF16]);
   lim->sms = sms;
   for (int i = 0; e == cudaSuccess && i < 4; ++i) {
     cudaLaunchAttribute attr;
