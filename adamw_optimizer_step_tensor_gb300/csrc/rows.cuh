@@ -4,6 +4,7 @@
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+#include <cuda_runtime.h>
 
 #include <cstdint>
 #include <type_traits>
@@ -38,6 +39,21 @@ __device__ __forceinline__ float block_sum(float x, float* s_warp) {
 #pragma unroll
   for (int i = 0; i < THREADS / 32; ++i) t += s_warp[i];
   return t;
+}
+
+// Kernels launched with early_start() may come up while the kernel before them
+// on the stream still runs; they wait here before they touch memory.  Without
+// it, wait_for_previous_kernel returns at once.
+__device__ __forceinline__ void wait_for_previous_kernel() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+__device__ __forceinline__ void let_next_kernel_start() {
+  asm volatile("griddepcontrol.launch_dependents;");
+}
+inline unsigned early_start(cudaLaunchAttribute* attr) {
+  attr->id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr->val.programmaticStreamSerializationAllowed = 1;
+  return 1;
 }
 
 // CTA `me` of `ctas` leaves four float64 sums (its thread 0's `mine`); the last

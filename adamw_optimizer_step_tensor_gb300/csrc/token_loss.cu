@@ -31,7 +31,7 @@ namespace {
 
 constexpr int kSlotWords = kPieceWords;
 constexpr int kSlotBytes = kSlotWords * 16;
-constexpr int kSlots = 13;
+constexpr int kMaxSlots = 13;
 constexpr int kWorkers = 16;                    // summing and gradient warps together
 constexpr int kFirstWorker = 4;                 // after loader, scheduler, finisher, storer
 constexpr int kRingThreads = (kFirstWorker + kWorkers) * 32;
@@ -51,6 +51,21 @@ __host__ __device__ constexpr int sum_warps(int pass) {
   return !sums(pass) ? 0 : (writes_gradient(pass) ? kWorkers / 2 : kWorkers);
 }
 __host__ __device__ constexpr int grad_warps(int pass) { return kWorkers - sum_warps(pass); }
+// Workers form teams, and the teams take a row's pieces in turn.  Where nothing
+// waits for a row as a whole, teams of 4 warps: a warp then waits once for 8
+// words per lane instead of once for every two, and the teams' waits overlap
+// (6080 rows of 50,257: 128 -> 108 us).  Where the gradient waits for the sum,
+// all summing warps take every piece, so that the row's sum is there sooner
+// (8192 rows of 128,256: 595 us against 683).  The slots are a multiple of the
+// teams: a team meets a slot's uses one after the other, as the parity of its
+// barrier needs.
+__host__ __device__ constexpr int team_warps(int pass) {
+  return sums(pass) && writes_gradient(pass) ? kWorkers / 2 : 4;
+}
+__host__ __device__ constexpr int slots(int pass) {
+  return sums(pass) && writes_gradient(pass) ? kMaxSlots : kMaxSlots / (kWorkers / 4) * (kWorkers / 4);
+}
+static_assert(kWorkers % 8 == 0, "whole teams");
 
 enum RowKind { kRowLive, kRowZero, kRowStop };
 // A row's inputs, one per scheduler lane: its elements off the 16-byte grid (the
@@ -71,7 +86,7 @@ struct QueueRow : DealtRow {
 };
 
 struct RingShared {
-  alignas(128) unsigned char slot[kSlots][kSlotBytes];
+  alignas(128) unsigned char slot[kMaxSlots][kSlotBytes];
   QueueRow queue[kQueue];
   DealtRow dealt[kBatch + 32 * kRowsPerLane];   // this cluster's next rows, scheduler only
   float2 part[kQueue][kWorkers];          // (c, s) of every summing warp
@@ -79,9 +94,9 @@ struct RingShared {
   struct {
     float c, f, coef, pad;
   } result[kQueue];                       // what the gradient warps need of a row
-  uint64_t full[kSlots];      // a slot's copy has landed
-  uint64_t done[kSlots];      // a slot's gradients are in place
-  uint64_t empty[kSlots];     // a slot may be filled again
+  uint64_t full[kMaxSlots];      // a slot's copy has landed
+  uint64_t done[kMaxSlots];      // a slot's gradients are in place
+  uint64_t empty[kMaxSlots];     // a slot may be filled again
   uint64_t queue_full[kQueue], queue_empty[kQueue];
   uint64_t summed[kQueue];    // a row's `part` is complete
   uint64_t joined[kJoins];    // a row's `cross` is complete
@@ -127,61 +142,86 @@ __device__ void schedule(const LossArgs& a, RingShared& sh) {
   uint32_t sent = 0;
   int64_t base = 0;                            // rows looked at
   int held = 0, next = 0;                      // rows in sh.dealt, and the first not sent yet
-  // labels and weights of the next step's rows, on their way while this step's
-  // rows are dealt
+  // labels and weights of the next step's rows (kRowsPerLane neighbours on each
+  // lane), on their way while this step's rows are dealt
   int64_t ahead_y[kRowsPerLane];
   float ahead_w[kRowsPerLane];
+  // gradients of known rows run from the last row to the first: the pass before
+  // ended there, so the end of the logits is still in L2
+  auto row_at = [&](int64_t i) { return PASS == kPassGrad ? a.rows - 1 - i : i; };
   auto look = [&](int64_t at) {
     const float* const weights = PASS == kPassGrad ? a.row_coef : a.weights;
 #pragma unroll
     for (int u = 0; u < kRowsPerLane; ++u) {
-      const int64_t i = at + 32 * u + lane;
-      // gradients of known rows run from the last row to the first: the pass
-      // before ended there, so the end of the logits is still in L2
-      const int64_t t = PASS == kPassGrad ? a.rows - 1 - i : i;
-      ahead_y[u] = i < a.rows ? label_of(a, t) : -1;
-      ahead_w[u] = i < a.rows && weights != nullptr ? weights[t] : 1.0f;
+      const int64_t i = at + lane * kRowsPerLane + u;
+      ahead_y[u] = i < a.rows ? label_of(a, row_at(i)) : -1;
+      ahead_w[u] = i < a.rows && weights != nullptr ? weights[row_at(i)] : 1.0f;
     }
   };
   look(0);
   for (;;) {
     if (next == held) next = held = 0;
     while (held - next < kBatch && held <= kBatch && base < a.rows) {
-      int64_t y[kRowsPerLane];
-      float w[kRowsPerLane];
+      int32_t y[kRowsPerLane];
+      uint32_t live = 0u;                      // bit u: row u of this lane is live
 #pragma unroll
       for (int u = 0; u < kRowsPerLane; ++u) {
-        y[u] = ahead_y[u];
-        w[u] = ahead_w[u];
+        y[u] = static_cast<int32_t>(ahead_y[u]);
+        if (ahead_w[u] != 0.0f && ahead_y[u] >= 0 && ahead_y[u] < a.vocab) live |= 1u << u;
       }
       look(base + 32 * kRowsPerLane);
+      const int64_t first = base + lane * kRowsPerLane;
+      const int mine_in = static_cast<int>(max(min(a.rows - first, (int64_t)kRowsPerLane), (int64_t)0));
+      const uint32_t dead = ((1u << mine_in) - 1u) & ~live;
+      // counts of live and dead rows before this lane's, packed in one scan
+      uint32_t scan = __popc(live) | __popc(dead) << 16;
+      const uint32_t own = scan;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t up = __shfl_up_sync(kFull, scan, o);
+        if (lane >= o) scan += up;
+      }
+      const uint32_t total = __shfl_sync(kFull, scan, 31);
+      uint32_t live_at = (live_turn + ((scan - own) & 0xFFFFu)) % clusters;
+      uint32_t dead_at = (zero_turn + ((scan - own) >> 16)) % clusters;
+      live_turn = (live_turn + (total & 0xFFFFu)) % clusters;
+      zero_turn = (zero_turn + (total >> 16)) % clusters;
+      uint32_t send = 0u;
 #pragma unroll
       for (int u = 0; u < kRowsPerLane; ++u) {
-        const int64_t i = base + 32 * u + lane;
-        const int64_t t = PASS == kPassGrad ? a.rows - 1 - i : i;
-        const bool is_live = w[u] != 0.0f && y[u] >= 0 && y[u] < a.vocab;
-        const uint32_t on = __ballot_sync(kFull, is_live);
-        const uint32_t off = __ballot_sync(kFull, i < a.rows && !is_live);
-        const uint32_t before = (1u << lane) - 1u;
-        const uint32_t turn = is_live ? (live_turn + __popc(on & before)) % clusters
-                                      : (zero_turn + __popc(off & before)) % clusters;
-        const bool mine = i < a.rows && turn == me;
-        live_turn = (live_turn + __popc(on)) % clusters;
-        zero_turn = (zero_turn + __popc(off)) % clusters;
+        const bool on = (live >> u) & 1u;
+        bool mine;
+        if (on) {
+          mine = live_at == me;
+          live_at = live_at + 1 == clusters ? 0 : live_at + 1;
+        } else {
+          mine = ((dead >> u) & 1u) && dead_at == me;
+          dead_at = dead_at + 1 == clusters ? 0 : dead_at + 1;
+        }
+        if (mine && (on || writes_gradient(PASS))) send |= 1u << u;
         if (mine && rank == 0) {
+          const int64_t t = row_at(first + u);
           if (PASS == kPassPrefer) a.row_coef[t] = 0.0f;
-          if (PASS != kPassGrad && !is_live) {
+          if (PASS != kPassGrad && !on) {
             a.logps[t] = 0.0f;
             if (a.lse != nullptr) a.lse[t] = 0.0f;
           }
         }
-        const bool send = mine && (is_live || writes_gradient(PASS));
-        const uint32_t sends = __ballot_sync(kFull, send);
-        if (send)
-          sh.dealt[held + __popc(sends & before)] = {t, is_live ? kRowLive : kRowZero,
-                                                     static_cast<int32_t>(y[u])};
-        held += __popc(sends);
       }
+      int place = __popc(send);
+      const int count = place;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int up = __shfl_up_sync(kFull, place, o);
+        if (lane >= o) place += up;
+      }
+      const int sends = __shfl_sync(kFull, place, 31);
+      place += held - count;
+#pragma unroll
+      for (int u = 0; u < kRowsPerLane; ++u)
+        if ((send >> u) & 1u)
+          sh.dealt[place++] = {row_at(first + u), (live >> u) & 1u ? kRowLive : kRowZero, y[u]};
+      held += sends;
       base += 32 * kRowsPerLane;
       __syncwarp();
     }
@@ -223,8 +263,9 @@ __device__ __forceinline__ bool take_row(RingShared& sh, uint32_t n, uint32_t si
   return false;
 }
 
-template <typename T>
+template <typename T, int PASS>
 __device__ void load_rows(const LossArgs& a, RingShared& sh) {
+  constexpr int kSlots = slots(PASS);
   const uint32_t rank = cluster_rank(), ranks = cluster_size();
   uint32_t use = 0;
   bool ok = true;
@@ -253,8 +294,9 @@ __device__ void load_rows(const LossArgs& a, RingShared& sh) {
       mbar_wait(&sh.full[u % kSlots], (u / kSlots) & 1u);
 }
 
-template <typename T>
+template <typename T, int PASS>
 __device__ void store_rows(const LossArgs& a, RingShared& sh, bool bulk_out) {
+  constexpr int kSlots = slots(PASS);
   const uint32_t rank = cluster_rank(), ranks = cluster_size();
   uint32_t stores = 0, released = 0;
   auto release_to = [&](uint32_t upto) {
@@ -307,11 +349,13 @@ __device__ __forceinline__ void leave_row(RingShared& sh, uint32_t n) {
 
 template <typename T, int PASS>
 __device__ void sum_rows(const LossArgs& a, RingShared& sh, int warp) {
-  constexpr int kThreadsHere = sum_warps(PASS) * 32;
-  constexpr int kEach = kSlotWords / kThreadsHere;       // words per thread and full piece
-  constexpr int kRun = kEach < 2 ? kEach : 2;            // words summed together
+  constexpr int kTeam = team_warps(PASS), kTeams = sum_warps(PASS) / kTeam;
+  constexpr int kThreadsHere = kTeam * 32;
+  constexpr int kSlots = slots(PASS);
+  constexpr int kRun = 2;                                // words summed together
   const uint32_t rank = cluster_rank(), ranks = cluster_size();
-  const int lane = threadIdx.x & 31, tid = warp * 32 + lane;
+  const uint32_t team = warp / kTeam;
+  const int lane = threadIdx.x & 31, tid = (warp % kTeam) * 32 + lane;
   uint32_t use = 0;
   for (uint32_t n = 0; take_row(sh, n, 4u); ++n) {
     const QueueRow& q = sh.queue[n % kQueue];
@@ -321,6 +365,7 @@ __device__ void sum_rows(const LossArgs& a, RingShared& sh, int warp) {
                               ranks);
       RowSum r{kLowest, 0.0f};
       for (int j = 0; j < share.pieces; ++j, ++use) {
+        if (use % kTeams != team) continue;
         const uint32_t slot = use % kSlots;
         if (!mbar_wait(&sh.full[slot], (use / kSlots) & 1u)) {
           atomicOr(&sh.gave_up, 8u);
@@ -330,7 +375,7 @@ __device__ void sum_rows(const LossArgs& a, RingShared& sh, int warp) {
         const int words = share.piece_words(j);
         if (words == kSlotWords) {
 #pragma unroll
-          for (int i = 0; i < kEach; i += kRun) {
+          for (int i = 0; i < kSlotWords / kThreadsHere; i += kRun) {
             uint4 v[kRun];
 #pragma unroll
             for (int m = 0; m < kRun; ++m) v[m] = w[(i + m) * kThreadsHere];
@@ -382,9 +427,8 @@ __device__ void finish_rows(const LossArgs& a, RingShared& sh, double (&acc)[4])
       }
       RowSum r{kLowest, 0.0f};
       if (lane < sum_warps(PASS)) r = RowSum{sh.part[e][lane].x, sh.part[e][lane].y};
-      r.join_lanes<sum_warps(PASS)>();
+      r.join_lanes();
       if (ranks > 1) {
-        r = RowSum{__shfl_sync(kFull, r.c, 0), __shfl_sync(kFull, r.s, 0)};
         const int b = joins % kJoins;
         if (lane < static_cast<int>(ranks)) {
           cluster_store2(cluster_map(&sh.cross[b][rank], lane), r.c, r.s);
@@ -397,7 +441,7 @@ __device__ void finish_rows(const LossArgs& a, RingShared& sh, double (&acc)[4])
         ++joins;
         r = RowSum{kLowest, 0.0f};
         if (lane < static_cast<int>(ranks)) r = RowSum{sh.cross[b][lane].x, sh.cross[b][lane].y};
-        r.join_lanes<kMaxCluster>();
+        r.join_lanes();
       }
       const Log2Sum l = log2_sum(r);
       const float logp = logp_of(a, q.in[kInToken], l);
@@ -431,10 +475,12 @@ __device__ void finish_rows(const LossArgs& a, RingShared& sh, double (&acc)[4])
 
 template <typename T, int PASS>
 __device__ void grad_rows(const LossArgs& a, RingShared& sh, int warp, bool bulk_out) {
-  constexpr int kThreadsHere = grad_warps(PASS) * 32;
-  constexpr int kEach = kSlotWords / (kThreadsHere > 0 ? kThreadsHere : 1);
+  constexpr int kTeam = team_warps(PASS), kTeams = grad_warps(PASS) / kTeam;
+  constexpr int kThreadsHere = kTeam * 32;
+  constexpr int kSlots = slots(PASS), kAllThreads = grad_warps(PASS) * 32;
   const uint32_t rank = cluster_rank(), ranks = cluster_size();
-  const int lane = threadIdx.x & 31, tid = warp * 32 + lane;
+  const uint32_t team = warp / kTeam;
+  const int lane = threadIdx.x & 31, tid = (warp % kTeam) * 32 + lane;
   const float out_scale = a.inv_temp * (a.grad_scale != nullptr ? *a.grad_scale : 1.0f);
   uint32_t use = 0;
   for (uint32_t n = 0; take_row(sh, n, 128u); ++n) {
@@ -449,9 +495,10 @@ __device__ void grad_rows(const LossArgs& a, RingShared& sh, int warp, bool bulk
     if (q.kind == kRowZero) {
       const RowShare<T> share(dz, a.vocab, rank, ranks);
       uint4* const out = reinterpret_cast<uint4*>(const_cast<unsigned char*>(share.base));
-      for (int i = tid; i < share.words; i += kThreadsHere) out[i] = make_uint4(0, 0, 0, 0);
-      if (rank == 0 && tid < share.head) dz[tid] = from_f32<T>(0.0f);
-      if (rank == 0 && tid < share.tail) dz[a.vocab - 1 - tid] = from_f32<T>(0.0f);
+      for (int i = warp * 32 + lane; i < share.words; i += kAllThreads)
+        out[i] = make_uint4(0, 0, 0, 0);
+      const int el = rank == 0 && warp == 0 ? ragged_element(share, a.vocab, lane) : -1;
+      if (el >= 0) dz[el] = from_f32<T>(0.0f);
       leave_row(sh, n);
       continue;
     }
@@ -471,6 +518,7 @@ __device__ void grad_rows(const LossArgs& a, RingShared& sh, int warp, bool bulk
     const int64_t from = share.first + tid * kPerWord<T>;
     const int at = static_cast<int>(q.y - from);            // vocab is at most 2^30
     for (int j = 0; j < share.pieces; ++j, ++use) {
+      if (use % kTeams != team) continue;
       const uint32_t slot = use % kSlots;
       if (!sums(PASS) && !mbar_wait(&sh.full[slot], (use / kSlots) & 1u)) {
         atomicOr(&sh.gave_up, 8u);
@@ -492,7 +540,7 @@ __device__ void grad_rows(const LossArgs& a, RingShared& sh, int warp, bool bulk
       };
       if (words == kSlotWords) {
 #pragma unroll
-        for (int i = 0; i < kEach; ++i) one(i * kThreadsHere);
+        for (int i = 0; i < kSlotWords / kThreadsHere; ++i) one(i * kThreadsHere);
       } else {
         for (int i = 0; tid + i < words; i += kThreadsHere) one(i);
       }
@@ -516,10 +564,10 @@ __global__ void __launch_bounds__(kRingThreads, 1) ring_kernel(const LossArgs a,
   RingShared& sh = *reinterpret_cast<RingShared*>(raw);
   const uint32_t ranks = cluster_size();
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kSlots; ++i) {
+    for (int i = 0; i < kMaxSlots; ++i) {
       mbar_init(&sh.full[i], 1);
-      mbar_init(&sh.done[i], grad_warps(PASS) > 0 ? grad_warps(PASS) : 1);
-      mbar_init(&sh.empty[i], writes_gradient(PASS) ? 1 : sum_warps(PASS));
+      mbar_init(&sh.done[i], team_warps(PASS));
+      mbar_init(&sh.empty[i], writes_gradient(PASS) ? 1 : team_warps(PASS));
     }
     for (int i = 0; i < kQueue; ++i) {
       mbar_init(&sh.queue_full[i], 1);
@@ -534,16 +582,18 @@ __global__ void __launch_bounds__(kRingThreads, 1) ring_kernel(const LossArgs a,
     fence_mbar_init();
   }
   cluster_sync();
+  let_next_kernel_start();
+  wait_for_previous_kernel();
   double acc[4] = {0.0, 0.0, 0.0, 0.0};
   const int warp = threadIdx.x >> 5;
   if (warp == 0) {
-    if (threadIdx.x == 0) load_rows<T>(a, sh);
+    if (threadIdx.x == 0) load_rows<T, PASS>(a, sh);
   } else if (warp == 1) {
     schedule<T, PASS>(a, sh);
   } else if (warp == 2) {
     if constexpr (sums(PASS)) finish_rows<T, PASS>(a, sh, acc);
   } else if (warp == 3) {
-    if (writes_gradient(PASS) && (threadIdx.x & 31) == 0) store_rows<T>(a, sh, bulk_out != 0);
+    if (writes_gradient(PASS) && (threadIdx.x & 31) == 0) store_rows<T, PASS>(a, sh, bulk_out != 0);
   } else if (warp - kFirstWorker < sum_warps(PASS)) {
     if constexpr (sums(PASS)) sum_rows<T, PASS>(a, sh, warp - kFirstWorker);
   } else {
@@ -573,67 +623,72 @@ __global__ void __launch_bounds__(kRingThreads, 1) ring_kernel(const LossArgs a,
 
 // ---- pairs
 
-constexpr int kPairThreads = 256;
+constexpr int kPairThreads = 1024;      // half of them per sequence
 
-__device__ __forceinline__ bool pref_live(const LossArgs& a, int64_t t, float& w) {
-  const int64_t y = label_of(a, t);
-  w = a.weights != nullptr ? a.weights[t] : 1.0f;
-  return w != 0.0f && y >= 0 && y < a.vocab;
-}
-// Sum over [lo, hi) of w (logp - ref), in every thread; rows without weight or
-// token add nothing.
-__device__ double sequence_sum(const LossArgs& a, int64_t lo, int64_t hi, double* s_warp) {
-  double x = 0.0;
-  for (int64_t t = lo + threadIdx.x; t < hi; t += kPairThreads) {
-    float w;
-    if (pref_live(a, t, w))
-      x += static_cast<double>(w) * (static_cast<double>(a.logps[t]) - a.ref_logps[t]);
+// A float32 sum with its rounding errors beside it (TwoSum, Knuth): 48 bits
+// without float64, which GB300 runs at 2 per SM and cycle.
+struct PairSum {
+  float s = 0.0f, e = 0.0f;
+  __device__ __forceinline__ void add(float x, float xe = 0.0f) {
+    const float t = s + x, b = t - s;
+    e += (s - (t - b)) + (x - b) + xe;
+    s = t;
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(kFull, x, o);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) s_warp[threadIdx.x >> 5] = x;
-  __syncthreads();
-  x = 0.0;
-  for (int i = 0; i < kPairThreads / 32; ++i) x += s_warp[i];
-  return x;
-}
+};
 
 // -log sigmoid(d)
 __device__ __forceinline__ float minus_log_sigmoid(float d) {
   return log1pf(expf(-fabsf(d))) + fmaxf(-d, 0.0f);
 }
 
-// One CTA per pair: both sequences' rewards, the pair's loss, and
-// d loss / d logp of their rows.
+// One CTA per pair, one half per sequence: both sequences' rewards
+// beta * sum of w (logp - ref) over their rows with a weight and a token, the
+// pair's loss, and d loss / d logp of those rows.
 __global__ void __launch_bounds__(kPairThreads) pair_kernel(const LossArgs a) {
-  __shared__ double s_warp[kPairThreads / 32];
-  const int p = blockIdx.x;
-  int64_t lo[2], hi[2];
-  double sum[2];
-#pragma unroll
-  for (int side = 0; side < 2; ++side) {
-    const int s = p + side * a.pairs;
-    lo[side] = min(max(static_cast<int64_t>(a.starts[s]), (int64_t)0), a.rows);
-    hi[side] = min(max(static_cast<int64_t>(a.starts[s + 1]), lo[side]), a.rows);
-    sum[side] = sequence_sum(a, lo[side], hi[side], s_warp);
+  constexpr int kHalf = kPairThreads / 2;
+  __shared__ float2 s_warp[kPairThreads / 32];
+  __shared__ float s_sum[2];
+  let_next_kernel_start();
+  wait_for_previous_kernel();
+  const int p = blockIdx.x, side = threadIdx.x / kHalf, tid = threadIdx.x % kHalf;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int q = p + side * a.pairs;
+  const int64_t lo = min(max(static_cast<int64_t>(a.starts[q]), (int64_t)0), a.rows);
+  const int64_t hi = min(max(static_cast<int64_t>(a.starts[q + 1]), lo), a.rows);
+  auto weight = [&](int64_t t) {
+    const int64_t y = label_of(a, t);
+    const float w = a.weights != nullptr ? a.weights[t] : 1.0f;
+    return y >= 0 && y < a.vocab ? w : 0.0f;
+  };
+  PairSum x;
+  for (int64_t t = lo + tid; t < hi; t += kHalf) {
+    const float lp = a.logps[t], ref = a.ref_logps[t], w = weight(t);
+    if (w != 0.0f) x.add(w * (lp - ref));
   }
-  const double beta = a.beta, chosen = beta * sum[0], rejected = beta * sum[1];
-  const float e = a.smoothing, d = static_cast<float>(chosen - rejected);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    x.add(__shfl_xor_sync(kFull, x.s, o), __shfl_xor_sync(kFull, x.e, o));
+  if (lane == 0) s_warp[warp] = make_float2(x.s, x.e);
+  __syncthreads();
+  if (tid < 32) {
+    x = PairSum{};
+    if (lane < kHalf / 32) x = PairSum{s_warp[warp + lane].x, s_warp[warp + lane].y};
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+      x.add(__shfl_xor_sync(kFull, x.s, o), __shfl_xor_sync(kFull, x.e, o));
+    if (lane == 0) s_sum[side] = a.beta * x.s + a.beta * x.e;
+  }
+  __syncthreads();
+  const float chosen = s_sum[0], rejected = s_sum[1], d = chosen - rejected, e = a.smoothing;
   // d loss / d d = e - sigmoid(-d), over the pairs' mean
-  const float t = expf(-fabsf(d));
-  const float sig = d >= 0.0f ? t / (1.0f + t) : 1.0f / (1.0f + t);
+  const float z = expf(-fabsf(d));
+  const float sig = d >= 0.0f ? z / (1.0f + z) : 1.0f / (1.0f + z);
   const float slope = (e - sig) * a.beta / static_cast<float>(a.pairs);
-  if (threadIdx.x == 0) {
-    a.rewards[p] = static_cast<float>(chosen);
-    a.rewards[p + a.pairs] = static_cast<float>(rejected);
+  if (tid == 0) a.rewards[q] = s_sum[side];
+  for (int64_t t = lo + tid; t < hi; t += kHalf) {
+    const float w = weight(t);
+    if (w != 0.0f) a.row_coef[t] = w * (side == 0 ? slope : -slope);
   }
-#pragma unroll
-  for (int side = 0; side < 2; ++side)
-    for (int64_t t = lo[side] + threadIdx.x; t < hi[side]; t += kPairThreads) {
-      float w;
-      if (pref_live(a, t, w)) a.row_coef[t] = w * (side == 0 ? slope : -slope);
-    }
   const double mine[4] = {(1.0f - e) * minus_log_sigmoid(d) + e * minus_log_sigmoid(-d),
                           d > 0.0f ? 1.0 : 0.0, chosen, rejected};
   double out[4];
@@ -675,7 +730,7 @@ cudaLaunchConfig_t ring_config(int clusters, int size, cudaStream_t s, cudaLaunc
 
 // CTAs per row.  Where a share of the row waits in the ring for the row's sum,
 // room beside it for the next rows is worth more CTAs per row: at most
-// kSharePieces of the kSlots.  With fewer rows than half the clusters, rows are
+// kSharePieces of the kMaxSlots.  With fewer rows than half the clusters, rows are
 // cut finer, down to one slot per CTA.
 int cluster_for(int pass, int64_t rows, int64_t row_bytes, int sms) {
   int size = 1;
@@ -705,9 +760,22 @@ cudaError_t launch_pass(const LossArgs& a, const LossLimits& lim, cudaStream_t s
   const int size = cluster_for(PASS, a.rows, static_cast<int64_t>(a.vocab) * sizeof(T), lim.sms);
   int most = lim.clusters[size == 1 ? 0 : size == 2 ? 1 : size == 4 ? 2 : 3];
   const int clusters = static_cast<int>(a.rows < 1 ? 1 : (a.rows < most ? a.rows : most));
-  cudaLaunchAttribute attr;
-  const cudaLaunchConfig_t c = ring_config(clusters, size, s, &attr);
+  cudaLaunchAttribute attr[2];
+  cudaLaunchConfig_t c = ring_config(clusters, size, s, attr);
+  // the second pass may come up while the one before drains
+  if (PASS == kPassGrad) c.numAttrs += early_start(&attr[1]);
   return cudaLaunchKernelEx(&c, ring_kernel<T, PASS>, a, same_grid ? 1 : 0);
+}
+
+cudaError_t launch_pairs(const LossArgs& a, cudaStream_t s) {
+  cudaLaunchAttribute attr;
+  cudaLaunchConfig_t c{};
+  c.gridDim = dim3(static_cast<unsigned>(a.pairs));
+  c.blockDim = dim3(kPairThreads);
+  c.stream = s;
+  c.attrs = &attr;
+  c.numAttrs = early_start(&attr);
+  return cudaLaunchKernelEx(&c, pair_kernel, a);
 }
 
 template <typename T>
@@ -723,7 +791,7 @@ cudaError_t launch_typed(LossKind kind, LossArgs a, const LossLimits& lim, cudaS
         return launch_pass<T, kPassPolicy>(a, lim, s);
       }
       // a share must fit the ring whole
-      if (row_bytes <= static_cast<int64_t>(kSlots - 1) * kSlotBytes * kMaxCluster)
+      if (row_bytes <= static_cast<int64_t>(kMaxSlots - 1) * kSlotBytes * kMaxCluster)
         return launch_pass<T, kPassPolicyGrad>(a, lim, s);
       e = cudaMemsetAsync(a.row_coef, 0, a.rows * sizeof(float), s);
       if (e == cudaSuccess) e = launch_pass<T, kPassPolicy>(a, lim, s);
@@ -732,8 +800,7 @@ cudaError_t launch_typed(LossKind kind, LossArgs a, const LossLimits& lim, cudaS
     case kLossPrefer:
       e = launch_pass<T, kPassPrefer>(a, lim, s);
       if (e != cudaSuccess) return e;
-      pair_kernel<<<a.pairs, kPairThreads, 0, s>>>(a);
-      if ((e = cudaGetLastError()) != cudaSuccess) return e;
+      if ((e = launch_pairs(a, s)) != cudaSuccess) return e;
       if (a.dlogits != nullptr && a.rows > 0) e = launch_pass<T, kPassGrad>(a, lim, s);
       return e;
   }

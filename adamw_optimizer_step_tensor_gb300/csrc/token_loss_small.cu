@@ -28,6 +28,8 @@ template <typename T, int G>
 __global__ void __launch_bounds__(kCta<G>, kThreadsPerSm / kCta<G>) small_vocab_kernel(const LossArgs a, const Pass pass,
                                                               const bool same_grid) {
   constexpr int kGroups = kCta<G> / G;
+  let_next_kernel_start();
+  wait_for_previous_kernel();
   __shared__ float2 s_part[2][kCta<G> / 32];
   const int group = threadIdx.x / G, tid = threadIdx.x % G;
   const int lane = tid & 31, warp = tid >> 5;
@@ -190,8 +192,15 @@ cudaError_t launch_group(Pass pass, const LossArgs& a, bool same_grid, int64_t r
   if (ctas > resident) ctas = resident;
   if (ctas > kLossMaxCtas) ctas = kLossMaxCtas;
   if (ctas < 1) ctas = 1;
-  small_vocab_kernel<T, G><<<static_cast<int>(ctas), kCta<G>, 0, s>>>(a, pass, same_grid);
-  return cudaGetLastError();
+  cudaLaunchAttribute attr;
+  cudaLaunchConfig_t c{};
+  c.gridDim = dim3(static_cast<unsigned>(ctas));
+  c.blockDim = dim3(kCta<G>);
+  c.stream = s;
+  c.attrs = &attr;
+  // the second pass may come up while the one before drains
+  c.numAttrs = pass == kPassGrad ? early_start(&attr) : 0;
+  return cudaLaunchKernelEx(&c, small_vocab_kernel<T, G>, a, pass, same_grid);
 }
 
 }  // namespace

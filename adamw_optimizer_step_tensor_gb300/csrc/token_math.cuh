@@ -94,11 +94,16 @@ struct RowSum {
     s = s * exp2_fast(c - hi) + s2 * exp2_fast(c2 - hi);
     c = hi;
   }
-  template <int LANES = 32>
+  // Over the warp, the same in every lane: the largest reference by an integer
+  // reduction (floats in integer order), then the sums at that reference.
   __device__ __forceinline__ void join_lanes() {
+    const int bits = __float_as_int(c);
+    const int top = __reduce_max_sync(kFull, bits ^ ((bits >> 31) & 0x7FFFFFFF));
+    const float hi = __int_as_float(top ^ ((top >> 31) & 0x7FFFFFFF));
+    s *= exp2_fast(c - hi);
+    c = hi;
 #pragma unroll
-    for (int o = LANES / 2; o > 0; o >>= 1)
-      join(__shfl_xor_sync(kFull, c, o), __shfl_xor_sync(kFull, s, o));
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kFull, s, o);
   }
 };
 

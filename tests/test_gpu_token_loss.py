@@ -422,6 +422,29 @@ def test_graph_replay():
     assert all(torch.equal(a, c) for a, c in zip(want, out))
 
 
+@pytest.mark.parametrize("vocab", [3000, 40_000])
+def test_preference_graph_replay(vocab):
+    """The three launches overlap at their ends; replayed back to back they give the same bits."""
+    b = Batch(400, vocab, torch.bfloat16)
+    ref = b.policy_inputs()[2]
+    loss = FusedTokenLoss(400, 7)
+    starts = dev(starts_of(400, 7, b.rng))
+    want = [t.clone() for t in loss.preference(b.logits, b.labels, b.w, ref, starts)]
+    out = [torch.zeros_like(t) for t in want]
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        for _ in range(3):
+            loss.preference(b.logits, b.labels, b.w, ref, starts, stats=out[0], rewards=out[1], logps=out[2],
+                            dlogits=out[3])
+    for _ in range(5):
+        for t in out:
+            t.fill_(-1.0)
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, c) for a, c in zip(want, out))
+
+
 def test_offsets_past_32_bits():
     rows, vocab = 17_000, 128_256           # 2.18e9 logits
     logits = torch.zeros(rows, vocab, dtype=torch.bfloat16, device="cuda")
