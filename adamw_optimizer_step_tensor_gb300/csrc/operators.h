@@ -63,10 +63,11 @@ struct LossArgs {
   uint32_t* fault;             // nonzero: a bounded wait gave up (bit per site)
 };
 constexpr int kLossMaxCtas = 4096;   // partial sums the plan holds
+constexpr int kSmallGroups = 5;      // group sizes of the small-vocabulary kernel
 struct LossLimits {
   int sms;
   int clusters[4];             // clusters of 1, 2, 4, 8 CTAs resident at once
-  int small_ctas[3][4];        // per adamw_dtype: resident CTAs of the small-vocabulary kernels
+  int small_ctas[3][kSmallGroups];        // per adamw_dtype: resident CTAs of the small-vocabulary kernels
 };
 cudaError_t prepare_token_loss(int sms, LossLimits* lim);
 cudaError_t launch_token_loss(adamw_dtype dt, LossKind kind, const LossArgs& a,

@@ -12,7 +12,9 @@ namespace adamw {
 namespace {
 
 constexpr int kWordsEach = 8;
-constexpr int kThreadsPerSm = 768;      // resident; 80 registers each
+// Resident threads per SM: 64 registers each where a row fills a CTA, 80 where
+// several rows share one.
+template <int G> constexpr int kThreadsPerSm = G >= 256 ? 1024 : 768;
 
 template <int G> constexpr int kCta = G < 128 ? 128 : G;
 
@@ -25,7 +27,7 @@ __device__ __forceinline__ void group_sync(int group) {
 }
 
 template <typename T, int G>
-__global__ void __launch_bounds__(kCta<G>, kThreadsPerSm / kCta<G>) small_vocab_kernel(const LossArgs a, const Pass pass,
+__global__ void __launch_bounds__(kCta<G>, kThreadsPerSm<G> / kCta<G>) small_vocab_kernel(const LossArgs a, const Pass pass,
                                                               const bool same_grid) {
   constexpr int kGroups = kCta<G> / G;
   let_next_kernel_start();
@@ -206,29 +208,31 @@ cudaError_t launch_group(Pass pass, const LossArgs& a, bool same_grid, int64_t r
 }  // namespace
 
 template <typename T>
-cudaError_t prepare_small_vocab(int sms, int (&ctas)[4]) {
+cudaError_t prepare_small_vocab(int sms, int (&ctas)[kSmallGroups]) {
   cudaError_t e = resident<T, 32>(&ctas[0]);
   if (e == cudaSuccess) e = resident<T, 64>(&ctas[1]);
   if (e == cudaSuccess) e = resident<T, 128>(&ctas[2]);
   if (e == cudaSuccess) e = resident<T, 256>(&ctas[3]);
+  if (e == cudaSuccess) e = resident<T, 512>(&ctas[4]);
   for (int& c : ctas) c *= sms;
   return e;
 }
 
 // The smallest group that holds the row: more rows at once per SM.
 template <typename T>
-cudaError_t launch_small_vocab(Pass pass, const LossArgs& a, bool same_grid, const int (&ctas)[4],
+cudaError_t launch_small_vocab(Pass pass, const LossArgs& a, bool same_grid, const int (&ctas)[kSmallGroups],
                                cudaStream_t s) {
   const int64_t words = static_cast<int64_t>(a.vocab) * sizeof(T) / 16;
   if (words <= 32 * kWordsEach) return launch_group<T, 32>(pass, a, same_grid, ctas[0], s);
   if (words <= 64 * kWordsEach) return launch_group<T, 64>(pass, a, same_grid, ctas[1], s);
   if (words <= 128 * kWordsEach) return launch_group<T, 128>(pass, a, same_grid, ctas[2], s);
-  return launch_group<T, 256>(pass, a, same_grid, ctas[3], s);
+  if (words <= 256 * kWordsEach) return launch_group<T, 256>(pass, a, same_grid, ctas[3], s);
+  return launch_group<T, 512>(pass, a, same_grid, ctas[4], s);
 }
 
 #define ADAMW_SMALL_VOCAB(T)                                                                 \
-  template cudaError_t prepare_small_vocab<T>(int, int (&)[4]);                              \
-  template cudaError_t launch_small_vocab<T>(Pass, const LossArgs&, bool, const int (&)[4], \
+  template cudaError_t prepare_small_vocab<T>(int, int (&)[kSmallGroups]);                              \
+  template cudaError_t launch_small_vocab<T>(Pass, const LossArgs&, bool, const int (&)[kSmallGroups], \
                                              cudaStream_t)
 ADAMW_SMALL_VOCAB(float);
 ADAMW_SMALL_VOCAB(__half);

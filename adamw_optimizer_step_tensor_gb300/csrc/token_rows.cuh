@@ -24,11 +24,11 @@ __host__ __device__ constexpr bool policy_pass(int pass) {
 __host__ __device__ constexpr bool sums(int pass) { return pass != kPassGrad; }
 // Vocabularies of up to this many bytes per row are held in registers
 // (token_loss_small.cu).
-constexpr int kSmallVocabBytes = 32768;
+constexpr int kSmallVocabBytes = 65536;
 template <typename T>
-cudaError_t prepare_small_vocab(int sms, int (&ctas)[4]);
+cudaError_t prepare_small_vocab(int sms, int (&ctas)[kSmallGroups]);
 template <typename T>
-cudaError_t launch_small_vocab(Pass pass, const LossArgs& a, bool same_grid, const int (&ctas)[4],
+cudaError_t launch_small_vocab(Pass pass, const LossArgs& a, bool same_grid, const int (&ctas)[kSmallGroups],
                                cudaStream_t s);
 
 namespace {
