@@ -96,6 +96,6 @@ cudaError_t launch_layer_norm_forward(adamw_dtype dt, adamw_dtype wdt, const Lay
 cudaError_t launch_layer_norm_backward(adamw_dtype dt, adamw_dtype wdt, const LayerNormArgs& a,
                                        int sms, cudaStream_t s);
 // Rows of column sums the backward pass keeps per plan.
-constexpr int kNormPartsPerSm = 2;
+constexpr int kNormPartsPerSm = 4;
 
 }  // namespace adamw
