@@ -99,6 +99,7 @@ _SIGNATURES = {
                                              ctypes.c_int64, _vp]),
     "adamw_layer_norm_plan_create": (ctypes.c_int, [ctypes.c_int32, ctypes.c_float, ctypes.POINTER(_vp)]),
     "adamw_layer_norm_plan_destroy": (ctypes.c_int, [_vp]),
+    "adamw_layer_norm_plan_status": (ctypes.c_int, [_vp, ctypes.POINTER(ctypes.c_uint32)]),
     "adamw_layer_norm_forward": (ctypes.c_int, [_vp, ctypes.c_int, ctypes.c_int, ctypes.c_int64, _vp,
                                                 ctypes.c_int64, _vp, _vp, _vp, ctypes.c_int64, _vp, _vp,
                                                 _vp]),
@@ -401,6 +402,13 @@ def adamw_layer_norm_plan_create(width: int, eps: float) -> int:
 
 def adamw_layer_norm_plan_destroy(plan: int) -> None:
     _check(load().adamw_layer_norm_plan_destroy(plan))
+
+
+def adamw_layer_norm_plan_status(plan: int) -> int:
+    """Fault bits of a layer norm plan's kernels; raises AdamWError (ETIMEOUT) if set."""
+    bits = ctypes.c_uint32()
+    _check(load().adamw_layer_norm_plan_status(plan, ctypes.byref(bits)))
+    return bits.value
 
 
 def adamw_layer_norm_forward(plan: int, dtype: int, weight_dtype: int, rows: int, x: int, x_stride: int,

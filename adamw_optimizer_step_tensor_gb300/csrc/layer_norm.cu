@@ -5,235 +5,411 @@
 //   dx = rstd (w dy - mean_j(w dy) - xhat mean_j(w dy xhat))
 //   dw = sum over rows of dy xhat,  db = sum over rows of dy
 //
-// A group of G threads holds a row in registers, 16 elements a thread, and a
-// resident grid walks the rows, the next row's loads under way while a row is
-// worked on.  A thread has the same columns of every row: the weight stays in
-// registers, and so do the column sums of the backward pass, which are added
-// over a CTA's groups, then over the CTAs by a second kernel, always in the same
-// order.  Statistics and sums are float32; the variance is the mean of squared
+// A group of G threads holds a row in registers, 16 or 32 elements a thread, and a
+// resident grid walks the rows, bulk copies (TMA engine) keeping each group's
+// next rows on their way into shared memory.  A thread has the same columns of
+// every row: the weight stays in registers, and so do the column sums of the
+// backward pass, which are added over a CTA's groups, then over the CTAs by a
+// second kernel, always in the same order.
+// Statistics and sums are float32; the variance is the mean of squared
 // differences from the mean (no cancellation).  What bounds both passes is
 // DRAM: two (three) accesses per element.  Rows wider than 8192 take the plain
 // loops at the end of this file.
+#include "async_copy.cuh"
 #include "operators.h"
 #include "rows.cuh"
 
 namespace adamw {
 namespace {
 
-constexpr int kEach = 16;              // elements per thread
-constexpr int kMaxGroup = 512;
+constexpr int kMaxWidth = 8192;        // of a row in registers
 template <int G> constexpr int kCta = G < 128 ? 128 : G;
-// Resident threads per SM, by the registers a thread needs: 80 in the forward
-// pass, 128 in the backward pass.
-constexpr int kForwardThreads = 768;
-constexpr int kBackwardThreads = 512;
+// Resident threads per SM, by the registers a thread with `each` elements needs.
+constexpr int forward_threads(bool vec, int each) {
+  return each == 16 ? (vec ? 1024 : 768) : 512;
+}
+constexpr int backward_threads(int each) { return each == 16 ? 512 : 256; }
+constexpr int kStages = 4;             // rows on their way per group, at most
+constexpr int kSmemPerSm = 184 * 1024;  // for the rows on their way
 
 template <typename W>
 __device__ __forceinline__ float param(const void* p, int j, float none) {
   return p != nullptr ? to_f32(static_cast<const W*>(p)[j]) : none;
 }
 
-// 16 elements of a row as loaded: 16-byte words where every row starts on the
+// A thread's EACH elements of a row as loaded: 16-byte words where every row starts on the
 // 16-byte grid, else single elements; thread tid has the columns
-// (i G + tid) E .. + E - 1.
-template <typename T, bool VEC, int G>
+// (i G + tid) E .. + E - 1.  The arithmetic takes them in pairs (two float32
+// operations per instruction: without, both passes issued 22 to 27 instructions
+// per element and were bound by that).
+template <typename T, bool VEC, int G, int EACH>
 struct Piece {
   static constexpr int E = VEC ? 16 / sizeof(T) : 1;
-  static constexpr int N = kEach / E;
+  static constexpr int N = EACH / E;
+  static constexpr int kPairs = EACH / 2;
   using Raw = typename std::conditional<VEC, uint4, T>::type;
   Raw raw[N];
 
-  static __device__ __forceinline__ int column(int i, int tid) { return (i * G + tid) * E; }
-  __device__ __forceinline__ void load(const T* row, int width, int tid) {
+  // Column of element m.
+  static __device__ __forceinline__ int column(int m, int tid) {
+    return (m / E * G + tid) * E + m % E;
+  }
+  static __device__ __forceinline__ Raw zero() {
+    if constexpr (VEC) return make_uint4(0u, 0u, 0u, 0u);
+    else return from_f32<T>(0.0f);
+  }
+  // From a row in shared memory; columns past the width read as 0.
+  __device__ __forceinline__ void load(const unsigned char* row, int width, int tid) {
 #pragma unroll
     for (int i = 0; i < N; ++i)
-      if (column(i, tid) < width)
-        raw[i] = __ldcs(reinterpret_cast<const Raw*>(row + column(i, tid)));
+      raw[i] = column(i * E, tid) < width ? reinterpret_cast<const Raw*>(row)[i * G + tid] : zero();
   }
-  // Element i * E + e; columns past the width hold garbage.
-  __device__ __forceinline__ float at(int i, int e) const {
+  __device__ __forceinline__ float2 pair(int k) const {
     if constexpr (!VEC) {
-      return to_f32(raw[i]);
+      return make_float2(to_f32(raw[2 * k]), to_f32(raw[2 * k + 1]));
+    } else if constexpr (sizeof(T) == 4) {
+      const uint4& r = raw[k / 2];
+      return k % 2 ? make_float2(__uint_as_float(r.z), __uint_as_float(r.w))
+                   : make_float2(__uint_as_float(r.x), __uint_as_float(r.y));
     } else {
-      const uint32_t v[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-      if constexpr (sizeof(T) == 4) return __uint_as_float(v[e]);
-      else if constexpr (std::is_same<T, __half>::value)
-        return __half2float(__ushort_as_half(static_cast<unsigned short>(v[e / 2] >> (e % 2 * 16))));
-      else return __uint_as_float(e % 2 ? v[e / 2] & 0xFFFF0000u : v[e / 2] << 16);
+      const uint4& r = raw[k / 4];
+      return unpack_pair<T>(k % 4 == 0 ? r.x : k % 4 == 1 ? r.y : k % 4 == 2 ? r.z : r.w);
     }
   }
-  // Stores f(i, e) at every column below the width, rounded once.
+  // x where pair k's columns lie below the width, else 0.
+  static __device__ __forceinline__ float2 inside(float2 x, int k, int width, int tid) {
+    if (column(2 * k, tid) >= width) x.x = 0.0f;
+    if (column(2 * k + 1, tid) >= width) x.y = 0.0f;
+    return x;
+  }
+  // Stores f(pair) at every column below the width, rounded once.
   template <typename F>
   static __device__ __forceinline__ void store(T* row, int width, int tid, F f) {
+    if constexpr (!VEC) {
 #pragma unroll
-    for (int i = 0; i < N; ++i)
-      if (column(i, tid) < width) {
-        alignas(16) T out[E];
-#pragma unroll
-        for (int e = 0; e < E; ++e) out[e] = from_f32<T>(f(i, e));
-        __stcs(reinterpret_cast<Raw*>(row + column(i, tid)), *reinterpret_cast<const Raw*>(out));
+      for (int k = 0; k < kPairs; ++k) {
+        const float2 x = f(k);
+        if (column(2 * k, tid) < width) row[column(2 * k, tid)] = from_f32<T>(x.x);
+        if (column(2 * k + 1, tid) < width) row[column(2 * k + 1, tid)] = from_f32<T>(x.y);
       }
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        if (column(i * E, tid) >= width) continue;
+        uint4 out;
+        if constexpr (sizeof(T) == 4) {
+          const float2 x = f(2 * i), y = f(2 * i + 1);
+          out = make_uint4(__float_as_uint(x.x), __float_as_uint(x.y), __float_as_uint(y.x),
+                           __float_as_uint(y.y));
+        } else {
+          out = make_uint4(pack_pair<T>(f(4 * i)), pack_pair<T>(f(4 * i + 1)),
+                           pack_pair<T>(f(4 * i + 2)), pack_pair<T>(f(4 * i + 3)));
+        }
+        __stcs(reinterpret_cast<uint4*>(row + column(i * E, tid)), out);
+      }
+    }
   }
 };
 
-// Sums over a group; every thread of it gets them.  Two places in turn, so that
-// one barrier per sum is enough.
-template <int G>
-struct GroupSum {
-  float2* part;          // this group's [2][G / 32]
-  int group, turn = 0;
-  __device__ __forceinline__ float2 operator()(float2 x) {
+// A thread's pairs of a parameter; 0 past the width.
+template <typename W, typename P>
+__device__ __forceinline__ void load_params(const void* p, float none, int width, int tid,
+                                            float2 (&out)[P::kPairs]) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      x.x += __shfl_xor_sync(kFull, x.x, o);
-      x.y += __shfl_xor_sync(kFull, x.y, o);
-    }
+  for (int k = 0; k < P::kPairs; ++k) {
+    const int j0 = P::column(2 * k, tid), j1 = P::column(2 * k + 1, tid);
+    out[k] = make_float2(j0 < width ? param<W>(p, j0, none) : 0.0f,
+                         j1 < width ? param<W>(p, j1, none) : 0.0f);
+  }
+}
+
+__device__ __forceinline__ float plus(float x, float y) { return x + y; }
+__device__ __forceinline__ float2 plus(float2 x, float2 y) { return add2(x, y); }
+__device__ __forceinline__ float from_lane(float x, int o) { return __shfl_xor_sync(kFull, x, o); }
+__device__ __forceinline__ float2 from_lane(float2 x, int o) {
+  return make_float2(__shfl_xor_sync(kFull, x.x, o), __shfl_xor_sync(kFull, x.y, o));
+}
+
+// Sums over a group, a warp or the whole CTA; every thread of it gets them.  Two
+// places in turn, so that one barrier per sum is enough.
+template <typename V, int G>
+struct GroupSum {
+  V* part;               // [2][G / 32]
+  int turn = 0;
+  __device__ __forceinline__ V operator()(V x) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x = plus(x, from_lane(x, o));
     if (G > 32) {
-      float2* const p = part + turn * (G / 32);
+      V* const p = part + turn * (G / 32);
       turn ^= 1;
-      if ((threadIdx.x & 31) == 0) p[threadIdx.x % G / 32] = x;
-      if (kCta<G> == G) __syncthreads();
-      else asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(G) : "memory");
+      if ((threadIdx.x & 31) == 0) p[threadIdx.x / 32] = x;
+      __syncthreads();
       x = p[0];
 #pragma unroll
-      for (int i = 1; i < G / 32; ++i) {
-        x.x += p[i].x;
-        x.y += p[i].y;
-      }
+      for (int i = 1; i < G / 32; ++i) x = plus(x, p[i]);
     }
     return x;
   }
 };
 
-template <typename T, typename W, bool VEC, int G>
-__global__ void __launch_bounds__(kCta<G>, kForwardThreads / kCta<G>)
-ln_forward_kernel(const LayerNormArgs a) {
-  using P = Piece<T, VEC, G>;
-  constexpr int kGroups = kCta<G> / G;
-  __shared__ float2 s_part[kGroups][2 * ((G + 31) / 32)];
-  const int group = threadIdx.x / G, tid = threadIdx.x % G;
-  GroupSum<G> group_sum{s_part[group], group};
-  float w[kEach], b[kEach];
+// The rows of a group, in turn, of ARRAYS matrices: bulk copies into a ring of
+// stages.  `take` leaves the current row in registers, `refill` (after every
+// thread of the group has taken its part) sends for the row that comes `stages`
+// rows later.  A row off the 16-byte grid (VEC false) lies in its stage at the
+// offset it has from the grid; its first and last elements outside whole words
+// come by plain loads, a row ahead, and the thread that has such an element puts
+// it into the stage for itself.
+template <typename P, typename T, bool VEC, int G, int ARRAYS>
+struct Rows {
+  const T* base[ARRAYS];
+  int64_t stride[ARRAYS];
+  int64_t rows, step, ahead;     // ahead: the next row to send for
+  int64_t row;                   // the current row
+  int32_t width, stages;
+  unsigned char* ring;           // [stages][ARRAYS][pitch]
+  uint64_t* full;                // [stages]
+  uint32_t n = 0;
+  bool lost = false;             // a wait gave up: no more waits, the fault is recorded
+  // of the current row off the grid: its offset, whether this thread has one of
+  // its first elements, the thread's column among its last ones, and both
+  uint32_t off[ARRAYS];
+  bool first[ARRAYS];
+  int mine[ARRAYS];
+  T edge[ARRAYS][2];
+
+  static __host__ __device__ __forceinline__ uint32_t pitch_of(int32_t width) {
+    return VEC ? width * sizeof(T) : (width * sizeof(T) + 15) / 16 * 16 + 16;
+  }
+  __device__ __forceinline__ unsigned char* slot(uint32_t stage, int m) const {
+    return ring + (stage * ARRAYS + m) * pitch_of(width);
+  }
+  __device__ __forceinline__ const T* at(int64_t r, int m) const { return base[m] + r * stride[m]; }
+
+  // A row's elements before its first and from its last 16-byte boundary on.
+  struct Edges {
+    uint32_t off;        // bytes from the grid to the row
+    int head, tail;      // elements [0, head) and [tail, width)
+  };
+  __device__ __forceinline__ Edges edges(const T* p) const {
+    const uint32_t lo = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p));
+    Edges e;
+    e.off = lo & 15u;
+    e.head = min(static_cast<int>((0u - lo & 15u) / sizeof(T)), width);
+    e.tail = max(width - static_cast<int>((lo + width * static_cast<uint32_t>(sizeof(T)) & 15u) / sizeof(T)),
+                 e.head);
+    return e;
+  }
+  // This thread's column among the last ones, or one past the width.
+  __device__ __forceinline__ int tail_column(const Edges& e, int tid) const {
+    return e.tail + (tid - e.tail & G - 1);
+  }
+  __device__ __forceinline__ void fetch_edges(int tid) {
+    if (VEC || row >= rows) return;
 #pragma unroll
-  for (int i = 0; i < P::N; ++i)
-#pragma unroll
-    for (int e = 0; e < P::E; ++e) {
-      const int j = P::column(i, tid) + e;
-      w[i * P::E + e] = j < a.width ? param<W>(a.weight, j, 1.0f) : 0.0f;
-      b[i * P::E + e] = j < a.width ? param<W>(a.bias, j, 0.0f) : 0.0f;
+    for (int m = 0; m < ARRAYS; ++m) {
+      const T* const p = at(row, m);
+      const Edges e = edges(p);
+      const int c = tail_column(e, tid);
+      off[m] = e.off;
+      mine[m] = c;
+      first[m] = tid < e.head;
+      if (first[m]) edge[m][0] = p[tid];
+      if (c < width) edge[m][1] = p[c];
     }
-  const float inv_width = 1.0f / static_cast<float>(a.width);
+  }
+  __device__ __forceinline__ void send(uint32_t stage) {
+    uint32_t bytes[ARRAYS], all = 0;
+    int from[ARRAYS];
+#pragma unroll
+    for (int m = 0; m < ARRAYS; ++m) {
+      from[m] = 0;
+      bytes[m] = width * sizeof(T);
+      if (!VEC) {
+        const Edges e = edges(at(ahead, m));
+        from[m] = e.head;
+        bytes[m] = static_cast<uint32_t>(e.tail - e.head) * sizeof(T);
+      }
+      all += bytes[m];
+    }
+    mbar_expect_tx(&full[stage], all);
+#pragma unroll
+    for (int m = 0; m < ARRAYS; ++m)
+      if (bytes[m] != 0u) {
+        const T* const p = at(ahead, m);
+        const uint32_t grid = VEC ? 0u : static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 15u);
+        bulk_g2s(slot(stage, m) + grid + from[m] * sizeof(T), p + from[m], bytes[m], &full[stage]);
+      }
+  }
+  // Called by every thread of the CTA.
+  __device__ __forceinline__ void start(int tid) {
+    if (tid == 0) {
+      for (int i = 0; i < stages; ++i) mbar_init(&full[i], 1);
+      fence_mbar_init();
+    }
+    __syncthreads();
+    for (int i = 0; i < stages; ++i, ahead += step)
+      if (tid == 0 && ahead < rows) send(i);
+    fetch_edges(tid);
+  }
+  __device__ __forceinline__ void take(P (&p)[ARRAYS], int tid) {
+    const uint32_t stage = n % stages;
+    if (!lost) lost = !mbar_wait(&full[stage], (n / stages) & 1u);
+#pragma unroll
+    for (int m = 0; m < ARRAYS; ++m) {
+      unsigned char* s = slot(stage, m);
+      if (!VEC) {
+        s += off[m];
+        if (first[m]) reinterpret_cast<T*>(s)[tid] = edge[m][0];
+        if (mine[m] < width) reinterpret_cast<T*>(s)[mine[m]] = edge[m][1];
+      }
+      p[m].load(s, width, tid);
+    }
+    row += step;
+    fetch_edges(tid);
+  }
+  __device__ __forceinline__ void refill(int tid) {
+    if (G == 32) __syncwarp();
+    if (tid == 0 && ahead < rows) {
+      if (!VEC) fence_proxy_async_smem();
+      send(n % stages);
+    }
+    ahead += step;
+    ++n;
+  }
+  // After a wait that gave up, copies still on their way land before the CTA
+  // may leave.
+  __device__ __forceinline__ void finish(int tid, uint32_t* fault) {
+    if (!lost || tid != 0) return;
+    atomicOr(fault, 1u);
+    for (uint32_t i = n > static_cast<uint32_t>(stages) ? n - stages : 0; i < n; ++i)
+      mbar_wait(&full[i % stages], (i / stages) & 1u);
+  }
+};
+
+template <typename T, typename W, bool VEC, int G, int EACH>
+__global__ void __launch_bounds__(kCta<G>, forward_threads(VEC, EACH) / kCta<G>)
+ln_forward_kernel(const LayerNormArgs a) {
+  using P = Piece<T, VEC, G, EACH>;
+  constexpr int kPairs = P::kPairs;
+  constexpr int kGroups = kCta<G> / G;
+  extern __shared__ __align__(16) unsigned char s_ring[];
+  __shared__ float s_part[2 * G / 32];
+  __shared__ uint64_t s_full[kGroups][kStages];
+  const int group = threadIdx.x / G, tid = threadIdx.x % G;
+  GroupSum<float, G> group_sum{s_part};
   const int64_t step = static_cast<int64_t>(gridDim.x) * kGroups;
   int64_t t = static_cast<int64_t>(blockIdx.x) * kGroups + group;
-  const T* const x = static_cast<const T*>(a.x);
-  P next;
-  if (t < a.rows) next.load(x + t * a.x_stride, a.width, tid);
+  using R = Rows<P, T, VEC, G, 1>;
+  R rows{{static_cast<const T*>(a.x)}, {a.x_stride}, a.rows, step, t, t, a.width, a.stages,
+         s_ring + group * a.stages * R::pitch_of(a.width), s_full[group]};
+  rows.start(tid);
+  float2 w[kPairs], b[kPairs];
+  load_params<W, P>(a.weight, 1.0f, a.width, tid, w);
+  load_params<W, P>(a.bias, 0.0f, a.width, tid, b);
+  const float inv_width = 1.0f / static_cast<float>(a.width);
   for (; t < a.rows; t += step) {
-    const P p = next;
-    if (t + step < a.rows) next.load(x + (t + step) * a.x_stride, a.width, tid);
-    float sum = 0.0f;
+    P p[1];
+    rows.take(p, tid);
+    float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
-    for (int i = 0; i < P::N; ++i)
-      if (P::column(i, tid) < a.width) {
+    for (int k = 0; k < kPairs; ++k) sum = add2(sum, p[0].pair(k));
+    const float mean = group_sum(sum.x + sum.y) * inv_width;
+    rows.refill(tid);
+    float2 sq = make_float2(0.0f, 0.0f);
 #pragma unroll
-        for (int e = 0; e < P::E; ++e) sum += p.at(i, e);
-      }
-    const float mean = group_sum(make_float2(sum, 0.0f)).x * inv_width;
-    float sq = 0.0f;
-#pragma unroll
-    for (int i = 0; i < P::N; ++i)
-      if (P::column(i, tid) < a.width) {
-#pragma unroll
-        for (int e = 0; e < P::E; ++e) {
-          const float d = p.at(i, e) - mean;
-          sq = fmaf(d, d, sq);
-        }
-      }
-    const float rstd = 1.0f / sqrtf(group_sum(make_float2(sq, 0.0f)).x * inv_width + a.eps);
-    P::store(static_cast<T*>(a.y) + t * a.y_stride, a.width, tid, [&](int i, int e) {
-      return fmaf((p.at(i, e) - mean) * rstd, w[i * P::E + e], b[i * P::E + e]);
+    for (int k = 0; k < kPairs; ++k) {
+      const float2 d = P::inside(add2(p[0].pair(k), both(-mean)), k, a.width, tid);
+      sq = fma2(d, d, sq);
+    }
+    const float var = group_sum(sq.x + sq.y) * inv_width;
+    const float rstd = 1.0f / sqrtf(var + a.eps);
+    P::store(static_cast<T*>(a.y) + t * a.y_stride, a.width, tid, [&](int k) {
+      return fma2(mul2(add2(p[0].pair(k), both(-mean)), both(rstd)), w[k], b[k]);
     });
     if (tid == 0) {
       a.mean[t] = mean;
       a.rstd[t] = rstd;
     }
   }
+  rows.finish(tid, a.fault);
 }
 
-template <typename T, typename W, bool VEC, int G>
-__global__ void __launch_bounds__(kCta<G>, kBackwardThreads / kCta<G>)
+template <typename T, typename W, bool VEC, int G, int EACH>
+__global__ void __launch_bounds__(kCta<G>, backward_threads(EACH) / kCta<G>)
 ln_backward_kernel(const LayerNormArgs a) {
-  using P = Piece<T, VEC, G>;
+  using P = Piece<T, VEC, G, EACH>;
+  constexpr int kPairs = P::kPairs;
   constexpr int kGroups = kCta<G> / G;
-  __shared__ float2 s_part[kGroups][2 * ((G + 31) / 32)];
-  __shared__ float2 s_add[kGroups > 1 ? kEach * G : 1];
+  extern __shared__ __align__(16) unsigned char s_ring[];
+  __shared__ float2 s_part[2 * G / 32];
+  __shared__ uint64_t s_full[kGroups][kStages];
+  __shared__ float2 s_add[kGroups > 1 ? EACH * G : 1];
   let_next_kernel_start();
   const int group = threadIdx.x / G, tid = threadIdx.x % G;
-  GroupSum<G> group_sum{s_part[group], group};
-  float w[kEach], gw[kEach], gb[kEach];
-#pragma unroll
-  for (int i = 0; i < P::N; ++i)
-#pragma unroll
-    for (int e = 0; e < P::E; ++e) {
-      const int j = P::column(i, tid) + e;
-      w[i * P::E + e] = j < a.width ? param<W>(a.weight, j, 1.0f) : 0.0f;
-      gw[i * P::E + e] = 0.0f;
-      gb[i * P::E + e] = 0.0f;
-    }
-  const float inv_width = 1.0f / static_cast<float>(a.width);
+  GroupSum<float2, G> group_sum{s_part};
   const int64_t step = static_cast<int64_t>(gridDim.x) * kGroups;
   int64_t t = static_cast<int64_t>(blockIdx.x) * kGroups + group;
-  const T* const x = static_cast<const T*>(a.x);
-  const T* const dy = static_cast<const T*>(a.dy);
-  P next_x, next_g;
+  using R = Rows<P, T, VEC, G, 2>;
+  R rows{{static_cast<const T*>(a.x), static_cast<const T*>(a.dy)}, {a.x_stride, a.dy_stride},
+         a.rows, step, t, t, a.width, a.stages,
+         s_ring + group * a.stages * 2 * R::pitch_of(a.width), s_full[group]};
+  rows.start(tid);
+  float2 w[kPairs], gw[kPairs], gb[kPairs];
+  load_params<W, P>(a.weight, 1.0f, a.width, tid, w);
+#pragma unroll
+  for (int k = 0; k < kPairs; ++k) gw[k] = gb[k] = make_float2(0.0f, 0.0f);
+  const float inv_width = 1.0f / static_cast<float>(a.width);
   float next_mean = 0.0f, next_rstd = 0.0f;
-  auto fetch = [&](int64_t r) {
-    if (r >= a.rows) return;
-    next_x.load(x + r * a.x_stride, a.width, tid);
-    next_g.load(dy + r * a.dy_stride, a.width, tid);
-    next_mean = a.mean[r];
-    next_rstd = a.rstd[r];
-  };
-  fetch(t);
+  if (t < a.rows) {
+    next_mean = a.mean[t];
+    next_rstd = a.rstd[t];
+  }
   for (; t < a.rows; t += step) {
-    const P px = next_x, pg = next_g;
     const float mean = next_mean, rstd = next_rstd;
-    fetch(t + step);
-    float2 s = make_float2(0.0f, 0.0f);
+    if (t + step < a.rows) {
+      next_mean = a.mean[t + step];
+      next_rstd = a.rstd[t + step];
+    }
+    P p[2];
+    rows.take(p, tid);
+    // xhat = (x - mean) rstd; past the width dy is 0, so nothing is added there
+    const float2 m = both(-mean), r = both(rstd);
+    float2 sum1 = make_float2(0.0f, 0.0f), sum2 = make_float2(0.0f, 0.0f);
 #pragma unroll
-    for (int i = 0; i < P::N; ++i)
-      if (P::column(i, tid) < a.width) {
-#pragma unroll
-        for (int e = 0; e < P::E; ++e) {
-          const int k = i * P::E + e;
-          const float g = pg.at(i, e), h = (px.at(i, e) - mean) * rstd, wg = g * w[k];
-          s.x += wg;
-          s.y = fmaf(wg, h, s.y);
-          gw[k] = fmaf(g, h, gw[k]);
-          gb[k] += g;
-        }
-      }
-    s = group_sum(s);
-    const float m1 = s.x * inv_width, m2 = s.y * inv_width;
-    P::store(static_cast<T*>(a.dx) + t * a.dx_stride, a.width, tid, [&](int i, int e) {
-      const float h = (px.at(i, e) - mean) * rstd;
-      return rstd * (fmaf(pg.at(i, e), w[i * P::E + e], -m1) - h * m2);
+    for (int k = 0; k < kPairs; ++k) {
+      const float2 g = p[1].pair(k), h = mul2(add2(p[0].pair(k), m), r), wg = mul2(g, w[k]);
+      sum1 = add2(sum1, wg);
+      sum2 = fma2(wg, h, sum2);
+      gw[k] = fma2(g, h, gw[k]);
+      gb[k] = add2(gb[k], g);
+    }
+    const float2 s = group_sum(make_float2(sum1.x + sum1.y, sum2.x + sum2.y));
+    rows.refill(tid);
+    // dx = rstd w dy - rstd m1 - (rstd m2) xhat
+    const float2 c1 = both(-rstd * (s.x * inv_width)), c2 = both(-rstd * (s.y * inv_width));
+    P::store(static_cast<T*>(a.dx) + t * a.dx_stride, a.width, tid, [&](int k) {
+      const float2 h = mul2(add2(p[0].pair(k), m), r);
+      return fma2(mul2(p[1].pair(k), w[k]), r, fma2(h, c2, c1));
     });
   }
+  rows.finish(tid, a.fault);
   if (a.partial == nullptr) return;
   // the CTA's groups, in their order
   for (int g = 1; g < kGroups; ++g) {
     __syncthreads();
     if (group == g) {
 #pragma unroll
-      for (int k = 0; k < kEach; ++k) s_add[k * G + tid] = make_float2(gw[k], gb[k]);
+      for (int k = 0; k < kPairs; ++k) {
+        s_add[(2 * k) * G + tid] = gw[k];
+        s_add[(2 * k + 1) * G + tid] = gb[k];
+      }
     }
     __syncthreads();
     if (group == 0) {
 #pragma unroll
-      for (int k = 0; k < kEach; ++k) {
-        gw[k] += s_add[k * G + tid].x;
-        gb[k] += s_add[k * G + tid].y;
+      for (int k = 0; k < kPairs; ++k) {
+        gw[k] = add2(gw[k], s_add[(2 * k) * G + tid]);
+        gb[k] = add2(gb[k], s_add[(2 * k + 1) * G + tid]);
       }
     }
   }
@@ -241,15 +417,17 @@ ln_backward_kernel(const LayerNormArgs a) {
   float* const pw = a.partial + static_cast<int64_t>(blockIdx.x) * a.width;
   float* const pb = pw + static_cast<int64_t>(a.parts) * a.width;
 #pragma unroll
-  for (int i = 0; i < P::N; ++i)
-#pragma unroll
-    for (int e = 0; e < P::E; ++e) {
-      const int j = P::column(i, tid) + e;
-      if (j < a.width) {
-        pw[j] = gw[i * P::E + e];
-        pb[j] = gb[i * P::E + e];
-      }
+  for (int k = 0; k < kPairs; ++k) {
+    const int j0 = P::column(2 * k, tid), j1 = P::column(2 * k + 1, tid);
+    if (j0 < a.width) {
+      pw[j0] = gw[k].x;
+      pb[j0] = gb[k].x;
     }
+    if (j1 < a.width) {
+      pw[j1] = gw[k].y;
+      pb[j1] = gb[k].y;
+    }
+  }
 }
 
 // dw (blockIdx.y 0) and db (1): the CTAs' column sums, 32 columns per CTA, the
@@ -345,64 +523,103 @@ __global__ void __launch_bounds__(kWideThreads) ln_backward_wide_kernel(const La
 
 int64_t at_most(int64_t n, int64_t most) { return n < most ? n : most; }
 
-template <typename T, typename W, bool VEC, int G>
-void forward_group(const LayerNormArgs& a, int sms, cudaStream_t s) {
-  constexpr int kGroups = kCta<G> / G;
-  const int64_t ctas = at_most((a.rows + kGroups - 1) / kGroups,
-                               static_cast<int64_t>(kForwardThreads / kCta<G>) * sms);
-  ln_forward_kernel<T, W, VEC, G><<<static_cast<int>(ctas), kCta<G>, 0, s>>>(a);
+// Rows on their way per group, as many as fit beside the other resident CTAs.
+template <int G>
+int stages_for(int64_t row_bytes, int per_sm) {
+  const int64_t fit = kSmemPerSm / per_sm / (kCta<G> / G) / row_bytes;
+  return static_cast<int>(fit < 1 ? 1 : (fit < kStages ? fit : kStages));
 }
 
-template <typename T, typename W, bool VEC, int G>
+template <typename T, typename W, bool VEC, int G, int EACH>
+int forward_group(LayerNormArgs a, int sms, cudaStream_t s) {
+  constexpr int kGroups = kCta<G> / G, kPerSm = forward_threads(VEC, EACH) / kCta<G>;
+  const int64_t ctas = at_most((a.rows + kGroups - 1) / kGroups, static_cast<int64_t>(kPerSm) * sms);
+  const int64_t row = Rows<Piece<T, VEC, G, EACH>, T, VEC, G, 1>::pitch_of(a.width);
+  a.stages = stages_for<G>(row, kPerSm);
+  ln_forward_kernel<T, W, VEC, G, EACH>
+      <<<static_cast<int>(ctas), kCta<G>, kGroups * a.stages * row, s>>>(a);
+  return 0;
+}
+
+template <typename T, typename W, bool VEC, int G, int EACH>
 int backward_group(LayerNormArgs a, int sms, cudaStream_t s) {
-  constexpr int kGroups = kCta<G> / G;
-  constexpr int kPerSm = kBackwardThreads / kCta<G>;
+  constexpr int kGroups = kCta<G> / G, kPerSm = backward_threads(EACH) / kCta<G>;
   static_assert(kPerSm <= kNormPartsPerSm, "partial sums of every CTA");
   a.parts = static_cast<int32_t>(
       at_most((a.rows + kGroups - 1) / kGroups, static_cast<int64_t>(kPerSm) * sms));
   if (a.dweight == nullptr && a.dbias == nullptr) a.partial = nullptr;
-  ln_backward_kernel<T, W, VEC, G><<<a.parts, kCta<G>, 0, s>>>(a);
+  const int64_t row = 2 * static_cast<int64_t>(
+                              Rows<Piece<T, VEC, G, EACH>, T, VEC, G, 2>::pitch_of(a.width));
+  a.stages = stages_for<G>(row, kPerSm);
+  ln_backward_kernel<T, W, VEC, G, EACH><<<a.parts, kCta<G>, kGroups * a.stages * row, s>>>(a);
   return a.parts;
 }
 
-// The smallest group that holds the row at 16 elements a thread.
-#define ADAMW_LN_GROUPS(fn, T, W, VEC)                                  \
-  (a.width <= 32 * kEach    ? fn<T, W, VEC, 32>(a, sms, s)              \
-   : a.width <= 64 * kEach  ? fn<T, W, VEC, 64>(a, sms, s)              \
-   : a.width <= 128 * kEach ? fn<T, W, VEC, 128>(a, sms, s)             \
-   : a.width <= 256 * kEach ? fn<T, W, VEC, 256>(a, sms, s)             \
-                            : fn<T, W, VEC, 512>(a, sms, s))
+// The group of a width.
+#define ADAMW_LN_GROUPS(call)           \
+  (a.width <= 512    ? call(32, 16)     \
+   : a.width <= 1024 ? call(32, 32)     \
+   : a.width <= 2048 ? call(128, 16)    \
+   : a.width <= 4096 ? call(256, 16)    \
+                     : call(512, 16))
+
+// Lets the row kernels of one width use the shared memory of their stages.
+template <typename T, typename W, bool VEC, int G, int EACH>
+cudaError_t prepare_group() {
+  const cudaError_t e = cudaFuncSetAttribute(ln_forward_kernel<T, W, VEC, G, EACH>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemPerSm);
+  if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(ln_backward_kernel<T, W, VEC, G, EACH>,
+                              cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemPerSm);
+}
+template <typename T, typename W>
+cudaError_t prepare_width(int32_t width) {
+  LayerNormArgs a{};
+  a.width = width;
+#define ADAMW_LN_CALL(G, EACH) prepare_group<T, W, true, G, EACH>()
+  const cudaError_t e = ADAMW_LN_GROUPS(ADAMW_LN_CALL);
+#undef ADAMW_LN_CALL
+  if (e != cudaSuccess) return e;
+#define ADAMW_LN_CALL(G, EACH) prepare_group<T, W, false, G, EACH>()
+  return ADAMW_LN_GROUPS(ADAMW_LN_CALL);
+#undef ADAMW_LN_CALL
+}
 
 bool on_grid(const void* p, int64_t stride_bytes) {
   return reinterpret_cast<uintptr_t>(p) % 16 == 0 && stride_bytes % 16 == 0;
 }
 
+#define ADAMW_LN_FORWARD(G, EACH)                            \
+  (vec ? forward_group<T, W, true, G, EACH>(a, sms, s)       \
+       : forward_group<T, W, false, G, EACH>(a, sms, s))
+#define ADAMW_LN_BACKWARD(G, EACH)                           \
+  (vec ? backward_group<T, W, true, G, EACH>(a, sms, s)      \
+       : backward_group<T, W, false, G, EACH>(a, sms, s))
+
 template <typename T, typename W>
 cudaError_t forward(const LayerNormArgs& a, int sms, cudaStream_t s) {
   const int64_t z = sizeof(T);
-  if (a.width > kMaxGroup * kEach)
+  const bool vec = on_grid(a.x, a.x_stride * z) && on_grid(a.y, a.y_stride * z) && a.width * z % 16 == 0;
+  if (a.width > kMaxWidth)
     ln_forward_wide_kernel<T, W>
         <<<static_cast<int>(at_most(a.rows, 4LL * sms)), kWideThreads, 0, s>>>(a);
-  else if (on_grid(a.x, a.x_stride * z) && on_grid(a.y, a.y_stride * z) && a.width * z % 16 == 0)
-    ADAMW_LN_GROUPS(forward_group, T, W, true);
   else
-    ADAMW_LN_GROUPS(forward_group, T, W, false);
+    ADAMW_LN_GROUPS(ADAMW_LN_FORWARD);
   return cudaGetLastError();
 }
 
 template <typename T, typename W>
 cudaError_t backward(LayerNormArgs a, int sms, cudaStream_t s) {
   const int64_t z = sizeof(T);
+  const bool vec = on_grid(a.x, a.x_stride * z) && on_grid(a.dy, a.dy_stride * z) &&
+                   on_grid(a.dx, a.dx_stride * z) && a.width * z % 16 == 0;
   if (a.rows == 0) {
     a.parts = 0;
-  } else if (a.width > kMaxGroup * kEach) {
+  } else if (a.width > kMaxWidth) {
     a.parts = static_cast<int32_t>(at_most(a.rows, static_cast<int64_t>(kNormPartsPerSm) * sms));
     ln_backward_wide_kernel<T, W><<<a.parts, kWideThreads, 0, s>>>(a);
-  } else if (on_grid(a.x, a.x_stride * z) && on_grid(a.dy, a.dy_stride * z) &&
-             on_grid(a.dx, a.dx_stride * z) && a.width * z % 16 == 0) {
-    a.parts = ADAMW_LN_GROUPS(backward_group, T, W, true);
   } else {
-    a.parts = ADAMW_LN_GROUPS(backward_group, T, W, false);
+    a.parts = ADAMW_LN_GROUPS(ADAMW_LN_BACKWARD);
   }
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || (a.dweight == nullptr && a.dbias == nullptr)) return e;
@@ -417,6 +634,15 @@ cudaError_t backward(LayerNormArgs a, int sms, cudaStream_t s) {
 }
 
 }  // namespace
+
+cudaError_t prepare_layer_norm(int32_t width) {
+  cudaError_t e = prepare_width<float, float>(width);
+  if (e == cudaSuccess) e = prepare_width<__half, float>(width);
+  if (e == cudaSuccess) e = prepare_width<__half, __half>(width);
+  if (e == cudaSuccess) e = prepare_width<__nv_bfloat16, float>(width);
+  if (e == cudaSuccess) e = prepare_width<__nv_bfloat16, __nv_bfloat16>(width);
+  return e;
+}
 
 #define ADAMW_LN_DISPATCH(fn)                                                     \
   if (dt == ADAMW_F32 && wdt == ADAMW_F32) return fn<float, float>(a, sms, s);    \
@@ -438,5 +664,7 @@ cudaError_t launch_layer_norm_backward(adamw_dtype dt, adamw_dtype wdt, const La
 }
 #undef ADAMW_LN_DISPATCH
 #undef ADAMW_LN_GROUPS
+#undef ADAMW_LN_FORWARD
+#undef ADAMW_LN_BACKWARD
 
 }  // namespace adamw

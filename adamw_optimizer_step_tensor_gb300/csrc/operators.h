@@ -90,7 +90,10 @@ struct LayerNormArgs {
   float eps;
   float* partial;              // plan-owned: [2][parts][width]
   int32_t parts;
+  int32_t stages;              // rows on their way per group (rows on the 16-byte grid)
+  uint32_t* fault;             // nonzero: a bounded wait gave up
 };
+cudaError_t prepare_layer_norm(int32_t width);
 cudaError_t launch_layer_norm_forward(adamw_dtype dt, adamw_dtype wdt, const LayerNormArgs& a,
                                       int sms, cudaStream_t s);
 cudaError_t launch_layer_norm_backward(adamw_dtype dt, adamw_dtype wdt, const LayerNormArgs& a,

@@ -26,6 +26,7 @@ struct adamw_layer_norm_plan {
   int32_t width = 0;
   float eps = 0.0f;
   float* d_partial = nullptr;
+  uint32_t* d_fault = nullptr;
 };
 
 namespace {
@@ -41,6 +42,7 @@ void free_loss_plan(adamw_loss_plan* p) {
 void free_layer_norm_plan(adamw_layer_norm_plan* p) {
   if (!p) return;
   cudaFree(p->d_partial);
+  cudaFree(p->d_fault);
   delete p;
 }
 
@@ -154,6 +156,20 @@ adamw_status layer_norm_args(const adamw_layer_norm_plan* plan, int dtype, int w
   a->width = plan->width;
   a->eps = plan->eps;
   a->partial = plan->d_partial;
+  a->fault = plan->d_fault;
+  return ADAMW_OK;
+}
+
+// Reads a plan's fault word after all work on the device.
+adamw_status read_fault(int device, const uint32_t* d_fault, uint32_t* fault_bits) {
+  adamw_status st = check_current_device(device, "plan");
+  if (st != ADAMW_OK) return st;
+  cudaError_t e = cudaDeviceSynchronize();
+  uint32_t bits = 0;
+  if (e == cudaSuccess) e = cudaMemcpy(&bits, d_fault, sizeof bits, cudaMemcpyDeviceToHost);
+  if (e != cudaSuccess) return cuda_fail(e, "read fault word");
+  if (fault_bits) *fault_bits = bits;
+  if (bits != 0) return fail(ADAMW_ETIMEOUT, "a bounded wait gave up (fault bits 0x%x)", bits);
   return ADAMW_OK;
 }
 
@@ -228,18 +244,8 @@ adamw_status adamw_loss_plan_create(int64_t max_rows, int32_t max_pairs, adamw_l
 
 adamw_status adamw_loss_plan_status(const adamw_loss_plan* plan, uint32_t* fault_bits) {
   if (!plan) return fail(ADAMW_EINVAL, "plan is NULL");
-  adamw_status st = check_current_device(plan->device, "plan");
-  if (st != ADAMW_OK) return st;
-  cudaError_t e = cudaDeviceSynchronize();
-  uint32_t bits = 0;
-  if (e == cudaSuccess)
-    e = cudaMemcpy(&bits, reinterpret_cast<uint32_t*>(plan->d_partial + 4 * kLossMaxCtas) + 1,
-                   sizeof bits, cudaMemcpyDeviceToHost);
-  if (e != cudaSuccess) return cuda_fail(e, "read fault word");
-  if (fault_bits) *fault_bits = bits;
-  if (bits != 0)
-    return fail(ADAMW_ETIMEOUT, "a bounded wait of a token loss gave up (fault bits 0x%x)", bits);
-  return ADAMW_OK;
+  return read_fault(plan->device, reinterpret_cast<uint32_t*>(plan->d_partial + 4 * kLossMaxCtas) + 1,
+                    fault_bits);
 }
 
 adamw_status adamw_loss_plan_destroy(adamw_loss_plan* plan) { return destroy(plan, free_loss_plan); }
@@ -344,11 +350,22 @@ adamw_status adamw_layer_norm_plan_create(int32_t width, float eps, adamw_layer_
   p->width = width;
   p->eps = eps;
   const size_t n = 2 * static_cast<size_t>(kNormPartsPerSm) * sms * width * sizeof(float);
-  cudaError_t e = cudaMalloc(&p->d_partial, n);
+  cudaError_t e = prepare_layer_norm(width);
+  if (e != cudaSuccess) return cuda_fail(e, "prepare the layer norm kernels");
+  e = cudaMalloc(&p->d_partial, n);
+  if (e == cudaSuccess) e = cudaMalloc(&p->d_fault, sizeof(uint32_t));
   if (e != cudaSuccess)
     return fail(ADAMW_ENOMEM, "cudaMalloc(layer norm plan): %s", cudaGetErrorString(e));
+  if ((e = cudaMemset(p->d_fault, 0, sizeof(uint32_t))) != cudaSuccess ||
+      (e = cudaStreamSynchronize(cudaStreamLegacy)) != cudaSuccess)
+    return cuda_fail(e, "clear the layer norm plan");
   *out = p.release();
   return ADAMW_OK;
+}
+
+adamw_status adamw_layer_norm_plan_status(const adamw_layer_norm_plan* plan, uint32_t* fault_bits) {
+  if (!plan) return fail(ADAMW_EINVAL, "plan is NULL");
+  return read_fault(plan->device, plan->d_fault, fault_bits);
 }
 
 adamw_status adamw_layer_norm_plan_destroy(adamw_layer_norm_plan* plan) {

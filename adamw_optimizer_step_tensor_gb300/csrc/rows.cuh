@@ -26,6 +26,53 @@ __device__ __forceinline__ T from_f32(float x) {
   else return __float2bfloat16_rn(x);
 }
 
+// Two 16-bit elements in a 32-bit word, the first one low.
+template <typename T>
+__device__ __forceinline__ float2 unpack_pair(uint32_t v) {
+  if constexpr (std::is_same<T, __half>::value)
+    return __half22float2(*reinterpret_cast<const __half2*>(&v));
+  else
+    return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
+}
+template <typename T>
+__device__ __forceinline__ uint32_t pack_pair(float2 x) {
+  if constexpr (std::is_same<T, __half>::value) {
+    const __half2 h = __float22half2_rn(x);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  } else {
+    const __nv_bfloat162 h = __float22bfloat162_rn(x);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+}
+
+// Two float32 operations per instruction.
+__device__ __forceinline__ float2 fma2(float2 x, float2 y, float2 z) {
+  float2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<unsigned long long&>(r))
+      : "l"(reinterpret_cast<const unsigned long long&>(x)),
+        "l"(reinterpret_cast<const unsigned long long&>(y)),
+        "l"(reinterpret_cast<const unsigned long long&>(z)));
+  return r;
+}
+__device__ __forceinline__ float2 add2(float2 x, float2 y) {
+  float2 r;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<unsigned long long&>(r))
+      : "l"(reinterpret_cast<const unsigned long long&>(x)),
+        "l"(reinterpret_cast<const unsigned long long&>(y)));
+  return r;
+}
+__device__ __forceinline__ float2 mul2(float2 x, float2 y) {
+  float2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<unsigned long long&>(r))
+      : "l"(reinterpret_cast<const unsigned long long&>(x)),
+        "l"(reinterpret_cast<const unsigned long long&>(y)));
+  return r;
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
 // Sum over the CTA's threads, the same value in every thread.
 template <int THREADS>
 __device__ __forceinline__ float block_sum(float x, float* s_warp) {

@@ -51,34 +51,6 @@ __device__ __forceinline__ float grad_arg(const LossArgs& a, float z, float c) {
   return std::is_same<T, float>::value ? arg(a, z, c) : fmaf(z, a.k, -c);
 }
 
-// Two float32 operations per instruction.
-__device__ __forceinline__ float2 fma2(float2 x, float2 y, float2 z) {
-  float2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;"
-      : "=l"(reinterpret_cast<unsigned long long&>(r))
-      : "l"(reinterpret_cast<const unsigned long long&>(x)),
-        "l"(reinterpret_cast<const unsigned long long&>(y)),
-        "l"(reinterpret_cast<const unsigned long long&>(z)));
-  return r;
-}
-__device__ __forceinline__ float2 add2(float2 x, float2 y) {
-  float2 r;
-  asm("add.rn.f32x2 %0, %1, %2;"
-      : "=l"(reinterpret_cast<unsigned long long&>(r))
-      : "l"(reinterpret_cast<const unsigned long long&>(x)),
-        "l"(reinterpret_cast<const unsigned long long&>(y)));
-  return r;
-}
-__device__ __forceinline__ float2 mul2(float2 x, float2 y) {
-  float2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;"
-      : "=l"(reinterpret_cast<unsigned long long&>(r))
-      : "l"(reinterpret_cast<const unsigned long long&>(x)),
-        "l"(reinterpret_cast<const unsigned long long&>(y)));
-  return r;
-}
-__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
-
 // Integer reference c and S = sum 2^(z k - c).
 struct RowSum {
   float c, s;
@@ -168,12 +140,7 @@ __device__ __forceinline__ void unpack(const uint4& w, float2 (&x)[kPerWord<T> /
     x[1] = make_float2(__uint_as_float(v[2]), __uint_as_float(v[3]));
   } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if constexpr (std::is_same<T, __half>::value)
-        x[i] = __half22float2(*reinterpret_cast<const __half2*>(&v[i]));
-      else
-        x[i] = make_float2(__uint_as_float(v[i] << 16), __uint_as_float(v[i] & 0xFFFF0000u));
-    }
+    for (int i = 0; i < 4; ++i) x[i] = unpack_pair<T>(v[i]);
   }
 }
 template <typename T>
@@ -182,18 +149,8 @@ __device__ __forceinline__ uint4 pack(const float2 (&x)[kPerWord<T> / 2]) {
     return make_uint4(__float_as_uint(x[0].x), __float_as_uint(x[0].y), __float_as_uint(x[1].x),
                       __float_as_uint(x[1].y));
   } else {
-    uint32_t v[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if constexpr (std::is_same<T, __half>::value) {
-        const __half2 h = __float22half2_rn(x[i]);
-        v[i] = *reinterpret_cast<const uint32_t*>(&h);
-      } else {
-        const __nv_bfloat162 h = __float22bfloat162_rn(x[i]);
-        v[i] = *reinterpret_cast<const uint32_t*>(&h);
-      }
-    }
-    return make_uint4(v[0], v[1], v[2], v[3]);
+    return make_uint4(pack_pair<T>(x[0]), pack_pair<T>(x[1]), pack_pair<T>(x[2]),
+                      pack_pair<T>(x[3]));
   }
 }
 

@@ -203,6 +203,10 @@ class FusedLayerNorm(_Plan):
         self.plan = _capi.adamw_layer_norm_plan_create(int(width), float(eps))
         self.width = int(width)
 
+    def status(self) -> int:
+        """Device-side fault bits (0 = healthy); raises AdamWError if a bounded wait gave up."""
+        return _capi.adamw_layer_norm_plan_status(self.plan)
+
     def _check(self, x, weight):
         if x.dtype not in _DTYPES:
             raise TypeError(f"unsupported dtype {x.dtype}")

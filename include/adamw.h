@@ -610,6 +610,8 @@ adamw_status adamw_preference_loss(adamw_loss_plan* plan, const adamw_logits* z,
  * one plan must not overlap one another. */
 typedef struct adamw_layer_norm_plan adamw_layer_norm_plan;
 adamw_status adamw_layer_norm_plan_create(int32_t width, float eps, adamw_layer_norm_plan** out);
+/* Device-side health, as adamw_plan_status. */
+adamw_status adamw_layer_norm_plan_status(const adamw_layer_norm_plan* plan, uint32_t* fault_bits);
 /* Frees a layer norm plan (NULL is allowed).  Synchronises with the device first. */
 adamw_status adamw_layer_norm_plan_destroy(adamw_layer_norm_plan* plan);
 
