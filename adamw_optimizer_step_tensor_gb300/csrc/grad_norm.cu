@@ -10,6 +10,7 @@
 // added in a fixed order by the last CTA to finish, so the norm is the same bit
 // for bit from run to run.
 #include "operators.h"
+#include "rows.cuh"
 #include "step_common.cuh"
 
 namespace adamw {
@@ -42,62 +43,80 @@ __device__ __forceinline__ void widen(const uint4& w, float (&x)[kPerLoad<GT>]) 
   }
 }
 
-// Sum of squares of the loaded words: float32 where that is safe, float64
-// squares where a partial sum left the range in which float32 holds them (a
-// grad above 2^63 or a batch of grads all below 2^-58) or is not finite.
+// Sum of squares of the words base, base + kThreads, ... of a chunk: float32
+// where that is safe, float64 squares where a partial sum left the range in
+// which float32 holds them (a grad above 2^63 or a batch of grads all below
+// 2^-58) or is not finite.  That rare path loads the words again, so that the
+// common one keeps few registers live.
 template <typename GT>
-__device__ __forceinline__ double sum_squares(const uint4 (&w)[kLoads]) {
-  float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-  for (int u = 0; u < kLoads; ++u) {
-    float x[kPerLoad<GT>];
-    widen<GT>(w[u], x);
-#pragma unroll
-    for (int i = 0; i < kPerLoad<GT>; ++i) s[i & 3] = fmaf(x[i], x[i], s[i & 3]);
-  }
-  const float t = (s[0] + s[1]) + (s[2] + s[3]);
-  if (t >= kSumMin && t <= kSumMax) return static_cast<double>(t);
-  uint32_t any = 0u;
-#pragma unroll
-  for (int u = 0; u < kLoads; ++u) any |= w[u].x | w[u].y | w[u].z | w[u].w;
-  if ((any & (sizeof(GT) == 4 ? 0x7FFFFFFFu : 0x7FFF7FFFu)) == 0u) return 0.0;
+__device__ __noinline__ double sum_squares_wide(const uint4* q, int base, int words) {
   double d = 0.0;
-#pragma unroll
   for (int u = 0; u < kLoads; ++u) {
+    const int i = base + u * kThreads;
+    if (i >= words) break;
+    const uint4 w = __ldcs(q + i);
+    // zeros are common (rows of an embedding that no token used) and add nothing
+    if (((w.x | w.y | w.z | w.w) & (sizeof(GT) == 4 ? 0x7FFFFFFFu : 0x7FFF7FFFu)) == 0u) continue;
     float x[kPerLoad<GT>];
-    widen<GT>(w[u], x);
-#pragma unroll
-    for (int i = 0; i < kPerLoad<GT>; ++i) d = fma((double)x[i], (double)x[i], d);
+    widen<GT>(w, x);
+    for (int e = 0; e < kPerLoad<GT>; ++e) d = fma((double)x[e], (double)x[e], d);
   }
   return d;
 }
+template <typename GT>
+__device__ __forceinline__ double sum_squares(const uint4* q, int base, int words) {
+  uint4 w[kLoads];
+#pragma unroll
+  for (int u = 0; u < kLoads; ++u) {
+    const int i = base + u * kThreads;
+    w[u] = i < words ? __ldcs(q + i) : make_uint4(0u, 0u, 0u, 0u);
+  }
+  float2 s[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+#pragma unroll
+  for (int u = 0; u < kLoads; ++u) {
+    float x[kPerLoad<GT>];
+    widen<GT>(w[u], x);
+#pragma unroll
+    for (int i = 0; i < kPerLoad<GT>; i += 2) {
+      const float2 p = make_float2(x[i], x[i + 1]);
+      s[i / 2 & 1] = fma2(p, p, s[i / 2 & 1]);
+    }
+  }
+  const float t = (s[0].x + s[1].x) + (s[0].y + s[1].y);
+  if (t >= kSumMin && t <= kSumMax) return static_cast<double>(t);
+  return sum_squares_wide<GT>(q, base, words);
+}
 
 template <typename GT>
-__global__ void __launch_bounds__(kThreads) grad_norm_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(kThreads, kNormCtasPerSm) grad_norm_kernel(const NormArgs a) {
   constexpr int kPer = kPerLoad<GT>;
   double sum = 0.0;
-  for (int64_t c = blockIdx.x; c < a.n_chunks; c += gridDim.x) {
+  // the next chunk's place in memory is looked up while a chunk is summed
+  const GT* next = nullptr;
+  int next_len = 0;
+  auto look = [&](int64_t c) {
+    if (c >= a.n_chunks) return;
     const Chunk ch = a.chunks[c];
-    const GT* const g = static_cast<const GT*>(a.tensors[ch.tensor].g) + ch.start;
+    next = static_cast<const GT*>(a.tensors[ch.tensor].g) + ch.start;
+    next_len = ch.len;
+  };
+  look(blockIdx.x);
+  for (int64_t c = blockIdx.x; c < a.n_chunks; c += gridDim.x) {
+    const GT* const g = next;
+    const int len = next_len;
+    look(c + gridDim.x);
     if ((reinterpret_cast<uintptr_t>(g) & 15u) == 0u) {
       const uint4* const q = reinterpret_cast<const uint4*>(g);
-      const int words = ch.len / kPer;
-      for (int base = threadIdx.x; base < words; base += kThreads * kLoads) {
-        uint4 w[kLoads];
-#pragma unroll
-        for (int u = 0; u < kLoads; ++u) {
-          const int i = base + u * kThreads;
-          w[u] = i < words ? __ldcs(q + i) : make_uint4(0u, 0u, 0u, 0u);
-        }
-        sum += sum_squares<GT>(w);
-      }
+      const int words = len / kPer;
+      for (int base = threadIdx.x; base < words; base += kThreads * kLoads)
+        sum += sum_squares<GT>(q, base, words);
       const int tail = words * kPer + threadIdx.x;
-      if (tail < ch.len) {
+      if (tail < len) {
         const double x = static_cast<double>(Grad<GT>::load1(g, tail));
         sum = fma(x, x, sum);
       }
     } else {
-      for (int i = threadIdx.x; i < ch.len; i += kThreads) {
+      for (int i = threadIdx.x; i < len; i += kThreads) {
         const double x = static_cast<double>(Grad<GT>::load1(g, i));
         sum = fma(x, x, sum);
       }

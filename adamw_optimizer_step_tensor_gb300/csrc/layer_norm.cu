@@ -24,9 +24,12 @@ namespace {
 
 constexpr int kMaxWidth = 8192;        // of a row in registers
 template <int G> constexpr int kCta = G < 128 ? 128 : G;
-// Resident threads per SM, by the registers a thread with `each` elements needs.
-constexpr int forward_threads(bool vec, int each) {
-  return each == 16 ? (vec ? 1024 : 768) : 512;
+// Resident threads per SM, by the registers a thread with `each` elements needs
+// (a CTA of 512 threads is better off with a second one beside it: 8192 columns
+// take 96 us with 1024 threads and 117 with 512; at 4096 columns 768 threads,
+// which do not spill, take 88 us against 98).
+constexpr int forward_threads(int group, int each) {
+  return group == 512 ? 1024 : (each == 16 ? 768 : 512);
 }
 constexpr int backward_threads(int each) { return each == 16 ? 512 : 256; }
 constexpr int kStages = 4;             // rows on their way per group, at most
@@ -76,11 +79,12 @@ struct Piece {
       return unpack_pair<T>(k % 4 == 0 ? r.x : k % 4 == 1 ? r.y : k % 4 == 2 ? r.z : r.w);
     }
   }
-  // x where pair k's columns lie below the width, else 0.
+  // x where pair k's columns lie below the width, else 0 (a word lies below it
+  // or past it as a whole).
   static __device__ __forceinline__ float2 inside(float2 x, int k, int width, int tid) {
-    if (column(2 * k, tid) >= width) x.x = 0.0f;
-    if (column(2 * k + 1, tid) >= width) x.y = 0.0f;
-    return x;
+    const bool in0 = column(2 * k / E * E, tid) < width;
+    const bool in1 = VEC ? in0 : column(2 * k + 1, tid) < width;
+    return make_float2(in0 ? x.x : 0.0f, in1 ? x.y : 0.0f);
   }
   // Stores f(pair) at every column below the width, rounded once.
   template <typename F>
@@ -134,23 +138,38 @@ __device__ __forceinline__ float2 from_lane(float2 x, int o) {
 // places in turn, so that one barrier per sum is enough.
 template <typename V, int G>
 struct GroupSum {
-  V* part;               // [2][G / 32]
+  static constexpr int kWarps = G / 32;
+  V* part;               // [2][kWarps], 16-byte aligned
   int turn = 0;
   __device__ __forceinline__ V operator()(V x) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) x = plus(x, from_lane(x, o));
     if (G > 32) {
-      V* const p = part + turn * (G / 32);
+      V* const p = part + turn * kWarps;
       turn ^= 1;
       if ((threadIdx.x & 31) == 0) p[threadIdx.x / 32] = x;
       __syncthreads();
-      x = p[0];
+      constexpr int kWords = kWarps * sizeof(V) / 16 > 0 ? kWarps * sizeof(V) / 16 : 1;
+      uint4 w[kWords];
 #pragma unroll
-      for (int i = 1; i < G / 32; ++i) x = plus(x, p[i]);
+      for (int i = 0; i < kWords; ++i) w[i] = reinterpret_cast<const uint4*>(p)[i];
+      const V* const v = reinterpret_cast<const V*>(w);
+      x = v[0];
+#pragma unroll
+      for (int i = 1; i < kWarps; ++i) x = plus(x, v[i]);
     }
     return x;
   }
 };
+
+// 1 / sqrt(x) for x >= 0: the hardware's approximation and one Newton step,
+// about an ulp, in a sixth of the instructions of a root and a division (0 gives
+// inf and inf gives 0, as they do).
+__device__ __forceinline__ float inverse_root(float x) {
+  const float y = rsqrtf(x);
+  const float z = fmaf(y * fmaf(-x * y, y, 1.0f), 0.5f, y);
+  return x > 0.0f && x <= 3.40282347e38f ? z : y;
+}
 
 // The rows of a group, in turn, of ARRAYS matrices: bulk copies into a ring of
 // stages.  `take` leaves the current row in registers, `refill` (after every
@@ -287,13 +306,13 @@ struct Rows {
 };
 
 template <typename T, typename W, bool VEC, int G, int EACH>
-__global__ void __launch_bounds__(kCta<G>, forward_threads(VEC, EACH) / kCta<G>)
+__global__ void __launch_bounds__(kCta<G>, forward_threads(G, EACH) / kCta<G>)
 ln_forward_kernel(const LayerNormArgs a) {
   using P = Piece<T, VEC, G, EACH>;
   constexpr int kPairs = P::kPairs;
   constexpr int kGroups = kCta<G> / G;
   extern __shared__ __align__(16) unsigned char s_ring[];
-  __shared__ float s_part[2 * G / 32];
+  __shared__ __align__(16) float s_part[2 * G / 32];
   __shared__ uint64_t s_full[kGroups][kStages];
   const int group = threadIdx.x / G, tid = threadIdx.x % G;
   GroupSum<float, G> group_sum{s_part};
@@ -322,7 +341,7 @@ ln_forward_kernel(const LayerNormArgs a) {
       sq = fma2(d, d, sq);
     }
     const float var = group_sum(sq.x + sq.y) * inv_width;
-    const float rstd = 1.0f / sqrtf(var + a.eps);
+    const float rstd = inverse_root(var + a.eps);
     P::store(static_cast<T*>(a.y) + t * a.y_stride, a.width, tid, [&](int k) {
       return fma2(mul2(add2(p[0].pair(k), both(-mean)), both(rstd)), w[k], b[k]);
     });
@@ -341,7 +360,7 @@ ln_backward_kernel(const LayerNormArgs a) {
   constexpr int kPairs = P::kPairs;
   constexpr int kGroups = kCta<G> / G;
   extern __shared__ __align__(16) unsigned char s_ring[];
-  __shared__ float2 s_part[2 * G / 32];
+  __shared__ __align__(16) float2 s_part[2 * G / 32];
   __shared__ uint64_t s_full[kGroups][kStages];
   __shared__ float2 s_add[kGroups > 1 ? EACH * G : 1];
   let_next_kernel_start();
@@ -532,7 +551,7 @@ int stages_for(int64_t row_bytes, int per_sm) {
 
 template <typename T, typename W, bool VEC, int G, int EACH>
 int forward_group(LayerNormArgs a, int sms, cudaStream_t s) {
-  constexpr int kGroups = kCta<G> / G, kPerSm = forward_threads(VEC, EACH) / kCta<G>;
+  constexpr int kGroups = kCta<G> / G, kPerSm = forward_threads(G, EACH) / kCta<G>;
   const int64_t ctas = at_most((a.rows + kGroups - 1) / kGroups, static_cast<int64_t>(kPerSm) * sms);
   const int64_t row = Rows<Piece<T, VEC, G, EACH>, T, VEC, G, 1>::pitch_of(a.width);
   a.stages = stages_for<G>(row, kPerSm);
