@@ -36,9 +36,10 @@ def _ptr(t) -> int | None:
 
 
 def _stream(stream) -> int | None:
-    import torch
     if stream is None:
-        stream = torch.cuda.current_stream()
+        # the handle alone: torch.cuda.current_stream() builds a Stream object, 3 us a call
+        from torch._C import _cuda_getCurrentRawStream, _cuda_getDevice
+        return _cuda_getCurrentRawStream(_cuda_getDevice())
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else stream
 
 

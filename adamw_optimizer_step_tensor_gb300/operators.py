@@ -12,16 +12,11 @@ from __future__ import annotations
 
 import torch
 
-from . import _capi
+from . import _capi, _stream
 
 _DTYPES = {torch.float32: _capi.F32, torch.float16: _capi.F16, torch.bfloat16: _capi.BF16}
 _LABEL_BYTES = {torch.int32: 4, torch.int64: 8}
-
-
-def _stream(stream):
-    if stream is None:
-        return torch.cuda.current_stream().cuda_stream
-    return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
+_F32 = torch.float32
 
 
 def _rows(name, t, dtype=None, shape=None):
@@ -30,20 +25,20 @@ def _rows(name, t, dtype=None, shape=None):
         raise ValueError(f"{name} must be a CUDA matrix")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    rows, width = t.shape
-    if width > 1 and t.stride(1) != 1:
+    rows, width = here = t.shape
+    if shape is not None and here != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(here)}")
+    stride, step = t.stride()
+    if step != 1 and width > 1:
         raise ValueError(f"{name} must be contiguous along its last axis")
     if rows < 2:
         return width
-    stride = t.stride(0)
     if stride < width:
         raise ValueError(f"{name} has overlapping rows")
     return stride
 
 
-def _vector(name, t, n, dtype=torch.float32):
+def _vector(name, t, n, dtype=_F32):
     """Address of a contiguous CUDA vector of n elements; None stays None."""
     if t is None:
         return None
@@ -52,6 +47,10 @@ def _vector(name, t, n, dtype=torch.float32):
     if not t.is_cuda or t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous CUDA tensor of {n} elements")
     return t.data_ptr()
+
+
+def _empty(n, like, dtype=_F32):
+    return torch.empty(n, dtype=dtype, device=like.device)
 
 
 class _Plan:
@@ -82,6 +81,7 @@ class FusedTokenLoss(_Plan):
 
     def __init__(self, max_rows: int, max_pairs: int = 0):
         self.plan = _capi.adamw_loss_plan_create(int(max_rows), int(max_pairs))
+        # the argument records, filled anew by every call
         self._z = _capi.adamw_logits()
         self._policy = _capi.adamw_policy()
         self._preference = _capi.adamw_preference()
@@ -110,7 +110,7 @@ class FusedTokenLoss(_Plan):
         if not backward:
             return None, None, 0
         if dlogits is None:
-            dlogits = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+            dlogits = torch.empty_like(logits)
         return dlogits, dlogits.data_ptr(), _rows("dlogits", dlogits, logits.dtype, logits.shape)
 
     def logps(self, logits, labels, *, temperature=1.0, logps=None, lse=None, stream=None):
@@ -119,9 +119,9 @@ class FusedTokenLoss(_Plan):
         z = self._logits(logits, labels, temperature)
         n = logits.shape[0]
         if logps is None:
-            logps = torch.empty(n, dtype=torch.float32, device=logits.device)
+            logps = _empty(n, logits)
         if lse is None:
-            lse = torch.empty(n, dtype=torch.float32, device=logits.device)
+            lse = _empty(n, logits)
         _capi.adamw_token_logps(self.plan, z, _vector("logps", logps, n), _vector("lse", lse, n),
                                 _stream(stream))
         return logps, lse
@@ -147,9 +147,9 @@ class FusedTokenLoss(_Plan):
         p.kl_coef = kl_coef
         p.grad_scale_dev = _vector("grad_scale", grad_scale, 1)
         if stats is None:
-            stats = torch.empty(4, dtype=torch.float32, device=logits.device)
+            stats = _empty(4, logits)
         if logps is None:
-            logps = torch.empty(n, dtype=torch.float32, device=logits.device)
+            logps = _empty(n, logits)
         dlogits, at, stride = self._gradient(logits, dlogits, backward)
         _capi.adamw_policy_loss(self.plan, z, p, _vector("stats", stats, 4), _vector("logps", logps, n),
                                 at, stride, _stream(stream))
@@ -178,11 +178,11 @@ class FusedTokenLoss(_Plan):
         p.label_smoothing = label_smoothing
         p.grad_scale_dev = _vector("grad_scale", grad_scale, 1)
         if stats is None:
-            stats = torch.empty(4, dtype=torch.float32, device=logits.device)
+            stats = _empty(4, logits)
         if rewards is None:
-            rewards = torch.empty(2 * pairs, dtype=torch.float32, device=logits.device)
+            rewards = _empty(2 * pairs, logits)
         if logps is None:
-            logps = torch.empty(n, dtype=torch.float32, device=logits.device)
+            logps = _empty(n, logits)
         dlogits, at, stride = self._gradient(logits, dlogits, backward)
         _capi.adamw_preference_loss(self.plan, z, p, _vector("stats", stats, 4),
                                     _vector("rewards", rewards, 2 * pairs), _vector("logps", logps, n),
@@ -222,11 +222,11 @@ class FusedLayerNorm(_Plan):
         stride, wdt = self._check(x, weight if weight is not None else bias)
         n = x.shape[0]
         if y is None:
-            y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+            y = torch.empty_like(x)
         if mean is None:
-            mean = torch.empty(n, dtype=torch.float32, device=x.device)
+            mean = _empty(n, x)
         if rstd is None:
-            rstd = torch.empty(n, dtype=torch.float32, device=x.device)
+            rstd = _empty(n, x)
         _capi.adamw_layer_norm_forward(
             self.plan, _DTYPES[x.dtype], _DTYPES[wdt], n, x.data_ptr(), stride,
             _vector("weight", weight, self.width, wdt), _vector("bias", bias, self.width, wdt),
@@ -240,11 +240,11 @@ class FusedLayerNorm(_Plan):
         stride, wdt = self._check(x, weight)
         n = x.shape[0]
         if dx is None:
-            dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+            dx = torch.empty_like(x)
         if dweight is None:
-            dweight = torch.empty(self.width, dtype=wdt, device=x.device)
+            dweight = _empty(self.width, x, wdt)
         if dbias is None:
-            dbias = torch.empty(self.width, dtype=wdt, device=x.device)
+            dbias = _empty(self.width, x, wdt)
         _capi.adamw_layer_norm_backward(
             self.plan, _DTYPES[x.dtype], _DTYPES[wdt], n, dy.data_ptr(),
             _rows("dy", dy, x.dtype, x.shape), x.data_ptr(), stride,
