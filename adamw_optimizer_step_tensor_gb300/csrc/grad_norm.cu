@@ -55,8 +55,6 @@ __device__ __noinline__ double sum_squares_wide(const uint4* q, int base, int wo
     const int i = base + u * kThreads;
     if (i >= words) break;
     const uint4 w = __ldcs(q + i);
-    // zeros are common (rows of an embedding that no token used) and add nothing
-    if (((w.x | w.y | w.z | w.w) & (sizeof(GT) == 4 ? 0x7FFFFFFFu : 0x7FFF7FFFu)) == 0u) continue;
     float x[kPerLoad<GT>];
     widen<GT>(w, x);
     for (int e = 0; e < kPerLoad<GT>; ++e) d = fma((double)x[e], (double)x[e], d);
@@ -84,7 +82,53 @@ __device__ __forceinline__ double sum_squares(const uint4* q, int base, int word
   }
   const float t = (s[0].x + s[1].x) + (s[0].y + s[1].y);
   if (t >= kSumMin && t <= kSumMax) return static_cast<double>(t);
+  // zeros are common (rows of an embedding that no token used)
+  uint32_t any = 0u;
+#pragma unroll
+  for (int u = 0; u < kLoads; ++u) any |= w[u].x | w[u].y | w[u].z | w[u].w;
+  if ((any & (sizeof(GT) == 4 ? 0x7FFFFFFFu : 0x7FFF7FFFu)) == 0u) return 0.0;
   return sum_squares_wide<GT>(q, base, words);
+}
+
+// The same for grads off the 16-byte grid, kRun elements at a time.
+constexpr int kRun = 16;
+template <typename GT>
+__device__ __noinline__ double sum_squares_single_wide(const GT* g, int base, int len) {
+  double d = 0.0;
+  for (int u = 0; u < kRun && base + u * kThreads < len; ++u) {
+    const double x = static_cast<double>(Grad<GT>::load1(g, base + u * kThreads));
+    d = fma(x, x, d);
+  }
+  return d;
+}
+template <typename GT>
+__device__ __forceinline__ double sum_squares_single(const GT* g, int base, int len) {
+  float x[kRun], s[2] = {0.0f, 0.0f};
+#pragma unroll
+  for (int u = 0; u < kRun; ++u)
+    x[u] = base + u * kThreads < len ? Grad<GT>::load1(g, base + u * kThreads) : 0.0f;
+#pragma unroll
+  for (int u = 0; u < kRun; ++u) s[u & 1] = fmaf(x[u], x[u], s[u & 1]);
+  const float t = s[0] + s[1];
+  bool zero = true;
+#pragma unroll
+  for (int u = 0; u < kRun; ++u) zero &= x[u] == 0.0f;
+  if (zero) return 0.0;
+  if (t >= kSumMin && t <= kSumMax) return static_cast<double>(t);
+  return sum_squares_single_wide<GT>(g, base, len);
+}
+
+// sqrt(x) / d rounded to float32 from a float64 x >= 0, by a float32 root of the
+// mantissa (float64 roots and divisions take most of a microsecond here).
+__device__ __forceinline__ float root_over(double x, float d) {
+  if (!(x > 0.0) || isinf(x)) return static_cast<float>(x) / d;
+  int e;
+  double m = frexp(x, &e);
+  if (e & 1) {
+    m *= 0.5;
+    ++e;
+  }
+  return ldexpf(sqrtf(static_cast<float>(m)) / d, e / 2);
 }
 
 template <typename GT>
@@ -116,10 +160,8 @@ __global__ void __launch_bounds__(kThreads, kNormCtasPerSm) grad_norm_kernel(con
         sum = fma(x, x, sum);
       }
     } else {
-      for (int i = threadIdx.x; i < len; i += kThreads) {
-        const double x = static_cast<double>(Grad<GT>::load1(g, i));
-        sum = fma(x, x, sum);
-      }
+      for (int base = threadIdx.x; base < len; base += kThreads * kRun)
+        sum += sum_squares_single<GT>(g, base, len);
     }
   }
 
@@ -138,32 +180,23 @@ __global__ void __launch_bounds__(kThreads, kNormCtasPerSm) grad_norm_kernel(con
     s_last = atomicAdd(ticket, 1u) == gridDim.x - 1;
   }
   __syncthreads();
-  if (!s_last) return;
+  if (!s_last || threadIdx.x >= 32) return;
   __threadfence();
   double total = 0.0;
-  for (int i = threadIdx.x; i < gridDim.x; i += kThreads) total += __ldcg(a.partial + i);
+  for (int i = threadIdx.x; i < gridDim.x; i += 32) total += __ldcg(a.partial + i);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, o);
-  if ((threadIdx.x & 31) == 0) s_warp[threadIdx.x >> 5] = total;
-  __syncthreads();
   if (threadIdx.x != 0) return;
-  total = 0.0;
-  for (int i = 0; i < kThreads / 32; ++i) total += s_warp[i];
   const float scale = a.grad_scale != nullptr ? *a.grad_scale : 1.0f;
-  const double norm = sqrt(total) / fabs(static_cast<double>(scale));
-  const float norm32 = static_cast<float>(norm);
-  *a.norm = norm32;
-  if (a.found_inf != nullptr) *a.found_inf = isfinite(norm32) ? 0.0f : 1.0f;
+  const float norm = root_over(total, fabsf(scale));
+  *a.norm = norm;
+  if (a.found_inf != nullptr) *a.found_inf = isfinite(norm) ? 0.0f : 1.0f;
   if (a.clip_scale != nullptr) {
-    // coef >= 1 keeps the scale itself, so an unclipped step is bit-identical
-    // to one without the norm; a NaN norm gives a NaN scale, an infinite one
-    // an infinite scale (grads of 0)
-    float out = scale;
-    if (!isinf(a.max_norm)) {
-      const double coef = static_cast<double>(a.max_norm) / (norm + 1e-6);
-      if (!(coef >= 1.0)) out = static_cast<float>(static_cast<double>(scale) / coef);
-    }
-    *a.clip_scale = out;
+    // at most max_norm keeps the scale itself, so an unclipped step is
+    // bit-identical to one without the norm; a NaN norm gives a NaN scale, an
+    // infinite one an infinite scale (grads of 0)
+    const float over = (norm + 1e-6f) / a.max_norm;
+    *a.clip_scale = isinf(a.max_norm) || over <= 1.0f ? scale : scale * over;
   }
   atomicExch(ticket, 0u);
 }

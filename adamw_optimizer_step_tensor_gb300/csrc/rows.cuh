@@ -120,17 +120,15 @@ __device__ __forceinline__ bool last_cta_sums(const double (&mine)[4], double* p
   if (!__syncthreads_or(last)) return false;
   __threadfence();
   if (threadIdx.x < 32) {
-    double t[4] = {0.0, 0.0, 0.0, 0.0};
-    for (unsigned c = threadIdx.x; c < ctas; c += 32) {
+    // lane 4 k + i: sum i of the CTAs k, k + 8, ... (float64 is slow here: as
+    // few additions after one another as the layout allows)
+    const unsigned i = threadIdx.x & 3u;
+    double t = 0.0;
+    for (unsigned c = threadIdx.x >> 2; c < ctas; c += 8) t += __ldcg(partial + 4 * c + i);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) t[i] += __ldcg(partial + 4 * c + i);
-    }
+    for (int o = 16; o >= 4; o >>= 1) t += __shfl_xor_sync(kFull, t, o);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) t[i] += __shfl_xor_sync(kFull, t[i], o);
-      out[i] = t[i];
-    }
+    for (int m = 0; m < 4; ++m) out[m] = __shfl_sync(kFull, t, m);
     if (threadIdx.x == 0) atomicExch(ticket, 0u);
   }
   return threadIdx.x == 0;

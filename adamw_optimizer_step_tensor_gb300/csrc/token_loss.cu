@@ -43,7 +43,7 @@ constexpr int kJoins = 2;
 constexpr int kStoresOut = 3;                   // copies out whose slots may be awaited later
 constexpr int kMaxCluster = 8;
 constexpr int kRowsPerLane = 8;                 // rows the scheduler looks at per lane and step
-constexpr int kBatch = 4;                       // rows whose inputs it fetches together
+constexpr int kBatch = 2;                       // rows whose inputs it fetches together
 constexpr int kSharePieces = 7;                 // of a row that waits for its sum, at most
 
 // Warps of either kind; a pass with one kind gives it all of them.
@@ -693,7 +693,8 @@ __global__ void __launch_bounds__(kPairThreads) pair_kernel(const LossArgs a) {
                           d > 0.0f ? 1.0 : 0.0, chosen, rejected};
   double out[4];
   if (last_cta_sums(mine, a.partial, a.ticket, blockIdx.x, gridDim.x, out))
-    for (int i = 0; i < 4; ++i) a.stats[i] = static_cast<float>(out[i] / a.pairs);
+    for (int i = 0; i < 4; ++i)
+      a.stats[i] = static_cast<float>(out[i]) / static_cast<float>(a.pairs);
 }
 
 // ---- launches

@@ -166,12 +166,15 @@ __global__ void __launch_bounds__(kCta<G>, kThreadsPerSm<G> / kCta<G>) small_voc
   if (!policy_pass(pass)) return;
   // the groups' sums in their order, then the CTAs'
   __shared__ double s_acc[kGroups][4];
-  if (tid == 0)
-    for (int m = 0; m < 4; ++m) s_acc[group][m] = acc[m];
-  __syncthreads();
-  double mine[4] = {0.0, 0.0, 0.0, 0.0}, out[4];
-  for (int g = 0; g < kGroups; ++g)
-    for (int m = 0; m < 4; ++m) mine[m] += s_acc[g][m];
+  double mine[4] = {acc[0], acc[1], acc[2], acc[3]}, out[4];
+  if (kGroups > 1) {
+    if (tid == 0)
+      for (int m = 0; m < 4; ++m) s_acc[group][m] = acc[m];
+    __syncthreads();
+    if (threadIdx.x == 0)
+      for (int g = 1; g < kGroups; ++g)
+        for (int m = 0; m < 4; ++m) mine[m] += s_acc[g][m];
+  }
   if (last_cta_sums(mine, a.partial, a.ticket, blockIdx.x, gridDim.x, out)) {
     a.stats[0] = static_cast<float>(out[1] + static_cast<double>(a.kl_coef) * out[2]);
     a.stats[1] = static_cast<float>(out[1]);
