@@ -13,8 +13,8 @@
 // second kernel, always in the same order.
 // Statistics and sums are float32; the variance is the mean of squared
 // differences from the mean (no cancellation).  What bounds both passes is
-// DRAM: two (three) accesses per element.  Rows wider than 8192 take the plain
-// loops at the end of this file.
+// DRAM: two (three) accesses per element.  Rows wider than 16384 take the loops at
+// the end of this file.
 #include "async_copy.cuh"
 #include "operators.h"
 #include "rows.cuh"
@@ -22,16 +22,21 @@
 namespace adamw {
 namespace {
 
-constexpr int kMaxWidth = 8192;        // of a row in registers
+constexpr int kMaxWidth = 16384;       // of a row in registers
 template <int G> constexpr int kCta = G < 128 ? 128 : G;
 // Resident threads per SM, by the registers a thread with `each` elements needs
 // (a CTA of 512 threads is better off with a second one beside it: 8192 columns
 // take 96 us with 1024 threads and 117 with 512; at 4096 columns 768 threads,
 // which do not spill, take 88 us against 98).
 constexpr int forward_threads(int group, int each) {
-  return group == 512 ? 1024 : (each == 16 ? 768 : 512);
+  return group >= 512 ? 1024 : (each == 16 ? 768 : 512);
 }
-constexpr int backward_threads(int each) { return each == 16 ? 512 : 256; }
+// A group of 1024 threads has no registers left for the column sums: they are a
+// kernel of their own then.
+__host__ __device__ constexpr bool sums_columns(int group) { return group <= 512; }
+constexpr int backward_threads(int group, int each) {
+  return !sums_columns(group) ? 1024 : (each == 16 ? 512 : 256);
+}
 constexpr int kStages = 4;             // rows on their way per group, at most
 constexpr int kSmemPerSm = 184 * 1024;  // for the rows on their way
 
@@ -354,7 +359,7 @@ ln_forward_kernel(const LayerNormArgs a) {
 }
 
 template <typename T, typename W, bool VEC, int G, int EACH>
-__global__ void __launch_bounds__(kCta<G>, backward_threads(EACH) / kCta<G>)
+__global__ void __launch_bounds__(kCta<G>, backward_threads(G, EACH) / kCta<G>)
 ln_backward_kernel(const LayerNormArgs a) {
   using P = Piece<T, VEC, G, EACH>;
   constexpr int kPairs = P::kPairs;
@@ -399,8 +404,10 @@ ln_backward_kernel(const LayerNormArgs a) {
       const float2 g = p[1].pair(k), h = mul2(add2(p[0].pair(k), m), r), wg = mul2(g, w[k]);
       sum1 = add2(sum1, wg);
       sum2 = fma2(wg, h, sum2);
-      gw[k] = fma2(g, h, gw[k]);
-      gb[k] = add2(gb[k], g);
+      if (sums_columns(G)) {
+        gw[k] = fma2(g, h, gw[k]);
+        gb[k] = add2(gb[k], g);
+      }
     }
     const float2 s = group_sum(make_float2(sum1.x + sum1.y, sum2.x + sum2.y));
     rows.refill(tid);
@@ -412,7 +419,7 @@ ln_backward_kernel(const LayerNormArgs a) {
     });
   }
   rows.finish(tid, a.fault);
-  if (a.partial == nullptr) return;
+  if (!sums_columns(G) || a.partial == nullptr) return;
   // the CTA's groups, in their order
   for (int g = 1; g < kGroups; ++g) {
     __syncthreads();
@@ -476,28 +483,123 @@ __global__ void __launch_bounds__(kTile * kTile) ln_reduce_kernel(const LayerNor
   if (col == 0 && jt < a.width) static_cast<W*>(out)[jt] = from_f32<W>(t);
 }
 
-// ---- rows wider than the registers of a group: two passes over the row
+// ---- rows wider than the registers of a group
+//
+// A CTA takes a row, its first kKeep words per thread in registers and the rest
+// read again (from L1 and L2) for each pass over it.  Column sums of rows of more
+// than 8192 columns are a kernel of their own, which reads x and dy once more.
 
-constexpr int kWideThreads = 512;
+constexpr int kWideThreads = 1024;
+constexpr int kKeep = 4;
 
-template <typename T, typename W>
+// Words of E elements of a row, E 1 where it is off the 16-byte grid.
+template <typename T, bool VEC>
+struct WideRow {
+  static constexpr int E = VEC ? 16 / sizeof(T) : 1;
+  using Raw = typename std::conditional<VEC, uint4, T>::type;
+  const Raw* p;
+  Raw keep[kKeep];
+  __device__ __forceinline__ WideRow(const T* row, int words) : p(reinterpret_cast<const Raw*>(row)) {
+#pragma unroll
+    for (int i = 0; i < kKeep; ++i)
+      if (static_cast<int>(threadIdx.x) + i * kWideThreads < words)
+        keep[i] = p[threadIdx.x + i * kWideThreads];
+  }
+  static __device__ __forceinline__ void widen(const Raw& r, float (&x)[E]) {
+    if constexpr (!VEC) {
+      x[0] = to_f32(r);
+    } else if constexpr (sizeof(T) == 4) {
+      x[0] = __uint_as_float(r.x);
+      x[1] = __uint_as_float(r.y);
+      x[2] = __uint_as_float(r.z);
+      x[3] = __uint_as_float(r.w);
+    } else {
+      const uint32_t v[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 f = unpack_pair<T>(v[i]);
+        x[2 * i] = f.x;
+        x[2 * i + 1] = f.y;
+      }
+    }
+  }
+  static __device__ __forceinline__ void store(T* row, int word, const float (&x)[E]) {
+    alignas(16) T out[E];
+#pragma unroll
+    for (int i = 0; i < E; ++i) out[i] = from_f32<T>(x[i]);
+    reinterpret_cast<Raw*>(row)[word] = *reinterpret_cast<const Raw*>(out);
+  }
+};
+
+// E consecutive elements of a parameter from column j on (a multiple of E), in
+// 16-byte loads where it lies on the grid: loaded singly, each warp's loads
+// touch a sector per lane, and 8000 x 12288 bf16 took 294 us forward.
+template <typename W, int E>
+__device__ __forceinline__ void param_word(const void* p, int j, float none, float (&out)[E]) {
+  constexpr int kPer = 16 / sizeof(W);
+  if (p == nullptr) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) out[e] = none;
+  } else if (E % kPer == 0 && (reinterpret_cast<uintptr_t>(p) & 15u) == 0u) {
+#pragma unroll
+    for (int i = 0; i < E / kPer; ++i) {
+      const uint4 r = __ldg(reinterpret_cast<const uint4*>(static_cast<const W*>(p) + j) + i);
+      float x[kPer];
+      WideRow<W, true>::widen(r, x);
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) out[i * kPer + e] = x[e];
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < E; ++e) out[e] = to_f32(static_cast<const W*>(p)[j + e]);
+  }
+}
+
+// f(word index, i) for every word of this thread; i < kKeep: it is in `keep`.
+template <typename F>
+__device__ __forceinline__ void wide_words(int words, F f) {
+#pragma unroll
+  for (int i = 0; i < kKeep; ++i)
+    if (static_cast<int>(threadIdx.x) + i * kWideThreads < words)
+      f(static_cast<int>(threadIdx.x) + i * kWideThreads, i);
+  for (int w = threadIdx.x + kKeep * kWideThreads; w < words; w += kWideThreads) f(w, kKeep);
+}
+
+template <typename T, typename W, bool VEC>
 __global__ void __launch_bounds__(kWideThreads) ln_forward_wide_kernel(const LayerNormArgs a) {
   __shared__ float s_warp[kWideThreads / 32];
+  using Row = WideRow<T, VEC>;
+  constexpr int E = Row::E;
+  const int words = a.width / E;
   for (int64_t t = blockIdx.x; t < a.rows; t += gridDim.x) {
-    const T* const x = static_cast<const T*>(a.x) + t * a.x_stride;
+    const Row x(static_cast<const T*>(a.x) + t * a.x_stride, words);
     T* const y = static_cast<T*>(a.y) + t * a.y_stride;
+    auto get = [&](int w, int i, float (&v)[E]) { Row::widen(i < kKeep ? x.keep[i] : x.p[w], v); };
     float sum = 0.0f;
-    for (int j = threadIdx.x; j < a.width; j += kWideThreads) sum += to_f32(x[j]);
+    wide_words(words, [&](int w, int i) {
+      float v[E];
+      get(w, i, v);
+#pragma unroll
+      for (int e = 0; e < E; ++e) sum += v[e];
+    });
     const float mean = block_sum<kWideThreads>(sum, s_warp) / a.width;
     float sq = 0.0f;
-    for (int j = threadIdx.x; j < a.width; j += kWideThreads) {
-      const float d = to_f32(x[j]) - mean;
-      sq = fmaf(d, d, sq);
-    }
-    const float rstd = 1.0f / sqrtf(block_sum<kWideThreads>(sq, s_warp) / a.width + a.eps);
-    for (int j = threadIdx.x; j < a.width; j += kWideThreads)
-      y[j] = from_f32<T>(fmaf((to_f32(x[j]) - mean) * rstd, param<W>(a.weight, j, 1.0f),
-                              param<W>(a.bias, j, 0.0f)));
+    wide_words(words, [&](int w, int i) {
+      float v[E];
+      get(w, i, v);
+#pragma unroll
+      for (int e = 0; e < E; ++e) sq = fmaf(v[e] - mean, v[e] - mean, sq);
+    });
+    const float rstd = inverse_root(block_sum<kWideThreads>(sq, s_warp) / a.width + a.eps);
+    wide_words(words, [&](int w, int i) {
+      float v[E], weight[E], bias[E];
+      get(w, i, v);
+      param_word<W, E>(a.weight, w * E, 1.0f, weight);
+      param_word<W, E>(a.bias, w * E, 0.0f, bias);
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[e] = fmaf((v[e] - mean) * rstd, weight[e], bias[e]);
+      Row::store(y, w, v);
+    });
     if (threadIdx.x == 0) {
       a.mean[t] = mean;
       a.rstd[t] = rstd;
@@ -505,36 +607,95 @@ __global__ void __launch_bounds__(kWideThreads) ln_forward_wide_kernel(const Lay
   }
 }
 
-// The column sums live in the CTA's own row of partial sums.
-template <typename T, typename W>
+template <typename T, typename W, bool VEC>
 __global__ void __launch_bounds__(kWideThreads) ln_backward_wide_kernel(const LayerNormArgs a) {
   __shared__ float s_warp[kWideThreads / 32];
-  let_next_kernel_start();
-  float* const pw = a.partial + static_cast<int64_t>(blockIdx.x) * a.width;
-  float* const pb = pw + static_cast<int64_t>(a.parts) * a.width;
-  bool first = true;
+  using Row = WideRow<T, VEC>;
+  constexpr int E = Row::E;
+  const int words = a.width / E;
   for (int64_t t = blockIdx.x; t < a.rows; t += gridDim.x) {
-    const T* const x = static_cast<const T*>(a.x) + t * a.x_stride;
-    const T* const dy = static_cast<const T*>(a.dy) + t * a.dy_stride;
+    const Row x(static_cast<const T*>(a.x) + t * a.x_stride, words);
+    const Row dy(static_cast<const T*>(a.dy) + t * a.dy_stride, words);
     T* const dx = static_cast<T*>(a.dx) + t * a.dx_stride;
     const float mean = a.mean[t], rstd = a.rstd[t];
+    // xhat and w dy of a word
+    auto get = [&](int w, int i, float (&h)[E], float (&g)[E]) {
+      Row::widen(i < kKeep ? x.keep[i] : x.p[w], h);
+      Row::widen(i < kKeep ? dy.keep[i] : dy.p[w], g);
+      float weight[E];
+      param_word<W, E>(a.weight, w * E, 1.0f, weight);
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        h[e] = (h[e] - mean) * rstd;
+        g[e] *= weight[e];
+      }
+    };
     float s1 = 0.0f, s2 = 0.0f;
-    for (int j = threadIdx.x; j < a.width; j += kWideThreads) {
-      const float g = to_f32(dy[j]), h = (to_f32(x[j]) - mean) * rstd;
-      const float wg = g * param<W>(a.weight, j, 1.0f);
-      s1 += wg;
-      s2 = fmaf(wg, h, s2);
-      pw[j] = first ? g * h : fmaf(g, h, pw[j]);
-      pb[j] = first ? g : pb[j] + g;
-    }
-    first = false;
+    wide_words(words, [&](int w, int i) {
+      float h[E], g[E];
+      get(w, i, h, g);
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        s1 += g[e];
+        s2 = fmaf(g[e], h[e], s2);
+      }
+    });
     const float m1 = block_sum<kWideThreads>(s1, s_warp) / a.width;
     const float m2 = block_sum<kWideThreads>(s2, s_warp) / a.width;
-    for (int j = threadIdx.x; j < a.width; j += kWideThreads) {
-      const float h = (to_f32(x[j]) - mean) * rstd;
-      const float wg = to_f32(dy[j]) * param<W>(a.weight, j, 1.0f);
-      dx[j] = from_f32<T>(rstd * (wg - m1 - h * m2));
+    wide_words(words, [&](int w, int i) {
+      float h[E], g[E];
+      get(w, i, h, g);
+#pragma unroll
+      for (int e = 0; e < E; ++e) g[e] = rstd * (g[e] - m1 - h[e] * m2);
+      Row::store(dx, w, g);
+    });
+  }
+}
+
+// Column sums over the rows blockIdx.y, blockIdx.y + parts, ...; a thread has one
+// word of columns.
+constexpr int kColumnThreads = 256;
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(kColumnThreads) ln_columns_wide_kernel(const LayerNormArgs a) {
+  using Row = WideRow<T, VEC>;
+  constexpr int E = Row::E;
+  constexpr int kRows = 4;               // loads of as many rows under way
+  const int w = blockIdx.x * kColumnThreads + threadIdx.x;
+  if (w * E >= a.width) return;
+  float gw[E], gb[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) gw[e] = gb[e] = 0.0f;
+  for (int64_t t0 = blockIdx.y; t0 < a.rows; t0 += static_cast<int64_t>(kRows) * a.parts) {
+    typename Row::Raw x[kRows], g[kRows];
+    float mean[kRows], rstd[kRows];
+#pragma unroll
+    for (int u = 0; u < kRows; ++u) {
+      const int64_t t = t0 + static_cast<int64_t>(u) * a.parts;
+      if (t >= a.rows) break;
+      x[u] = reinterpret_cast<const typename Row::Raw*>(static_cast<const T*>(a.x) + t * a.x_stride)[w];
+      g[u] = reinterpret_cast<const typename Row::Raw*>(static_cast<const T*>(a.dy) + t * a.dy_stride)[w];
+      mean[u] = a.mean[t];
+      rstd[u] = a.rstd[t];
     }
+#pragma unroll
+    for (int u = 0; u < kRows; ++u) {
+      if (t0 + static_cast<int64_t>(u) * a.parts >= a.rows) break;
+      float h[E], d[E];
+      Row::widen(x[u], h);
+      Row::widen(g[u], d);
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        gw[e] = fmaf(d[e], (h[e] - mean[u]) * rstd[u], gw[e]);
+        gb[e] += d[e];
+      }
+    }
+  }
+  float* const pw = a.partial + static_cast<int64_t>(blockIdx.y) * a.width + w * E;
+  float* const pb = pw + static_cast<int64_t>(a.parts) * a.width;
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    pw[e] = gw[e];
+    pb[e] = gb[e];
   }
 }
 
@@ -562,16 +723,17 @@ int forward_group(LayerNormArgs a, int sms, cudaStream_t s) {
 
 template <typename T, typename W, bool VEC, int G, int EACH>
 int backward_group(LayerNormArgs a, int sms, cudaStream_t s) {
-  constexpr int kGroups = kCta<G> / G, kPerSm = backward_threads(EACH) / kCta<G>;
+  constexpr int kGroups = kCta<G> / G, kPerSm = backward_threads(G, EACH) / kCta<G>;
   static_assert(kPerSm <= kNormPartsPerSm, "partial sums of every CTA");
-  a.parts = static_cast<int32_t>(
+  const int32_t ctas = static_cast<int32_t>(
       at_most((a.rows + kGroups - 1) / kGroups, static_cast<int64_t>(kPerSm) * sms));
+  a.parts = ctas;
   if (a.dweight == nullptr && a.dbias == nullptr) a.partial = nullptr;
   const int64_t row = 2 * static_cast<int64_t>(
                               Rows<Piece<T, VEC, G, EACH>, T, VEC, G, 2>::pitch_of(a.width));
   a.stages = stages_for<G>(row, kPerSm);
-  ln_backward_kernel<T, W, VEC, G, EACH><<<a.parts, kCta<G>, kGroups * a.stages * row, s>>>(a);
-  return a.parts;
+  ln_backward_kernel<T, W, VEC, G, EACH><<<ctas, kCta<G>, kGroups * a.stages * row, s>>>(a);
+  return ctas;
 }
 
 // The group of a width.
@@ -580,7 +742,8 @@ int backward_group(LayerNormArgs a, int sms, cudaStream_t s) {
    : a.width <= 1024 ? call(32, 32)     \
    : a.width <= 2048 ? call(128, 16)    \
    : a.width <= 4096 ? call(256, 16)    \
-                     : call(512, 16))
+   : a.width <= 8192 ? call(512, 16)    \
+                     : call(1024, 16))
 
 // Lets the row kernels of one width use the shared memory of their stages.
 template <typename T, typename W, bool VEC, int G, int EACH>
@@ -619,11 +782,13 @@ template <typename T, typename W>
 cudaError_t forward(const LayerNormArgs& a, int sms, cudaStream_t s) {
   const int64_t z = sizeof(T);
   const bool vec = on_grid(a.x, a.x_stride * z) && on_grid(a.y, a.y_stride * z) && a.width * z % 16 == 0;
-  if (a.width > kMaxWidth)
-    ln_forward_wide_kernel<T, W>
-        <<<static_cast<int>(at_most(a.rows, 4LL * sms)), kWideThreads, 0, s>>>(a);
-  else
+  if (a.width > kMaxWidth) {
+    const int ctas = static_cast<int>(at_most(a.rows, 2LL * sms));
+    if (vec) ln_forward_wide_kernel<T, W, true><<<ctas, kWideThreads, 0, s>>>(a);
+    else ln_forward_wide_kernel<T, W, false><<<ctas, kWideThreads, 0, s>>>(a);
+  } else {
     ADAMW_LN_GROUPS(ADAMW_LN_FORWARD);
+  }
   return cudaGetLastError();
 }
 
@@ -634,11 +799,26 @@ cudaError_t backward(LayerNormArgs a, int sms, cudaStream_t s) {
                    on_grid(a.dx, a.dx_stride * z) && a.width * z % 16 == 0;
   if (a.rows == 0) {
     a.parts = 0;
-  } else if (a.width > kMaxWidth) {
-    a.parts = static_cast<int32_t>(at_most(a.rows, static_cast<int64_t>(kNormPartsPerSm) * sms));
-    ln_backward_wide_kernel<T, W><<<a.parts, kWideThreads, 0, s>>>(a);
   } else {
-    a.parts = ADAMW_LN_GROUPS(ADAMW_LN_BACKWARD);
+    const bool own_columns = a.width > 512 * 16;
+    if (own_columns && (a.dweight != nullptr || a.dbias != nullptr)) {
+      // before the rows: dx may be dy.  One wave of CTAs.
+      const int columns = (a.width / (vec ? 16 / static_cast<int>(sizeof(T)) : 1) + kColumnThreads - 1) /
+                          kColumnThreads;
+      const int64_t most = static_cast<int64_t>(kNormPartsPerSm) * sms;
+      a.parts = static_cast<int32_t>(at_most(a.rows, columns < most ? most / columns : 1));
+      const dim3 grid(columns, a.parts);
+      if (vec) ln_columns_wide_kernel<T, true><<<grid, kColumnThreads, 0, s>>>(a);
+      else ln_columns_wide_kernel<T, false><<<grid, kColumnThreads, 0, s>>>(a);
+    }
+    if (a.width > kMaxWidth) {
+      const int ctas = static_cast<int>(at_most(a.rows, 2LL * sms));
+      if (vec) ln_backward_wide_kernel<T, W, true><<<ctas, kWideThreads, 0, s>>>(a);
+      else ln_backward_wide_kernel<T, W, false><<<ctas, kWideThreads, 0, s>>>(a);
+    } else {
+      const int ctas = ADAMW_LN_GROUPS(ADAMW_LN_BACKWARD);
+      if (!own_columns) a.parts = ctas;
+    }
   }
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || (a.dweight == nullptr && a.dbias == nullptr)) return e;

@@ -612,12 +612,8 @@ __global__ void __launch_bounds__(kRingThreads, 1) ring_kernel(const LossArgs a,
     __syncthreads();
     const double mine[4] = {s_acc[0], s_acc[1], s_acc[2], s_acc[3]};
     double out[4];
-    if (last_cta_sums(mine, a.partial, a.ticket, blockIdx.x / ranks, gridDim.x / ranks, out)) {
-      a.stats[0] = static_cast<float>(out[1] + static_cast<double>(a.kl_coef) * out[2]);
-      a.stats[1] = static_cast<float>(out[1]);
-      a.stats[2] = static_cast<float>(out[2]);
-      a.stats[3] = static_cast<float>(out[3]);
-    }
+    if (last_cta_sums(mine, a.partial, a.ticket, blockIdx.x / ranks, gridDim.x / ranks, out))
+      write_policy_stats(a, out);
   }
 }
 
@@ -631,7 +627,7 @@ struct PairSum {
   float s = 0.0f, e = 0.0f;
   __device__ __forceinline__ void add(float x, float xe = 0.0f) {
     const float t = s + x, b = t - s;
-    e += (s - (t - b)) + (x - b) + xe;
+    if (isfinite(t)) e += (s - (t - b)) + (x - b) + xe;   // an infinite sum has no error
     s = t;
   }
 };
@@ -689,8 +685,9 @@ __global__ void __launch_bounds__(kPairThreads) pair_kernel(const LossArgs a) {
     const float w = weight(t);
     if (w != 0.0f) a.row_coef[t] = w * (side == 0 ? slope : -slope);
   }
-  const double mine[4] = {(1.0f - e) * minus_log_sigmoid(d) + e * minus_log_sigmoid(-d),
-                          d > 0.0f ? 1.0 : 0.0, chosen, rejected};
+  float loss = (1.0f - e) * minus_log_sigmoid(d);
+  if (e > 0.0f) loss += e * minus_log_sigmoid(-d);         // not 0 * inf
+  const double mine[4] = {loss, d > 0.0f ? 1.0 : 0.0, chosen, rejected};
   double out[4];
   if (last_cta_sums(mine, a.partial, a.ticket, blockIdx.x, gridDim.x, out))
     for (int i = 0; i < 4; ++i)

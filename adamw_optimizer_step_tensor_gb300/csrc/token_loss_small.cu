@@ -175,12 +175,8 @@ __global__ void __launch_bounds__(kCta<G>, kThreadsPerSm<G> / kCta<G>) small_voc
       for (int g = 1; g < kGroups; ++g)
         for (int m = 0; m < 4; ++m) mine[m] += s_acc[g][m];
   }
-  if (last_cta_sums(mine, a.partial, a.ticket, blockIdx.x, gridDim.x, out)) {
-    a.stats[0] = static_cast<float>(out[1] + static_cast<double>(a.kl_coef) * out[2]);
-    a.stats[1] = static_cast<float>(out[1]);
-    a.stats[2] = static_cast<float>(out[2]);
-    a.stats[3] = static_cast<float>(out[3]);
-  }
+  if (last_cta_sums(mine, a.partial, a.ticket, blockIdx.x, gridDim.x, out))
+    write_policy_stats(a, out);
 }
 
 template <typename T, int G>

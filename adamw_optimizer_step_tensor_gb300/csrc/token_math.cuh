@@ -120,13 +120,24 @@ __device__ __forceinline__ PolicyTerm policy_term(const LossArgs& a, const Polic
   r.slope = cut ? 0.0f : -in.adv * ratio;
   r.kl = 0.0f;
   if (a.ref_logps != nullptr) {
+    // e^x - x - 1 is inf where e^x is, and a term without a coefficient adds
+    // nothing, inf or not
     const float x = in.ref - logp;
     const float e = expm1f(x);
-    r.kl = in.w * (e - x);
-    r.slope = fmaf(-a.kl_coef, e, r.slope);
+    r.kl = in.w * (isinf(e) ? e : e - x);
+    if (a.kl_coef > 0.0f) r.slope = fmaf(-a.kl_coef, e, r.slope);
   }
   r.slope *= in.w;
   return r;
+}
+
+// stats from the rows' sums { -, policy, KL, clipped weight }.
+__device__ __forceinline__ void write_policy_stats(const LossArgs& a, const double (&sum)[4]) {
+  const double kl = a.kl_coef > 0.0f ? static_cast<double>(a.kl_coef) * sum[2] : 0.0;
+  a.stats[0] = static_cast<float>(sum[1] + kl);
+  a.stats[1] = static_cast<float>(sum[1]);
+  a.stats[2] = static_cast<float>(sum[2]);
+  a.stats[3] = static_cast<float>(sum[3]);
 }
 
 // ---- 16-byte words of a row: 8 or 4 elements, in pairs

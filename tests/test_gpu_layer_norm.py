@@ -102,6 +102,13 @@ def test_rows(rows, width):
     check(rows, width, torch.bfloat16, torch.bfloat16)
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("width", [8193, 10_001, 12_288, 36_864])
+def test_wide_rows(width, dtype):
+    check(700 if width < 20_000 else 310, width, dtype, dtype)
+    check(5, width, dtype, torch.float32, pad=3, shift=1)
+
+
 def test_many_rows():
     check(33_000, 65, torch.float32, torch.float32)
     check(33_000, 128, torch.float16, torch.float16)

@@ -277,6 +277,32 @@ def test_very_large_vocabularies(dtype, vocab):
     check_preference(b, np.array([0, 2, 5], np.int32))
 
 
+def test_losses_of_a_token_of_probability_zero():
+    """An infinite log ratio stays in its pair's numbers: no NaN where the definition has none."""
+    def edit(z, y, w, rng):
+        z[1, y[1]] = -np.inf
+    for vocab in (300, 40_003):
+        b = Batch(8, vocab, torch.float32, edit=edit, masked=0.0)
+        ref = b.vec(np.full(8, -5.0))
+        loss = FusedTokenLoss(8, 2)
+        inf, one = float("inf"), torch.ones(8, device="cuda")
+        # row 1 in the first chosen sequence
+        stats, rewards, _, dz = loss.preference(b.logits, b.labels, None, ref, dev(np.array([0, 2, 4, 6, 8], np.int32)))
+        assert float(rewards[0]) == -inf and torch.isfinite(rewards[1:]).all()
+        assert float(stats[0]) == inf and float(stats[2]) == -inf and torch.isfinite(dz[2:]).all()
+        # and in the first rejected one: the pair is won
+        stats, rewards, _, dz = loss.preference(b.logits, b.labels, None, ref, dev(np.array([2, 4, 6, 6, 8], np.int32)))
+        stats2, rewards2, _, dz2 = loss.preference(
+            b.logits.roll(6, 0), b.labels.roll(6, 0), None, ref, dev(np.array([0, 2, 4, 8, 8], np.int32)))
+        assert torch.isfinite(stats).all() and torch.isfinite(dz).all()
+        assert float(rewards2[2]) == -inf and torch.isfinite(stats2[:3]).all() and torch.isfinite(dz2).all()
+        # the policy's KL is infinite, its clipped part is not; without a coefficient nothing is
+        stats, _, _ = loss.policy(b.logits, b.labels, one, one, ref, ref, kl_coef=0.1, backward=False)
+        assert torch.isfinite(stats[1]) and float(stats[2]) == inf and float(stats[0]) == inf
+        stats, _, dz = loss.policy(b.logits, b.labels, one, one, ref, ref, kl_coef=0.0)
+        assert torch.isfinite(stats[:2]).all() and torch.isfinite(dz).all()
+
+
 def test_large_logits():
     """Logits of several hundred: the softmax depends on differences alone."""
     for vocab in (500, 30_000):
