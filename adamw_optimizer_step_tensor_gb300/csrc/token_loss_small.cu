@@ -1,11 +1,13 @@
 // token_loss_small.cu -- the token losses' row kernel for small vocabularies: a
-// group of 32 to 256 threads holds a row's logits in registers (at most 8
+// group of 32 to 512 threads holds a row's logits in registers (at most 8
 // words of 16 bytes each), sums, and writes the gradient from them.  Rows are
 // dealt out to the groups of a resident grid in turn.
 //
-// A row of 32 KB or less keeps an SM's share of DRAM busy for 1.5 us or less,
-// which the ring kernel's hand-over from role to role costs by itself; here
-// many independent groups per SM overlap one another's waits.
+// A row of 64 KB or less keeps an SM's share of DRAM busy for 3 us or less, much
+// of which the ring kernel's hand-over from role to role costs by itself (8000
+// bf16 rows of 16,384: 145 us there, 84 here); here many independent groups per
+// SM overlap one another's waits.  Fetching the next row ahead into shared memory
+// was slower (95 us): issue, not load latency, is what the groups share.
 #include "token_rows.cuh"
 
 namespace adamw {
@@ -82,7 +84,7 @@ __global__ void __launch_bounds__(kCta<G>, kThreadsPerSm<G> / kCta<G>) small_voc
     uint4 v[kWordsEach];
 #pragma unroll
     for (int m = 0; m < kWordsEach; ++m)
-      if (tid + m * G < share.words) v[m] = __ldcs(q + tid + m * G);
+      v[m] = tid + m * G < share.words ? __ldcs(q + tid + m * G) : lowest_word<T>();
     const int e = tid < 16 ? ragged_element(share, a.vocab, tid) : -1;
     const float edge = e >= 0 ? to_f32(z[e]) : 0.0f;
     RowSum r{kLowest, 0.0f};
@@ -96,10 +98,10 @@ __global__ void __launch_bounds__(kCta<G>, kThreadsPerSm<G> / kCta<G>) small_voc
         if (a.ref_logps != nullptr) in.ref = a.ref_logps[t];
       }
 #pragma unroll
-      for (int m = 0; m < kWordsEach; ++m)
+      for (int m = 0; m < kWordsEach; m += 2)
         if (tid + m * G < share.words) {
-          const uint4 one[1] = {v[m]};
-          add_words<T, 1>(a, one, r);
+          const uint4 two[2] = {v[m], v[m + 1]};
+          add_words<T, 2>(a, two, r);
         }
       if (e >= 0) {
         r.raise(edge * a.k);
@@ -113,9 +115,9 @@ __global__ void __launch_bounds__(kCta<G>, kThreadsPerSm<G> / kCta<G>) small_voc
         turn ^= 1;
         if (lane == 0) part[warp] = make_float2(r.c, r.s);
         group_sync<G>(group);
-        r = RowSum{part[0].x, part[0].y};
-#pragma unroll
-        for (int m = 1; m < G / 32; ++m) r.join(part[m].x, part[m].y);
+        r = RowSum{kLowest, 0.0f};
+        if (lane < G / 32) r = RowSum{part[lane].x, part[lane].y};
+        r.join_lanes();
       }
       const Log2Sum l = log2_sum(r);
       const float logp = logp_of(a, zy, l);

@@ -165,6 +165,14 @@ __device__ __forceinline__ uint4 pack(const float2 (&x)[kPerWord<T> / 2]) {
   }
 }
 
+// A word of -inf: it adds nothing to a sum.
+template <typename T>
+__device__ __forceinline__ uint4 lowest_word() {
+  constexpr uint32_t v = sizeof(T) == 4 ? 0xFF800000u
+                                        : (std::is_same<T, __half>::value ? 0xFC00FC00u : 0xFF80FF80u);
+  return make_uint4(v, v, v, v);
+}
+
 // The largest element of N words, NaN ignored (16-bit types two at a time).
 template <typename T, int N>
 __device__ __forceinline__ float words_max(const uint4 (&w)[N]) {
