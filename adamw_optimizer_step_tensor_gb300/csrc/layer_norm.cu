@@ -45,35 +45,75 @@ __device__ __forceinline__ float param(const void* p, int j, float none) {
   return p != nullptr ? to_f32(static_cast<const W*>(p)[j]) : none;
 }
 
-// A thread's EACH elements of a row as loaded: 16-byte words where every row starts on the
-// 16-byte grid, else single elements; thread tid has the columns
-// (i G + tid) E .. + E - 1.  The arithmetic takes them in pairs (two float32
-// operations per instruction: without, both passes issued 22 to 27 instructions
-// per element and were bound by that).
-template <typename T, bool VEC, int G, int EACH>
-struct Piece {
-  static constexpr int E = VEC ? 16 / sizeof(T) : 1;
-  static constexpr int N = EACH / E;
-  static constexpr int kPairs = EACH / 2;
-  using Raw = typename std::conditional<VEC, uint4, T>::type;
-  Raw raw[N];
+// How the rows of a call's matrices lie: on the 16-byte grid; off it, a row of
+// each matrix by the same shift (dense rows of an odd width); each in its own way.
+enum class Lie { grid, shifted, any };
 
-  // Column of element m.
-  static __device__ __forceinline__ int column(int m, int tid) {
-    return (m / E * G + tid) * E + m % E;
-  }
+// A thread's EACH elements of a row as loaded: 16-byte words of a row whose
+// first one starts after `head` elements, or single elements where the matrices
+// lie each in its own way; thread tid has the columns
+// head + (i G + tid) E .. + E - 1.  A shifted row's elements before its first and
+// after its last whole word, fewer than E each, go one each to the last threads
+// as a pair more.  (Masked words at both ends instead cost every warp with one of
+// them as much again as the rest of a row.)  Rows `period` apart have the same
+// shift and a CTA keeps to such rows, so that a thread keeps its columns.
+// 32768 rows of bfloat16, with words against single elements, us: 1601 columns
+// forward 55 against 74, backward 78 against 92; 5001 columns 197 against 404 and
+// 268 against 370.  float32 gains less (5001: 231 against 390, 335 against 360)
+// and nothing at 1601 (80 against 74, 102 against 104).
+// The arithmetic takes the columns in pairs (two float32 operations per
+// instruction: without, both passes issued 22 to 27 instructions per element and
+// were bound by that).
+template <typename T, Lie LIE, int G, int EACH>
+struct Piece {
+  static constexpr bool kWords = LIE != Lie::any;
+  static constexpr bool kShifted = LIE == Lie::shifted;
+  static constexpr int E = kWords ? 16 / sizeof(T) : 1;
+  static constexpr int N = EACH / E;
+  static constexpr int kPairs = EACH / 2 + (kShifted ? 1 : 0);
+  using Raw = typename std::conditional<kWords, uint4, T>::type;
+  Raw raw[N];
+  T end[2];              // of a shifted row: of its first and of its last elements
+
+  // A thread's place in the rows.
+  struct Place {
+    int tid, width;
+    int shift;           // elements from the 16-byte grid to the row
+    int head, tail;      // columns [0, head) and [tail, width) lie outside whole words
+    __device__ __forceinline__ Place(int tid_, int width_, int shift_)
+        : tid(tid_), width(width_), shift(kShifted ? shift_ : 0), head(0), tail(width_) {
+      if (kShifted) {
+        head = min((E - shift) % E, width);
+        tail = head + (width - head) / E * E;
+      }
+    }
+    // Column of element m, and whether the thread has it.
+    __device__ __forceinline__ int column(int m) const {
+      if (m >= EACH) return (m == EACH ? 0 : tail) + G - 1 - tid;
+      return head + (m / E * G + tid) * E + m % E;
+    }
+    __device__ __forceinline__ bool has(int m) const {
+      return column(m) < (m < EACH ? tail : m == EACH ? head : width);
+    }
+    // Whether it has no part in pair k, the one more of a shifted row.
+    __device__ __forceinline__ bool idle(int k) const { return k >= EACH / 2 && tid < G - E; }
+    // Whether it has word i (a word has all its elements or none).
+    __device__ __forceinline__ bool word(int i) const { return has(i * E); }
+  };
+
   static __device__ __forceinline__ Raw zero() {
-    if constexpr (VEC) return make_uint4(0u, 0u, 0u, 0u);
+    if constexpr (kWords) return make_uint4(0u, 0u, 0u, 0u);
     else return from_f32<T>(0.0f);
   }
-  // From a row in shared memory; columns past the width read as 0.
-  __device__ __forceinline__ void load(const unsigned char* row, int width, int tid) {
+  // From a row's whole words in shared memory; elements it has not read as 0.
+  __device__ __forceinline__ void load(const unsigned char* words, const Place& at) {
 #pragma unroll
     for (int i = 0; i < N; ++i)
-      raw[i] = column(i * E, tid) < width ? reinterpret_cast<const Raw*>(row)[i * G + tid] : zero();
+      raw[i] = at.word(i) ? reinterpret_cast<const Raw*>(words)[i * G + at.tid] : zero();
   }
   __device__ __forceinline__ float2 pair(int k) const {
-    if constexpr (!VEC) {
+    if (k >= EACH / 2) return make_float2(to_f32(end[0]), to_f32(end[1]));
+    if constexpr (!kWords) {
       return make_float2(to_f32(raw[2 * k]), to_f32(raw[2 * k + 1]));
     } else if constexpr (sizeof(T) == 4) {
       const uint4& r = raw[k / 2];
@@ -84,27 +124,26 @@ struct Piece {
       return unpack_pair<T>(k % 4 == 0 ? r.x : k % 4 == 1 ? r.y : k % 4 == 2 ? r.z : r.w);
     }
   }
-  // x where pair k's columns lie below the width, else 0 (a word lies below it
-  // or past it as a whole).
-  static __device__ __forceinline__ float2 inside(float2 x, int k, int width, int tid) {
-    const bool in0 = column(2 * k / E * E, tid) < width;
-    const bool in1 = VEC ? in0 : column(2 * k + 1, tid) < width;
+  // x where the thread has pair k's elements, else 0.
+  static __device__ __forceinline__ float2 inside(float2 x, int k, const Place& at) {
+    const bool in0 = k < EACH / 2 ? at.word(2 * k / E) : at.has(2 * k);
+    const bool in1 = kWords && k < EACH / 2 ? in0 : at.has(2 * k + 1);
     return make_float2(in0 ? x.x : 0.0f, in1 ? x.y : 0.0f);
   }
-  // Stores f(pair) at every column below the width, rounded once.
+  // Stores f(pair) at every column the thread has, rounded once.
   template <typename F>
-  static __device__ __forceinline__ void store(T* row, int width, int tid, F f) {
-    if constexpr (!VEC) {
+  static __device__ __forceinline__ void store(T* row, const Place& at, F f) {
 #pragma unroll
-      for (int k = 0; k < kPairs; ++k) {
-        const float2 x = f(k);
-        if (column(2 * k, tid) < width) row[column(2 * k, tid)] = from_f32<T>(x.x);
-        if (column(2 * k + 1, tid) < width) row[column(2 * k + 1, tid)] = from_f32<T>(x.y);
-      }
-    } else {
+    for (int k = kWords ? EACH / 2 : 0; k < kPairs; ++k) {
+      if (at.idle(k)) continue;
+      const float2 x = f(k);
+      if (at.has(2 * k)) row[at.column(2 * k)] = from_f32<T>(x.x);
+      if (at.has(2 * k + 1)) row[at.column(2 * k + 1)] = from_f32<T>(x.y);
+    }
+    if constexpr (kWords) {
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        if (column(i * E, tid) >= width) continue;
+        if (!at.word(i)) continue;
         uint4 out;
         if constexpr (sizeof(T) == 4) {
           const float2 x = f(2 * i), y = f(2 * i + 1);
@@ -114,22 +153,20 @@ struct Piece {
           out = make_uint4(pack_pair<T>(f(4 * i)), pack_pair<T>(f(4 * i + 1)),
                            pack_pair<T>(f(4 * i + 2)), pack_pair<T>(f(4 * i + 3)));
         }
-        __stcs(reinterpret_cast<uint4*>(row + column(i * E, tid)), out);
+        __stcs(reinterpret_cast<uint4*>(row + at.column(i * E)), out);
       }
     }
   }
 };
 
-// A thread's pairs of a parameter; 0 past the width.
+// A thread's pairs of a parameter; 0 where it has no column.
 template <typename W, typename P>
-__device__ __forceinline__ void load_params(const void* p, float none, int width, int tid,
+__device__ __forceinline__ void load_params(const void* p, float none, const typename P::Place& at,
                                             float2 (&out)[P::kPairs]) {
 #pragma unroll
-  for (int k = 0; k < P::kPairs; ++k) {
-    const int j0 = P::column(2 * k, tid), j1 = P::column(2 * k + 1, tid);
-    out[k] = make_float2(j0 < width ? param<W>(p, j0, none) : 0.0f,
-                         j1 < width ? param<W>(p, j1, none) : 0.0f);
-  }
+  for (int k = 0; k < P::kPairs; ++k)
+    out[k] = make_float2(at.has(2 * k) ? param<W>(p, at.column(2 * k), none) : 0.0f,
+                         at.has(2 * k + 1) ? param<W>(p, at.column(2 * k + 1), none) : 0.0f);
 }
 
 __device__ __forceinline__ float plus(float x, float y) { return x + y; }
@@ -179,11 +216,14 @@ __device__ __forceinline__ float inverse_root(float x) {
 // The rows of a group, in turn, of ARRAYS matrices: bulk copies into a ring of
 // stages.  `take` leaves the current row in registers, `refill` (after every
 // thread of the group has taken its part) sends for the row that comes `stages`
-// rows later.  A row off the 16-byte grid (VEC false) lies in its stage at the
-// offset it has from the grid; its first and last elements outside whole words
-// come by plain loads, a row ahead, and the thread that has such an element puts
-// it into the stage for itself.
-template <typename P, typename T, bool VEC, int G, int ARRAYS>
+// rows later.
+// Shifted rows are copied with what else their first and last words hold, the
+// rows beside them; where that would be memory before the first row or after the
+// last one, the threads read the elements of that word for themselves.
+// Of rows that lie each in its own way whole words are copied, each row to the
+// offset it has from the grid; the elements outside whole words come by plain
+// loads, a row ahead, and the thread that has one puts it into the stage.
+template <typename P, typename T, Lie LIE, int G, int ARRAYS>
 struct Rows {
   const T* base[ARRAYS];
   int64_t stride[ARRAYS];
@@ -200,15 +240,32 @@ struct Rows {
   bool first[ARRAYS];
   int mine[ARRAYS];
   T edge[ARRAYS][2];
+  // of shifted rows: their words; the first `low` of them are copied without
+  // their first, the last `high` without their last word
+  int32_t words, low, high;
 
+  using Place = typename P::Place;
   static __host__ __device__ __forceinline__ uint32_t pitch_of(int32_t width) {
-    return VEC ? width * sizeof(T) : (width * sizeof(T) + 15) / 16 * 16 + 16;
+    return LIE == Lie::grid ? width * sizeof(T) : (width * sizeof(T) + 15) / 16 * 16 + 16;
   }
   __device__ __forceinline__ unsigned char* slot(uint32_t stage, int m) const {
     return ring + (stage * ARRAYS + m) * pitch_of(width);
   }
-  __device__ __forceinline__ const T* at(int64_t r, int m) const { return base[m] + r * stride[m]; }
+  __device__ __forceinline__ const T* start_of(int64_t r, int m) const { return base[m] + r * stride[m]; }
 
+  // Of shifted rows, those whose first (last) word reaches past a matrix.
+  __device__ __forceinline__ void find_edges(const Place& at) {
+    words = (at.shift + width + P::E - 1) / P::E;
+    low = 0;
+    high = 0;
+#pragma unroll
+    for (int m = 0; m < ARRAYS; ++m) {
+      const int over = words * P::E - at.shift - width;
+      const int s = static_cast<int>(min(stride[m], static_cast<int64_t>(P::E)));
+      low = max(low, (at.shift + s - 1) / s);
+      high = max(high, (over + s - 1) / s);
+    }
+  }
   // A row's elements before its first and from its last 16-byte boundary on.
   struct Edges {
     uint32_t off;        // bytes from the grid to the row
@@ -228,10 +285,10 @@ struct Rows {
     return e.tail + (tid - e.tail & G - 1);
   }
   __device__ __forceinline__ void fetch_edges(int tid) {
-    if (VEC || row >= rows) return;
+    if (LIE != Lie::any || row >= rows) return;
 #pragma unroll
     for (int m = 0; m < ARRAYS; ++m) {
-      const T* const p = at(row, m);
+      const T* const p = start_of(row, m);
       const Edges e = edges(p);
       const int c = tail_column(e, tid);
       off[m] = e.off;
@@ -241,79 +298,114 @@ struct Rows {
       if (c < width) edge[m][1] = p[c];
     }
   }
-  __device__ __forceinline__ void send(uint32_t stage) {
-    uint32_t bytes[ARRAYS], all = 0;
-    int from[ARRAYS];
+  __device__ __forceinline__ void send(uint32_t stage, const Place& at) {
+    // bytes [from, from + bytes) of the row's place in the stage
+    uint32_t from[ARRAYS], bytes[ARRAYS], all = 0;
+    const T* source[ARRAYS];
 #pragma unroll
     for (int m = 0; m < ARRAYS; ++m) {
-      from[m] = 0;
-      bytes[m] = width * sizeof(T);
-      if (!VEC) {
-        const Edges e = edges(at(ahead, m));
-        from[m] = e.head;
+      const T* const p = start_of(ahead, m);
+      if (LIE == Lie::grid) {
+        from[m] = 0;
+        bytes[m] = width * sizeof(T);
+        source[m] = p;
+      } else if (LIE == Lie::shifted) {
+        const int w0 = ahead < low ? 1 : 0, w1 = ahead + high < rows ? words : words - 1;
+        from[m] = 16 * w0;
+        bytes[m] = w1 > w0 ? 16 * (w1 - w0) : 0;
+        source[m] = p - at.shift + w0 * P::E;
+      } else {
+        const Edges e = edges(p);
+        from[m] = e.off + e.head * sizeof(T);
         bytes[m] = static_cast<uint32_t>(e.tail - e.head) * sizeof(T);
+        source[m] = p + e.head;
       }
       all += bytes[m];
     }
     mbar_expect_tx(&full[stage], all);
 #pragma unroll
     for (int m = 0; m < ARRAYS; ++m)
-      if (bytes[m] != 0u) {
-        const T* const p = at(ahead, m);
-        const uint32_t grid = VEC ? 0u : static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 15u);
-        bulk_g2s(slot(stage, m) + grid + from[m] * sizeof(T), p + from[m], bytes[m], &full[stage]);
-      }
+      if (bytes[m] != 0u) bulk_g2s(slot(stage, m) + from[m], source[m], bytes[m], &full[stage]);
   }
   // Called by every thread of the CTA.
-  __device__ __forceinline__ void start(int tid) {
-    if (tid == 0) {
+  __device__ __forceinline__ void start(const Place& at) {
+    if (at.tid == 0) {
       for (int i = 0; i < stages; ++i) mbar_init(&full[i], 1);
       fence_mbar_init();
     }
     __syncthreads();
+    if (LIE == Lie::shifted) find_edges(at);
     for (int i = 0; i < stages; ++i, ahead += step)
-      if (tid == 0 && ahead < rows) send(i);
-    fetch_edges(tid);
+      if (at.tid == 0 && ahead < rows) send(i, at);
+    fetch_edges(at.tid);
   }
-  __device__ __forceinline__ void take(P (&p)[ARRAYS], int tid) {
+  __device__ __forceinline__ void take(P (&p)[ARRAYS], const Place& at) {
     const uint32_t stage = n % stages;
     if (!lost) lost = !mbar_wait(&full[stage], (n / stages) & 1u);
 #pragma unroll
     for (int m = 0; m < ARRAYS; ++m) {
       unsigned char* s = slot(stage, m);
-      if (!VEC) {
+      if (LIE == Lie::any) {
         s += off[m];
-        if (first[m]) reinterpret_cast<T*>(s)[tid] = edge[m][0];
+        if (first[m]) reinterpret_cast<T*>(s)[at.tid] = edge[m][0];
         if (mine[m] < width) reinterpret_cast<T*>(s)[mine[m]] = edge[m][1];
       }
-      p[m].load(s, width, tid);
+      if (LIE == Lie::shifted) {
+        p[m].end[0] = p[m].end[1] = from_f32<T>(0.0f);
+        if (!at.idle(P::kPairs - 1)) {
+          constexpr int m0 = 2 * P::kPairs - 2, m1 = m0 + 1;
+          const bool has0 = at.has(m0), has1 = at.has(m1);
+          const int c0 = at.column(m0), c1 = at.column(m1);
+          const T* const x = reinterpret_cast<const T*>(s) + at.shift;
+          if (has0) p[m].end[0] = x[c0];
+          if (has1) p[m].end[1] = x[c1];
+          if (row < low || row + high >= rows) {
+            const T* const g = start_of(row, m);
+            if (has0) p[m].end[0] = g[c0];
+            if (has1) p[m].end[1] = g[c1];
+          }
+        }
+        if (at.shift != 0) s += 16;
+      }
+      p[m].load(s, at);
     }
     row += step;
-    fetch_edges(tid);
+    fetch_edges(at.tid);
   }
-  __device__ __forceinline__ void refill(int tid) {
+  __device__ __forceinline__ void refill(const Place& at) {
     if (G == 32) __syncwarp();
-    if (tid == 0 && ahead < rows) {
-      if (!VEC) fence_proxy_async_smem();
-      send(n % stages);
+    if (at.tid == 0 && ahead < rows) {
+      if (LIE == Lie::any) fence_proxy_async_smem();
+      send(n % stages, at);
     }
     ahead += step;
     ++n;
   }
   // After a wait that gave up, copies still on their way land before the CTA
   // may leave.
-  __device__ __forceinline__ void finish(int tid, uint32_t* fault) {
-    if (!lost || tid != 0) return;
+  __device__ __forceinline__ void finish(const Place& at, uint32_t* fault) {
+    if (!lost || at.tid != 0) return;
     atomicOr(fault, 1u);
     for (uint32_t i = n > static_cast<uint32_t>(stages) ? n - stages : 0; i < n; ++i)
       mbar_wait(&full[i % stages], (i / stages) & 1u);
   }
 };
 
-template <typename T, typename W, bool VEC, int G, int EACH>
+// A group's first row: a CTA has rows that are its own number modulo `period`.
+template <int GROUPS>
+__device__ __forceinline__ int64_t first_row(int period, int group) {
+  const int64_t b = blockIdx.x;
+  return b % period + period * (b / period * GROUPS + group);
+}
+template <typename T>
+__device__ __forceinline__ int shift_of(const T* row) {
+  return static_cast<int>((reinterpret_cast<uintptr_t>(row) & 15u) / sizeof(T));
+}
+
+template <typename T, typename W, Lie LIE, int G, int EACH>
 __global__ void __launch_bounds__(kCta<G>, forward_threads(G, EACH) / kCta<G>)
 ln_forward_kernel(const LayerNormArgs a) {
-  using P = Piece<T, VEC, G, EACH>;
+  using P = Piece<T, LIE, G, EACH>;
   constexpr int kPairs = P::kPairs;
   constexpr int kGroups = kCta<G> / G;
   extern __shared__ __align__(16) unsigned char s_ring[];
@@ -322,32 +414,35 @@ ln_forward_kernel(const LayerNormArgs a) {
   const int group = threadIdx.x / G, tid = threadIdx.x % G;
   GroupSum<float, G> group_sum{s_part};
   const int64_t step = static_cast<int64_t>(gridDim.x) * kGroups;
-  int64_t t = static_cast<int64_t>(blockIdx.x) * kGroups + group;
-  using R = Rows<P, T, VEC, G, 1>;
+  int64_t t = first_row<kGroups>(a.period, group);
+  const typename P::Place at(tid, a.width, shift_of(static_cast<const T*>(a.x) + t * a.x_stride));
+  using R = Rows<P, T, LIE, G, 1>;
   R rows{{static_cast<const T*>(a.x)}, {a.x_stride}, a.rows, step, t, t, a.width, a.stages,
          s_ring + group * a.stages * R::pitch_of(a.width), s_full[group]};
-  rows.start(tid);
+  rows.start(at);
   float2 w[kPairs], b[kPairs];
-  load_params<W, P>(a.weight, 1.0f, a.width, tid, w);
-  load_params<W, P>(a.bias, 0.0f, a.width, tid, b);
+  load_params<W, P>(a.weight, 1.0f, at, w);
+  load_params<W, P>(a.bias, 0.0f, at, b);
   const float inv_width = 1.0f / static_cast<float>(a.width);
   for (; t < a.rows; t += step) {
     P p[1];
-    rows.take(p, tid);
+    rows.take(p, at);
     float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
-    for (int k = 0; k < kPairs; ++k) sum = add2(sum, p[0].pair(k));
+    for (int k = 0; k < kPairs; ++k)
+      if (!at.idle(k)) sum = add2(sum, p[0].pair(k));
     const float mean = group_sum(sum.x + sum.y) * inv_width;
-    rows.refill(tid);
+    rows.refill(at);
     float2 sq = make_float2(0.0f, 0.0f);
 #pragma unroll
     for (int k = 0; k < kPairs; ++k) {
-      const float2 d = P::inside(add2(p[0].pair(k), both(-mean)), k, a.width, tid);
+      if (at.idle(k)) continue;
+      const float2 d = P::inside(add2(p[0].pair(k), both(-mean)), k, at);
       sq = fma2(d, d, sq);
     }
     const float var = group_sum(sq.x + sq.y) * inv_width;
     const float rstd = inverse_root(var + a.eps);
-    P::store(static_cast<T*>(a.y) + t * a.y_stride, a.width, tid, [&](int k) {
+    P::store(static_cast<T*>(a.y) + t * a.y_stride, at, [&](int k) {
       return fma2(mul2(add2(p[0].pair(k), both(-mean)), both(rstd)), w[k], b[k]);
     });
     if (tid == 0) {
@@ -355,31 +450,32 @@ ln_forward_kernel(const LayerNormArgs a) {
       a.rstd[t] = rstd;
     }
   }
-  rows.finish(tid, a.fault);
+  rows.finish(at, a.fault);
 }
 
-template <typename T, typename W, bool VEC, int G, int EACH>
+template <typename T, typename W, Lie LIE, int G, int EACH>
 __global__ void __launch_bounds__(kCta<G>, backward_threads(G, EACH) / kCta<G>)
 ln_backward_kernel(const LayerNormArgs a) {
-  using P = Piece<T, VEC, G, EACH>;
+  using P = Piece<T, LIE, G, EACH>;
   constexpr int kPairs = P::kPairs;
   constexpr int kGroups = kCta<G> / G;
   extern __shared__ __align__(16) unsigned char s_ring[];
   __shared__ __align__(16) float2 s_part[2 * G / 32];
   __shared__ uint64_t s_full[kGroups][kStages];
-  __shared__ float2 s_add[kGroups > 1 ? EACH * G : 1];
+  __shared__ float2 s_add[kGroups > 1 ? 2 * kPairs * G : 1];
   let_next_kernel_start();
   const int group = threadIdx.x / G, tid = threadIdx.x % G;
   GroupSum<float2, G> group_sum{s_part};
   const int64_t step = static_cast<int64_t>(gridDim.x) * kGroups;
-  int64_t t = static_cast<int64_t>(blockIdx.x) * kGroups + group;
-  using R = Rows<P, T, VEC, G, 2>;
+  int64_t t = first_row<kGroups>(a.period, group);
+  const typename P::Place at(tid, a.width, shift_of(static_cast<const T*>(a.x) + t * a.x_stride));
+  using R = Rows<P, T, LIE, G, 2>;
   R rows{{static_cast<const T*>(a.x), static_cast<const T*>(a.dy)}, {a.x_stride, a.dy_stride},
          a.rows, step, t, t, a.width, a.stages,
          s_ring + group * a.stages * 2 * R::pitch_of(a.width), s_full[group]};
-  rows.start(tid);
+  rows.start(at);
   float2 w[kPairs], gw[kPairs], gb[kPairs];
-  load_params<W, P>(a.weight, 1.0f, a.width, tid, w);
+  load_params<W, P>(a.weight, 1.0f, at, w);
 #pragma unroll
   for (int k = 0; k < kPairs; ++k) gw[k] = gb[k] = make_float2(0.0f, 0.0f);
   const float inv_width = 1.0f / static_cast<float>(a.width);
@@ -395,12 +491,13 @@ ln_backward_kernel(const LayerNormArgs a) {
       next_rstd = a.rstd[t + step];
     }
     P p[2];
-    rows.take(p, tid);
-    // xhat = (x - mean) rstd; past the width dy is 0, so nothing is added there
+    rows.take(p, at);
+    // xhat = (x - mean) rstd; outside the row dy is 0, so nothing is added there
     const float2 m = both(-mean), r = both(rstd);
     float2 sum1 = make_float2(0.0f, 0.0f), sum2 = make_float2(0.0f, 0.0f);
 #pragma unroll
     for (int k = 0; k < kPairs; ++k) {
+      if (at.idle(k)) continue;
       const float2 g = p[1].pair(k), h = mul2(add2(p[0].pair(k), m), r), wg = mul2(g, w[k]);
       sum1 = add2(sum1, wg);
       sum2 = fma2(wg, h, sum2);
@@ -410,15 +507,15 @@ ln_backward_kernel(const LayerNormArgs a) {
       }
     }
     const float2 s = group_sum(make_float2(sum1.x + sum1.y, sum2.x + sum2.y));
-    rows.refill(tid);
+    rows.refill(at);
     // dx = rstd w dy - rstd m1 - (rstd m2) xhat
     const float2 c1 = both(-rstd * (s.x * inv_width)), c2 = both(-rstd * (s.y * inv_width));
-    P::store(static_cast<T*>(a.dx) + t * a.dx_stride, a.width, tid, [&](int k) {
+    P::store(static_cast<T*>(a.dx) + t * a.dx_stride, at, [&](int k) {
       const float2 h = mul2(add2(p[0].pair(k), m), r);
       return fma2(mul2(p[1].pair(k), w[k]), r, fma2(h, c2, c1));
     });
   }
-  rows.finish(tid, a.fault);
+  rows.finish(at, a.fault);
   if (!sums_columns(G) || a.partial == nullptr) return;
   // the CTA's groups, in their order
   for (int g = 1; g < kGroups; ++g) {
@@ -444,14 +541,13 @@ ln_backward_kernel(const LayerNormArgs a) {
   float* const pb = pw + static_cast<int64_t>(a.parts) * a.width;
 #pragma unroll
   for (int k = 0; k < kPairs; ++k) {
-    const int j0 = P::column(2 * k, tid), j1 = P::column(2 * k + 1, tid);
-    if (j0 < a.width) {
-      pw[j0] = gw[k].x;
-      pb[j0] = gb[k].x;
+    if (at.has(2 * k)) {
+      pw[at.column(2 * k)] = gw[k].x;
+      pb[at.column(2 * k)] = gb[k].x;
     }
-    if (j1 < a.width) {
-      pw[j1] = gw[k].y;
-      pb[j1] = gb[k].y;
+    if (at.has(2 * k + 1)) {
+      pw[at.column(2 * k + 1)] = gw[k].y;
+      pb[at.column(2 * k + 1)] = gb[k].y;
     }
   }
 }
@@ -710,29 +806,35 @@ int stages_for(int64_t row_bytes, int per_sm) {
   return static_cast<int>(fit < 1 ? 1 : (fit < kStages ? fit : kStages));
 }
 
-template <typename T, typename W, bool VEC, int G, int EACH>
-int forward_group(LayerNormArgs a, int sms, cudaStream_t s) {
-  constexpr int kGroups = kCta<G> / G, kPerSm = forward_threads(G, EACH) / kCta<G>;
-  const int64_t ctas = at_most((a.rows + kGroups - 1) / kGroups, static_cast<int64_t>(kPerSm) * sms);
-  const int64_t row = Rows<Piece<T, VEC, G, EACH>, T, VEC, G, 1>::pitch_of(a.width);
-  a.stages = stages_for<G>(row, kPerSm);
-  ln_forward_kernel<T, W, VEC, G, EACH>
-      <<<static_cast<int>(ctas), kCta<G>, kGroups * a.stages * row, s>>>(a);
-  return 0;
+// CTAs of a launch: as many as there are rows for, at most what is resident; a
+// multiple of the period.
+template <int GROUPS>
+int ctas_for(const LayerNormArgs& a, int64_t resident) {
+  const int64_t need = (a.rows + GROUPS - 1) / GROUPS + a.period - 1;
+  return static_cast<int>(at_most(need, resident) / a.period * a.period);
 }
 
-template <typename T, typename W, bool VEC, int G, int EACH>
+template <typename T, typename W, Lie LIE, int G, int EACH>
+int forward_group(LayerNormArgs a, int sms, cudaStream_t s) {
+  constexpr int kGroups = kCta<G> / G, kPerSm = forward_threads(G, EACH) / kCta<G>;
+  const int ctas = ctas_for<kGroups>(a, static_cast<int64_t>(kPerSm) * sms);
+  const int64_t row = Rows<Piece<T, LIE, G, EACH>, T, LIE, G, 1>::pitch_of(a.width);
+  a.stages = stages_for<G>(row, kPerSm);
+  ln_forward_kernel<T, W, LIE, G, EACH><<<ctas, kCta<G>, kGroups * a.stages * row, s>>>(a);
+  return ctas;
+}
+
+template <typename T, typename W, Lie LIE, int G, int EACH>
 int backward_group(LayerNormArgs a, int sms, cudaStream_t s) {
   constexpr int kGroups = kCta<G> / G, kPerSm = backward_threads(G, EACH) / kCta<G>;
   static_assert(kPerSm <= kNormPartsPerSm, "partial sums of every CTA");
-  const int32_t ctas = static_cast<int32_t>(
-      at_most((a.rows + kGroups - 1) / kGroups, static_cast<int64_t>(kPerSm) * sms));
+  const int ctas = ctas_for<kGroups>(a, static_cast<int64_t>(kPerSm) * sms);
   a.parts = ctas;
   if (a.dweight == nullptr && a.dbias == nullptr) a.partial = nullptr;
   const int64_t row = 2 * static_cast<int64_t>(
-                              Rows<Piece<T, VEC, G, EACH>, T, VEC, G, 2>::pitch_of(a.width));
+                              Rows<Piece<T, LIE, G, EACH>, T, LIE, G, 2>::pitch_of(a.width));
   a.stages = stages_for<G>(row, kPerSm);
-  ln_backward_kernel<T, W, VEC, G, EACH><<<ctas, kCta<G>, kGroups * a.stages * row, s>>>(a);
+  ln_backward_kernel<T, W, LIE, G, EACH><<<ctas, kCta<G>, kGroups * a.stages * row, s>>>(a);
   return ctas;
 }
 
@@ -746,45 +848,67 @@ int backward_group(LayerNormArgs a, int sms, cudaStream_t s) {
                      : call(1024, 16))
 
 // Lets the row kernels of one width use the shared memory of their stages.
-template <typename T, typename W, bool VEC, int G, int EACH>
+template <typename T, typename W, Lie LIE, int G, int EACH>
 cudaError_t prepare_group() {
-  const cudaError_t e = cudaFuncSetAttribute(ln_forward_kernel<T, W, VEC, G, EACH>,
+  const cudaError_t e = cudaFuncSetAttribute(ln_forward_kernel<T, W, LIE, G, EACH>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemPerSm);
   if (e != cudaSuccess) return e;
-  return cudaFuncSetAttribute(ln_backward_kernel<T, W, VEC, G, EACH>,
+  return cudaFuncSetAttribute(ln_backward_kernel<T, W, LIE, G, EACH>,
                               cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemPerSm);
 }
-template <typename T, typename W>
-cudaError_t prepare_width(int32_t width) {
+template <typename T, typename W, Lie LIE>
+cudaError_t prepare_lie(int32_t width) {
   LayerNormArgs a{};
   a.width = width;
-#define ADAMW_LN_CALL(G, EACH) prepare_group<T, W, true, G, EACH>()
-  const cudaError_t e = ADAMW_LN_GROUPS(ADAMW_LN_CALL);
-#undef ADAMW_LN_CALL
-  if (e != cudaSuccess) return e;
-#define ADAMW_LN_CALL(G, EACH) prepare_group<T, W, false, G, EACH>()
+#define ADAMW_LN_CALL(G, EACH) prepare_group<T, W, LIE, G, EACH>()
   return ADAMW_LN_GROUPS(ADAMW_LN_CALL);
 #undef ADAMW_LN_CALL
 }
-
-bool on_grid(const void* p, int64_t stride_bytes) {
-  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && stride_bytes % 16 == 0;
+template <typename T, typename W>
+cudaError_t prepare_width(int32_t width) {
+  cudaError_t e = prepare_lie<T, W, Lie::grid>(width);
+  if (e == cudaSuccess) e = prepare_lie<T, W, Lie::shifted>(width);
+  if (e == cudaSuccess) e = prepare_lie<T, W, Lie::any>(width);
+  return e;
 }
 
-#define ADAMW_LN_FORWARD(G, EACH)                            \
-  (vec ? forward_group<T, W, true, G, EACH>(a, sms, s)       \
-       : forward_group<T, W, false, G, EACH>(a, sms, s))
-#define ADAMW_LN_BACKWARD(G, EACH)                           \
-  (vec ? backward_group<T, W, true, G, EACH>(a, sms, s)      \
-       : backward_group<T, W, false, G, EACH>(a, sms, s))
+// How a call's matrices lie, of `width` columns and elements of `size` bytes.
+struct Layout {
+  uintptr_t at;
+  int64_t stride;        // bytes
+  bool grid, same = true;
+  Layout(const void* p, int64_t stride_, int64_t width, int64_t size)
+      : at(reinterpret_cast<uintptr_t>(p)), stride(stride_ * size),
+        grid(at % 16 == 0 && stride % 16 == 0 && width * size % 16 == 0) {}
+  void join(const void* p, int64_t stride_, int64_t size) {
+    same = same && (reinterpret_cast<uintptr_t>(p) - at) % 16 == 0 && (stride_ * size - stride) % 16 == 0;
+  }
+  Lie lie() const { return !same ? Lie::any : (grid ? Lie::grid : Lie::shifted); }
+  int period() const {
+    int p = 1;
+    while (lie() == Lie::shifted && stride * p % 16 != 0) p *= 2;
+    return p;
+  }
+};
+
+#define ADAMW_LN_FORWARD(G, EACH)                                                     \
+  (lie == Lie::grid      ? forward_group<T, W, Lie::grid, G, EACH>(a, sms, s)         \
+   : lie == Lie::shifted ? forward_group<T, W, Lie::shifted, G, EACH>(a, sms, s)      \
+                         : forward_group<T, W, Lie::any, G, EACH>(a, sms, s))
+#define ADAMW_LN_BACKWARD(G, EACH)                                                    \
+  (lie == Lie::grid      ? backward_group<T, W, Lie::grid, G, EACH>(a, sms, s)        \
+   : lie == Lie::shifted ? backward_group<T, W, Lie::shifted, G, EACH>(a, sms, s)     \
+                         : backward_group<T, W, Lie::any, G, EACH>(a, sms, s))
 
 template <typename T, typename W>
-cudaError_t forward(const LayerNormArgs& a, int sms, cudaStream_t s) {
-  const int64_t z = sizeof(T);
-  const bool vec = on_grid(a.x, a.x_stride * z) && on_grid(a.y, a.y_stride * z) && a.width * z % 16 == 0;
+cudaError_t forward(LayerNormArgs a, int sms, cudaStream_t s) {
+  Layout lay(a.x, a.x_stride, a.width, sizeof(T));
+  lay.join(a.y, a.y_stride, sizeof(T));
+  const Lie lie = lay.lie();
+  a.period = lay.period();
   if (a.width > kMaxWidth) {
     const int ctas = static_cast<int>(at_most(a.rows, 2LL * sms));
-    if (vec) ln_forward_wide_kernel<T, W, true><<<ctas, kWideThreads, 0, s>>>(a);
+    if (lie == Lie::grid) ln_forward_wide_kernel<T, W, true><<<ctas, kWideThreads, 0, s>>>(a);
     else ln_forward_wide_kernel<T, W, false><<<ctas, kWideThreads, 0, s>>>(a);
   } else {
     ADAMW_LN_GROUPS(ADAMW_LN_FORWARD);
@@ -794,15 +918,18 @@ cudaError_t forward(const LayerNormArgs& a, int sms, cudaStream_t s) {
 
 template <typename T, typename W>
 cudaError_t backward(LayerNormArgs a, int sms, cudaStream_t s) {
-  const int64_t z = sizeof(T);
-  const bool vec = on_grid(a.x, a.x_stride * z) && on_grid(a.dy, a.dy_stride * z) &&
-                   on_grid(a.dx, a.dx_stride * z) && a.width * z % 16 == 0;
+  Layout lay(a.x, a.x_stride, a.width, sizeof(T));
+  lay.join(a.dy, a.dy_stride, sizeof(T));
+  lay.join(a.dx, a.dx_stride, sizeof(T));
+  const Lie lie = lay.lie();
+  a.period = lay.period();
   if (a.rows == 0) {
     a.parts = 0;
   } else {
     const bool own_columns = a.width > 512 * 16;
     if (own_columns && (a.dweight != nullptr || a.dbias != nullptr)) {
       // before the rows: dx may be dy.  One wave of CTAs.
+      const bool vec = lie == Lie::grid;
       const int columns = (a.width / (vec ? 16 / static_cast<int>(sizeof(T)) : 1) + kColumnThreads - 1) /
                           kColumnThreads;
       const int64_t most = static_cast<int64_t>(kNormPartsPerSm) * sms;
@@ -813,7 +940,7 @@ cudaError_t backward(LayerNormArgs a, int sms, cudaStream_t s) {
     }
     if (a.width > kMaxWidth) {
       const int ctas = static_cast<int>(at_most(a.rows, 2LL * sms));
-      if (vec) ln_backward_wide_kernel<T, W, true><<<ctas, kWideThreads, 0, s>>>(a);
+      if (lie == Lie::grid) ln_backward_wide_kernel<T, W, true><<<ctas, kWideThreads, 0, s>>>(a);
       else ln_backward_wide_kernel<T, W, false><<<ctas, kWideThreads, 0, s>>>(a);
     } else {
       const int ctas = ADAMW_LN_GROUPS(ADAMW_LN_BACKWARD);

@@ -90,7 +90,8 @@ struct LayerNormArgs {
   float eps;
   float* partial;              // plan-owned: [2][parts][width]
   int32_t parts;
-  int32_t stages;              // rows on their way per group (rows on the 16-byte grid)
+  int32_t stages;              // rows on their way per group
+  int32_t period;              // rows this far apart lie alike on the 16-byte grid
   uint32_t* fault;             // nonzero: a bounded wait gave up
 };
 cudaError_t prepare_layer_norm(int32_t width);

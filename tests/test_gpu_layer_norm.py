@@ -121,6 +121,72 @@ def test_strides_and_alignment(width, dtype, pad, shift):
     check(9, width, dtype, dtype, pad, shift)
 
 
+def compare(x, dy, y, dx):
+    """Both passes without parameters, on matrices given, with the bounds above."""
+    X, DY, dtype = wide(x), wide(dy), x.dtype
+    ln = FusedLayerNorm(x.shape[1])
+    _, mean, rstd = ln.forward(x, y=y)
+    _, dw, db = ln.backward(dy, x, None, mean, rstd, dx=dx)
+    torch.cuda.synchronize()
+    assert_guards_intact()
+    wy, wm, wr = LN.forward(X)
+    gx, gw, gb = LN.backward(DY, X, None, wide(mean), wide(rstd))
+    xhat = np.abs((X - wm[:, None]) * wr[:, None])
+    ratio = 1 + np.abs(wm * wr)[:, None]
+    g = np.abs(DY)
+    close(y, wy, xhat + ratio, dtype, 4e-6)
+    size = wide(rstd)[:, None] * (g + g.mean(1, keepdims=True)
+                                  + xhat * (g * (xhat + ratio)).mean(1, keepdims=True))
+    close(dx, gx, size * ratio, dtype, 4e-6)
+    close(dw, gw, (g * (xhat + ratio)).sum(0), dtype, 2e-5)
+    close(db, gb, g.sum(0), dtype, 2e-5)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("rows", [1, 7, 40, 700])
+@pytest.mark.parametrize("width", [3, 8, 17, 505, 509, 1021, 2045, 8190])
+@pytest.mark.parametrize("pad,shift", [(0, 1), (1, 2), (2, 7), (4, 3)])
+def test_what_lies_beside_a_row_is_not_used(rows, width, dtype, pad, shift):
+    """NaN between the rows, which share 16-byte words with it; rows of few elements in one word."""
+    rng = np.random.default_rng(rows + 31 * width + pad)
+    make = lambda a: rows_of(a, dtype, pad, shift)
+    x, dy = make(rng.normal(0.5, 1.5, (rows, width))), make(rng.normal(0, 1, (rows, width)))
+    y, dx = make(np.zeros((rows, width))), make(np.zeros((rows, width)))
+    for t in (x, dy):
+        t.as_strided((rows, pad), t.stride(), t.storage_offset() + width).fill_(float("nan"))
+    compare(x, dy, y, dx)
+    for t in (y, dx):
+        assert (t.as_strided((rows, pad), t.stride(), t.storage_offset() + width) == 7.0).all()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("width", [5, 64, 1000, 1601, 4100, 9001, 20_003])
+@pytest.mark.parametrize("rows", [1, 40, 700])
+def test_matrices_that_lie_each_in_its_own_way(rows, width, dtype):
+    rng = np.random.default_rng(rows + 31 * width)
+    x = rows_of(rng.normal(0.5, 1.5, (rows, width)), dtype, 3, 1)
+    dy = rows_of(rng.normal(0, 1, (rows, width)), dtype, 0, 2)
+    y, dx = rows_of(np.zeros((rows, width)), dtype), rows_of(np.zeros((rows, width)), dtype, 1, 5)
+    compare(x, dy, y, dx)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("width", [17, 501, 1601, 9001])
+def test_odd_rows_in_place(width, dtype):
+    """dx over dy and y over x: rows share words with rows that another CTA writes."""
+    rng = np.random.default_rng(width)
+    x = rows_of(rng.normal(0.5, 1.5, (900, width)), dtype)
+    dy = rows_of(rng.normal(0, 1, (900, width)), dtype)
+    ln = FusedLayerNorm(width)
+    y, mean, rstd = ln.forward(x)
+    dx, _, _ = ln.backward(dy, x, None, mean, rstd)
+    ln.backward(dy, x, None, mean, rstd, dx=dy)
+    ln.forward(x, y=x)
+    torch.cuda.synchronize()
+    assert_guards_intact()
+    assert torch.equal(dx, dy) and torch.equal(x, y)
+
+
 @pytest.mark.parametrize("dtype", DTYPES)
 def test_without_weight_and_bias(dtype):
     check(17, 500, dtype, dtype, none=True)
