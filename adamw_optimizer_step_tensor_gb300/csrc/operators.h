@@ -45,6 +45,7 @@ struct LossArgs {
   const float* ref_logps;      // policy: null without the KL term; preference: required
   const float* grad_scale;     // may be null
   float k, k_lo;               // log2(e) / temperature = k + k_lo, k_lo > 0
+  float k_part;                // k_lo / k
   float inv_temp;
   float clip_lo, clip_hi;      // 1 - low, 1 + high
   float kl_coef;

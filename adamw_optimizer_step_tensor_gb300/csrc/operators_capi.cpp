@@ -109,6 +109,7 @@ adamw_status loss_args(const adamw_loss_plan* plan, const adamw_logits* z, float
   a->k = static_cast<float>(k);
   if (a->k > k) a->k = std::nextafterf(a->k, 0.0f);
   a->k_lo = std::fmax(static_cast<float>(k - a->k), 1e-30f);
+  a->k_part = a->k_lo / a->k;
   a->logps = logps;
   a->row_stat = plan->d_stat;
   a->row_coef = plan->d_coef;

@@ -456,7 +456,7 @@ __device__ void finish_rows(const LossArgs& a, RingShared& sh, double (&acc)[4])
       if (lane == 0) {
         if (writes_gradient(PASS)) {
           const float coef = slope * out_scale;
-          sh.result[e] = {r.c, -coef / r.s, coef, 0.0f};
+          sh.result[e] = {r.c, grad_factor<T>(a, r, coef), coef, 0.0f};
         }
         if (rank == 0) {
           a.logps[row] = logp;
@@ -512,7 +512,7 @@ __device__ void grad_rows(const LossArgs& a, RingShared& sh, int warp, bool bulk
     } else {
       c = q.in[kInReference];
       coef = q.in[kInSlope] * out_scale;
-      f = -coef / q.in[kInSum];
+      f = grad_factor<T>(a, RowSum{c, q.in[kInSum]}, coef);
     }
     // the token's place relative to this thread's first word
     const int64_t from = share.first + tid * kPerWord<T>;

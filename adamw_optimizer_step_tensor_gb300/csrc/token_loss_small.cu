@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(kCta<G>, kThreadsPerSm<G> / kCta<G>) small_voc
     }
     if (!with_grad) continue;
     const float coef = slope * out_scale;
-    const float f = -coef / r.s;
+    const float f = grad_factor<T>(a, r, coef);
     const int at = static_cast<int>(y - share.first) - tid * kPerWord<T>;
 #pragma unroll
     for (int m = 0; m < kWordsEach; ++m)

@@ -45,7 +45,8 @@ __device__ __forceinline__ float exp2_fast(float x) {
 __device__ __forceinline__ float arg(const LossArgs& a, float z, float c) {
   return fmaf(z, a.k_lo, fmaf(z, a.k, -c));
 }
-// The same for a gradient entry: 16-bit gradients do not see k_lo.
+// The same for a gradient entry.  16-bit gradients leave out the k_lo of an entry's
+// distance to c (under 2^-17 of it); the k_lo of c itself is in grad_factor.
 template <typename T>
 __device__ __forceinline__ float grad_arg(const LossArgs& a, float z, float c) {
   return std::is_same<T, float>::value ? arg(a, z, c) : fmaf(z, a.k, -c);
@@ -95,6 +96,13 @@ __device__ __forceinline__ float logp_of(const LossArgs& a, float zy, const Log2
   return (fmaf(zy, a.k, -l.whole) + fmaf(zy, a.k_lo, -l.rest)) * kLn2;
 }
 __device__ __forceinline__ float lse_of(const Log2Sum& l) { return (l.whole + l.rest) * kLn2; }
+
+// What 2^a_j is multiplied by in the gradient's entries.
+template <typename T>
+__device__ __forceinline__ float grad_factor(const LossArgs& a, const RowSum& r, float coef) {
+  const float f = -coef / r.s;
+  return std::is_same<T, float>::value ? f : f * exp2_fast(r.c * a.k_part);
+}
 
 __device__ __forceinline__ int64_t label_of(const LossArgs& a, int64_t t) {
   return a.labels64 ? static_cast<const int64_t*>(a.labels)[t]
