@@ -67,7 +67,10 @@ __host__ __device__ constexpr int slots(int pass) {
 }
 static_assert(kWorkers % 8 == 0, "whole teams");
 
-enum RowKind { kRowLive, kRowZero, kRowStop };
+// A live row whose sum is a far row's (see token_math.cuh) becomes kRowFar for the
+// gradient warps, by the finisher, or with known sums by the scheduler; the other
+// roles need not see the difference.
+enum RowKind { kRowLive, kRowZero, kRowStop, kRowFar };
 // A row's inputs, one per scheduler lane: its elements off the 16-byte grid (the
 // first ones on lanes 0.., the last ones on lanes 8..), then
 enum Input {
@@ -243,7 +246,8 @@ __device__ void schedule(const LossArgs& a, RingShared& sh) {
         return;
       }
       if (lane < kInputs) sh.queue[q].in[lane] = in[i];
-      if (lane == 0) static_cast<DealtRow&>(sh.queue[q]) = d;
+      const bool far = PASS == kPassGrad && __any_sync(kFull, lane == kInSum && in[i] < 0.0f);
+      if (lane == 0) static_cast<DealtRow&>(sh.queue[q]) = {d.row, far ? kRowFar : d.kind, d.y};
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.queue_full[q]);
       ++sent;
@@ -363,7 +367,7 @@ __device__ void sum_rows(const LossArgs& a, RingShared& sh, int warp) {
     if (q.kind == kRowLive) {
       const RowShare<T> share(static_cast<const T*>(a.logits) + q.row * a.stride, a.vocab, rank,
                               ranks);
-      RowSum r{kLowest, 0.0f};
+      RowSum r{-kFar, 0.0f};
       for (int j = 0; j < share.pieces; ++j, ++use) {
         if (use % kTeams != team) continue;
         const uint32_t slot = use % kSlots;
@@ -409,6 +413,46 @@ __device__ void sum_rows(const LossArgs& a, RingShared& sh, int warp) {
   }
 }
 
+// Gives the other CTAs of the cluster x; lane i gets what CTA i gave (lanes past
+// the cluster keep theirs).  False if the wait gave up.
+__device__ __forceinline__ bool exchange(RingShared& sh, RowSum& x, uint32_t join, uint32_t rank,
+                                         uint32_t ranks) {
+  const uint32_t lane = threadIdx.x & 31;
+  const int b = join % kJoins;
+  if (lane < ranks) {
+    cluster_store2(cluster_map(&sh.cross[b][rank], lane), x.c, x.s);
+    cluster_arrive(cluster_map(&sh.joined[b], lane));
+  }
+  if (!mbar_wait_cluster(&sh.joined[b], (join / kJoins) & 1u)) {
+    atomicOr(&sh.gave_up, 64u);
+    return false;
+  }
+  if (lane < ranks) x = RowSum{sh.cross[b][lane].x, sh.cross[b][lane].y};
+  return true;
+}
+
+// A far row's sum (see token_math.cuh), from two more passes over the row in memory;
+// 1 if a wait gave up.  Called by the finisher; far rows are rare, and a function of
+// its own leaves the other rows' code alone.
+template <typename T>
+__device__ __noinline__ RowSum far_sums(const LossArgs& a, RingShared& sh, int64_t row, uint32_t join) {
+  const uint32_t rank = cluster_rank(), ranks = cluster_size();
+  const int lane = threadIdx.x & 31;
+  const T* const z = static_cast<const T*>(a.logits) + row * a.stride;
+  RowSum r{lanes_max(far_max<T>(z, a.vocab, rank, ranks, lane, 32)), 0.0f};
+  if (ranks > 1) {
+    if (!exchange(sh, r, join, rank, ranks)) return RowSum{0.0f, 1.0f};
+    r.c = lanes_max(lane < static_cast<int>(ranks) ? r.c : -INFINITY);
+  }
+  const float top = r.c;
+  r.s = lanes_sum(far_sum<T>(z, a.vocab, rank, ranks, lane, 32, top, a.k, a.k_lo));
+  if (ranks > 1) {
+    if (!exchange(sh, r, join + 1, rank, ranks)) return RowSum{0.0f, 1.0f};
+    r.s = lanes_sum(lane < static_cast<int>(ranks) ? r.s : 0.0f);
+  }
+  return RowSum{top, -r.s};
+}
+
 template <typename T, int PASS>
 __device__ void finish_rows(const LossArgs& a, RingShared& sh, double (&acc)[4]) {
   const uint32_t rank = cluster_rank(), ranks = cluster_size();
@@ -425,29 +469,29 @@ __device__ void finish_rows(const LossArgs& a, RingShared& sh, double (&acc)[4])
         atomicOr(&sh.gave_up, 32u);
         return;
       }
-      RowSum r{kLowest, 0.0f};
+      RowSum r{-kFar, 0.0f};
       if (lane < sum_warps(PASS)) r = RowSum{sh.part[e][lane].x, sh.part[e][lane].y};
       r.join_lanes();
       if (ranks > 1) {
-        const int b = joins % kJoins;
-        if (lane < static_cast<int>(ranks)) {
-          cluster_store2(cluster_map(&sh.cross[b][rank], lane), r.c, r.s);
-          cluster_arrive(cluster_map(&sh.joined[b], lane));
-        }
-        if (!mbar_wait_cluster(&sh.joined[b], (joins / kJoins) & 1u)) {
-          atomicOr(&sh.gave_up, 64u);
-          return;
-        }
-        ++joins;
-        r = RowSum{kLowest, 0.0f};
-        if (lane < static_cast<int>(ranks)) r = RowSum{sh.cross[b][lane].x, sh.cross[b][lane].y};
+        if (!exchange(sh, r, joins++, rank, ranks)) return;
+        if (lane >= static_cast<int>(ranks)) r = RowSum{-kFar, 0.0f};
         r.join_lanes();
       }
-      const Log2Sum l = log2_sum(r);
-      const float logp = logp_of(a, q.in[kInToken], l);
+      RowLog l;
+      if (r.ordinary()) {                  // the same in every CTA of the cluster
+        l = row_log(a, r, q.in[kInToken]);
+      } else {
+        if (!r.undefined()) {
+          r = far_sums<T>(a, sh, row, joins);
+          if (ranks > 1) joins += 2;
+          if (r.s > 0.0f) return;          // a wait gave up
+        }
+        if (r.far() && lane == 0) sh.queue[e].kind = kRowFar;
+        l = far_row_log(a, r, q.in[kInToken]);
+      }
       float slope = 0.0f;
       if (policy_pass(PASS)) {
-        const PolicyTerm p = policy_term(a, {q.in[kInWeight], q.in[kInAdvantage], q.in[kInOld], q.in[kInRef]}, logp);
+        const PolicyTerm p = policy_term(a, {q.in[kInWeight], q.in[kInAdvantage], q.in[kInOld], q.in[kInRef]}, l.logp);
         slope = p.slope;
         acc[1] += p.policy;
         acc[2] += p.kl;
@@ -455,22 +499,76 @@ __device__ void finish_rows(const LossArgs& a, RingShared& sh, double (&acc)[4])
       }
       if (lane == 0) {
         if (writes_gradient(PASS)) {
+          // first of all: the gradient warps wait for it
           const float coef = slope * out_scale;
           sh.result[e] = {r.c, grad_factor<T>(a, r, coef), coef, 0.0f};
+          mbar_arrive(&sh.ready[e]);
         }
         if (rank == 0) {
-          a.logps[row] = logp;
-          if (a.lse != nullptr) a.lse[row] = lse_of(l);
+          a.logps[row] = l.logp;
+          if (a.lse != nullptr) a.lse[row] = l.lse;
           if ((PASS == kPassPrefer || PASS == kPassPolicy) && a.row_stat != nullptr) {
             a.row_stat[row] = make_float2(r.c, r.s);
             if (PASS == kPassPolicy) a.row_coef[row] = slope;
           }
         }
       }
+    } else if (writes_gradient(PASS) && lane == 0) {
+      mbar_arrive(&sh.ready[e]);                         // keeps the phases in step
     }
-    if (writes_gradient(PASS) && lane == 0) mbar_arrive(&sh.ready[e]);
     leave_row(sh, n);
   }
+}
+
+// A far row's gradient, by the warp `warp` of the gradient warps; false if a wait
+// gave up.
+template <typename T, int PASS>
+__device__ __forceinline__ bool far_pieces(const LossArgs& a, RingShared& sh, uint32_t n, int warp,
+                                           uint32_t& use, bool bulk_out) {
+  constexpr int kTeam = team_warps(PASS), kTeams = grad_warps(PASS) / kTeam;
+  constexpr int kThreadsHere = kTeam * 32, kSlots = slots(PASS);
+  const QueueRow& q = sh.queue[n % kQueue];
+  const uint32_t team = warp / kTeam;
+  const int lane = threadIdx.x & 31, tid = (warp % kTeam) * 32 + lane;
+  const float out_scale = a.inv_temp * (a.grad_scale != nullptr ? *a.grad_scale : 1.0f);
+  const float c = sums(PASS) ? sh.result[n % kQueue].c : q.in[kInReference];
+  const float coef = sums(PASS) ? sh.result[n % kQueue].coef : q.in[kInSlope] * out_scale;
+  const float f = sums(PASS) ? sh.result[n % kQueue].f : coef / q.in[kInSum];
+  T* const dz = static_cast<T*>(a.dlogits) + q.row * a.dstride;
+  const RowShare<T> share(static_cast<const T*>(a.logits) + q.row * a.stride, a.vocab, cluster_rank(),
+                          cluster_size());
+#pragma unroll 1
+  for (int j = 0; j < share.pieces; ++j, ++use) {
+    if (use % kTeams != team) continue;
+    const uint32_t slot = use % kSlots;
+    if (!sums(PASS) && !mbar_wait(&sh.full[slot], (use / kSlots) & 1u)) {
+      atomicOr(&sh.gave_up, 8u);
+      return false;
+    }
+    uint4* const w = reinterpret_cast<uint4*>(sh.slot[slot]);
+    const int64_t from = share.first + static_cast<int64_t>(j) * kSlotWords * kPerWord<T>;
+    const int words = share.piece_words(j);
+#pragma unroll 1
+    for (int i = tid; i < words; i += kThreadsHere) {
+      const int64_t first = from + i * kPerWord<T>;
+      const uint4 d = far_grad_word<T>(a, w[i], c, f, coef, static_cast<int>(q.y - first));
+      if (bulk_out) {
+        w[i] = d;
+      } else {
+        const T* const el = reinterpret_cast<const T*>(&d);
+        for (int m = 0; m < kPerWord<T>; ++m) dz[first + m] = el[m];
+      }
+    }
+    if (bulk_out) fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh.done[slot]);
+  }
+  const int el = cluster_rank() == 0 && warp == 0 ? ragged_element(share, a.vocab, lane) : -1;
+  if (el >= 0) {
+    const float d = f * far_power(half_below(q.in[lane], c), a.k, a.k_lo);
+    dz[el] = from_f32<T>(el == q.y ? d + coef : d);
+  }
+  return true;
 }
 
 template <typename T, int PASS>
@@ -492,13 +590,17 @@ __device__ void grad_rows(const LossArgs& a, RingShared& sh, int warp, bool bulk
       atomicOr(&sh.gave_up, 256u);
       return;
     }
-    if (q.kind == kRowZero) {
-      const RowShare<T> share(dz, a.vocab, rank, ranks);
-      uint4* const out = reinterpret_cast<uint4*>(const_cast<unsigned char*>(share.base));
-      for (int i = warp * 32 + lane; i < share.words; i += kAllThreads)
-        out[i] = make_uint4(0, 0, 0, 0);
-      const int el = rank == 0 && warp == 0 ? ragged_element(share, a.vocab, lane) : -1;
-      if (el >= 0) dz[el] = from_f32<T>(0.0f);
+    if (q.kind != kRowLive) {
+      if (q.kind == kRowZero) {
+        const RowShare<T> share(dz, a.vocab, rank, ranks);
+        uint4* const out = reinterpret_cast<uint4*>(const_cast<unsigned char*>(share.base));
+        for (int i = warp * 32 + lane; i < share.words; i += kAllThreads)
+          out[i] = make_uint4(0, 0, 0, 0);
+        const int el = rank == 0 && warp == 0 ? ragged_element(share, a.vocab, lane) : -1;
+        if (el >= 0) dz[el] = from_f32<T>(0.0f);
+      } else {
+        if (!far_pieces<T, PASS>(a, sh, n, warp, use, bulk_out)) return;
+      }
       leave_row(sh, n);
       continue;
     }
@@ -559,7 +661,7 @@ __device__ void grad_rows(const LossArgs& a, RingShared& sh, int warp, bool bulk
 }
 
 template <typename T, int PASS>
-__global__ void __launch_bounds__(kRingThreads, 1) ring_kernel(const LossArgs a, const int bulk_out) {
+__global__ void __launch_bounds__(kRingThreads, 1) ring_kernel(const __grid_constant__ LossArgs a, const int bulk_out) {
   extern __shared__ __align__(128) unsigned char raw[];
   RingShared& sh = *reinterpret_cast<RingShared*>(raw);
   const uint32_t ranks = cluster_size();

@@ -28,8 +28,115 @@ __device__ __forceinline__ void group_sync(int group) {
   else asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(G) : "memory");
 }
 
+// The rows' order.  Gradients of known rows run from the last row to the first: the
+// pass before ended there, so the end of the logits is still in L2.
+__device__ __forceinline__ int64_t row_of(const LossArgs& a, Pass pass, int64_t i) {
+  return pass == kPassGrad ? a.rows - 1 - i : i;
+}
+
+// This thread's entries of the gradient; each word is read by the thread that
+// writes it, as the gradient may take the logits' place.
+template <typename T>
+__device__ __forceinline__ void far_gradient(const LossArgs& a, int64_t t, int64_t y, const RowSum& r,
+                                             float coef, int tid, int threads) {
+  const T* const z = static_cast<const T*>(a.logits) + t * a.stride;
+  T* const dz = static_cast<T*>(a.dlogits) + t * a.dstride;
+  const RowShare<T> share(z, a.vocab, 0, 1);
+  const bool same_grid =
+      (reinterpret_cast<uintptr_t>(dz) - reinterpret_cast<uintptr_t>(z)) % 16 == 0;
+  const float f = coef / r.s;
+  for (int m = tid; m < share.words; m += threads) {
+    const int64_t first = share.first + static_cast<int64_t>(m) * kPerWord<T>;
+    const uint4 w = reinterpret_cast<const uint4*>(share.base)[m];
+    const uint4 d = far_grad_word<T>(a, w, r.c, f, coef, static_cast<int>(y - first));
+    if (same_grid) {
+      *reinterpret_cast<uint4*>(dz + first) = d;
+    } else {
+      const T* const el = reinterpret_cast<const T*>(&d);
+      for (int x = 0; x < kPerWord<T>; ++x) dz[first + x] = el[x];
+    }
+  }
+  const int e = tid < 16 ? ragged_element(share, a.vocab, tid) : -1;
+  if (e >= 0) {
+    const float d = f * far_power(half_below(to_f32(z[e]), r.c), a.k, a.k_lo);
+    dz[e] = from_f32<T>(e == y ? d + coef : d);
+  }
+}
+// What far rows add to the policy loss.
+struct PolicySums {
+  double policy, kl, clipped;
+};
+
+// The far rows of a group (see token_math.cuh), after its others: they are rare,
+// and with their code among the rows' the kernel spilled (8000 bf16 rows of 20,001
+// took 162 us instead of 146).  Where sums were taken a far row's log-probability
+// is kFarMark until now; they are read again from memory, each word by the thread
+// that writes its gradient, which may take the logits' place.
+constexpr uint32_t kFarMark = 0x7FA5F0F0u;     // a NaN that no instruction gives
 template <typename T, int G>
-__global__ void __launch_bounds__(kCta<G>, kThreadsPerSm<G> / kCta<G>) small_vocab_kernel(const LossArgs a, const Pass pass,
+__device__ __noinline__ PolicySums far_rows(const LossArgs& a, Pass pass, float2* s_part) {
+  constexpr int kGroups = kCta<G> / G;
+  const int group = threadIdx.x / G, tid = threadIdx.x % G;
+  const int lane = tid & 31, warp = tid >> 5;
+  float2* const part = s_part + group * (G / 32);
+  const float out_scale = a.inv_temp * (a.grad_scale != nullptr ? *a.grad_scale : 1.0f);
+  PolicySums acc{0.0, 0.0, 0.0};
+  group_sync<G>(group);                        // the marks are there
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kGroups + group; i < a.rows;
+       i += static_cast<int64_t>(gridDim.x) * kGroups) {
+    const int64_t t = row_of(a, pass, i);
+    const int64_t y = label_of(a, t);
+    if (y < 0 || y >= a.vocab) continue;
+    const T* const z = static_cast<const T*>(a.logits) + t * a.stride;
+    RowSum r;
+    float slope = 0.0f;
+    if (sums(pass)) {
+      const bool marked = __float_as_uint(a.logps[t]) == kFarMark;
+      group_sync<G>(group);                    // every thread has read the mark
+      if (!marked) continue;
+      r.c = lanes_max(far_max<T>(z, a.vocab, 0, 1, tid, G));
+      if (G > 32) {
+        if (lane == 0) part[warp].x = r.c;
+        group_sync<G>(group);
+        r.c = lanes_max(lane < G / 32 ? part[lane].x : -INFINITY);
+      }
+      r.s = lanes_sum(far_sum<T>(z, a.vocab, 0, 1, tid, G, r.c, a.k, a.k_lo));
+      if (G > 32) {
+        if (lane == 0) part[warp].y = r.s;
+        group_sync<G>(group);
+        r.s = lanes_sum(lane < G / 32 ? part[lane].y : 0.0f);
+      }
+      r.s = -r.s;
+      const RowLog l = far_row_log(a, r, to_f32(z[y]));
+      if (policy_pass(pass)) {
+        const PolicyRow in{a.weights != nullptr ? a.weights[t] : 1.0f, a.advantages[t],
+                           a.old_logps != nullptr ? a.old_logps[t] : 0.0f,
+                           a.ref_logps != nullptr ? a.ref_logps[t] : 0.0f};
+        const PolicyTerm p = policy_term(a, in, l.logp);
+        slope = p.slope;
+        acc.policy += p.policy;
+        acc.kl += p.kl;
+        acc.clipped += p.clipped;
+      }
+      group_sync<G>(group);                    // zy has been read
+      if (tid == 0) {
+        a.logps[t] = l.logp;
+        if (a.lse != nullptr) a.lse[t] = l.lse;
+        if (pass == kPassPrefer) a.row_stat[t] = make_float2(r.c, r.s);
+      }
+    } else {
+      slope = a.row_coef[t];
+      r = RowSum{a.row_stat[t].x, a.row_stat[t].y};
+      if (slope == 0.0f || !r.far()) continue;
+    }
+    if (!writes_gradient(pass)) continue;
+    far_gradient<T>(a, t, y, r, slope * out_scale, tid, G);
+  }
+  return acc;
+}
+
+template <typename T, int G>
+__global__ void __launch_bounds__(kCta<G>, kThreadsPerSm<G> / kCta<G>) small_vocab_kernel(const __grid_constant__ LossArgs a, const Pass pass,
                                                               const bool same_grid) {
   constexpr int kGroups = kCta<G> / G;
   let_next_kernel_start();
@@ -43,21 +150,19 @@ __global__ void __launch_bounds__(kCta<G>, kThreadsPerSm<G> / kCta<G>) small_voc
   double acc[4] = {0.0, 0.0, 0.0, 0.0};
   const int64_t step = static_cast<int64_t>(gridDim.x) * kGroups;
   int turn = 0;
+  bool any_far = false;
   int64_t i = static_cast<int64_t>(blockIdx.x) * kGroups + group;
-  // gradients of known rows run from the last row to the first: the pass
-  // before ended there, so the end of the logits is still in L2
-  auto row_of = [&](int64_t at) { return pass == kPassGrad ? a.rows - 1 - at : at; };
   int64_t next_y = -1;
   float next_w = 0.0f;
   auto look = [&](int64_t at) {
     if (at < a.rows) {
-      next_y = label_of(a, row_of(at));
-      next_w = weights != nullptr ? weights[row_of(at)] : 1.0f;
+      next_y = label_of(a, row_of(a, pass, at));
+      next_w = weights != nullptr ? weights[row_of(a, pass, at)] : 1.0f;
     }
   };
   look(i);
   for (; i < a.rows; i += step) {
-    const int64_t t = row_of(i);
+    const int64_t t = row_of(a, pass, i);
     const int64_t y = next_y;
     const float w = next_w;
     look(i + step);
@@ -87,7 +192,7 @@ __global__ void __launch_bounds__(kCta<G>, kThreadsPerSm<G> / kCta<G>) small_voc
       v[m] = tid + m * G < share.words ? __ldcs(q + tid + m * G) : lowest_word<T>();
     const int e = tid < 16 ? ragged_element(share, a.vocab, tid) : -1;
     const float edge = e >= 0 ? to_f32(z[e]) : 0.0f;
-    RowSum r{kLowest, 0.0f};
+    RowSum r{-kFar, 0.0f};
     float slope;
     if (with_sums) {
       const float zy = to_f32(z[y]);
@@ -115,15 +220,19 @@ __global__ void __launch_bounds__(kCta<G>, kThreadsPerSm<G> / kCta<G>) small_voc
         turn ^= 1;
         if (lane == 0) part[warp] = make_float2(r.c, r.s);
         group_sync<G>(group);
-        r = RowSum{kLowest, 0.0f};
+        r = RowSum{-kFar, 0.0f};
         if (lane < G / 32) r = RowSum{part[lane].x, part[lane].y};
         r.join_lanes();
       }
-      const Log2Sum l = log2_sum(r);
-      const float logp = logp_of(a, zy, l);
+      if (!r.ordinary()) {                 // the same in every thread of the group
+        if (tid == 0) a.logps[t] = __uint_as_float(kFarMark);
+        any_far = true;
+        continue;
+      }
+      const RowLog l = row_log(a, r, zy);
       slope = 0.0f;
       if (policy_pass(pass)) {
-        const PolicyTerm p = policy_term(a, in, logp);
+        const PolicyTerm p = policy_term(a, in, l.logp);
         slope = p.slope;
         if (tid == 0) {
           acc[1] += p.policy;
@@ -132,8 +241,8 @@ __global__ void __launch_bounds__(kCta<G>, kThreadsPerSm<G> / kCta<G>) small_voc
         }
       }
       if (tid == 0) {
-        a.logps[t] = logp;
-        if (a.lse != nullptr) a.lse[t] = lse_of(l);
+        a.logps[t] = l.logp;
+        if (a.lse != nullptr) a.lse[t] = l.lse;
         if (pass == kPassPrefer) a.row_stat[t] = make_float2(r.c, r.s);
       }
     } else {
@@ -144,6 +253,10 @@ __global__ void __launch_bounds__(kCta<G>, kThreadsPerSm<G> / kCta<G>) small_voc
     }
     if (!with_grad) continue;
     const float coef = slope * out_scale;
+    if (r.far()) {
+      any_far = true;
+      continue;
+    }
     const float f = grad_factor<T>(a, r, coef);
     const int at = static_cast<int>(y - share.first) - tid * kPerWord<T>;
 #pragma unroll
@@ -164,6 +277,12 @@ __global__ void __launch_bounds__(kCta<G>, kThreadsPerSm<G> / kCta<G>) small_voc
       if (e == y) d += coef;
       dz[e] = from_f32<T>(d);
     }
+  }
+  if (any_far) {
+    const PolicySums far = far_rows<T, G>(a, pass, s_part[0]);
+    acc[1] += far.policy;
+    acc[2] += far.kl;
+    acc[3] += far.clipped;
   }
   if (!policy_pass(pass)) return;
   // the groups' sums in their order, then the CTAs'

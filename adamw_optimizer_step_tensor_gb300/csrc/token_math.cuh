@@ -14,6 +14,11 @@
 // log2 S takes back the mean error of the hardware's 2^x; and exponentials are
 // summed in runs of 8 or 16 before they join a long sum, which would round the
 // small ones away.
+// That needs z k with its fraction, and no infinity: it holds for |z k| up to
+// 2^23.  A running reference starts at -2^23, so a thread that has seen masked
+// entries alone (-1e10, the type's lowest value) leaves a sum of 0 there.  A row
+// whose largest z k lies beyond either end is summed anew around its largest
+// logit m instead, with a_j = (z_j - m) k, which no size of the logits spoils.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -29,7 +34,8 @@ namespace adamw {
 namespace {
 
 constexpr float kLn2 = 0.69314718055994530942f;
-constexpr float kLowest = -3.40282347e38f;
+constexpr float kFar = 8388608.0f;             // 2^23
+constexpr float kFaint = 8.67361738e-19f;      // 2^-60
 
 // ex2.approx is exact at integers and elsewhere low by 4.9e-8 on average,
 // whatever the fraction (measured on GB300 over 4 M arguments in [-17, 0); the
@@ -52,9 +58,18 @@ __device__ __forceinline__ float grad_arg(const LossArgs& a, float z, float c) {
   return std::is_same<T, float>::value ? arg(a, z, c) : fmaf(z, a.k, -c);
 }
 
-// Integer reference c and S = sum 2^(z k - c).
+// Integer reference c and S = sum 2^(z k - c); of a far row c is its largest logit
+// and s = -sum 2^((z - c) k), NaN with a NaN or +inf logit, -0 with nothing but -inf.
 struct RowSum {
   float c, s;
+  // Whether c and s are good as they are: not where the reference left the range in
+  // which z k - c is, or nothing of weight came above -kFar (terms lost to underflow
+  // weigh under 2^-36 of a sum that is not faint), or where s is NaN.
+  __device__ __forceinline__ bool ordinary() const {
+    return s >= kFaint && s <= 3.40282347e38f && c <= kFar;
+  }
+  __device__ __forceinline__ bool undefined() const { return isnan(s) && c <= kFar; }
+  __device__ __forceinline__ bool far() const { return s < 0.0f; }
   __device__ __forceinline__ void raise(float zk) {
     if (zk > c) {
       const float hi = ceilf(zk);
@@ -80,13 +95,12 @@ struct RowSum {
   }
 };
 
-// c + log2 S as an integer plus a small rest, so that a difference to z_y k
-// rounds relative to the difference.
+// c + log2 S of an ordinary sum as an integer plus a small rest, so that a
+// difference to z_y k rounds relative to the difference.
 struct Log2Sum {
   float whole, rest;
 };
 __device__ __forceinline__ Log2Sum log2_sum(const RowSum& r) {
-  if (!(r.s >= 1.17549435e-38f && r.s <= 3.40282347e38f)) return {r.c, log2f(r.s)};
   const uint32_t b = __float_as_uint(r.s);
   const float f = __uint_as_float((b & 0x007FFFFFu) | 0x3F800000u);     // [1, 2)
   const float e = static_cast<float>(static_cast<int>(b >> 23) - 127);
@@ -100,8 +114,33 @@ __device__ __forceinline__ float lse_of(const Log2Sum& l) { return (l.whole + l.
 // What 2^a_j is multiplied by in the gradient's entries.
 template <typename T>
 __device__ __forceinline__ float grad_factor(const LossArgs& a, const RowSum& r, float coef) {
-  const float f = -coef / r.s;
-  return std::is_same<T, float>::value ? f : f * exp2_fast(r.c * a.k_part);
+  const float f = -coef / fabsf(r.s);
+  return std::is_same<T, float>::value || r.far() ? f : f * exp2_fast(r.c * a.k_part);
+}
+
+// (z - m) / 2 for the largest logit m of a far row: half of it, as the difference
+// itself may pass float32.
+__device__ __forceinline__ float half_below(float z, float m) { return fmaf(z, 0.5f, -0.5f * m); }
+// 2^((z - m) k) of it.
+__device__ __forceinline__ float far_power(float half, float k, float k_lo) {
+  return exp2_fast(fmaf(half, 2.0f * k_lo, half * (2.0f * k)));
+}
+
+// A row's log-probability of a token with logit zy, and log sum exp.
+struct RowLog {
+  float logp, lse;
+};
+__device__ __forceinline__ RowLog row_log(const LossArgs& a, const RowSum& r, float zy) {
+  const Log2Sum l = log2_sum(r);
+  const float lse = lse_of(l);
+  // a token far below its row has a log-probability that is its logit but for rounding
+  return {fabsf(zy * a.k) < kFar ? logp_of(a, zy, l) : fmaf(zy, a.inv_temp, -lse), lse};
+}
+// The same of a far row, and of one with a NaN or without a finite logit.
+__device__ __forceinline__ RowLog far_row_log(const LossArgs& a, const RowSum& r, float zy) {
+  if (!r.far()) return {NAN, r.c == -INFINITY && r.s == 0.0f ? -INFINITY : NAN};
+  const float log_s = lse_of(log2_sum(RowSum{0.0f, -r.s}));
+  return {fmaf(half_below(zy, r.c), 2.0f * a.inv_temp, -log_s), fmaf(r.c, a.inv_temp, log_s)};
 }
 
 __device__ __forceinline__ int64_t label_of(const LossArgs& a, int64_t t) {
@@ -185,7 +224,7 @@ __device__ __forceinline__ uint4 lowest_word() {
 template <typename T, int N>
 __device__ __forceinline__ float words_max(const uint4 (&w)[N]) {
   if constexpr (sizeof(T) == 4) {
-    float m = kLowest;
+    float m = -INFINITY;
 #pragma unroll
     for (int i = 0; i < N; ++i)
       m = fmaxf(m, fmaxf(fmaxf(__uint_as_float(w[i].x), __uint_as_float(w[i].y)),
@@ -238,6 +277,20 @@ __device__ __forceinline__ uint4 grad_word(const LossArgs& a, const uint4& w, fl
       if (2 * j == at) x[j].x += coef;
       if (2 * j + 1 == at) x[j].y += coef;
     }
+  }
+  return pack<T>(x);
+}
+
+// The same of a far row: f 2^((z - c) k).
+template <typename T>
+__device__ __forceinline__ uint4 far_grad_word(const LossArgs& a, const uint4& w, float c, float f,
+                                               float coef, int at) {
+  float2 x[kPerWord<T> / 2];
+  unpack<T>(w, x);
+#pragma unroll
+  for (int j = 0; j < kPerWord<T> / 2; ++j) {
+    x[j].x = f * far_power(half_below(x[j].x, c), a.k, a.k_lo) + (2 * j == at ? coef : 0.0f);
+    x[j].y = f * far_power(half_below(x[j].y, c), a.k, a.k_lo) + (2 * j + 1 == at ? coef : 0.0f);
   }
   return pack<T>(x);
 }

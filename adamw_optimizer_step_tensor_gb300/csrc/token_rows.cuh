@@ -80,5 +80,57 @@ __device__ __forceinline__ int ragged_element(const RowShare<T>& share, int voca
   return lane < 16 && lane - 8 < share.tail ? vocab - share.tail + lane - 8 : -1;
 }
 
+// ---- far rows (see token_math.cuh)
+
+// A word's sum of 2^((z - m) k).
+template <typename T>
+__device__ __forceinline__ float far_word(const uint4& w, float m, float k, float k_lo) {
+  float2 x[kPerWord<T> / 2];
+  unpack<T>(w, x);
+  float t = 0.0f;
+#pragma unroll
+  for (int j = 0; j < kPerWord<T> / 2; ++j)
+    t += far_power(half_below(x[j].x, m), k, k_lo) + far_power(half_below(x[j].y, m), k, k_lo);
+  return t;
+}
+// Of the logits that thread `tid` of `threads` looks after, the largest (NaN
+// ignored), and the sum of 2^((z - m) k).
+template <typename T>
+__device__ __forceinline__ float far_max(const T* z, int vocab, uint32_t rank, uint32_t ranks, int tid,
+                                         int threads) {
+  const RowShare<T> share(z, vocab, rank, ranks);
+  const uint4* const w = reinterpret_cast<const uint4*>(share.base);
+  float m = -INFINITY;
+#pragma unroll 1
+  for (int i = tid; i < share.words; i += threads) {
+    const uint4 v[1] = {w[i]};
+    m = fmaxf(m, words_max<T, 1>(v));
+  }
+  const int e = rank == 0 && tid < 16 ? ragged_element(share, vocab, tid) : -1;
+  return e >= 0 ? fmaxf(m, to_f32(z[e])) : m;
+}
+template <typename T>
+__device__ __forceinline__ float far_sum(const T* z, int vocab, uint32_t rank, uint32_t ranks, int tid,
+                                         int threads, float m, float k, float k_lo) {
+  const RowShare<T> share(z, vocab, rank, ranks);
+  const uint4* const w = reinterpret_cast<const uint4*>(share.base);
+  m = fmaxf(m, -3.40282347e38f);        // -inf logits alone add nothing
+  float s = 0.0f;
+#pragma unroll 1
+  for (int i = tid; i < share.words; i += threads) s += far_word<T>(w[i], m, k, k_lo);
+  const int e = rank == 0 && tid < 16 ? ragged_element(share, vocab, tid) : -1;
+  return e >= 0 ? s + far_power(half_below(to_f32(z[e]), m), k, k_lo) : s;
+}
+__device__ __forceinline__ float lanes_max(float x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(kFull, x, o));
+  return x;
+}
+__device__ __forceinline__ float lanes_sum(float x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(kFull, x, o);
+  return x;
+}
+
 }  // namespace
 }  // namespace adamw

@@ -10,12 +10,14 @@ import numpy as np
 
 
 def log_softmax(logits, temperature=1.0):
-    """(log softmax, log sum exp) per row; -inf logits have probability 0."""
-    z = np.asarray(logits, np.float64) / temperature
+    """(log softmax, log sum exp) per row; -inf logits have probability 0.  The log
+    softmax is a sum of differences, which rows far from zero do not round away."""
+    z = np.asarray(logits, np.float64)
     with np.errstate(invalid="ignore", divide="ignore", over="ignore"):
         top = z.max(1, keepdims=True)
-        lse = top + np.log(np.exp(z - top).sum(1, keepdims=True))
-        return z - lse, lse[:, 0]
+        below = (z - top) / temperature
+        log_sum = np.log(np.exp(below).sum(1, keepdims=True))
+        return below - log_sum, (top / temperature + log_sum)[:, 0]
 
 
 def live_rows(labels, vocab, weights=None):
