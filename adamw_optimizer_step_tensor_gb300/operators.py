@@ -5,7 +5,9 @@ preference loss with the gradient of the logits.  ``FusedLayerNorm`` is layer
 norm forward and backward with the gradients of its weight and bias.  Both hold
 a plan of the library (its workspace) on the current device, check their
 arguments and launch on the current stream or ``stream``; all arithmetic runs in
-the library's CUDA kernels.
+the library's CUDA kernels.  Outputs that are not given are allocated for the stream
+of the launch.  Inputs stay the caller's: one that was made on another stream has to
+be ready on this one, and to be kept until the work is done.
 """
 
 from __future__ import annotations
@@ -51,6 +53,14 @@ def _vector(name, t, n, dtype=_F32):
 
 def _empty(n, like, dtype=_F32):
     return torch.empty(n, dtype=dtype, device=like.device)
+
+
+def _on(stream):
+    """A context with ``stream`` (a stream or its handle) as the current one."""
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = int(getattr(stream, "cuda_stream", stream))    # 0 and 1: the default one
+        stream = torch.cuda.ExternalStream(handle) if handle > 1 else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
 
 
 class _Plan:
@@ -116,6 +126,9 @@ class FusedTokenLoss(_Plan):
     def logps(self, logits, labels, *, temperature=1.0, logps=None, lse=None, stream=None):
         """(logps, lse) of every row: the log-probability of its token and the log of its sum of
         exponentials, 0 where the row has no token."""
+        if stream is not None:
+            with _on(stream):
+                return self.logps(logits, labels, temperature=temperature, logps=logps, lse=lse)
         z = self._logits(logits, labels, temperature)
         n = logits.shape[0]
         if logps is None:
@@ -123,7 +136,7 @@ class FusedTokenLoss(_Plan):
         if lse is None:
             lse = _empty(n, logits)
         _capi.adamw_token_logps(self.plan, z, _vector("logps", logps, n), _vector("lse", lse, n),
-                                _stream(stream))
+                                _stream(None))
         return logps, lse
 
     def policy(self, logits, labels, weights, advantages, old_logps=None, ref_logps=None, *,
@@ -136,6 +149,11 @@ class FusedTokenLoss(_Plan):
         the mean runs over.  dlogits (None when ``backward`` is false) is the gradient of
         stats[0], times ``grad_scale``; it may be given, also as the logits themselves.
         """
+        if stream is not None:
+            with _on(stream):
+                return self.policy(logits, labels, weights, advantages, old_logps, ref_logps, clip=clip,
+                                   kl_coef=kl_coef, temperature=temperature, grad_scale=grad_scale,
+                                   backward=backward, stats=stats, logps=logps, dlogits=dlogits)
         z = self._logits(logits, labels, temperature)
         n = logits.shape[0]
         p = self._policy
@@ -152,7 +170,7 @@ class FusedTokenLoss(_Plan):
             logps = _empty(n, logits)
         dlogits, at, stride = self._gradient(logits, dlogits, backward)
         _capi.adamw_policy_loss(self.plan, z, p, _vector("stats", stats, 4), _vector("logps", logps, n),
-                                at, stride, _stream(stream))
+                                at, stride, _stream(None))
         return stats, logps, dlogits
 
     def preference(self, logits, labels, weights, ref_logps, seq_starts, *, beta=0.1,
@@ -166,6 +184,12 @@ class FusedTokenLoss(_Plan):
         the share of pairs with the chosen one ahead, mean chosen and mean rejected reward;
         rewards float32 [2 pairs].
         """
+        if stream is not None:
+            with _on(stream):
+                return self.preference(logits, labels, weights, ref_logps, seq_starts, beta=beta,
+                                       label_smoothing=label_smoothing, temperature=temperature,
+                                       grad_scale=grad_scale, backward=backward, stats=stats, rewards=rewards,
+                                       logps=logps, dlogits=dlogits)
         z = self._logits(logits, labels, temperature)
         n = logits.shape[0]
         pairs = (seq_starts.numel() - 1) // 2
@@ -186,7 +210,7 @@ class FusedTokenLoss(_Plan):
         dlogits, at, stride = self._gradient(logits, dlogits, backward)
         _capi.adamw_preference_loss(self.plan, z, p, _vector("stats", stats, 4),
                                     _vector("rewards", rewards, 2 * pairs), _vector("logps", logps, n),
-                                    at, stride, _stream(stream))
+                                    at, stride, _stream(None))
         return stats, rewards, logps, dlogits
 
 
@@ -219,6 +243,9 @@ class FusedLayerNorm(_Plan):
 
     def forward(self, x, weight=None, bias=None, *, y=None, mean=None, rstd=None, stream=None):
         """(y, mean, rstd)"""
+        if stream is not None:
+            with _on(stream):
+                return self.forward(x, weight, bias, y=y, mean=mean, rstd=rstd)
         stride, wdt = self._check(x, weight if weight is not None else bias)
         n = x.shape[0]
         if y is None:
@@ -231,12 +258,15 @@ class FusedLayerNorm(_Plan):
             self.plan, _DTYPES[x.dtype], _DTYPES[wdt], n, x.data_ptr(), stride,
             _vector("weight", weight, self.width, wdt), _vector("bias", bias, self.width, wdt),
             y.data_ptr(), _rows("y", y, x.dtype, x.shape), _vector("mean", mean, n),
-            _vector("rstd", rstd, n), _stream(stream))
+            _vector("rstd", rstd, n), _stream(None))
         return y, mean, rstd
 
     def backward(self, dy, x, weight, mean, rstd, *, dx=None, dweight=None, dbias=None, stream=None):
         """(dx, dweight, dbias) from the forward pass's x, mean and rstd; the weight's and bias's
         gradients in the weight's dtype (the rows' when the weight is None)."""
+        if stream is not None:
+            with _on(stream):
+                return self.backward(dy, x, weight, mean, rstd, dx=dx, dweight=dweight, dbias=dbias)
         stride, wdt = self._check(x, weight)
         n = x.shape[0]
         if dx is None:
@@ -251,5 +281,5 @@ class FusedLayerNorm(_Plan):
             _vector("weight", weight, self.width, wdt), _vector("mean", mean, n),
             _vector("rstd", rstd, n), dx.data_ptr(), _rows("dx", dx, x.dtype, x.shape),
             _vector("dweight", dweight, self.width, wdt), _vector("dbias", dbias, self.width, wdt),
-            _stream(stream))
+            _stream(None))
         return dx, dweight, dbias
