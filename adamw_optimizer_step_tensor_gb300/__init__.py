@@ -23,7 +23,8 @@ from ._capi import (  # noqa: F401
     adamw_q8_set_maps, adamw_step, adamw_step_amp, adamw_step_noalloc, adamw_step_noalloc_status,
     adamw_wait_selftest, adamw_grad_norm, adamw_clip_grads, adamw_loss_plan_create,
     adamw_loss_plan_destroy, adamw_loss_plan_status, adamw_token_logps, adamw_policy_loss, adamw_preference_loss,
-    adamw_layer_norm_plan_create, adamw_layer_norm_plan_destroy, adamw_layer_norm_plan_status, adamw_layer_norm_forward,
+    adamw_layer_norm_plan_create, adamw_layer_norm_plan_destroy, adamw_layer_norm_plan_status, adamw_layer_norm_plan_set_wait_limit,
+    adamw_layer_norm_forward,
     adamw_layer_norm_backward,
 )
 

@@ -99,6 +99,7 @@ _SIGNATURES = {
                                              ctypes.c_int64, _vp]),
     "adamw_layer_norm_plan_create": (ctypes.c_int, [ctypes.c_int32, ctypes.c_float, ctypes.POINTER(_vp)]),
     "adamw_layer_norm_plan_destroy": (ctypes.c_int, [_vp]),
+    "adamw_layer_norm_plan_set_wait_limit": (ctypes.c_int, [_vp, ctypes.c_int32]),
     "adamw_layer_norm_plan_status": (ctypes.c_int, [_vp, ctypes.POINTER(ctypes.c_uint32)]),
     "adamw_layer_norm_forward": (ctypes.c_int, [_vp, ctypes.c_int, ctypes.c_int, ctypes.c_int64, _vp,
                                                 ctypes.c_int64, _vp, _vp, _vp, ctypes.c_int64, _vp, _vp,
@@ -402,6 +403,10 @@ def adamw_layer_norm_plan_create(width: int, eps: float) -> int:
 
 def adamw_layer_norm_plan_destroy(plan: int) -> None:
     _check(load().adamw_layer_norm_plan_destroy(plan))
+
+
+def adamw_layer_norm_plan_set_wait_limit(plan: int, limit_us: int) -> None:
+    _check(load().adamw_layer_norm_plan_set_wait_limit(plan, limit_us))
 
 
 def adamw_layer_norm_plan_status(plan: int) -> int:

@@ -213,6 +213,18 @@ __device__ __forceinline__ float inverse_root(float x) {
   return x > 0.0f && x <= 3.40282347e38f ? z : y;
 }
 
+// Whether a barrier's phase has completed, without waiting.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // The rows of a group, in turn, of ARRAYS matrices: bulk copies into a ring of
 // stages.  `take` leaves the current row in registers, `refill` (after every
 // thread of the group has taken its part) sends for the row that comes `stages`
@@ -232,8 +244,13 @@ struct Rows {
   int32_t width, stages;
   unsigned char* ring;           // [stages][ARRAYS][pitch]
   uint64_t* full;                // [stages]
+  uint64_t wait_ns;              // limit of a wait
+  uint32_t* fault;
   uint32_t n = 0;
-  bool lost = false;             // a wait gave up: no more waits, the fault is recorded
+  // 1 + the use for which this thread's wait gave up: it waits no more, and thread
+  // 0 sends no more.  (Where thread 0's own wait for a use succeeded its stage may be
+  // filled again, whoever else gave up on it.)
+  uint32_t lost = 0;
   // of the current row off the grid: its offset, whether this thread has one of
   // its first elements, the thread's column among its last ones, and both
   uint32_t off[ARRAYS];
@@ -341,7 +358,13 @@ struct Rows {
   }
   __device__ __forceinline__ void take(P (&p)[ARRAYS], const Place& at) {
     const uint32_t stage = n % stages;
-    if (!lost) lost = !mbar_wait(&full[stage], (n / stages) & 1u);
+    if (lost == 0u) {
+      const uint32_t parity = (n / stages) & 1u;
+      if (!(wait_ns != 0 ? mbar_wait(&full[stage], parity, wait_ns) : mbar_test(&full[stage], parity))) {
+        lost = n + 1;
+        atomicOr(fault, 1u);
+      }
+    }
 #pragma unroll
     for (int m = 0; m < ARRAYS; ++m) {
       unsigned char* s = slot(stage, m);
@@ -374,20 +397,20 @@ struct Rows {
   }
   __device__ __forceinline__ void refill(const Place& at) {
     if (G == 32) __syncwarp();
-    if (at.tid == 0 && ahead < rows) {
+    if (at.tid == 0 && ahead < rows && lost == 0u) {
       if (LIE == Lie::any) fence_proxy_async_smem();
       send(n % stages, at);
     }
     ahead += step;
     ++n;
   }
-  // After a wait that gave up, copies still on their way land before the CTA
-  // may leave.
-  __device__ __forceinline__ void finish(const Place& at, uint32_t* fault) {
-    if (!lost || at.tid != 0) return;
-    atomicOr(fault, 1u);
-    for (uint32_t i = n > static_cast<uint32_t>(stages) ? n - stages : 0; i < n; ++i)
-      mbar_wait(&full[i % stages], (i / stages) & 1u);
+  // After a wait of the sender's that gave up, the copies that may still be on their
+  // way (the newest of each stage) land before the CTA may leave.
+  __device__ __forceinline__ void finish(const Place& at) {
+    if (at.tid != 0 || lost == 0u) return;
+    const uint32_t all = stages, sent = min(lost - 1u + all, n);
+    for (uint32_t i = sent > all ? sent - all : 0; i < sent; ++i)
+      mbar_wait(&full[i % all], (i / all) & 1u);
   }
 };
 
@@ -418,7 +441,7 @@ ln_forward_kernel(const LayerNormArgs a) {
   const typename P::Place at(tid, a.width, shift_of(static_cast<const T*>(a.x) + t * a.x_stride));
   using R = Rows<P, T, LIE, G, 1>;
   R rows{{static_cast<const T*>(a.x)}, {a.x_stride}, a.rows, step, t, t, a.width, a.stages,
-         s_ring + group * a.stages * R::pitch_of(a.width), s_full[group]};
+         s_ring + group * a.stages * R::pitch_of(a.width), s_full[group], a.wait_ns, a.fault};
   rows.start(at);
   float2 w[kPairs], b[kPairs];
   load_params<W, P>(a.weight, 1.0f, at, w);
@@ -450,7 +473,7 @@ ln_forward_kernel(const LayerNormArgs a) {
       a.rstd[t] = rstd;
     }
   }
-  rows.finish(at, a.fault);
+  rows.finish(at);
 }
 
 template <typename T, typename W, Lie LIE, int G, int EACH>
@@ -472,7 +495,7 @@ ln_backward_kernel(const LayerNormArgs a) {
   using R = Rows<P, T, LIE, G, 2>;
   R rows{{static_cast<const T*>(a.x), static_cast<const T*>(a.dy)}, {a.x_stride, a.dy_stride},
          a.rows, step, t, t, a.width, a.stages,
-         s_ring + group * a.stages * 2 * R::pitch_of(a.width), s_full[group]};
+         s_ring + group * a.stages * 2 * R::pitch_of(a.width), s_full[group], a.wait_ns, a.fault};
   rows.start(at);
   float2 w[kPairs], gw[kPairs], gb[kPairs];
   load_params<W, P>(a.weight, 1.0f, at, w);
@@ -515,7 +538,7 @@ ln_backward_kernel(const LayerNormArgs a) {
       return fma2(mul2(p[1].pair(k), w[k]), r, fma2(h, c2, c1));
     });
   }
-  rows.finish(at, a.fault);
+  rows.finish(at);
   if (!sums_columns(G) || a.partial == nullptr) return;
   // the CTA's groups, in their order
   for (int g = 1; g < kGroups; ++g) {

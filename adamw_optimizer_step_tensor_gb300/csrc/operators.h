@@ -93,8 +93,10 @@ struct LayerNormArgs {
   int32_t parts;
   int32_t stages;              // rows on their way per group
   int32_t period;              // rows this far apart lie alike on the 16-byte grid
+  uint64_t wait_ns;            // limit of a wait
   uint32_t* fault;             // nonzero: a bounded wait gave up
 };
+constexpr uint64_t kNormWaitNs = 2000000000ull;   // 2 s, unless the plan has another
 cudaError_t prepare_layer_norm(int32_t width);
 cudaError_t launch_layer_norm_forward(adamw_dtype dt, adamw_dtype wdt, const LayerNormArgs& a,
                                       int sms, cudaStream_t s);

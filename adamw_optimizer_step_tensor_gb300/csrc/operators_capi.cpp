@@ -25,6 +25,7 @@ struct adamw_layer_norm_plan {
   int sms = 0;
   int32_t width = 0;
   float eps = 0.0f;
+  uint64_t wait_ns = kNormWaitNs;
   float* d_partial = nullptr;
   uint32_t* d_fault = nullptr;
 };
@@ -157,6 +158,7 @@ adamw_status layer_norm_args(const adamw_layer_norm_plan* plan, int dtype, int w
   a->width = plan->width;
   a->eps = plan->eps;
   a->partial = plan->d_partial;
+  a->wait_ns = plan->wait_ns;
   a->fault = plan->d_fault;
   return ADAMW_OK;
 }
@@ -367,6 +369,13 @@ adamw_status adamw_layer_norm_plan_create(int32_t width, float eps, adamw_layer_
 adamw_status adamw_layer_norm_plan_status(const adamw_layer_norm_plan* plan, uint32_t* fault_bits) {
   if (!plan) return fail(ADAMW_EINVAL, "plan is NULL");
   return read_fault(plan->device, plan->d_fault, fault_bits);
+}
+
+adamw_status adamw_layer_norm_plan_set_wait_limit(adamw_layer_norm_plan* plan, int32_t limit_us) {
+  if (!plan) return fail(ADAMW_EINVAL, "plan is NULL");
+  if (limit_us < 0) return fail(ADAMW_EINVAL, "limit_us < 0");
+  plan->wait_ns = static_cast<uint64_t>(limit_us) * 1000u;
+  return ADAMW_OK;
 }
 
 adamw_status adamw_layer_norm_plan_destroy(adamw_layer_norm_plan* plan) {

@@ -612,6 +612,10 @@ typedef struct adamw_layer_norm_plan adamw_layer_norm_plan;
 adamw_status adamw_layer_norm_plan_create(int32_t width, float eps, adamw_layer_norm_plan** out);
 /* Device-side health, as adamw_plan_status. */
 adamw_status adamw_layer_norm_plan_status(const adamw_layer_norm_plan* plan, uint32_t* fault_bits);
+/* Limit of each wait of the plan's row kernels, 2,000,000 us unless set: a wait that
+ * takes longer gives up, and adamw_layer_norm_plan_status then reports the call.  0
+ * gives up wherever a row is not there at once. */
+adamw_status adamw_layer_norm_plan_set_wait_limit(adamw_layer_norm_plan* plan, int32_t limit_us);
 /* Frees a layer norm plan (NULL is allowed).  Synchronises with the device first. */
 adamw_status adamw_layer_norm_plan_destroy(adamw_layer_norm_plan* plan);
 
