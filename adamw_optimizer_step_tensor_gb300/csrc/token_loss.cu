@@ -273,7 +273,7 @@ __device__ void load_rows(const LossArgs& a, RingShared& sh) {
   const uint32_t rank = cluster_rank(), ranks = cluster_size();
   uint32_t use = 0;
   bool ok = true;
-  for (uint32_t n = 0; ok && (ok = take_row(sh, n, 2u)); ++n) {
+  for (uint32_t n = 0; ok && take_row(sh, n, 2u); ++n) {
     const int64_t row = sh.queue[n % kQueue].row;
     const int kind = sh.queue[n % kQueue].kind;
     mbar_arrive(&sh.queue_empty[n % kQueue]);
@@ -292,10 +292,10 @@ __device__ void load_rows(const LossArgs& a, RingShared& sh) {
       bulk_g2s(sh.slot[s], share.base + static_cast<int64_t>(j) * kSlotBytes, bytes, &sh.full[s]);
     }
   }
-  // after a wait that gave up, the copies in flight land before the CTA may leave
-  if (!ok)
-    for (uint32_t u = use > kSlots ? use - kSlots : 0; u < use; ++u)
-      mbar_wait(&sh.full[u % kSlots], (u / kSlots) & 1u);
+  // the copies in flight land before the CTA may leave, whichever role it is whose
+  // wait gave up (otherwise they have all been waited for by now)
+  for (uint32_t u = use > kSlots ? use - kSlots : 0; u < use; ++u)
+    mbar_wait(&sh.full[u % kSlots], (u / kSlots) & 1u);
 }
 
 template <typename T, int PASS>
