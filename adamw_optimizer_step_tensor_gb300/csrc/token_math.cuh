@@ -160,11 +160,14 @@ __device__ __forceinline__ PolicyTerm policy_term(const LossArgs& a, const Polic
                                                   float logp) {
   const float ratio = a.old_logps != nullptr ? expf(logp - in.old) : 1.0f;
   const float bound = fminf(fmaxf(ratio, a.clip_lo), a.clip_hi);
-  const bool cut = bound * in.adv < ratio * in.adv;
+  // an advantage of 0 takes a ratio past float32 to 0
+  auto gain = [&](float r) { return in.adv != 0.0f || isnan(r) ? r * in.adv : 0.0f; };
+  const float full = gain(ratio), held = gain(bound);
+  const bool cut = held < full;
   PolicyTerm r;
-  r.policy = -in.w * ((cut ? bound : ratio) * in.adv);
+  r.policy = -in.w * (cut ? held : full);
   r.clipped = cut ? in.w : 0.0f;
-  r.slope = cut ? 0.0f : -in.adv * ratio;
+  r.slope = cut ? 0.0f : -full;
   r.kl = 0.0f;
   if (a.ref_logps != nullptr) {
     // e^x - x - 1 is inf where e^x is, and a term without a coefficient adds
