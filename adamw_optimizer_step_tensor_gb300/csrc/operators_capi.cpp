@@ -392,6 +392,8 @@ adamw_status adamw_layer_norm_forward(adamw_layer_norm_plan* plan, adamw_dtype d
   if (st != ADAMW_OK) return st;
   if (rows > 0 && (!y || !mean || !rstd)) return fail(ADAMW_EINVAL, "y, mean and rstd must be set");
   if (y_stride < plan->width) return fail(ADAMW_EINVAL, "a row stride is less than the width");
+  if (rows > 1 && y == x && y_stride != x_stride)
+    return fail(ADAMW_EINVAL, "y in place of x needs x's row stride");
   if (!aligned(bias, dtype_bytes(weight_dtype)) || !aligned(y, dtype_bytes(dtype)) ||
       !aligned(mean, 4) || !aligned(rstd, 4))
     return fail(ADAMW_EALIGN, "a pointer is not aligned to its element size");
@@ -419,6 +421,8 @@ adamw_status adamw_layer_norm_backward(adamw_layer_norm_plan* plan, adamw_dtype 
     return fail(ADAMW_EINVAL, "dy, mean, rstd and dx must be set");
   if (dy_stride < plan->width || dx_stride < plan->width)
     return fail(ADAMW_EINVAL, "a row stride is less than the width");
+  if (rows > 1 && ((dx == dy && dx_stride != dy_stride) || (dx == x && dx_stride != x_stride)))
+    return fail(ADAMW_EINVAL, "dx in place of another matrix needs its row stride");
   if (!aligned(dy, dtype_bytes(dtype)) || !aligned(dx, dtype_bytes(dtype)) || !aligned(mean, 4) ||
       !aligned(rstd, 4) || !aligned(dweight, dtype_bytes(weight_dtype)) ||
       !aligned(dbias, dtype_bytes(weight_dtype)))

@@ -623,7 +623,7 @@ adamw_status adamw_layer_norm_plan_destroy(adamw_layer_norm_plan* plan);
  * y = (x - mean) rstd * weight + bias per row, rstd = 1 / sqrt(var + eps) with
  * the variance over width elements.  Row strides in elements, >= width.  weight
  * and bias are float32 or of the rows' dtype (EUNSUPPORTED otherwise) and may
- * be NULL (1 and 0).  mean, rstd: float32 [rows].  y may be x.
+ * be NULL (1 and 0).  mean, rstd: float32 [rows].  y may be x (same stride).
  */
 adamw_status adamw_layer_norm_forward(adamw_layer_norm_plan* plan, adamw_dtype dtype,
                                       adamw_dtype weight_dtype, int64_t rows, const void* x,
@@ -635,7 +635,7 @@ adamw_status adamw_layer_norm_forward(adamw_layer_norm_plan* plan, adamw_dtype d
  * dx = rstd (w dy - mean(w dy) - xhat mean(w dy xhat)),  dweight = sum over rows
  * of dy xhat,  dbias = sum over rows of dy, from the forward pass's mean and
  * rstd.  dweight and dbias are of the weight's dtype, written (not added to),
- * and may be NULL.  dx may be dy (same stride).
+ * and may be NULL.  dx may be dy or x (same stride).
  */
 adamw_status adamw_layer_norm_backward(adamw_layer_norm_plan* plan, adamw_dtype dtype,
                                        adamw_dtype weight_dtype, int64_t rows, const void* dy,
