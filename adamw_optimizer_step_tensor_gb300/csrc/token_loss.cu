@@ -489,18 +489,13 @@ __device__ void finish_rows(const LossArgs& a, RingShared& sh, double (&acc)[4])
         if (r.far() && lane == 0) sh.queue[e].kind = kRowFar;
         l = far_row_log(a, r, q.in[kInToken]);
       }
-      float slope = 0.0f;
-      if (policy_pass(PASS)) {
-        const PolicyTerm p = policy_term(a, {q.in[kInWeight], q.in[kInAdvantage], q.in[kInOld], q.in[kInRef]}, l.logp);
-        slope = p.slope;
-        acc[1] += p.policy;
-        acc[2] += p.kl;
-        acc[3] += p.clipped;
-      }
+      PolicyTerm p{0.0f, 0.0f, 0.0f, 0.0f};
+      if (policy_pass(PASS))
+        p = policy_term(a, {q.in[kInWeight], q.in[kInAdvantage], q.in[kInOld], q.in[kInRef]}, l.logp);
       if (lane == 0) {
         if (writes_gradient(PASS)) {
           // first of all: the gradient warps wait for it
-          const float coef = slope * out_scale;
+          const float coef = p.slope * out_scale;
           sh.result[e] = {r.c, grad_factor<T>(a, r, coef), coef, 0.0f};
           mbar_arrive(&sh.ready[e]);
         }
@@ -509,9 +504,14 @@ __device__ void finish_rows(const LossArgs& a, RingShared& sh, double (&acc)[4])
           if (a.lse != nullptr) a.lse[row] = l.lse;
           if ((PASS == kPassPrefer || PASS == kPassPolicy) && a.row_stat != nullptr) {
             a.row_stat[row] = make_float2(r.c, r.s);
-            if (PASS == kPassPolicy) a.row_coef[row] = slope;
+            if (PASS == kPassPolicy) a.row_coef[row] = p.slope;
           }
         }
+      }
+      if (policy_pass(PASS)) {
+        acc[1] += p.policy;
+        acc[2] += p.kl;
+        acc[3] += p.clipped;
       }
     } else if (writes_gradient(PASS) && lane == 0) {
       mbar_arrive(&sh.ready[e]);                         // keeps the phases in step
