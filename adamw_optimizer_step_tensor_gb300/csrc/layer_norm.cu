@@ -772,19 +772,39 @@ __global__ void __launch_bounds__(kWideThreads) ln_backward_wide_kernel(const La
 }
 
 // Column sums over the rows blockIdx.y, blockIdx.y + parts, ...; a thread has one
-// word of columns.
+// word of columns.  The wider the rows, the fewer the parts of one wave of CTAs, and
+// the longer a part's sum (32768 rows of 65537 columns: 16384 terms).  So it goes to
+// memory every kRun rows, and an error is at most kRun + terms / kRun units.
 constexpr int kColumnThreads = 256;
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kColumnThreads) ln_columns_wide_kernel(const LayerNormArgs a) {
   using Row = WideRow<T, VEC>;
   constexpr int E = Row::E;
   constexpr int kRows = 4;               // loads of as many rows under way
+  constexpr int kRun = 256;
   const int w = blockIdx.x * kColumnThreads + threadIdx.x;
   if (w * E >= a.width) return;
   float gw[E], gb[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) gw[e] = gb[e] = 0.0f;
+  float* const pw = a.partial + static_cast<int64_t>(blockIdx.y) * a.width + w * E;
+  float* const pb = pw + static_cast<int64_t>(a.parts) * a.width;
+  int run = 0;
+  bool first = true;
+  auto put = [&] {
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      pw[e] = first ? gw[e] : pw[e] + gw[e];
+      pb[e] = first ? gb[e] : pb[e] + gb[e];
+      gw[e] = gb[e] = 0.0f;
+    }
+    first = false;
+  };
   for (int64_t t0 = blockIdx.y; t0 < a.rows; t0 += static_cast<int64_t>(kRows) * a.parts) {
+    if (++run > kRun / kRows) {
+      put();
+      run = 1;
+    }
     typename Row::Raw x[kRows], g[kRows];
     float mean[kRows], rstd[kRows];
 #pragma unroll
@@ -809,13 +829,7 @@ __global__ void __launch_bounds__(kColumnThreads) ln_columns_wide_kernel(const L
       }
     }
   }
-  float* const pw = a.partial + static_cast<int64_t>(blockIdx.y) * a.width + w * E;
-  float* const pb = pw + static_cast<int64_t>(a.parts) * a.width;
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    pw[e] = gw[e];
-    pb[e] = gb[e];
-  }
+  put();
 }
 
 // ---- launches

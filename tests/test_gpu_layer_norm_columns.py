@@ -1,0 +1,35 @@
+"""GPU: column sums over many rows, with the bound of test_gpu_layer_norm.py.
+
+dy = 1 + 2^-k everywhere, a term that a float32 sum of 2^(23 - k) or more rounds down
+every time: one long sum of such terms is off by up to 2^-k of its size.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+from adamw_optimizer_step_tensor_gb300 import FusedLayerNorm
+from test_gpu_layer_norm import close, wide
+
+pytestmark = pytest.mark.gpu
+
+
+def check(rows, width, k):
+    x = torch.empty(rows, width, device="cuda")
+    x.normal_(generator=torch.Generator(device="cuda").manual_seed(rows))
+    dy = torch.full((rows, width), 1 + 2.0 ** -k, device="cuda")
+    norm = FusedLayerNorm(width)
+    mean, rstd = torch.zeros(rows, device="cuda"), torch.ones(rows, device="cuda")     # xhat = x
+    _, dw, db = norm.backward(dy, x, None, mean, rstd, dx=dy)
+    want, size = np.zeros(width), np.zeros(width)
+    for at in range(0, rows, 1 << 16):
+        part = x[at:at + (1 << 16)].double()
+        want += wide(part.sum(0)) * (1 + 2.0 ** -k)
+        size += wide(part.abs().sum(0)) * (1 + 2.0 ** -k)
+    close(dw, want, size, torch.float32, 2e-5)
+    close(db, np.full(width, rows * (1 + 2.0 ** -k)), rows, torch.float32, 2e-5)
+
+
+@pytest.mark.parametrize("rows,width,k", [(20_000, 20_003, 13), (8000, 40_960, 13), (3000, 160_001, 13)])
+def test_rows_wider_than_registers(rows, width, k):
+    check(rows, width, k)
