@@ -836,6 +836,17 @@ __global__ void __launch_bounds__(kColumnThreads) ln_columns_wide_kernel(const L
 
 int64_t at_most(int64_t n, int64_t most) { return n < most ? n : most; }
 
+// Wider rows have their column sums taken by ln_columns_wide_kernel, by CTAs of
+// kColumnThreads words of `each` elements (at most 8), in this many parts.
+constexpr int kOwnColumns = 512 * 16;
+int wide_columns(int32_t width, int each) {
+  return (width / each + kColumnThreads - 1) / kColumnThreads;
+}
+int64_t wide_parts(int columns, int sms) {
+  const int64_t most = static_cast<int64_t>(kNormPartsPerSm) * sms;
+  return columns < most ? most / columns : 1;
+}
+
 // Rows on their way per group, as many as fit beside the other resident CTAs.
 template <int G>
 int stages_for(int64_t row_bytes, int per_sm) {
@@ -963,14 +974,12 @@ cudaError_t backward(LayerNormArgs a, int sms, cudaStream_t s) {
   if (a.rows == 0) {
     a.parts = 0;
   } else {
-    const bool own_columns = a.width > 512 * 16;
+    const bool own_columns = a.width > kOwnColumns;
     if (own_columns && (a.dweight != nullptr || a.dbias != nullptr)) {
       // before the rows: dx may be dy.  One wave of CTAs.
       const bool vec = lie == Lie::grid;
-      const int columns = (a.width / (vec ? 16 / static_cast<int>(sizeof(T)) : 1) + kColumnThreads - 1) /
-                          kColumnThreads;
-      const int64_t most = static_cast<int64_t>(kNormPartsPerSm) * sms;
-      a.parts = static_cast<int32_t>(at_most(a.rows, columns < most ? most / columns : 1));
+      const int columns = wide_columns(a.width, vec ? 16 / static_cast<int>(sizeof(T)) : 1);
+      a.parts = static_cast<int32_t>(at_most(a.rows, wide_parts(columns, sms)));
       const dim3 grid(columns, a.parts);
       if (vec) ln_columns_wide_kernel<T, true><<<grid, kColumnThreads, 0, s>>>(a);
       else ln_columns_wide_kernel<T, false><<<grid, kColumnThreads, 0, s>>>(a);
@@ -997,6 +1006,10 @@ cudaError_t backward(LayerNormArgs a, int sms, cudaStream_t s) {
 }
 
 }  // namespace
+
+int64_t norm_parts(int32_t width, int sms) {
+  return width > kOwnColumns ? wide_parts(wide_columns(width, 8), sms) : int64_t{kNormPartsPerSm} * sms;
+}
 
 cudaError_t prepare_layer_norm(int32_t width) {
   cudaError_t e = prepare_width<float, float>(width);

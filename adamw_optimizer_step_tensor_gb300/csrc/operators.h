@@ -102,7 +102,8 @@ cudaError_t launch_layer_norm_forward(adamw_dtype dt, adamw_dtype wdt, const Lay
                                       int sms, cudaStream_t s);
 cudaError_t launch_layer_norm_backward(adamw_dtype dt, adamw_dtype wdt, const LayerNormArgs& a,
                                        int sms, cudaStream_t s);
-// Rows of column sums the backward pass keeps per plan.
+// Rows of column sums the backward pass keeps per plan, at most kNormPartsPerSm per SM.
 constexpr int kNormPartsPerSm = 4;
+int64_t norm_parts(int32_t width, int sms);
 
 }  // namespace adamw

@@ -352,7 +352,7 @@ adamw_status adamw_layer_norm_plan_create(int32_t width, float eps, adamw_layer_
   p->sms = sms;
   p->width = width;
   p->eps = eps;
-  const size_t n = 2 * static_cast<size_t>(kNormPartsPerSm) * sms * width * sizeof(float);
+  const size_t n = 2 * static_cast<size_t>(norm_parts(width, sms)) * width * sizeof(float);
   cudaError_t e = prepare_layer_norm(width);
   if (e != cudaSuccess) return cuda_fail(e, "prepare the layer norm kernels");
   e = cudaMalloc(&p->d_partial, n);
