@@ -39,6 +39,7 @@ constexpr int backward_threads(int group, int each) {
 }
 constexpr int kStages = 4;             // rows on their way per group, at most
 constexpr int kSmemPerSm = 184 * 1024;  // for the rows on their way
+constexpr int kRunRows = 256;          // of a group whose column sums one launch adds up
 
 template <typename W>
 __device__ __forceinline__ float param(const void* p, int j, float none) {
@@ -562,15 +563,16 @@ ln_backward_kernel(const LayerNormArgs a) {
   if (group != 0) return;
   float* const pw = a.partial + static_cast<int64_t>(blockIdx.x) * a.width;
   float* const pb = pw + static_cast<int64_t>(a.parts) * a.width;
+  auto put = [&](float* p, float x) { *p = a.add != 0 ? *p + x : x; };
 #pragma unroll
   for (int k = 0; k < kPairs; ++k) {
     if (at.has(2 * k)) {
-      pw[at.column(2 * k)] = gw[k].x;
-      pb[at.column(2 * k)] = gb[k].x;
+      put(pw + at.column(2 * k), gw[k].x);
+      put(pb + at.column(2 * k), gb[k].x);
     }
     if (at.has(2 * k + 1)) {
-      pw[at.column(2 * k + 1)] = gw[k].y;
-      pb[at.column(2 * k + 1)] = gb[k].y;
+      put(pw + at.column(2 * k + 1), gw[k].y);
+      put(pb + at.column(2 * k + 1), gb[k].y);
     }
   }
 }
@@ -882,7 +884,25 @@ int backward_group(LayerNormArgs a, int sms, cudaStream_t s) {
   const int64_t row = 2 * static_cast<int64_t>(
                               Rows<Piece<T, LIE, G, EACH>, T, LIE, G, 2>::pitch_of(a.width));
   a.stages = stages_for<G>(row, kPerSm);
-  ln_backward_kernel<T, W, LIE, G, EACH><<<ctas, kCta<G>, kGroups * a.stages * row, s>>>(a);
+  // a launch for every kRunRows rows of a group, so that no column sum in registers
+  // has more terms: an error is then at most kRunRows + launches units
+  const int64_t rows = a.rows;
+  const int64_t runs = a.partial == nullptr || !sums_columns(G)
+                           ? 1
+                           : (rows - 1) / (static_cast<int64_t>(kRunRows) * kGroups * ctas) + 1;
+  // the same number of rows each, and their shift on the 16-byte grid
+  const int64_t each = ((rows - 1) / runs / a.period + 1) * a.period;
+  const LayerNormArgs all = a;
+  for (int64_t from = 0; from < rows; from += each) {
+    a.x = static_cast<const T*>(all.x) + from * a.x_stride;
+    a.dy = static_cast<const T*>(all.dy) + from * a.dy_stride;
+    a.dx = static_cast<T*>(all.dx) + from * a.dx_stride;
+    a.mean = all.mean + from;
+    a.rstd = all.rstd + from;
+    a.rows = at_most(rows - from, each);
+    a.add = from > 0;
+    ln_backward_kernel<T, W, LIE, G, EACH><<<ctas, kCta<G>, kGroups * a.stages * row, s>>>(a);
+  }
   return ctas;
 }
 

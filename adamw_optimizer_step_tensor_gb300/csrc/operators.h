@@ -91,6 +91,7 @@ struct LayerNormArgs {
   float eps;
   float* partial;              // plan-owned: [2][parts][width]
   int32_t parts;
+  int32_t add;                 // add to the partial sums that are there
   int32_t stages;              // rows on their way per group
   int32_t period;              // rows this far apart lie alike on the 16-byte grid
   uint64_t wait_ns;            // limit of a wait
