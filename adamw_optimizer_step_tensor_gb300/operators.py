@@ -21,9 +21,19 @@ _LABEL_BYTES = {torch.int32: 4, torch.int64: 8}
 _F32 = torch.float32
 
 
-def _rows(name, t, dtype=None, shape=None):
+def _elsewhere(name, t, device, what):
+    """Raises unless no device in particular is asked for and t is on a GPU."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a {what}")
+    if device is not None:
+        raise ValueError(f"{name} is on device {t.get_device()}, the plan on device {device}")
+
+
+def _rows(name, t, dtype=None, shape=None, device=None):
     """Checks a matrix of rows (the last axis contiguous) and returns its row stride."""
-    if not t.is_cuda or t.dim() != 2:
+    if t.get_device() != device:
+        _elsewhere(name, t, device, "CUDA matrix")
+    if t.dim() != 2:
         raise ValueError(f"{name} must be a CUDA matrix")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
@@ -40,13 +50,15 @@ def _rows(name, t, dtype=None, shape=None):
     return stride
 
 
-def _vector(name, t, n, dtype=_F32):
+def _vector(name, t, n, device=None, dtype=_F32):
     """Address of a contiguous CUDA vector of n elements; None stays None."""
     if t is None:
         return None
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if not t.is_cuda or t.numel() != n or not t.is_contiguous():
+    if t.get_device() != device:
+        _elsewhere(name, t, device, f"contiguous CUDA tensor of {n} elements")
+    if t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous CUDA tensor of {n} elements")
     return t.data_ptr()
 
@@ -64,6 +76,8 @@ def _on(stream):
 
 
 class _Plan:
+    """A plan of the library on the device that was current when it was made."""
+
     _destroy = None
 
     def close(self) -> None:
@@ -91,6 +105,7 @@ class FusedTokenLoss(_Plan):
 
     def __init__(self, max_rows: int, max_pairs: int = 0):
         self.plan = _capi.adamw_loss_plan_create(int(max_rows), int(max_pairs))
+        self.device = torch.cuda.current_device()
         # the argument records, filled anew by every call
         self._z = _capi.adamw_logits()
         self._policy = _capi.adamw_policy()
@@ -105,23 +120,22 @@ class FusedTokenLoss(_Plan):
             raise TypeError(f"unsupported logits dtype {logits.dtype}")
         if labels.dtype not in _LABEL_BYTES:
             raise TypeError(f"labels must be int32 or int64, got {labels.dtype}")
-        z = self._z
-        z.row_stride = _rows("logits", logits)
+        z, dev = self._z, self.device
+        z.row_stride = _rows("logits", logits, None, None, dev)
         z.rows, z.vocab = logits.shape
-        z.labels = _vector("labels", labels, logits.shape[0], labels.dtype)
+        z.labels = _vector("labels", labels, logits.shape[0], dev, labels.dtype)
         z.logits = logits.data_ptr()
         z.label_bytes = _LABEL_BYTES[labels.dtype]
         z.dtype = _DTYPES[logits.dtype]
         z.temperature = temperature
         return z
 
-    @staticmethod
-    def _gradient(logits, dlogits, backward):
+    def _gradient(self, logits, dlogits, backward):
         if not backward:
             return None, None, 0
         if dlogits is None:
             dlogits = torch.empty_like(logits)
-        return dlogits, dlogits.data_ptr(), _rows("dlogits", dlogits, logits.dtype, logits.shape)
+        return dlogits, dlogits.data_ptr(), _rows("dlogits", dlogits, logits.dtype, logits.shape, self.device)
 
     def logps(self, logits, labels, *, temperature=1.0, logps=None, lse=None, stream=None):
         """(logps, lse) of every row: the log-probability of its token and the log of its sum of
@@ -130,12 +144,12 @@ class FusedTokenLoss(_Plan):
             with _on(stream):
                 return self.logps(logits, labels, temperature=temperature, logps=logps, lse=lse)
         z = self._logits(logits, labels, temperature)
-        n = logits.shape[0]
+        n, dev = logits.shape[0], self.device
         if logps is None:
             logps = _empty(n, logits)
         if lse is None:
             lse = _empty(n, logits)
-        _capi.adamw_token_logps(self.plan, z, _vector("logps", logps, n), _vector("lse", lse, n),
+        _capi.adamw_token_logps(self.plan, z, _vector("logps", logps, n, dev), _vector("lse", lse, n, dev),
                                 _stream(None))
         return logps, lse
 
@@ -155,22 +169,22 @@ class FusedTokenLoss(_Plan):
                                    kl_coef=kl_coef, temperature=temperature, grad_scale=grad_scale,
                                    backward=backward, stats=stats, logps=logps, dlogits=dlogits)
         z = self._logits(logits, labels, temperature)
-        n = logits.shape[0]
+        n, dev = logits.shape[0], self.device
         p = self._policy
-        p.weights = _vector("weights", weights, n)
-        p.advantages = _vector("advantages", advantages, n)
-        p.old_logps = _vector("old_logps", old_logps, n)
-        p.ref_logps = _vector("ref_logps", ref_logps, n)
+        p.weights = _vector("weights", weights, n, dev)
+        p.advantages = _vector("advantages", advantages, n, dev)
+        p.old_logps = _vector("old_logps", old_logps, n, dev)
+        p.ref_logps = _vector("ref_logps", ref_logps, n, dev)
         p.clip_low, p.clip_high = clip
         p.kl_coef = kl_coef
-        p.grad_scale_dev = _vector("grad_scale", grad_scale, 1)
+        p.grad_scale_dev = _vector("grad_scale", grad_scale, 1, dev)
         if stats is None:
             stats = _empty(4, logits)
         if logps is None:
             logps = _empty(n, logits)
         dlogits, at, stride = self._gradient(logits, dlogits, backward)
-        _capi.adamw_policy_loss(self.plan, z, p, _vector("stats", stats, 4), _vector("logps", logps, n),
-                                at, stride, _stream(None))
+        _capi.adamw_policy_loss(self.plan, z, p, _vector("stats", stats, 4, dev),
+                                _vector("logps", logps, n, dev), at, stride, _stream(None))
         return stats, logps, dlogits
 
     def preference(self, logits, labels, weights, ref_logps, seq_starts, *, beta=0.1,
@@ -191,16 +205,16 @@ class FusedTokenLoss(_Plan):
                                        grad_scale=grad_scale, backward=backward, stats=stats, rewards=rewards,
                                        logps=logps, dlogits=dlogits)
         z = self._logits(logits, labels, temperature)
-        n = logits.shape[0]
+        n, dev = logits.shape[0], self.device
         pairs = (seq_starts.numel() - 1) // 2
         p = self._preference
-        p.weights = _vector("weights", weights, n)
-        p.ref_logps = _vector("ref_logps", ref_logps, n)
-        p.seq_starts = _vector("seq_starts", seq_starts, 2 * pairs + 1, torch.int32)
+        p.weights = _vector("weights", weights, n, dev)
+        p.ref_logps = _vector("ref_logps", ref_logps, n, dev)
+        p.seq_starts = _vector("seq_starts", seq_starts, 2 * pairs + 1, dev, torch.int32)
         p.n_pairs = pairs
         p.beta = beta
         p.label_smoothing = label_smoothing
-        p.grad_scale_dev = _vector("grad_scale", grad_scale, 1)
+        p.grad_scale_dev = _vector("grad_scale", grad_scale, 1, dev)
         if stats is None:
             stats = _empty(4, logits)
         if rewards is None:
@@ -208,9 +222,9 @@ class FusedTokenLoss(_Plan):
         if logps is None:
             logps = _empty(n, logits)
         dlogits, at, stride = self._gradient(logits, dlogits, backward)
-        _capi.adamw_preference_loss(self.plan, z, p, _vector("stats", stats, 4),
-                                    _vector("rewards", rewards, 2 * pairs), _vector("logps", logps, n),
-                                    at, stride, _stream(None))
+        _capi.adamw_preference_loss(self.plan, z, p, _vector("stats", stats, 4, dev),
+                                    _vector("rewards", rewards, 2 * pairs, dev),
+                                    _vector("logps", logps, n, dev), at, stride, _stream(None))
         return stats, rewards, logps, dlogits
 
 
@@ -225,6 +239,7 @@ class FusedLayerNorm(_Plan):
 
     def __init__(self, width: int, eps: float = 1e-5):
         self.plan = _capi.adamw_layer_norm_plan_create(int(width), float(eps))
+        self.device = torch.cuda.current_device()
         self.width = int(width)
 
     def status(self) -> int:
@@ -236,7 +251,7 @@ class FusedLayerNorm(_Plan):
             raise TypeError(f"unsupported dtype {x.dtype}")
         if weight is not None and weight.dtype not in (torch.float32, x.dtype):
             raise TypeError(f"the weight must be float32 or {x.dtype}, got {weight.dtype}")
-        stride = _rows("x", x)
+        stride = _rows("x", x, None, None, self.device)
         if x.shape[1] != self.width:
             raise ValueError(f"x must have {self.width} columns, got {x.shape[1]}")
         return stride, (x.dtype if weight is None else weight.dtype)
@@ -247,7 +262,7 @@ class FusedLayerNorm(_Plan):
             with _on(stream):
                 return self.forward(x, weight, bias, y=y, mean=mean, rstd=rstd)
         stride, wdt = self._check(x, weight if weight is not None else bias)
-        n = x.shape[0]
+        n, dev = x.shape[0], self.device
         if y is None:
             y = torch.empty_like(x)
         if mean is None:
@@ -256,9 +271,9 @@ class FusedLayerNorm(_Plan):
             rstd = _empty(n, x)
         _capi.adamw_layer_norm_forward(
             self.plan, _DTYPES[x.dtype], _DTYPES[wdt], n, x.data_ptr(), stride,
-            _vector("weight", weight, self.width, wdt), _vector("bias", bias, self.width, wdt),
-            y.data_ptr(), _rows("y", y, x.dtype, x.shape), _vector("mean", mean, n),
-            _vector("rstd", rstd, n), _stream(None))
+            _vector("weight", weight, self.width, dev, wdt), _vector("bias", bias, self.width, dev, wdt),
+            y.data_ptr(), _rows("y", y, x.dtype, x.shape, dev), _vector("mean", mean, n, dev),
+            _vector("rstd", rstd, n, dev), _stream(None))
         return y, mean, rstd
 
     def backward(self, dy, x, weight, mean, rstd, *, dx=None, dweight=None, dbias=None, stream=None):
@@ -268,7 +283,7 @@ class FusedLayerNorm(_Plan):
             with _on(stream):
                 return self.backward(dy, x, weight, mean, rstd, dx=dx, dweight=dweight, dbias=dbias)
         stride, wdt = self._check(x, weight)
-        n = x.shape[0]
+        n, dev = x.shape[0], self.device
         if dx is None:
             dx = torch.empty_like(x)
         if dweight is None:
@@ -277,9 +292,9 @@ class FusedLayerNorm(_Plan):
             dbias = _empty(self.width, x, wdt)
         _capi.adamw_layer_norm_backward(
             self.plan, _DTYPES[x.dtype], _DTYPES[wdt], n, dy.data_ptr(),
-            _rows("dy", dy, x.dtype, x.shape), x.data_ptr(), stride,
-            _vector("weight", weight, self.width, wdt), _vector("mean", mean, n),
-            _vector("rstd", rstd, n), dx.data_ptr(), _rows("dx", dx, x.dtype, x.shape),
-            _vector("dweight", dweight, self.width, wdt), _vector("dbias", dbias, self.width, wdt),
+            _rows("dy", dy, x.dtype, x.shape, dev), x.data_ptr(), stride,
+            _vector("weight", weight, self.width, dev, wdt), _vector("mean", mean, n, dev),
+            _vector("rstd", rstd, n, dev), dx.data_ptr(), _rows("dx", dx, x.dtype, x.shape, dev),
+            _vector("dweight", dweight, self.width, dev, wdt), _vector("dbias", dbias, self.width, dev, wdt),
             _stream(None))
         return dx, dweight, dbias
