@@ -47,6 +47,8 @@ void free_layer_norm_plan(adamw_layer_norm_plan* p) {
   delete p;
 }
 
+constexpr int64_t kMaxPlanRows = int64_t{1} << 40;
+
 bool float_dtype(int d) { return d == ADAMW_F32 || d == ADAMW_F16 || d == ADAMW_BF16; }
 size_t dtype_bytes(int d) { return d == ADAMW_F32 ? 4 : 2; }
 
@@ -218,6 +220,8 @@ adamw_status adamw_loss_plan_create(int64_t max_rows, int32_t max_pairs, adamw_l
   if (!out) return fail(ADAMW_EINVAL, "out is NULL");
   *out = nullptr;
   if (max_rows < 0 || max_pairs < 0) return fail(ADAMW_EINVAL, "max_rows and max_pairs must be >= 0");
+  if (max_rows > kMaxPlanRows)         // 16 TB of statistics; the byte counts wrap at 2^62
+    return fail(ADAMW_EUNSUPPORTED, "more than 2^40 rows");
   if (max_pairs > kLossMaxCtas)
     return fail(ADAMW_EUNSUPPORTED, "more than %d pairs", kLossMaxCtas);
   int device = -1, sms = 0;
@@ -341,6 +345,7 @@ adamw_status adamw_layer_norm_plan_create(int32_t width, float eps, adamw_layer_
   if (!out) return fail(ADAMW_EINVAL, "out is NULL");
   *out = nullptr;
   if (width < 1) return fail(ADAMW_EINVAL, "width < 1");
+  if (width > (1 << 30)) return fail(ADAMW_EUNSUPPORTED, "width is more than 2^30");
   if (!(eps >= 0.0f) || !std::isfinite(eps)) return fail(ADAMW_EINVAL, "eps must be finite and >= 0");
   int device = -1, sms = 0;
   adamw_status st = here(&device, &sms);

@@ -531,9 +531,9 @@ typedef struct {
 } adamw_logits;
 
 /* Workspace of the token losses: per-row statistics of up to max_rows rows and
- * the CTAs' partial sums.  max_pairs (at most 4096) bounds the preference loss's
- * pairs.  Synchronous (allocates and clears device memory).  Calls on one plan
- * must not overlap one another. */
+ * the CTAs' partial sums.  max_rows is at most 2^40 (EUNSUPPORTED above); max_pairs
+ * (at most 4096) bounds the preference loss's pairs.  Synchronous (allocates and
+ * clears device memory).  Calls on one plan must not overlap one another. */
 typedef struct adamw_loss_plan adamw_loss_plan;
 adamw_status adamw_loss_plan_create(int64_t max_rows, int32_t max_pairs, adamw_loss_plan** out);
 /* Device-side health, as adamw_plan_status: every wait of the row kernels is
@@ -605,8 +605,8 @@ adamw_status adamw_preference_loss(adamw_loss_plan* plan, const adamw_logits* z,
                                    float* logps, void* dlogits, int64_t dlogits_stride,
                                    void* stream);
 
-/* Workspace of layer norm over rows of `width` elements: the partial sums of the
- * weight's and bias's gradients.  Synchronous.  eps finite and >= 0.  Calls on
+/* Workspace of layer norm over rows of `width` (1 .. 2^30) elements: the partial sums
+ * of the weight's and bias's gradients.  Synchronous.  eps finite and >= 0.  Calls on
  * one plan must not overlap one another. */
 typedef struct adamw_layer_norm_plan adamw_layer_norm_plan;
 adamw_status adamw_layer_norm_plan_create(int32_t width, float eps, adamw_layer_norm_plan** out);
