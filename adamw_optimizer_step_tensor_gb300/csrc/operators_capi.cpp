@@ -52,12 +52,20 @@ constexpr int64_t kMaxPlanRows = int64_t{1} << 40;
 bool float_dtype(int d) { return d == ADAMW_F32 || d == ADAMW_F16 || d == ADAMW_BF16; }
 size_t dtype_bytes(int d) { return d == ADAMW_F32 ? 4 : 2; }
 
+// A CUDA call's failure.  The runtime keeps it for the thread until it is read: left
+// there, the next launch would report it as its own.
+adamw_status failed(cudaError_t e, const char* what, adamw_status st = ADAMW_ECUDA) {
+  cudaGetLastError();
+  if (st == ADAMW_ECUDA) return cuda_fail(e, what);
+  return fail(st, "%s: %s", what, cudaGetErrorString(e));
+}
+
 // The current device and its SM count.
 adamw_status here(int* device, int* sms) {
   cudaError_t e = cudaGetDevice(device);
-  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+  if (e != cudaSuccess) return failed(e, "cudaGetDevice");
   e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, *device);
-  if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceGetAttribute");
+  if (e != cudaSuccess) return failed(e, "cudaDeviceGetAttribute");
   return ADAMW_OK;
 }
 
@@ -172,7 +180,7 @@ adamw_status read_fault(int device, const uint32_t* d_fault, uint32_t* fault_bit
   cudaError_t e = cudaDeviceSynchronize();
   uint32_t bits = 0;
   if (e == cudaSuccess) e = cudaMemcpy(&bits, d_fault, sizeof bits, cudaMemcpyDeviceToHost);
-  if (e != cudaSuccess) return cuda_fail(e, "read fault word");
+  if (e != cudaSuccess) return failed(e, "read fault word");
   if (fault_bits) *fault_bits = bits;
   if (bits != 0) return fail(ADAMW_ETIMEOUT, "a bounded wait gave up (fault bits 0x%x)", bits);
   return ADAMW_OK;
@@ -198,7 +206,7 @@ adamw_status adamw_grad_norm(adamw_plan* plan, float max_norm, const float* grad
   const NormArgs a{plan->d_tensors, plan->d_chunks, plan->n_chunks, plan->d_norm, grad_scale_dev,
                    max_norm, norm_dev, clip_scale_dev, found_inf_dev};
   cudaError_t e = launch_grad_norm(plan->gdt, a, plan->grid_norm, static_cast<cudaStream_t>(stream));
-  return e == cudaSuccess ? ADAMW_OK : cuda_fail(e, "launch gradient norm");
+  return e == cudaSuccess ? ADAMW_OK : failed(e, "launch gradient norm");
 }
 
 adamw_status adamw_clip_grads(adamw_plan* plan, const float* clip_scale_dev, void* stream) {
@@ -211,7 +219,7 @@ adamw_status adamw_clip_grads(adamw_plan* plan, const float* clip_scale_dev, voi
   cudaError_t e = launch_clip_grads(plan->gdt, plan->d_tensors, plan->d_chunks, plan->n_chunks,
                                     clip_scale_dev, plan->grid_check,
                                     static_cast<cudaStream_t>(stream));
-  return e == cudaSuccess ? ADAMW_OK : cuda_fail(e, "launch gradient clip");
+  return e == cudaSuccess ? ADAMW_OK : failed(e, "launch gradient clip");
 }
 
 // ---------------------------------------------------------------- token losses
@@ -235,16 +243,16 @@ adamw_status adamw_loss_plan_create(int64_t max_rows, int32_t max_pairs, adamw_l
   p->max_pairs = max_pairs;
   const size_t sums = (4 * kLossMaxCtas + 1) * sizeof(double);
   cudaError_t e = prepare_token_loss(sms, &p->limits);
-  if (e != cudaSuccess) return cuda_fail(e, "prepare the token loss kernels");
+  if (e != cudaSuccess) return failed(e, "prepare the token loss kernels");
   e = cudaMalloc(&p->d_partial, sums);
   if (e == cudaSuccess && max_rows > 0) {
     e = cudaMalloc(&p->d_stat, static_cast<size_t>(max_rows) * sizeof(float2));
     if (e == cudaSuccess) e = cudaMalloc(&p->d_coef, static_cast<size_t>(max_rows) * sizeof(float));
   }
-  if (e != cudaSuccess) return fail(ADAMW_ENOMEM, "cudaMalloc(loss plan): %s", cudaGetErrorString(e));
+  if (e != cudaSuccess) return failed(e, "cudaMalloc(loss plan)", ADAMW_ENOMEM);
   if ((e = cudaMemset(p->d_partial, 0, sums)) != cudaSuccess ||
       (e = cudaStreamSynchronize(cudaStreamLegacy)) != cudaSuccess)
-    return cuda_fail(e, "clear the loss plan");
+    return failed(e, "clear the loss plan");
   *out = p.release();
   return ADAMW_OK;
 }
@@ -267,7 +275,7 @@ adamw_status adamw_token_logps(adamw_loss_plan* plan, const adamw_logits* z, flo
   if ((st = check_current_device(plan->device, "plan")) != ADAMW_OK || z->rows == 0) return st;
   cudaError_t e = launch_token_loss(static_cast<adamw_dtype>(z->dtype), kLossLogps, a,
                                     plan->limits, static_cast<cudaStream_t>(stream));
-  return e == cudaSuccess ? ADAMW_OK : cuda_fail(e, "launch token log-probabilities");
+  return e == cudaSuccess ? ADAMW_OK : failed(e, "launch token log-probabilities");
 }
 
 adamw_status adamw_policy_loss(adamw_loss_plan* plan, const adamw_logits* z, const adamw_policy* p,
@@ -300,7 +308,7 @@ adamw_status adamw_policy_loss(adamw_loss_plan* plan, const adamw_logits* z, con
   if ((st = check_current_device(plan->device, "plan")) != ADAMW_OK) return st;
   cudaError_t e = launch_token_loss(static_cast<adamw_dtype>(z->dtype), kLossPolicy, a,
                                     plan->limits, static_cast<cudaStream_t>(stream));
-  return e == cudaSuccess ? ADAMW_OK : cuda_fail(e, "launch policy loss");
+  return e == cudaSuccess ? ADAMW_OK : failed(e, "launch policy loss");
 }
 
 adamw_status adamw_preference_loss(adamw_loss_plan* plan, const adamw_logits* z,
@@ -336,7 +344,7 @@ adamw_status adamw_preference_loss(adamw_loss_plan* plan, const adamw_logits* z,
   if ((st = check_current_device(plan->device, "plan")) != ADAMW_OK) return st;
   cudaError_t e = launch_token_loss(static_cast<adamw_dtype>(z->dtype), kLossPrefer, a,
                                     plan->limits, static_cast<cudaStream_t>(stream));
-  return e == cudaSuccess ? ADAMW_OK : cuda_fail(e, "launch preference loss");
+  return e == cudaSuccess ? ADAMW_OK : failed(e, "launch preference loss");
 }
 
 // ---------------------------------------------------------------- layer norm
@@ -359,14 +367,13 @@ adamw_status adamw_layer_norm_plan_create(int32_t width, float eps, adamw_layer_
   p->eps = eps;
   const size_t n = 2 * static_cast<size_t>(norm_parts(width, sms)) * width * sizeof(float);
   cudaError_t e = prepare_layer_norm(width);
-  if (e != cudaSuccess) return cuda_fail(e, "prepare the layer norm kernels");
+  if (e != cudaSuccess) return failed(e, "prepare the layer norm kernels");
   e = cudaMalloc(&p->d_partial, n);
   if (e == cudaSuccess) e = cudaMalloc(&p->d_fault, sizeof(uint32_t));
-  if (e != cudaSuccess)
-    return fail(ADAMW_ENOMEM, "cudaMalloc(layer norm plan): %s", cudaGetErrorString(e));
+  if (e != cudaSuccess) return failed(e, "cudaMalloc(layer norm plan)", ADAMW_ENOMEM);
   if ((e = cudaMemset(p->d_fault, 0, sizeof(uint32_t))) != cudaSuccess ||
       (e = cudaStreamSynchronize(cudaStreamLegacy)) != cudaSuccess)
-    return cuda_fail(e, "clear the layer norm plan");
+    return failed(e, "clear the layer norm plan");
   *out = p.release();
   return ADAMW_OK;
 }
@@ -410,7 +417,7 @@ adamw_status adamw_layer_norm_forward(adamw_layer_norm_plan* plan, adamw_dtype d
   if ((st = check_current_device(plan->device, "plan")) != ADAMW_OK || rows == 0) return st;
   cudaError_t e = launch_layer_norm_forward(dtype, weight_dtype, a, plan->sms,
                                             static_cast<cudaStream_t>(stream));
-  return e == cudaSuccess ? ADAMW_OK : cuda_fail(e, "launch layer norm");
+  return e == cudaSuccess ? ADAMW_OK : failed(e, "launch layer norm");
 }
 
 adamw_status adamw_layer_norm_backward(adamw_layer_norm_plan* plan, adamw_dtype dtype,
@@ -443,7 +450,7 @@ adamw_status adamw_layer_norm_backward(adamw_layer_norm_plan* plan, adamw_dtype 
   if ((st = check_current_device(plan->device, "plan")) != ADAMW_OK) return st;
   cudaError_t e = launch_layer_norm_backward(dtype, weight_dtype, a, plan->sms,
                                              static_cast<cudaStream_t>(stream));
-  return e == cudaSuccess ? ADAMW_OK : cuda_fail(e, "launch layer norm backward");
+  return e == cudaSuccess ? ADAMW_OK : failed(e, "launch layer norm backward");
 }
 
 }  // extern "C"
