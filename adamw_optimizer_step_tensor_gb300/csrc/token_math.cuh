@@ -77,11 +77,6 @@ struct RowSum {
       c = hi;
     }
   }
-  __device__ __forceinline__ void join(float c2, float s2) {
-    const float hi = fmaxf(c, c2);
-    s = s * exp2_fast(c - hi) + s2 * exp2_fast(c2 - hi);
-    c = hi;
-  }
   // Over the warp, the same in every lane: the largest reference by an integer
   // reduction (floats in integer order), then the sums at that reference.
   __device__ __forceinline__ void join_lanes() {
