@@ -40,7 +40,8 @@ def test_many_rows_in_registers():
 
 
 @pytest.mark.parametrize("rows,width,dtype", [(1_300_001, 33, torch.float32), (400_003, 1001, torch.bfloat16),
-                                              (90_001, 4096, torch.bfloat16)])
+                                              (90_001, 4096, torch.bfloat16), (700_003, 1001, torch.bfloat16),
+                                              (180_001, 2050, torch.bfloat16)])
 def test_rows_of_several_launches(rows, width, dtype):
     """Odd rows, and in place; rows give the same bits in a call of their own that lies the same way."""
     g = torch.Generator(device="cuda").manual_seed(width)

@@ -20,7 +20,7 @@ def _captured(run):
 
 
 # one launch, a column kernel beside the rows', rows wider than registers, several launches
-@pytest.mark.parametrize("rows,width", [(700, 96), (700, 1601), (300, 4096), (200, 9001), (100, 20_003), (620_000, 5)])
+@pytest.mark.parametrize("rows,width", [(700, 96), (700, 1601), (300, 4096), (200, 9001), (100, 20_003), (620_000, 5), (1_300_000, 5)])
 def test_layer_norm(rows, width):
     x, dy = torch.empty(rows, width, device="cuda"), torch.empty(rows, width, device="cuda")
     w, b = torch.rand(width, device="cuda"), torch.rand(width, device="cuda")
