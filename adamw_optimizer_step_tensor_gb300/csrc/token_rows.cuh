@@ -93,6 +93,14 @@ __device__ __forceinline__ float far_word(const uint4& w, float m, float k, floa
     t += far_power(half_below(x[j].x, m), k, k_lo) + far_power(half_below(x[j].y, m), k, k_lo);
   return t;
 }
+constexpr int kFarLoads = 4;             // words on their way per thread
+template <typename T>
+__device__ __forceinline__ void far_load(const uint4* w, int i, int threads, int words,
+                                         uint4 (&v)[kFarLoads]) {
+#pragma unroll
+  for (int u = 0; u < kFarLoads; ++u)
+    v[u] = i + u * threads < words ? w[i + u * threads] : lowest_word<T>();
+}
 // Of the logits that thread `tid` of `threads` looks after, the largest (NaN
 // ignored), and the sum of 2^((z - m) k).
 template <typename T>
@@ -102,9 +110,10 @@ __device__ __forceinline__ float far_max(const T* z, int vocab, uint32_t rank, u
   const uint4* const w = reinterpret_cast<const uint4*>(share.base);
   float m = -INFINITY;
 #pragma unroll 1
-  for (int i = tid; i < share.words; i += threads) {
-    const uint4 v[1] = {w[i]};
-    m = fmaxf(m, words_max<T, 1>(v));
+  for (int i = tid; i < share.words; i += kFarLoads * threads) {
+    uint4 v[kFarLoads];
+    far_load<T>(w, i, threads, share.words, v);
+    m = fmaxf(m, words_max<T, kFarLoads>(v));
   }
   const int e = rank == 0 && tid < 16 ? ragged_element(share, vocab, tid) : -1;
   return e >= 0 ? fmaxf(m, to_f32(z[e])) : m;
@@ -117,7 +126,12 @@ __device__ __forceinline__ float far_sum(const T* z, int vocab, uint32_t rank, u
   m = fmaxf(m, -3.40282347e38f);        // -inf logits alone add nothing
   float s = 0.0f;
 #pragma unroll 1
-  for (int i = tid; i < share.words; i += threads) s += far_word<T>(w[i], m, k, k_lo);
+  for (int i = tid; i < share.words; i += kFarLoads * threads) {
+    uint4 v[kFarLoads];
+    far_load<T>(w, i, threads, share.words, v);
+#pragma unroll
+    for (int u = 0; u < kFarLoads; ++u) s += far_word<T>(v[u], m, k, k_lo);
+  }
   const int e = rank == 0 && tid < 16 ? ragged_element(share, vocab, tid) : -1;
   return e >= 0 ? s + far_power(half_below(to_f32(z[e]), m), k, k_lo) : s;
 }
