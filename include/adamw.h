@@ -545,8 +545,9 @@ adamw_status adamw_loss_plan_destroy(adamw_loss_plan* plan);
 /*
  * logps[t] = log softmax(logits[t] / temperature)[labels[t]] and, if lse is not
  * NULL, lse[t] = log sum exp(logits[t] / temperature); both 0 for rows without
- * a token.  -inf logits are entries of probability 0; a NaN or +inf logit, or a
- * row of -inf alone, makes the row's log-probability (and gradient) NaN.
+ * a token.  Any finite logits have the definition's numbers, masks of the type's
+ * lowest value too.  -inf logits are entries of probability 0; a NaN or +inf logit,
+ * or a row of -inf alone, makes the row's log-probability (and gradient) NaN.
  */
 adamw_status adamw_token_logps(adamw_loss_plan* plan, const adamw_logits* z, float* logps,
                                float* lse, void* stream);
