@@ -107,6 +107,13 @@ struct RingShared {
   uint32_t gave_up;
 };
 
+// A bounded wait of a whole warp, the same answer in every lane: lanes that each timed
+// their own could part at the limit, and those that went on would wait for the others
+// at the next shuffle.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
+  return __all_sync(kFull, mbar_wait(bar, parity));
+}
+
 // ---- scheduler
 
 // Lane `lane`'s input of a row.
@@ -241,7 +248,7 @@ __device__ void schedule(const LossArgs& a, RingShared& sh) {
       // with nothing left, one last row says so
       const DealtRow d = n == 0 ? DealtRow{0, kRowStop, 0} : sh.dealt[next + i];
       const uint32_t q = sent % kQueue;
-      if (sent >= kQueue && !mbar_wait(&sh.queue_empty[q], (sent / kQueue - 1) & 1u)) {
+      if (sent >= kQueue && !warp_wait(&sh.queue_empty[q], (sent / kQueue - 1) & 1u)) {
         atomicOr(&sh.gave_up, 1u);
         return;
       }
@@ -261,8 +268,11 @@ __device__ void schedule(const LossArgs& a, RingShared& sh) {
 // ---- loader and storer
 
 // Waits for the next row of the queue; false if the wait gave up.
+template <bool WARP = true>
 __device__ __forceinline__ bool take_row(RingShared& sh, uint32_t n, uint32_t site) {
-  if (mbar_wait(&sh.queue_full[n % kQueue], (n / kQueue) & 1u)) return true;
+  uint64_t* const bar = &sh.queue_full[n % kQueue];
+  const uint32_t parity = (n / kQueue) & 1u;
+  if (WARP ? warp_wait(bar, parity) : mbar_wait(bar, parity)) return true;
   atomicOr(&sh.gave_up, site);
   return false;
 }
@@ -273,7 +283,7 @@ __device__ void load_rows(const LossArgs& a, RingShared& sh) {
   const uint32_t rank = cluster_rank(), ranks = cluster_size();
   uint32_t use = 0;
   bool ok = true;
-  for (uint32_t n = 0; ok && take_row(sh, n, 2u); ++n) {
+  for (uint32_t n = 0; ok && take_row<false>(sh, n, 2u); ++n) {
     const int64_t row = sh.queue[n % kQueue].row;
     const int kind = sh.queue[n % kQueue].kind;
     mbar_arrive(&sh.queue_empty[n % kQueue]);
@@ -371,7 +381,7 @@ __device__ void sum_rows(const LossArgs& a, RingShared& sh, int warp) {
       for (int j = 0; j < share.pieces; ++j, ++use) {
         if (use % kTeams != team) continue;
         const uint32_t slot = use % kSlots;
-        if (!mbar_wait(&sh.full[slot], (use / kSlots) & 1u)) {
+        if (!warp_wait(&sh.full[slot], (use / kSlots) & 1u)) {
           atomicOr(&sh.gave_up, 8u);
           return;
         }
@@ -423,7 +433,7 @@ __device__ __forceinline__ bool exchange(RingShared& sh, RowSum& x, uint32_t joi
     cluster_store2(cluster_map(&sh.cross[b][rank], lane), x.c, x.s);
     cluster_arrive(cluster_map(&sh.joined[b], lane));
   }
-  if (!mbar_wait_cluster(&sh.joined[b], (join / kJoins) & 1u)) {
+  if (!__all_sync(kFull, mbar_wait_cluster(&sh.joined[b], (join / kJoins) & 1u))) {
     atomicOr(&sh.gave_up, 64u);
     return false;
   }
@@ -465,7 +475,7 @@ __device__ void finish_rows(const LossArgs& a, RingShared& sh, double (&acc)[4])
     if (q.kind == kRowStop) return;
     const int e = n % kQueue;
     if (q.kind == kRowLive) {
-      if (!mbar_wait(&sh.summed[e], (n / kQueue) & 1u)) {
+      if (!warp_wait(&sh.summed[e], (n / kQueue) & 1u)) {
         atomicOr(&sh.gave_up, 32u);
         return;
       }
@@ -541,7 +551,7 @@ __device__ __forceinline__ bool far_pieces(const LossArgs& a, RingShared& sh, ui
   for (int j = 0; j < share.pieces; ++j, ++use) {
     if (use % kTeams != team) continue;
     const uint32_t slot = use % kSlots;
-    if (!sums(PASS) && !mbar_wait(&sh.full[slot], (use / kSlots) & 1u)) {
+    if (!sums(PASS) && !warp_wait(&sh.full[slot], (use / kSlots) & 1u)) {
       atomicOr(&sh.gave_up, 8u);
       return false;
     }
@@ -586,7 +596,7 @@ __device__ void grad_rows(const LossArgs& a, RingShared& sh, int warp, bool bulk
     if (q.kind == kRowStop) return;
     const int e = n % kQueue;
     T* const dz = static_cast<T*>(a.dlogits) + q.row * a.dstride;
-    if (sums(PASS) && !mbar_wait(&sh.ready[e], (n / kQueue) & 1u)) {
+    if (sums(PASS) && !warp_wait(&sh.ready[e], (n / kQueue) & 1u)) {
       atomicOr(&sh.gave_up, 256u);
       return;
     }
@@ -622,7 +632,7 @@ __device__ void grad_rows(const LossArgs& a, RingShared& sh, int warp, bool bulk
     for (int j = 0; j < share.pieces; ++j, ++use) {
       if (use % kTeams != team) continue;
       const uint32_t slot = use % kSlots;
-      if (!sums(PASS) && !mbar_wait(&sh.full[slot], (use / kSlots) & 1u)) {
+      if (!sums(PASS) && !warp_wait(&sh.full[slot], (use / kSlots) & 1u)) {
         atomicOr(&sh.gave_up, 8u);
         return;
       }
