@@ -7,7 +7,9 @@ and keeps the tensors alive for the plan's lifetime.  Every step of the
 update runs in the library's CUDA kernels; there is no CPU fallback -- if the
 library is missing, importing ``_capi``'s functions raises.
 ``FusedTokenLoss`` and ``FusedLayerNorm`` (operators.py) are the losses and the
-layer norm whose gradients the step consumes.
+layer norm whose gradients the step consumes; ``FusedDropout``, ``FusedRouter`` and
+``FusedGroupNorm`` (block_operators.py) are a block's other operators between its
+matrix products.
 """
 
 from __future__ import annotations
@@ -25,7 +27,9 @@ from ._capi import (  # noqa: F401
     adamw_loss_plan_destroy, adamw_loss_plan_status, adamw_token_logps, adamw_policy_loss, adamw_preference_loss,
     adamw_layer_norm_plan_create, adamw_layer_norm_plan_destroy, adamw_layer_norm_plan_status, adamw_layer_norm_plan_set_wait_limit,
     adamw_layer_norm_forward,
-    adamw_layer_norm_backward,
+    adamw_layer_norm_backward, adamw_dropout, adamw_router_plan_create, adamw_router_plan_destroy, adamw_route,
+    adamw_route_backward, adamw_route_balance, adamw_route_dispatch, adamw_route_combine, adamw_route_combine_backward,
+    adamw_group_norm_plan_create, adamw_group_norm_plan_destroy, adamw_group_norm_forward, adamw_group_norm_backward,
 )
 
 MODES = {"fp32": _capi.MODE_FP32, "bf16_rem": _capi.MODE_BF16_REM, "q8": _capi.MODE_Q8,
@@ -213,4 +217,7 @@ def __getattr__(name):
     if name in ("FusedTokenLoss", "FusedLayerNorm"):
         from . import operators
         return getattr(operators, name)
+    if name in ("FusedDropout", "FusedRouter", "FusedGroupNorm"):
+        from . import block_operators
+        return getattr(block_operators, name)
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -85,7 +85,49 @@ class adamw_preference(ctypes.Structure):
     ]
 
 
+class adamw_router(ctypes.Structure):
+    _fields_ = [
+        ("experts", ctypes.c_int32),
+        ("top_k", ctypes.c_int32),
+        ("groups", ctypes.c_int32),
+        ("top_groups", ctypes.c_int32),
+        ("score", ctypes.c_int32),
+        ("group_score", ctypes.c_int32),
+        ("renormalise", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+    ]
+
+
+class adamw_channels_last(ctypes.Structure):
+    _fields_ = [
+        ("data", _vp),
+        ("sample_stride", ctypes.c_int64),
+        ("position_stride", ctypes.c_int64),
+    ]
+
+
+_i32, _i64, _f = ctypes.c_int32, ctypes.c_int64, ctypes.c_float
 _SIGNATURES = {
+    "adamw_dropout": (ctypes.c_int, [ctypes.c_int, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _f, ctypes.c_uint64,
+                                     _vp, ctypes.c_uint32, _vp]),
+    "adamw_router_plan_create": (ctypes.c_int, [ctypes.POINTER(adamw_router), _i64, ctypes.POINTER(_vp)]),
+    "adamw_router_plan_destroy": (ctypes.c_int, [_vp]),
+    "adamw_route": (ctypes.c_int, [_vp, ctypes.c_int, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "adamw_route_backward": (ctypes.c_int, [_vp, ctypes.c_int, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _vp]),
+    "adamw_route_balance": (ctypes.c_int, [_vp, _vp, _f, _vp, _vp]),
+    "adamw_route_dispatch": (ctypes.c_int, [_vp, ctypes.c_int, _i64, _i64, _vp, _i64, _vp, _vp, _i64, _i64, _vp]),
+    "adamw_route_combine": (ctypes.c_int, [_vp, ctypes.c_int, _i64, _i64, _vp, _i64, _i64, _vp, _vp, _vp, _i64, _vp]),
+    "adamw_route_combine_backward": (ctypes.c_int, [_vp, ctypes.c_int, _i64, _i64, _vp, _i64, _vp, _i64, _i64, _vp,
+                                                    _vp, _vp, _i64, _vp, _vp]),
+    "adamw_group_norm_plan_create": (ctypes.c_int, [_i32, _i32, _i64, _f, ctypes.c_int, ctypes.POINTER(_vp)]),
+    "adamw_group_norm_plan_destroy": (ctypes.c_int, [_vp]),
+    "adamw_group_norm_forward": (ctypes.c_int, [_vp, ctypes.c_int, ctypes.c_int, _i64, _i64,
+                                                ctypes.POINTER(adamw_channels_last), _vp, _vp,
+                                                ctypes.POINTER(adamw_channels_last), _vp, _vp, _vp]),
+    "adamw_group_norm_backward": (ctypes.c_int, [_vp, ctypes.c_int, ctypes.c_int, _i64, _i64,
+                                                 ctypes.POINTER(adamw_channels_last),
+                                                 ctypes.POINTER(adamw_channels_last), _vp, _vp, _vp, _vp,
+                                                 ctypes.POINTER(adamw_channels_last), _vp, _vp, _vp]),
     "adamw_grad_norm": (ctypes.c_int, [_vp, ctypes.c_float, _vp, _vp, _vp, _vp, _vp]),
     "adamw_clip_grads": (ctypes.c_int, [_vp, _vp, _vp]),
     "adamw_loss_plan_create": (ctypes.c_int, [ctypes.c_int64, ctypes.c_int32, ctypes.POINTER(_vp)]),
@@ -429,3 +471,78 @@ def adamw_layer_norm_backward(plan: int, dtype: int, weight_dtype: int, rows: in
                               dbias: int | None, stream: int | None) -> None:
     _check(load().adamw_layer_norm_backward(plan, dtype, weight_dtype, rows, dy, dy_stride, x, x_stride,
                                             weight, mean, rstd, dx, dx_stride, dweight, dbias, stream))
+
+
+def adamw_dropout(dtype: int, rows: int, width: int, x: int, x_stride: int, residual: int | None,
+                  residual_stride: int, y: int, y_stride: int, p: float, seed: int, step_dev: int | None, site: int,
+                  stream: int | None) -> None:
+    _check(load().adamw_dropout(dtype, rows, width, x, x_stride, residual, residual_stride, y, y_stride, p, seed,
+                                step_dev, site, stream))
+
+
+def adamw_router_plan_create(router: adamw_router, max_tokens: int) -> int:
+    out = _vp()
+    _check(load().adamw_router_plan_create(router, max_tokens, ctypes.byref(out)))
+    return out.value
+
+
+def adamw_router_plan_destroy(plan: int) -> None:
+    _check(load().adamw_router_plan_destroy(plan))
+
+
+def adamw_route(plan: int, dtype: int, tokens: int, logits: int, row_stride: int, bias: int | None, weights: int,
+                ids: int, slots: int | None, starts: int | None, stream: int | None) -> None:
+    _check(load().adamw_route(plan, dtype, tokens, logits, row_stride, bias, weights, ids, slots, starts, stream))
+
+
+def adamw_route_backward(plan: int, dtype: int, tokens: int, logits: int, row_stride: int, ids: int, dweights: int,
+                         dlogits: int, dlogits_stride: int, stream: int | None) -> None:
+    _check(load().adamw_route_backward(plan, dtype, tokens, logits, row_stride, ids, dweights, dlogits, dlogits_stride,
+                                       stream))
+
+
+def adamw_route_balance(plan: int, starts: int, rate: float, bias: int, stream: int | None) -> None:
+    _check(load().adamw_route_balance(plan, starts, rate, bias, stream))
+
+
+def adamw_route_dispatch(plan: int, dtype: int, tokens: int, width: int, x: int, x_stride: int, slots: int, xs: int,
+                         xs_rows: int, xs_stride: int, stream: int | None) -> None:
+    _check(load().adamw_route_dispatch(plan, dtype, tokens, width, x, x_stride, slots, xs, xs_rows, xs_stride, stream))
+
+
+def adamw_route_combine(plan: int, dtype: int, tokens: int, width: int, ys: int, ys_rows: int, ys_stride: int,
+                        slots: int, weights: int | None, y: int, y_stride: int, stream: int | None) -> None:
+    _check(load().adamw_route_combine(plan, dtype, tokens, width, ys, ys_rows, ys_stride, slots, weights, y, y_stride,
+                                      stream))
+
+
+def adamw_route_combine_backward(plan: int, dtype: int, tokens: int, width: int, dy: int, dy_stride: int, ys: int,
+                                 ys_rows: int, ys_stride: int, slots: int, weights: int, dys: int, dys_stride: int,
+                                 dweights: int, stream: int | None) -> None:
+    _check(load().adamw_route_combine_backward(plan, dtype, tokens, width, dy, dy_stride, ys, ys_rows, ys_stride, slots,
+                                               weights, dys, dys_stride, dweights, stream))
+
+
+def adamw_group_norm_plan_create(channels: int, groups: int, max_samples: int, eps: float, activation: int) -> int:
+    out = _vp()
+    _check(load().adamw_group_norm_plan_create(channels, groups, max_samples, eps, activation, ctypes.byref(out)))
+    return out.value
+
+
+def adamw_group_norm_plan_destroy(plan: int) -> None:
+    _check(load().adamw_group_norm_plan_destroy(plan))
+
+
+def adamw_group_norm_forward(plan: int, dtype: int, weight_dtype: int, samples: int, positions: int,
+                             x: adamw_channels_last, weight: int | None, bias: int | None, y: adamw_channels_last,
+                             mean: int, rstd: int, stream: int | None) -> None:
+    _check(load().adamw_group_norm_forward(plan, dtype, weight_dtype, samples, positions, x, weight, bias, y, mean,
+                                           rstd, stream))
+
+
+def adamw_group_norm_backward(plan: int, dtype: int, weight_dtype: int, samples: int, positions: int,
+                              dy: adamw_channels_last, x: adamw_channels_last, weight: int | None, bias: int | None,
+                              mean: int, rstd: int, dx: adamw_channels_last, dweight: int | None, dbias: int | None,
+                              stream: int | None) -> None:
+    _check(load().adamw_group_norm_backward(plan, dtype, weight_dtype, samples, positions, dy, x, weight, bias, mean,
+                                            rstd, dx, dweight, dbias, stream))

@@ -1,0 +1,105 @@
+// block_ops.h -- launch arguments of a block's operators between its matrix
+// products: dropout, routing to experts and the experts' rows, group norm.
+#pragma once
+
+#include <cstdint>
+
+#include "internal.h"
+
+namespace adamw {
+
+// ---- dropout (dropout.cu)
+struct DropoutArgs {
+  const void* x;
+  const void* residual;        // may be null
+  void* y;
+  int64_t rows, width, x_stride, r_stride, y_stride;
+  uint32_t threshold;          // words below it are dropped
+  uint32_t some;               // 0: everything is dropped (p = 1)
+  float scale;                 // 1 / (1 - p)
+  uint32_t site;
+  uint32_t key[20];            // the ten rounds' keys, low word first
+  const int32_t* step;         // may be null
+};
+cudaError_t launch_dropout(adamw_dtype dt, const DropoutArgs& a, cudaStream_t s);
+
+// ---- routing (router.cu)
+constexpr int kMaxExperts = 1024;
+constexpr int kMaxTopK = 32;
+constexpr int kMaxGroups = 32;
+
+struct RouteArgs {
+  adamw_router router;
+  const void* logits;
+  int64_t stride;
+  int32_t tokens;
+  const float* bias;           // may be null
+  float* weights;
+  int32_t* ids;
+  int32_t* slots;              // null: no places
+  int32_t* starts;             // null: no places
+  const float* dweights;       // backward
+  void* dlogits;               // backward
+  int64_t dstride;
+  int32_t* counts;             // plan-owned: [chunks][experts]
+  int32_t chunks;              // CTAs that share the tokens, in their order
+  int32_t per_chunk;           // tokens of a chunk
+};
+// Chunks of a plan at most: its table of counts has as many rows.
+int router_chunks(int sms);
+cudaError_t prepare_router(const adamw_router& router);
+cudaError_t launch_route(adamw_dtype dt, RouteArgs a, int sms, cudaStream_t s);
+cudaError_t launch_route_backward(adamw_dtype dt, const RouteArgs& a, int sms, cudaStream_t s);
+cudaError_t launch_route_balance(const int32_t* starts, int32_t experts, float rate, float* bias,
+                                 cudaStream_t s);
+
+// ---- experts' rows (expert_rows.cu)
+struct ExpertRowsArgs {
+  const void* x;               // dispatch: x; combine backward: dy.  [tokens][width]
+  int64_t x_stride;
+  const void* ys;              // combine, combine backward.  [n_rows][width]
+  int64_t ys_stride;
+  void* y;                     // combine: y [tokens]; dispatch: xs, combine backward: dys [n_rows]
+  int64_t y_stride;
+  const int32_t* slots;
+  const float* weights;        // may be null (combine)
+  float* dweights;
+  int64_t tokens, width, n_rows;
+  int32_t top_k;
+};
+cudaError_t launch_dispatch(adamw_dtype dt, const ExpertRowsArgs& a, int sms, cudaStream_t s);
+cudaError_t launch_combine(adamw_dtype dt, const ExpertRowsArgs& a, int sms, cudaStream_t s);
+cudaError_t launch_combine_backward(adamw_dtype dt, const ExpertRowsArgs& a, int sms,
+                                    cudaStream_t s);
+
+// ---- group norm (group_norm.cu)
+struct GroupNormArgs {
+  const void* x;
+  const void* dy;              // backward
+  const void* weight;          // null: 1
+  const void* bias;            // null: 0
+  void* out;                   // y or dx
+  int64_t x_sample, x_position, dy_sample, dy_position, out_sample, out_position;
+  float* mean;
+  float* rstd;
+  void* dweight;               // may be null
+  void* dbias;                 // may be null
+  int64_t samples, positions;
+  int32_t channels, groups;
+  float eps;
+  int32_t silu;
+  float* stats;                // plan-owned: partial statistics of samples' parts
+  float* columns;              // plan-owned: partial column sums [2][parts][channels]
+  int32_t parts;               // parts of a sample
+};
+struct GroupNormSpace {
+  int64_t stats, columns;      // floats
+};
+GroupNormSpace group_norm_space(int32_t channels, int32_t groups, int64_t max_samples, int sms);
+cudaError_t prepare_group_norm();
+cudaError_t launch_group_norm_forward(adamw_dtype dt, adamw_dtype wdt, GroupNormArgs a, int sms,
+                                      cudaStream_t s);
+cudaError_t launch_group_norm_backward(adamw_dtype dt, adamw_dtype wdt, GroupNormArgs a, int sms,
+                                       cudaStream_t s);
+
+}  // namespace adamw

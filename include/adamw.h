@@ -645,6 +645,183 @@ adamw_status adamw_layer_norm_backward(adamw_layer_norm_plan* plan, adamw_dtype 
                                        void* dx, int64_t dx_stride, void* dweight, void* dbias,
                                        void* stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * A block's operators between its matrix products, beside layer norm: dropout
+ * with the add of the residual stream, routing to experts with the rows' way
+ * there and back, and group norm with an activation.  The conventions above hold.
+ * ---------------------------------------------------------------------------
+ */
+
+/*
+ * Dropout whose mask is computed, never stored.  Over rows x width elements:
+ *     y = residual + (kept ? x / (1 - p) : 0)
+ * Element i = row * width + column is dropped where word i % 4 of Philox4x32-10
+ * (Salmon, Moraes, Dror, Shaw, "Parallel random numbers: as easy as 1, 2, 3", 2011)
+ * at counter (i / 4 low, i / 4 high, *step_dev, site) under the key `seed` (low half
+ * first) is less than p 2^32, rounded to a whole number.  The mask depends on nothing
+ * else: not on strides, alignment or the type.  The backward pass is the same call on
+ * the gradient without a residual: dx = kept ? dy / (1 - p) : 0, and the residual's
+ * gradient is dy itself.  step_dev (NULL: 0) is read on the device when the work runs:
+ * with the step counter of adamw_step, each replay of a captured training step draws
+ * another mask, and the forward and backward pass of one step draw the same.  `site`
+ * tells the dropouts of one model apart.
+ * p in [0, 1]; a dropped element's x is not used, NaN or infinite as it may be.  x,
+ * residual (NULL: none) and y of one dtype, row strides in elements, >= width; y may be
+ * x or residual (same stride).  The sum is float32 and rounded once.
+ */
+adamw_status adamw_dropout(adamw_dtype dtype, int64_t rows, int64_t width, const void* x,
+                           int64_t x_stride, const void* residual, int64_t residual_stride, void* y,
+                           int64_t y_stride, float p, uint64_t seed, const int32_t* step_dev,
+                           uint32_t site, void* stream);
+
+typedef enum { ADAMW_SCORE_SOFTMAX = 0, ADAMW_SCORE_SIGMOID = 1 } adamw_score;
+typedef enum { ADAMW_GROUP_MAX = 0, ADAMW_GROUP_TOP2 = 1 } adamw_group_score;
+
+/* How tokens are routed. */
+typedef struct {
+  int32_t experts;       /* 1 .. 1024 (EUNSUPPORTED above)                            */
+  int32_t top_k;         /* experts per token: 1 .. 32 (EUNSUPPORTED above), at most
+                            top_groups * experts / groups                             */
+  int32_t groups;        /* divides experts; 1 .. 32 (EUNSUPPORTED above); 1: no groups */
+  int32_t top_groups;    /* 1 .. groups: a token's experts are of that many groups      */
+  int32_t score;         /* adamw_score                                                */
+  int32_t group_score;   /* adamw_group_score                                          */
+  int32_t renormalise;   /* nonzero: a token's weights sum to scale                     */
+  float scale;           /* > 0                                                        */
+} adamw_router;
+
+/* Workspace of the routing of up to max_tokens tokens (max_tokens * top_k < 2^31,
+ * EUNSUPPORTED above).  Synchronous.  Calls on one plan must not overlap one another. */
+typedef struct adamw_router_plan adamw_router_plan;
+adamw_status adamw_router_plan_create(const adamw_router* router, int64_t max_tokens,
+                                      adamw_router_plan** out);
+/* Frees a router plan (NULL is allowed).  Synchronises with the device first. */
+adamw_status adamw_router_plan_destroy(adamw_router_plan* plan);
+
+/*
+ * Routes each token by its row of logits z (float32, float16 or bfloat16 [tokens][experts]):
+ *     s = softmax(z) or sigmoid(z),   key = s + bias
+ *     a group's score = its largest key, or the sum of its two largest
+ *     ids = the top_k largest keys of the top_groups best groups, largest first
+ *     weights = scale * s[ids], or scale * s[ids] / sum of s[ids] (renormalise)
+ * Equal keys and groups go to the lowest index; keys are compared as 64-bit values, and
+ * without a bias (or with one of zeros) in the order of the logits.
+ * bias float32 [experts] (NULL: 0) takes part in the choice alone.  An expert whose logit
+ * or bias is -inf (or whose bias is NaN) is not there for the token: where fewer than
+ * top_k are, the rest of ids and slots is -1 and of weights 0; a row of -inf alone (a
+ * padded token) goes nowhere.  Any finite logits have the definition's weights.  A NaN
+ * logit, or a +inf one under softmax, makes the row's weights NaN; its experts are then
+ * those of its largest logits that are numbers, whatever the bias.
+ *     starts[e] = number of assignments to experts before e; starts[experts] = all
+ *     slots[t][j] = place of token t's j-th assignment when all are ordered by expert,
+ *                   and by token within an expert
+ * weights float32, ids and slots int32 [tokens][top_k], starts int32 [experts + 1]; slots
+ * and starts may both be NULL.
+ */
+adamw_status adamw_route(adamw_router_plan* plan, adamw_dtype dtype, int64_t tokens,
+                         const void* logits, int64_t row_stride, const float* bias, float* weights,
+                         int32_t* ids, int32_t* slots, int32_t* starts, void* stream);
+
+/*
+ * dlogits = the gradient of the logits from that of the weights (float32
+ * [tokens][top_k]), every entry of every row, rounded once to the logits' type; the choice
+ * of experts and the bias have none.  ids as adamw_route wrote them (-1, and what lies
+ * outside [0, experts), has no weight).  dlogits may be the logits (same stride).
+ */
+adamw_status adamw_route_backward(adamw_router_plan* plan, adamw_dtype dtype, int64_t tokens,
+                                  const void* logits, int64_t row_stride, const int32_t* ids,
+                                  const float* dweights, void* dlogits, int64_t dlogits_stride,
+                                  void* stream);
+
+/*
+ * Steps the bias against the load: bias[e] += rate * sign(mean - load[e]), where load[e] =
+ * starts[e + 1] - starts[e] (the sums of several calls' starts do as well).
+ */
+adamw_status adamw_route_balance(adamw_router_plan* plan, const int32_t* starts, float rate,
+                                 float* bias, void* stream);
+
+/*
+ * Rows to the experts: xs[slots[t][j]] = x[t].  A slot outside [0, xs_rows) is passed
+ * over; rows of xs that no slot names are left as they were.  Row strides in elements.
+ */
+adamw_status adamw_route_dispatch(adamw_router_plan* plan, adamw_dtype dtype, int64_t tokens,
+                                  int64_t width, const void* x, int64_t x_stride,
+                                  const int32_t* slots, void* xs, int64_t xs_rows,
+                                  int64_t xs_stride, void* stream);
+
+/*
+ * Rows back from the experts: y[t] = sum over j of weights[t][j] * ys[slots[t][j]], in
+ * float32, rounded once.  weights NULL: 1 (the backward pass of the dispatch).  A slot
+ * outside [0, ys_rows) adds nothing.
+ */
+adamw_status adamw_route_combine(adamw_router_plan* plan, adamw_dtype dtype, int64_t tokens,
+                                 int64_t width, const void* ys, int64_t ys_rows,
+                                 int64_t ys_stride, const int32_t* slots, const float* weights,
+                                 void* y, int64_t y_stride, void* stream);
+
+/*
+ * dys[slots[t][j]] = weights[t][j] * dy[t],  dweights[t][j] = <dy[t], ys[slots[t][j]]> (0
+ * without a slot).  dys has ys_rows rows, and may be ys (same stride); rows that no slot
+ * names are left as they were.
+ */
+adamw_status adamw_route_combine_backward(adamw_router_plan* plan, adamw_dtype dtype,
+                                          int64_t tokens, int64_t width, const void* dy,
+                                          int64_t dy_stride, const void* ys, int64_t ys_rows,
+                                          int64_t ys_stride, const int32_t* slots,
+                                          const float* weights, void* dys, int64_t dys_stride,
+                                          float* dweights, void* stream);
+
+typedef enum { ADAMW_ACT_NONE = 0, ADAMW_ACT_SILU = 1 } adamw_activation;
+
+/* Workspace of group norm over `channels` (1 .. 2^20, EUNSUPPORTED above) channels in
+ * `groups` (divides channels) groups, for up to max_samples samples.  Synchronous.  eps
+ * finite and >= 0.  Calls on one plan must not overlap one another. */
+typedef struct adamw_group_norm_plan adamw_group_norm_plan;
+adamw_status adamw_group_norm_plan_create(int32_t channels, int32_t groups, int64_t max_samples,
+                                          float eps, adamw_activation activation,
+                                          adamw_group_norm_plan** out);
+/* Frees a group norm plan (NULL is allowed).  Synchronises with the device first. */
+adamw_status adamw_group_norm_plan_destroy(adamw_group_norm_plan* plan);
+
+/* A channels-last tensor [samples][positions][channels]: the channels contiguous, the
+ * other strides in elements. */
+typedef struct {
+  const void* data;
+  int64_t sample_stride;
+  int64_t position_stride;   /* >= channels */
+} adamw_channels_last;
+
+/*
+ * Per sample and group, over positions x channels / groups elements:
+ *     xhat = (x - mean) rstd,  rstd = 1 / sqrt(var + eps)
+ *     z = xhat weight + bias,  y = z or z sigmoid(z)
+ * weight and bias [channels], float32 or of the elements' dtype (EUNSUPPORTED
+ * otherwise), may be NULL (1 and 0).  mean, rstd: float32 [samples][groups].  positions
+ * >= 1.  y may be x (same strides).
+ */
+adamw_status adamw_group_norm_forward(adamw_group_norm_plan* plan, adamw_dtype dtype,
+                                      adamw_dtype weight_dtype, int64_t samples, int64_t positions,
+                                      const adamw_channels_last* x, const void* weight,
+                                      const void* bias, const adamw_channels_last* y, float* mean,
+                                      float* rstd, void* stream);
+
+/*
+ * With dz = dy times the activation's slope at z, and means over the group:
+ *     dx = rstd (w dz - mean(w dz) - xhat mean(w dz xhat))
+ *     dweight = sum over samples and positions of dz xhat,  dbias = that of dz
+ * from the forward pass's mean and rstd.  dweight and dbias are of the weight's dtype (a
+ * NULL weight's and bias's: weight_dtype), written (not added to), and may be NULL.  dx may
+ * be dy or x (same strides).
+ */
+adamw_status adamw_group_norm_backward(adamw_group_norm_plan* plan, adamw_dtype dtype,
+                                       adamw_dtype weight_dtype, int64_t samples,
+                                       int64_t positions, const adamw_channels_last* dy,
+                                       const adamw_channels_last* x, const void* weight,
+                                       const void* bias, const float* mean, const float* rstd,
+                                       const adamw_channels_last* dx, void* dweight, void* dbias,
+                                       void* stream);
+
 /* Message for the calling thread's last non-OK status ("" if none). */
 const char* adamw_last_error(void);
 

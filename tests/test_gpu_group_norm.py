@@ -1,0 +1,205 @@
+"""GPU: group norm with an activation against the float64 definition.
+
+Tolerances (u = 2^-24).  The mean is off by a few u of the largest value's distance from the
+first one and of itself; rstd by the spread's error: a run of n <= 64 values loses at most 2 n u
+of it, joins by counts a few u: 160 u.  xhat then is off by under 200 u (1 + |xhat|) + 4 u
+|mean| rstd: 2^-16 (1 + |xhat|) while |mean| rstd < 10.  The activation's slope is below 1.1 and
+its fast exponential off by (|z| + 4) u: 2^-15 of (1 + |z|) covers both.  A group's or a column's
+sum of n terms, over runs, threads and CTAs, is off by at most 400 u of its magnitudes (the
+longest chain of additions here) plus the terms' own 2^-15: 2^-14.  16-bit outputs add half a
+step.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+from adamw_optimizer_step_tensor_gb300 import AdamWError, FusedGroupNorm
+from oracle import group_norm as GN
+
+from _support import assert_guards_intact, empty, guarded_empty
+
+pytestmark = pytest.mark.gpu
+HALF = {torch.float32: 2.0 ** -24, torch.float16: 2.0 ** -11, torch.bfloat16: 2.0 ** -8}
+TINY = {torch.float32: 2.0 ** -126, torch.float16: 2.0 ** -24, torch.bfloat16: 2.0 ** -126}
+DTYPES = [torch.float32, torch.float16, torch.bfloat16]
+
+
+def wide(t):
+    return t.detach().double().cpu().numpy()
+
+
+def tensor_of(a, dtype, pad=0, shift=0, swap=False):
+    """A guarded device tensor of a's values: `pad` elements behind each position's channels; samples inside
+    positions with `swap`."""
+    n, length, c = a.shape
+    t = guarded_empty(n * length * (c + pad), dtype, shift)
+    t = t.view(length, n, c + pad).transpose(0, 1) if swap else t.view(n, length, c + pad)
+    t.fill_(7.0)
+    t = t[:, :, :c]
+    t.copy_(torch.from_numpy(a.astype(np.float32)))
+    return t
+
+
+def vec_of(a, dtype):
+    t = empty(a.size, dtype)
+    t.copy_(torch.from_numpy(a.astype(np.float32)))
+    return t
+
+
+def near(got, want, size, rel, dtype):
+    err = np.abs(wide(got) - want)
+    bound = rel * size + HALF[dtype] * (np.abs(want) + rel * size) + TINY[dtype]
+    assert (err <= bound).all(), (float((err - bound).max()), float(err.max()))
+
+
+def check(shape, groups, dtype=torch.float32, wdtype=torch.float32, silu=False, pad=0, shift=0, swap=False, offset=0.5, none=False):
+    n, length, c = shape
+    rng = np.random.default_rng(n * 7 + length * 3 + c)
+    x = tensor_of(rng.normal(offset, 1.5, shape) * (1 + 0.3 * np.arange(c) / c), dtype, pad, shift, swap)
+    dy = tensor_of(rng.normal(0, 1, shape), dtype, pad, shift, swap)
+    w = None if none else vec_of(rng.normal(1, 0.2, c), wdtype)
+    b = None if none else vec_of(rng.normal(0, 0.2, c), wdtype)
+    y, dx = (tensor_of(np.zeros(shape), dtype, pad, shift, swap) for _ in range(2))
+    odt = dtype if none else wdtype
+    dw, db = empty(c, odt), empty(c, odt)
+    mean, rstd = (empty(n * groups).view(n, groups) for _ in range(2))
+    norm = FusedGroupNorm(c, groups, n, activation="silu" if silu else "none")
+    norm.forward(x, w, b, y=y, mean=mean, rstd=rstd)
+    norm.backward(dy, x, w, b, mean, rstd, dx=dx, dweight=dw, dbias=db)
+    assert_guards_intact()
+    xx, ww, bb = wide(x), None if none else wide(w), None if none else wide(b)
+    want, m, r = GN.forward(xx, groups, ww, bb, silu=silu)
+    span = np.abs(xx.reshape(n, length, groups, -1)).max((1, 3))
+    assert (np.abs(wide(mean) - m) <= 2.0 ** -20 * span).all()
+    assert (np.abs(wide(rstd) - r) <= 2.0 ** -16 * r).all()
+    xhat = GN.forward(xx, groups)[0]
+    wabs = 1 if none else np.abs(ww)
+    z = np.abs(xhat * (1 if none else ww)) + (0 if none else np.abs(bb))
+    size = wabs * (1 + np.abs(xhat)) + z
+    near(y, want, size, 2.0 ** -15, dtype)
+    mm, rr = wide(mean), wide(rstd)
+    gx, gw, gb = GN.backward(wide(dy), xx, groups, ww, bb, mm, rr, silu)
+    term = np.abs(wide(dy)) * 1.1 * (2 + z) * (1 + np.abs(xhat))      # of dz and dz xhat
+    spread = lambda t: np.repeat(t.reshape(n, length, groups, -1).mean((1, 3)), c // groups, 1)[:, None, :]  # noqa: E731
+    size = np.repeat(rr, c // groups, 1)[:, None, :] * (term * wabs + spread(term * wabs) * (1 + np.abs(xhat)))
+    near(dx, gx, size, 2.0 ** -14, dtype)
+    near(dw, gw, term.sum((0, 1)), 2.0 ** -14, odt)
+    near(db, gb, term.sum((0, 1)), 2.0 ** -14, odt)
+    return norm, x, w, b, y, mean, rstd
+
+
+SHAPES = [((1, 1, 1), 1), ((2, 3, 4), 2), ((3, 1, 64), 8), ((1, 257, 8), 1), ((2, 100, 40), 5), ((5, 33, 96), 32), ((2, 70, 330), 30),
+          ((1, 1000, 128), 4), ((3, 17, 2056), 8), ((2, 9, 5000), 10), ((300, 1, 512), 16), ((40, 2, 264), 33), ((1, 5, 20_000), 1),
+          ((2, 4096, 32), 32), ((7, 64, 7), 7), ((2, 3, 600), 2)]
+
+
+@pytest.mark.parametrize("dtype,wdtype", [(torch.float32, torch.float32), (torch.float16, torch.float32), (torch.float16, torch.float16),
+                                          (torch.bfloat16, torch.float32), (torch.bfloat16, torch.bfloat16)])
+@pytest.mark.parametrize("shape,groups", SHAPES)
+def test_matches_the_definition(shape, groups, dtype, wdtype):
+    check(shape, groups, dtype, wdtype, silu=True)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("shape,groups", SHAPES[:8])
+def test_without_activation_or_weights(shape, groups, dtype):
+    check(shape, groups, dtype)
+    check(shape, groups, dtype, none=True, silu=True)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("pad,shift,swap", [(8, 0, False), (1, 0, False), (0, 1, False), (0, 0, True), (3, 1, True), (8, 8, True)])
+def test_strides(pad, shift, swap, dtype):
+    check((3, 40, 96), 4, dtype, silu=True, pad=pad, shift=shift, swap=swap)
+    check((1, 300, 40), 5, dtype, silu=True, pad=pad, shift=shift, swap=swap)
+
+
+def test_means_far_from_zero():
+    """xhat is off by 4 u |mean| rstd more: 700 / 1.5 of them are 1.2e-4."""
+    x = torch.randn(2, 500, 64, dtype=torch.float64).mul(1.5).add(700).float()
+    norm = FusedGroupNorm(64, 4, 2)
+    y, mean, rstd = norm.forward(x.cuda())
+    want, m, r = GN.forward(x.double().numpy(), 4)
+    assert np.abs(wide(mean) - m).max() < 700 * 2.0 ** -22
+    assert (np.abs(wide(rstd) - r) < 2.0 ** -16 * r).all()
+    assert np.abs(wide(y) - want).max() < 700 / 1.5 * 2.0 ** -21 + 2.0 ** -16 * 6
+
+
+def test_a_first_value_far_from_the_rest():
+    """The sums' own shift is then the value that the spread is made of."""
+    x = torch.randn(1, 4000, 8, generator=torch.Generator().manual_seed(0))
+    x[0, 0] = 3e4
+    norm = FusedGroupNorm(8, 2, 1)
+    y, mean, rstd = norm.forward(x.cuda())
+    want, m, r = GN.forward(x.double().numpy(), 2)
+    assert (np.abs(wide(mean) - m) < 2.0 ** -20 * 3e4).all() and (np.abs(wide(rstd) - r) < 2.0 ** -16 * r).all()
+
+
+def test_constant_groups_and_values_that_are_no_numbers():
+    x = torch.full((2, 50, 16), 3.25, device="cuda")
+    norm = FusedGroupNorm(16, 4, 2, eps=1e-5)
+    y, mean, rstd = norm.forward(x)
+    assert not y.any() and (mean == 3.25).all() and ((rstd - 1e5 ** 0.5).abs() < 1e-4).all()
+    x.normal_()
+    for bad in (float("nan"), float("inf"), float("-inf")):
+        for at in ((0, 0, 0), (0, 49, 5), (1, 20, 10)):
+            z = x.clone()
+            z[at] = bad
+            y, mean, rstd = norm.forward(z)
+            hit = torch.zeros(2, 4, dtype=torch.bool, device="cuda")
+            hit[at[0], at[2] // 4] = True
+            assert rstd[hit].isnan().all() and rstd[~hit].isfinite().all()
+            per = y.view(2, 50, 4, 4).transpose(1, 2)
+            assert per[hit].isnan().all() and per[~hit].isfinite().all()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_in_place(dtype):
+    norm, x, w, b, y, mean, rstd = check((3, 50, 64), 8, dtype, silu=True)
+    dy = torch.randn(3, 50, 64, device="cuda").to(dtype)
+    want = norm.backward(dy, x, w, b, mean, rstd)
+    for into in ("dy", "x"):
+        t = {"dy": dy.clone(), "x": x.clone()}
+        got = norm.backward(t["dy"], t["x"], w, b, mean, rstd, dx=t[into])
+        assert all(torch.equal(a, c) for a, c in zip(got, want))
+    z = x.clone()
+    norm.forward(z, w, b, y=z)
+    assert torch.equal(z, y)
+
+
+def test_no_samples_and_refusals():
+    norm = FusedGroupNorm(8, 2, 3)
+    x = torch.randn(3, 5, 8, device="cuda")
+    y, mean, rstd = norm.forward(x[:0])
+    assert y.shape == (0, 5, 8) and mean.shape == (0, 2)
+    dx, dw, db = norm.backward(x[:0], x[:0], None, None, mean, rstd)
+    assert not dw.any() and not db.any()
+    with pytest.raises(AdamWError, match="4 samples"):
+        norm.forward(torch.randn(4, 5, 8, device="cuda"))
+    with pytest.raises(AdamWError, match="no elements"):
+        norm.forward(torch.randn(3, 0, 8, device="cuda"))
+    with pytest.raises(AdamWError, match="strides"):
+        norm.forward(x, y=x.as_strided((3, 5, 8), (8, 24, 1)))
+    with pytest.raises(AdamWError, match="overlapping"):
+        norm.forward(x, y=torch.empty(100, device="cuda").as_strided((3, 5, 8), (8, 8, 1)))
+
+
+def test_gradient_by_differences():
+    rng = np.random.default_rng(12)
+    x, dy = rng.normal(size=(2, 6, 8)).astype(np.float32), rng.normal(size=(2, 6, 8)).astype(np.float32)
+    w, b = rng.normal(1, 0.2, 8).astype(np.float32), rng.normal(0, 0.2, 8).astype(np.float32)
+    put = lambda a: torch.from_numpy(a).cuda()  # noqa: E731
+    norm = FusedGroupNorm(8, 2, 2, activation="silu")
+    _, mean, rstd = norm.forward(put(x), put(w), put(b))
+    got = norm.backward(put(dy), put(x), put(w), put(b), mean, rstd)
+    args = [a.astype(np.float64) for a in (x, w, b)]
+    loss = lambda x, w, b: (GN.forward(x, 2, w, b, silu=True)[0] * dy).sum()  # noqa: E731
+    for i, g in enumerate(got):
+        want = np.zeros_like(args[i])
+        for at in np.ndindex(want.shape):
+            up, down = [a.copy() for a in args], [a.copy() for a in args]
+            up[i][at] += 1e-6
+            down[i][at] -= 1e-6
+            want[at] = (loss(*up) - loss(*down)) / 2e-6
+        assert np.abs(wide(g) - want).max() < 2e-5   # differences 1e-8; float32 2^-15 of terms of a few units
