@@ -29,7 +29,8 @@ from ._capi import (  # noqa: F401
     adamw_layer_norm_forward,
     adamw_layer_norm_backward, adamw_dropout, adamw_router_plan_create, adamw_router_plan_destroy, adamw_route,
     adamw_route_backward, adamw_route_balance, adamw_route_dispatch, adamw_route_combine, adamw_route_combine_backward,
-    adamw_group_norm_plan_create, adamw_group_norm_plan_destroy, adamw_group_norm_forward, adamw_group_norm_backward,
+    adamw_group_norm_plan_create, adamw_group_norm_plan_destroy, adamw_group_norm_plan_status,
+    adamw_group_norm_plan_set_wait_limit, adamw_group_norm_forward, adamw_group_norm_backward,
 )
 
 MODES = {"fp32": _capi.MODE_FP32, "bf16_rem": _capi.MODE_BF16_REM, "q8": _capi.MODE_Q8,

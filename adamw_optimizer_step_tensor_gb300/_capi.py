@@ -121,6 +121,8 @@ _SIGNATURES = {
                                                     _vp, _vp, _i64, _vp, _vp]),
     "adamw_group_norm_plan_create": (ctypes.c_int, [_i32, _i32, _i64, _f, ctypes.c_int, ctypes.POINTER(_vp)]),
     "adamw_group_norm_plan_destroy": (ctypes.c_int, [_vp]),
+    "adamw_group_norm_plan_set_wait_limit": (ctypes.c_int, [_vp, ctypes.c_int32]),
+    "adamw_group_norm_plan_status": (ctypes.c_int, [_vp, ctypes.POINTER(ctypes.c_uint32)]),
     "adamw_group_norm_forward": (ctypes.c_int, [_vp, ctypes.c_int, ctypes.c_int, _i64, _i64,
                                                 ctypes.POINTER(adamw_channels_last), _vp, _vp,
                                                 ctypes.POINTER(adamw_channels_last), _vp, _vp, _vp]),
@@ -531,6 +533,17 @@ def adamw_group_norm_plan_create(channels: int, groups: int, max_samples: int, e
 
 def adamw_group_norm_plan_destroy(plan: int) -> None:
     _check(load().adamw_group_norm_plan_destroy(plan))
+
+
+def adamw_group_norm_plan_set_wait_limit(plan: int, limit_us: int) -> None:
+    _check(load().adamw_group_norm_plan_set_wait_limit(plan, limit_us))
+
+
+def adamw_group_norm_plan_status(plan: int) -> int:
+    """Fault bits of a group norm plan's kernels (read, then cleared); raises AdamWError (ETIMEOUT) if set."""
+    bits = ctypes.c_uint32()
+    _check(load().adamw_group_norm_plan_status(plan, ctypes.byref(bits)))
+    return bits.value
 
 
 def adamw_group_norm_forward(plan: int, dtype: int, weight_dtype: int, samples: int, positions: int,

@@ -266,6 +266,10 @@ class FusedGroupNorm(_Plan):
         # the argument records, filled anew by every call
         self._views = {name: _capi.adamw_channels_last() for name in ("x", "y", "dy", "dx")}
 
+    def status(self) -> int:
+        """Device-side fault bits (0 = healthy); raises AdamWError if a bounded wait gave up."""
+        return _capi.adamw_group_norm_plan_status(self.plan)
+
     def _view(self, name, t, like=None):
         if t.get_device() != self.device:
             _elsewhere(name, t, self.device, "CUDA tensor")

@@ -6,6 +6,7 @@
 #include <new>
 
 #include "block_ops.h"
+#include "operators.h"
 #include "plan_calls.h"
 
 using namespace adamw;
@@ -25,8 +26,11 @@ struct adamw_group_norm_plan {
   int64_t max_samples = 0;
   float eps = 0.0f;
   adamw_activation activation = ADAMW_ACT_NONE;
-  float* d_stats = nullptr;
-  float* d_columns = nullptr;
+  uint64_t wait_ns = kNormWaitNs;
+  float* d_space = nullptr;      // column sums, statistics, joined ones
+  int64_t stats_at = 0, joined_at = 0;
+  uint32_t* d_words = nullptr;   // the samples' words, then the ticket and the fault word
+  int64_t n_words = 0;
 };
 
 namespace {
@@ -39,8 +43,8 @@ void free_router_plan(adamw_router_plan* p) {
 
 void free_group_norm_plan(adamw_group_norm_plan* p) {
   if (!p) return;
-  cudaFree(p->d_stats);
-  cudaFree(p->d_columns);
+  cudaFree(p->d_space);
+  cudaFree(p->d_words);
   delete p;
 }
 
@@ -111,7 +115,7 @@ adamw_status group_norm_args(const adamw_group_norm_plan* plan, int dtype, int w
     return fail(ADAMW_EINVAL, "%lld samples, but the plan was made for %lld", (long long)samples,
                 (long long)plan->max_samples);
   if (positions < 1) return fail(ADAMW_EINVAL, "positions < 1: a group of no elements has no mean");
-  if (positions > (int64_t{1} << 40)) return fail(ADAMW_EUNSUPPORTED, "more than 2^40 positions");
+  if (positions > INT32_MAX) return fail(ADAMW_EUNSUPPORTED, "more than 2^31 - 1 positions");
   if (!aligned(weight, dtype_bytes(weight_dtype)) || !aligned(bias, dtype_bytes(weight_dtype)))
     return fail(ADAMW_EALIGN, "a pointer is not aligned to its element size");
   *a = GroupNormArgs{};
@@ -122,9 +126,17 @@ adamw_status group_norm_args(const adamw_group_norm_plan* plan, int dtype, int w
   a->channels = plan->channels;
   a->groups = plan->groups;
   a->eps = plan->eps;
+  a->max_samples = plan->max_samples;
+  a->size = static_cast<int32_t>(dtype_bytes(dtype));
+  a->weight_f32 = weight_dtype == ADAMW_F32;
   a->silu = plan->activation == ADAMW_ACT_SILU;
-  a->stats = plan->d_stats;
-  a->columns = plan->d_columns;
+  a->columns = plan->d_space;
+  a->stats = plan->d_space + plan->stats_at;
+  a->joined = plan->d_space + plan->joined_at;
+  a->words = plan->d_words;
+  a->ticket = plan->d_words + plan->n_words;
+  a->fault = a->ticket + 1;
+  a->wait_ns = plan->wait_ns;
   return ADAMW_OK;
 }
 
@@ -414,7 +426,7 @@ adamw_status adamw_group_norm_plan_create(int32_t channels, int32_t groups, int6
   *out = nullptr;
   if (channels < 1 || groups < 1 || max_samples < 0)
     return fail(ADAMW_EINVAL, "channels and groups must be >= 1, max_samples >= 0");
-  if (channels > (1 << 20)) return fail(ADAMW_EUNSUPPORTED, "more than 2^20 channels");
+  if (channels > kMaxChannels) return fail(ADAMW_EUNSUPPORTED, "more than %d channels", kMaxChannels);
   if (channels % groups != 0) return fail(ADAMW_EINVAL, "groups must divide channels");
   if (max_samples > (int64_t{1} << 40) / groups)
     return fail(ADAMW_EUNSUPPORTED, "more than 2^40 groups in all");
@@ -434,13 +446,34 @@ adamw_status adamw_group_norm_plan_create(int32_t channels, int32_t groups, int6
   p->max_samples = max_samples;
   p->eps = eps;
   p->activation = activation;
-  cudaError_t e = prepare_group_norm();
-  if (e != cudaSuccess) return failed(e, "prepare the group norm kernels");
   const GroupNormSpace n = group_norm_space(channels, groups, max_samples, sms);
-  if (n.stats > 0) e = cudaMalloc(&p->d_stats, n.stats * sizeof(float));
-  if (e == cudaSuccess && n.columns > 0) e = cudaMalloc(&p->d_columns, n.columns * sizeof(float));
+  p->stats_at = (n.columns + 3) & ~int64_t{3};
+  p->joined_at = p->stats_at + ((n.stats + 3) & ~int64_t{3});
+  p->n_words = n.words;
+  cudaError_t e = cudaMalloc(&p->d_space, (p->joined_at + n.joined) * sizeof(float));
+  if (e == cudaSuccess) e = cudaMalloc(&p->d_words, (n.words + 2) * sizeof(uint32_t));
   if (e != cudaSuccess) return failed(e, "cudaMalloc(group norm plan)", ADAMW_ENOMEM);
+  if ((e = cudaMemset(p->d_words, 0, (n.words + 2) * sizeof(uint32_t))) != cudaSuccess ||
+      (e = cudaStreamSynchronize(cudaStreamLegacy)) != cudaSuccess)
+    return failed(e, "clear the group norm plan");
   *out = p.release();
+  return ADAMW_OK;
+}
+
+adamw_status adamw_group_norm_plan_status(adamw_group_norm_plan* plan, uint32_t* fault_bits) {
+  if (!plan) return fail(ADAMW_EINVAL, "plan is NULL");
+  uint32_t* d_fault = plan->d_words + plan->n_words + 1;
+  const adamw_status st = read_fault(plan->device, d_fault, fault_bits);
+  if (st != ADAMW_ETIMEOUT) return st;
+  cudaError_t e = cudaMemset(d_fault, 0, sizeof(uint32_t));
+  if (e == cudaSuccess) e = cudaStreamSynchronize(cudaStreamLegacy);
+  return e == cudaSuccess ? st : failed(e, "clear the fault word");
+}
+
+adamw_status adamw_group_norm_plan_set_wait_limit(adamw_group_norm_plan* plan, int32_t limit_us) {
+  if (!plan) return fail(ADAMW_EINVAL, "plan is NULL");
+  if (limit_us < 0) return fail(ADAMW_EINVAL, "limit_us < 0");
+  plan->wait_ns = static_cast<uint64_t>(limit_us) * 1000u;
   return ADAMW_OK;
 }
 
@@ -471,8 +504,7 @@ adamw_status adamw_group_norm_forward(adamw_group_norm_plan* plan, adamw_dtype d
   a.out_position = y->position_stride;
   a.mean = mean;
   a.rstd = rstd;
-  cudaError_t e = launch_group_norm_forward(dtype, weight_dtype, a, plan->sms,
-                                            static_cast<cudaStream_t>(stream));
+  cudaError_t e = launch_group_norm_forward(dtype, a, plan->sms, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? ADAMW_OK : failed(e, "launch group norm");
 }
 
@@ -510,8 +542,7 @@ adamw_status adamw_group_norm_backward(adamw_group_norm_plan* plan, adamw_dtype 
   a.rstd = const_cast<float*>(rstd);
   a.dweight = dweight;
   a.dbias = dbias;
-  cudaError_t e = launch_group_norm_backward(dtype, weight_dtype, a, plan->sms,
-                                             static_cast<cudaStream_t>(stream));
+  cudaError_t e = launch_group_norm_backward(dtype, a, plan->sms, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? ADAMW_OK : failed(e, "launch group norm backward");
 }
 

@@ -72,7 +72,7 @@ cudaError_t launch_combine(adamw_dtype dt, const ExpertRowsArgs& a, int sms, cud
 cudaError_t launch_combine_backward(adamw_dtype dt, const ExpertRowsArgs& a, int sms,
                                     cudaStream_t s);
 
-// ---- group norm (group_norm.cu)
+// ---- group norm (group_norm.cu, group_norm_backward.cu)
 struct GroupNormArgs {
   const void* x;
   const void* dy;              // backward
@@ -84,22 +84,27 @@ struct GroupNormArgs {
   float* rstd;
   void* dweight;               // may be null
   void* dbias;                 // may be null
-  int64_t samples, positions;
+  int64_t samples, positions, max_samples;
   int32_t channels, groups;
-  float eps;
+  int32_t size;                // bytes of an element
+  int32_t weight_f32;          // weights are float32, else of the elements' type
   int32_t silu;
-  float* stats;                // plan-owned: partial statistics of samples' parts
-  float* columns;              // plan-owned: partial column sums [2][parts][channels]
-  int32_t parts;               // parts of a sample
+  float eps;
+  // plan-owned
+  float* stats;                // statistics of parts of samples
+  float* joined;               // backward: two means per sample and group
+  float* columns;              // column sums [2][CTAs][channels]
+  uint32_t* words;             // two per sample, 0 between calls
+  uint32_t* ticket;            // CTAs that have left the kernel, 0 between calls
+  uint32_t* fault;             // nonzero: a bounded wait gave up
+  uint64_t wait_ns;            // limit of a wait
 };
+constexpr int kMaxChannels = 1 << 16;
 struct GroupNormSpace {
-  int64_t stats, columns;      // floats
+  int64_t stats, joined, columns, words;   // 4-byte words of each
 };
 GroupNormSpace group_norm_space(int32_t channels, int32_t groups, int64_t max_samples, int sms);
-cudaError_t prepare_group_norm();
-cudaError_t launch_group_norm_forward(adamw_dtype dt, adamw_dtype wdt, GroupNormArgs a, int sms,
-                                      cudaStream_t s);
-cudaError_t launch_group_norm_backward(adamw_dtype dt, adamw_dtype wdt, GroupNormArgs a, int sms,
-                                       cudaStream_t s);
+cudaError_t launch_group_norm_forward(adamw_dtype dt, const GroupNormArgs& a, int sms, cudaStream_t s);
+cudaError_t launch_group_norm_backward(adamw_dtype dt, const GroupNormArgs& a, int sms, cudaStream_t s);
 
 }  // namespace adamw

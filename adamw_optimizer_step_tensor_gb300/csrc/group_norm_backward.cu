@@ -1,0 +1,361 @@
+// group_norm_backward.cu -- group norm's backward pass:
+//     dz = dy act'(z),  A = mean(w dz),  B = mean(w dz xhat) over the group
+//     dx = rstd (w dz - A - xhat B),  dweight = sum dz xhat,  dbias = sum dz
+// A and B come from the same sums per channel as the columns' (A = sum_c w_c sum dz), so a
+// thread keeps sums of its channels alone.  Column sums go from threads to CTAs to a
+// table [CTAs][channels], whose rows the last kernel adds in their order.
+#include "group_norm.cuh"
+
+namespace adamw {
+namespace {
+
+constexpr int kSmallBackward = 4;       // pieces of x and of dy a thread of the small kernel holds
+constexpr int kFlush = 64;              // samples whose column sums a thread adds up before they join the rest
+
+// The CTA's column sums from its threads', rows of threads in order.
+template <int N>
+__device__ __forceinline__ void gn_columns_out(const GroupNormArgs& a, const GnCut& c, const GnPlace<N>& at,
+                                               const float2 (&dw)[gn_pairs<N>()], const float2 (&db)[gn_pairs<N>()],
+                                               float* s) {
+  if (a.dweight == nullptr && a.dbias == nullptr) return;
+#pragma unroll
+  for (int which = 0; which < 2; ++which) {
+    float* out = a.columns + (static_cast<int64_t>(which) * gridDim.x + blockIdx.x) * a.channels;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float2 v = which == 0 ? dw[i / 2] : db[i / 2];
+      __syncthreads();
+      s[threadIdx.x] = i % 2 == 0 ? v.x : v.y;
+      __syncthreads();
+      if (at.there && at.row0 == 0) {
+        float t = 0.0f;
+        for (int r = 0; r < c.at_once; ++r) t += s[r * c.wide + threadIdx.x];
+        out[at.channel() + i] = t;
+      }
+    }
+  }
+}
+
+template <typename T, int N, bool SILU, int K>
+__global__ void __launch_bounds__(kGnThreads) gn_backward_small_kernel(const GroupNormArgs a, const GnCut c) {
+  using P = GnPiece<T, N>;
+  constexpr int kPairs = gn_pairs<N>();
+  __shared__ float s_sum[kGnThreads], s_group[kGnThreads];
+  const GnPlace<N> at(c);
+  const int team = at.row0 / c.team_rows, row0 = at.row0 - team * c.team_rows;
+  const bool mine = at.there && team < c.teams;
+  float2 w[kPairs], b[kPairs];
+  gn_weights<T, N>(a.weight, a.weight_f32, 1.0f, at, w);
+  gn_weights<T, N>(a.bias, a.weight_f32, 0.0f, at, b);
+  const float inv = 1.0f / (static_cast<float>(a.positions) * static_cast<float>(c.per));
+  const int rows = static_cast<int>(a.positions);
+  float2 all_w[kPairs] = {}, all_b[kPairs] = {}, col_w[kPairs] = {}, col_b[kPairs] = {};
+  int since = 0;
+  for (int64_t n0 = static_cast<int64_t>(blockIdx.x) * c.teams; n0 < a.samples; n0 += static_cast<int64_t>(gridDim.x) * c.teams) {
+    const int64_t sample = n0 + team;
+    const bool live = mine && sample < a.samples;
+    const T* x = static_cast<const T*>(a.x) + sample * a.x_sample + at.channel();
+    const T* dy = static_cast<const T*>(a.dy) + sample * a.dy_sample + at.channel();
+    P p[K], q[K];
+    float mean = 0.0f, rstd = 0.0f;
+    if (live) {
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        const int l = row0 + k * c.team_rows;
+        if (l < rows) {
+          p[k].load_last(x + l * a.x_position);
+          q[k].load_last(dy + l * a.dy_position);
+        }
+      }
+      mean = __ldg(a.mean + sample * a.groups + at.group);
+      rstd = __ldg(a.rstd + sample * a.groups + at.group);
+    }
+    const float start = -mean * rstd;
+    float2 one = both(0.0f), two = both(0.0f);
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+      if (live && row0 + k * c.team_rows < rows) {
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i) {
+          const float2 xhat = fma2(p[k].pair(i), both(rstd), both(start));
+          const float2 dz = through<T, SILU>(q[k].pair(i), fma2(xhat, w[i], b[i]));
+          col_b[i] = add2(col_b[i], dz);
+          col_w[i] = fma2(dz, xhat, col_w[i]);
+          const float2 g = mul2(dz, w[i]);
+          one = add2(one, g);
+          two = fma2(g, xhat, two);
+        }
+      }
+    const float mean_g = gn_team_sum(one.x + one.y, c, s_sum, s_group) * inv;
+    const float mean_gx = gn_team_sum(two.x + two.y, c, s_sum, s_group) * inv;
+    if (++since == kFlush) {
+      since = 0;
+#pragma unroll
+      for (int i = 0; i < kPairs; ++i) {
+        all_w[i] = add2(all_w[i], col_w[i]);
+        all_b[i] = add2(all_b[i], col_b[i]);
+        col_w[i] = col_b[i] = both(0.0f);
+      }
+    }
+    if (!live) continue;
+    T* dx = static_cast<T*>(a.out) + sample * a.out_sample + at.channel();
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int l = row0 + k * c.team_rows;
+      if (l < rows) {
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i) {
+          const float2 xhat = fma2(p[k].pair(i), both(rstd), both(start));
+          const float2 dz = through<T, SILU>(q[k].pair(i), fma2(xhat, w[i], b[i]));
+          p[k].set(i, mul2(both(rstd), fma2(xhat, both(-mean_gx), fma2(dz, w[i], both(-mean_g)))));
+        }
+        p[k].store(dx + l * a.out_position);
+      }
+    }
+  }
+  let_next_kernel_start();
+#pragma unroll
+  for (int i = 0; i < kPairs; ++i) {
+    all_w[i] = add2(all_w[i], col_w[i]);
+    all_b[i] = add2(all_b[i], col_b[i]);
+  }
+  gn_columns_out<N>(a, c, at, all_w, all_b, s_sum);
+}
+
+__device__ __forceinline__ float2 gn_from(float2 t, int lanes) {
+  return make_float2(__shfl_xor_sync(kFull, t.x, lanes), __shfl_xor_sync(kFull, t.y, lanes));
+}
+// The two means of groups first .. first + groups - 1 of a sample from its parts' sums, by a warp.
+__device__ __forceinline__ void gn_join_sums(const GroupNormArgs& a, const GnCut& c, int64_t sample, int first, int groups) {
+  const GnLanes l(groups);
+  const int pitch = gn_pitch(a, c);
+  const float inv = 1.0f / (static_cast<float>(a.positions) * static_cast<float>(c.per));
+  for (int g0 = 0; g0 < groups; g0 += l.wide) {
+    const int g = first + g0 + l.slot;
+    float2 t = both(0.0f);
+    if (g < first + groups) {
+      for (int tile = g * c.group_pieces / c.wide; tile <= ((g + 1) * c.group_pieces - 1) / c.wide; ++tile) {
+        const float2* p = gn_stats(a, c, sample, 0) + g + (c.aligned ? 0 : tile);
+        for (int part = l.at; part < c.parts; part += 8 * l.share) {
+          float2 v[8];
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            v[u] = both(0.0f);
+            if (part + u * l.share < c.parts) v[u] = __ldcg(p + static_cast<int64_t>(part + u * l.share) * pitch);
+          }
+#pragma unroll
+          for (int u = 0; u < 8; ++u) t = add2(t, v[u]);
+        }
+      }
+    }
+    for (int o = l.wide; o < 32; o *= 2) t = add2(t, gn_from(t, o));
+    if (l.at == 0 && g < first + groups)
+      __stcg(reinterpret_cast<float2*>(a.joined) + sample * a.groups + g, mul2(t, both(inv)));
+  }
+}
+
+template <typename T, int N, bool SILU>
+__global__ void __launch_bounds__(kGnThreads, kGnCtasPerSm) gn_backward_fused_kernel(const GroupNormArgs a, const GnCut c) {
+  using P = GnPiece<T, N>;
+  constexpr int kPairs = gn_pairs<N>(), kLoad = 4;
+  __shared__ float2 s_stat[2][kGnThreads];     // as in the forward pass
+  __shared__ float s_column[kGnThreads];
+  const GnPlace<N> at(c);
+  const GnLanes lanes(at.groups);
+  float2 w[kPairs], b[kPairs];
+  gn_weights<T, N>(a.weight, a.weight_f32, 1.0f, at, w);
+  gn_weights<T, N>(a.bias, a.weight_f32, 0.0f, at, b);
+  float2 all_w[kPairs] = {}, all_b[kPairs] = {};
+  const int64_t items = gn_items(a, c);
+  const int64_t pace = c.at_once * a.x_position, dy_pace = c.at_once * a.dy_position;
+  uint64_t limit = a.wait_ns;
+  int turn = 0;
+  const uint32_t unit_items = static_cast<uint32_t>(c.batch) * c.parts;
+  uint32_t unit = blockIdx.x / unit_items, rest = blockIdx.x % unit_items;
+  for (int64_t i = blockIdx.x; i < items; i += gridDim.x, rest += gridDim.x) {
+    while (rest >= unit_items) {
+      rest -= unit_items;
+      ++unit;
+    }
+    GnItem it;
+    if (!gn_item(unit, rest, a, c, &it)) continue;
+    const int rows = at.there ? gn_rows(it.rows, at.row0, c.at_once) : 0;
+    const int64_t row = it.first + at.row0;
+    const T* x = static_cast<const T*>(a.x) + it.sample * a.x_sample + row * a.x_position + at.channel();
+    const T* dy = static_cast<const T*>(a.dy) + it.sample * a.dy_sample + row * a.dy_position + at.channel();
+    P p[kLoad], q[kLoad];
+#pragma unroll
+    for (int u = 0; u < kLoad; ++u)
+      if (u < rows) {
+        p[u].load(x + u * pace);
+        q[u].load(dy + u * dy_pace);
+      }
+    float rstd = 0.0f, start = 0.0f;
+    if (at.there) {
+      rstd = __ldg(a.rstd + it.sample * a.groups + at.group);
+      start = -__ldg(a.mean + it.sample * a.groups + at.group) * rstd;
+    }
+    if (!it.result) {
+      float2 col_w[kPairs] = {}, col_b[kPairs] = {};
+      for (int k0 = 0; k0 < rows; k0 += kLoad) {
+        if (k0 > 0) {
+#pragma unroll
+          for (int u = 0; u < kLoad; ++u)
+            if (k0 + u < rows) {
+              p[u].load(x + (k0 + u) * pace);
+              q[u].load(dy + (k0 + u) * dy_pace);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kLoad; ++u)
+          if (k0 + u < rows) {
+#pragma unroll
+            for (int j = 0; j < kPairs; ++j) {
+              const float2 xhat = fma2(p[u].pair(j), both(rstd), both(start));
+              const float2 dz = through<T, SILU>(q[u].pair(j), fma2(xhat, w[j], b[j]));
+              col_b[j] = add2(col_b[j], dz);
+              col_w[j] = fma2(dz, xhat, col_w[j]);
+            }
+          }
+      }
+      float2 one = both(0.0f), two = both(0.0f);
+#pragma unroll
+      for (int j = 0; j < kPairs; ++j) {
+        one = fma2(w[j], col_b[j], one);
+        two = fma2(w[j], col_w[j], two);
+        all_w[j] = add2(all_w[j], col_w[j]);
+        all_b[j] = add2(all_b[j], col_b[j]);
+      }
+      float2 t = N == 1 ? make_float2(one.x, two.x) : make_float2(one.x + one.y, two.x + two.y);
+      float2* s = s_stat[turn];
+      turn ^= 1;
+      const int tile_groups = at.groups;
+      if (c.by_lanes) {
+        for (int o = 1; o < c.group_pieces; o *= 2)
+          t = add2(t, gn_from(t, o));
+        if (at.there && at.piece % c.group_pieces == 0) s[at.row0 * tile_groups + at.group - at.first_group] = t;
+      } else if (at.row0 < c.at_once) {
+        s[threadIdx.x] = t;
+      }
+      __syncthreads();
+      if (threadIdx.x >= 32) continue;
+      float2* out = gn_stats(a, c, it.sample, it.part) + at.first_group + (c.aligned ? 0 : blockIdx.y);
+      for (int g0 = 0; g0 < tile_groups; g0 += lanes.wide) {
+        const int g = g0 + lanes.slot;
+        float2 u = both(0.0f);
+        if (g < tile_groups) {
+          if (c.by_lanes) {
+            for (int r = lanes.at; r < c.at_once; r += lanes.share) u = add2(u, s[r * tile_groups + g]);
+          } else {
+            const int lo = max((at.first_group + g) * c.group_pieces, at.tile0) - at.tile0;
+            const int q = min((at.first_group + g + 1) * c.group_pieces, at.tile0 + at.tile_pieces) - at.tile0 - lo;
+            for (int e = lanes.at; e < q * c.at_once; e += lanes.share) u = add2(u, s[e / q * c.wide + lo + e % q]);
+          }
+        }
+        for (int o = lanes.wide; o < 32; o *= 2) u = add2(u, gn_from(u, o));
+        if (lanes.at == 0 && g < tile_groups) __stcg(out + g, u);
+      }
+      if (gn_arrive(a, c, it.sample)) {
+        if (c.aligned) gn_join_sums(a, c, it.sample, at.first_group, tile_groups);
+        else gn_join_sums(a, c, it.sample, 0, a.groups);
+        gn_open(a, c, it.sample);
+      }
+      continue;
+    }
+    if (!gn_wait_open(a, c, it.sample, &limit)) continue;
+    float2 means = both(0.0f);
+    if (at.there) means = __ldcg(reinterpret_cast<const float2*>(a.joined) + it.sample * a.groups + at.group);
+    T* dx = static_cast<T*>(a.out) + it.sample * a.out_sample + row * a.out_position + at.channel();
+    const int64_t out_pace = c.at_once * a.out_position;
+    for (int k0 = 0; k0 < rows; k0 += kLoad) {
+      if (k0 > 0) {
+#pragma unroll
+        for (int u = 0; u < kLoad; ++u)
+          if (k0 + u < rows) {
+            p[u].load(x + (k0 + u) * pace);
+            q[u].load(dy + (k0 + u) * dy_pace);
+          }
+      }
+#pragma unroll
+      for (int u = 0; u < kLoad; ++u)
+        if (k0 + u < rows) {
+#pragma unroll
+          for (int j = 0; j < kPairs; ++j) {
+            const float2 xhat = fma2(p[u].pair(j), both(rstd), both(start));
+            const float2 dz = through<T, SILU>(q[u].pair(j), fma2(xhat, w[j], b[j]));
+            p[u].set(j, mul2(both(rstd), fma2(xhat, both(-means.y), fma2(dz, w[j], both(-means.x)))));
+          }
+          p[u].store(dx + (k0 + u) * out_pace);
+        }
+    }
+  }
+  gn_columns_out<N>(a, c, at, all_w, all_b, s_column);
+  gn_leave(a, c);
+}
+
+// Sums the CTAs' column sums, in their order: blockIdx.y 0 the weight's, 1 the bias's.
+template <typename W>
+__global__ void __launch_bounds__(1024) gn_columns_kernel(const GroupNormArgs a, const int rows) {
+  __shared__ float s_sum[32][33];
+  const int col = blockIdx.x * 32 + threadIdx.x % 32, r0 = threadIdx.x / 32;
+  W* out = static_cast<W*>(blockIdx.y == 0 ? a.dweight : a.dbias);
+  wait_for_previous_kernel();
+  float t = 0.0f;
+  if (col < a.channels) {
+#pragma unroll 4
+    for (int r = r0; r < rows; r += 32)
+      t += __ldcg(a.columns + (static_cast<int64_t>(blockIdx.y) * rows + r) * a.channels + col);
+  }
+  s_sum[r0][threadIdx.x % 32] = t;
+  __syncthreads();
+  t = warp_total(s_sum[threadIdx.x % 32][threadIdx.x / 32]);
+  const int mine = blockIdx.x * 32 + threadIdx.x / 32;
+  if (threadIdx.x % 32 == 0 && out != nullptr && mine < a.channels) out[mine] = from_f32<W>(t);
+}
+
+template <typename W>
+cudaError_t gn_columns(const GroupNormArgs& a, int rows, cudaStream_t s) {
+  cudaLaunchAttribute attr;
+  cudaLaunchConfig_t l{};
+  l.gridDim = dim3(static_cast<unsigned>((a.channels + 31) / 32), 2);
+  l.blockDim = dim3(1024);
+  l.stream = s;
+  l.attrs = &attr;
+  l.numAttrs = early_start(&attr);
+  return cudaLaunchKernelEx(&l, gn_columns_kernel<W>, a, rows);
+}
+
+template <typename T, int N, bool SILU>
+cudaError_t gn_backward(const GroupNormArgs& a, int sms, cudaStream_t s) {
+  const GnCut c = gn_cut(a, N, kSmallBackward, sms);
+  const dim3 grid(c.ctas, c.tiles);
+  if (a.samples > 0) {
+    const cudaError_t e =
+        c.team_rows == 0              ? gn_launch(gn_backward_fused_kernel<T, N, SILU>, grid, true, s, a, c)
+        : a.positions <= c.team_rows ? gn_launch(gn_backward_small_kernel<T, N, SILU, 1>, grid, false, s, a, c)
+                                      : gn_launch(gn_backward_small_kernel<T, N, SILU, kSmallBackward>, grid, false, s, a, c);
+    if (e != cudaSuccess) return e;
+  }
+  if (a.dweight == nullptr && a.dbias == nullptr) return cudaSuccess;
+  const int rows = a.samples > 0 ? c.ctas : 0;
+  return a.weight_f32 ? gn_columns<float>(a, rows, s) : gn_columns<T>(a, rows, s);
+}
+template <typename T>
+cudaError_t gn_backward_type(const GroupNormArgs& a, int sms, cudaStream_t s) {
+  constexpr int kWide = 16 / sizeof(T);
+  const int n = gn_piece(a, sizeof(T));
+  if (n == kWide) return a.silu ? gn_backward<T, kWide, true>(a, sms, s) : gn_backward<T, kWide, false>(a, sms, s);
+  if constexpr (sizeof(T) == 2)
+    if (n == 2) return a.silu ? gn_backward<T, 2, true>(a, sms, s) : gn_backward<T, 2, false>(a, sms, s);
+  return a.silu ? gn_backward<T, 1, true>(a, sms, s) : gn_backward<T, 1, false>(a, sms, s);
+}
+
+}  // namespace
+
+cudaError_t launch_group_norm_backward(adamw_dtype dt, const GroupNormArgs& a, int sms, cudaStream_t s) {
+  if (dt == ADAMW_F32) return gn_backward_type<float>(a, sms, s);
+  if (dt == ADAMW_F16) return gn_backward_type<__half>(a, sms, s);
+  return gn_backward_type<__nv_bfloat16>(a, sms, s);
+}
+
+}  // namespace adamw

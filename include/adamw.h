@@ -774,13 +774,20 @@ adamw_status adamw_route_combine_backward(adamw_router_plan* plan, adamw_dtype d
 
 typedef enum { ADAMW_ACT_NONE = 0, ADAMW_ACT_SILU = 1 } adamw_activation;
 
-/* Workspace of group norm over `channels` (1 .. 2^20, EUNSUPPORTED above) channels in
+/* Workspace of group norm over `channels` (1 .. 2^16, EUNSUPPORTED above) channels in
  * `groups` (divides channels) groups, for up to max_samples samples.  Synchronous.  eps
  * finite and >= 0.  Calls on one plan must not overlap one another. */
 typedef struct adamw_group_norm_plan adamw_group_norm_plan;
 adamw_status adamw_group_norm_plan_create(int32_t channels, int32_t groups, int64_t max_samples,
                                           float eps, adamw_activation activation,
                                           adamw_group_norm_plan** out);
+/* Device-side health, as adamw_plan_status: the parts of a sample wait for one another,
+ * 2 s at most; a wait that gave up left its call's outputs incomplete.  Reports it once; the
+ * plan stays fit for use. */
+adamw_status adamw_group_norm_plan_status(adamw_group_norm_plan* plan, uint32_t* fault_bits);
+/* Limit of each such wait, 2,000,000 us unless set; 0 gives up wherever a sample is not
+ * ready at once. */
+adamw_status adamw_group_norm_plan_set_wait_limit(adamw_group_norm_plan* plan, int32_t limit_us);
 /* Frees a group norm plan (NULL is allowed).  Synchronises with the device first. */
 adamw_status adamw_group_norm_plan_destroy(adamw_group_norm_plan* plan);
 
@@ -798,7 +805,7 @@ typedef struct {
  *     z = xhat weight + bias,  y = z or z sigmoid(z)
  * weight and bias [channels], float32 or of the elements' dtype (EUNSUPPORTED
  * otherwise), may be NULL (1 and 0).  mean, rstd: float32 [samples][groups].  positions
- * >= 1.  y may be x (same strides).
+ * 1 .. 2^31 - 1.  y may be x (same strides).
  */
 adamw_status adamw_group_norm_forward(adamw_group_norm_plan* plan, adamw_dtype dtype,
                                       adamw_dtype weight_dtype, int64_t samples, int64_t positions,

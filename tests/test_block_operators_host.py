@@ -84,7 +84,7 @@ def test_group_norm_plans_are_checked_first():
     for args in ((0, 1, 1, 1e-5, 0), (8, 0, 1, 1e-5, 0), (8, 3, 1, 1e-5, 0), (8, 2, -1, 1e-5, 0), (8, 2, 1, -1.0, 0),
                  (8, 2, 1, float("nan"), 0)):
         assert _status(C.adamw_group_norm_plan_create, *args) == C.EINVAL, args
-    assert _status(C.adamw_group_norm_plan_create, 2 ** 21, 1, 1, 1e-5, 0) == C.EUNSUPPORTED
+    assert _status(C.adamw_group_norm_plan_create, 2 ** 16 + 1, 1, 1, 1e-5, 0) == C.EUNSUPPORTED
     assert _status(C.adamw_group_norm_plan_create, 8, 8, 2 ** 38, 1e-5, 0) == C.EUNSUPPORTED
     assert _status(C.adamw_group_norm_plan_create, 8, 2, 1, 1e-5, 2) == C.EDTYPE
     assert C.load().adamw_group_norm_plan_create(8, 2, 1, 1e-5, 0, None) == C.EINVAL
@@ -100,6 +100,8 @@ def test_null_plans_are_refused():
     assert _status(C.adamw_route_combine_backward, None, 0, 1, 8, 16, 8, 16, 2, 8, 16, 16, 16, 8, 16, None) == C.EINVAL
     assert _status(C.adamw_group_norm_forward, None, 0, 0, 1, 1, v, None, None, v, 16, 16, None) == C.EINVAL
     assert _status(C.adamw_group_norm_backward, None, 0, 0, 1, 1, v, v, None, None, 16, 16, v, None, None, None) == C.EINVAL
+    assert _status(C.adamw_group_norm_plan_status, None) == C.EINVAL
+    assert _status(C.adamw_group_norm_plan_set_wait_limit, None, 0) == C.EINVAL
     C.adamw_router_plan_destroy(None)
     C.adamw_group_norm_plan_destroy(None)
 

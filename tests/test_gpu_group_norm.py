@@ -203,3 +203,32 @@ def test_gradient_by_differences():
             down[i][at] -= 1e-6
             want[at] = (loss(*up) - loss(*down)) / 2e-6
         assert np.abs(wide(g) - want).max() < 2e-5   # differences 1e-8; float32 2^-15 of terms of a few units
+
+
+@pytest.mark.parametrize("shape,groups", [((1, 60_000, 64), 4), ((40, 3000, 40), 5), ((3, 20_000, 264), 33), ((700, 90, 264), 3), ((2, 3000, 4104), 2)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_samples_in_many_parts(shape, groups, dtype):
+    check(shape, groups, dtype, silu=True)
+
+
+def test_a_wait_that_gives_up_is_reported_and_the_plan_is_fit_again():
+    from adamw_optimizer_step_tensor_gb300 import _capi
+    x = torch.randn(2, 100_000, 64, device="cuda")
+    norm = FusedGroupNorm(64, 4, 2)
+    want = norm.forward(x)
+    back = norm.backward(x, x, None, None, *want[1:])
+    assert norm.status() == 0
+    for _ in range(3):
+        _capi.adamw_group_norm_plan_set_wait_limit(norm.plan, 0)
+        norm.forward(x)
+        with pytest.raises(AdamWError) as e:
+            norm.status()
+        assert e.value.status == _capi.ETIMEOUT
+        assert norm.status() == 0
+        norm.backward(x, x, None, None, *want[1:])
+        with pytest.raises(AdamWError):
+            norm.status()
+        _capi.adamw_group_norm_plan_set_wait_limit(norm.plan, 2_000_000)
+        assert all(torch.equal(a, b) for a, b in zip(norm.forward(x), want))
+        assert all(torch.equal(a, b) for a, b in zip(norm.backward(x, x, None, None, *want[1:]), back))
+        assert norm.status() == 0
