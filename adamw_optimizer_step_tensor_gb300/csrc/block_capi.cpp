@@ -29,7 +29,7 @@ struct adamw_group_norm_plan {
   uint64_t wait_ns = kNormWaitNs;
   float* d_space = nullptr;      // column sums, statistics, joined ones
   int64_t stats_at = 0, joined_at = 0;
-  uint32_t* d_words = nullptr;   // the samples' words, then the ticket and the fault word
+  uint32_t* d_words = nullptr;   // the kernels' words, then the ticket and the fault word
   int64_t n_words = 0;
 };
 
@@ -126,7 +126,6 @@ adamw_status group_norm_args(const adamw_group_norm_plan* plan, int dtype, int w
   a->channels = plan->channels;
   a->groups = plan->groups;
   a->eps = plan->eps;
-  a->max_samples = plan->max_samples;
   a->size = static_cast<int32_t>(dtype_bytes(dtype));
   a->weight_f32 = weight_dtype == ADAMW_F32;
   a->silu = plan->activation == ADAMW_ACT_SILU;
@@ -450,7 +449,9 @@ adamw_status adamw_group_norm_plan_create(int32_t channels, int32_t groups, int6
   p->stats_at = (n.columns + 3) & ~int64_t{3};
   p->joined_at = p->stats_at + ((n.stats + 3) & ~int64_t{3});
   p->n_words = n.words;
-  cudaError_t e = cudaMalloc(&p->d_space, (p->joined_at + n.joined) * sizeof(float));
+  cudaError_t e = prepare_group_norm();
+  if (e != cudaSuccess) return failed(e, "prepare the group norm kernels");
+  e = cudaMalloc(&p->d_space, (p->joined_at + n.joined) * sizeof(float));
   if (e == cudaSuccess) e = cudaMalloc(&p->d_words, (n.words + 2) * sizeof(uint32_t));
   if (e != cudaSuccess) return failed(e, "cudaMalloc(group norm plan)", ADAMW_ENOMEM);
   if ((e = cudaMemset(p->d_words, 0, (n.words + 2) * sizeof(uint32_t))) != cudaSuccess ||

@@ -84,7 +84,7 @@ struct GroupNormArgs {
   float* rstd;
   void* dweight;               // may be null
   void* dbias;                 // may be null
-  int64_t samples, positions, max_samples;
+  int64_t samples, positions;
   int32_t channels, groups;
   int32_t size;                // bytes of an element
   int32_t weight_f32;          // weights are float32, else of the elements' type
@@ -94,7 +94,7 @@ struct GroupNormArgs {
   float* stats;                // statistics of parts of samples
   float* joined;               // backward: two means per sample and group
   float* columns;              // column sums [2][CTAs][channels]
-  uint32_t* words;             // two per sample, 0 between calls
+  uint32_t* words;             // of the CTAs that share samples, 0 between calls
   uint32_t* ticket;            // CTAs that have left the kernel, 0 between calls
   uint32_t* fault;             // nonzero: a bounded wait gave up
   uint64_t wait_ns;            // limit of a wait
@@ -104,6 +104,8 @@ struct GroupNormSpace {
   int64_t stats, joined, columns, words;   // 4-byte words of each
 };
 GroupNormSpace group_norm_space(int32_t channels, int32_t groups, int64_t max_samples, int sms);
+cudaError_t prepare_group_norm();
+cudaError_t prepare_group_norm_backward();
 cudaError_t launch_group_norm_forward(adamw_dtype dt, const GroupNormArgs& a, int sms, cudaStream_t s);
 cudaError_t launch_group_norm_backward(adamw_dtype dt, const GroupNormArgs& a, int sms, cudaStream_t s);
 

@@ -105,7 +105,8 @@ __device__ __forceinline__ float3 gn_from(float3 t, int lanes) {
 
 // Means and reciprocal deviations of groups first .. first + groups - 1 of a sample from its
 // parts' statistics, by a warp.
-__device__ __forceinline__ void gn_join(const GroupNormArgs& a, const GnCut& c, int64_t sample, int first, int groups, int piece) {
+__device__ __noinline__ void gn_join(const GroupNormArgs& a, const GnCut& c, const float2* stats, int64_t sample, int first,
+                                        int groups, int piece) {
   const GnLanes l(groups);
   const int pitch = gn_pitch(a, c);
   const float inv = 1.0f / (static_cast<float>(a.positions) * static_cast<float>(c.per));
@@ -115,7 +116,7 @@ __device__ __forceinline__ void gn_join(const GroupNormArgs& a, const GnCut& c, 
     if (g < first + groups) {
       for (int tile = p0 / c.wide; tile <= (p1 - 1) / c.wide; ++tile) {
         const float ch = static_cast<float>((min(p1, (tile + 1) * c.wide) - max(p0, tile * c.wide)) * piece);
-        const float2* p = gn_stats(a, c, sample, 0) + g + (c.aligned ? 0 : tile);
+        const float2* p = stats + g + (c.aligned ? 0 : tile);
         for (int part = l.at; part < c.parts; part += 8 * l.share) {
           float2 v[8];
 #pragma unroll
@@ -139,69 +140,29 @@ __device__ __forceinline__ void gn_join(const GroupNormArgs& a, const GnCut& c, 
   }
 }
 
+constexpr int kForwardDepth = 16;       // steps on their way, at most 60 KB a CTA
+
 template <typename T, int N, bool SILU>
-__global__ void __launch_bounds__(kGnThreads, kGnCtasPerSm) gn_forward_fused_kernel(const GroupNormArgs a, const GnCut c) {
+__global__ void __launch_bounds__(kGnFusedThreads, kGnCtasPerSm) gn_forward_fused_kernel(const GroupNormArgs a, const GnCut c) {
+  using Ring = GnRing<T, N, 1, kForwardDepth>;
   using P = GnPiece<T, N>;
   constexpr int kPairs = gn_pairs<N>();
-  // means and spreads of the threads (or, by lanes, of rows of threads and groups) of an
-  // item and of the one before it, which warp 0 may still be reading
+  extern __shared__ uint4 s_ring[];
+  // means and spreads of the threads (or, by lanes, of rows of threads and groups)
   __shared__ float2 s_stat[2][kGnThreads];
   const GnPlace<N> at(c);
-  const GnLanes lanes(at.groups);
-  float2 w[kPairs], b[kPairs];
-  gn_weights<T, N>(a.weight, a.weight_f32, 1.0f, at, w);
-  gn_weights<T, N>(a.bias, a.weight_f32, 0.0f, at, b);
-  const int64_t items = gn_items(a, c);
-  const int64_t pace = c.at_once * a.x_position;
-  uint64_t limit = a.wait_ns;
-  int turn = 0;
-  const uint32_t unit_items = static_cast<uint32_t>(c.batch) * c.parts;
-  uint32_t unit = blockIdx.x / unit_items, rest = blockIdx.x % unit_items;
-  for (int64_t i = blockIdx.x; i < items; i += gridDim.x, rest += gridDim.x) {
-    while (rest >= unit_items) {
-      rest -= unit_items;
-      ++unit;
-    }
-    GnItem it;
-    if (!gn_item(unit, rest, a, c, &it)) continue;
-    const int rows = at.there ? gn_rows(it.rows, at.row0, c.at_once) : 0;
-    const T* x = static_cast<const T*>(a.x) + it.sample * a.x_sample + static_cast<int64_t>(it.first + at.row0) * a.x_position + at.channel();
-    if (!it.result) {
-      float3 t = make_float3(0.0f, 0.0f, 0.0f);
-      for (int k0 = 0; k0 < rows; k0 += kRun) {
-        const int run = min(rows - k0, kRun);
-        P p[kRun];
-#pragma unroll
-        for (int u = 0; u < kRun; ++u)
-          if (u < run) p[u].load(x + (k0 + u) * pace);
-        const float shift = p[0].pair(0).x;
-        float2 sum = both(0.0f), square = both(0.0f);
-#pragma unroll
-        for (int u = 0; u < kRun; ++u)
-          if (u < run) {
-#pragma unroll
-            for (int j = 0; j < kPairs; ++j) {
-              float2 d = add2(p[u].pair(j), both(-shift));
-              if constexpr (N == 1) d.y = 0.0f;
-              sum = add2(sum, d);
-              square = fma2(d, d, square);
-            }
-          }
-        const float n = static_cast<float>(run * N), total = sum.x + sum.y, off = __fdividef(total, n);
-        t = gn_merge(t, make_float3(n, shift + off, fmaxf(fmaf(-off, total, square.x + square.y), 0.0f)));
-      }
-      float2* s = s_stat[turn];
-      turn ^= 1;
-      const int tile_groups = at.groups;
-      if (c.by_lanes) {
-        for (int o = 1; o < c.group_pieces; o *= 2) t = gn_merge(t, gn_from(t, o));
-        if (at.there && at.piece % c.group_pieces == 0) s[at.row0 * tile_groups + at.group - at.first_group] = make_float2(t.y, t.z);
-      } else if (at.row0 < c.at_once) {
-        s[threadIdx.x] = make_float2(t.y, t.z);
-      }
-      __syncthreads();
-      if (threadIdx.x >= 32) continue;
-      float2* out = gn_stats(a, c, it.sample, it.part) + at.first_group + (c.aligned ? 0 : blockIdx.y);
+  const GnPart part(a, c);
+  uint32_t* words = gn_words(a, c, part);
+  const int tile_groups = at.groups;
+  if (threadIdx.x >= kGnThreads) {
+    const GnLanes lanes(tile_groups);
+    const int least = part.rows / c.at_once, more = part.rows - least * c.at_once;   // rows of a thread; those that have one more
+    const int place = part.part * gn_pitch(a, c) + at.first_group + (c.aligned ? 0 : blockIdx.y);
+    for (uint32_t batch = 0; part.sample(batch, c) < a.samples; ++batch) {
+      const int64_t sample = part.sample(batch, c);
+      float2* stats = gn_stats(a, c, batch, part);
+      const float2* s = s_stat[batch % 2];
+      gn_wait_filled(batch % 2);
       for (int g0 = 0; g0 < tile_groups; g0 += lanes.wide) {
         const int g = g0 + lanes.slot;
         float3 u = make_float3(0.0f, 0.0f, 0.0f);
@@ -209,7 +170,7 @@ __global__ void __launch_bounds__(kGnThreads, kGnCtasPerSm) gn_forward_fused_ker
           if (c.by_lanes) {
             for (int r = lanes.at; r < c.at_once; r += lanes.share) {
               const float2 v = s[r * tile_groups + g];
-              u = gn_merge(u, make_float3(static_cast<float>(gn_rows(it.rows, r, c.at_once) * c.per), v.x, v.y));
+              u = gn_merge(u, make_float3(static_cast<float>((least + (r < more)) * c.per), v.x, v.y));
             }
           } else {
             const int lo = max((at.first_group + g) * c.group_pieces, at.tile0) - at.tile0;
@@ -217,31 +178,72 @@ __global__ void __launch_bounds__(kGnThreads, kGnCtasPerSm) gn_forward_fused_ker
             for (int e = lanes.at; e < q * c.at_once; e += lanes.share) {
               const int r = e / q;
               const float2 v = s[r * c.wide + lo + e - r * q];
-              u = gn_merge(u, make_float3(static_cast<float>(gn_rows(it.rows, r, c.at_once) * N), v.x, v.y));
+              u = gn_merge(u, make_float3(static_cast<float>((least + (r < more)) * N), v.x, v.y));
             }
           }
         }
         for (int o = lanes.wide; o < 32; o *= 2) u = gn_merge(u, gn_from(u, o));
-        if (lanes.at == 0 && g < tile_groups) __stcg(out + g, make_float2(u.y, u.z));
+        if (lanes.at == 0 && g < tile_groups) __stcg(stats + place + g, make_float2(u.y, u.z));
       }
-      if (gn_arrive(a, c, it.sample)) {
-        if (c.aligned) gn_join(a, c, it.sample, at.first_group, tile_groups, N);
-        else gn_join(a, c, it.sample, 0, a.groups, N);
-        gn_open(a, c, it.sample);
+      if (part.sample(batch + 2, c) < a.samples) gn_freed(batch % 2);
+      if (gn_arrive(c, words, batch)) {
+        if (c.aligned) gn_join(a, c, stats, sample, at.first_group, tile_groups, N);
+        else gn_join(a, c, stats, sample, 0, a.groups, N);
+        gn_open(words, batch);
       }
+    }
+    gn_leave(a, c);
+    return;
+  }
+  Ring ring(s_ring, a, c, part, at);
+  float2 w[kPairs], b[kPairs];
+  gn_weights<T, N>(a.weight, a.weight_f32, 1.0f, at, w);
+  gn_weights<T, N>(a.bias, a.weight_f32, 0.0f, at, b);
+  uint64_t limit = a.wait_ns;
+  for (uint32_t n = 0; n < part.turns; ++n) {
+    const GnTurn turn(n);
+    const int64_t sample = part.sample(turn.batch, c);
+    if (sample >= a.samples) continue;
+    if (!turn.result) {
+      float3 t = make_float3(0.0f, 0.0f, 0.0f);
+      float shift = 0.0f;
+      float2 sum = both(0.0f), square = both(0.0f);
+      int run = 0;
+      for (int k = 0; k < part.steps; ++k) {
+        P p[1];
+        ring.get(p);
+        if (k >= ring.rows) continue;
+        if (run == 0) shift = p[0].pair(0).x;
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) {
+          float2 d = add2(p[0].pair(j), both(-shift));
+          if constexpr (N == 1) d.y = 0.0f;
+          sum = add2(sum, d);
+          square = fma2(d, d, square);
+        }
+        if (++run == kRun || k == ring.rows - 1) {
+          const float count = static_cast<float>(run * N), total = sum.x + sum.y, off = __fdividef(total, count);
+          t = gn_merge(t, make_float3(count, shift + off, fmaxf(fmaf(-off, total, square.x + square.y), 0.0f)));
+          run = 0;
+          sum = square = both(0.0f);
+        }
+      }
+      if (c.by_lanes)
+        for (int o = 1; o < c.group_pieces; o *= 2) t = gn_merge(t, gn_from(t, o));
+      float2* s = s_stat[turn.batch % 2];
+      if (turn.batch >= 2) gn_wait_freed(turn.batch % 2);
+      if (!c.by_lanes) s[threadIdx.x] = make_float2(t.y, t.z);
+      else if (at.there && at.piece % c.group_pieces == 0) s[at.row0 * tile_groups + at.group - at.first_group] = make_float2(t.y, t.z);
+      gn_filled(turn.batch % 2);
       continue;
     }
-    P p[4];
-#pragma unroll
-    for (int u = 0; u < 4; ++u)
-      if (u < rows) p[u].load_last(x + u * pace);
-    if (!gn_wait_open(a, c, it.sample, &limit)) continue;
+    const bool open = gn_wait_open(a, words, turn.batch, &limit);
     float mean = 0.0f, rstd = 0.0f;
     if (at.there) {
-      mean = __ldcg(a.mean + it.sample * a.groups + at.group);
-      rstd = __ldcg(a.rstd + it.sample * a.groups + at.group);
+      mean = __ldcg(a.mean + sample * a.groups + at.group);
+      rstd = __ldcg(a.rstd + sample * a.groups + at.group);
     }
-    T* y = static_cast<T*>(a.out) + it.sample * a.out_sample + static_cast<int64_t>(it.first + at.row0) * a.out_position + at.channel();
+    T* y = static_cast<T*>(a.out) + sample * a.out_sample + static_cast<int64_t>(part.first + at.row0) * a.out_position + at.channel();
     const int64_t out_pace = c.at_once * a.out_position;
     float2 slope[kPairs], start[kPairs];
 #pragma unroll
@@ -249,19 +251,14 @@ __global__ void __launch_bounds__(kGnThreads, kGnCtasPerSm) gn_forward_fused_ker
       slope[j] = mul2(w[j], both(rstd));
       start[j] = fma2(slope[j], both(-mean), b[j]);
     }
-    for (int k0 = 0; k0 < rows; k0 += 4) {
-      if (k0 > 0) {
+    for (int k = 0; k < part.steps; ++k) {
+      P p[1];
+      ring.get(p);
+      if (k >= ring.rows || !open) continue;
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
-          if (k0 + u < rows) p[u].load_last(x + (k0 + u) * pace);
-      }
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (k0 + u < rows) {
-#pragma unroll
-          for (int j = 0; j < kPairs; ++j) p[u].set(j, activate<T, SILU>(fma2(p[u].pair(j), slope[j], start[j])));
-          p[u].store(y + (k0 + u) * out_pace);
-        }
+      for (int j = 0; j < kPairs; ++j) p[0].set(j, activate<T, SILU>(fma2(p[0].pair(j), slope[j], start[j])));
+      p[0].store(y);
+      y += out_pace;
     }
   }
   gn_leave(a, c);
@@ -271,9 +268,12 @@ template <typename T, int N, bool SILU>
 cudaError_t gn_forward(const GroupNormArgs& a, int sms, cudaStream_t s) {
   const GnCut c = gn_cut(a, N, kSmallForward, sms);
   const dim3 grid(c.ctas, c.tiles);
-  if (c.team_rows == 0) return gn_launch(gn_forward_fused_kernel<T, N, SILU>, grid, true, s, a, c);
-  if (a.positions <= c.team_rows) return gn_launch(gn_forward_small_kernel<T, N, SILU, 1>, grid, false, s, a, c);
-  return gn_launch(gn_forward_small_kernel<T, N, SILU, kSmallForward>, grid, false, s, a, c);
+  if (c.team_rows == 0) {
+    constexpr int kBytes = GnRing<T, N, 1, kForwardDepth>::kBytes;
+    return gn_launch(gn_forward_fused_kernel<T, N, SILU>, grid, kGnFusedThreads, kBytes, s, a, c);
+  }
+  if (a.positions <= c.team_rows) return gn_launch(gn_forward_small_kernel<T, N, SILU, 1>, grid, kGnThreads, 0, s, a, c);
+  return gn_launch(gn_forward_small_kernel<T, N, SILU, kSmallForward>, grid, kGnThreads, 0, s, a, c);
 }
 template <typename T>
 cudaError_t gn_forward_type(const GroupNormArgs& a, int sms, cudaStream_t s) {
@@ -341,17 +341,8 @@ void cut_narrow(GnCut* c, int piece_bytes, int64_t most, int ctas) {
   c->at_once = kGnThreads / c->wide;
 }
 
-constexpr int64_t kItemBytes = 48 << 10;    // of one tensor, that an item has at most
+constexpr int64_t kItemBytes = 96 << 10;    // that an item reads, if there is enough for every CTA
 constexpr int kSmallCtasPerSm = 6;
-
-// Items whose statistics the plan holds.
-int64_t stat_slots(int64_t max_samples, int sms) {
-  const int64_t more = 8 * max_samples;
-  return max_samples + (more < 32768 ? more : 32768) + 64LL * sms;
-}
-
-// Samples' tiles whose words it holds.
-int64_t word_slots(int64_t max_samples) { return max_samples + (1 << 17); }
 
 }  // namespace
 
@@ -389,37 +380,33 @@ GnCut gn_cut(const GroupNormArgs& a, int piece, int most, int sms) {
   }
   const int64_t samples = a.samples > 0 ? a.samples : 1;
   const int resident = kGnCtasPerSm * sms;
-  cut_narrow(&c, piece * a.size, word_slots(a.max_samples) / samples, resident);
+  cut_narrow(&c, piece * a.size, resident, resident);
   c.by_lanes = c.aligned && lanes;
-  int64_t ctas = resident / c.tiles > 0 ? resident / c.tiles : 1;
-  int64_t rows = kItemBytes / (static_cast<int64_t>(c.wide) * piece * a.size);
-  const int64_t fair = up(samples * a.positions, ctas);
-  if (rows > fair) rows = fair;
-  if (rows < c.at_once) rows = c.at_once;
-  // the statistics of many narrow groups stay below 1/32 of the elements
-  const int64_t dense = up(8 * 32, static_cast<int64_t>(c.per) * a.size);
-  if (rows < dense) rows = dense;
-  // no more parts than give every CTA one, or 64: they are joined one after another
-  int64_t parts = up(a.positions, rows), room = stat_slots(a.max_samples, sms) / samples;
-  const int64_t enough = ctas / samples > 64 ? ctas / samples : 64;
-  if (parts > enough) parts = enough;
-  if (parts > room) parts = room;
+  // the batch whose parts come closest to an item's bytes, one part for each of a tile's CTAs
+  const int64_t ctas = resident / c.tiles > 0 ? resident / c.tiles : 1;
+  const int64_t row_bytes = static_cast<int64_t>(c.wide) * piece * a.size * (a.dy != nullptr ? 2 : 1);
+  const int64_t rows = kItemBytes / row_bytes > c.at_once ? kItemBytes / row_bytes : c.at_once;
+  int64_t batch = ctas / up(a.positions, rows);
+  if (batch < 1) batch = 1;
+  batch = up(samples, up(samples, batch));        // as many in the last one, or nearly
+  int64_t parts = ctas / batch;
+  const int64_t most_parts = up(a.positions, c.at_once);
+  if (parts > most_parts) parts = most_parts;
   c.part_rows = static_cast<int32_t>(up(a.positions, parts));
   c.parts = static_cast<int32_t>(up(a.positions, c.part_rows));
-  if (ctas > samples * c.parts) ctas = samples * c.parts;
-  c.ctas = static_cast<int32_t>(ctas);
-  c.batch = static_cast<int32_t>(up(c.ctas, c.parts));
+  c.batch = static_cast<int32_t>(batch);
+  c.ctas = c.batch * c.parts;
   return c;
 }
 
 GroupNormSpace group_norm_space(int32_t channels, int32_t groups, int64_t max_samples, int sms) {
   GroupNormSpace n{};
-  n.stats = stat_slots(max_samples, sms) * (groups + up(channels, kGnThreads)) * 2;
+  const int64_t resident = static_cast<int64_t>(kGnCtasPerSm) * sms;
+  n.stats = kGnKept * resident * (groups + up(channels, kGnThreads)) * 2;
   n.joined = max_samples * groups * 2;
-  n.words = 2 * word_slots(max_samples);
-  // rows of column sums: what the small kernels' CTAs leave with the fewest tiles, which the
-  // fused ones' stay below
-  const int64_t rows = static_cast<int64_t>(kSmallCtasPerSm) * sms;
+  n.words = kGnWords * resident;
+  // rows of column sums: what the CTAs of either kind of kernel leave, at most
+  const int64_t rows = (kSmallCtasPerSm > kGnCtasPerSm ? kSmallCtasPerSm : kGnCtasPerSm) * static_cast<int64_t>(sms);
   for (int piece : {1, 2, 4, 8}) {
     if (channels / groups % piece != 0) continue;
     const int64_t tiles = up(channels / piece, kGnThreads);
@@ -427,6 +414,22 @@ GroupNormSpace group_norm_space(int32_t channels, int32_t groups, int64_t max_sa
     if (2 * ctas * channels > n.columns) n.columns = 2 * ctas * channels;
   }
   return n;
+}
+
+template <typename T, int N, bool SILU>
+cudaError_t gn_prepare_forward() {
+  return cudaFuncSetAttribute(gn_forward_fused_kernel<T, N, SILU>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              GnRing<T, N, 1, kForwardDepth>::kBytes);
+}
+cudaError_t prepare_group_norm() {
+  cudaError_t e = prepare_group_norm_backward();
+  if (e == cudaSuccess) e = gn_prepare_forward<float, 4, true>();
+  if (e == cudaSuccess) e = gn_prepare_forward<float, 4, false>();
+  if (e == cudaSuccess) e = gn_prepare_forward<__half, 8, true>();
+  if (e == cudaSuccess) e = gn_prepare_forward<__half, 8, false>();
+  if (e == cudaSuccess) e = gn_prepare_forward<__nv_bfloat16, 8, true>();
+  if (e == cudaSuccess) e = gn_prepare_forward<__nv_bfloat16, 8, false>();
+  return e;
 }
 
 cudaError_t launch_group_norm_forward(adamw_dtype dt, const GroupNormArgs& a, int sms, cudaStream_t s) {

@@ -10,16 +10,20 @@
 // once: statistics and result from the registers (the small kernels).  This takes tiles
 // of whole groups.
 //
-// Larger samples are read twice by one launch (the fused kernels).  A sample is cut into
-// parts; an item is the statistics of one part or the result of one.  CTAs take items in
-// one order: the statistics of a batch of samples, then the results of the batch before
-// it, whose elements the L2 still holds.  Tiles are narrow here (256 bytes of whole groups,
-// if that suits), so that a tile of a sample has few parts: the warp that leaves the last
-// statistics of one joins them, in the order of parts, and opens it for its results.  What
-// that takes (about 5 us) has to pass while other items run, or every CTA waits for it.
-// Only one warp of a CTA does it: the others go on to the next item.  An item waits only
-// for items before it in that order, and all CTAs are resident (a cooperative launch), so
-// every wait ends; each is bounded all the same.
+// Larger samples are read twice by one launch (the fused kernels), the second time out of
+// the L2.  A sample is cut into parts; an item is the statistics of one part or the result
+// of one.  A batch of samples has one part for each CTA of a tile, and a CTA takes the same
+// part of every batch: the statistics of batch 0, then in turn those of batch j and the
+// result of batch j - 1.  The warp that leaves the last statistics of a sample (of a tile of
+// it, if tiles are of whole groups) joins them, in the order of parts, and opens it for its
+// results; about 5 us that pass while other items run.  An item waits only for items before
+// it in that order, and all CTAs are resident (a cooperative launch), so every wait ends;
+// each is bounded all the same.
+//
+// Elements come in by asynchronous copies, each thread's into its own places of a ring in
+// shared memory, which run ahead across items: no barrier, no registers, and the copies
+// do not pause where an item ends or waits.  A ninth warp takes the threads' statistics
+// over, adds them up and does all that concerns other CTAs; the eight go on at once.
 #pragma once
 
 #include "async_copy.cuh"
@@ -31,6 +35,7 @@ namespace {
 
 constexpr int kGnThreads = 256;
 constexpr int kGnWarps = kGnThreads / 32;
+constexpr int kGnFusedThreads = kGnThreads + 32;
 
 // How a call is cut up.
 struct GnCut {
@@ -47,7 +52,7 @@ struct GnCut {
   int32_t parts;                 // of a sample
   int32_t batch;                 // samples of a batch
   int32_t part_rows;
-  int32_t ctas;                  // per tile
+  int32_t ctas;                  // per tile; fused kernels: batch x parts
 };
 
 template <typename T, int N>
@@ -96,22 +101,23 @@ __device__ __forceinline__ float warp_total(float x) {
   return x;
 }
 
-// sigmoid(z).  For 16-bit elements two share one reciprocal, 1 / (d d'), since the special
-// function unit would bound the pass: three operations there instead of four.  Below
-// -43 the sigmoid counts as that of -43 (2^-62), which keeps d d' in range.
+// sigmoid(z).  For 16-bit elements by the approximate exponential and reciprocal: off by
+// |z| 2^-24 and a few 2^-23, well below the elements' rounding.  (One reciprocal for two
+// elements, 1 / (d d'), took more instructions than it saved: the special function unit
+// is not what bounds the pass.)
 template <typename T>
 __device__ __forceinline__ float2 sigmoid2(float2 z) {
   if constexpr (sizeof(T) == 4) {
     return make_float2(__fdividef(1.0f, 1.0f + expf(-z.x)), __fdividef(1.0f, 1.0f + expf(-z.y)));
   } else {
-    const float2 t = mul2(make_float2(fmaxf(z.x, -43.0f), fmaxf(z.y, -43.0f)), both(-1.4426950408889634f));
-    float2 e;
-    float r;
+    const float2 t = mul2(z, both(-1.4426950408889634f));
+    float2 e, s;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(t.x));
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(t.y));
     const float2 d = add2(e, both(1.0f));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d.x * d.y));
-    return mul2(both(r), make_float2(d.y, d.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s.x) : "f"(d.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s.y) : "f"(d.y));
+    return s;
   }
 }
 // The activation's value at z, and dy times its slope there.
@@ -124,8 +130,8 @@ template <typename T, bool SILU>
 __device__ __forceinline__ float2 through(float2 dy, float2 z) {
   if constexpr (!SILU) return dy;
   const float2 s = sigmoid2<T>(z);
-  const float2 zs = mul2(z, s);                       // s (1 + z (1 - s)) = s + z s - s z s
-  return mul2(dy, fma2(mul2(s, both(-1.0f)), zs, add2(s, zs)));
+  const float2 u = fma2(s, both(-1.0f), both(1.0f));   // 1 - s
+  return mul2(mul2(dy, s), fma2(z, u, both(1.0f)));
 }
 
 // This thread's place.
@@ -168,37 +174,151 @@ __device__ __forceinline__ void gn_weights(const void* p, bool f32, float one, c
 
 // ---------------------------------------------------------------- fused kernels
 
-struct GnItem {
-  bool result;           // the result of a part, else its statistics
-  int64_t sample;
-  int part, first, rows; // rows: of the part
+// What a CTA does: item n of batches 0, 1, ... is the statistics of batch 0, then in turn
+// those of batch j (n = 2 j - 1) and the results of batch j (n = 2 j + 2).
+struct GnTurn {
+  bool result;
+  uint32_t batch;
+  __device__ __forceinline__ explicit GnTurn(uint32_t n)
+      : result(n > 0 && n % 2 == 0), batch(n == 0 ? 0 : (n % 2 == 0 ? n / 2 - 1 : (n + 1) / 2)) {}
 };
-// Units of batch x parts items: the statistics of batch 0, then in turn those of batch
-// j and the results of batch j - 1.
-__device__ __forceinline__ int64_t gn_items(const GroupNormArgs& a, const GnCut& c) {
-  const int64_t batches = (a.samples + c.batch - 1) / c.batch;
-  return (2 * batches + 1) * c.batch * c.parts;
-}
-__device__ __forceinline__ bool gn_item(uint32_t unit, uint32_t rest, const GroupNormArgs& a, const GnCut& c, GnItem* it) {
-  it->result = unit > 0 && unit % 2 == 0;
-  const uint32_t batch = it->result ? unit / 2 - 1 : (unit + 1) / 2;
-  const uint32_t within = rest / static_cast<uint32_t>(c.parts);
-  it->sample = static_cast<int64_t>(batch) * c.batch + within;
-  it->part = static_cast<int>(rest - within * c.parts);
-  it->first = it->part * c.part_rows;
-  it->rows = min(c.part_rows, static_cast<int>(a.positions) - it->first);
-  return it->sample < a.samples;
-}
+// This CTA's part of its sample of each batch.
+struct GnPart {
+  uint32_t turns;        // items, the missing ones of the last batch among them
+  int64_t sample0;       // its sample of batch 0
+  int part, first, rows; // rows: of the part
+  int steps;             // rows of a thread, at most
+  __device__ __forceinline__ GnPart(const GroupNormArgs& a, const GnCut& c) {
+    turns = 2 * static_cast<uint32_t>((a.samples + c.batch - 1) / c.batch) + 1;
+    sample0 = blockIdx.x / c.parts;
+    part = blockIdx.x % c.parts;
+    first = part * c.part_rows;
+    rows = min(c.part_rows, static_cast<int>(a.positions) - first);
+    steps = (rows + c.at_once - 1) / c.at_once;
+  }
+  __device__ __forceinline__ int64_t sample(uint32_t batch, const GnCut& c) const {
+    return sample0 + static_cast<int64_t>(batch) * c.batch;
+  }
+};
 // Rows of a part that row0's threads have.
 __device__ __forceinline__ int gn_rows(int rows, int row0, int at_once) {
   return rows > row0 ? (rows - row0 + at_once - 1) / at_once : 0;
 }
 
+// The two buffers in which the eight warps leave their statistics: filled (the eight arrive,
+// the ninth waits) and free again (the ninth arrives, the eight wait, from the third on).
+__device__ __forceinline__ void gn_filled(uint32_t buffer) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(1 + buffer), "n"(kGnFusedThreads) : "memory");
+}
+__device__ __forceinline__ void gn_wait_filled(uint32_t buffer) {
+  asm volatile("bar.sync %0, %1;" ::"r"(1 + buffer), "n"(kGnFusedThreads) : "memory");
+}
+__device__ __forceinline__ void gn_freed(uint32_t buffer) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(3 + buffer), "n"(kGnFusedThreads) : "memory");
+}
+__device__ __forceinline__ void gn_wait_freed(uint32_t buffer) {
+  asm volatile("bar.sync %0, %1;" ::"r"(3 + buffer), "n"(kGnFusedThreads) : "memory");
+}
+
+// An asynchronous copy of a thread's piece to its place in shared memory (two bytes are too
+// few for one: they are copied at once).
+template <typename P, typename T>
+__device__ __forceinline__ void gn_copy(P* to, const T* from) {
+  if constexpr (P::kBytes == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from) : "memory");
+  else if constexpr (P::kBytes == 4)
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(to)), "l"(from) : "memory");
+  else
+    to->load(from);
+}
+__device__ __forceinline__ void gn_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT>
+__device__ __forceinline__ void gn_arrived() { asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory"); }
+
+// Copies of a thread's pieces of `TENSORS` tensors, `DEPTH` - 1 steps ahead of its work: the
+// place that is filled is the one whose piece was worked on a step ago.
+template <typename T, int N, int TENSORS, int DEPTH>
+struct GnRing {
+  using P = GnPiece<T, N>;
+  P* place;              // [DEPTH][TENSORS][kGnThreads], this thread's
+  const T *x0, *dy0;     // of this thread's first row in sample 0 of the tensor
+  const T *x, *dy;
+  int64_t pace, dy_pace;
+  uint32_t n = 0;
+  int step = 0, fill = 0, take = 0;
+  const GroupNormArgs& a;
+  const GnCut& c;
+  const GnPart& part;
+  int rows;              // of this thread
+
+  __device__ __forceinline__ GnRing(void* smem, const GroupNormArgs& a_, const GnCut& c_, const GnPart& part_,
+                                    const GnPlace<N>& at)
+      : place(static_cast<P*>(smem) + threadIdx.x), a(a_), c(c_), part(part_) {
+    rows = at.there ? gn_rows(part.rows, at.row0, c.at_once) : 0;
+    const int64_t row = part.first + at.row0;
+    x0 = static_cast<const T*>(a.x) + row * a.x_position + at.channel();
+    pace = c.at_once * a.x_position;
+    if (TENSORS == 2) {
+      dy0 = static_cast<const T*>(a.dy) + row * a.dy_position + at.channel();
+      dy_pace = c.at_once * a.dy_position;
+    }
+    enter();
+#pragma unroll 1
+    for (int d = 0; d < DEPTH - 1; ++d) put();
+  }
+  // To the first item from n on that there is.
+  __device__ __forceinline__ void enter() {
+    for (; n < part.turns; ++n) {
+      const int64_t sample = part.sample(GnTurn(n).batch, c);
+      if (sample < a.samples) {
+        x = x0 + sample * a.x_sample;
+        if (TENSORS == 2) dy = dy0 + sample * a.dy_sample;
+        break;
+      }
+    }
+    step = 0;
+  }
+  __device__ __forceinline__ void put() {
+    if (n < part.turns) {
+      if (step < rows) {
+        P* p = place + fill * (TENSORS * kGnThreads);
+        gn_copy(p, x);
+        x += pace;
+        if (TENSORS == 2) {
+          gn_copy(p + kGnThreads, dy);
+          dy += dy_pace;
+        }
+      }
+      if (++step == part.steps) {
+        ++n;
+        enter();
+      }
+    }
+    gn_commit();
+    fill = fill + 1 == DEPTH ? 0 : fill + 1;
+  }
+  // The next step's pieces; then the copies go one step further.
+  __device__ __forceinline__ void get(P (&p)[TENSORS]) {
+    gn_arrived<DEPTH - 2>();
+#pragma unroll
+    for (int t = 0; t < TENSORS; ++t) p[t] = place[(take * TENSORS + t) * kGnThreads];
+    take = take + 1 == DEPTH ? 0 : take + 1;
+    put();
+  }
+  static constexpr int kBytes = DEPTH * TENSORS * kGnThreads * static_cast<int>(sizeof(P));
+};
+
+// Statistics of parts and means of samples are kept for three batches: a CTA leaves those of
+// batch j + 3 after its results of batch j + 1, whose sample was opened when all parts of
+// batch j had been joined.
+constexpr int kGnKept = 3;
+
 // Partial statistics of a part: group g, or where tiles may begin inside a group g + t for
 // tile t (each such tile adds one, so the places are distinct).
 __device__ __forceinline__ int gn_pitch(const GroupNormArgs& a, const GnCut& c) { return a.groups + (c.aligned ? 0 : c.tiles); }
-__device__ __forceinline__ float2* gn_stats(const GroupNormArgs& a, const GnCut& c, int64_t sample, int part) {
-  return reinterpret_cast<float2*>(a.stats) + (sample * c.parts + part) * gn_pitch(a, c);
+__device__ __forceinline__ float2* gn_stats(const GroupNormArgs& a, const GnCut& c, uint32_t batch, const GnPart& part) {
+  return reinterpret_cast<float2*>(a.stats) +
+         (static_cast<int64_t>(batch % kGnKept) * c.batch + part.sample0) * c.parts * gn_pitch(a, c);
 }
 
 // Lanes of a warp that joins entries of several groups: `wide` groups side by side, and
@@ -215,38 +335,39 @@ struct GnLanes {
   }
 };
 
-// Words of a sample, or of a tile of one: items that left their statistics, and whether it
-// is open.  All are 0 between calls: the last CTA to leave the kernel clears them.
-__device__ __forceinline__ uint32_t* gn_words(const GroupNormArgs& a, const GnCut& c, int64_t sample) {
-  return a.words + 2 * (c.aligned ? sample * c.tiles + blockIdx.y : sample);
+// Words of the CTAs that share a sample (or a tile of one) of each batch: the number that
+// left their statistics, for each of the batches kept, and the batches that are open.  They
+// only grow; the last CTA to leave the kernel clears them.
+constexpr int kGnWords = kGnKept + 1;
+__device__ __forceinline__ uint32_t* gn_words(const GroupNormArgs& a, const GnCut& c, const GnPart& part) {
+  return a.words + kGnWords * (c.aligned ? part.sample0 * c.tiles + blockIdx.y : part.sample0);
 }
 
 // Called by a warp that has written an item's statistics: true if they are the sample's last.
-__device__ __forceinline__ bool gn_arrive(const GroupNormArgs& a, const GnCut& c, int64_t sample) {
+__device__ __forceinline__ bool gn_arrive(const GnCut& c, uint32_t* words, uint32_t batch) {
   __syncwarp();
   bool last = false;
   if ((threadIdx.x & 31) == 0) {
     uint32_t before;
-    asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(before) : "l"(gn_words(a, c, sample)) : "memory");
-    last = before == static_cast<uint32_t>(c.parts) * (c.aligned ? 1 : c.tiles) - 1;
+    asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(before) : "l"(words + batch % kGnKept) : "memory");
+    const uint32_t all = static_cast<uint32_t>(c.parts) * (c.aligned ? 1 : c.tiles);
+    last = before + 1 == all * (batch / kGnKept + 1);
   }
   return __shfl_sync(kFull, static_cast<int>(last), 0) != 0;
 }
-__device__ __forceinline__ void gn_open(const GroupNormArgs& a, const GnCut& c, int64_t sample) {
+__device__ __forceinline__ void gn_open(uint32_t* words, uint32_t batch) {
   __syncwarp();
-  if ((threadIdx.x & 31) == 0) {
-    asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(gn_words(a, c, sample) + 1), "r"(1u) : "memory");
-  }
+  if ((threadIdx.x & 31) == 0)
+    asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(words + kGnKept), "r"(batch + 1) : "memory");
 }
-// A warp waits until the sample is open: false when the wait gave up.  One that gave up
-// does not wait again.
-__device__ __forceinline__ bool gn_wait_open(const GroupNormArgs& a, const GnCut& c, int64_t sample, uint64_t* limit_ns) {
+// A warp waits until its sample of the batch is open: false when the wait gave up.  One that
+// gave up does not wait again.
+__device__ __forceinline__ bool gn_wait_open(const GroupNormArgs& a, const uint32_t* words, uint32_t batch, uint64_t* limit_ns) {
   bool open = true;
   if ((threadIdx.x & 31) == 0) {
-    const uint32_t* word = gn_words(a, c, sample) + 1;
     uint32_t v;
-    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(word) : "memory");
-    if (v == 0) {
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(words + kGnKept) : "memory");
+    if (v <= batch) {
       const uint64_t t0 = global_ns();
       while (true) {
         if (global_ns() - t0 >= *limit_ns) {
@@ -255,8 +376,8 @@ __device__ __forceinline__ bool gn_wait_open(const GroupNormArgs& a, const GnCut
           break;
         }
         __nanosleep(50);
-        asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(word) : "memory");
-        if (v != 0) break;
+        asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(words + kGnKept) : "memory");
+        if (v > batch) break;
       }
     }
   }
@@ -264,7 +385,7 @@ __device__ __forceinline__ bool gn_wait_open(const GroupNormArgs& a, const GnCut
   if (!open) *limit_ns = 0;
   return open;
 }
-// Every CTA leaves by here; the last one clears the samples' words.
+// Every CTA leaves by here; the last one clears the words.
 __device__ __forceinline__ void gn_leave(const GroupNormArgs& a, const GnCut& c) {
   __syncthreads();
   bool last = false;
@@ -273,8 +394,7 @@ __device__ __forceinline__ void gn_leave(const GroupNormArgs& a, const GnCut& c)
     last = atomicAdd(a.ticket, 1u) == gridDim.x * gridDim.y - 1;
   }
   if (!__syncthreads_or(last)) return;
-  const int64_t words = 2 * a.samples * (c.aligned ? c.tiles : 1);
-  for (int64_t i = threadIdx.x; i < words; i += kGnThreads) a.words[i] = 0;
+  for (int i = threadIdx.x; i < kGnWords * c.batch * (c.aligned ? c.tiles : 1); i += blockDim.x) a.words[i] = 0;
   if (threadIdx.x == 0) *a.ticket = 0;
 }
 
@@ -324,21 +444,22 @@ __device__ __forceinline__ float gn_team_sum(float x, const GnCut& c, float* s, 
 // Cuts a call up (group_norm.cu).  `most`: pieces per thread of the small kernels; 0 rows
 // of threads (team_rows) where the fused ones take it.
 GnCut gn_cut(const GroupNormArgs& a, int piece, int most, int sms);
+constexpr int kGnCtasPerSm = 2;          // of the fused kernels
 // The widest piece of the call, in elements of `size` bytes.
 int gn_piece(const GroupNormArgs& a, int size);
-constexpr int kGnCtasPerSm = 2;
 
 template <typename K>
-cudaError_t gn_launch(K kernel, dim3 grid, bool cooperative, cudaStream_t s, const GroupNormArgs& a, const GnCut& c) {
+cudaError_t gn_launch(K kernel, dim3 grid, int threads, int smem, cudaStream_t s, const GroupNormArgs& a, const GnCut& c) {
   cudaLaunchAttribute attr;
   cudaLaunchConfig_t l{};
   l.gridDim = grid;
-  l.blockDim = dim3(kGnThreads);
+  l.blockDim = dim3(threads);
+  l.dynamicSmemBytes = smem;
   l.stream = s;
   l.attrs = &attr;
   attr.id = cudaLaunchAttributeCooperative;
   attr.val.cooperative = 1;
-  l.numAttrs = cooperative ? 1 : 0;
+  l.numAttrs = threads == kGnFusedThreads ? 1 : 0;
   return cudaLaunchKernelEx(&l, kernel, a, c);
 }
 

@@ -126,7 +126,8 @@ __device__ __forceinline__ float2 gn_from(float2 t, int lanes) {
   return make_float2(__shfl_xor_sync(kFull, t.x, lanes), __shfl_xor_sync(kFull, t.y, lanes));
 }
 // The two means of groups first .. first + groups - 1 of a sample from its parts' sums, by a warp.
-__device__ __forceinline__ void gn_join_sums(const GroupNormArgs& a, const GnCut& c, int64_t sample, int first, int groups) {
+__device__ __noinline__ void gn_join_sums(const GroupNormArgs& a, const GnCut& c, const float2* stats, int64_t sample, int first,
+                                             int groups) {
   const GnLanes l(groups);
   const int pitch = gn_pitch(a, c);
   const float inv = 1.0f / (static_cast<float>(a.positions) * static_cast<float>(c.per));
@@ -135,7 +136,7 @@ __device__ __forceinline__ void gn_join_sums(const GroupNormArgs& a, const GnCut
     float2 t = both(0.0f);
     if (g < first + groups) {
       for (int tile = g * c.group_pieces / c.wide; tile <= ((g + 1) * c.group_pieces - 1) / c.wide; ++tile) {
-        const float2* p = gn_stats(a, c, sample, 0) + g + (c.aligned ? 0 : tile);
+        const float2* p = stats + g + (c.aligned ? 0 : tile);
         for (int part = l.at; part < c.parts; part += 8 * l.share) {
           float2 v[8];
 #pragma unroll
@@ -154,92 +155,103 @@ __device__ __forceinline__ void gn_join_sums(const GroupNormArgs& a, const GnCut
   }
 }
 
+constexpr int kBackwardDepth = 10;      // steps on their way, at most 72 KB a CTA
+
+// The items of the eight warps.  s_column: this thread's column sums, [2 kPairs][kGnThreads].
 template <typename T, int N, bool SILU>
-__global__ void __launch_bounds__(kGnThreads, kGnCtasPerSm) gn_backward_fused_kernel(const GroupNormArgs a, const GnCut c) {
+__device__ __forceinline__ void gn_backward_items(const GroupNormArgs& a, const GnCut& c, const GnPlace<N>& at, const GnPart& part,
+                                                  const uint32_t* words, void* s_ring, float2 (*s_stat)[kGnThreads], float2* s_column) {
+  using Ring = GnRing<T, N, 2, kBackwardDepth>;
   using P = GnPiece<T, N>;
-  constexpr int kPairs = gn_pairs<N>(), kLoad = 4;
-  __shared__ float2 s_stat[2][kGnThreads];     // as in the forward pass
-  __shared__ float s_column[kGnThreads];
-  const GnPlace<N> at(c);
-  const GnLanes lanes(at.groups);
+  constexpr int kPairs = gn_pairs<N>();
+  Ring ring(s_ring, a, c, part, at);
   float2 w[kPairs], b[kPairs];
   gn_weights<T, N>(a.weight, a.weight_f32, 1.0f, at, w);
   gn_weights<T, N>(a.bias, a.weight_f32, 0.0f, at, b);
-  float2 all_w[kPairs] = {}, all_b[kPairs] = {};
-  const int64_t items = gn_items(a, c);
-  const int64_t pace = c.at_once * a.x_position, dy_pace = c.at_once * a.dy_position;
-  uint64_t limit = a.wait_ns;
-  int turn = 0;
-  const uint32_t unit_items = static_cast<uint32_t>(c.batch) * c.parts;
-  uint32_t unit = blockIdx.x / unit_items, rest = blockIdx.x % unit_items;
-  for (int64_t i = blockIdx.x; i < items; i += gridDim.x, rest += gridDim.x) {
-    while (rest >= unit_items) {
-      rest -= unit_items;
-      ++unit;
-    }
-    GnItem it;
-    if (!gn_item(unit, rest, a, c, &it)) continue;
-    const int rows = at.there ? gn_rows(it.rows, at.row0, c.at_once) : 0;
-    const int64_t row = it.first + at.row0;
-    const T* x = static_cast<const T*>(a.x) + it.sample * a.x_sample + row * a.x_position + at.channel();
-    const T* dy = static_cast<const T*>(a.dy) + it.sample * a.dy_sample + row * a.dy_position + at.channel();
-    P p[kLoad], q[kLoad];
 #pragma unroll
-    for (int u = 0; u < kLoad; ++u)
-      if (u < rows) {
-        p[u].load(x + u * pace);
-        q[u].load(dy + u * dy_pace);
-      }
+  for (int j = 0; j < 2 * kPairs; ++j) s_column[j * kGnThreads] = both(0.0f);
+  uint64_t limit = a.wait_ns;
+  for (uint32_t n = 0; n < part.turns; ++n) {
+    const GnTurn turn(n);
+    const int64_t sample = part.sample(turn.batch, c);
+    if (sample >= a.samples) continue;
     float rstd = 0.0f, start = 0.0f;
     if (at.there) {
-      rstd = __ldg(a.rstd + it.sample * a.groups + at.group);
-      start = -__ldg(a.mean + it.sample * a.groups + at.group) * rstd;
+      rstd = __ldg(a.rstd + sample * a.groups + at.group);
+      start = -__ldg(a.mean + sample * a.groups + at.group) * rstd;
     }
-    if (!it.result) {
+    if (!turn.result) {
       float2 col_w[kPairs] = {}, col_b[kPairs] = {};
-      for (int k0 = 0; k0 < rows; k0 += kLoad) {
-        if (k0 > 0) {
+      for (int k = 0; k < part.steps; ++k) {
+        P p[2];
+        ring.get(p);
+        if (k >= ring.rows) continue;
 #pragma unroll
-          for (int u = 0; u < kLoad; ++u)
-            if (k0 + u < rows) {
-              p[u].load(x + (k0 + u) * pace);
-              q[u].load(dy + (k0 + u) * dy_pace);
-            }
+        for (int j = 0; j < kPairs; ++j) {
+          const float2 xhat = fma2(p[0].pair(j), both(rstd), both(start));
+          const float2 dz = through<T, SILU>(p[1].pair(j), fma2(xhat, w[j], b[j]));
+          col_b[j] = add2(col_b[j], dz);
+          col_w[j] = fma2(dz, xhat, col_w[j]);
         }
-#pragma unroll
-        for (int u = 0; u < kLoad; ++u)
-          if (k0 + u < rows) {
-#pragma unroll
-            for (int j = 0; j < kPairs; ++j) {
-              const float2 xhat = fma2(p[u].pair(j), both(rstd), both(start));
-              const float2 dz = through<T, SILU>(q[u].pair(j), fma2(xhat, w[j], b[j]));
-              col_b[j] = add2(col_b[j], dz);
-              col_w[j] = fma2(dz, xhat, col_w[j]);
-            }
-          }
       }
       float2 one = both(0.0f), two = both(0.0f);
 #pragma unroll
       for (int j = 0; j < kPairs; ++j) {
         one = fma2(w[j], col_b[j], one);
         two = fma2(w[j], col_w[j], two);
-        all_w[j] = add2(all_w[j], col_w[j]);
-        all_b[j] = add2(all_b[j], col_b[j]);
+        s_column[2 * j * kGnThreads] = add2(s_column[2 * j * kGnThreads], col_w[j]);
+        s_column[(2 * j + 1) * kGnThreads] = add2(s_column[(2 * j + 1) * kGnThreads], col_b[j]);
       }
       float2 t = N == 1 ? make_float2(one.x, two.x) : make_float2(one.x + one.y, two.x + two.y);
-      float2* s = s_stat[turn];
-      turn ^= 1;
-      const int tile_groups = at.groups;
-      if (c.by_lanes) {
-        for (int o = 1; o < c.group_pieces; o *= 2)
-          t = add2(t, gn_from(t, o));
-        if (at.there && at.piece % c.group_pieces == 0) s[at.row0 * tile_groups + at.group - at.first_group] = t;
-      } else if (at.row0 < c.at_once) {
-        s[threadIdx.x] = t;
+      if (c.by_lanes)
+        for (int o = 1; o < c.group_pieces; o *= 2) t = add2(t, gn_from(t, o));
+      float2* s = s_stat[turn.batch % 2];
+      if (turn.batch >= 2) gn_wait_freed(turn.batch % 2);
+      if (!c.by_lanes) s[threadIdx.x] = t;
+      else if (at.there && at.piece % c.group_pieces == 0) s[at.row0 * at.groups + at.group - at.first_group] = t;
+      gn_filled(turn.batch % 2);
+      continue;
+    }
+    const bool open = gn_wait_open(a, words, turn.batch, &limit);
+    float2 means = both(0.0f);
+    if (at.there) means = mul2(__ldcg(reinterpret_cast<const float2*>(a.joined) + sample * a.groups + at.group), both(-rstd));
+    T* dx = static_cast<T*>(a.out) + sample * a.out_sample + static_cast<int64_t>(part.first + at.row0) * a.out_position + at.channel();
+    const int64_t out_pace = c.at_once * a.out_position;
+    for (int k = 0; k < part.steps; ++k) {
+      P p[2];
+      ring.get(p);
+      if (k >= ring.rows || !open) continue;
+#pragma unroll
+      for (int j = 0; j < kPairs; ++j) {
+        const float2 xhat = fma2(p[0].pair(j), both(rstd), both(start));
+        const float2 dz = through<T, SILU>(p[1].pair(j), fma2(xhat, w[j], b[j]));
+        p[0].set(j, fma2(xhat, both(means.y), fma2(mul2(dz, w[j]), both(rstd), both(means.x))));
       }
-      __syncthreads();
-      if (threadIdx.x >= 32) continue;
-      float2* out = gn_stats(a, c, it.sample, it.part) + at.first_group + (c.aligned ? 0 : blockIdx.y);
+      p[0].store(dx);
+      dx += out_pace;
+    }
+  }
+}
+
+template <typename T, int N, bool SILU>
+__global__ void __launch_bounds__(kGnFusedThreads, kGnCtasPerSm) gn_backward_fused_kernel(const GroupNormArgs a, const GnCut c) {
+  using Ring = GnRing<T, N, 2, kBackwardDepth>;
+  constexpr int kPairs = gn_pairs<N>();
+  extern __shared__ uint4 s_ring[];
+  __shared__ float2 s_stat[2][kGnThreads];     // as in the forward pass
+  float2* s_column = reinterpret_cast<float2*>(reinterpret_cast<char*>(s_ring) + Ring::kBytes) + threadIdx.x % kGnThreads;
+  const GnPlace<N> at(c);
+  const GnPart part(a, c);
+  uint32_t* words = gn_words(a, c, part);
+  const int tile_groups = at.groups;
+  if (threadIdx.x >= kGnThreads) {
+    const GnLanes lanes(tile_groups);
+    const int place = part.part * gn_pitch(a, c) + at.first_group + (c.aligned ? 0 : blockIdx.y);
+    for (uint32_t batch = 0; part.sample(batch, c) < a.samples; ++batch) {
+      const int64_t sample = part.sample(batch, c);
+      float2* stats = gn_stats(a, c, batch, part);
+      const float2* s = s_stat[batch % 2];
+      gn_wait_filled(batch % 2);
       for (int g0 = 0; g0 < tile_groups; g0 += lanes.wide) {
         const int g = g0 + lanes.slot;
         float2 u = both(0.0f);
@@ -253,44 +265,31 @@ __global__ void __launch_bounds__(kGnThreads, kGnCtasPerSm) gn_backward_fused_ke
           }
         }
         for (int o = lanes.wide; o < 32; o *= 2) u = add2(u, gn_from(u, o));
-        if (lanes.at == 0 && g < tile_groups) __stcg(out + g, u);
+        if (lanes.at == 0 && g < tile_groups) __stcg(stats + place + g, u);
       }
-      if (gn_arrive(a, c, it.sample)) {
-        if (c.aligned) gn_join_sums(a, c, it.sample, at.first_group, tile_groups);
-        else gn_join_sums(a, c, it.sample, 0, a.groups);
-        gn_open(a, c, it.sample);
+      if (part.sample(batch + 2, c) < a.samples) gn_freed(batch % 2);
+      if (gn_arrive(c, words, batch)) {
+        if (c.aligned) gn_join_sums(a, c, stats, sample, at.first_group, tile_groups);
+        else gn_join_sums(a, c, stats, sample, 0, a.groups);
+        gn_open(words, batch);
       }
-      continue;
     }
-    if (!gn_wait_open(a, c, it.sample, &limit)) continue;
-    float2 means = both(0.0f);
-    if (at.there) means = __ldcg(reinterpret_cast<const float2*>(a.joined) + it.sample * a.groups + at.group);
-    T* dx = static_cast<T*>(a.out) + it.sample * a.out_sample + row * a.out_position + at.channel();
-    const int64_t out_pace = c.at_once * a.out_position;
-    for (int k0 = 0; k0 < rows; k0 += kLoad) {
-      if (k0 > 0) {
-#pragma unroll
-        for (int u = 0; u < kLoad; ++u)
-          if (k0 + u < rows) {
-            p[u].load(x + (k0 + u) * pace);
-            q[u].load(dy + (k0 + u) * dy_pace);
-          }
-      }
-#pragma unroll
-      for (int u = 0; u < kLoad; ++u)
-        if (k0 + u < rows) {
-#pragma unroll
-          for (int j = 0; j < kPairs; ++j) {
-            const float2 xhat = fma2(p[u].pair(j), both(rstd), both(start));
-            const float2 dz = through<T, SILU>(q[u].pair(j), fma2(xhat, w[j], b[j]));
-            p[u].set(j, mul2(both(rstd), fma2(xhat, both(-means.y), fma2(dz, w[j], both(-means.x)))));
-          }
-          p[u].store(dx + (k0 + u) * out_pace);
-        }
-    }
+  } else {
+    gn_backward_items<T, N, SILU>(a, c, at, part, words, s_ring, s_stat, s_column);
   }
-  gn_columns_out<N>(a, c, at, all_w, all_b, s_column);
+  float2 all_w[kPairs], all_b[kPairs];
+#pragma unroll
+  for (int j = 0; j < kPairs; ++j) {
+    all_w[j] = s_column[2 * j * kGnThreads];
+    all_b[j] = s_column[(2 * j + 1) * kGnThreads];
+  }
+  gn_columns_out<N>(a, c, at, all_w, all_b, reinterpret_cast<float*>(s_stat));
   gn_leave(a, c);
+}
+
+template <typename T, int N>
+constexpr int gn_backward_smem() {
+  return GnRing<T, N, 2, kBackwardDepth>::kBytes + 2 * gn_pairs<N>() * kGnThreads * static_cast<int>(sizeof(float2));
 }
 
 // Sums the CTAs' column sums, in their order: blockIdx.y 0 the weight's, 1 the bias's.
@@ -331,9 +330,10 @@ cudaError_t gn_backward(const GroupNormArgs& a, int sms, cudaStream_t s) {
   const dim3 grid(c.ctas, c.tiles);
   if (a.samples > 0) {
     const cudaError_t e =
-        c.team_rows == 0              ? gn_launch(gn_backward_fused_kernel<T, N, SILU>, grid, true, s, a, c)
-        : a.positions <= c.team_rows ? gn_launch(gn_backward_small_kernel<T, N, SILU, 1>, grid, false, s, a, c)
-                                      : gn_launch(gn_backward_small_kernel<T, N, SILU, kSmallBackward>, grid, false, s, a, c);
+        c.team_rows == 0 ? gn_launch(gn_backward_fused_kernel<T, N, SILU>, grid, kGnFusedThreads, gn_backward_smem<T, N>(), s, a, c)
+        : a.positions <= c.team_rows
+            ? gn_launch(gn_backward_small_kernel<T, N, SILU, 1>, grid, kGnThreads, 0, s, a, c)
+            : gn_launch(gn_backward_small_kernel<T, N, SILU, kSmallBackward>, grid, kGnThreads, 0, s, a, c);
     if (e != cudaSuccess) return e;
   }
   if (a.dweight == nullptr && a.dbias == nullptr) return cudaSuccess;
@@ -350,7 +350,23 @@ cudaError_t gn_backward_type(const GroupNormArgs& a, int sms, cudaStream_t s) {
   return a.silu ? gn_backward<T, 1, true>(a, sms, s) : gn_backward<T, 1, false>(a, sms, s);
 }
 
+template <typename T, int N, bool SILU>
+cudaError_t gn_prepare_backward() {
+  return cudaFuncSetAttribute(gn_backward_fused_kernel<T, N, SILU>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              gn_backward_smem<T, N>());
+}
+
 }  // namespace
+
+cudaError_t prepare_group_norm_backward() {
+  cudaError_t e = gn_prepare_backward<float, 4, true>();
+  if (e == cudaSuccess) e = gn_prepare_backward<float, 4, false>();
+  if (e == cudaSuccess) e = gn_prepare_backward<__half, 8, true>();
+  if (e == cudaSuccess) e = gn_prepare_backward<__half, 8, false>();
+  if (e == cudaSuccess) e = gn_prepare_backward<__nv_bfloat16, 8, true>();
+  if (e == cudaSuccess) e = gn_prepare_backward<__nv_bfloat16, 8, false>();
+  return e;
+}
 
 cudaError_t launch_group_norm_backward(adamw_dtype dt, const GroupNormArgs& a, int sms, cudaStream_t s) {
   if (dt == ADAMW_F32) return gn_backward_type<float>(a, sms, s);
