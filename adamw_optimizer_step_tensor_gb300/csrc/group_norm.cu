@@ -7,7 +7,7 @@
 // difference loses log2(2 n) bits at worst, whatever the mean.  From there on means and
 // spreads are joined by counts: M2 = sum M2_i + n_i (mean_i - mean)^2.  The small kernel
 // has the values in registers and sums about their mean.
-#include "group_norm.cuh"
+#include "group_norm_cluster.cuh"
 
 namespace adamw {
 namespace {
@@ -140,6 +140,100 @@ __device__ __noinline__ void gn_join(const GroupNormArgs& a, const GnCut& c, con
   }
 }
 
+template <typename T, int N, bool SILU>
+__global__ void __launch_bounds__(kGnThreads, 3) gn_forward_cluster_kernel(const GroupNormArgs a, const GnCut c) {
+  using P = GnPiece<T, N>;
+  constexpr int kPairs = gn_pairs<N>();
+  extern __shared__ uint4 s_tile[];
+  __shared__ float2 s_sum[kGnThreads], s_group[kGnTileGroups], s_slots[2][kGnClusterMax][kGnTileGroups];
+  __shared__ float s_here[kGnTileGroups];
+  const GnPlace<N> at(c);
+  const int rank = c.cluster > 1 ? static_cast<int>(cluster_rank()) : 0;
+  const int first = rank * c.part_rows;
+  const int rows = max(0, min(c.part_rows, static_cast<int>(a.positions) - first));
+  const int tile_bytes = at.tile_pieces * P::kBytes;
+  float2 w[kPairs], b[kPairs];
+  gn_weights<T, N>(a.weight, a.weight_f32, 1.0f, at, w);
+  gn_weights<T, N>(a.bias, a.weight_f32, 0.0f, at, b);
+  const float mine = rows > 0 ? __fdividef(1.0f, static_cast<float>(rows) * static_cast<float>(c.per)) : 0.0f;
+  const float inv = 1.0f / (static_cast<float>(a.positions) * static_cast<float>(c.per));
+  const int group = at.there ? at.group - at.first_group : 0;
+  const char* tile = reinterpret_cast<const char*>(s_tile) + (threadIdx.x % c.wide) * P::kBytes;
+  const int row_bytes = c.at_once * tile_bytes;
+  int turn = 0;
+  for (int64_t sample = blockIdx.x / c.cluster; sample < a.samples; sample += gridDim.x / c.cluster) {
+    __syncthreads();                    // the sample before is done with
+    gn_fetch(reinterpret_cast<char*>(s_tile),
+             reinterpret_cast<const char*>(static_cast<const T*>(a.x) + sample * a.x_sample + first * a.x_position) + at.tile0 * P::kBytes,
+             rows, tile_bytes, a.x_position * static_cast<int64_t>(sizeof(T)), c.unit);
+    gn_fetched();
+    float2 t = both(0.0f);
+    if (at.there) {
+      const char* p = tile + at.row0 * tile_bytes;
+#pragma unroll 4
+      for (int l = at.row0; l < rows; l += c.at_once, p += row_bytes) {
+        const P v = *reinterpret_cast<const P*>(p);
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) t = add2(t, v.pair(j));
+      }
+    }
+    gn_block_sums<N>(c, at, make_float2(t.x + t.y, 0.0f), s_sum, s_group);
+    // about this CTA's mean, which the differences' own sum puts right
+    const float here = s_group[group].x * mine;
+    if (threadIdx.x < at.groups) s_here[threadIdx.x] = s_group[threadIdx.x].x * mine;
+    float2 off = both(0.0f);
+    t = both(0.0f);
+    if (at.there) {
+      const char* p = tile + at.row0 * tile_bytes;
+#pragma unroll 4
+      for (int l = at.row0; l < rows; l += c.at_once, p += row_bytes) {
+        const P v = *reinterpret_cast<const P*>(p);
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) {
+          float2 d = add2(v.pair(j), both(-here));
+          if constexpr (N == 1) d.y = 0.0f;
+          off = add2(off, d);
+          t = fma2(d, d, t);
+        }
+      }
+    }
+    __syncthreads();                    // s_group has been read
+    gn_block_sums<N>(c, at, make_float2(off.x + off.y, t.x + t.y), s_sum, s_group);
+    if (threadIdx.x < at.groups) {
+      const float2 v = s_group[threadIdx.x];
+      const float d = v.x * mine;
+      s_group[threadIdx.x] = make_float2(s_here[threadIdx.x] + d, fmaxf(fmaf(-d, v.x, v.y), 0.0f));
+    }
+    __syncthreads();
+    // two sets of slots: a CTA may be a sample ahead of one that still reads
+    gn_exchange(c.cluster, rank, at.groups, s_group, s_slots[turn]);
+    float3 u = make_float3(0.0f, 0.0f, 0.0f);
+    for (int r = 0; r < c.cluster; ++r) {
+      const int n = max(0, min(c.part_rows, static_cast<int>(a.positions) - r * c.part_rows));
+      const float2 v = s_slots[turn][r][group];
+      u = gn_merge(u, make_float3(static_cast<float>(n) * static_cast<float>(c.per), v.x, v.y));
+    }
+    turn ^= 1;
+    const float mean = u.y, rstd = __frcp_rn(__fsqrt_rn(fmaf(u.z, inv, a.eps)));
+    if (!at.there) continue;
+    if (rank == 0 && at.row0 == 0 && at.piece % c.group_pieces == 0) {
+      a.mean[sample * a.groups + at.group] = mean;
+      a.rstd[sample * a.groups + at.group] = rstd;
+    }
+    T* y = static_cast<T*>(a.out) + sample * a.out_sample + (first + at.row0) * a.out_position + at.channel();
+    const int64_t pace = c.at_once * a.out_position;
+    const char* p = tile + at.row0 * tile_bytes;
+#pragma unroll 2
+    for (int l = at.row0; l < rows; l += c.at_once, p += row_bytes, y += pace) {
+      P v = *reinterpret_cast<const P*>(p);
+#pragma unroll
+      for (int j = 0; j < kPairs; ++j)
+        v.set(j, activate<T, SILU>(fma2(mul2(add2(v.pair(j), both(-mean)), both(rstd)), w[j], b[j])));
+      v.store(y);
+    }
+  }
+}
+
 constexpr int kForwardDepth = 16;       // steps on their way, at most 60 KB a CTA
 
 template <typename T, int N, bool SILU>
@@ -268,6 +362,7 @@ template <typename T, int N, bool SILU>
 cudaError_t gn_forward(const GroupNormArgs& a, int sms, cudaStream_t s) {
   const GnCut c = gn_cut(a, N, kSmallForward, sms);
   const dim3 grid(c.ctas, c.tiles);
+  if (c.cluster > 0) return gn_cluster_launch(gn_forward_cluster_kernel<T, N, SILU>, gn_cluster_bytes(a, c, N), s, a, c);
   if (c.team_rows == 0) {
     constexpr int kBytes = GnRing<T, N, 1, kForwardDepth>::kBytes;
     return gn_launch(gn_forward_fused_kernel<T, N, SILU>, grid, kGnFusedThreads, kBytes, s, a, c);
@@ -341,6 +436,51 @@ void cut_narrow(GnCut* c, int piece_bytes, int64_t most, int ctas) {
   c->at_once = kGnThreads / c->wide;
 }
 
+// Tiles and clusters of the cluster kernels: of all that fit, by a model of the time with
+// the rates measured on GB300 (6.8 bytes/ns in all, 40 a CTA; 3 us for a sample's barriers
+// and latencies).  False where nothing fits.
+bool cut_cluster(GnCut* c, const GroupNormArgs& a, int piece, int sms) {
+  const int q = c->group_pieces, tensors = a.dy != nullptr ? 2 : 1;
+  if (q > kGnThreads) return false;
+  const int groups = a.groups;
+  double best = 0.0;
+  for (int m = 1; ; m = 2 * m < groups ? 2 * m : groups) {
+    const int wide = m * q;
+    if (wide > kGnThreads || m > kGnTileGroups) break;
+    const int64_t tiles = up(groups, m), tile_bytes = static_cast<int64_t>(wide) * piece * a.size;
+    const int at_once = kGnThreads / wide;
+    for (int cluster = 1; cluster <= kGnClusterMax; cluster *= 2) {
+      const int64_t rows = up(a.positions, cluster), bytes = rows * tile_bytes * tensors;
+      if (bytes > kGnClusterBytes || (cluster > 1 && rows * (cluster - 1) >= a.positions)) continue;
+      int64_t per_sm = (224 << 10) / (bytes + (8 << 10));
+      if (per_sm > 3) per_sm = 3;
+      int64_t clusters = per_sm * sms / cluster / tiles;
+      if (clusters < 1) clusters = 1;
+      if (clusters > a.samples) clusters = a.samples;
+      const int64_t rounds = up(a.samples, clusters);
+      const double busy = static_cast<double>(clusters * cluster * tiles);
+      const double waves = busy > static_cast<double>(per_sm * sms) ? busy / static_cast<double>(per_sm * sms) : 1.0;
+      double rate = 6800.0 / (busy / waves);
+      if (rate > 40.0) rate = 40.0;
+      rate *= static_cast<double>(wide * at_once) / kGnThreads;
+      if (tile_bytes < 128 && tiles > 1) rate *= tile_bytes < 64 ? 0.5 : 0.8;
+      const double time = static_cast<double>(rounds) * waves *
+                          (3000.0 + (cluster > 1 ? 1000.0 : 0.0) + static_cast<double>(bytes) * (1.0 + 1.0 / tensors) / rate);
+      if (best == 0.0 || time < best) {
+        best = time;
+        c->wide = wide;
+        c->tiles = static_cast<int32_t>(tiles);
+        c->at_once = at_once;
+        c->cluster = cluster;
+        c->part_rows = static_cast<int32_t>(rows);
+        c->ctas = static_cast<int32_t>(clusters * cluster);
+      }
+    }
+    if (m == groups) break;
+  }
+  return best > 0.0;
+}
+
 constexpr int64_t kItemBytes = 96 << 10;    // that an item reads, if there is enough for every CTA
 constexpr int kSmallCtasPerSm = 6;
 
@@ -378,6 +518,19 @@ GnCut gn_cut(const GroupNormArgs& a, int piece, int most, int sms) {
     c.ctas = static_cast<int32_t>(ctas < all ? ctas : all);
     return c;
   }
+  if (a.samples > 0 && cut_cluster(&c, a, piece, sms)) {
+    c.by_lanes = lanes;
+    const int64_t step = static_cast<int64_t>(c.wide) * piece * a.size;     // bytes from tile to tile
+    c.unit = a.size;
+    for (int unit : {16, 4}) {
+      if (unit > a.size && step % unit == 0 && static_cast<int64_t>(a.channels) * a.size % unit == 0 &&
+          on_grid(a.x, a.x_sample, a.x_position, a, a.size, unit) && on_grid(a.dy, a.dy_sample, a.dy_position, a, a.size, unit)) {
+        c.unit = unit;
+        break;
+      }
+    }
+    return c;
+  }
   const int64_t samples = a.samples > 0 ? a.samples : 1;
   const int resident = kGnCtasPerSm * sms;
   cut_narrow(&c, piece * a.size, resident, resident);
@@ -399,6 +552,10 @@ GnCut gn_cut(const GroupNormArgs& a, int piece, int most, int sms) {
   return c;
 }
 
+int gn_cluster_bytes(const GroupNormArgs& a, const GnCut& c, int piece) {
+  return c.part_rows * c.wide * piece * a.size * (a.dy != nullptr ? 2 : 1);
+}
+
 GroupNormSpace group_norm_space(int32_t channels, int32_t groups, int64_t max_samples, int sms) {
   GroupNormSpace n{};
   const int64_t resident = static_cast<int64_t>(kGnCtasPerSm) * sms;
@@ -410,25 +567,34 @@ GroupNormSpace group_norm_space(int32_t channels, int32_t groups, int64_t max_sa
   for (int piece : {1, 2, 4, 8}) {
     if (channels / groups % piece != 0) continue;
     const int64_t tiles = up(channels / piece, kGnThreads);
-    const int64_t ctas = rows / tiles > 0 ? rows / tiles : 1;
+    const int64_t ctas = rows / tiles > kGnClusterMax ? rows / tiles : kGnClusterMax;
     if (2 * ctas * channels > n.columns) n.columns = 2 * ctas * channels;
   }
   return n;
 }
 
 template <typename T, int N, bool SILU>
+cudaError_t gn_prepare_one() {
+  const cudaError_t e = cudaFuncSetAttribute(gn_forward_fused_kernel<T, N, SILU>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             GnRing<T, N, 1, kForwardDepth>::kBytes);
+  if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(gn_forward_cluster_kernel<T, N, SILU>, cudaFuncAttributeMaxDynamicSharedMemorySize, kGnClusterBytes);
+}
+template <typename T, int N>
 cudaError_t gn_prepare_forward() {
-  return cudaFuncSetAttribute(gn_forward_fused_kernel<T, N, SILU>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              GnRing<T, N, 1, kForwardDepth>::kBytes);
+  const cudaError_t e = gn_prepare_one<T, N, true>();
+  return e == cudaSuccess ? gn_prepare_one<T, N, false>() : e;
 }
 cudaError_t prepare_group_norm() {
   cudaError_t e = prepare_group_norm_backward();
-  if (e == cudaSuccess) e = gn_prepare_forward<float, 4, true>();
-  if (e == cudaSuccess) e = gn_prepare_forward<float, 4, false>();
-  if (e == cudaSuccess) e = gn_prepare_forward<__half, 8, true>();
-  if (e == cudaSuccess) e = gn_prepare_forward<__half, 8, false>();
-  if (e == cudaSuccess) e = gn_prepare_forward<__nv_bfloat16, 8, true>();
-  if (e == cudaSuccess) e = gn_prepare_forward<__nv_bfloat16, 8, false>();
+  if (e == cudaSuccess) e = gn_prepare_forward<float, 4>();
+  if (e == cudaSuccess) e = gn_prepare_forward<float, 1>();
+  if (e == cudaSuccess) e = gn_prepare_forward<__half, 8>();
+  if (e == cudaSuccess) e = gn_prepare_forward<__half, 2>();
+  if (e == cudaSuccess) e = gn_prepare_forward<__half, 1>();
+  if (e == cudaSuccess) e = gn_prepare_forward<__nv_bfloat16, 8>();
+  if (e == cudaSuccess) e = gn_prepare_forward<__nv_bfloat16, 2>();
+  if (e == cudaSuccess) e = gn_prepare_forward<__nv_bfloat16, 1>();
   return e;
 }
 

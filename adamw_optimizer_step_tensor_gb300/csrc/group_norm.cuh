@@ -8,9 +8,10 @@
 //
 // Samples whose tile fits into the registers of a CTA or a part of it (`team`) are read
 // once: statistics and result from the registers (the small kernels).  This takes tiles
-// of whole groups.
+// of whole groups, and so does the next larger size: samples whose tile fits into the
+// shared memory of a cluster (group_norm_cluster.cuh).
 //
-// Larger samples are read twice by one launch (the fused kernels), the second time out of
+// Still larger samples are read twice by one launch (the fused kernels), the second time out of
 // the L2.  A sample is cut into parts; an item is the statistics of one part or the result
 // of one.  A batch of samples has one part for each CTA of a tile, and a CTA takes the same
 // part of every batch: the statistics of batch 0, then in turn those of batch j and the
@@ -31,11 +32,6 @@
 #include "rows.cuh"
 
 namespace adamw {
-namespace {
-
-constexpr int kGnThreads = 256;
-constexpr int kGnWarps = kGnThreads / 32;
-constexpr int kGnFusedThreads = kGnThreads + 32;
 
 // How a call is cut up.
 struct GnCut {
@@ -47,6 +43,9 @@ struct GnCut {
   // small kernels
   int32_t team_rows;             // rows of threads per sample
   int32_t teams;                 // samples a CTA takes at once
+  // cluster kernels
+  int32_t cluster;               // CTAs that share a sample's tile; 0: other kernels
+  int32_t unit;                  // bytes of a copy
   // fused kernels
   int32_t aligned;               // tiles are of whole groups: each of a sample's is open by itself
   int32_t parts;                 // of a sample
@@ -54,6 +53,12 @@ struct GnCut {
   int32_t part_rows;
   int32_t ctas;                  // per tile; fused kernels: batch x parts
 };
+
+namespace {
+
+constexpr int kGnThreads = 256;
+constexpr int kGnWarps = kGnThreads / 32;
+constexpr int kGnFusedThreads = kGnThreads + 32;
 
 template <typename T, int N>
 struct GnPiece {
@@ -444,6 +449,9 @@ __device__ __forceinline__ float gn_team_sum(float x, const GnCut& c, float* s, 
 // Cuts a call up (group_norm.cu).  `most`: pieces per thread of the small kernels; 0 rows
 // of threads (team_rows) where the fused ones take it.
 GnCut gn_cut(const GroupNormArgs& a, int piece, int most, int sms);
+// Shared memory of a CTA of the cluster kernels, for its elements.
+int gn_cluster_bytes(const GroupNormArgs& a, const GnCut& c, int piece);
+constexpr int kGnClusterBytes = 208 << 10;   // of them, at most
 constexpr int kGnCtasPerSm = 2;          // of the fused kernels
 // The widest piece of the call, in elements of `size` bytes.
 int gn_piece(const GroupNormArgs& a, int size);

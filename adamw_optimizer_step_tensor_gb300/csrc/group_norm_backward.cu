@@ -4,7 +4,7 @@
 // A and B come from the same sums per channel as the columns' (A = sum_c w_c sum dz), so a
 // thread keeps sums of its channels alone.  Column sums go from threads to CTAs to a
 // table [CTAs][channels], whose rows the last kernel adds in their order.
-#include "group_norm.cuh"
+#include "group_norm_cluster.cuh"
 
 namespace adamw {
 namespace {
@@ -153,6 +153,92 @@ __device__ __noinline__ void gn_join_sums(const GroupNormArgs& a, const GnCut& c
     if (l.at == 0 && g < first + groups)
       __stcg(reinterpret_cast<float2*>(a.joined) + sample * a.groups + g, mul2(t, both(inv)));
   }
+}
+
+template <typename T, int N, bool SILU>
+__global__ void __launch_bounds__(kGnThreads, 3) gn_backward_cluster_kernel(const GroupNormArgs a, const GnCut c) {
+  using P = GnPiece<T, N>;
+  constexpr int kPairs = gn_pairs<N>();
+  extern __shared__ uint4 s_tile[];
+  __shared__ float2 s_sum[kGnThreads], s_group[kGnTileGroups], s_slots[2][kGnClusterMax][kGnTileGroups];
+  const GnPlace<N> at(c);
+  const int rank = c.cluster > 1 ? static_cast<int>(cluster_rank()) : 0;
+  const int first = rank * c.part_rows;
+  const int rows = max(0, min(c.part_rows, static_cast<int>(a.positions) - first));
+  const int tile_bytes = at.tile_pieces * P::kBytes;
+  float2 w[kPairs], b[kPairs], all_w[kPairs] = {}, all_b[kPairs] = {};
+  gn_weights<T, N>(a.weight, a.weight_f32, 1.0f, at, w);
+  gn_weights<T, N>(a.bias, a.weight_f32, 0.0f, at, b);
+  const float inv = 1.0f / (static_cast<float>(a.positions) * static_cast<float>(c.per));
+  const int group = at.there ? at.group - at.first_group : 0;
+  const int size = sizeof(T), other = c.part_rows * c.wide * P::kBytes;      // from x to dy
+  const char* tile = reinterpret_cast<const char*>(s_tile) + (threadIdx.x % c.wide) * P::kBytes;
+  const int row_bytes = c.at_once * tile_bytes;
+  int turn = 0;
+  for (int64_t sample = blockIdx.x / c.cluster; sample < a.samples; sample += gridDim.x / c.cluster) {
+    __syncthreads();                    // the sample before is done with
+    char* to = reinterpret_cast<char*>(s_tile);
+    gn_fetch(to, reinterpret_cast<const char*>(static_cast<const T*>(a.x) + sample * a.x_sample + first * a.x_position) + at.tile0 * P::kBytes,
+             rows, tile_bytes, a.x_position * size, c.unit);
+    gn_fetch(to + other,
+             reinterpret_cast<const char*>(static_cast<const T*>(a.dy) + sample * a.dy_sample + first * a.dy_position) + at.tile0 * P::kBytes,
+             rows, tile_bytes, a.dy_position * size, c.unit);
+    float rstd = 0.0f, start = 0.0f;
+    if (at.there) {
+      rstd = __ldg(a.rstd + sample * a.groups + at.group);
+      start = -__ldg(a.mean + sample * a.groups + at.group) * rstd;
+    }
+    gn_fetched();
+    float2 col_w[kPairs] = {}, col_b[kPairs] = {};
+    if (at.there) {
+      const char* p = tile + at.row0 * tile_bytes;
+#pragma unroll 2
+      for (int l = at.row0; l < rows; l += c.at_once, p += row_bytes) {
+        const P v = *reinterpret_cast<const P*>(p), g = *reinterpret_cast<const P*>(p + other);
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) {
+          const float2 xhat = fma2(v.pair(j), both(rstd), both(start));
+          const float2 dz = through<T, SILU>(g.pair(j), fma2(xhat, w[j], b[j]));
+          col_b[j] = add2(col_b[j], dz);
+          col_w[j] = fma2(dz, xhat, col_w[j]);
+        }
+      }
+    }
+    float2 one = both(0.0f), two = both(0.0f);
+#pragma unroll
+    for (int j = 0; j < kPairs; ++j) {
+      one = fma2(w[j], col_b[j], one);
+      two = fma2(w[j], col_w[j], two);
+      all_w[j] = add2(all_w[j], col_w[j]);
+      all_b[j] = add2(all_b[j], col_b[j]);
+    }
+    gn_block_sums<N>(c, at, N == 1 ? make_float2(one.x, two.x) : make_float2(one.x + one.y, two.x + two.y), s_sum, s_group);
+    // two sets of slots: a CTA may be a sample ahead of one that still reads
+    gn_exchange(c.cluster, rank, at.groups, s_group, s_slots[turn]);
+    float2 means = both(0.0f);
+    for (int r = 0; r < c.cluster; ++r) means = add2(means, s_slots[turn][r][group]);
+    turn ^= 1;
+    means = mul2(means, both(-inv * rstd));
+    if (!at.there) continue;
+    T* dx = static_cast<T*>(a.out) + sample * a.out_sample + (first + at.row0) * a.out_position + at.channel();
+    const int64_t pace = c.at_once * a.out_position;
+    const char* p = tile + at.row0 * tile_bytes;
+#pragma unroll 2
+    for (int l = at.row0; l < rows; l += c.at_once, p += row_bytes, dx += pace) {
+      P v = *reinterpret_cast<const P*>(p);
+      const P g = *reinterpret_cast<const P*>(p + other);
+#pragma unroll
+      for (int j = 0; j < kPairs; ++j) {
+        const float2 xhat = fma2(v.pair(j), both(rstd), both(start));
+        const float2 dz = through<T, SILU>(g.pair(j), fma2(xhat, w[j], b[j]));
+        v.set(j, fma2(xhat, both(means.y), fma2(mul2(dz, w[j]), both(rstd), both(means.x))));
+      }
+      v.store(dx);
+    }
+  }
+  let_next_kernel_start();
+  __syncthreads();
+  gn_columns_out<N>(a, c, at, all_w, all_b, reinterpret_cast<float*>(s_sum));
 }
 
 constexpr int kBackwardDepth = 10;      // steps on their way, at most 72 KB a CTA
@@ -330,7 +416,8 @@ cudaError_t gn_backward(const GroupNormArgs& a, int sms, cudaStream_t s) {
   const dim3 grid(c.ctas, c.tiles);
   if (a.samples > 0) {
     const cudaError_t e =
-        c.team_rows == 0 ? gn_launch(gn_backward_fused_kernel<T, N, SILU>, grid, kGnFusedThreads, gn_backward_smem<T, N>(), s, a, c)
+        c.cluster > 0 ? gn_cluster_launch(gn_backward_cluster_kernel<T, N, SILU>, gn_cluster_bytes(a, c, N), s, a, c)
+        : c.team_rows == 0 ? gn_launch(gn_backward_fused_kernel<T, N, SILU>, grid, kGnFusedThreads, gn_backward_smem<T, N>(), s, a, c)
         : a.positions <= c.team_rows
             ? gn_launch(gn_backward_small_kernel<T, N, SILU, 1>, grid, kGnThreads, 0, s, a, c)
             : gn_launch(gn_backward_small_kernel<T, N, SILU, kSmallBackward>, grid, kGnThreads, 0, s, a, c);
@@ -351,20 +438,30 @@ cudaError_t gn_backward_type(const GroupNormArgs& a, int sms, cudaStream_t s) {
 }
 
 template <typename T, int N, bool SILU>
+cudaError_t gn_prepare_one() {
+  const cudaError_t e = cudaFuncSetAttribute(gn_backward_fused_kernel<T, N, SILU>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             gn_backward_smem<T, N>());
+  if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(gn_backward_cluster_kernel<T, N, SILU>, cudaFuncAttributeMaxDynamicSharedMemorySize, kGnClusterBytes);
+}
+template <typename T, int N>
 cudaError_t gn_prepare_backward() {
-  return cudaFuncSetAttribute(gn_backward_fused_kernel<T, N, SILU>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              gn_backward_smem<T, N>());
+  const cudaError_t e = gn_prepare_one<T, N, true>();
+  return e == cudaSuccess ? gn_prepare_one<T, N, false>() : e;
 }
 
 }  // namespace
 
 cudaError_t prepare_group_norm_backward() {
-  cudaError_t e = gn_prepare_backward<float, 4, true>();
-  if (e == cudaSuccess) e = gn_prepare_backward<float, 4, false>();
-  if (e == cudaSuccess) e = gn_prepare_backward<__half, 8, true>();
-  if (e == cudaSuccess) e = gn_prepare_backward<__half, 8, false>();
-  if (e == cudaSuccess) e = gn_prepare_backward<__nv_bfloat16, 8, true>();
-  if (e == cudaSuccess) e = gn_prepare_backward<__nv_bfloat16, 8, false>();
+  cudaError_t e = cudaSuccess;
+  if (e == cudaSuccess) e = gn_prepare_backward<float, 4>();
+  if (e == cudaSuccess) e = gn_prepare_backward<float, 1>();
+  if (e == cudaSuccess) e = gn_prepare_backward<__half, 8>();
+  if (e == cudaSuccess) e = gn_prepare_backward<__half, 2>();
+  if (e == cudaSuccess) e = gn_prepare_backward<__half, 1>();
+  if (e == cudaSuccess) e = gn_prepare_backward<__nv_bfloat16, 8>();
+  if (e == cudaSuccess) e = gn_prepare_backward<__nv_bfloat16, 2>();
+  if (e == cudaSuccess) e = gn_prepare_backward<__nv_bfloat16, 1>();
   return e;
 }
 
