@@ -345,13 +345,13 @@ __global__ void __launch_bounds__(kGnFusedThreads, kGnCtasPerSm) gn_forward_fuse
       slope[j] = mul2(w[j], both(rstd));
       start[j] = fma2(slope[j], both(-mean), b[j]);
     }
+    const int rows = open ? ring.rows : 0;
     for (int k = 0; k < part.steps; ++k) {
       P p[1];
       ring.get(p);
-      if (k >= ring.rows || !open) continue;
 #pragma unroll
       for (int j = 0; j < kPairs; ++j) p[0].set(j, activate<T, SILU>(fma2(p[0].pair(j), slope[j], start[j])));
-      p[0].store(y);
+      if (k < rows) p[0].store(y);
       y += out_pace;
     }
   }

@@ -225,92 +225,103 @@ __device__ __forceinline__ void gn_wait_freed(uint32_t buffer) {
   asm volatile("bar.sync %0, %1;" ::"r"(3 + buffer), "n"(kGnFusedThreads) : "memory");
 }
 
-// An asynchronous copy of a thread's piece to its place in shared memory (two bytes are too
-// few for one: they are copied at once).
-template <typename P, typename T>
-__device__ __forceinline__ void gn_copy(P* to, const T* from) {
-  if constexpr (P::kBytes == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from) : "memory");
-  else if constexpr (P::kBytes == 4)
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(to)), "l"(from) : "memory");
-  else
-    to->load(from);
-}
-__device__ __forceinline__ void gn_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int LEFT>
-__device__ __forceinline__ void gn_arrived() { asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory"); }
-
 // Copies of a thread's pieces of `TENSORS` tensors, `DEPTH` - 1 steps ahead of its work: the
-// place that is filled is the one whose piece was worked on a step ago.
+// place that is filled is the one whose piece was worked on a step ago.  A thread without a
+// row for a step gets zeros, without a read.
 template <typename T, int N, int TENSORS, int DEPTH>
 struct GnRing {
   using P = GnPiece<T, N>;
-  P* place;              // [DEPTH][TENSORS][kGnThreads], this thread's
-  const T *x0, *dy0;     // of this thread's first row in sample 0 of the tensor
-  const T *x, *dy;
-  int64_t pace, dy_pace;
-  uint32_t n = 0;
-  int step = 0, fill = 0, take = 0;
+  static constexpr int kTensor = kGnThreads * P::kBytes;      // bytes of one tensor's places
+  static constexpr int kBytes = DEPTH * TENSORS * kTensor;
   const GroupNormArgs& a;
   const GnCut& c;
   const GnPart& part;
+  uint32_t base, fill, take = 0;
+  const char *x0, *dy0;  // of this thread's first row in sample 0 of the tensor
+  const char *x, *dy;
+  int64_t pace, dy_pace; // bytes
+  uint32_t n = 0;
+  int step = 0, steps;   // of the item whose copies run
   int rows;              // of this thread
 
   __device__ __forceinline__ GnRing(void* smem, const GroupNormArgs& a_, const GnCut& c_, const GnPart& part_,
                                     const GnPlace<N>& at)
-      : place(static_cast<P*>(smem) + threadIdx.x), a(a_), c(c_), part(part_) {
+      : a(a_), c(c_), part(part_), base(smem_u32(smem) + threadIdx.x * P::kBytes) {
+    constexpr int kSize = sizeof(T);
     rows = at.there ? gn_rows(part.rows, at.row0, c.at_once) : 0;
+    steps = part.steps;
     const int64_t row = part.first + at.row0;
-    x0 = static_cast<const T*>(a.x) + row * a.x_position + at.channel();
-    pace = c.at_once * a.x_position;
+    x0 = static_cast<const char*>(a.x) + (row * a.x_position + at.channel()) * kSize;
+    pace = c.at_once * a.x_position * kSize;
     if (TENSORS == 2) {
-      dy0 = static_cast<const T*>(a.dy) + row * a.dy_position + at.channel();
-      dy_pace = c.at_once * a.dy_position;
+      dy0 = static_cast<const char*>(a.dy) + (row * a.dy_position + at.channel()) * kSize;
+      dy_pace = c.at_once * a.dy_position * kSize;
     }
     enter();
+    fill = 0;
 #pragma unroll 1
-    for (int d = 0; d < DEPTH - 1; ++d) put();
+    for (int d = 0; d < DEPTH - 1; ++d) {
+      put();
+      fill += TENSORS * kTensor;
+    }
   }
-  // To the first item from n on that there is.
+  // To the first item from n on that there is; behind the last one nothing is copied.
   __device__ __forceinline__ void enter() {
+    step = 0;
     for (; n < part.turns; ++n) {
       const int64_t sample = part.sample(GnTurn(n).batch, c);
       if (sample < a.samples) {
-        x = x0 + sample * a.x_sample;
-        if (TENSORS == 2) dy = dy0 + sample * a.dy_sample;
-        break;
+        x = x0 + sample * a.x_sample * static_cast<int64_t>(sizeof(T));
+        if (TENSORS == 2) dy = dy0 + sample * a.dy_sample * static_cast<int64_t>(sizeof(T));
+        return;
       }
     }
-    step = 0;
+    steps = 0x7FFFFFFF;
+    step = 0x40000000;     // no thread has as many rows, and the end is far
+  }
+  __device__ __forceinline__ static void copy(uint32_t to, const char* from, bool there) {
+    if constexpr (P::kBytes == 2) {                          // too few bytes for an asynchronous copy
+      const uint16_t v = there ? *reinterpret_cast<const uint16_t*>(from) : uint16_t{0};
+      asm volatile("st.shared.u16 [%0], %1;" ::"r"(to), "h"(v) : "memory");
+    } else if constexpr (P::kBytes == 4) {
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(from), "r"(there ? 4 : 0) : "memory");
+    } else {
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(there ? 16 : 0) : "memory");
+    }
   }
   __device__ __forceinline__ void put() {
-    if (n < part.turns) {
-      if (step < rows) {
-        P* p = place + fill * (TENSORS * kGnThreads);
-        gn_copy(p, x);
-        x += pace;
-        if (TENSORS == 2) {
-          gn_copy(p + kGnThreads, dy);
-          dy += dy_pace;
-        }
-      }
-      if (++step == part.steps) {
-        ++n;
-        enter();
-      }
+    const bool there = step < rows;
+    copy(base + fill, x, there);
+    x += pace;
+    if (TENSORS == 2) {
+      copy(base + fill + kTensor, dy, there);
+      dy += dy_pace;
     }
-    gn_commit();
-    fill = fill + 1 == DEPTH ? 0 : fill + 1;
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    if (++step == steps) {
+      ++n;
+      enter();
+    }
+  }
+  __device__ __forceinline__ static P at(uint32_t place) {
+    P p;
+    if constexpr (P::kBytes == 16)
+      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(p.v.x), "=r"(p.v.y), "=r"(p.v.z), "=r"(p.v.w) : "r"(place) : "memory");
+    else if constexpr (P::kBytes == 4)
+      asm volatile("ld.shared.u32 %0, [%1];" : "=r"(p.v) : "r"(place) : "memory");
+    else
+      asm volatile("ld.shared.u16 %0, [%1];" : "=h"(p.v) : "r"(place) : "memory");
+    return p;
   }
   // The next step's pieces; then the copies go one step further.
   __device__ __forceinline__ void get(P (&p)[TENSORS]) {
-    gn_arrived<DEPTH - 2>();
+    asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 2) : "memory");
 #pragma unroll
-    for (int t = 0; t < TENSORS; ++t) p[t] = place[(take * TENSORS + t) * kGnThreads];
-    take = take + 1 == DEPTH ? 0 : take + 1;
+    for (int t = 0; t < TENSORS; ++t) p[t] = at(base + take + t * kTensor);
     put();
+    fill = take;
+    take = take == kBytes - TENSORS * kTensor ? 0 : take + TENSORS * kTensor;
   }
-  static constexpr int kBytes = DEPTH * TENSORS * kGnThreads * static_cast<int>(sizeof(P));
 };
 
 // Statistics of parts and means of samples are kept for three batches: a CTA leaves those of

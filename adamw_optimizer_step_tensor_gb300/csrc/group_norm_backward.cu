@@ -270,8 +270,7 @@ __device__ __forceinline__ void gn_backward_items(const GroupNormArgs& a, const 
       float2 col_w[kPairs] = {}, col_b[kPairs] = {};
       for (int k = 0; k < part.steps; ++k) {
         P p[2];
-        ring.get(p);
-        if (k >= ring.rows) continue;
+        ring.get(p);                       // a dy of 0 where there is no row
 #pragma unroll
         for (int j = 0; j < kPairs; ++j) {
           const float2 xhat = fma2(p[0].pair(j), both(rstd), both(start));
@@ -303,17 +302,20 @@ __device__ __forceinline__ void gn_backward_items(const GroupNormArgs& a, const 
     if (at.there) means = mul2(__ldcg(reinterpret_cast<const float2*>(a.joined) + sample * a.groups + at.group), both(-rstd));
     T* dx = static_cast<T*>(a.out) + sample * a.out_sample + static_cast<int64_t>(part.first + at.row0) * a.out_position + at.channel();
     const int64_t out_pace = c.at_once * a.out_position;
+    const int rows = open ? ring.rows : 0;
+    float2 slope[kPairs];
+#pragma unroll
+    for (int j = 0; j < kPairs; ++j) slope[j] = mul2(w[j], both(rstd));
     for (int k = 0; k < part.steps; ++k) {
       P p[2];
       ring.get(p);
-      if (k >= ring.rows || !open) continue;
 #pragma unroll
       for (int j = 0; j < kPairs; ++j) {
         const float2 xhat = fma2(p[0].pair(j), both(rstd), both(start));
         const float2 dz = through<T, SILU>(p[1].pair(j), fma2(xhat, w[j], b[j]));
-        p[0].set(j, fma2(xhat, both(means.y), fma2(mul2(dz, w[j]), both(rstd), both(means.x))));
+        p[0].set(j, fma2(xhat, both(means.y), fma2(dz, slope[j], both(means.x))));
       }
-      p[0].store(dx);
+      if (k < rows) p[0].store(dx);
       dx += out_pace;
     }
   }
