@@ -14,9 +14,10 @@ namespace {
 
 constexpr int kRun = 8;                 // rows of a run of sums: 64 values of 16 bits
 constexpr int kSmallForward = 8;        // pieces a thread of the small kernel holds
+constexpr int kSmallCtasPerSm = 4;      // of the small kernels forward, on which their grid goes; backward 3
 
 template <typename T, int N, bool SILU, int K>
-__global__ void __launch_bounds__(kGnThreads) gn_forward_small_kernel(const GroupNormArgs a, const GnCut c) {
+__global__ void __launch_bounds__(kGnThreads, K == 1 ? kSmallCtasPerSm : 2) gn_forward_small_kernel(const GroupNormArgs a, const GnCut c) {
   using P = GnPiece<T, N>;
   constexpr int kPairs = gn_pairs<N>();
   __shared__ float s_sum[kGnThreads], s_group[kGnThreads];
@@ -436,13 +437,14 @@ void cut_narrow(GnCut* c, int piece_bytes, int64_t most, int ctas) {
   c->at_once = kGnThreads / c->wide;
 }
 
-// Tiles and clusters of the cluster kernels: of all that fit, by a model of the time with
-// the rates measured on GB300 (6.8 bytes/ns in all, 40 a CTA; 3 us for a sample's barriers
-// and latencies).  False where nothing fits.
-bool cut_cluster(GnCut* c, const GroupNormArgs& a, int piece, int sms) {
-  const int q = c->group_pieces, tensors = a.dy != nullptr ? 2 : 1;
+// Tiles and clusters of the cluster kernels: of all that fit, by a model of the time that was
+// fitted to 146 measured choices of ten calls (its picks are within a quarter of the best).
+// A sample takes 3 us, 0.4 more for each CTA of a cluster, and the larger of its copies
+// (5.5 bytes/ns in all) and its instructions (8 (8 N + 60) per warp, row and tensor for pieces
+// of N), and half the smaller one.  False where nothing fits, or takes more than `limit` ns.
+bool cut_cluster(GnCut* c, const GroupNormArgs& a, int piece, int sms, double limit) {
+  const int q = c->group_pieces, tensors = a.dy != nullptr ? 2 : 1, groups = a.groups;
   if (q > kGnThreads) return false;
-  const int groups = a.groups;
   double best = 0.0;
   for (int m = 1; ; m = 2 * m < groups ? 2 * m : groups) {
     const int wide = m * q;
@@ -452,20 +454,18 @@ bool cut_cluster(GnCut* c, const GroupNormArgs& a, int piece, int sms) {
     for (int cluster = 1; cluster <= kGnClusterMax; cluster *= 2) {
       const int64_t rows = up(a.positions, cluster), bytes = rows * tile_bytes * tensors;
       if (bytes > kGnClusterBytes || (cluster > 1 && rows * (cluster - 1) >= a.positions)) continue;
-      int64_t per_sm = (224 << 10) / (bytes + (8 << 10));
+      int64_t per_sm = (224 << 10) / (bytes + (12 << 10));
       if (per_sm > 3) per_sm = 3;
+      const double slots = static_cast<double>(per_sm * sms);
       int64_t clusters = per_sm * sms / cluster / tiles;
       if (clusters < 1) clusters = 1;
       if (clusters > a.samples) clusters = a.samples;
-      const int64_t rounds = up(a.samples, clusters);
-      const double busy = static_cast<double>(clusters * cluster * tiles);
-      const double waves = busy > static_cast<double>(per_sm * sms) ? busy / static_cast<double>(per_sm * sms) : 1.0;
-      double rate = 6800.0 / (busy / waves);
-      if (rate > 40.0) rate = 40.0;
-      rate *= static_cast<double>(wide * at_once) / kGnThreads;
-      if (tile_bytes < 128 && tiles > 1) rate *= tile_bytes < 64 ? 0.5 : 0.8;
-      const double time = static_cast<double>(rounds) * waves *
-                          (3000.0 + (cluster > 1 ? 1000.0 : 0.0) + static_cast<double>(bytes) * (1.0 + 1.0 / tensors) / rate);
+      const double busy = static_cast<double>(clusters * cluster * tiles), waves = busy > slots ? busy / slots : 1.0;
+      const double ctas = busy < slots ? busy : slots, on_sm = ctas > sms ? ctas / sms : 1.0;
+      const double compute = static_cast<double>(up(rows, at_once) * 8 * (8 * piece + 60) * tensors) * on_sm / 7.6;
+      const double copies = static_cast<double>(bytes) * (1.0 + 1.0 / tensors) * ctas / 5500.0;
+      const double time = static_cast<double>(up(a.samples, clusters)) * waves *
+                          (3000.0 + (cluster > 1 ? 400.0 * cluster : 0.0) + (compute > copies ? compute + 0.5 * copies : copies + 0.5 * compute));
       if (best == 0.0 || time < best) {
         best = time;
         c->wide = wide;
@@ -478,11 +478,14 @@ bool cut_cluster(GnCut* c, const GroupNormArgs& a, int piece, int sms) {
     }
     if (m == groups) break;
   }
+  if (best > limit) best = c->cluster = 0;
   return best > 0.0;
 }
 
-constexpr int64_t kItemBytes = 96 << 10;    // that an item reads, if there is enough for every CTA
-constexpr int kSmallCtasPerSm = 6;
+// Bytes that an item of the fused kernels reads, if there is enough for every CTA: 16 x 4096 x
+// 1024 bf16 forward 159 us with 48 KB, 73 with 96, 66 with 160, 70 with 192 (backward 130, 130,
+// 113, 122): short items leave the waits bare, long ones lose the L2.
+constexpr int64_t kItemBytes = 160 << 10;
 
 }  // namespace
 
@@ -507,7 +510,7 @@ GnCut gn_cut(const GroupNormArgs& a, int piece, int most, int sms) {
   if (cut_whole(&c) && a.positions <= static_cast<int64_t>(most) * c.at_once) {
     // with samples enough for every CTA's threads, as few threads a sample as hold it;
     // else as many as it has work for
-    const int64_t resident = static_cast<int64_t>(kSmallCtasPerSm) * sms;
+    const int64_t resident = static_cast<int64_t>(a.dy != nullptr ? 3 : kSmallCtasPerSm) * sms;
     const bool many = a.samples * c.tiles >= resident * c.at_once;
     const int64_t rows = many ? up(a.positions, most) : (a.positions < c.at_once ? a.positions : c.at_once);
     c.by_lanes = lanes;
@@ -516,19 +519,6 @@ GnCut gn_cut(const GroupNormArgs& a, int piece, int most, int sms) {
     int64_t ctas = up(a.samples, c.teams), all = resident / c.tiles;
     if (all < 1) all = 1;
     c.ctas = static_cast<int32_t>(ctas < all ? ctas : all);
-    return c;
-  }
-  if (a.samples > 0 && cut_cluster(&c, a, piece, sms)) {
-    c.by_lanes = lanes;
-    const int64_t step = static_cast<int64_t>(c.wide) * piece * a.size;     // bytes from tile to tile
-    c.unit = a.size;
-    for (int unit : {16, 4}) {
-      if (unit > a.size && step % unit == 0 && static_cast<int64_t>(a.channels) * a.size % unit == 0 &&
-          on_grid(a.x, a.x_sample, a.x_position, a, a.size, unit) && on_grid(a.dy, a.dy_sample, a.dy_position, a, a.size, unit)) {
-        c.unit = unit;
-        break;
-      }
-    }
     return c;
   }
   const int64_t samples = a.samples > 0 ? a.samples : 1;
@@ -549,6 +539,26 @@ GnCut gn_cut(const GroupNormArgs& a, int piece, int most, int sms) {
   c.parts = static_cast<int32_t>(up(a.positions, c.part_rows));
   c.batch = static_cast<int32_t>(batch);
   c.ctas = c.batch * c.parts;
+  // What it takes: 13 us a batch, or 1.7 times the floor (3 and 5 times with pieces of 4 and 2
+  // bytes), and 8 us for the first statistics and the last results.
+  const int bytes = piece * a.size;
+  const double floor = static_cast<double>(samples) * static_cast<double>(a.positions) * a.channels * a.size * (a.dy != nullptr ? 3 : 2) / 6800.0;
+  const double work = floor * (bytes == 16 ? 1.7 : (bytes == 4 ? 3.0 : 5.0)), turns = 13000.0 * static_cast<double>(up(samples, batch));
+  const double fused = 8000.0 + (work > turns ? work : turns);
+  GnCut k = c;
+  if (a.samples > 0 && cut_cluster(&k, a, piece, sms, fused)) {
+    k.by_lanes = lanes;
+    const int64_t step = static_cast<int64_t>(k.wide) * piece * a.size;     // bytes from tile to tile
+    k.unit = a.size;
+    for (int unit : {16, 4}) {
+      if (unit > a.size && step % unit == 0 && static_cast<int64_t>(a.channels) * a.size % unit == 0 &&
+          on_grid(a.x, a.x_sample, a.x_position, a, a.size, unit) && on_grid(a.dy, a.dy_sample, a.dy_position, a, a.size, unit)) {
+        k.unit = unit;
+        break;
+      }
+    }
+    return k;
+  }
   return c;
 }
 

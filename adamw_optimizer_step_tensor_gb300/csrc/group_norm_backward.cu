@@ -37,40 +37,66 @@ __device__ __forceinline__ void gn_columns_out(const GroupNormArgs& a, const GnC
 }
 
 template <typename T, int N, bool SILU, int K>
-__global__ void __launch_bounds__(kGnThreads) gn_backward_small_kernel(const GroupNormArgs a, const GnCut c) {
+__global__ void __launch_bounds__(kGnThreads, K == 1 ? 3 : 2) gn_backward_small_kernel(const GroupNormArgs a, const GnCut c) {
   using P = GnPiece<T, N>;
   constexpr int kPairs = gn_pairs<N>();
   __shared__ float s_sum[kGnThreads], s_group[kGnThreads];
+  __shared__ float2 s_column[2 * kPairs][kGnThreads];     // sums of all but the last few samples
   const GnPlace<N> at(c);
   const int team = at.row0 / c.team_rows, row0 = at.row0 - team * c.team_rows;
   const bool mine = at.there && team < c.teams;
-  float2 w[kPairs], b[kPairs];
+  float2 w[kPairs], b[kPairs], col_w[kPairs] = {}, col_b[kPairs] = {};
   gn_weights<T, N>(a.weight, a.weight_f32, 1.0f, at, w);
   gn_weights<T, N>(a.bias, a.weight_f32, 0.0f, at, b);
+#pragma unroll
+  for (int j = 0; j < 2 * kPairs; ++j) s_column[j][threadIdx.x] = both(0.0f);
   const float inv = 1.0f / (static_cast<float>(a.positions) * static_cast<float>(c.per));
   const int rows = static_cast<int>(a.positions);
-  float2 all_w[kPairs] = {}, all_b[kPairs] = {}, col_w[kPairs] = {}, col_b[kPairs] = {};
+  const int64_t pace = static_cast<int64_t>(gridDim.x) * c.teams;
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * c.teams + team;
+  // of a lone piece the next sample's is on its way, with its statistics
+  const bool one_row = mine && row0 < rows;
+  const T* x = static_cast<const T*>(a.x) + first * a.x_sample + row0 * a.x_position + at.channel();
+  const T* dy = static_cast<const T*>(a.dy) + first * a.dy_sample + row0 * a.dy_position + at.channel();
+  const float *mean = a.mean + first * a.groups + at.group, *rstds = a.rstd + first * a.groups + at.group;
+  T* dx = static_cast<T*>(a.out) + first * a.out_sample + row0 * a.out_position + at.channel();
+  P next_x, next_dy;
+  float next_mean = 0.0f, next_rstd = 0.0f;
+  if (K == 1 && one_row && first < a.samples) {
+    next_x.load_last(x);
+    next_dy.load_last(dy);
+    next_mean = __ldg(mean);
+    next_rstd = __ldg(rstds);
+  }
   int since = 0;
-  for (int64_t n0 = static_cast<int64_t>(blockIdx.x) * c.teams; n0 < a.samples; n0 += static_cast<int64_t>(gridDim.x) * c.teams) {
-    const int64_t sample = n0 + team;
+  for (int64_t sample = first; sample - team < a.samples; sample += pace) {
     const bool live = mine && sample < a.samples;
-    const T* x = static_cast<const T*>(a.x) + sample * a.x_sample + at.channel();
-    const T* dy = static_cast<const T*>(a.dy) + sample * a.dy_sample + at.channel();
     P p[K], q[K];
-    float mean = 0.0f, rstd = 0.0f;
-    if (live) {
-#pragma unroll
-      for (int k = 0; k < K; ++k) {
-        const int l = row0 + k * c.team_rows;
-        if (l < rows) {
-          p[k].load_last(x + l * a.x_position);
-          q[k].load_last(dy + l * a.dy_position);
-        }
+    float start, rstd;
+    if constexpr (K == 1) {
+      p[0] = next_x;
+      q[0] = next_dy;
+      rstd = next_rstd;
+      start = -next_mean * rstd;
+      if (one_row && sample + pace < a.samples) {
+        next_x.load_last(x + pace * a.x_sample);
+        next_dy.load_last(dy + pace * a.dy_sample);
+        next_mean = __ldg(mean + pace * a.groups);
+        next_rstd = __ldg(rstds + pace * a.groups);
       }
-      mean = __ldg(a.mean + sample * a.groups + at.group);
-      rstd = __ldg(a.rstd + sample * a.groups + at.group);
+    } else {
+      rstd = start = 0.0f;
+      if (live) {
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+          if (row0 + k * c.team_rows < rows) {
+            p[k].load_last(x + k * c.team_rows * a.x_position);
+            q[k].load_last(dy + k * c.team_rows * a.dy_position);
+          }
+        rstd = __ldg(rstds);
+        start = -__ldg(mean) * rstd;
+      }
     }
-    const float start = -mean * rstd;
     float2 one = both(0.0f), two = both(0.0f);
 #pragma unroll
     for (int k = 0; k < K; ++k)
@@ -86,40 +112,41 @@ __global__ void __launch_bounds__(kGnThreads) gn_backward_small_kernel(const Gro
           two = fma2(g, xhat, two);
         }
       }
-    const float mean_g = gn_team_sum(one.x + one.y, c, s_sum, s_group) * inv;
-    const float mean_gx = gn_team_sum(two.x + two.y, c, s_sum, s_group) * inv;
+    const float mean_g = gn_team_sum(N == 1 ? one.x : one.x + one.y, c, s_sum, s_group) * inv;
+    const float mean_gx = gn_team_sum(N == 1 ? two.x : two.x + two.y, c, s_sum, s_group) * inv;
     if (++since == kFlush) {
       since = 0;
 #pragma unroll
       for (int i = 0; i < kPairs; ++i) {
-        all_w[i] = add2(all_w[i], col_w[i]);
-        all_b[i] = add2(all_b[i], col_b[i]);
+        s_column[2 * i][threadIdx.x] = add2(s_column[2 * i][threadIdx.x], col_w[i]);
+        s_column[2 * i + 1][threadIdx.x] = add2(s_column[2 * i + 1][threadIdx.x], col_b[i]);
         col_w[i] = col_b[i] = both(0.0f);
       }
     }
-    if (!live) continue;
-    T* dx = static_cast<T*>(a.out) + sample * a.out_sample + at.channel();
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int l = row0 + k * c.team_rows;
-      if (l < rows) {
+    for (int k = 0; k < K; ++k)
+      if (live && row0 + k * c.team_rows < rows) {
 #pragma unroll
         for (int i = 0; i < kPairs; ++i) {
           const float2 xhat = fma2(p[k].pair(i), both(rstd), both(start));
           const float2 dz = through<T, SILU>(q[k].pair(i), fma2(xhat, w[i], b[i]));
           p[k].set(i, mul2(both(rstd), fma2(xhat, both(-mean_gx), fma2(dz, w[i], both(-mean_g)))));
         }
-        p[k].store(dx + l * a.out_position);
+        p[k].store(dx + k * c.team_rows * a.out_position);
       }
-    }
+    x += pace * a.x_sample;
+    dy += pace * a.dy_sample;
+    dx += pace * a.out_sample;
+    mean += pace * a.groups;
+    rstds += pace * a.groups;
   }
   let_next_kernel_start();
 #pragma unroll
   for (int i = 0; i < kPairs; ++i) {
-    all_w[i] = add2(all_w[i], col_w[i]);
-    all_b[i] = add2(all_b[i], col_b[i]);
+    col_w[i] = add2(s_column[2 * i][threadIdx.x], col_w[i]);
+    col_b[i] = add2(s_column[2 * i + 1][threadIdx.x], col_b[i]);
   }
-  gn_columns_out<N>(a, c, at, all_w, all_b, s_sum);
+  gn_columns_out<N>(a, c, at, col_w, col_b, s_sum);
 }
 
 __device__ __forceinline__ float2 gn_from(float2 t, int lanes) {
