@@ -254,7 +254,7 @@ adamw_status adamw_router_plan_create(const adamw_router* r, int64_t max_tokens,
   cudaError_t e = prepare_router(*r);
   if (e != cudaSuccess) return failed(e, "prepare the routing kernels");
   e = cudaMalloc(&p->d_counts,
-                 static_cast<size_t>(router_chunks(sms)) * r->experts * sizeof(int32_t));
+                 static_cast<size_t>(router_chunks(sms)) * router_pitch(r->experts) * sizeof(int32_t));
   if (e != cudaSuccess) return failed(e, "cudaMalloc(router plan)", ADAMW_ENOMEM);
   *out = p.release();
   return ADAMW_OK;

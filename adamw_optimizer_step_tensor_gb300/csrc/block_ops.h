@@ -41,12 +41,16 @@ struct RouteArgs {
   const float* dweights;       // backward
   void* dlogits;               // backward
   int64_t dstride;
-  int32_t* counts;             // plan-owned: [chunks][experts]
+  int32_t* counts;             // plan-owned: [chunks][pitch]
+  int32_t pitch;               // experts, up to a multiple of four
+  int32_t per_group;           // experts of a group
+  int32_t group_factor;        // e * factor >> 20 is the group of e < 1024
   int32_t chunks;              // CTAs that share the tokens, in their order
   int32_t per_chunk;           // tokens of a chunk
 };
 // Chunks of a plan at most: its table of counts has as many rows.
 int router_chunks(int sms);
+int router_pitch(int experts);
 cudaError_t prepare_router(const adamw_router& router);
 cudaError_t launch_route(adamw_dtype dt, RouteArgs a, int sms, cudaStream_t s);
 cudaError_t launch_route_backward(adamw_dtype dt, const RouteArgs& a, int sms, cudaStream_t s);

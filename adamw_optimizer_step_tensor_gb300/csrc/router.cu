@@ -2,24 +2,33 @@
 // weights, every assignment's place when all are ordered by expert, the gradient of
 // the logits, and the balance step of the bias.
 //
-// One warp per token; lane l holds the logits of experts l V .. l V + V - 1.  The choice
-// is top_k rounds of two warp-wide reductions: the largest key as an ordered integer,
-// then the lowest expert that has it.  Where no bias takes part the order of the scores
-// is that of the logits, and no score is computed for it.
+// One warp per token; lane l holds experts l, l + 32, ...  A key is an ordered integer whose
+// lowest bits, as many as number a lane's experts, give way to the place i in the lane
+// (counted down), so that the choice is top_k rounds of one warp-wide maximum: it names the
+// place, a ballot the lane, and of equal keys the lowest expert wins.  Where no bias takes
+// part the order of the scores is that of the logits, and no score is computed for it.
 //
-// With a bias the keys are score + bias in float32, which are off by a few units of
-// their last bits.  A choice in which any two keys that matter lie closer than that
-// (about one token in a thousand) is made again from 64-bit scores, so that the experts
-// are those of the definition and not of a rounding.
+// float32 keys are off by a few units of the scores' last bits, more for the bits given
+// away (16-bit logits have none there).  A choice in which two keys that matter lie closer
+// than that (about one token in a thousand) is made again from 64-bit scores, so that the
+// experts are those of the definition and not of a rounding.
+//
+// What bounds it: the rounds' latency, about 60 instructions each at 256 experts, against
+// which an SM has 32 warps; the next token's logits are loaded ahead.  A round of a maximum
+// and a minimum over untouched keys, with a scan of a lane's experts for each, took twice
+// the instructions.
 #include "block_ops.h"
 #include "rows.cuh"
 
 namespace adamw {
 namespace {
 
-constexpr int kRouteWarps = 16;
-constexpr int kRouteThreads = 32 * kRouteWarps;
 constexpr int kBackWarps = 8;
+constexpr int kPlaceThreads = 1024;
+
+// Warps of the routing kernel's CTA: with many experts in registers fewer fit.
+template <int V>
+__host__ __device__ constexpr int route_warps() { return V <= 8 ? 32 : 16; }
 
 // Floats as integers of the same order; 0 is below all of them and means "not there".
 __device__ __forceinline__ uint32_t ordered(float x) {
@@ -41,111 +50,80 @@ __device__ __forceinline__ float warp_sum(float x) {
 }
 __device__ __forceinline__ float sigmoid(float z) { return __fdividef(1.0f, 1.0f + expf(-z)); }
 
-// Lane l's V logits, -inf behind the last expert.
-template <typename T, int V>
-__device__ __forceinline__ void load_row(const T* row, int experts, bool vec, float (&z)[V]) {
-  const int lane = threadIdx.x & 31;
-  constexpr int kBytes = V * static_cast<int>(sizeof(T));
-  if constexpr (kBytes >= 4) {
-    if (vec) {                          // 32 V experts, rows on the grid of a lane's bytes
-      constexpr int kWords = kBytes / 4;
-      uint32_t w[kWords];
-      const T* p = row + lane * V;
-      if constexpr (kBytes >= 16) {
-#pragma unroll
-        for (int i = 0; i < kWords / 4; ++i) {
-          const uint4 q = __ldcs(reinterpret_cast<const uint4*>(p) + i);
-          w[4 * i] = q.x;
-          w[4 * i + 1] = q.y;
-          w[4 * i + 2] = q.z;
-          w[4 * i + 3] = q.w;
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < kWords; ++i) w[i] = __ldcs(reinterpret_cast<const uint32_t*>(p) + i);
-      }
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        if constexpr (sizeof(T) == 4) {
-          z[i] = __uint_as_float(w[i]);
-        } else {
-          const float2 f = unpack_pair<T>(w[i / 2]);
-          z[i] = i % 2 == 0 ? f.x : f.y;
-        }
-      }
-      return;
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int e = lane * V + i;
-    z[i] = e < experts ? to_f32(row[e]) : -INFINITY;
-  }
-}
-
-// The weight of lane j's chosen logit z before `scale`; `row_top` and `row_sum` are the
-// softmax's largest logit and sum over the whole row (used without renormalisation).
+// The weight of a lane's chosen logit z before `scale`, among the `wide` (a power of two)
+// neighbouring lanes of its token; `row_top` and `row_sum` are the softmax's largest logit
+// and sum over the whole row (used without renormalisation).
 __device__ __forceinline__ float weight_of(float z, bool chosen, const adamw_router& r,
-                                           float row_top, float row_sum) {
+                                           float row_top, float row_sum, int wide) {
   if (r.renormalise) {
     // Only ratios count, so small scores are taken relative to the largest chosen one:
     // below a logit of -30 the sigmoid is e^z to the last bit.
-    const float top = warp_max(chosen ? z : -INFINITY);
+    float top = chosen ? z : -INFINITY;
+    for (int o = wide / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
     const bool ratio = r.score == ADAMW_SCORE_SOFTMAX || top < -30.0f;
     const float s = chosen ? (ratio ? expf(z - top) : sigmoid(z)) : 0.0f;
-    const float total = warp_sum(s);
+    float total = s;
+    for (int o = wide / 2; o > 0; o >>= 1) total += __shfl_xor_sync(kFull, total, o);
     return chosen ? __fdiv_rn(s, total) : 0.0f;
   }
   if (!chosen) return 0.0f;
   return r.score == ADAMW_SCORE_SOFTMAX ? __fdiv_rn(expf(z - row_top), row_sum) : sigmoid(z);
 }
+// Lanes of a token: the smallest power of two that holds its choice.
+__host__ __device__ __forceinline__ int choice_lanes(int top_k) {
+  int w = 1;
+  while (w < top_k) w *= 2;
+  return w;
+}
 
 // ---------------------------------------------------------------- the choice
 
-// Best of lane-held keys: the largest, and the lowest expert that has it.  Returns
-// false when none is there.  `at` is what each lane's best key stands for.
-__device__ __forceinline__ bool warp_best(uint32_t key, uint32_t at, uint32_t* best_key,
-                                          uint32_t* best_at) {
-  *best_key = __reduce_max_sync(kFull, key);
-  *best_at = __reduce_min_sync(kFull, key == *best_key ? at : 0xFFFFFFFFu);
-  return *best_key != 0;
-}
-__device__ __forceinline__ bool warp_best(uint64_t key, uint32_t at, uint64_t* best_key,
-                                          uint32_t* best_at) {
-  const uint32_t hi = __reduce_max_sync(kFull, static_cast<uint32_t>(key >> 32));
-  const uint32_t lo = __reduce_max_sync(
-      kFull, static_cast<uint32_t>(key >> 32) == hi ? static_cast<uint32_t>(key) : 0u);
-  *best_key = static_cast<uint64_t>(hi) << 32 | lo;
-  *best_at = __reduce_min_sync(kFull, key == *best_key ? at : 0xFFFFFFFFu);
-  return *best_key != 0;
-}
 __device__ __forceinline__ uint64_t ordered64(double x) {
   const uint64_t b = static_cast<uint64_t>(__double_as_longlong(x + 0.0));
   return (b >> 63) != 0 ? ~b : b | 0x8000000000000000ull;
 }
+// The largest of the lanes' keys, and the lowest `at` of the lanes that have it; false when
+// no key is there.
+__device__ __forceinline__ bool warp_best(uint64_t key, uint32_t at, uint32_t* best_at) {
+  const uint32_t hi = __reduce_max_sync(kFull, static_cast<uint32_t>(key >> 32));
+  const uint32_t lo = __reduce_max_sync(
+      kFull, static_cast<uint32_t>(key >> 32) == hi ? static_cast<uint32_t>(key) : 0u);
+  const uint64_t best = static_cast<uint64_t>(hi) << 32 | lo;
+  *best_at = __reduce_min_sync(kFull, key == best ? at : 0xFFFFFFFFu);
+  return best != 0;
+}
 
-// The 64-bit choice, over the warp's own array of keys (in shared memory; -inf: not
-// there).  Lane j gets the j-th expert, -1 without one.
-__device__ __noinline__ int choose_exactly(const float* z, const float* bias, double* key,
+// The 64-bit choice from a token's logits, over the warp's own array of keys (in shared
+// memory; -inf: not there).  by_logit: whatever the bias, the order is that of the logits, and
+// `bad` that of groups too.  Lane j gets the j-th expert, -1 without one.
+template <typename T>
+__device__ __noinline__ int choose_exactly(const T* row, const float* bias, bool by_logit, bool bad, double* key,
                                            const adamw_router& r) {
   const int lane = threadIdx.x & 31, per = r.experts / r.groups;
-  double top = -INFINITY, total = 0.0;
-  if (r.score == ADAMW_SCORE_SOFTMAX) {
-    for (int e = lane; e < r.experts; e += 32) top = fmax(top, static_cast<double>(z[e]));
+  const bool by_group = r.groups > 1 && r.top_groups < r.groups;
+  const bool scores = !bad && (!by_logit || (by_group && r.group_score == ADAMW_GROUP_TOP2));
+  double top = -INFINITY, total = 1.0;
+  if (scores && r.score == ADAMW_SCORE_SOFTMAX) {
+    for (int e = lane; e < r.experts; e += 32) top = fmax(top, static_cast<double>(to_f32(row[e])));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmax(top, __shfl_xor_sync(kFull, top, o));
-    for (int e = lane; e < r.experts; e += 32) total += exp(static_cast<double>(z[e]) - top);
+    total = 0.0;
+    for (int e = lane; e < r.experts; e += 32) total += exp(static_cast<double>(to_f32(row[e])) - top);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(kFull, total, o);
   }
   for (int e = lane; e < r.experts; e += 32) {
-    const double v = z[e];
+    const float z = to_f32(row[e]);
     const float b = bias != nullptr ? bias[e] : 0.0f;
-    const double s = r.score == ADAMW_SCORE_SOFTMAX ? exp(v - top) / total : 1.0 / (1.0 + exp(-v));
-    key[e] = z[e] > -INFINITY && b > -INFINITY ? s + static_cast<double>(b) : -INFINITY;
+    double s = z;
+    if (scores) {
+      s = r.score == ADAMW_SCORE_SOFTMAX ? exp(z - top) / total : 1.0 / (1.0 + exp(-s));
+      if (!by_logit) s += static_cast<double>(b);
+    }
+    key[e] = z > -INFINITY && b > -INFINITY ? s : -INFINITY;       // a NaN is not there
   }
   __syncwarp();
-  if (r.groups > 1) {
+  if (by_group) {
     double of = -INFINITY;
     if (lane < r.groups) {
       double one = -INFINITY, two = -INFINITY;
@@ -158,14 +136,13 @@ __device__ __noinline__ int choose_exactly(const float* z, const float* bias, do
           two = v;
         }
       }
-      of = r.group_score == ADAMW_GROUP_TOP2 && two > -INFINITY ? one + two : one;
+      of = r.group_score == ADAMW_GROUP_TOP2 && !bad && two > -INFINITY ? one + two : one;
     }
     uint64_t mine = of > -INFINITY ? ordered64(of) : 0;
     uint32_t kept = 0;
     for (int g = 0; g < r.top_groups; ++g) {
-      uint64_t k;
       uint32_t at;
-      if (!warp_best(mine, lane, &k, &at)) break;
+      if (!warp_best(mine, lane, &at)) break;
       kept |= 1u << at;
       if (lane == static_cast<int>(at)) mine = 0;
     }
@@ -173,9 +150,9 @@ __device__ __noinline__ int choose_exactly(const float* z, const float* bias, do
       if ((kept >> (e / per) & 1u) == 0) key[e] = -INFINITY;
     __syncwarp();
   }
-  if (bias == nullptr) {                // in the groups the order is that of the logits
+  if (by_logit) {
     for (int e = lane; e < r.experts; e += 32)
-      if (key[e] > -INFINITY) key[e] = z[e];
+      if (key[e] > -INFINITY) key[e] = to_f32(row[e]);
     __syncwarp();
   }
   int id = -1;
@@ -189,9 +166,8 @@ __device__ __noinline__ int choose_exactly(const float* z, const float* bias, do
         at = e;
       }
     }
-    uint64_t k;
     uint32_t win;
-    if (!warp_best(best, at, &k, &win)) break;
+    if (!warp_best(best, at, &win)) break;
     if (lane == j) id = static_cast<int>(win);
     if (lane == static_cast<int>(win % 32)) key[win] = -INFINITY;
     __syncwarp();
@@ -199,150 +175,139 @@ __device__ __noinline__ int choose_exactly(const float* z, const float* bias, do
   return id;
 }
 
-// How far a float32 key may be off: a score's relative error (sigmoid: the exponential's,
-// the quotient's and the sum's few units; softmax: the exponent's rounding too, |z - top|
-// 2^-24, up to where the exponential is 0) and the sum's.  |score| <= |key| + |bias|.
-__device__ __forceinline__ float key_error(float key, float bias, float relative) {
-  return fmaf(relative, fabsf(key) + 2.0f * fabsf(bias), 1e-36f);
+template <int V>
+__device__ __forceinline__ uint32_t largest(const uint32_t (&key)[V]) {
+  uint32_t best = key[0];
+#pragma unroll
+  for (int i = 1; i < V; ++i) best = max(best, key[i]);
+  return best;
 }
 
-// Chooses from the lanes' logits.  bias: null, or shared memory.  Lane j gets the j-th
-// expert (-1: none).  `z_row` and `exact` are shared memory of this warp alone.
-template <int V>
-__device__ __forceinline__ int choose(const float (&z)[V], const float* bias, bool bad, float top,
-                                      float total, float* z_row, double* exact,
-                                      const adamw_router& r) {
-  const int lane = threadIdx.x & 31;
-  const int per = r.experts / r.groups;
+// Chooses from the lanes' logits (NaN as -inf).  bias: null, or shared memory with its largest
+// finite magnitude.  Lane j gets the j-th expert (-1: none).  `own`: shared memory of this warp.
+template <typename T, int V>
+__device__ __forceinline__ int choose(const T* row, const float (&z)[V], const float* bias, float bias_max, bool bad, float top,
+                                      float total, double* own, const RouteArgs& a) {
+  const adamw_router& r = a.router;
+  constexpr uint32_t kPlace = V - 1;       // V is a power of two
+  const int lane = threadIdx.x & 31, per = a.per_group;
+  const bool softmax = r.score == ADAMW_SCORE_SOFTMAX;
   const bool by_logit = bias == nullptr || bad;
   const bool by_group = r.groups > 1 && r.top_groups < r.groups;
   const bool two = by_group && r.group_score == ADAMW_GROUP_TOP2 && !bad;
-  const float relative = r.score == ADAMW_SCORE_SOFTMAX ? 0x1p-17f : 0x1p-20f;
-  uint32_t key[V];
+  // Errors of a score are at most 2^-20 of the row's largest (of 1 for the sigmoid): the
+  // exponential's and the quotient's few units, the sum's, and for softmax the rounding of
+  // z - top, where |d| e^-d < 1.  The place takes V units of the key's last bit.
+  const float off = (0x1p-20f + V * 0x1p-23f) * ((softmax ? __fdividef(1.0f, total) : 1.0f) + 3.0f * bias_max) + 1e-36f;
+  const float inv = __fdividef(1.0f, total);
+  float k[V];
+  uint32_t there = 0;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    float k = z[i];
-    bool there = z[i] > -INFINITY;
+    const int e = 32 * i + lane;
+    k[i] = z[i];
+    bool on = z[i] > -INFINITY;
     if (bias != nullptr) {
-      const int e = lane * V + i;
-      const float b = e < r.experts ? bias[e] : 0.0f;
-      there = there && b > -INFINITY;
-      if (!bad) {
-        const float s = r.score == ADAMW_SCORE_SOFTMAX ? __fdividef(expf(z[i] - top), total)
-                                                       : sigmoid(z[i]);
-        k = s + b;
-      }
+      const float b = e < r.experts ? bias[e] : -INFINITY;
+      on = on && b > -INFINITY;
+      if (!bad) k[i] = (softmax ? expf(z[i] - top) * inv : sigmoid(z[i])) + b;
     }
-    key[i] = there ? ordered(k) : 0u;
+    there |= on ? 1u << i : 0u;
   }
   bool sure = true;
   if (by_group) {
-    // lane g scores group g
-    __syncwarp();
+    // lane g scores group g: its largest keys one and next
+    float one = -INFINITY, next = -INFINITY;
+    if (per == 32 && V <= 8) {             // a group is one place of every lane
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int e = lane * V + i;
-      if (e < r.experts) {
-        float k = key[i] != 0 ? unordered(key[i]) : -INFINITY;
-        if (two && by_logit && key[i] != 0)
-          k = r.score == ADAMW_SCORE_SOFTMAX ? __fdividef(expf(k - top), total) : sigmoid(k);
-        z_row[e] = k;
-      }
-    }
-    __syncwarp();
-    float one = -INFINITY, next = -INFINITY, off = 0.0f;
-    if (lane < r.groups) {
-      for (int i = 0; i < per; ++i) {
-        const float v = z_row[lane * per + i];
-        next = fmaxf(next, fminf(one, v));
-        one = fmaxf(one, v);
-      }
-      if (!bad && (two || !by_logit)) {
-        float b = 0.0f;                 // the group's largest bias bounds every key's error
-        if (!by_logit)
-          for (int i = 0; i < per; ++i) {
-            const float v = fabsf(bias[lane * per + i]);
-            b = v < INFINITY ? fmaxf(b, v) : b;
+      for (int i = 0; i < V; ++i) {
+        if (i < r.groups) {
+          float v = k[i];
+          if (two && by_logit) v = softmax ? expf(v - top) * inv : sigmoid(v);
+          uint32_t o = (there >> i & 1u) != 0 ? ordered(v) : 0u;
+          const uint32_t first = __reduce_max_sync(kFull, o);
+          uint32_t second = 0;
+          if (two) {
+            if (lane == __ffs(__ballot_sync(kFull, o == first)) - 1) o = 0u;
+            second = __reduce_max_sync(kFull, o);
           }
-        off = key_error(one, b, relative) + (two && next > -INFINITY ? key_error(next, b, relative) : 0.0f);
+          if (lane == i) {
+            one = first != 0 ? unordered(first) : -INFINITY;
+            next = second != 0 ? unordered(second) : -INFINITY;
+          }
+        }
       }
+    } else {
+      float* s = reinterpret_cast<float*>(own);
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int e = 32 * i + lane;
+        if (e < r.experts) {
+          float v = k[i];
+          if (two && by_logit) v = softmax ? expf(v - top) * inv : sigmoid(v);
+          s[e] = (there >> i & 1u) != 0 ? v : -INFINITY;
+        }
+      }
+      __syncwarp();
+      if (lane < r.groups)
+        for (int i = 0; i < per; ++i) {
+          const float v = s[lane * per + i];
+          next = fmaxf(next, fminf(one, v));
+          one = fmaxf(one, v);
+        }
+      __syncwarp();
     }
     const float of = two && next > -INFINITY ? one + next : one;
-    uint32_t mine = of > -INFINITY ? ordered(of) : 0u;
-    uint32_t kept = 0;
-    float least = INFINITY;             // of a kept group's score, at its lowest
+    uint32_t mine = lane < r.groups && of > -INFINITY ? ordered(of) : 0u, kept = 0, least = 0;
     for (int g = 0; g < r.top_groups; ++g) {
-      uint32_t k, at;
-      if (!warp_best(mine, lane, &k, &at)) break;
+      const uint32_t best = __reduce_max_sync(kFull, mine);
+      if (best == 0) break;
+      const int at = __ffs(__ballot_sync(kFull, mine == best)) - 1;
       kept |= 1u << at;
-      if (lane == static_cast<int>(at)) {
-        mine = 0;
-        least = of - off;
-      }
+      least = best;
+      if (lane == at) mine = 0;
     }
-    const float most = warp_max(mine != 0 ? of + off : -INFINITY);
-    const float low = -warp_max(-least);
-    // without errors equal scores went to the lowest group already
-    sure = (!two && by_logit) || most < low || most == -INFINITY;
+    const uint32_t most = __reduce_max_sync(kFull, mine);
+    // without scores equal groups went to the lowest already
+    sure = (!two && by_logit) || most == 0 || unordered(least) - unordered(most) > 4.0f * off;
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int e = lane * V + i;
-      if (e < r.experts && (kept >> (e / per) & 1u) == 0) key[i] = 0;
-    }
+    for (int i = 0; i < V; ++i)
+      if ((kept >> ((32 * i + lane) * a.group_factor >> 20) & 1u) == 0) there &= ~(1u << i);
   }
+  uint32_t key[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+    key[i] = (there >> i & 1u) != 0 ? (ordered(k[i]) & ~kPlace) | (kPlace - i) : 0u;
   int id = -1;
-  uint32_t id_key = 0;
+  uint32_t mine = 0, best = largest(key);
   for (int j = 0; j < r.top_k; ++j) {
-    uint32_t best = 0, at = 0xFFFFFFFFu;
-#pragma unroll
-    for (int i = V - 1; i >= 0; --i)
-      if (key[i] >= best && key[i] != 0) {
-        best = key[i];
-        at = lane * V + i;
-      }
-    uint32_t k, win;
-    if (!warp_best(best, at, &k, &win)) break;
+    const uint32_t most = __reduce_max_sync(kFull, best);
+    if (most == 0) break;
+    const int who = __ffs(__ballot_sync(kFull, best == most)) - 1;
+    const int place = static_cast<int>(kPlace - (most & kPlace));
     if (lane == j) {
-      id = static_cast<int>(win);
-      id_key = k;
+      id = 32 * place + who;
+      mine = most;
     }
+    const int gone = lane == who ? place : -1;
 #pragma unroll
     for (int i = 0; i < V; ++i)
-      if (static_cast<int>(win) == lane * V + i) key[i] = 0;
+      if (gone == i) key[i] = 0;
+    best = largest(key);
   }
-  if (!by_logit) {
-    // each chosen key, at its lowest, above all that come after it, at their highest
-    float high = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (key[i] != 0) {
-        const float k = unordered(key[i]);
-        high = fmaxf(high, k + key_error(k, bias[lane * V + i], relative));
-      }
-    high = warp_max(high);
-    const float k = id >= 0 ? unordered(id_key) : -INFINITY;
-    const float off = id >= 0 ? key_error(k, bias[id], relative) : 0.0f;
-    float after = id >= 0 ? k + off : high;
-    if (lane == 31 || lane >= r.top_k) after = fmaxf(after, high);
-    // the largest of the lanes after this one
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const float v = __shfl_down_sync(kFull, after, o);
-      if (lane + o < 32) after = fmaxf(after, v);
-    }
-    after = __shfl_down_sync(kFull, after, 1);
-    if (lane == 31) after = high;
-    sure = sure && (id < 0 || k - off > after || after == -INFINITY);
+  // each chosen key is far enough above the one that comes after it
+  if (!by_logit || sizeof(T) == 4) {
+    const uint32_t rest = __reduce_max_sync(kFull, best);
+    uint32_t after = __shfl_down_sync(kFull, mine, 1);
+    if (lane == 31 || after == 0) after = rest;
+    mine &= ~kPlace;
+    after &= ~kPlace;
+    if (id >= 0 && after != 0)
+      sure = sure && (by_logit ? (V == 1 || mine != after) : unordered(mine) - unordered(after) > 2.0f * off);
   }
   if (!__all_sync(kFull, sure)) {
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int e = lane * V + i;
-      if (e < r.experts) z_row[e] = z[i];
-    }
-    __syncwarp();
-    id = choose_exactly(z_row, by_logit ? nullptr : bias, exact, r);
+    id = choose_exactly(row, bias, by_logit, bad, own, r);
     __syncwarp();
   }
   return id;
@@ -354,16 +319,29 @@ __device__ __forceinline__ int choose(const float (&z)[V], const float* bias, bo
 // each expert the assignments of the chunks before this one, and of all chunks (shared
 // memory, [experts]); `of_warp`: shared memory [warps][experts].
 __device__ __forceinline__ void place_chunk(const RouteArgs& a, int first, int tokens, int* before,
-                                            const int* all, int* of_warp, int* s_scan, bool write_starts) {
+                                            const int* all, int* of_warp, int warps, int* s_scan, bool write_starts) {
   const int experts = a.router.experts;
-  const int warps = blockDim.x / 32, warp = threadIdx.x / 32, lane = threadIdx.x & 31;
-  // exclusive sum over the experts of all chunks' counts
+  const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+  // the warps' runs of assignments are counted while the first warp adds up the experts
+  const int n = tokens * a.router.top_k;
+  const int run = (n + warps - 1) / warps;
+  const int lo = warp < warps ? min(n, warp * run) : n, hi = min(n, lo + run);
+  const int64_t base = static_cast<int64_t>(first) * a.router.top_k;
+  for (int i = threadIdx.x; i < warps * experts; i += blockDim.x) of_warp[i] = 0;
   __syncthreads();
-  int carry = 0;
-  for (int e0 = 0; e0 < experts; e0 += blockDim.x) {
-    const int e = e0 + threadIdx.x;
-    const int n = e < experts ? all[e] : 0;
-    int sum = n;
+  int id = lo + lane < hi ? __ldcg(a.ids + base + lo + lane) : -1;
+  if (id >= 0) atomicAdd(&of_warp[warp * experts + id], 1);
+  for (int i = lo + 32 + lane; i < hi; i += 32) {
+    const int e = __ldcg(a.ids + base + i);
+    if (e >= 0) atomicAdd(&of_warp[warp * experts + e], 1);
+  }
+  // exclusive sum of all chunks' counts over the experts, 1024 of them at most
+  const int e = threadIdx.x;
+  int sum = 0;
+  for (int e0 = 0, carry = 0; e0 < experts; e0 += blockDim.x) {
+    const int x = e0 + e;
+    const int c = x < experts ? all[x] : 0;
+    sum = c;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int v = __shfl_up_sync(kFull, sum, o);
@@ -371,43 +349,34 @@ __device__ __forceinline__ void place_chunk(const RouteArgs& a, int first, int t
     }
     if (lane == 31) s_scan[warp] = sum;
     __syncthreads();
-    int ahead = carry;
-    for (int w = 0; w < warp; ++w) ahead += s_scan[w];
-    int whole = carry;
-    for (int w = 0; w < warps; ++w) whole += s_scan[w];
-    if (e < experts) {
-      const int start = ahead + sum - n;
-      before[e] += start;
-      if (write_starts) a.starts[e] = start;
+    int w = lane < static_cast<int>(blockDim.x / 32) ? s_scan[lane] : 0;
+    int whole = w;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(kFull, whole, o);
+      if (lane >= o) whole += v;
     }
-    carry = whole;
+    const int ahead = carry + __shfl_sync(kFull, whole - w, warp) + sum - c;
+    if (x < experts) {
+      before[x] += ahead;
+      if (write_starts) a.starts[x] = ahead;
+    }
+    carry += __shfl_sync(kFull, whole, 31);
+    if (write_starts && x + 1 == experts) a.starts[experts] = ahead + c;
     __syncthreads();
   }
-  if (write_starts && threadIdx.x == 0) a.starts[experts] = carry;
-  // each warp's run of assignments: counts, then places in order
-  for (int i = threadIdx.x; i < warps * experts; i += blockDim.x) of_warp[i] = 0;
-  __syncthreads();
-  const int n = tokens * a.router.top_k;
-  const int run = (n + warps - 1) / warps;
-  const int lo = min(n, warp * run), hi = min(n, lo + run);
-  const int64_t base = static_cast<int64_t>(first) * a.router.top_k;
-  for (int i = lo + lane; i < hi; i += 32) {
-    const int id = __ldcg(a.ids + base + i);
-    if (id >= 0) atomicAdd(&of_warp[warp * experts + id], 1);
-  }
-  __syncthreads();
-  for (int e = threadIdx.x; e < experts; e += blockDim.x) {
-    int sum = before[e];
+  for (int x = threadIdx.x; x < experts; x += blockDim.x) {
+    int at = before[x];
     for (int w = 0; w < warps; ++w) {
-      const int c = of_warp[w * experts + e];
-      of_warp[w * experts + e] = sum;
-      sum += c;
+      const int c = of_warp[w * experts + x];
+      of_warp[w * experts + x] = at;
+      at += c;
     }
   }
   __syncthreads();
   for (int i0 = lo; i0 < hi; i0 += 32) {
     const int i = i0 + lane;
-    const int id = i < hi ? __ldcg(a.ids + base + i) : -1;
+    if (i0 > lo) id = i < hi ? __ldcg(a.ids + base + i) : -1;
     const uint32_t same = __match_any_sync(kFull, id);
     int slot = -1;
     if (id >= 0) slot = of_warp[warp * experts + id] + __popc(same & ((1u << lane) - 1u));
@@ -418,62 +387,83 @@ __device__ __forceinline__ void place_chunk(const RouteArgs& a, int first, int t
   }
 }
 
-// Warps that a CTA's places take: their counts fill at most 64 KB.
-__host__ __device__ __forceinline__ int place_warps(int experts) {
+// Warps among which a chunk's assignments are dealt out: their counts fill at most 64 KB.
+__host__ __device__ __forceinline__ int place_warps(int experts, int most) {
   const int w = 16384 / experts;
-  return w < 1 ? 1 : (w > kRouteWarps ? kRouteWarps : w);
+  return w < most ? w : most;
 }
 
 // ---------------------------------------------------------------- kernels
 
-// Shared memory of the routing kernel: the bias, this chunk's counts, and per warp a row
-// of logits and one of 64-bit keys; the places use the rows' part again.
 __host__ __device__ __forceinline__ int even(int n) { return (n + 1) & ~1; }
+// Shared memory of the routing kernel: per warp a row of 64-bit keys (the places of a lone
+// chunk use them again), the bias, this chunk's counts and its places' starts.
+template <int V>
 __host__ __device__ __forceinline__ size_t route_smem(int experts) {
-  return sizeof(float) * (3 * even(experts)) + static_cast<size_t>(kRouteWarps) * even(experts) * 12;
+  return static_cast<size_t>(route_warps<V>()) * even(experts) * sizeof(double) + sizeof(float) * 3 * even(experts);
+}
+
+// Lane l's V logits, -inf behind the last expert.
+template <typename T, int V>
+__device__ __forceinline__ void load_row(const T* row, int experts, T (&z)[V]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int e = 32 * i + lane;
+    z[i] = e < experts ? __ldcs(row + e) : from_f32<T>(-INFINITY);
+  }
 }
 
 template <typename T, int V>
-__global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteArgs a, const bool vec) {
+__global__ void __launch_bounds__(32 * route_warps<V>(), 1) route_kernel(const RouteArgs a) {
+  constexpr int kWarps = route_warps<V>(), kThreads = 32 * kWarps;
   extern __shared__ double s_all[];
   const int experts = a.router.experts, even_experts = even(experts);
-  double* s_exact = s_all;                                        // [warps][even]
-  float* s_rows = reinterpret_cast<float*>(s_exact + kRouteWarps * even_experts);
-  float* s_bias = s_rows + kRouteWarps * even_experts;
+  float* s_bias = reinterpret_cast<float*>(s_all + kWarps * even_experts);
   int* s_counts = reinterpret_cast<int*>(s_bias + even_experts);
   int* s_before = s_counts + even_experts;
   __shared__ int s_scan[32];
+  __shared__ uint32_t s_bias_max;
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
   const int first = blockIdx.x * a.per_chunk;
   const int tokens = min(a.tokens - first, a.per_chunk);
+  const T* rows = static_cast<const T*>(a.logits) + static_cast<int64_t>(first) * a.stride;
+  T next[V];
+  if (warp < tokens) load_row<T, V>(rows + warp * a.stride, experts, next);
+  if (threadIdx.x == 0) s_bias_max = 0;
+  __syncthreads();
   bool any = false;
-  for (int e = threadIdx.x; e < experts; e += kRouteThreads) {
+  for (int e = threadIdx.x; e < experts; e += kThreads) {
     s_counts[e] = 0;
     if (a.bias != nullptr) {
       const float b = __ldg(a.bias + e);
       s_bias[e] = b > -INFINITY ? b : -INFINITY;                  // NaN: not there
       any = any || !(b == 0.0f);
+      if (fabsf(b) < INFINITY) atomicMax(&s_bias_max, __float_as_uint(fabsf(b)));
     }
   }
   // a bias of zeros changes nothing
   const float* bias = __syncthreads_or(any) ? s_bias : nullptr;
+  const float bias_max = __uint_as_float(s_bias_max);
   const bool softmax = a.router.score == ADAMW_SCORE_SOFTMAX;
   // the row's largest logit and sum: for softmax keys and weights
   const bool sums = softmax && (bias != nullptr || !a.router.renormalise ||
                                 (a.router.groups > 1 && a.router.group_score == ADAMW_GROUP_TOP2));
-  for (int t = warp; t < tokens; t += kRouteWarps) {
-    const T* row = static_cast<const T*>(a.logits) + (static_cast<int64_t>(first) + t) * a.stride;
+  const int wide = choice_lanes(a.router.top_k);
+  for (int t = warp; t < tokens; t += kWarps) {
+    const T* row = rows + t * a.stride;
     float z[V];
-    load_row<T, V>(row, experts, vec, z);
     bool nan = false, inf = false;
     float top = -INFINITY, total = 1.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
+      z[i] = to_f32(next[i]);
       nan = nan || z[i] != z[i];
       inf = inf || z[i] == INFINITY;
       z[i] = z[i] == z[i] ? z[i] : -INFINITY;
       top = fmaxf(top, z[i]);
     }
+    if (t + kWarps < tokens) load_row<T, V>(row + kWarps * a.stride, experts, next);
     const bool bad = __any_sync(kFull, nan || (softmax && inf));
     if (sums) {
       top = warp_max(top);
@@ -482,10 +472,9 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteArgs a,
       for (int i = 0; i < V; ++i) sum += z[i] > -INFINITY ? expf(z[i] - top) : 0.0f;
       total = warp_sum(sum);
     }
-    const int id = choose<V>(z, bias, bad, top, total, s_rows + warp * even_experts,
-                             s_exact + warp * even_experts, a.router);
+    const int id = choose<T, V>(row, z, bias, bias_max, bad, top, total, s_all + warp * even_experts, a);
     const float zj = id >= 0 ? to_f32(row[id]) : 0.0f;
-    float w = a.router.scale * weight_of(zj, id >= 0, a.router, top, total);
+    float w = a.router.scale * weight_of(zj, id >= 0, a.router, top, total, wide);
     if (bad) w = __int_as_float(0x7FFFFFFF);
     if (lane < a.router.top_k) {
       const int64_t at = (static_cast<int64_t>(first) + t) * a.router.top_k + lane;
@@ -494,131 +483,162 @@ __global__ void __launch_bounds__(kRouteThreads) route_kernel(const RouteArgs a,
       if (id >= 0) atomicAdd(&s_counts[id], 1);
     }
   }
-  if (a.slots == nullptr && a.starts == nullptr) return;
+  if (a.starts == nullptr) return;
   __syncthreads();
   if (gridDim.x == 1) {
-    for (int e = threadIdx.x; e < experts; e += kRouteThreads) s_before[e] = 0;
-    place_chunk(a, first, tokens, s_before, s_counts, reinterpret_cast<int*>(s_all), s_scan, true);
+    for (int e = threadIdx.x; e < experts; e += kThreads) s_before[e] = 0;
+    place_chunk(a, first, tokens, s_before, s_counts, reinterpret_cast<int*>(s_all), place_warps(experts, kWarps), s_scan, true);
   } else {
-    for (int e = threadIdx.x; e < experts; e += kRouteThreads)
-      a.counts[static_cast<int64_t>(blockIdx.x) * experts + e] = s_counts[e];
+    for (int e = threadIdx.x; e < experts; e += kThreads)
+      a.counts[static_cast<int64_t>(blockIdx.x) * a.pitch + e] = s_counts[e];
     let_next_kernel_start();
   }
 }
 
-// Every chunk's places from the table of counts.
-__global__ void __launch_bounds__(kRouteThreads) place_kernel(const RouteArgs a) {
+// Every chunk's places from the table of counts, rows of `pitch` (a multiple of four).
+__global__ void __launch_bounds__(kPlaceThreads) place_kernel(const RouteArgs a) {
   extern __shared__ int s_place[];
   __shared__ int s_scan[32];
   const int experts = a.router.experts;
   int* before = s_place;
-  int* all = before + experts;
-  int* of_warp = all + experts;
-  for (int e = threadIdx.x; e < 2 * experts; e += blockDim.x) before[e] = 0;
+  int* all = before + a.pitch;
+  int* of_warp = all + a.pitch;
+  for (int e = threadIdx.x; e < 2 * a.pitch; e += kPlaceThreads) before[e] = 0;
   wait_for_previous_kernel();
   __syncthreads();
-  // thread = an expert and every `step`-th chunk; sums of whole numbers in any order
-  const int wide = min(experts, static_cast<int>(blockDim.x));
-  const int step = blockDim.x / wide;
-  const int c0 = threadIdx.x / wide;
+  // thread = four experts and every `step`-th chunk; sums of whole numbers in any order
+  const int quads = a.pitch / 4, step = kPlaceThreads / quads;
+  const int q = threadIdx.x % quads, c0 = threadIdx.x / quads;
   if (c0 < step) {
-    for (int e = threadIdx.x % wide; e < experts; e += wide) {
-      int mine = 0, whole = 0;
-#pragma unroll 8
-      for (int c = c0; c < a.chunks; c += step) {
-        const int n = __ldcg(a.counts + static_cast<int64_t>(c) * experts + e);
-        whole += n;
-        mine += c < static_cast<int>(blockIdx.x) ? n : 0;
+    int4 mine = make_int4(0, 0, 0, 0), whole = mine;
+    const int4* table = reinterpret_cast<const int4*>(a.counts) + q;
+    for (int c = c0; c < a.chunks; c += 8 * step) {
+      int4 n[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        n[u] = make_int4(0, 0, 0, 0);
+        if (c + u * step < a.chunks) n[u] = __ldcg(table + static_cast<int64_t>(c + u * step) * quads);
       }
-      atomicAdd(&before[e], mine);
-      atomicAdd(&all[e], whole);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const bool ahead = c + u * step < static_cast<int>(blockIdx.x);
+        whole = make_int4(whole.x + n[u].x, whole.y + n[u].y, whole.z + n[u].z, whole.w + n[u].w);
+        if (ahead) mine = make_int4(mine.x + n[u].x, mine.y + n[u].y, mine.z + n[u].z, mine.w + n[u].w);
+      }
     }
+    atomicAdd(&before[4 * q], mine.x);
+    atomicAdd(&before[4 * q + 1], mine.y);
+    atomicAdd(&before[4 * q + 2], mine.z);
+    atomicAdd(&before[4 * q + 3], mine.w);
+    atomicAdd(&all[4 * q], whole.x);
+    atomicAdd(&all[4 * q + 1], whole.y);
+    atomicAdd(&all[4 * q + 2], whole.z);
+    atomicAdd(&all[4 * q + 3], whole.w);
   }
   const int first = blockIdx.x * a.per_chunk;
-  place_chunk(a, first, min(a.tokens - first, a.per_chunk), before, all, of_warp, s_scan,
+  place_chunk(a, first, min(a.tokens - first, a.per_chunk), before, all, of_warp, place_warps(experts, 32), s_scan,
               blockIdx.x == 0);
 }
 
+// The gradient: a warp takes as many tokens at once as their choices fill its lanes.
 template <typename T, int V>
-__global__ void __launch_bounds__(32 * kBackWarps) route_backward_kernel(const RouteArgs a, const bool vec,
-                                                                         const bool vec_out) {
+__global__ void __launch_bounds__(32 * kBackWarps) route_backward_kernel(const RouteArgs a, const bool vec) {
   extern __shared__ float s_grad[];
   const adamw_router& r = a.router;
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+  const int wide = choice_lanes(r.top_k), at_once = 32 / wide, sub = lane / wide, j = lane % wide;
   float* mine = s_grad + warp * (32 * V);
   const bool softmax = r.score == ADAMW_SCORE_SOFTMAX;
   const bool dense = softmax && !r.renormalise;
-  for (int64_t t = static_cast<int64_t>(blockIdx.x) * kBackWarps + warp; t < a.tokens;
-       t += static_cast<int64_t>(gridDim.x) * kBackWarps) {
-    const T* row = static_cast<const T*>(a.logits) + t * a.stride;
-    int id = -1;
-    float zj = 0.0f, dw = 0.0f;
-    if (lane < r.top_k) {
-      id = __ldg(a.ids + t * r.top_k + lane);
-      if (id < 0 || id >= r.experts) id = -1;
-      if (id >= 0) {
-        dw = r.scale * __ldg(a.dweights + t * r.top_k + lane);
-        zj = to_f32(row[id]);
-      }
+  const int64_t pace = static_cast<int64_t>(gridDim.x) * kBackWarps * at_once;
+  for (int i = lane; i < 32 * V; i += 32) mine[i] = 0.0f;
+  __syncwarp();
+  int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kBackWarps + warp) * at_once;
+  int next_id = -1;
+  float next_dw = 0.0f;
+  const auto fetch = [&](int64_t t) {
+    next_id = -1;
+    if (j < r.top_k && t < a.tokens) {
+      next_id = __ldg(a.ids + t * r.top_k + j);
+      next_dw = __ldg(a.dweights + t * r.top_k + j);
     }
-    float z[V], top = 0.0f, total = 1.0f;
+  };
+  fetch(t0 + sub);
+  for (; t0 < a.tokens; t0 += pace) {
+    const int64_t t = t0 + sub;
+    const T* rows = static_cast<const T*>(a.logits);
+    const int id = next_id >= 0 && next_id < r.experts ? next_id : -1;
+    const float dw = id >= 0 ? r.scale * next_dw : 0.0f;
+    const float zj = id >= 0 ? to_f32(rows[t * a.stride + id]) : 0.0f;
+    fetch(t + pace);
+    const int many = static_cast<int>(min(static_cast<int64_t>(at_once), a.tokens - t0));
+    float top = 0.0f, total = 1.0f;
     if (dense) {
-      load_row<T, V>(row, r.experts, vec, z);
-      top = -INFINITY;
-      bool nan = false;
+      for (int u = 0; u < many; ++u) {
+        T z[V];
+        load_row<T, V>(rows + (t0 + u) * a.stride, r.experts, z);
+        float m = -INFINITY, sum = 0.0f;
+        bool nan = false;
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        nan = nan || z[i] != z[i];
-        top = fmaxf(top, z[i]);
+        for (int i = 0; i < V; ++i) {
+          const float f = to_f32(z[i]);
+          nan = nan || f != f;
+          m = fmaxf(m, f);
+        }
+        m = warp_max(m);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const float f = to_f32(z[i]);
+          sum += f > -INFINITY ? expf(f - m) : 0.0f;
+        }
+        sum = __any_sync(kFull, nan) ? __int_as_float(0x7FFFFFFF) : warp_sum(sum);
+        if (sub == u) {
+          top = m;
+          total = sum;
+        }
       }
-      top = warp_max(top);
-      float sum = 0.0f;
-#pragma unroll
-      for (int i = 0; i < V; ++i) sum += z[i] > -INFINITY ? expf(z[i] - top) : 0.0f;
-      total = warp_sum(sum);
-      if (__any_sync(kFull, nan)) total = __int_as_float(0x7FFFFFFF);
     }
-    const float w = weight_of(zj, id >= 0, r, top, total);
-    const float mean = warp_sum(id >= 0 ? dw * w : 0.0f);
+    const float w = weight_of(zj, id >= 0, r, top, total, wide);
+    float mean = dw * w;
+    for (int o = wide / 2; o > 0; o >>= 1) mean += __shfl_xor_sync(kFull, mean, o);
     float d = 0.0f;                               // this lane's chosen logit's gradient
     if (dense) d = w * dw;
     else if (r.renormalise) d = w * (dw - mean) * (softmax ? 1.0f : sigmoid(-zj));
     else d = dw * w * sigmoid(-zj);
-    __syncwarp();
+    for (int u = 0; u < many; ++u) {
+      const bool here = sub == u && id >= 0;
+      if (here) mine[id] = d;
+      __syncwarp();
+      T* out = static_cast<T*>(a.dlogits) + (t0 + u) * a.dstride;
+      if (dense) {
+        const float m = __shfl_sync(kFull, mean, u * wide), row_top = __shfl_sync(kFull, top, u * wide),
+                    row_sum = __shfl_sync(kFull, total, u * wide);
+        T z[V];
+        load_row<T, V>(rows + (t0 + u) * a.stride, r.experts, z);
 #pragma unroll
-    for (int i = 0; i < V; ++i) mine[i * 32 + lane] = 0.0f;
-    __syncwarp();
-    if (id >= 0) mine[id] = d;
-    __syncwarp();
-    T* out = static_cast<T*>(a.dlogits) + t * a.dstride;
-    float g[V];
+        for (int i = 0; i < V; ++i) {
+          const float f = to_f32(z[i]);
+          const float g = mine[32 * i + lane] - (f > -INFINITY || f != f ? __fdiv_rn(expf(f - row_top), row_sum) * m : 0.0f);
+          if (32 * i + lane < r.experts) out[32 * i + lane] = from_f32<T>(g);
+        }
+      } else if (vec) {                           // rows on the 16-byte grid
+        constexpr int kPer = 16 / sizeof(T);
+        for (int e = lane * kPer; e < r.experts; e += 32 * kPer) {
+          uint4 q;
+          uint32_t* word = reinterpret_cast<uint32_t*>(&q);
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      g[i] = mine[lane * V + i];
-      if (dense) g[i] -= z[i] > -INFINITY ? __fdiv_rn(expf(z[i] - top), total) * mean : 0.0f;
-    }
-    if (V * sizeof(T) >= 4 && vec_out) {
-      constexpr int kWords = V * sizeof(T) >= 4 ? V * static_cast<int>(sizeof(T)) / 4 : 1;
-      uint32_t word[kWords];
-#pragma unroll
-      for (int i = 0; i < kWords; ++i) {
-        if constexpr (sizeof(T) == 4) word[i] = __float_as_uint(g[i]);
-        else word[i] = pack_pair<T>(make_float2(g[2 * i % V], g[(2 * i + 1) % V]));
-      }
-      uint32_t* p = reinterpret_cast<uint32_t*>(out + lane * V);
-      if constexpr (kWords >= 4) {
-#pragma unroll
-        for (int i = 0; i < kWords / 4; ++i)
-          __stcs(reinterpret_cast<uint4*>(p) + i,
-                 make_uint4(word[4 * i], word[4 * i + 1], word[4 * i + 2], word[4 * i + 3]));
+          for (int i = 0; i < 4; ++i) {
+            if constexpr (sizeof(T) == 4) word[i] = __float_as_uint(mine[e + i]);
+            else word[i] = pack_pair<T>(make_float2(mine[e + 2 * i], mine[e + 2 * i + 1]));
+          }
+          __stcs(reinterpret_cast<uint4*>(out + e), q);
+        }
       } else {
-#pragma unroll
-        for (int i = 0; i < kWords; ++i) p[i] = word[i];
+        for (int e = lane; e < r.experts; e += 32) out[e] = from_f32<T>(mine[e]);
       }
-    } else {
-#pragma unroll
-      for (int i = 0; i < V; ++i)
-        if (lane * V + i < r.experts) out[lane * V + i] = from_f32<T>(g[i]);
+      __syncwarp();
+      if (here) mine[id] = 0.0f;
+      __syncwarp();
     }
   }
 }
@@ -633,26 +653,19 @@ __global__ void balance_kernel(const int32_t* starts, int32_t experts, float rat
 
 // ---------------------------------------------------------------- launches
 
-template <typename T>
-bool lanes_on_grid(const void* p, int64_t stride, int experts, int v) {
-  const size_t bytes = v * sizeof(T), grid = bytes < 16 ? bytes : 16;
-  return experts == 32 * v && bytes >= 4 && reinterpret_cast<uintptr_t>(p) % grid == 0 &&
-         stride * sizeof(T) % grid == 0;
-}
-
 template <typename T, int V>
 cudaError_t route_width(const RouteArgs& a, cudaStream_t s) {
-  const bool vec = lanes_on_grid<T>(a.logits, a.stride, a.router.experts, V);
-  route_kernel<T, V><<<a.chunks, kRouteThreads, route_smem(a.router.experts), s>>>(a, vec);
+  route_kernel<T, V><<<a.chunks, 32 * route_warps<V>(), route_smem<V>(a.router.experts), s>>>(a);
   return cudaGetLastError();
 }
 template <typename T, int V>
 cudaError_t back_width(const RouteArgs& a, int sms, cudaStream_t s) {
-  const bool vec = lanes_on_grid<T>(a.logits, a.stride, a.router.experts, V);
-  const bool vec_out = lanes_on_grid<T>(a.dlogits, a.dstride, a.router.experts, V);
-  const int64_t ctas = (a.tokens + kBackWarps - 1) / kBackWarps, most = 8LL * sms;
+  const bool vec = reinterpret_cast<uintptr_t>(a.dlogits) % 16 == 0 && a.dstride * sizeof(T) % 16 == 0 &&
+                   a.router.experts * sizeof(T) % 16 == 0;
+  const int64_t per_cta = kBackWarps * (32 / choice_lanes(a.router.top_k));
+  const int64_t ctas = (a.tokens + per_cta - 1) / per_cta, most = 8LL * sms;
   route_backward_kernel<T, V><<<static_cast<unsigned>(ctas < most ? ctas : most), 32 * kBackWarps,
-                                kBackWarps * 32 * V * sizeof(float), s>>>(a, vec, vec_out);
+                                kBackWarps * 32 * V * sizeof(float), s>>>(a, vec);
   return cudaGetLastError();
 }
 
@@ -671,6 +684,12 @@ cudaError_t route_type(const RouteArgs& a, cudaStream_t s) {
 #undef ADAMW_ROUTE_CALL
 }
 template <typename T>
+int chunk_warps(const RouteArgs& a) {
+#define ADAMW_ROUTE_CALL(V) route_warps<V>()
+  return ADAMW_ROUTE_WIDTH(a.router.experts, ADAMW_ROUTE_CALL);
+#undef ADAMW_ROUTE_CALL
+}
+template <typename T>
 cudaError_t back_type(const RouteArgs& a, int sms, cudaStream_t s) {
 #define ADAMW_ROUTE_CALL(V) back_width<T, V>(a, sms, s)
   return ADAMW_ROUTE_WIDTH(a.router.experts, ADAMW_ROUTE_CALL);
@@ -680,7 +699,7 @@ template <typename T, int V>
 cudaError_t prepare_width() {
   // what the most experts of this width take: one plan's must not shrink another's
   return cudaFuncSetAttribute(route_kernel<T, V>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              static_cast<int>(route_smem(32 * V)));
+                              static_cast<int>(route_smem<V>(32 * V)));
 }
 template <typename T>
 cudaError_t prepare_type(int experts) {
@@ -689,30 +708,34 @@ cudaError_t prepare_type(int experts) {
 #undef ADAMW_ROUTE_CALL
 }
 size_t place_smem(int experts) {
-  return sizeof(int) * experts * (2 + place_warps(experts));
+  return sizeof(int) * (2 * router_pitch(experts) + experts * place_warps(experts, 32));
 }
 
 }  // namespace
 
 int router_chunks(int sms) { return sms; }
+int router_pitch(int experts) { return (experts + 3) & ~3; }
 
 cudaError_t prepare_router(const adamw_router& r) {
   cudaError_t e = prepare_type<float>(r.experts);
   if (e == cudaSuccess) e = prepare_type<__half>(r.experts);
   if (e == cudaSuccess) e = prepare_type<__nv_bfloat16>(r.experts);
   if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(place_smem(kMaxExperts)));
+    e = cudaFuncSetAttribute(place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 80 << 10);
   return e;
 }
 
 cudaError_t launch_route(adamw_dtype dt, RouteArgs a, int sms, cudaStream_t s) {
   // one CTA for what its warps take in two turns, else a share of every SM's
+  const int warps = chunk_warps<float>(a);
   const int64_t most = router_chunks(sms);
-  int64_t chunks = a.tokens <= 2 * kRouteWarps ? 1 : (a.tokens + kRouteWarps - 1) / kRouteWarps;
+  int64_t chunks = a.tokens <= 2 * warps ? 1 : (a.tokens + warps - 1) / warps;
   if (chunks > most) chunks = most;
   a.per_chunk = static_cast<int32_t>((a.tokens + chunks - 1) / chunks);
   a.chunks = a.per_chunk > 0 ? (a.tokens + a.per_chunk - 1) / a.per_chunk : 1;
+  a.pitch = router_pitch(a.router.experts);
+  a.per_group = a.router.experts / a.router.groups;
+  a.group_factor = ((1 << 20) + a.per_group - 1) / a.per_group;
   cudaError_t e = dt == ADAMW_F32   ? route_type<float>(a, s)
                   : dt == ADAMW_F16 ? route_type<__half>(a, s)
                                     : route_type<__nv_bfloat16>(a, s);
@@ -720,7 +743,7 @@ cudaError_t launch_route(adamw_dtype dt, RouteArgs a, int sms, cudaStream_t s) {
   cudaLaunchAttribute attr;
   cudaLaunchConfig_t c{};
   c.gridDim = dim3(static_cast<unsigned>(a.chunks));
-  c.blockDim = dim3(32 * place_warps(a.router.experts));
+  c.blockDim = dim3(kPlaceThreads);
   c.dynamicSmemBytes = place_smem(a.router.experts);
   c.stream = s;
   c.attrs = &attr;
