@@ -5,18 +5,17 @@
 // One warp per token; lane l holds experts l, l + 32, ...  A key is an ordered integer whose
 // lowest bits, as many as number a lane's experts, give way to the place i in the lane
 // (counted down), so that the choice is top_k rounds of one warp-wide maximum: it names the
-// place, a ballot the lane, and of equal keys the lowest expert wins.  Where no bias takes
-// part the order of the scores is that of the logits, and no score is computed for it.
+// place, a ballot the lane, and of equal keys the lowest expert wins.  A lane keeps its two
+// best keys, and looks for a third only when both are gone.  Where no bias takes part the
+// order of the scores is that of the logits, and no score is computed for it.
 //
 // float32 keys are off by a few units of the scores' last bits, more for the bits given
 // away (16-bit logits have none there).  A choice in which two keys that matter lie closer
 // than that (about one token in a thousand) is made again from 64-bit scores, so that the
 // experts are those of the definition and not of a rounding.
 //
-// What bounds it: the rounds' latency, about 60 instructions each at 256 experts, against
-// which an SM has 32 warps; the next token's logits are loaded ahead.  A round of a maximum
-// and a minimum over untouched keys, with a scan of a lane's experts for each, took twice
-// the instructions.
+// What bounds it: instructions, about 500 a token at 256 experts, and the rounds' latency,
+// against which an SM has 32 warps; the next token's logits are loaded ahead.
 #include "block_ops.h"
 #include "rows.cuh"
 
@@ -30,13 +29,27 @@ constexpr int kPlaceThreads = 1024;
 template <int V>
 __host__ __device__ constexpr int route_warps() { return V <= 8 ? 32 : 16; }
 
-// Floats as integers of the same order; 0 is below all of them and means "not there".
+// Floats as integers of the same order.  Up to kNone they stand for -inf, "not there"; 0
+// is a key that has been taken.
+constexpr uint32_t kNone = 0x007FFFFFu;
 __device__ __forceinline__ uint32_t ordered(float x) {
   const uint32_t b = __float_as_uint(x + 0.0f);          // -0 and 0 are one value
-  return (b & 0x80000000u) != 0 ? ~b : b | 0x80000000u;
+  return b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ float unordered(uint32_t o) {
   return __uint_as_float((o & 0x80000000u) != 0 ? o & 0x7FFFFFFFu : ~o);
+}
+// e^x and 1 / (1 + e^-x) for keys, whose errors the choice allows for: x log2 e is rounded
+// once, then the hardware's 2^x and reciprocal.
+__device__ __forceinline__ float key_exp(float x) {
+  float e;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * 1.4426950408889634f));
+  return e;
+}
+__device__ __forceinline__ float key_sigmoid(float x) {
+  float s;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.0f + key_exp(-x)));
+  return s;
 }
 __device__ __forceinline__ float warp_max(float x) {
 #pragma unroll
@@ -175,136 +188,161 @@ __device__ __noinline__ int choose_exactly(const T* row, const float* bias, bool
   return id;
 }
 
+// The two largest keys of each group of 32 experts, a place of every lane: halves of the
+// groups are exchanged between halves of the lanes until a lane has one group, whose 32 / V
+// lanes then join theirs.  Lane l gets those of group l V / 32.
 template <int V>
-__device__ __forceinline__ uint32_t largest(const uint32_t (&key)[V]) {
-  uint32_t best = key[0];
+__device__ __forceinline__ float2 group_tops(const float (&k)[V]) {
+  const int lane = threadIdx.x & 31;
+  float one[V], next[V];
 #pragma unroll
-  for (int i = 1; i < V; ++i) best = max(best, key[i]);
-  return best;
+  for (int i = 0; i < V; ++i) {
+    one[i] = k[i];
+    next[i] = -INFINITY;
+  }
+  int o = 16;
+#pragma unroll
+  for (int half = V / 2; half > 0; half /= 2, o /= 2) {
+    const bool upper = (lane & o) != 0;
+#pragma unroll
+    for (int i = 0; i < half; ++i) {
+      const float give1 = upper ? one[i] : one[i + half], keep1 = upper ? one[i + half] : one[i];
+      const float got1 = __shfl_xor_sync(kFull, give1, o);
+      float got2 = -INFINITY, keep2 = -INFINITY;
+      if (half < V / 2) {                 // the first exchange has no second ones
+        keep2 = upper ? next[i + half] : next[i];
+        got2 = __shfl_xor_sync(kFull, upper ? next[i] : next[i + half], o);
+      }
+      one[i] = fmaxf(keep1, got1);
+      next[i] = fmaxf(fminf(keep1, got1), fmaxf(keep2, got2));
+    }
+  }
+  for (; o > 0; o /= 2) {
+    const float got1 = __shfl_xor_sync(kFull, one[0], o), got2 = __shfl_xor_sync(kFull, next[0], o);
+    next[0] = fmaxf(fminf(one[0], got1), fmaxf(next[0], got2));
+    one[0] = fmaxf(one[0], got1);
+  }
+  return make_float2(one[0], next[0]);
 }
 
 // Chooses from the lanes' logits (NaN as -inf).  bias: null, or shared memory with its largest
 // finite magnitude.  Lane j gets the j-th expert (-1: none).  `own`: shared memory of this warp.
 template <typename T, int V>
-__device__ __forceinline__ int choose(const T* row, const float (&z)[V], const float* bias, float bias_max, bool bad, float top,
+__device__ __forceinline__ int choose(const T* row, float (&k)[V], const float* bias, float bias_max, bool bad, float top,
                                       float total, double* own, const RouteArgs& a) {
-  const adamw_router& r = a.router;
   constexpr uint32_t kPlace = V - 1;       // V is a power of two
+  const adamw_router& r = a.router;
   const int lane = threadIdx.x & 31, per = a.per_group;
   const bool softmax = r.score == ADAMW_SCORE_SOFTMAX;
   const bool by_logit = bias == nullptr || bad;
   const bool by_group = r.groups > 1 && r.top_groups < r.groups;
   const bool two = by_group && r.group_score == ADAMW_GROUP_TOP2 && !bad;
-  // Errors of a score are at most 2^-20 of the row's largest (of 1 for the sigmoid): the
-  // exponential's and the quotient's few units, the sum's, and for softmax the rounding of
-  // z - top, where |d| e^-d < 1.  The place takes V units of the key's last bit.
-  const float off = (0x1p-20f + V * 0x1p-23f) * ((softmax ? __fdividef(1.0f, total) : 1.0f) + 3.0f * bias_max) + 1e-36f;
+  // A score is off by at most this part of the row's largest (of 1 for the sigmoid): 2^-21 for
+  // the exponential and the reciprocal (the argument's rounding counts |d| e^-d < 1), the sum's
+  // V + 8 roundings, and the V units of the key's last bit that the place takes.
   const float inv = __fdividef(1.0f, total);
-  float k[V];
-  uint32_t there = 0;
+  const float off = (0x1p-20f + V * 0x1.8p-23f) * ((softmax ? inv : 1.0f) + 3.0f * bias_max) + 1e-36f;
+  if (bias != nullptr) {
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int e = 32 * i + lane;
-    k[i] = z[i];
-    bool on = z[i] > -INFINITY;
-    if (bias != nullptr) {
-      const float b = e < r.experts ? bias[e] : -INFINITY;
-      on = on && b > -INFINITY;
-      if (!bad) k[i] = (softmax ? expf(z[i] - top) * inv : sigmoid(z[i])) + b;
+    for (int i = 0; i < V; ++i) {
+      const int e = 32 * i + lane;
+      const float b = V > 1 || e < r.experts ? bias[min(e, r.experts - 1)] : -INFINITY;
+      const float s = bad ? k[i] : (softmax ? key_exp(k[i] - top) * inv : key_sigmoid(k[i])) + b;
+      k[i] = k[i] > -INFINITY && b > -INFINITY ? s : -INFINITY;
     }
-    there |= on ? 1u << i : 0u;
   }
   bool sure = true;
+  uint32_t kept = 0xFFFFFFFFu;
   if (by_group) {
-    // lane g scores group g: its largest keys one and next
-    float one = -INFINITY, next = -INFINITY;
-    if (per == 32 && V <= 8) {             // a group is one place of every lane
+    float2 tops = make_float2(-INFINITY, -INFINITY);
+    float v[V];
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        if (i < r.groups) {
-          float v = k[i];
-          if (two && by_logit) v = softmax ? expf(v - top) * inv : sigmoid(v);
-          uint32_t o = (there >> i & 1u) != 0 ? ordered(v) : 0u;
-          const uint32_t first = __reduce_max_sync(kFull, o);
-          uint32_t second = 0;
-          if (two) {
-            if (lane == __ffs(__ballot_sync(kFull, o == first)) - 1) o = 0u;
-            second = __reduce_max_sync(kFull, o);
-          }
-          if (lane == i) {
-            one = first != 0 ? unordered(first) : -INFINITY;
-            next = second != 0 ? unordered(second) : -INFINITY;
-          }
-        }
-      }
+    for (int i = 0; i < V; ++i) {
+      v[i] = k[i];
+      if (two && by_logit) v[i] = k[i] > -INFINITY ? (softmax ? key_exp(k[i] - top) * inv : key_sigmoid(k[i])) : -INFINITY;
+    }
+    const bool by_place = per == 32 && r.groups == V && V <= 8;
+    int group = lane;                      // that this lane scores
+    if (by_place) {
+      tops = group_tops<V>(v);
+      group = lane / (32 / (V <= 8 ? V : 1));
     } else {
       float* s = reinterpret_cast<float*>(own);
       __syncwarp();
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const int e = 32 * i + lane;
-        if (e < r.experts) {
-          float v = k[i];
-          if (two && by_logit) v = softmax ? expf(v - top) * inv : sigmoid(v);
-          s[e] = (there >> i & 1u) != 0 ? v : -INFINITY;
-        }
-      }
+      for (int i = 0; i < V; ++i)
+        if (32 * i + lane < r.experts) s[32 * i + lane] = v[i];
       __syncwarp();
       if (lane < r.groups)
         for (int i = 0; i < per; ++i) {
-          const float v = s[lane * per + i];
-          next = fmaxf(next, fminf(one, v));
-          one = fmaxf(one, v);
+          const float x = s[lane * per + i];
+          tops.y = fmaxf(tops.y, fminf(tops.x, x));
+          tops.x = fmaxf(tops.x, x);
         }
       __syncwarp();
     }
-    const float of = two && next > -INFINITY ? one + next : one;
-    uint32_t mine = lane < r.groups && of > -INFINITY ? ordered(of) : 0u, kept = 0, least = 0;
+    const float of = two && tops.y > -INFINITY ? tops.x + tops.y : tops.x;
+    uint32_t mine = group < r.groups ? ordered(of) : 0u, least = 0;
+    kept = 0;
     for (int g = 0; g < r.top_groups; ++g) {
       const uint32_t best = __reduce_max_sync(kFull, mine);
-      if (best == 0) break;
-      const int at = __ffs(__ballot_sync(kFull, mine == best)) - 1;
+      if (best <= kNone) break;
+      const int at = __shfl_sync(kFull, group, __ffs(__ballot_sync(kFull, mine == best)) - 1);
       kept |= 1u << at;
       least = best;
-      if (lane == at) mine = 0;
+      if (group == at) mine = 0;
     }
     const uint32_t most = __reduce_max_sync(kFull, mine);
     // without scores equal groups went to the lowest already
-    sure = (!two && by_logit) || most == 0 || unordered(least) - unordered(most) > 4.0f * off;
+    sure = (!two && by_logit) || most <= kNone || unordered(least) - unordered(most) > 4.0f * off;
+    if (by_place) {
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-      if ((kept >> ((32 * i + lane) * a.group_factor >> 20) & 1u) == 0) there &= ~(1u << i);
+      for (int i = 0; i < V; ++i)
+        if ((kept >> i & 1u) == 0) k[i] = -INFINITY;
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if ((kept >> ((32 * i + lane) * a.group_factor >> 20) & 1u) == 0) k[i] = -INFINITY;
+    }
   }
-  uint32_t key[V];
+  uint32_t key[V], best = 0, second = 0;
 #pragma unroll
-  for (int i = 0; i < V; ++i)
-    key[i] = (there >> i & 1u) != 0 ? (ordered(k[i]) & ~kPlace) | (kPlace - i) : 0u;
-  int id = -1;
-  uint32_t mine = 0, best = largest(key);
+  for (int i = 0; i < V; ++i) {
+    key[i] = (ordered(k[i]) & ~kPlace) | (kPlace - i);
+    if (V > 1) second = max(second, min(best, key[i]));
+    best = max(best, key[i]);
+  }
+  uint32_t mine = 0;
+  int lane_of = 0;
   for (int j = 0; j < r.top_k; ++j) {
     const uint32_t most = __reduce_max_sync(kFull, best);
-    if (most == 0) break;
+    if (most <= kNone) break;
     const int who = __ffs(__ballot_sync(kFull, best == most)) - 1;
-    const int place = static_cast<int>(kPlace - (most & kPlace));
     if (lane == j) {
-      id = 32 * place + who;
       mine = most;
+      lane_of = who;
     }
-    const int gone = lane == who ? place : -1;
+    if (lane == who) {
+      best = second;
+      second = 0;
+    }
+    if (V > 2 && __any_sync(kFull, best == 0)) {
+      if (best == 0) {
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (gone == i) key[i] = 0;
-    best = largest(key);
+        for (int i = 0; i < V; ++i) best = max(best, key[i] < most ? key[i] : 0u);
+        if (best == 0) best = 1;           // none left
+      }
+    }
   }
+  int id = mine > kNone ? 32 * static_cast<int>(kPlace - (mine & kPlace)) + lane_of : -1;
   // each chosen key is far enough above the one that comes after it
-  if (!by_logit || sizeof(T) == 4) {
+  if (!by_logit || (sizeof(T) == 4 && V > 1)) {
     const uint32_t rest = __reduce_max_sync(kFull, best);
     uint32_t after = __shfl_down_sync(kFull, mine, 1);
     if (lane == 31 || after == 0) after = rest;
-    mine &= ~kPlace;
-    after &= ~kPlace;
-    if (id >= 0 && after != 0)
-      sure = sure && (by_logit ? (V == 1 || mine != after) : unordered(mine) - unordered(after) > 2.0f * off);
+    if (id >= 0 && after > kNone)
+      sure = sure && (by_logit ? ((mine ^ after) & ~kPlace) != 0
+                               : unordered(mine & ~kPlace) - unordered(after & ~kPlace) > 2.0f * off);
   }
   if (!__all_sync(kFull, sure)) {
     id = choose_exactly(row, bias, by_logit, bad, own, r);
@@ -453,23 +491,22 @@ __global__ void __launch_bounds__(32 * route_warps<V>(), 1) route_kernel(const R
   for (int t = warp; t < tokens; t += kWarps) {
     const T* row = rows + t * a.stride;
     float z[V];
-    bool nan = false, inf = false;
+    bool nan = false;
     float top = -INFINITY, total = 1.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      z[i] = to_f32(next[i]);
-      nan = nan || z[i] != z[i];
-      inf = inf || z[i] == INFINITY;
-      z[i] = z[i] == z[i] ? z[i] : -INFINITY;
+      const float f = to_f32(next[i]);
+      nan = nan || f != f;
+      z[i] = fmaxf(f, -INFINITY);                                 // a NaN is not there
       top = fmaxf(top, z[i]);
     }
     if (t + kWarps < tokens) load_row<T, V>(row + kWarps * a.stride, experts, next);
-    const bool bad = __any_sync(kFull, nan || (softmax && inf));
+    const bool bad = __any_sync(kFull, nan || (softmax && top == INFINITY));
     if (sums) {
       top = warp_max(top);
       float sum = 0.0f;
 #pragma unroll
-      for (int i = 0; i < V; ++i) sum += z[i] > -INFINITY ? expf(z[i] - top) : 0.0f;
+      for (int i = 0; i < V; ++i) sum += z[i] > -INFINITY ? key_exp(z[i] - top) : 0.0f;
       total = warp_sum(sum);
     }
     const int id = choose<T, V>(row, z, bias, bias_max, bad, top, total, s_all + warp * even_experts, a);
