@@ -2,20 +2,21 @@
 // weights, every assignment's place when all are ordered by expert, the gradient of
 // the logits, and the balance step of the bias.
 //
-// One warp per token; lane l holds experts l, l + 32, ...  A key is an ordered integer whose
-// lowest bits, as many as number a lane's experts, give way to the place i in the lane
-// (counted down), so that the choice is top_k rounds of one warp-wide maximum: it names the
-// place, a ballot the lane, and of equal keys the lowest expert wins.  A lane keeps its two
-// best keys, and looks for a third only when both are gone.  Where no bias takes part the
-// order of the scores is that of the logits, and no score is computed for it.
+// The choice is top_k rounds of a maximum over integers, each a key and the expert's number
+// counted down, so that one maximum names the expert and of equal keys the lowest wins.  A
+// lane keeps its two best and looks for a third only when both are gone.  Where no bias takes
+// part the order of the scores is that of the logits, and no score is computed for it.
 //
-// float32 keys are off by a few units of the scores' last bits, more for the bits given
-// away (16-bit logits have none there).  A choice in which two keys that matter lie closer
-// than that (about one token in a thousand) is made again from 64-bit scores, so that the
-// experts are those of the definition and not of a rounding.
+// Up to 512 experts, and 32 chosen, a token has a team of 8, 16 or 32 lanes and a warp several
+// tokens (route_teams_kernel; groups of whole lanes): 5 and 2.5 times fewer instructions a token
+// than with a warp for each (128 and 256 experts), and it is instructions that bound it.  Else a
+// warp takes a token (route_kernel).
 //
-// What bounds it: instructions, about 500 a token at 256 experts, and the rounds' latency,
-// against which an SM has 32 warps; the next token's logits are loaded ahead.
+// Keys are off by a few units of the scores' last bits and by the bits that the number takes
+// (none that 16-bit logits have).  A choice in which two keys that matter lie closer than that
+// (about one token in a thousand) is made again from 64-bit scores, so that the experts are those
+// of the definition and not of a rounding: of the few experts that can matter, a lane each, or of
+// all of them.
 #include "block_ops.h"
 #include "rows.cuh"
 
@@ -63,24 +64,28 @@ __device__ __forceinline__ float warp_sum(float x) {
 }
 __device__ __forceinline__ float sigmoid(float z) { return __fdividef(1.0f, 1.0f + expf(-z)); }
 
-// The weight of a lane's chosen logit z before `scale`, among the `wide` (a power of two)
-// neighbouring lanes of its token; `row_top` and `row_sum` are the softmax's largest logit
-// and sum over the whole row (used without renormalisation).
+// The weight of a lane's chosen logit z before `scale`, among the WIDE neighbouring lanes of
+// its token (0: `wide` of them); `row_top` and `row_sum` are the softmax's largest logit and
+// sum over the whole row (used without renormalisation).
+template <int WIDE>
 __device__ __forceinline__ float weight_of(float z, bool chosen, const adamw_router& r,
-                                           float row_top, float row_sum, int wide) {
+                                           float row_top, float row_sum, int wide = WIDE) {
+  if (WIDE > 0) wide = WIDE;
   if (r.renormalise) {
     // Only ratios count, so small scores are taken relative to the largest chosen one:
     // below a logit of -30 the sigmoid is e^z to the last bit.
     float top = chosen ? z : -INFINITY;
+#pragma unroll
     for (int o = wide / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
     const bool ratio = r.score == ADAMW_SCORE_SOFTMAX || top < -30.0f;
     const float s = chosen ? (ratio ? expf(z - top) : sigmoid(z)) : 0.0f;
     float total = s;
+#pragma unroll
     for (int o = wide / 2; o > 0; o >>= 1) total += __shfl_xor_sync(kFull, total, o);
-    return chosen ? __fdiv_rn(s, total) : 0.0f;
+    return chosen ? __fdividef(s, total) : 0.0f;
   }
   if (!chosen) return 0.0f;
-  return r.score == ADAMW_SCORE_SOFTMAX ? __fdiv_rn(expf(z - row_top), row_sum) : sigmoid(z);
+  return r.score == ADAMW_SCORE_SOFTMAX ? __fdividef(expf(z - row_top), row_sum) : sigmoid(z);
 }
 // Lanes of a token: the smallest power of two that holds its choice.
 __host__ __device__ __forceinline__ int choice_lanes(int top_k) {
@@ -226,7 +231,7 @@ __device__ __forceinline__ float2 group_tops(const float (&k)[V]) {
 }
 
 // Chooses from the lanes' logits (NaN as -inf).  bias: null, or shared memory with its largest
-// finite magnitude.  Lane j gets the j-th expert (-1: none).  `own`: shared memory of this warp.
+// magnitude.  Lane j gets the j-th expert (-1: none).  `own`: shared memory of this warp.
 template <typename T, int V>
 __device__ __forceinline__ int choose(const T* row, float (&k)[V], const float* bias, float bias_max, bool bad, float top,
                                       float total, double* own, const RouteArgs& a) {
@@ -251,7 +256,7 @@ __device__ __forceinline__ int choose(const T* row, float (&k)[V], const float* 
       k[i] = k[i] > -INFINITY && b > -INFINITY ? s : -INFINITY;
     }
   }
-  bool sure = true;
+  bool sure = by_logit || bias_max < INFINITY;
   uint32_t kept = 0xFFFFFFFFu;
   if (by_group) {
     float2 tops = make_float2(-INFINITY, -INFINITY);
@@ -294,7 +299,7 @@ __device__ __forceinline__ int choose(const T* row, float (&k)[V], const float* 
     }
     const uint32_t most = __reduce_max_sync(kFull, mine);
     // without scores equal groups went to the lowest already
-    sure = (!two && by_logit) || most <= kNone || unordered(least) - unordered(most) > 4.0f * off;
+    sure = sure && ((!two && by_logit) || most <= kNone || unordered(least) - unordered(most) > 4.0f * off);
     if (by_place) {
 #pragma unroll
       for (int i = 0; i < V; ++i)
@@ -477,7 +482,7 @@ __global__ void __launch_bounds__(32 * route_warps<V>(), 1) route_kernel(const R
       const float b = __ldg(a.bias + e);
       s_bias[e] = b > -INFINITY ? b : -INFINITY;                  // NaN: not there
       any = any || !(b == 0.0f);
-      if (fabsf(b) < INFINITY) atomicMax(&s_bias_max, __float_as_uint(fabsf(b)));
+      if (b > -INFINITY) atomicMax(&s_bias_max, __float_as_uint(fabsf(b)));
     }
   }
   // a bias of zeros changes nothing
@@ -511,7 +516,7 @@ __global__ void __launch_bounds__(32 * route_warps<V>(), 1) route_kernel(const R
     }
     const int id = choose<T, V>(row, z, bias, bias_max, bad, top, total, s_all + warp * even_experts, a);
     const float zj = id >= 0 ? to_f32(row[id]) : 0.0f;
-    float w = a.router.scale * weight_of(zj, id >= 0, a.router, top, total, wide);
+    float w = a.router.scale * weight_of<0>(zj, id >= 0, a.router, top, total, wide);
     if (bad) w = __int_as_float(0x7FFFFFFF);
     if (lane < a.router.top_k) {
       const int64_t at = (static_cast<int64_t>(first) + t) * a.router.top_k + lane;
@@ -525,6 +530,331 @@ __global__ void __launch_bounds__(32 * route_warps<V>(), 1) route_kernel(const R
   if (gridDim.x == 1) {
     for (int e = threadIdx.x; e < experts; e += kThreads) s_before[e] = 0;
     place_chunk(a, first, tokens, s_before, s_counts, reinterpret_cast<int*>(s_all), place_warps(experts, kWarps), s_scan, true);
+  } else {
+    for (int e = threadIdx.x; e < experts; e += kThreads)
+      a.counts[static_cast<int64_t>(blockIdx.x) * a.pitch + e] = s_counts[e];
+    let_next_kernel_start();
+  }
+}
+
+// ---------------------------------------------------------------- teams
+
+constexpr int kTeamWarps = 24;
+constexpr uint32_t kNumber = 511;        // experts are numbered in a key's lowest bits
+constexpr float kFirstUnit = 16400.0f;   // of the scores' scale: its keys lie above kNone
+
+template <int LANES>
+__device__ __forceinline__ uint32_t team_max(uint32_t x) {
+  if constexpr (LANES == 32) return __reduce_max_sync(kFull, x);
+#pragma unroll
+  for (int o = LANES / 2; o > 0; o /= 2) x = max(x, __shfl_xor_sync(kFull, x, o));
+  return x;
+}
+template <int LANES>
+__device__ __forceinline__ float team_max(float x) {
+#pragma unroll
+  for (int o = LANES / 2; o > 0; o /= 2) x = fmaxf(x, __shfl_xor_sync(kFull, x, o));
+  return x;
+}
+template <int LANES>
+__device__ __forceinline__ float team_sum(float x) {
+#pragma unroll
+  for (int o = LANES / 2; o > 0; o /= 2) x += __shfl_xor_sync(kFull, x, o);
+  return x;
+}
+
+// V logits of a lane: experts V l to V l + V - 1 of its token.
+template <typename T, int V>
+struct TeamRow {
+  static constexpr int kBytes = V * static_cast<int>(sizeof(T));
+  uint32_t word[kBytes / 4];
+  __device__ __forceinline__ void load(const T* row, int e0, int experts, bool vec) {
+    if (vec) {                            // whole rows, on the grid of a lane's bytes (16 at most)
+      const T* p = row + e0;
+      if constexpr (kBytes >= 16) {
+#pragma unroll
+        for (int i = 0; i < kBytes / 16; ++i) {
+          const uint4 q = __ldcs(reinterpret_cast<const uint4*>(p) + i);
+          word[4 * i] = q.x;
+          word[4 * i + 1] = q.y;
+          word[4 * i + 2] = q.z;
+          word[4 * i + 3] = q.w;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kBytes / 4; ++i) word[i] = __ldcs(reinterpret_cast<const uint32_t*>(p) + i);
+      }
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const T z = e0 + i < experts ? __ldcs(row + e0 + i) : from_f32<T>(-INFINITY);
+      if constexpr (sizeof(T) == 4) {
+        word[i] = __float_as_uint(z);
+      } else {
+        const uint32_t h = *reinterpret_cast<const uint16_t*>(&z);
+        word[i / 2] = i % 2 == 0 ? h : word[i / 2] | h << 16;
+      }
+    }
+  }
+  __device__ __forceinline__ float at(int i) const {
+    if constexpr (sizeof(T) == 4) return __uint_as_float(word[i]);
+    const float2 f = unpack_pair<T>(word[i / 2]);
+    return i % 2 == 0 ? f.x : f.y;
+  }
+};
+
+// A token's key in 64 bits, of an expert's logit and bias.  Out of line: few tokens need it.
+__device__ __noinline__ double exact_key(float z, float b, bool by_logit) {
+  return by_logit ? static_cast<double>(z) : 1.0 / (1.0 + exp(-static_cast<double>(z))) + static_cast<double>(b);
+}
+
+template <int LANES>
+__host__ __device__ __forceinline__ size_t team_smem(int experts) {
+  return static_cast<size_t>(kTeamWarps) * even(experts) * sizeof(double) + sizeof(float) * (3 * even(experts) + 32);
+}
+
+template <typename T, int LANES, int V>
+__global__ void __launch_bounds__(32 * kTeamWarps, 1) route_teams_kernel(const RouteArgs a, const bool vec) {
+  constexpr int kThreads = 32 * kTeamWarps, kTokens = 32 / LANES;
+  extern __shared__ double s_all[];
+  const adamw_router& r = a.router;
+  const int experts = r.experts, even_experts = even(experts);
+  float* s_bias = reinterpret_cast<float*>(s_all + kTeamWarps * even_experts);     // V at a time may pass the last one
+  int* s_counts = reinterpret_cast<int*>(s_bias + even_experts + 32);
+  int* s_before = s_counts + even_experts;
+  __shared__ int s_scan[32];
+  __shared__ uint32_t s_bias_max;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, sub = lane / LANES, l = lane % LANES;
+  const int first = blockIdx.x * a.per_chunk;
+  const int tokens = min(a.tokens - first, a.per_chunk);
+  const T* rows = static_cast<const T*>(a.logits) + static_cast<int64_t>(first) * a.stride;
+  const int e0 = l * V;
+  TeamRow<T, V> next;
+  const int start = warp * kTokens + sub;
+  if (start < tokens) next.load(rows + start * a.stride, e0, experts, vec);
+  if (threadIdx.x == 0) s_bias_max = 0;
+  __syncthreads();
+  bool any = false;
+  for (int e = threadIdx.x; e < experts; e += kThreads) {
+    s_counts[e] = 0;
+    if (a.bias != nullptr) {
+      const float b = __ldg(a.bias + e);
+      s_bias[e] = b > -INFINITY ? b : -INFINITY;                  // NaN: not there
+      any = any || !(b == 0.0f);
+      if (b > -INFINITY) atomicMax(&s_bias_max, __float_as_uint(fabsf(b)));
+    }
+  }
+  // a bias of zeros changes nothing
+  const float* bias = __syncthreads_or(any) ? s_bias : nullptr;
+  const float bias_max = __uint_as_float(s_bias_max);
+  const bool softmax = r.score == ADAMW_SCORE_SOFTMAX;
+  const bool by_group = r.groups > 1 && r.top_groups < r.groups;
+  const bool two = by_group && r.group_score == ADAMW_GROUP_TOP2;
+  const bool scored = bias != nullptr || two;           // keys are scores, not logits
+  const bool sums = softmax && (scored || !r.renormalise);
+  const int group_lanes = by_group ? a.per_group / V : LANES, group = by_group ? l / group_lanes : 0;
+  for (int t0 = warp * kTokens; t0 < tokens; t0 += kTeamWarps * kTokens) {
+    const int t = t0 + sub;
+    const bool live = t < tokens;
+    const T* row = rows + static_cast<int64_t>(live ? t : t0) * a.stride;
+    float z[V];
+    bool nan = false;
+    float top = -INFINITY, total = 1.0f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const float f = live ? next.at(i) : -INFINITY;
+      nan = nan || f != f;
+      z[i] = fmaxf(f, -INFINITY);                                 // a NaN is not there
+      top = fmaxf(top, z[i]);
+    }
+    if (t + kTeamWarps * kTokens < tokens) next.load(row + static_cast<int64_t>(kTeamWarps * kTokens) * a.stride, e0, experts, vec);
+    constexpr uint32_t kTeam = kFull >> (32 - LANES);
+    const bool bad = (__ballot_sync(kFull, nan || (softmax && top == INFINITY)) >> (sub * LANES) & kTeam) != 0;
+    if (sums) {
+      top = team_max<LANES>(top);
+      float sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) sum += z[i] > -INFINITY ? key_exp(z[i] - top) : 0.0f;
+      total = team_sum<LANES>(sum);
+    }
+    // Scores become whole units of a scale from the lowest possible key to the highest, a
+    // float's 23 bits by adding 2^23: off by a unit, and by their own errors: softmax as the
+    // warp's kernel has it; sigmoid, in 2^-24: the exponential's 2 units and its argument's
+    // rounding, each times s (1 - s), the sum's 1, the reciprocal's 2 and the bias's 1, below 6.
+    const float inv = __fdividef(1.0f, total), most_score = softmax ? inv : 1.0f;
+    const float units = __fdividef(8388608.0f - 17000.0f, most_score + 2.0f * bias_max);
+    const float off = (softmax ? 0x1p-20f + V * 0x1p-24f : 0x1.8p-22f) * (most_score + bias_max) * units + 1.5f;
+    uint32_t key[V], best = 0, second = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const uint32_t number = kNumber - e0 - i;
+      if (scored && !bad) {
+        const float b = bias != nullptr ? bias[e0 + i] : 0.0f;
+        const float s = (softmax ? key_exp(z[i] - top) * inv : key_sigmoid(z[i])) + b;
+        const uint32_t unit = __float_as_uint(fmaf(s + bias_max, units, 8388608.0f + kFirstUnit));
+        key[i] = z[i] > -INFINITY && b > -INFINITY ? unit << 9 | number : 0u;
+      } else {
+        const bool there = z[i] > -INFINITY && (bias == nullptr || bias[e0 + i] > -INFINITY);
+        key[i] = there ? (ordered(z[i]) & ~kNumber) | number : 0u;
+      }
+      second = max(second, min(best, key[i]));
+      best = max(best, key[i]);
+    }
+    bool sure = bias_max < INFINITY || !live;     // no scale holds an infinite bias
+    best = max(best, 1u);                         // 1: none left
+    if (by_group) {
+      uint32_t one = best, other = second;
+      for (int o = 1; o < group_lanes; o *= 2) {
+        const uint32_t x = __shfl_xor_sync(kFull, one, o), y = __shfl_xor_sync(kFull, other, o);
+        other = max(min(one, x), max(other, y));
+        one = max(one, x);
+      }
+      const bool summed = two && !bad;
+      uint32_t mine = one >> 9;
+      if (summed && one > kNone)
+        // of one key alone: as if the other were 0, which lies bias_max above the scale's start
+        mine += other > kNone ? other >> 9 : static_cast<uint32_t>(fmaf(bias_max, units, kFirstUnit));
+      mine = one > kNone ? mine << 5 | (31 - group) : 0u;
+      uint32_t least = 0;
+      bool kept = false;
+      for (int g = 0; g < r.top_groups; ++g) {
+        const uint32_t most = team_max<LANES>(mine);
+        if (most != 0) least = most;
+        if (mine == most) {
+          kept = true;
+          mine = 0;
+        }
+      }
+      const uint32_t most = team_max<LANES>(mine);
+      const bool exact = !scored || bad;
+      if (most != 0)
+        sure = sure && (exact ? sizeof(T) == 2 || least >> 5 != most >> 5
+                              : static_cast<float>((least >> 5) - (most >> 5)) > 2.0f * off * (summed ? 2.0f : 1.0f));
+      if (!(softmax && scored) && __any_sync(kFull, !sure)) {
+        // again from the 64-bit keys of each lane's two best, if its third is far enough below
+        uint32_t third = 0;
+#pragma unroll
+        for (int i = 0; i < V; ++i) third = max(third, key[i] < second ? key[i] : 0u);
+        const bool far = second <= kNone || third <= kNone || (exact ? second >> 9 != third >> 9 : static_cast<float>((second >> 9) - (third >> 9)) > 2.0f * off);
+        double x[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t k = i == 0 ? best : second;
+          const int e = static_cast<int>(kNumber - (k & kNumber));
+          x[i] = k > kNone ? exact_key(to_f32(row[e]), bias != nullptr ? bias[e] : 0.0f, exact) : -INFINITY;
+        }
+        double one64 = fmax(x[0], x[1]), other64 = fmin(x[0], x[1]);
+        for (int o = 1; o < group_lanes; o *= 2) {
+          const double u = __shfl_xor_sync(kFull, one64, o), v = __shfl_xor_sync(kFull, other64, o);
+          other64 = fmax(fmin(one64, u), fmax(other64, v));
+          one64 = fmax(one64, u);
+        }
+        const double of = summed && other64 > -INFINITY ? one64 + other64 : one64;
+        int before = 0;                    // groups that come before this lane's
+        for (int g = 0; g < r.groups; ++g) {
+          const double v = __shfl_sync(kFull, of, g * group_lanes, LANES);
+          before += v > of || (v == of && g < group);
+        }
+        const bool all_far = (__ballot_sync(kFull, far) >> (sub * LANES) & kTeam) == kTeam;
+        if (!sure && all_far && bias_max < INFINITY) {
+          kept = before < r.top_groups && of > -INFINITY;
+          sure = true;
+        }
+      }
+      if (!kept) {
+        best = 1;
+        second = 0;
+      }
+#pragma unroll
+      for (int i = 0; i < V; ++i) key[i] = kept ? key[i] : 0u;
+    }
+    const bool sure_of_groups = sure;
+    uint32_t mine = 0;
+    for (int j = 0; j < r.top_k; ++j) {
+      const uint32_t most = team_max<LANES>(best);
+      if (l == j) mine = most;
+      if (best == most) {
+        best = second;
+        second = 0;
+      }
+      if (V > 2 && __any_sync(kFull, best == 0)) {
+        if (best == 0) {
+#pragma unroll
+          for (int i = 0; i < V; ++i) best = max(best, key[i] < most ? key[i] : 0u);
+          if (best == 0) best = 1;          // none left
+        }
+      }
+    }
+    int id = mine > kNone ? static_cast<int>(kNumber - (mine & kNumber)) : -1;
+    // each chosen key is far enough above the one that comes after it
+    const uint32_t rest = team_max<LANES>(best);
+    uint32_t after = __shfl_down_sync(kFull, mine, 1, LANES);
+    if (l == LANES - 1 || l + 1 >= r.top_k) after = rest;
+    if (id >= 0 && after > kNone) {
+      if (scored && !bad) sure = sure && static_cast<float>((mine >> 9) - (after >> 9)) > 2.0f * off;
+      else if (sizeof(T) == 4) sure = sure && mine >> 9 != after >> 9;
+    }
+    sure = (__ballot_sync(kFull, sure) >> (sub * LANES) & kTeam) == kTeam;      // one answer for the team
+    if (__any_sync(kFull, !sure && live) && !(softmax && scored)) {
+      // Again from 64-bit keys: as many best as the team has lanes, each in its lane, if the one
+      // after them is far enough below the last chosen.
+      const bool by_logit = bias == nullptr || bad, grouped = sure_of_groups;
+      uint32_t mine64 = l < r.top_k ? mine : 0u;
+      for (int j = r.top_k; j < LANES; ++j) {
+        const uint32_t most = team_max<LANES>(best);
+        if (l == j) mine64 = most;
+        if (best == most) {
+          best = 1;
+#pragma unroll
+          for (int i = 0; i < V; ++i) best = max(best, key[i] < most ? key[i] : 0u);
+        }
+      }
+      const uint32_t last = __shfl_sync(kFull, mine, r.top_k - 1, LANES), then = team_max<LANES>(best);
+      const bool far = then <= kNone || (scored && !bad ? static_cast<float>((last >> 9) - (then >> 9)) > 2.0f * off : last >> 9 != then >> 9);
+      const int e = mine64 > kNone ? static_cast<int>(kNumber - (mine64 & kNumber)) : -1;
+      const double x = e >= 0 ? exact_key(to_f32(row[e]), bias != nullptr ? bias[e] : 0.0f, by_logit) : -INFINITY;
+      int before = 0, now = -1;
+      for (int j = 0; j < LANES; ++j) {
+        const double v = __shfl_sync(kFull, x, j, LANES);
+        const int other = __shfl_sync(kFull, e, j, LANES);
+        before += other >= 0 && (v > x || (v == x && other < e));
+      }
+      for (int j = 0; j < LANES; ++j) {
+        const int place = __shfl_sync(kFull, before, j, LANES), other = __shfl_sync(kFull, e, j, LANES);
+        if (other >= 0 && place == l) now = other;
+      }
+      if (!sure && grouped && far && bias_max < INFINITY) {
+        id = l < r.top_k ? now : -1;
+        sure = true;
+      }
+    }
+    uint32_t again = __ballot_sync(kFull, !sure && live);
+    while (again != 0) {
+      const int u = (__ffs(again) - 1) / LANES;
+      const bool bad_u = __shfl_sync(kFull, static_cast<int>(bad), u * LANES) != 0;
+      const int chosen = choose_exactly(rows + static_cast<int64_t>(t0 + u) * a.stride, bias, bias == nullptr || bad_u, bad_u,
+                                        s_all + warp * even_experts, r);
+      __syncwarp();
+      const int got = __shfl_sync(kFull, chosen, l);
+      if (sub == u) id = l < r.top_k ? got : -1;
+      again &= ~(kTeam << (u * LANES));
+    }
+    const float zj = id >= 0 ? to_f32(row[id]) : 0.0f;
+    float w = r.scale * weight_of<LANES>(zj, id >= 0, r, top, total);
+    if (bad) w = __int_as_float(0x7FFFFFFF);
+    if (live && l < r.top_k) {
+      const int64_t at = (static_cast<int64_t>(first) + t) * r.top_k + l;
+      a.ids[at] = id;
+      a.weights[at] = w;
+      if (id >= 0) atomicAdd(&s_counts[id], 1);
+    }
+  }
+  if (a.starts == nullptr) return;
+  __syncthreads();
+  if (gridDim.x == 1) {
+    for (int e = threadIdx.x; e < experts; e += kThreads) s_before[e] = 0;
+    place_chunk(a, first, tokens, s_before, s_counts, reinterpret_cast<int*>(s_all), place_warps(experts, kTeamWarps), s_scan, true);
   } else {
     for (int e = threadIdx.x; e < experts; e += kThreads)
       a.counts[static_cast<int64_t>(blockIdx.x) * a.pitch + e] = s_counts[e];
@@ -635,7 +965,7 @@ __global__ void __launch_bounds__(32 * kBackWarps) route_backward_kernel(const R
         }
       }
     }
-    const float w = weight_of(zj, id >= 0, r, top, total, wide);
+    const float w = weight_of<0>(zj, id >= 0, r, top, total, wide);
     float mean = dw * w;
     for (int o = wide / 2; o > 0; o >>= 1) mean += __shfl_xor_sync(kFull, mean, o);
     float d = 0.0f;                               // this lane's chosen logit's gradient
@@ -695,6 +1025,39 @@ cudaError_t route_width(const RouteArgs& a, cudaStream_t s) {
   route_kernel<T, V><<<a.chunks, 32 * route_warps<V>(), route_smem<V>(a.router.experts), s>>>(a);
   return cudaGetLastError();
 }
+template <typename T, int LANES, int V>
+cudaError_t route_teams(const RouteArgs& a, cudaStream_t s) {
+  constexpr int kGrid = V * sizeof(T) < 16 ? V * sizeof(T) : 16;
+  const bool vec = a.router.experts == LANES * V && reinterpret_cast<uintptr_t>(a.logits) % kGrid == 0 &&
+                   a.stride * sizeof(T) % kGrid == 0;
+  route_teams_kernel<T, LANES, V><<<a.chunks, 32 * kTeamWarps, team_smem<LANES>(a.router.experts), s>>>(a, vec);
+  return cudaGetLastError();
+}
+// Lanes of a token's team and experts of a lane; 0 lanes where a warp takes the token: more
+// experts than the teams hold, or groups that are not of whole lanes, a power of two of them.
+struct Team {
+  int lanes, experts;
+};
+Team team_for(const adamw_router& r) {
+  Team t{0, 0};
+  const int lanes = r.top_k <= 8 && r.experts <= 128 ? 8 : (r.top_k <= 16 && r.experts <= 256 ? 16 : 32);
+  for (int v = 4; v <= 16; v *= 2)
+    if (r.experts <= lanes * v) {
+      t = Team{lanes, v};
+      break;
+    }
+  if (r.groups > 1 && r.top_groups < r.groups) {
+    const int per = r.experts / r.groups, of = t.experts > 0 ? per / t.experts : 0;
+    if (t.experts == 0 || per % t.experts != 0 || (of & (of - 1)) != 0) t = Team{0, 0};
+  }
+  return t;
+}
+
+#define ADAMW_ROUTE_TEAM(t, CALL)                                                             \
+  ((t).lanes == 8    ? ((t).experts == 4 ? CALL(8, 4) : (t).experts == 8 ? CALL(8, 8) : CALL(8, 16))     \
+   : (t).lanes == 16 ? ((t).experts == 4 ? CALL(16, 4) : (t).experts == 8 ? CALL(16, 8) : CALL(16, 16))  \
+                     : ((t).experts == 4 ? CALL(32, 4) : (t).experts == 8 ? CALL(32, 8) : CALL(32, 16)))
+
 template <typename T, int V>
 cudaError_t back_width(const RouteArgs& a, int sms, cudaStream_t s) {
   const bool vec = reinterpret_cast<uintptr_t>(a.dlogits) % 16 == 0 && a.dstride * sizeof(T) % 16 == 0 &&
@@ -715,7 +1078,10 @@ cudaError_t back_width(const RouteArgs& a, int sms, cudaStream_t s) {
                       : CALL(32))
 
 template <typename T>
-cudaError_t route_type(const RouteArgs& a, cudaStream_t s) {
+cudaError_t route_type(const RouteArgs& a, Team team, cudaStream_t s) {
+#define ADAMW_ROUTE_CALL(LANES, V) route_teams<T, LANES, V>(a, s)
+  if (team.lanes > 0) return ADAMW_ROUTE_TEAM(team, ADAMW_ROUTE_CALL);
+#undef ADAMW_ROUTE_CALL
 #define ADAMW_ROUTE_CALL(V) route_width<T, V>(a, s)
   return ADAMW_ROUTE_WIDTH(a.router.experts, ADAMW_ROUTE_CALL);
 #undef ADAMW_ROUTE_CALL
@@ -738,8 +1104,16 @@ cudaError_t prepare_width() {
   return cudaFuncSetAttribute(route_kernel<T, V>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               static_cast<int>(route_smem<V>(32 * V)));
 }
+template <typename T, int LANES, int V>
+cudaError_t prepare_team() {
+  return cudaFuncSetAttribute(route_teams_kernel<T, LANES, V>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              static_cast<int>(team_smem<LANES>(LANES * V)));
+}
 template <typename T>
-cudaError_t prepare_type(int experts) {
+cudaError_t prepare_type(int experts, Team team) {
+#define ADAMW_ROUTE_CALL(LANES, V) prepare_team<T, LANES, V>()
+  if (team.lanes > 0) return ADAMW_ROUTE_TEAM(team, ADAMW_ROUTE_CALL);
+#undef ADAMW_ROUTE_CALL
 #define ADAMW_ROUTE_CALL(V) prepare_width<T, V>()
   return ADAMW_ROUTE_WIDTH(experts, ADAMW_ROUTE_CALL);
 #undef ADAMW_ROUTE_CALL
@@ -754,28 +1128,30 @@ int router_chunks(int sms) { return sms; }
 int router_pitch(int experts) { return (experts + 3) & ~3; }
 
 cudaError_t prepare_router(const adamw_router& r) {
-  cudaError_t e = prepare_type<float>(r.experts);
-  if (e == cudaSuccess) e = prepare_type<__half>(r.experts);
-  if (e == cudaSuccess) e = prepare_type<__nv_bfloat16>(r.experts);
+  const Team team = team_for(r);
+  cudaError_t e = prepare_type<float>(r.experts, team);
+  if (e == cudaSuccess) e = prepare_type<__half>(r.experts, team);
+  if (e == cudaSuccess) e = prepare_type<__nv_bfloat16>(r.experts, team);
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 80 << 10);
   return e;
 }
 
 cudaError_t launch_route(adamw_dtype dt, RouteArgs a, int sms, cudaStream_t s) {
-  // one CTA for what its warps take in two turns, else a share of every SM's
-  const int warps = chunk_warps<float>(a);
+  // one CTA up to 64 tokens, which spares the second kernel, else a share of every SM's
+  const Team team = team_for(a.router);
+  const int turn = team.lanes > 0 ? kTeamWarps * (32 / team.lanes) : chunk_warps<float>(a);
   const int64_t most = router_chunks(sms);
-  int64_t chunks = a.tokens <= 2 * warps ? 1 : (a.tokens + warps - 1) / warps;
+  int64_t chunks = a.tokens <= 64 ? 1 : (a.tokens + turn - 1) / turn;
   if (chunks > most) chunks = most;
   a.per_chunk = static_cast<int32_t>((a.tokens + chunks - 1) / chunks);
   a.chunks = a.per_chunk > 0 ? (a.tokens + a.per_chunk - 1) / a.per_chunk : 1;
   a.pitch = router_pitch(a.router.experts);
   a.per_group = a.router.experts / a.router.groups;
   a.group_factor = ((1 << 20) + a.per_group - 1) / a.per_group;
-  cudaError_t e = dt == ADAMW_F32   ? route_type<float>(a, s)
-                  : dt == ADAMW_F16 ? route_type<__half>(a, s)
-                                    : route_type<__nv_bfloat16>(a, s);
+  cudaError_t e = dt == ADAMW_F32   ? route_type<float>(a, team, s)
+                  : dt == ADAMW_F16 ? route_type<__half>(a, team, s)
+                                    : route_type<__nv_bfloat16>(a, team, s);
   if (e != cudaSuccess || a.chunks == 1 || a.starts == nullptr) return e;
   cudaLaunchAttribute attr;
   cudaLaunchConfig_t c{};

@@ -167,7 +167,7 @@ def test_experts_that_are_not_there(score, groups, top, bias):
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 def test_numbers_that_are_none(score):
-    z = torch.randn(12, 48, device="cuda")
+    z = torch.randn(12, 48, device="cuda", generator=torch.Generator(device="cuda").manual_seed(7))
     z[3, 40] = float("nan")
     z[4, :] = float("nan")
     z[5, 7] = float("inf")
@@ -178,7 +178,15 @@ def test_numbers_that_are_none(score):
     w, ids = w.cpu(), ids.cpu()
     nan = [3, 4] + ([5] if score == "softmax" else [])
     assert w[nan].isnan().all() and w[[t for t in range(12) if t not in nan]].isfinite().all()
-    assert (ids[4] == -1).all() and 40 not in ids[3] and not (ids == 9).any() and ids[5, 0] == 7
+    assert (ids[4] == -1).all() and 40 not in ids[3] and not (ids == 9).any()
+    # the row with an infinite logit: by its logits under softmax, by scores and bias (whose groups may be others) else
+    zz = wide(z[5])
+    zz[9] = -np.inf
+    if score == "softmax":
+        infinite = RO.choose(zz, None, 4, "sigmoid", 4, 2, "max")
+    else:
+        infinite = RO.choose(zz, np.nan_to_num(wide(bias), nan=-np.inf), 4, "sigmoid", 4, 2, "top2")
+    assert ids[5].tolist() == infinite and (score == "sigmoid" or ids[5, 0] == 7)
     assert (ids[[t for t in range(12) if t != 4]] >= 0).all()
     assert int(starts[-1]) == 11 * 4
     d = router.backward(torch.ones(12, 4, device="cuda"), z, ids.cuda())
@@ -275,3 +283,28 @@ def test_balance():
     for _ in range(60):
         router.balance(b, router.route(z, b)[3], 0.01)
     assert router.route(z, b)[3].diff().float().std() < 0.5 * first
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("experts,groups,top,k", [(64, 8, 3, 6), (256, 8, 4, 8), (60, 5, 2, 7), (1000, 8, 2, 9), (16, 1, 1, 3)])
+def test_a_bias_that_is_infinite(experts, groups, top, k, score):
+    rng = np.random.default_rng(experts)
+    z, bias = rng.normal(0, 1, (50, experts)), 0.01 * rng.integers(-5, 6, experts)
+    bias[3] = bias[7] = np.inf
+    bias[5] = -np.inf
+    for group_score in ("max", "top2"):
+        ids = check(z, bias, k, score, groups, top, group_score)
+        assert (ids == 3).any(1).all() and (ids == 7).any(1).all() and not (ids == 5).any()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("experts,k", [(3, 3), (32, 8), (48, 9), (64, 17), (120, 5), (200, 8), (256, 17), (300, 6), (512, 20), (513, 2)])
+def test_teams_of_every_size(experts, k, dtype):
+    rng = np.random.default_rng(experts * k)
+    z = rng.normal(0, 1.5, (75, experts))
+    z[5] = -np.inf
+    bias = 0.001 * rng.integers(-30, 31, experts)
+    for b, score in ((None, "softmax"), (bias, "sigmoid"), (bias, "softmax")):
+        check(z, b, k, score, dtype=dtype)
+    z[10] = np.sort(z[10])                      # a lane holds all that is chosen
+    check(z, None, k, "sigmoid", renorm=False, dtype=dtype)
