@@ -70,11 +70,11 @@ struct ExpertRowsArgs {
   float* dweights;
   int64_t tokens, width, n_rows;
   int32_t top_k;
+  int32_t lanes;               // of a row, a power of two
 };
-cudaError_t launch_dispatch(adamw_dtype dt, const ExpertRowsArgs& a, int sms, cudaStream_t s);
-cudaError_t launch_combine(adamw_dtype dt, const ExpertRowsArgs& a, int sms, cudaStream_t s);
-cudaError_t launch_combine_backward(adamw_dtype dt, const ExpertRowsArgs& a, int sms,
-                                    cudaStream_t s);
+cudaError_t launch_dispatch(adamw_dtype dt, ExpertRowsArgs a, int sms, cudaStream_t s);
+cudaError_t launch_combine(adamw_dtype dt, ExpertRowsArgs a, int sms, cudaStream_t s);
+cudaError_t launch_combine_backward(adamw_dtype dt, ExpertRowsArgs a, int sms, cudaStream_t s);
 
 // ---- group norm (group_norm.cu, group_norm_backward.cu)
 struct GroupNormArgs {

@@ -12,6 +12,10 @@ namespace adamw {
 namespace {
 
 constexpr int kDropThreads = 256;
+#ifndef V_W
+#define V_W 2
+#endif
+constexpr int kDropWords = V_W;           // 16-byte words of each matrix on their way per thread
 
 struct Words {
   uint32_t w[4];
@@ -77,10 +81,10 @@ __global__ void __launch_bounds__(kDropThreads) dropout_dense_kernel(const Dropo
   const uint4* x = static_cast<const uint4*>(a.x);
   const uint4* r = static_cast<const uint4*>(a.residual);
   uint4* y = static_cast<uint4*>(a.y);
-  const int64_t i0 = static_cast<int64_t>(blockIdx.x) * (2 * kDropThreads) + threadIdx.x;
-  uint4 xv[2], rv[2] = {};
+  const int64_t i0 = static_cast<int64_t>(blockIdx.x) * (kDropWords * kDropThreads) + threadIdx.x;
+  uint4 xv[kDropWords], rv[kDropWords] = {};
 #pragma unroll
-  for (int u = 0; u < 2; ++u) {
+  for (int u = 0; u < kDropWords; ++u) {
     const int64_t i = i0 + u * kDropThreads;
     if (i < words) {
       xv[u] = __ldcs(x + i);
@@ -88,7 +92,7 @@ __global__ void __launch_bounds__(kDropThreads) dropout_dense_kernel(const Dropo
     }
   }
 #pragma unroll
-  for (int u = 0; u < 2; ++u) {
+  for (int u = 0; u < kDropWords; ++u) {
     const int64_t i = i0 + u * kDropThreads;
     if (i < words)
       __stcs(y + i, drop_word<T, RES>(xv[u], rv[u], static_cast<uint64_t>(i) * kPer / 4, step, a));
@@ -135,7 +139,7 @@ cudaError_t drop_launch(DropoutArgs a, cudaStream_t s) {
   const int64_t n = a.rows * a.width;
   if (dense && on_grid(a.x) && on_grid(a.y) && (!RES || on_grid(a.residual))) {
     const int64_t words = n / (16 / static_cast<int>(sizeof(T)));
-    const int64_t ctas = (words + 2 * kDropThreads - 1) / (2 * kDropThreads);
+    const int64_t ctas = (words + kDropWords * kDropThreads - 1) / (kDropWords * kDropThreads);
     if (ctas <= 0x7FFFFFFF) {
       a.width = n;
       dropout_dense_kernel<T, RES><<<static_cast<unsigned>(ctas > 0 ? ctas : 1), kDropThreads, 0, s>>>(a);

@@ -85,7 +85,7 @@ def check(tokens, width, k, dtype, pad=0, shift=0, experts=None):
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("tokens,width,k,pad,shift", [
     (1, 1, 1, 0, 0), (3, 7, 2, 0, 0), (5, 4096, 4, 0, 0), (40, 256, 8, 0, 0), (33, 129, 3, 0, 0), (20, 64, 6, 8, 0),
-    (20, 64, 6, 1, 0), (20, 64, 5, 0, 1), (9, 1601, 2, 0, 0), (7, 520, 32, 0, 0), (200, 8, 1, 0, 0), (11, 6000, 2, 0, 0)])
+    (20, 64, 6, 1, 0), (20, 64, 5, 0, 1), (301, 24, 3, 0, 0), (100, 40, 32, 0, 0), (57, 3, 2, 0, 0), (65, 130, 2, 2, 0), (9, 1601, 2, 0, 0), (7, 520, 32, 0, 0), (200, 8, 1, 0, 0), (11, 6000, 2, 0, 0)])
 def test_matches_the_definition(tokens, width, k, pad, shift, dtype):
     check(tokens, width, k, dtype, pad, shift)
 
