@@ -48,7 +48,7 @@ def step_of(t):
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("rows,width,pad,shift", [
     (1, 1, 0, 0), (1, 3, 0, 0), (1, 4, 0, 0), (3, 5, 0, 0), (2, 1024, 0, 0), (1, 8191, 0, 0), (33, 257, 0, 0), (17, 96, 8, 0),
-    (17, 96, 3, 0), (5, 129, 1, 1), (9, 64, 0, 1), (1000, 1, 2, 0), (7, 4096, 0, 0)])
+    (17, 96, 3, 0), (5, 129, 1, 1), (9, 64, 0, 1), (300, 264, 16, 0), (1000, 1, 2, 0), (7, 4096, 0, 0)])
 def test_matches_the_definition(rows, width, pad, shift, dtype):
     rng = np.random.default_rng(rows * 31 + width)
     x, r, dy = (rows_of(rng.normal(0, 1.5, (rows, width)), dtype, pad, shift) for _ in range(3))
