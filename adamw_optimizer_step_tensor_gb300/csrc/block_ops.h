@@ -39,11 +39,13 @@ struct RouteArgs {
   int32_t* slots;              // null: no places
   int32_t* starts;             // null: no places
   const float* dweights;       // backward
+  int32_t wide;                // backward: lanes of a token
   void* dlogits;               // backward
   int64_t dstride;
   int32_t* counts;             // plan-owned: [chunks][pitch]
   int32_t pitch;               // experts, up to a multiple of four
   int32_t per_group;           // experts of a group
+  int32_t group_lanes;         // lanes of a group in a team
   int32_t group_factor;        // e * factor >> 20 is the group of e < 1024
   int32_t chunks;              // CTAs that share the tokens, in their order
   int32_t per_chunk;           // tokens of a chunk

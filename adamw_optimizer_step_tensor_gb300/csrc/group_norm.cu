@@ -563,7 +563,10 @@ GnCut gn_cut(const GroupNormArgs& a, int piece, int most, int sms) {
 }
 
 int gn_cluster_bytes(const GroupNormArgs& a, const GnCut& c, int piece) {
-  return c.part_rows * c.wide * piece * a.size * (a.dy != nullptr ? 2 : 1);
+  const int bytes = c.part_rows * c.wide * piece * a.size * (a.dy != nullptr ? 2 : 1);
+  // the threads' column sums take the elements' place at the end
+  const int columns = a.dy != nullptr ? 2 * ((piece + 1) / 2) * kGnThreads * static_cast<int>(sizeof(float2)) : 0;
+  return bytes > columns ? bytes : columns;
 }
 
 GroupNormSpace group_norm_space(int32_t channels, int32_t groups, int64_t max_samples, int sms) {

@@ -12,27 +12,30 @@ namespace {
 constexpr int kSmallBackward = 4;       // pieces of x and of dy a thread of the small kernel holds
 constexpr int kFlush = 64;              // samples whose column sums a thread adds up before they join the rest
 
-// The CTA's column sums from its threads', rows of threads in order.
+// The CTA's column sums from its threads': s holds [2 kPairs][kGnThreads] pairs, of the weight
+// and the bias in turn.  Rows of threads are added up by halves.  Called by all threads.
 template <int N>
-__device__ __forceinline__ void gn_columns_out(const GroupNormArgs& a, const GnCut& c, const GnPlace<N>& at,
-                                               const float2 (&dw)[gn_pairs<N>()], const float2 (&db)[gn_pairs<N>()],
-                                               float* s) {
+__device__ __forceinline__ void gn_columns_out(const GroupNormArgs& a, const GnCut& c, const GnPlace<N>& at, float2* s) {
+  constexpr int kPairs = gn_pairs<N>();
   if (a.dweight == nullptr && a.dbias == nullptr) return;
-#pragma unroll
-  for (int which = 0; which < 2; ++which) {
-    float* out = a.columns + (static_cast<int64_t>(which) * gridDim.x + blockIdx.x) * a.channels;
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const float2 v = which == 0 ? dw[i / 2] : db[i / 2];
+  int half = 1;
+  while (2 * half < c.at_once) half *= 2;
+  if (c.at_once > 1)
+    for (; half > 0; half /= 2) {
       __syncthreads();
-      s[threadIdx.x] = i % 2 == 0 ? v.x : v.y;
-      __syncthreads();
-      if (at.there && at.row0 == 0) {
-        float t = 0.0f;
-        for (int r = 0; r < c.at_once; ++r) t += s[r * c.wide + threadIdx.x];
-        out[at.channel() + i] = t;
+      if (at.there && at.row0 < half && at.row0 + half < c.at_once) {
+        float2* mine = s + threadIdx.x;
+#pragma unroll
+        for (int j = 0; j < 2 * kPairs; ++j) mine[j * kGnThreads] = add2(mine[j * kGnThreads], mine[j * kGnThreads + half * c.wide]);
       }
     }
+  if (!at.there || at.row0 != 0) return;
+  float* out = a.columns + static_cast<int64_t>(blockIdx.x) * a.channels + at.channel();
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const float2 w = s[(2 * (i / 2)) * kGnThreads + threadIdx.x], b = s[(2 * (i / 2) + 1) * kGnThreads + threadIdx.x];
+    out[i] = i % 2 == 0 ? w.x : w.y;
+    out[static_cast<int64_t>(gridDim.x) * a.channels + i] = i % 2 == 0 ? b.x : b.y;
   }
 }
 
@@ -143,10 +146,10 @@ __global__ void __launch_bounds__(kGnThreads, K == 1 ? 3 : 2) gn_backward_small_
   let_next_kernel_start();
 #pragma unroll
   for (int i = 0; i < kPairs; ++i) {
-    col_w[i] = add2(s_column[2 * i][threadIdx.x], col_w[i]);
-    col_b[i] = add2(s_column[2 * i + 1][threadIdx.x], col_b[i]);
+    s_column[2 * i][threadIdx.x] = add2(s_column[2 * i][threadIdx.x], col_w[i]);
+    s_column[2 * i + 1][threadIdx.x] = add2(s_column[2 * i + 1][threadIdx.x], col_b[i]);
   }
-  gn_columns_out<N>(a, c, at, col_w, col_b, s_sum);
+  gn_columns_out<N>(a, c, at, &s_column[0][0]);
 }
 
 __device__ __forceinline__ float2 gn_from(float2 t, int lanes) {
@@ -264,8 +267,14 @@ __global__ void __launch_bounds__(kGnThreads, 3) gn_backward_cluster_kernel(cons
     }
   }
   let_next_kernel_start();
-  __syncthreads();
-  gn_columns_out<N>(a, c, at, all_w, all_b, reinterpret_cast<float*>(s_sum));
+  __syncthreads();                        // the last sample is done with
+  float2* s_column = reinterpret_cast<float2*>(s_tile) + threadIdx.x;
+#pragma unroll
+  for (int j = 0; j < kPairs; ++j) {
+    s_column[2 * j * kGnThreads] = all_w[j];
+    s_column[(2 * j + 1) * kGnThreads] = all_b[j];
+  }
+  gn_columns_out<N>(a, c, at, reinterpret_cast<float2*>(s_tile));
 }
 
 constexpr int kBackwardDepth = 10;      // steps on their way, at most 72 KB a CTA
@@ -392,13 +401,7 @@ __global__ void __launch_bounds__(kGnFusedThreads, kGnCtasPerSm) gn_backward_fus
   } else {
     gn_backward_items<T, N, SILU>(a, c, at, part, words, s_ring, s_stat, s_column);
   }
-  float2 all_w[kPairs], all_b[kPairs];
-#pragma unroll
-  for (int j = 0; j < kPairs; ++j) {
-    all_w[j] = s_column[2 * j * kGnThreads];
-    all_b[j] = s_column[(2 * j + 1) * kGnThreads];
-  }
-  gn_columns_out<N>(a, c, at, all_w, all_b, reinterpret_cast<float*>(s_stat));
+  gn_columns_out<N>(a, c, at, reinterpret_cast<float2*>(reinterpret_cast<char*>(s_ring) + Ring::kBytes));
   gn_leave(a, c);
 }
 

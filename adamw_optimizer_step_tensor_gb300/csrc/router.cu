@@ -278,12 +278,19 @@ __device__ __forceinline__ int choose(const T* row, float (&k)[V], const float* 
       for (int i = 0; i < V; ++i)
         if (32 * i + lane < r.experts) s[32 * i + lane] = v[i];
       __syncwarp();
-      if (lane < r.groups)
-        for (int i = 0; i < per; ++i) {
-          const float x = s[lane * per + i];
+      const int share = 32 / choice_lanes(r.groups);       // lanes of a group
+      group = lane / share;
+      if (group < r.groups)
+        for (int i = lane - group * share; i < per; i += share) {
+          const float x = s[group * per + i];
           tops.y = fmaxf(tops.y, fminf(tops.x, x));
           tops.x = fmaxf(tops.x, x);
         }
+      for (int o = 1; o < share; o *= 2) {
+        const float x = __shfl_xor_sync(kFull, tops.x, o), y = __shfl_xor_sync(kFull, tops.y, o);
+        tops.y = fmaxf(fminf(tops.x, x), fmaxf(tops.y, y));
+        tops.x = fmaxf(tops.x, x);
+      }
       __syncwarp();
     }
     const float of = two && tops.y > -INFINITY ? tops.x + tops.y : tops.x;
@@ -563,12 +570,12 @@ __device__ __forceinline__ float team_sum(float x) {
   return x;
 }
 
-// V logits of a lane: experts V l to V l + V - 1 of its token.
+// V logits of a lane from expert e0 on; -inf from `end` on.
 template <typename T, int V>
 struct TeamRow {
   static constexpr int kBytes = V * static_cast<int>(sizeof(T));
   uint32_t word[kBytes / 4];
-  __device__ __forceinline__ void load(const T* row, int e0, int experts, bool vec) {
+  __device__ __forceinline__ void load(const T* row, int e0, int end, bool vec) {
     if (vec) {                            // whole rows, on the grid of a lane's bytes (16 at most)
       const T* p = row + e0;
       if constexpr (kBytes >= 16) {
@@ -588,7 +595,7 @@ struct TeamRow {
     }
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const T z = e0 + i < experts ? __ldcs(row + e0 + i) : from_f32<T>(-INFINITY);
+      const T z = e0 + i < end ? __ldcs(row + e0 + i) : from_f32<T>(-INFINITY);
       if constexpr (sizeof(T) == 4) {
         word[i] = __float_as_uint(z);
       } else {
@@ -604,9 +611,24 @@ struct TeamRow {
   }
 };
 
-// A token's key in 64 bits, of an expert's logit and bias.  Out of line: few tokens need it.
-__device__ __noinline__ double exact_key(float z, float b, bool by_logit) {
-  return by_logit ? static_cast<double>(z) : 1.0 / (1.0 + exp(-static_cast<double>(z))) + static_cast<double>(b);
+// A token's key in 64 bits, of an expert's logit and bias: by the logit alone, or the softmax's
+// (of the row's largest logit and sum) or the sigmoid's score.  Out of line: few tokens need it.
+__device__ __noinline__ double exact_key(float z, float b, bool by_logit, bool softmax, double top, double total) {
+  if (by_logit) return z;
+  const double e = exp(softmax ? z - top : -static_cast<double>(z));
+  return (softmax ? e / total : 1.0 / (1.0 + e)) + static_cast<double>(b);
+}
+// A team's sum of exponentials in 64 bits.
+template <typename T, int LANES>
+__device__ __noinline__ double exact_sum(const T* row, int e0, int end, int many, float top) {
+  double t = 0.0;
+  for (int i = 0; i < many && e0 + i < end; ++i) {
+    const float z = to_f32(row[e0 + i]);
+    t += z > -INFINITY ? exp(static_cast<double>(z) - top) : 0.0;
+  }
+#pragma unroll
+  for (int o = LANES / 2; o > 0; o /= 2) t += __shfl_xor_sync(kFull, t, o);
+  return t;
 }
 
 template <int LANES>
@@ -629,10 +651,13 @@ __global__ void __launch_bounds__(32 * kTeamWarps, 1) route_teams_kernel(const R
   const int first = blockIdx.x * a.per_chunk;
   const int tokens = min(a.tokens - first, a.per_chunk);
   const T* rows = static_cast<const T*>(a.logits) + static_cast<int64_t>(first) * a.stride;
-  const int e0 = l * V;
+  // A group has lanes of its own, a power of two of them (without groups all are one).
+  const bool by_group = r.groups > 1 && r.top_groups < r.groups;
+  const int per = by_group ? a.per_group : experts, group_lanes = by_group ? a.group_lanes : LANES, group = by_group ? l / group_lanes : 0;
+  const int e0 = min(group * per + (l - group * group_lanes) * V, experts), end = min((group + 1) * per, experts);
   TeamRow<T, V> next;
   const int start = warp * kTokens + sub;
-  if (start < tokens) next.load(rows + start * a.stride, e0, experts, vec);
+  if (start < tokens) next.load(rows + static_cast<int64_t>(start) * a.stride, e0, end, vec);
   if (threadIdx.x == 0) s_bias_max = 0;
   __syncthreads();
   bool any = false;
@@ -649,11 +674,9 @@ __global__ void __launch_bounds__(32 * kTeamWarps, 1) route_teams_kernel(const R
   const float* bias = __syncthreads_or(any) ? s_bias : nullptr;
   const float bias_max = __uint_as_float(s_bias_max);
   const bool softmax = r.score == ADAMW_SCORE_SOFTMAX;
-  const bool by_group = r.groups > 1 && r.top_groups < r.groups;
   const bool two = by_group && r.group_score == ADAMW_GROUP_TOP2;
   const bool scored = bias != nullptr || two;           // keys are scores, not logits
   const bool sums = softmax && (scored || !r.renormalise);
-  const int group_lanes = by_group ? a.per_group / V : LANES, group = by_group ? l / group_lanes : 0;
   for (int t0 = warp * kTokens; t0 < tokens; t0 += kTeamWarps * kTokens) {
     const int t = t0 + sub;
     const bool live = t < tokens;
@@ -668,23 +691,29 @@ __global__ void __launch_bounds__(32 * kTeamWarps, 1) route_teams_kernel(const R
       z[i] = fmaxf(f, -INFINITY);                                 // a NaN is not there
       top = fmaxf(top, z[i]);
     }
-    if (t + kTeamWarps * kTokens < tokens) next.load(row + static_cast<int64_t>(kTeamWarps * kTokens) * a.stride, e0, experts, vec);
+    if (t + kTeamWarps * kTokens < tokens) next.load(row + static_cast<int64_t>(kTeamWarps * kTokens) * a.stride, e0, end, vec);
     constexpr uint32_t kTeam = kFull >> (32 - LANES);
     const bool bad = (__ballot_sync(kFull, nan || (softmax && top == INFINITY)) >> (sub * LANES) & kTeam) != 0;
     if (sums) {
       top = team_max<LANES>(top);
-      float sum = 0.0f;
+      float sum[V];
 #pragma unroll
-      for (int i = 0; i < V; ++i) sum += z[i] > -INFINITY ? key_exp(z[i] - top) : 0.0f;
-      total = team_sum<LANES>(sum);
+      for (int i = 0; i < V; ++i) sum[i] = z[i] > -INFINITY ? key_exp(z[i] - top) : 0.0f;
+#pragma unroll
+      for (int half = V / 2; half > 0; half /= 2)
+#pragma unroll
+        for (int i = 0; i < half; ++i) sum[i] += sum[i + half];
+      total = team_sum<LANES>(sum[0]);
     }
     // Scores become whole units of a scale from the lowest possible key to the highest, a
-    // float's 23 bits by adding 2^23: off by a unit, and by their own errors: softmax as the
-    // warp's kernel has it; sigmoid, in 2^-24: the exponential's 2 units and its argument's
-    // rounding, each times s (1 - s), the sum's 1, the reciprocal's 2 and the bias's 1, below 6.
+    // float's 23 bits by adding 2^23: off by a unit, and by their own errors, in 2^-24 of the
+    // row's largest score.  Sigmoid: the exponential's 2 units and its argument's rounding, each
+    // times s (1 - s), the sum's 1, the reciprocal's 2 and the bias's 1, below 6.  Softmax: the
+    // exponential's 4, its argument's 2 roundings times |d| e^-d, the sum's 9 (of pairs, in a lane
+    // and across the team) and the quotient's 5, the bias's 1, below 24.
     const float inv = __fdividef(1.0f, total), most_score = softmax ? inv : 1.0f;
     const float units = __fdividef(8388608.0f - 17000.0f, most_score + 2.0f * bias_max);
-    const float off = (softmax ? 0x1p-20f + V * 0x1p-24f : 0x1.8p-22f) * (most_score + bias_max) * units + 1.5f;
+    const float off = (softmax ? 0x1.8p-20f : 0x1.8p-22f) * (most_score + bias_max) * units + 1.5f;
     uint32_t key[V], best = 0, second = 0;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -702,6 +731,7 @@ __global__ void __launch_bounds__(32 * kTeamWarps, 1) route_teams_kernel(const R
       best = max(best, key[i]);
     }
     bool sure = bias_max < INFINITY || !live;     // no scale holds an infinite bias
+    double total64 = 0.0;                         // once it is needed
     best = max(best, 1u);                         // 1: none left
     if (by_group) {
       uint32_t one = best, other = second;
@@ -731,7 +761,8 @@ __global__ void __launch_bounds__(32 * kTeamWarps, 1) route_teams_kernel(const R
       if (most != 0)
         sure = sure && (exact ? sizeof(T) == 2 || least >> 5 != most >> 5
                               : static_cast<float>((least >> 5) - (most >> 5)) > 2.0f * off * (summed ? 2.0f : 1.0f));
-      if (!(softmax && scored) && __any_sync(kFull, !sure)) {
+      if (__any_sync(kFull, !sure)) {
+        if (softmax && scored) total64 = exact_sum<T, LANES>(row, e0, end, V, top);
         // again from the 64-bit keys of each lane's two best, if its third is far enough below
         uint32_t third = 0;
 #pragma unroll
@@ -742,7 +773,7 @@ __global__ void __launch_bounds__(32 * kTeamWarps, 1) route_teams_kernel(const R
         for (int i = 0; i < 2; ++i) {
           const uint32_t k = i == 0 ? best : second;
           const int e = static_cast<int>(kNumber - (k & kNumber));
-          x[i] = k > kNone ? exact_key(to_f32(row[e]), bias != nullptr ? bias[e] : 0.0f, exact) : -INFINITY;
+          x[i] = k > kNone ? exact_key(to_f32(row[e]), bias != nullptr ? bias[e] : 0.0f, exact, softmax, top, total64) : -INFINITY;
         }
         double one64 = fmax(x[0], x[1]), other64 = fmin(x[0], x[1]);
         for (int o = 1; o < group_lanes; o *= 2) {
@@ -796,7 +827,8 @@ __global__ void __launch_bounds__(32 * kTeamWarps, 1) route_teams_kernel(const R
       else if (sizeof(T) == 4) sure = sure && mine >> 9 != after >> 9;
     }
     sure = (__ballot_sync(kFull, sure) >> (sub * LANES) & kTeam) == kTeam;      // one answer for the team
-    if (__any_sync(kFull, !sure && live) && !(softmax && scored)) {
+    if (__any_sync(kFull, !sure && live)) {
+      if (softmax && bias != nullptr && total64 == 0.0) total64 = exact_sum<T, LANES>(row, e0, end, V, top);
       // Again from 64-bit keys: as many best as the team has lanes, each in its lane, if the one
       // after them is far enough below the last chosen.
       const bool by_logit = bias == nullptr || bad, grouped = sure_of_groups;
@@ -813,7 +845,7 @@ __global__ void __launch_bounds__(32 * kTeamWarps, 1) route_teams_kernel(const R
       const uint32_t last = __shfl_sync(kFull, mine, r.top_k - 1, LANES), then = team_max<LANES>(best);
       const bool far = then <= kNone || (scored && !bad ? static_cast<float>((last >> 9) - (then >> 9)) > 2.0f * off : last >> 9 != then >> 9);
       const int e = mine64 > kNone ? static_cast<int>(kNumber - (mine64 & kNumber)) : -1;
-      const double x = e >= 0 ? exact_key(to_f32(row[e]), bias != nullptr ? bias[e] : 0.0f, by_logit) : -INFINITY;
+      const double x = e >= 0 ? exact_key(to_f32(row[e]), bias != nullptr ? bias[e] : 0.0f, by_logit, softmax, top, total64) : -INFINITY;
       int before = 0, now = -1;
       for (int j = 0; j < LANES; ++j) {
         const double v = __shfl_sync(kFull, x, j, LANES);
@@ -907,13 +939,13 @@ __global__ void __launch_bounds__(kPlaceThreads) place_kernel(const RouteArgs a)
               blockIdx.x == 0);
 }
 
-// The gradient: a warp takes as many tokens at once as their choices fill its lanes.
+// The gradient: a warp takes as many tokens at once as fill its lanes, `wide` each.
 template <typename T, int V>
 __global__ void __launch_bounds__(32 * kBackWarps) route_backward_kernel(const RouteArgs a, const bool vec) {
   extern __shared__ float s_grad[];
   const adamw_router& r = a.router;
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
-  const int wide = choice_lanes(r.top_k), at_once = 32 / wide, sub = lane / wide, j = lane % wide;
+  const int wide = a.wide, at_once = 32 / wide, sub = lane / wide, j = lane % wide;
   float* mine = s_grad + warp * (32 * V);
   const bool softmax = r.score == ADAMW_SCORE_SOFTMAX;
   const bool dense = softmax && !r.renormalise;
@@ -1028,29 +1060,25 @@ cudaError_t route_width(const RouteArgs& a, cudaStream_t s) {
 template <typename T, int LANES, int V>
 cudaError_t route_teams(const RouteArgs& a, cudaStream_t s) {
   constexpr int kGrid = V * sizeof(T) < 16 ? V * sizeof(T) : 16;
-  const bool vec = a.router.experts == LANES * V && reinterpret_cast<uintptr_t>(a.logits) % kGrid == 0 &&
+  const bool vec = a.router.experts == LANES * V && (a.router.groups == 1 || a.per_group % V == 0) && reinterpret_cast<uintptr_t>(a.logits) % kGrid == 0 &&
                    a.stride * sizeof(T) % kGrid == 0;
   route_teams_kernel<T, LANES, V><<<a.chunks, 32 * kTeamWarps, team_smem<LANES>(a.router.experts), s>>>(a, vec);
   return cudaGetLastError();
 }
-// Lanes of a token's team and experts of a lane; 0 lanes where a warp takes the token: more
-// experts than the teams hold, or groups that are not of whole lanes, a power of two of them.
+// Lanes of a token's team, experts of a lane and lanes of a group: the fewest lanes that hold
+// them.  0 lanes where a warp takes the token: more experts than 32 lanes of 16 hold.
 struct Team {
-  int lanes, experts;
+  int lanes, experts, group_lanes;
 };
 Team team_for(const adamw_router& r) {
-  Team t{0, 0};
-  const int lanes = r.top_k <= 8 && r.experts <= 128 ? 8 : (r.top_k <= 16 && r.experts <= 256 ? 16 : 32);
-  for (int v = 4; v <= 16; v *= 2)
-    if (r.experts <= lanes * v) {
-      t = Team{lanes, v};
-      break;
+  const bool by_group = r.groups > 1 && r.top_groups < r.groups;
+  const int groups = by_group ? r.groups : 1, per = r.experts / groups;
+  for (int lanes = 8; lanes <= 32; lanes *= 2)
+    for (int v = 4; v <= 16; v *= 2) {
+      const int of_group = by_group ? choice_lanes((per + v - 1) / v) : (per + v - 1) / v;
+      if (r.top_k <= lanes && groups * of_group <= lanes) return Team{lanes, v, of_group};
     }
-  if (r.groups > 1 && r.top_groups < r.groups) {
-    const int per = r.experts / r.groups, of = t.experts > 0 ? per / t.experts : 0;
-    if (t.experts == 0 || per % t.experts != 0 || (of & (of - 1)) != 0) t = Team{0, 0};
-  }
-  return t;
+  return Team{0, 0, 0};
 }
 
 #define ADAMW_ROUTE_TEAM(t, CALL)                                                             \
@@ -1059,10 +1087,13 @@ Team team_for(const adamw_router& r) {
                      : ((t).experts == 4 ? CALL(32, 4) : (t).experts == 8 ? CALL(32, 8) : CALL(32, 16)))
 
 template <typename T, int V>
-cudaError_t back_width(const RouteArgs& a, int sms, cudaStream_t s) {
+cudaError_t back_width(RouteArgs a, int sms, cudaStream_t s) {
+  // the lanes of a choice, or more where that leaves an SM fewer than 16 warps
+  a.wide = choice_lanes(a.router.top_k);
+  while (a.wide < 32 && static_cast<int64_t>(a.tokens) * a.wide < 32LL * 16 * sms) a.wide *= 2;
   const bool vec = reinterpret_cast<uintptr_t>(a.dlogits) % 16 == 0 && a.dstride * sizeof(T) % 16 == 0 &&
                    a.router.experts * sizeof(T) % 16 == 0;
-  const int64_t per_cta = kBackWarps * (32 / choice_lanes(a.router.top_k));
+  const int64_t per_cta = kBackWarps * (32 / a.wide);
   const int64_t ctas = (a.tokens + per_cta - 1) / per_cta, most = 8LL * sms;
   route_backward_kernel<T, V><<<static_cast<unsigned>(ctas < most ? ctas : most), 32 * kBackWarps,
                                 kBackWarps * 32 * V * sizeof(float), s>>>(a, vec);
@@ -1138,17 +1169,19 @@ cudaError_t prepare_router(const adamw_router& r) {
 }
 
 cudaError_t launch_route(adamw_dtype dt, RouteArgs a, int sms, cudaStream_t s) {
-  // one CTA up to 64 tokens, which spares the second kernel, else a share of every SM's
+  // one CTA for what it takes in two turns, up to 64 tokens, which spares the second kernel;
+  // else a share of every SM's, a third of a turn at least
   const Team team = team_for(a.router);
   const int turn = team.lanes > 0 ? kTeamWarps * (32 / team.lanes) : chunk_warps<float>(a);
   const int64_t most = router_chunks(sms);
-  int64_t chunks = a.tokens <= 64 ? 1 : (a.tokens + turn - 1) / turn;
+  int64_t chunks = a.tokens <= 2 * turn && a.tokens <= 64 ? 1 : (a.tokens + turn / 3 - 1) / (turn / 3);
   if (chunks > most) chunks = most;
   a.per_chunk = static_cast<int32_t>((a.tokens + chunks - 1) / chunks);
   a.chunks = a.per_chunk > 0 ? (a.tokens + a.per_chunk - 1) / a.per_chunk : 1;
   a.pitch = router_pitch(a.router.experts);
   a.per_group = a.router.experts / a.router.groups;
   a.group_factor = ((1 << 20) + a.per_group - 1) / a.per_group;
+  a.group_lanes = team.group_lanes;
   cudaError_t e = dt == ADAMW_F32   ? route_type<float>(a, team, s)
                   : dt == ADAMW_F16 ? route_type<__half>(a, team, s)
                                     : route_type<__nv_bfloat16>(a, team, s);
