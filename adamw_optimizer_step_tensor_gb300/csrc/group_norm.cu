@@ -20,7 +20,7 @@ template <typename T, int N, bool SILU, int K>
 __global__ void __launch_bounds__(kGnThreads, K == 1 ? kSmallCtasPerSm : 2) gn_forward_small_kernel(const GroupNormArgs a, const GnCut c) {
   using P = GnPiece<T, N>;
   constexpr int kPairs = gn_pairs<N>();
-  __shared__ float s_sum[kGnThreads], s_group[kGnThreads];
+  __shared__ float2 s_sum[kGnThreads], s_group[kGnThreads];
   const GnPlace<N> at(c);
   const int team = at.row0 / c.team_rows, row0 = at.row0 - team * c.team_rows;
   const bool mine = at.there && team < c.teams;
@@ -57,7 +57,7 @@ __global__ void __launch_bounds__(kGnThreads, K == 1 ? kSmallCtasPerSm : 2) gn_f
 #pragma unroll
         for (int i = 0; i < kPairs; ++i) sum = add2(sum, p[k].pair(i));
       }
-    const float mean = gn_team_sum(sum.x + sum.y, c, s_sum, s_group) * inv;
+    const float mean = gn_team_sums(make_float2(sum.x + sum.y, 0.0f), c, s_sum, s_group).x * inv;
     float2 square = both(0.0f);
 #pragma unroll
     for (int k = 0; k < K; ++k)
@@ -69,7 +69,7 @@ __global__ void __launch_bounds__(kGnThreads, K == 1 ? kSmallCtasPerSm : 2) gn_f
           square = fma2(d, d, square);
         }
       }
-    const float spread = gn_team_sum(square.x + square.y, c, s_sum, s_group);
+    const float spread = gn_team_sums(make_float2(square.x + square.y, 0.0f), c, s_sum, s_group).x;
     const float rstd = __frcp_rn(__fsqrt_rn(fmaf(spread, inv, a.eps)));
     if (!live) continue;
     if (row0 == 0 && at.piece % c.group_pieces == 0) {

@@ -416,11 +416,12 @@ __device__ __forceinline__ void gn_leave(const GroupNormArgs& a, const GnCut& c)
 
 // ---------------------------------------------------------------- small kernels
 
-// The sum over each group's threads of one sample (one team), the same in all of them.
-// s: kGnThreads floats; used by all threads of the CTA at the same time.
-__device__ __forceinline__ float gn_team_sum(float x, const GnCut& c, float* s, float* s_group) {
+// The sums of two numbers over each group's threads of one sample (one team), the same in all
+// of them.  s, s_group: kGnThreads pairs; used by all threads of the CTA at the same time.
+__device__ __forceinline__ float2 gn_team_sums(float2 x, const GnCut& c, float2* s, float2* s_group) {
   if (c.by_lanes && c.team_rows == 1) {
-    for (int o = 1; o < c.group_pieces; o <<= 1) x += __shfl_xor_sync(kFull, x, o);
+    for (int o = 1; o < c.group_pieces; o <<= 1)
+      x = add2(x, make_float2(__shfl_xor_sync(kFull, x.x, o), __shfl_xor_sync(kFull, x.y, o)));
     return x;
   }
   const int row = threadIdx.x / c.wide, p = threadIdx.x - row * c.wide;
@@ -428,31 +429,32 @@ __device__ __forceinline__ float gn_team_sum(float x, const GnCut& c, float* s, 
   __syncthreads();
   s[threadIdx.x] = x;
   __syncthreads();
-  const int all = c.teams * tile_groups, entries = c.team_rows * c.group_pieces;
-  if (entries <= 16 || all >= kGnThreads / 2) {
+  const int all = c.teams * tile_groups, q = c.group_pieces, entries = c.team_rows * q;
+  // entry e of a group: piece e % q of row e / q.  A thread adds up a few entries, a warp many.
+  if (entries <= 8 || all >= kGnThreads / 2) {
     for (int g = threadIdx.x; g < all; g += kGnThreads) {
-      const int team = g / tile_groups, q = g - team * tile_groups;
-      float t = 0.0f;
+      const int team = g / tile_groups, first = team * c.team_rows * c.wide + (g - team * tile_groups) * q;
+      float2 t = both(0.0f);
       for (int r = 0; r < c.team_rows; ++r)
-        for (int k = 0; k < c.group_pieces; ++k)
-          t += s[(team * c.team_rows + r) * c.wide + q * c.group_pieces + k];
+        for (int k = 0; k < q; ++k) t = add2(t, s[first + r * c.wide + k]);
       s_group[g] = t;
     }
   } else {
     const int lane = threadIdx.x & 31;
     for (int g = threadIdx.x / 32; g < all; g += kGnWarps) {
-      const int team = g / tile_groups, q = g - team * tile_groups;
-      float t = 0.0f;
-      for (int r = 0; r < c.team_rows; ++r)
-        for (int k = lane; k < c.group_pieces; k += 32)
-          t += s[(team * c.team_rows + r) * c.wide + q * c.group_pieces + k];
-      t = warp_total(t);
+      const int team = g / tile_groups, first = team * c.team_rows * c.wide + (g - team * tile_groups) * q;
+      float2 t = both(0.0f);
+      for (int e = lane; e < entries; e += 32) {
+        const int r = e / q;
+        t = add2(t, s[first + r * (c.wide - q) + e]);
+      }
+      t = make_float2(warp_total(t.x), warp_total(t.y));
       if (lane == 0) s_group[g] = t;
     }
   }
   __syncthreads();
   const int team = row / c.team_rows;
-  return team < c.teams ? s_group[team * tile_groups + p / c.group_pieces] : 0.0f;
+  return team < c.teams ? s_group[team * tile_groups + p / q] : both(0.0f);
 }
 
 }  // namespace

@@ -43,7 +43,7 @@ template <typename T, int N, bool SILU, int K>
 __global__ void __launch_bounds__(kGnThreads, K == 1 ? 3 : 2) gn_backward_small_kernel(const GroupNormArgs a, const GnCut c) {
   using P = GnPiece<T, N>;
   constexpr int kPairs = gn_pairs<N>();
-  __shared__ float s_sum[kGnThreads], s_group[kGnThreads];
+  __shared__ float2 s_sum[kGnThreads], s_group[kGnThreads];
   __shared__ float2 s_column[2 * kPairs][kGnThreads];     // sums of all but the last few samples
   const GnPlace<N> at(c);
   const int team = at.row0 / c.team_rows, row0 = at.row0 - team * c.team_rows;
@@ -115,8 +115,8 @@ __global__ void __launch_bounds__(kGnThreads, K == 1 ? 3 : 2) gn_backward_small_
           two = fma2(g, xhat, two);
         }
       }
-    const float mean_g = gn_team_sum(N == 1 ? one.x : one.x + one.y, c, s_sum, s_group) * inv;
-    const float mean_gx = gn_team_sum(N == 1 ? two.x : two.x + two.y, c, s_sum, s_group) * inv;
+    const float2 means = mul2(gn_team_sums(N == 1 ? make_float2(one.x, two.x) : make_float2(one.x + one.y, two.x + two.y), c, s_sum, s_group),
+                              both(-inv));
     if (++since == kFlush) {
       since = 0;
 #pragma unroll
@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(kGnThreads, K == 1 ? 3 : 2) gn_backward_small_
         for (int i = 0; i < kPairs; ++i) {
           const float2 xhat = fma2(p[k].pair(i), both(rstd), both(start));
           const float2 dz = through<T, SILU>(q[k].pair(i), fma2(xhat, w[i], b[i]));
-          p[k].set(i, mul2(both(rstd), fma2(xhat, both(-mean_gx), fma2(dz, w[i], both(-mean_g)))));
+          p[k].set(i, mul2(both(rstd), fma2(xhat, both(means.y), fma2(dz, w[i], both(means.x)))));
         }
         p[k].store(dx + k * c.team_rows * a.out_position);
       }
