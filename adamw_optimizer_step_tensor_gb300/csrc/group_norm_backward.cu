@@ -152,6 +152,95 @@ __global__ void __launch_bounds__(kGnThreads, K == 1 ? 3 : 2) gn_backward_small_
   gn_columns_out<N>(a, c, at, &s_column[0][0]);
 }
 
+// As the forward pass's kernel for samples of one position and groups of neighbouring lanes.
+constexpr int kLaneSamples = 2;
+template <typename T, int N, bool SILU>
+__global__ void __launch_bounds__(kGnThreads, 3) gn_backward_lanes_kernel(const GroupNormArgs a, const GnCut c) {
+  using P = GnPiece<T, N>;
+  constexpr int kPairs = gn_pairs<N>(), U = kLaneSamples;
+  __shared__ float2 s_column[2 * kPairs][kGnThreads];     // sums of all but the last few samples
+  const GnPlace<N> at(c);
+  float2 w[kPairs], b[kPairs], col_w[kPairs] = {}, col_b[kPairs] = {};
+  gn_weights<T, N>(a.weight, a.weight_f32, 1.0f, at, w);
+  gn_weights<T, N>(a.bias, a.weight_f32, 0.0f, at, b);
+#pragma unroll
+  for (int j = 0; j < 2 * kPairs; ++j) s_column[j][threadIdx.x] = both(0.0f);
+  const float inv = 1.0f / static_cast<float>(c.per);
+  const int64_t pace = static_cast<int64_t>(gridDim.x) * c.teams;
+  const T *x0 = static_cast<const T*>(a.x) + at.channel(), *dy0 = static_cast<const T*>(a.dy) + at.channel();
+  int since = 0;
+  for (int64_t n0 = static_cast<int64_t>(blockIdx.x) * c.teams; n0 < a.samples; n0 += U * pace) {
+    P p[U], q[U];
+    float rstd[U], start[U];
+    float2 t[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t sample = n0 + u * pace + at.row0;
+      p[u].v = {};
+      q[u].v = {};
+      rstd[u] = start[u] = 0.0f;
+      if (at.there && sample < a.samples) {
+        p[u].load_last(x0 + sample * a.x_sample);
+        q[u].load_last(dy0 + sample * a.dy_sample);
+        rstd[u] = __ldg(a.rstd + sample * a.groups + at.group);
+        start[u] = __ldg(a.mean + sample * a.groups + at.group);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const bool live = at.there && n0 + u * pace + at.row0 < a.samples;
+      start[u] *= -rstd[u];
+      float2 one = both(0.0f), two = both(0.0f);
+      if (live) {
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i) {
+          const float2 xhat = fma2(p[u].pair(i), both(rstd[u]), both(start[u]));
+          const float2 dz = through<T, SILU>(q[u].pair(i), fma2(xhat, w[i], b[i]));
+          col_b[i] = add2(col_b[i], dz);
+          col_w[i] = fma2(dz, xhat, col_w[i]);
+          const float2 g = mul2(dz, w[i]);
+          one = add2(one, g);
+          two = fma2(g, xhat, two);
+        }
+      }
+      t[u] = N == 1 ? make_float2(one.x, two.x) : make_float2(one.x + one.y, two.x + two.y);
+    }
+    for (int o = 1; o < c.group_pieces; o *= 2)
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        t[u] = add2(t[u], make_float2(__shfl_xor_sync(kFull, t[u].x, o), __shfl_xor_sync(kFull, t[u].y, o)));
+    if (++since == kFlush / U) {
+      since = 0;
+#pragma unroll
+      for (int i = 0; i < kPairs; ++i) {
+        s_column[2 * i][threadIdx.x] = add2(s_column[2 * i][threadIdx.x], col_w[i]);
+        s_column[2 * i + 1][threadIdx.x] = add2(s_column[2 * i + 1][threadIdx.x], col_b[i]);
+        col_w[i] = col_b[i] = both(0.0f);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t sample = n0 + u * pace + at.row0;
+      if (!at.there || sample >= a.samples) continue;
+      const float2 means = mul2(t[u], both(-inv));
+#pragma unroll
+      for (int i = 0; i < kPairs; ++i) {
+        const float2 xhat = fma2(p[u].pair(i), both(rstd[u]), both(start[u]));
+        const float2 dz = through<T, SILU>(q[u].pair(i), fma2(xhat, w[i], b[i]));
+        p[u].set(i, mul2(both(rstd[u]), fma2(xhat, both(means.y), fma2(dz, w[i], both(means.x)))));
+      }
+      p[u].store(static_cast<T*>(a.out) + sample * a.out_sample + at.channel());
+    }
+  }
+  let_next_kernel_start();
+#pragma unroll
+  for (int i = 0; i < kPairs; ++i) {
+    s_column[2 * i][threadIdx.x] = add2(s_column[2 * i][threadIdx.x], col_w[i]);
+    s_column[2 * i + 1][threadIdx.x] = add2(s_column[2 * i + 1][threadIdx.x], col_b[i]);
+  }
+  gn_columns_out<N>(a, c, at, &s_column[0][0]);
+}
+
 __device__ __forceinline__ float2 gn_from(float2 t, int lanes) {
   return make_float2(__shfl_xor_sync(kFull, t.x, lanes), __shfl_xor_sync(kFull, t.y, lanes));
 }
@@ -450,6 +539,8 @@ cudaError_t gn_backward(const GroupNormArgs& a, int sms, cudaStream_t s) {
     const cudaError_t e =
         c.cluster > 0 ? gn_cluster_launch(gn_backward_cluster_kernel<T, N, SILU>, gn_cluster_bytes(a, c, N), s, a, c)
         : c.team_rows == 0 ? gn_launch(gn_backward_fused_kernel<T, N, SILU>, grid, kGnFusedThreads, gn_backward_smem<T, N>(), s, a, c)
+        : a.positions == 1 && c.by_lanes && c.teams == c.at_once
+            ? gn_launch(gn_backward_lanes_kernel<T, N, SILU>, grid, kGnThreads, 0, s, a, c)
         : a.positions <= c.team_rows
             ? gn_launch(gn_backward_small_kernel<T, N, SILU, 1>, grid, kGnThreads, 0, s, a, c)
             : gn_launch(gn_backward_small_kernel<T, N, SILU, kSmallBackward>, grid, kGnThreads, 0, s, a, c);

@@ -235,7 +235,7 @@ def test_a_wait_that_gives_up_is_reported_and_the_plan_is_fit_again():
 
 
 @pytest.mark.parametrize("shape,groups", [((9, 28, 16), 2), ((112, 359, 58), 2), ((1500, 20, 96), 3), ((1, 3, 40), 5), ((700, 1, 2056), 257),
-                                          ((3, 600, 1032), 8), ((1, 400, 8), 8), ((5, 77, 65536), 64), ((1, 9, 129 * 400), 400)])
+                                          ((3, 600, 1032), 8), ((1, 400, 8), 8), ((2500, 1, 256), 8), ((1300, 1, 4096), 64), ((7, 1, 16), 16), ((900, 1, 96), 12), ((5, 77, 65536), 64), ((1, 9, 129 * 400), 400)])
 @pytest.mark.parametrize("dtype", DTYPES)
 def test_cuts_of_every_kind(shape, groups, dtype):
     check(shape, groups, dtype, silu=True)
