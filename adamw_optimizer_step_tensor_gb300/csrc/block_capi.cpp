@@ -1,6 +1,7 @@
 // block_capi.cpp -- the extern "C" entry points of a block's operators between
 // its matrix products: dropout, routing, experts' rows, group norm.  Argument
 // validation, the plans' workspaces, and launches.
+#include <atomic>
 #include <cmath>
 #include <memory>
 #include <new>
@@ -34,6 +35,16 @@ struct adamw_group_norm_plan {
 };
 
 namespace {
+
+// The group norm's kernels ask for their shared memory once on a device.
+cudaError_t prepare_group_norm_once(int device) {
+  constexpr int kDevices = 64;
+  static std::atomic<bool> done[kDevices];
+  if (device < kDevices && done[device].load()) return cudaSuccess;
+  const cudaError_t e = prepare_group_norm();
+  if (e == cudaSuccess && device < kDevices) done[device].store(true);
+  return e;
+}
 
 void free_router_plan(adamw_router_plan* p) {
   if (!p) return;
@@ -449,7 +460,7 @@ adamw_status adamw_group_norm_plan_create(int32_t channels, int32_t groups, int6
   p->stats_at = (n.columns + 3) & ~int64_t{3};
   p->joined_at = p->stats_at + ((n.stats + 3) & ~int64_t{3});
   p->n_words = n.words;
-  cudaError_t e = prepare_group_norm();
+  cudaError_t e = prepare_group_norm_once(device);
   if (e != cudaSuccess) return failed(e, "prepare the group norm kernels");
   e = cudaMalloc(&p->d_space, (p->joined_at + n.joined) * sizeof(float));
   if (e == cudaSuccess) e = cudaMalloc(&p->d_words, (n.words + 2) * sizeof(uint32_t));

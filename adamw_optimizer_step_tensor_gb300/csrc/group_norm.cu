@@ -640,15 +640,18 @@ int gn_cluster_bytes(const GroupNormArgs& a, const GnCut& c, int piece) {
 GroupNormSpace group_norm_space(int32_t channels, int32_t groups, int64_t max_samples, int sms) {
   GroupNormSpace n{};
   const int64_t resident = static_cast<int64_t>(kGnCtasPerSm) * sms;
-  n.stats = kGnKept * resident * (groups + up(channels, kGnThreads)) * 2;
   n.joined = max_samples * groups * 2;
   n.words = kGnWords * resident;
-  // rows of column sums: what the CTAs of either kind of kernel leave, at most
+  // of the CTAs of a tile, the most where tiles are widest: fused ones leave statistics, all
+  // leave a row of column sums
   const int64_t rows = (kSmallCtasPerSm > kGnCtasPerSm ? kSmallCtasPerSm : kGnCtasPerSm) * static_cast<int64_t>(sms);
   for (int piece : {1, 2, 4, 8}) {
     if (channels / groups % piece != 0) continue;
     const int64_t tiles = up(channels / piece, kGnThreads);
+    const int64_t parts = resident / tiles > 1 ? resident / tiles : 1;
+    const int64_t stats = kGnKept * parts * (groups + tiles) * 2;
     const int64_t ctas = rows / tiles > kGnClusterMax ? rows / tiles : kGnClusterMax;
+    if (stats > n.stats) n.stats = stats;
     if (2 * ctas * channels > n.columns) n.columns = 2 * ctas * channels;
   }
   return n;

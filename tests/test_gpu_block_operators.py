@@ -176,3 +176,75 @@ def test_captured_calls_give_the_bits_of_plain_ones():
             g.replay()
             torch.cuda.synchronize()
             assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+# the kernels that a group norm's sizes choose among: lanes, a CTA's part, a cluster, parts of samples
+@pytest.mark.parametrize("shape,groups", [((900, 1, 256), 8), ((40, 6, 96), 4), ((6, 700, 320), 32), ((2, 60_000, 64), 4), ((9, 9000, 512), 8)])
+def test_a_captured_group_norm_gives_the_bits_of_plain_calls(shape, groups):
+    n, length, c = shape
+    x, dy = torch.empty(shape, device="cuda", dtype=torch.bfloat16), torch.empty(shape, device="cuda", dtype=torch.bfloat16)
+    w, b = torch.rand(c, device="cuda"), torch.rand(c, device="cuda")
+    norm = FusedGroupNorm(c, groups, n, activation="silu")
+    out = [torch.empty_like(x), torch.empty(n, groups, device="cuda"), torch.empty(n, groups, device="cuda"), torch.empty_like(x),
+           torch.empty_like(w), torch.empty_like(w)]
+
+    def run():
+        norm.forward(x, w, b, y=out[0], mean=out[1], rstd=out[2])
+        norm.backward(dy, x, w, b, out[1], out[2], dx=out[3], dweight=out[4], dbias=out[5])
+
+    x.normal_(), dy.normal_()
+    run()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        for _ in range(3):
+            run()
+    for _ in range(3):
+        x.normal_(), dy.normal_()
+        run()
+        want = [t.clone() for t in out]
+        for t in out:
+            t.fill_(-1.0)
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, c) for a, c in zip(want, out))
+    assert norm.status() == 0
+
+
+def test_two_plans_at_once_do_not_disturb_one_another():
+    """Samples in parts wait for one another; on two streams each plan's have words of their own."""
+    x = [torch.randn(3, 30_000, 96, device="cuda") for _ in range(2)]
+    norms = [FusedGroupNorm(96, 4, 3) for _ in range(2)]
+    routers = [FusedRouter(5000, 64, 4) for _ in range(2)]
+    z = [torch.randn(5000, 64, device="cuda") for _ in range(2)]
+    want = [[*norms[i].forward(x[i]), *routers[i].route(z[i])] for i in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [None, None]
+    for _ in range(10):
+        for i, s in enumerate(streams):
+            got[i] = [*norms[i].forward(x[i], stream=s), *routers[i].route(z[i], stream=s)]
+    torch.cuda.synchronize()
+    for a, b in zip(want, got):
+        assert all(torch.equal(u, v) for u, v in zip(a, b))
+    assert norms[0].status() == norms[1].status() == 0
+
+
+def test_calls_after_a_plan_that_did_not_fit():
+    from adamw_optimizer_step_tensor_gb300 import AdamWError, _capi
+    for call in _cases():
+        want = [t.clone() for t in call()]
+        with pytest.raises(AdamWError) as e:
+            FusedGroupNorm(1 << 16, 1 << 16, 1 << 24)          # 8 TB of means
+        assert e.value.status == _capi.ENOMEM
+        assert all(torch.equal(a, b) for a, b in zip(want, call()))
+
+
+def test_routes_without_places():
+    from adamw_optimizer_step_tensor_gb300 import _capi
+    router, z = FusedRouter(3000, 64, 4), torch.randn(3000, 64, device="cuda")
+    w, ids, _, _ = router.route(z)
+    w2, ids2 = torch.zeros_like(w), torch.zeros_like(ids)
+    _capi.adamw_route(router.plan, _capi.F32, 3000, z.data_ptr(), 64, None, w2.data_ptr(), ids2.data_ptr(), None, None,
+                      torch.cuda.current_stream().cuda_stream)
+    assert torch.equal(w, w2) and torch.equal(ids, ids2)
