@@ -7,10 +7,11 @@
 // lane keeps its two best and looks for a third only when both are gone.  Where no bias takes
 // part the order of the scores is that of the logits, and no score is computed for it.
 //
-// Up to 512 experts, and 32 chosen, a token has a team of 8, 16 or 32 lanes and a warp several
-// tokens (route_teams_kernel; groups of whole lanes): 5 and 2.5 times fewer instructions a token
-// than with a warp for each (128 and 256 experts), and it is instructions that bound it.  Else a
-// warp takes a token (route_kernel).
+// Up to 256 experts, and up to 512 without groups, a token has a team of 8, 16 or 32 lanes and a
+// warp several tokens (route_teams_kernel; groups of whole lanes): 5 and 2.5 times fewer
+// instructions a token than with a warp for each (128 and 256 experts), and it is instructions
+// that bound it.  Where 32 lanes of 16 experts do not hold the groups, or the experts, a warp
+// takes a token (route_kernel).
 //
 // Keys are off by a few units of the scores' last bits and by the bits that the number takes
 // (none that 16-bit logits have).  A choice in which two keys that matter lie closer than that
@@ -26,9 +27,9 @@ namespace {
 constexpr int kBackWarps = 8;
 constexpr int kPlaceThreads = 1024;
 
-// Warps of the routing kernel's CTA: with many experts in registers fewer fit.
-template <int V>
-__host__ __device__ constexpr int route_warps() { return V <= 8 ? 32 : 16; }
+// Experts of a lane where a warp takes a token, and the warps of its CTA.
+constexpr int kWarpExperts = 32;
+constexpr int kRouteWarps = 16;
 
 // Floats as integers of the same order.  Up to kNone they stand for -inf, "not there"; 0
 // is a key that has been taken.
@@ -193,49 +194,13 @@ __device__ __noinline__ int choose_exactly(const T* row, const float* bias, bool
   return id;
 }
 
-// The two largest keys of each group of 32 experts, a place of every lane: halves of the
-// groups are exchanged between halves of the lanes until a lane has one group, whose 32 / V
-// lanes then join theirs.  Lane l gets those of group l V / 32.
-template <int V>
-__device__ __forceinline__ float2 group_tops(const float (&k)[V]) {
-  const int lane = threadIdx.x & 31;
-  float one[V], next[V];
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    one[i] = k[i];
-    next[i] = -INFINITY;
-  }
-  int o = 16;
-#pragma unroll
-  for (int half = V / 2; half > 0; half /= 2, o /= 2) {
-    const bool upper = (lane & o) != 0;
-#pragma unroll
-    for (int i = 0; i < half; ++i) {
-      const float give1 = upper ? one[i] : one[i + half], keep1 = upper ? one[i + half] : one[i];
-      const float got1 = __shfl_xor_sync(kFull, give1, o);
-      float got2 = -INFINITY, keep2 = -INFINITY;
-      if (half < V / 2) {                 // the first exchange has no second ones
-        keep2 = upper ? next[i + half] : next[i];
-        got2 = __shfl_xor_sync(kFull, upper ? next[i] : next[i + half], o);
-      }
-      one[i] = fmaxf(keep1, got1);
-      next[i] = fmaxf(fminf(keep1, got1), fmaxf(keep2, got2));
-    }
-  }
-  for (; o > 0; o /= 2) {
-    const float got1 = __shfl_xor_sync(kFull, one[0], o), got2 = __shfl_xor_sync(kFull, next[0], o);
-    next[0] = fmaxf(fminf(one[0], got1), fmaxf(next[0], got2));
-    one[0] = fmaxf(one[0], got1);
-  }
-  return make_float2(one[0], next[0]);
-}
-
 // Chooses from the lanes' logits (NaN as -inf).  bias: null, or shared memory with its largest
 // magnitude.  Lane j gets the j-th expert (-1: none).  `own`: shared memory of this warp.
-template <typename T, int V>
-__device__ __forceinline__ int choose(const T* row, float (&k)[V], const float* bias, float bias_max, bool bad, float top,
+template <typename T>
+__device__ __forceinline__ int choose(const T* row, float (&k)[kWarpExperts], const float* bias, float bias_max, bool bad, float top,
                                       float total, double* own, const RouteArgs& a) {
-  constexpr uint32_t kPlace = V - 1;       // V is a power of two
+  constexpr int V = kWarpExperts;
+  constexpr uint32_t kPlace = V - 1;
   const adamw_router& r = a.router;
   const int lane = threadIdx.x & 31, per = a.per_group;
   const bool softmax = r.score == ADAMW_SCORE_SOFTMAX;
@@ -251,7 +216,7 @@ __device__ __forceinline__ int choose(const T* row, float (&k)[V], const float* 
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int e = 32 * i + lane;
-      const float b = V > 1 || e < r.experts ? bias[min(e, r.experts - 1)] : -INFINITY;
+      const float b = bias[min(e, r.experts - 1)];
       const float s = bad ? k[i] : (softmax ? key_exp(k[i] - top) * inv : key_sigmoid(k[i])) + b;
       k[i] = k[i] > -INFINITY && b > -INFINITY ? s : -INFINITY;
     }
@@ -266,33 +231,26 @@ __device__ __forceinline__ int choose(const T* row, float (&k)[V], const float* 
       v[i] = k[i];
       if (two && by_logit) v[i] = k[i] > -INFINITY ? (softmax ? key_exp(k[i] - top) * inv : key_sigmoid(k[i])) : -INFINITY;
     }
-    const bool by_place = per == 32 && r.groups == V && V <= 8;
-    int group = lane;                      // that this lane scores
-    if (by_place) {
-      tops = group_tops<V>(v);
-      group = lane / (32 / (V <= 8 ? V : 1));
-    } else {
-      float* s = reinterpret_cast<float*>(own);
-      __syncwarp();
+    float* lines = reinterpret_cast<float*>(own);
+    __syncwarp();
 #pragma unroll
-      for (int i = 0; i < V; ++i)
-        if (32 * i + lane < r.experts) s[32 * i + lane] = v[i];
-      __syncwarp();
-      const int share = 32 / choice_lanes(r.groups);       // lanes of a group
-      group = lane / share;
-      if (group < r.groups)
-        for (int i = lane - group * share; i < per; i += share) {
-          const float x = s[group * per + i];
-          tops.y = fmaxf(tops.y, fminf(tops.x, x));
-          tops.x = fmaxf(tops.x, x);
-        }
-      for (int o = 1; o < share; o *= 2) {
-        const float x = __shfl_xor_sync(kFull, tops.x, o), y = __shfl_xor_sync(kFull, tops.y, o);
-        tops.y = fmaxf(fminf(tops.x, x), fmaxf(tops.y, y));
+    for (int i = 0; i < V; ++i)
+      if (32 * i + lane < r.experts) lines[32 * i + lane] = v[i];
+    __syncwarp();
+    const int share = 32 / choice_lanes(r.groups);         // lanes of a group
+    const int group = lane / share;                        // that this lane scores
+    if (group < r.groups)
+      for (int i = lane - group * share; i < per; i += share) {
+        const float x = lines[group * per + i];
+        tops.y = fmaxf(tops.y, fminf(tops.x, x));
         tops.x = fmaxf(tops.x, x);
       }
-      __syncwarp();
+    for (int o = 1; o < share; o *= 2) {
+      const float x = __shfl_xor_sync(kFull, tops.x, o), y = __shfl_xor_sync(kFull, tops.y, o);
+      tops.y = fmaxf(fminf(tops.x, x), fmaxf(tops.y, y));
+      tops.x = fmaxf(tops.x, x);
     }
+    __syncwarp();
     const float of = two && tops.y > -INFINITY ? tops.x + tops.y : tops.x;
     uint32_t mine = group < r.groups ? ordered(of) : 0u, least = 0;
     kept = 0;
@@ -307,21 +265,15 @@ __device__ __forceinline__ int choose(const T* row, float (&k)[V], const float* 
     const uint32_t most = __reduce_max_sync(kFull, mine);
     // without scores equal groups went to the lowest already
     sure = sure && ((!two && by_logit) || most <= kNone || unordered(least) - unordered(most) > 4.0f * off);
-    if (by_place) {
 #pragma unroll
-      for (int i = 0; i < V; ++i)
-        if ((kept >> i & 1u) == 0) k[i] = -INFINITY;
-    } else {
-#pragma unroll
-      for (int i = 0; i < V; ++i)
-        if ((kept >> ((32 * i + lane) * a.group_factor >> 20) & 1u) == 0) k[i] = -INFINITY;
-    }
+    for (int i = 0; i < V; ++i)
+      if ((kept >> ((32 * i + lane) * a.group_factor >> 20) & 1u) == 0) k[i] = -INFINITY;
   }
   uint32_t key[V], best = 0, second = 0;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     key[i] = (ordered(k[i]) & ~kPlace) | (kPlace - i);
-    if (V > 1) second = max(second, min(best, key[i]));
+    second = max(second, min(best, key[i]));
     best = max(best, key[i]);
   }
   uint32_t mine = 0;
@@ -338,7 +290,7 @@ __device__ __forceinline__ int choose(const T* row, float (&k)[V], const float* 
       best = second;
       second = 0;
     }
-    if (V > 2 && __any_sync(kFull, best == 0)) {
+    if (__any_sync(kFull, best == 0)) {
       if (best == 0) {
 #pragma unroll
         for (int i = 0; i < V; ++i) best = max(best, key[i] < most ? key[i] : 0u);
@@ -348,7 +300,7 @@ __device__ __forceinline__ int choose(const T* row, float (&k)[V], const float* 
   }
   int id = mine > kNone ? 32 * static_cast<int>(kPlace - (mine & kPlace)) + lane_of : -1;
   // each chosen key is far enough above the one that comes after it
-  if (!by_logit || (sizeof(T) == 4 && V > 1)) {
+  if (!by_logit || sizeof(T) == 4) {
     const uint32_t rest = __reduce_max_sync(kFull, best);
     uint32_t after = __shfl_down_sync(kFull, mine, 1);
     if (lane == 31 || after == 0) after = rest;
@@ -448,9 +400,8 @@ __host__ __device__ __forceinline__ int place_warps(int experts, int most) {
 __host__ __device__ __forceinline__ int even(int n) { return (n + 1) & ~1; }
 // Shared memory of the routing kernel: per warp a row of 64-bit keys (the places of a lone
 // chunk use them again), the bias, this chunk's counts and its places' starts.
-template <int V>
-__host__ __device__ __forceinline__ size_t route_smem(int experts) {
-  return static_cast<size_t>(route_warps<V>()) * even(experts) * sizeof(double) + sizeof(float) * 3 * even(experts);
+size_t route_smem(int experts) {
+  return static_cast<size_t>(kRouteWarps) * even(experts) * sizeof(double) + sizeof(float) * 3 * even(experts);
 }
 
 // Lane l's V logits, -inf behind the last expert.
@@ -464,9 +415,9 @@ __device__ __forceinline__ void load_row(const T* row, int experts, T (&z)[V]) {
   }
 }
 
-template <typename T, int V>
-__global__ void __launch_bounds__(32 * route_warps<V>(), 1) route_kernel(const RouteArgs a) {
-  constexpr int kWarps = route_warps<V>(), kThreads = 32 * kWarps;
+template <typename T>
+__global__ void __launch_bounds__(32 * kRouteWarps, 1) route_kernel(const RouteArgs a) {
+  constexpr int V = kWarpExperts, kWarps = kRouteWarps, kThreads = 32 * kWarps;
   extern __shared__ double s_all[];
   const int experts = a.router.experts, even_experts = even(experts);
   float* s_bias = reinterpret_cast<float*>(s_all + kWarps * even_experts);
@@ -521,7 +472,7 @@ __global__ void __launch_bounds__(32 * route_warps<V>(), 1) route_kernel(const R
       for (int i = 0; i < V; ++i) sum += z[i] > -INFINITY ? key_exp(z[i] - top) : 0.0f;
       total = warp_sum(sum);
     }
-    const int id = choose<T, V>(row, z, bias, bias_max, bad, top, total, s_all + warp * even_experts, a);
+    const int id = choose<T>(row, z, bias, bias_max, bad, top, total, s_all + warp * even_experts, a);
     const float zj = id >= 0 ? to_f32(row[id]) : 0.0f;
     float w = a.router.scale * weight_of<0>(zj, id >= 0, a.router, top, total, wide);
     if (bad) w = __int_as_float(0x7FFFFFFF);
@@ -1052,11 +1003,6 @@ __global__ void balance_kernel(const int32_t* starts, int32_t experts, float rat
 
 // ---------------------------------------------------------------- launches
 
-template <typename T, int V>
-cudaError_t route_width(const RouteArgs& a, cudaStream_t s) {
-  route_kernel<T, V><<<a.chunks, 32 * route_warps<V>(), route_smem<V>(a.router.experts), s>>>(a);
-  return cudaGetLastError();
-}
 template <typename T, int LANES, int V>
 cudaError_t route_teams(const RouteArgs& a, cudaStream_t s) {
   constexpr int kGrid = V * sizeof(T) < 16 ? V * sizeof(T) : 16;
@@ -1066,7 +1012,7 @@ cudaError_t route_teams(const RouteArgs& a, cudaStream_t s) {
   return cudaGetLastError();
 }
 // Lanes of a token's team, experts of a lane and lanes of a group: the fewest lanes that hold
-// them.  0 lanes where a warp takes the token: more experts than 32 lanes of 16 hold.
+// them.  0 lanes where none do and a warp takes the token.
 struct Team {
   int lanes, experts, group_lanes;
 };
@@ -1113,15 +1059,8 @@ cudaError_t route_type(const RouteArgs& a, Team team, cudaStream_t s) {
 #define ADAMW_ROUTE_CALL(LANES, V) route_teams<T, LANES, V>(a, s)
   if (team.lanes > 0) return ADAMW_ROUTE_TEAM(team, ADAMW_ROUTE_CALL);
 #undef ADAMW_ROUTE_CALL
-#define ADAMW_ROUTE_CALL(V) route_width<T, V>(a, s)
-  return ADAMW_ROUTE_WIDTH(a.router.experts, ADAMW_ROUTE_CALL);
-#undef ADAMW_ROUTE_CALL
-}
-template <typename T>
-int chunk_warps(const RouteArgs& a) {
-#define ADAMW_ROUTE_CALL(V) route_warps<V>()
-  return ADAMW_ROUTE_WIDTH(a.router.experts, ADAMW_ROUTE_CALL);
-#undef ADAMW_ROUTE_CALL
+  route_kernel<T><<<a.chunks, 32 * kRouteWarps, route_smem(a.router.experts), s>>>(a);
+  return cudaGetLastError();
 }
 template <typename T>
 cudaError_t back_type(const RouteArgs& a, int sms, cudaStream_t s) {
@@ -1129,25 +1068,19 @@ cudaError_t back_type(const RouteArgs& a, int sms, cudaStream_t s) {
   return ADAMW_ROUTE_WIDTH(a.router.experts, ADAMW_ROUTE_CALL);
 #undef ADAMW_ROUTE_CALL
 }
-template <typename T, int V>
-cudaError_t prepare_width() {
-  // what the most experts of this width take: one plan's must not shrink another's
-  return cudaFuncSetAttribute(route_kernel<T, V>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              static_cast<int>(route_smem<V>(32 * V)));
-}
 template <typename T, int LANES, int V>
 cudaError_t prepare_team() {
   return cudaFuncSetAttribute(route_teams_kernel<T, LANES, V>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               static_cast<int>(team_smem<LANES>(LANES * V)));
 }
+// What the most experts of a kernel take: one plan's must not shrink another's.
 template <typename T>
-cudaError_t prepare_type(int experts, Team team) {
+cudaError_t prepare_type(Team team) {
 #define ADAMW_ROUTE_CALL(LANES, V) prepare_team<T, LANES, V>()
   if (team.lanes > 0) return ADAMW_ROUTE_TEAM(team, ADAMW_ROUTE_CALL);
 #undef ADAMW_ROUTE_CALL
-#define ADAMW_ROUTE_CALL(V) prepare_width<T, V>()
-  return ADAMW_ROUTE_WIDTH(experts, ADAMW_ROUTE_CALL);
-#undef ADAMW_ROUTE_CALL
+  return cudaFuncSetAttribute(route_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              static_cast<int>(route_smem(32 * kWarpExperts)));
 }
 size_t place_smem(int experts) {
   return sizeof(int) * (2 * router_pitch(experts) + experts * place_warps(experts, 32));
@@ -1160,9 +1093,9 @@ int router_pitch(int experts) { return (experts + 3) & ~3; }
 
 cudaError_t prepare_router(const adamw_router& r) {
   const Team team = team_for(r);
-  cudaError_t e = prepare_type<float>(r.experts, team);
-  if (e == cudaSuccess) e = prepare_type<__half>(r.experts, team);
-  if (e == cudaSuccess) e = prepare_type<__nv_bfloat16>(r.experts, team);
+  cudaError_t e = prepare_type<float>(team);
+  if (e == cudaSuccess) e = prepare_type<__half>(team);
+  if (e == cudaSuccess) e = prepare_type<__nv_bfloat16>(team);
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 80 << 10);
   return e;
@@ -1172,7 +1105,7 @@ cudaError_t launch_route(adamw_dtype dt, RouteArgs a, int sms, cudaStream_t s) {
   // one CTA for what it takes in two turns, up to 64 tokens, which spares the second kernel;
   // else a share of every SM's, a third of a turn at least
   const Team team = team_for(a.router);
-  const int turn = team.lanes > 0 ? kTeamWarps * (32 / team.lanes) : chunk_warps<float>(a);
+  const int turn = team.lanes > 0 ? kTeamWarps * (32 / team.lanes) : kRouteWarps;
   const int64_t most = router_chunks(sms);
   int64_t chunks = a.tokens <= 2 * turn && a.tokens <= 64 ? 1 : (a.tokens + turn / 3 - 1) / (turn / 3);
   if (chunks > most) chunks = most;

@@ -38,7 +38,7 @@ def rows_of(a, dtype, pad=0, shift=0):
 
 
 def check(z, bias, k, score="softmax", groups=1, top=1, group_score="max", renorm=True, scale=1.0, dtype=torch.float32,
-          pad=0, shift=0, seed=3, exact_slots=True):
+          pad=0, shift=0, seed=3):
     tokens, experts = z.shape
     logits = rows_of(z, dtype, pad, shift)
     zz = wide(logits)
@@ -88,7 +88,7 @@ def test_without_a_bias(tokens, experts, k, dtype):
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("group_score", ["max", "top2"])
 @pytest.mark.parametrize("experts,groups,top,k", [(64, 8, 3, 6), (256, 8, 4, 8), (96, 32, 5, 9), (40, 4, 4, 8), (60, 5, 2, 7),
-                                                 (12, 12, 3, 3), (1024, 16, 2, 32)])
+                                                 (12, 12, 3, 3), (1024, 16, 2, 32), (480, 20, 4, 8), (289, 17, 8, 3)])
 def test_groups_and_biases(experts, groups, top, k, group_score, score):
     rng = np.random.default_rng(experts + groups)
     z = rng.normal(0, 1.5, (60, experts))
