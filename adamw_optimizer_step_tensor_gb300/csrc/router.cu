@@ -329,13 +329,29 @@ __device__ __forceinline__ void place_chunk(const RouteArgs& a, int first, int t
   const int run = (n + warps - 1) / warps;
   const int lo = warp < warps ? min(n, warp * run) : n, hi = min(n, lo + run);
   const int64_t base = static_cast<int64_t>(first) * a.router.top_k;
+  constexpr int kIds = 4;                  // of a lane on their way at once
+  int* mine = of_warp + warp * experts;
+  const auto load = [&](int i0, int (&id)[kIds]) {
+#pragma unroll
+    for (int u = 0; u < kIds; ++u) {
+      const int i = i0 + 32 * u + lane;
+      id[u] = i < hi ? __ldcg(a.ids + base + i) : -1;
+    }
+  };
+  const auto count = [&](const int (&id)[kIds]) {
+#pragma unroll
+    for (int u = 0; u < kIds; ++u)
+      if (id[u] >= 0) atomicAdd(&mine[id[u]], 1);
+  };
+  int id[kIds];
+  load(lo, id);
   for (int i = threadIdx.x; i < warps * experts; i += blockDim.x) of_warp[i] = 0;
   __syncthreads();
-  int id = lo + lane < hi ? __ldcg(a.ids + base + lo + lane) : -1;
-  if (id >= 0) atomicAdd(&of_warp[warp * experts + id], 1);
-  for (int i = lo + 32 + lane; i < hi; i += 32) {
-    const int e = __ldcg(a.ids + base + i);
-    if (e >= 0) atomicAdd(&of_warp[warp * experts + e], 1);
+  count(id);
+  for (int i0 = lo + 32 * kIds; i0 < hi; i0 += 32 * kIds) {
+    int more[kIds];
+    load(i0, more);
+    count(more);
   }
   // exclusive sum of all chunks' counts over the experts, 1024 of them at most
   const int e = threadIdx.x;
@@ -376,16 +392,20 @@ __device__ __forceinline__ void place_chunk(const RouteArgs& a, int first, int t
     }
   }
   __syncthreads();
-  for (int i0 = lo; i0 < hi; i0 += 32) {
-    const int i = i0 + lane;
-    if (i0 > lo) id = i < hi ? __ldcg(a.ids + base + i) : -1;
-    const uint32_t same = __match_any_sync(kFull, id);
-    int slot = -1;
-    if (id >= 0) slot = of_warp[warp * experts + id] + __popc(same & ((1u << lane) - 1u));
-    __syncwarp();
-    if (id >= 0 && (same >> lane) == 1u) of_warp[warp * experts + id] += __popc(same);
-    __syncwarp();
-    if (i < hi) a.slots[base + i] = slot;
+  for (int i0 = lo; i0 < hi; i0 += 32 * kIds) {
+    if (i0 > lo) load(i0, id);
+#pragma unroll
+    for (int u = 0; u < kIds; ++u) {
+      const int i = i0 + 32 * u + lane;
+      if (i0 + 32 * u >= hi) break;
+      const uint32_t same = __match_any_sync(kFull, id[u]);
+      int slot = -1;
+      if (id[u] >= 0) slot = mine[id[u]] + __popc(same & ((1u << lane) - 1u));
+      __syncwarp();
+      if (id[u] >= 0 && (same >> lane) == 1u) mine[id[u]] += __popc(same);
+      __syncwarp();
+      if (i < hi) a.slots[base + i] = slot;
+    }
   }
 }
 
@@ -497,7 +517,9 @@ __global__ void __launch_bounds__(32 * kRouteWarps, 1) route_kernel(const RouteA
 
 // ---------------------------------------------------------------- teams
 
-constexpr int kTeamWarps = 24;
+// Warps of a CTA, at most: 8192 x 256 float32 in 8 groups 26 us, with 24 (80 registers a thread
+// for 72) 28.5.  A CTA of fewer tokens than they hold has fewer.
+constexpr int kTeamWarps = 28;
 constexpr uint32_t kNumber = 511;        // experts are numbered in a key's lowest bits
 constexpr float kFirstUnit = 16400.0f;   // of the scores' scale: its keys lie above kNone
 
@@ -582,18 +604,18 @@ __device__ __noinline__ double exact_sum(const T* row, int e0, int end, int many
   return t;
 }
 
-template <int LANES>
-__host__ __device__ __forceinline__ size_t team_smem(int experts) {
-  return static_cast<size_t>(kTeamWarps) * even(experts) * sizeof(double) + sizeof(float) * (3 * even(experts) + 32);
+size_t team_smem(int experts, int warps) {
+  return static_cast<size_t>(warps) * even(experts) * sizeof(double) + sizeof(float) * (3 * even(experts) + 32);
 }
 
 template <typename T, int LANES, int V>
 __global__ void __launch_bounds__(32 * kTeamWarps, 1) route_teams_kernel(const RouteArgs a, const bool vec) {
-  constexpr int kThreads = 32 * kTeamWarps, kTokens = 32 / LANES;
+  constexpr int kTokens = 32 / LANES;
+  const int warps = blockDim.x / 32;
   extern __shared__ double s_all[];
   const adamw_router& r = a.router;
   const int experts = r.experts, even_experts = even(experts);
-  float* s_bias = reinterpret_cast<float*>(s_all + kTeamWarps * even_experts);     // V at a time may pass the last one
+  float* s_bias = reinterpret_cast<float*>(s_all + warps * even_experts);     // V at a time may pass the last one
   int* s_counts = reinterpret_cast<int*>(s_bias + even_experts + 32);
   int* s_before = s_counts + even_experts;
   __shared__ int s_scan[32];
@@ -612,7 +634,7 @@ __global__ void __launch_bounds__(32 * kTeamWarps, 1) route_teams_kernel(const R
   if (threadIdx.x == 0) s_bias_max = 0;
   __syncthreads();
   bool any = false;
-  for (int e = threadIdx.x; e < experts; e += kThreads) {
+  for (int e = threadIdx.x; e < experts; e += 32 * warps) {
     s_counts[e] = 0;
     if (a.bias != nullptr) {
       const float b = __ldg(a.bias + e);
@@ -628,7 +650,7 @@ __global__ void __launch_bounds__(32 * kTeamWarps, 1) route_teams_kernel(const R
   const bool two = by_group && r.group_score == ADAMW_GROUP_TOP2;
   const bool scored = bias != nullptr || two;           // keys are scores, not logits
   const bool sums = softmax && (scored || !r.renormalise);
-  for (int t0 = warp * kTokens; t0 < tokens; t0 += kTeamWarps * kTokens) {
+  for (int t0 = warp * kTokens; t0 < tokens; t0 += warps * kTokens) {
     const int t = t0 + sub;
     const bool live = t < tokens;
     const T* row = rows + static_cast<int64_t>(live ? t : t0) * a.stride;
@@ -642,7 +664,7 @@ __global__ void __launch_bounds__(32 * kTeamWarps, 1) route_teams_kernel(const R
       z[i] = fmaxf(f, -INFINITY);                                 // a NaN is not there
       top = fmaxf(top, z[i]);
     }
-    if (t + kTeamWarps * kTokens < tokens) next.load(row + static_cast<int64_t>(kTeamWarps * kTokens) * a.stride, e0, end, vec);
+    if (t + warps * kTokens < tokens) next.load(row + static_cast<int64_t>(warps * kTokens) * a.stride, e0, end, vec);
     constexpr uint32_t kTeam = kFull >> (32 - LANES);
     const bool bad = (__ballot_sync(kFull, nan || (softmax && top == INFINITY)) >> (sub * LANES) & kTeam) != 0;
     if (sums) {
@@ -836,10 +858,10 @@ __global__ void __launch_bounds__(32 * kTeamWarps, 1) route_teams_kernel(const R
   if (a.starts == nullptr) return;
   __syncthreads();
   if (gridDim.x == 1) {
-    for (int e = threadIdx.x; e < experts; e += kThreads) s_before[e] = 0;
-    place_chunk(a, first, tokens, s_before, s_counts, reinterpret_cast<int*>(s_all), place_warps(experts, kTeamWarps), s_scan, true);
+    for (int e = threadIdx.x; e < experts; e += 32 * warps) s_before[e] = 0;
+    place_chunk(a, first, tokens, s_before, s_counts, reinterpret_cast<int*>(s_all), place_warps(experts, warps), s_scan, true);
   } else {
-    for (int e = threadIdx.x; e < experts; e += kThreads)
+    for (int e = threadIdx.x; e < experts; e += 32 * warps)
       a.counts[static_cast<int64_t>(blockIdx.x) * a.pitch + e] = s_counts[e];
     let_next_kernel_start();
   }
@@ -1008,7 +1030,8 @@ cudaError_t route_teams(const RouteArgs& a, cudaStream_t s) {
   constexpr int kGrid = V * sizeof(T) < 16 ? V * sizeof(T) : 16;
   const bool vec = a.router.experts == LANES * V && (a.router.groups == 1 || a.per_group % V == 0) && reinterpret_cast<uintptr_t>(a.logits) % kGrid == 0 &&
                    a.stride * sizeof(T) % kGrid == 0;
-  route_teams_kernel<T, LANES, V><<<a.chunks, 32 * kTeamWarps, team_smem<LANES>(a.router.experts), s>>>(a, vec);
+  const int need = (a.per_chunk + 32 / LANES - 1) / (32 / LANES), warps = need < 4 ? 4 : need < kTeamWarps ? need : kTeamWarps;
+  route_teams_kernel<T, LANES, V><<<a.chunks, 32 * warps, team_smem(a.router.experts, warps), s>>>(a, vec);
   return cudaGetLastError();
 }
 // Lanes of a token's team, experts of a lane and lanes of a group: the fewest lanes that hold
@@ -1071,7 +1094,7 @@ cudaError_t back_type(const RouteArgs& a, int sms, cudaStream_t s) {
 template <typename T, int LANES, int V>
 cudaError_t prepare_team() {
   return cudaFuncSetAttribute(route_teams_kernel<T, LANES, V>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              static_cast<int>(team_smem<LANES>(LANES * V)));
+                              static_cast<int>(team_smem(LANES * V, kTeamWarps)));
 }
 // What the most experts of a kernel take: one plan's must not shrink another's.
 template <typename T>
