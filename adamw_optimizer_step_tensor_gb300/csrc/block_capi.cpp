@@ -347,6 +347,7 @@ adamw_status adamw_route_dispatch(adamw_router_plan* plan, adamw_dtype dtype, in
       (st = matrix("x", x, tokens, width, x_stride, dtype)) != ADAMW_OK ||
       (st = matrix("xs", xs, tokens > 0 ? xs_rows : 0, width, xs_stride, dtype)) != ADAMW_OK)
     return st;
+  if (xs == x && tokens > 0 && xs_rows > 0) return fail(ADAMW_EINVAL, "xs may not be x");
   if ((st = check_current_device(plan->device, "plan")) != ADAMW_OK || tokens == 0 || xs_rows == 0)
     return st;
   ExpertRowsArgs a{};

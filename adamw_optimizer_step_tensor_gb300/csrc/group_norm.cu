@@ -2,17 +2,20 @@
 // are cut up, and the forward pass.
 //
 // Statistics of the fused kernel: a thread sums x - K and its square, K the first of its
-// own values, and starts anew every kRun rows.  K is one of the n values it is subtracted
+// own values, and starts anew after kRun values.  K is one of the n values it is subtracted
 // from, so the sum of squares is at most 2 n times the spread about their mean: the
-// difference loses log2(2 n) bits at worst, whatever the mean.  From there on means and
-// spreads are joined by counts: M2 = sum M2_i + n_i (mean_i - mean)^2.  The small kernel
-// has the values in registers and sums about their mean.
+// difference loses log2(2 n) bits at worst, whatever the mean.  From there on spreads are
+// joined by counts: M2 = sum M2_i + n_i (mean_i - mean)^2.  The mean itself comes from the
+// sum of the values as they are, a thread's runs added with their rounding errors: a mean
+// near 0 of large values keeps its bits, which the K would take.  The small kernel has the
+// values in registers and sums about their mean.
 #include "group_norm_cluster.cuh"
 
 namespace adamw {
 namespace {
 
-constexpr int kRun = 8;                 // rows of a run of sums: 64 values of 16 bits
+constexpr int kRun = 64;                // values of a run of sums
+constexpr int kGnTiles = 65535;         // of a grid's second axis
 constexpr int kSmallForward = 8;        // pieces a thread of the small kernel holds
 constexpr int kSmallCtasPerSm = 4;      // of the small kernels forward, on which their grid goes; backward 3
 
@@ -159,12 +162,23 @@ __global__ void __launch_bounds__(kGnThreads, kSmallCtasPerSm) gn_forward_lanes_
 }
 
 // Joins (count, mean, spread) u to t.
+__device__ __forceinline__ float3 gn_merge_means(float3 t, float3 u) {
+  const float all = t.x + u.x, share = __fdividef(u.x, all), d = u.y - t.y;
+  if (t.x == 0.0f) return u;
+  return make_float3(all, fmaf(d, share, t.y), t.z + fmaf(d * d, t.x * share, u.z));
+}
+// Joins (count, sum, spread) u to t.
 __device__ __forceinline__ float3 gn_merge(float3 t, float3 u) {
-  const float all = t.x + u.x, share = u.x > 0.0f ? __fdividef(u.x, all) : 0.0f;
-  const float d = u.y - t.y;
   if (t.x == 0.0f) return u;
   if (u.x == 0.0f) return t;
-  return make_float3(all, fmaf(d, share, t.y), t.z + fmaf(d * d, t.x * share, u.z));
+  const float all = t.x + u.x, d = __fdividef(u.y, u.x) - __fdividef(t.y, t.x);
+  return make_float3(all, t.y + u.y, t.z + fmaf(d * d, __fdividef(t.x * u.x, all), u.z));
+}
+// hi + lo += x, without the rounding error of hi.
+__device__ __forceinline__ void add_exactly(float x, float* hi, float* lo) {
+  const float s = *hi + x, of_x = s - *hi;
+  *lo += (*hi - (s - of_x)) + (x - of_x);
+  *hi = s;
 }
 __device__ __forceinline__ float3 gn_from(float3 t, int lanes) {
   return make_float3(__shfl_xor_sync(kFull, t.x, lanes), __shfl_xor_sync(kFull, t.y, lanes), __shfl_xor_sync(kFull, t.z, lanes));
@@ -176,7 +190,7 @@ __device__ __noinline__ void gn_join(const GroupNormArgs& a, const GnCut& c, con
                                         int groups, int piece) {
   const GnLanes l(groups);
   const int pitch = gn_pitch(a, c);
-  const float inv = 1.0f / (static_cast<float>(a.positions) * static_cast<float>(c.per));
+  const float all = static_cast<float>(a.positions) * static_cast<float>(c.per), inv = 1.0f / all;
   for (int g0 = 0; g0 < groups; g0 += l.wide) {
     const int g = first + g0 + l.slot, p0 = g * c.group_pieces, p1 = p0 + c.group_pieces;
     float3 t = make_float3(0.0f, 0.0f, 0.0f);
@@ -201,7 +215,7 @@ __device__ __noinline__ void gn_join(const GroupNormArgs& a, const GnCut& c, con
     }
     for (int o = l.wide; o < 32; o *= 2) t = gn_merge(t, gn_from(t, o));
     if (l.at == 0 && g < first + groups) {
-      a.mean[sample * a.groups + g] = t.y;
+      a.mean[sample * a.groups + g] = __fdiv_rn(t.y, all);
       a.rstd[sample * a.groups + g] = __frcp_rn(__fsqrt_rn(fmaf(t.z, inv, a.eps)));
     }
   }
@@ -223,7 +237,7 @@ __global__ void __launch_bounds__(kGnThreads, 3) gn_forward_cluster_kernel(const
   gn_weights<T, N>(a.weight, a.weight_f32, 1.0f, at, w);
   gn_weights<T, N>(a.bias, a.weight_f32, 0.0f, at, b);
   const float mine = rows > 0 ? __fdividef(1.0f, static_cast<float>(rows) * static_cast<float>(c.per)) : 0.0f;
-  const float inv = 1.0f / (static_cast<float>(a.positions) * static_cast<float>(c.per));
+  const float all = static_cast<float>(a.positions) * static_cast<float>(c.per), inv = 1.0f / all;
   const int group = at.there ? at.group - at.first_group : 0;
   const char* tile = reinterpret_cast<const char*>(s_tile) + (threadIdx.x % c.wide) * P::kBytes;
   const int row_bytes = c.at_once * tile_bytes;
@@ -240,14 +254,17 @@ __global__ void __launch_bounds__(kGnThreads, 3) gn_forward_cluster_kernel(const
 #pragma unroll 4
       for (int l = at.row0; l < rows; l += c.at_once, p += row_bytes) {
         const P v = *reinterpret_cast<const P*>(p);
+        float2 of_row = v.pair(0);
 #pragma unroll
-        for (int j = 0; j < kPairs; ++j) t = add2(t, v.pair(j));
+        for (int j = 1; j < kPairs; ++j) of_row = add2(of_row, v.pair(j));
+        t = add2(t, of_row);
       }
     }
     gn_block_sums<N>(c, at, make_float2(t.x + t.y, 0.0f), s_sum, s_group);
-    // about this CTA's mean, which the differences' own sum puts right
+    // about this CTA's mean, whose rounding the differences' own sum takes back; the mean comes
+    // from the values' sum (the differences of 16-bit values are all rounded the same way)
     const float here = s_group[group].x * mine;
-    if (threadIdx.x < at.groups) s_here[threadIdx.x] = s_group[threadIdx.x].x * mine;
+    if (threadIdx.x < at.groups) s_here[threadIdx.x] = s_group[threadIdx.x].x;
     float2 off = both(0.0f);
     t = both(0.0f);
     if (at.there) {
@@ -269,7 +286,7 @@ __global__ void __launch_bounds__(kGnThreads, 3) gn_forward_cluster_kernel(const
     if (threadIdx.x < at.groups) {
       const float2 v = s_group[threadIdx.x];
       const float d = v.x * mine;
-      s_group[threadIdx.x] = make_float2(s_here[threadIdx.x] + d, fmaxf(fmaf(-d, v.x, v.y), 0.0f));
+      s_group[threadIdx.x] = make_float2(s_here[threadIdx.x], fmaxf(fmaf(-d, v.x, v.y), 0.0f));
     }
     __syncthreads();
     // two sets of slots: a CTA may be a sample ahead of one that still reads
@@ -281,7 +298,7 @@ __global__ void __launch_bounds__(kGnThreads, 3) gn_forward_cluster_kernel(const
       u = gn_merge(u, make_float3(static_cast<float>(n) * static_cast<float>(c.per), v.x, v.y));
     }
     turn ^= 1;
-    const float mean = u.y, rstd = __frcp_rn(__fsqrt_rn(fmaf(u.z, inv, a.eps)));
+    const float mean = __fdiv_rn(u.y, all), rstd = __frcp_rn(__fsqrt_rn(fmaf(u.z, inv, a.eps)));
     if (!at.there) continue;
     if (rank == 0 && at.row0 == 0 && at.piece % c.group_pieces == 0) {
       a.mean[sample * a.groups + at.group] = mean;
@@ -309,7 +326,7 @@ __global__ void __launch_bounds__(kGnFusedThreads, kGnCtasPerSm) gn_forward_fuse
   using P = GnPiece<T, N>;
   constexpr int kPairs = gn_pairs<N>();
   extern __shared__ uint4 s_ring[];
-  // means and spreads of the threads (or, by lanes, of rows of threads and groups)
+  // sums and spreads of the threads (or, by lanes, of rows of threads and groups)
   __shared__ float2 s_stat[2][kGnThreads];
   const GnPlace<N> at(c);
   const GnPart part(a, c);
@@ -367,28 +384,37 @@ __global__ void __launch_bounds__(kGnFusedThreads, kGnCtasPerSm) gn_forward_fuse
     if (sample >= a.samples) continue;
     if (!turn.result) {
       float3 t = make_float3(0.0f, 0.0f, 0.0f);
-      float shift = 0.0f;
-      float2 sum = both(0.0f), square = both(0.0f);
+      float shift = 0.0f, whole = 0.0f, rest = 0.0f;
+      float2 raw = both(0.0f), sum = both(0.0f), square = both(0.0f);
       int run = 0;
       for (int k = 0; k < part.steps; ++k) {
         P p[1];
         ring.get(p);
         if (k >= ring.rows) continue;
         if (run == 0) shift = p[0].pair(0).x;
+        if constexpr (N == 1) {
+          const float x = p[0].pair(0).x, d = x - shift;
+          raw.x += x;
+          sum.x += d;
+          square.x = fmaf(d, d, square.x);
+        } else {
 #pragma unroll
-        for (int j = 0; j < kPairs; ++j) {
-          float2 d = add2(p[0].pair(j), both(-shift));
-          if constexpr (N == 1) d.y = 0.0f;
-          sum = add2(sum, d);
-          square = fma2(d, d, square);
+          for (int j = 0; j < kPairs; ++j) {
+            const float2 d = add2(p[0].pair(j), both(-shift));
+            raw = add2(raw, p[0].pair(j));
+            sum = add2(sum, d);
+            square = fma2(d, d, square);
+          }
         }
-        if (++run == kRun || k == ring.rows - 1) {
+        if (++run == kRun / N || k == ring.rows - 1) {
           const float count = static_cast<float>(run * N), total = sum.x + sum.y, off = __fdividef(total, count);
-          t = gn_merge(t, make_float3(count, shift + off, fmaxf(fmaf(-off, total, square.x + square.y), 0.0f)));
+          t = gn_merge_means(t, make_float3(count, shift + off, fmaxf(fmaf(-off, total, square.x + square.y), 0.0f)));
+          add_exactly(raw.x + raw.y, &whole, &rest);
           run = 0;
-          sum = square = both(0.0f);
+          raw = sum = square = both(0.0f);
         }
       }
+      t.y = whole + rest;
       if (c.by_lanes)
         for (int o = 1; o < c.group_pieces; o *= 2) t = gn_merge(t, gn_from(t, o));
       float2* s = s_stat[turn.batch % 2];
@@ -519,7 +545,7 @@ bool cut_cluster(GnCut* c, const GroupNormArgs& a, int piece, int sms, double li
     if (wide > kGnThreads || m > kGnTileGroups) break;
     const int64_t tiles = up(groups, m), tile_bytes = static_cast<int64_t>(wide) * piece * a.size;
     const int at_once = kGnThreads / wide;
-    for (int cluster = 1; cluster <= kGnClusterMax; cluster *= 2) {
+    for (int cluster = 1; cluster <= kGnClusterMax && tiles <= kGnTiles; cluster *= 2) {
       const int64_t rows = up(a.positions, cluster), bytes = rows * tile_bytes * tensors;
       if (bytes > kGnClusterBytes || (cluster > 1 && rows * (cluster - 1) >= a.positions)) continue;
       int64_t per_sm = (224 << 10) / (bytes + (12 << 10));

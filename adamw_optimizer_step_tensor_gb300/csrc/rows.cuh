@@ -1,5 +1,5 @@
-// rows.cuh -- device pieces shared by the row kernels (token_loss.cu,
-// layer_norm.cu): element types and the fixed-order sum across a grid's CTAs.
+// rows.cuh -- device pieces shared by the row kernels (token losses, layer norm, a
+// block's operators): element types and the fixed-order sum across a grid's CTAs.
 #pragma once
 
 #include <cuda_bf16.h>

@@ -726,8 +726,9 @@ adamw_status adamw_route(adamw_router_plan* plan, adamw_dtype dtype, int64_t tok
 /*
  * dlogits = the gradient of the logits from that of the weights (float32
  * [tokens][top_k]), every entry of every row, rounded once to the logits' type; the choice
- * of experts and the bias have none.  ids as adamw_route wrote them (-1, and what lies
- * outside [0, experts), has no weight).  dlogits may be the logits (same stride).
+ * of experts and the bias have none.  ids as adamw_route wrote them: different ones in a
+ * row (of equal ones, one counts); -1, and what lies outside [0, experts), has no weight.
+ * dlogits may be the logits (same stride).
  */
 adamw_status adamw_route_backward(adamw_router_plan* plan, adamw_dtype dtype, int64_t tokens,
                                   const void* logits, int64_t row_stride, const int32_t* ids,
@@ -743,7 +744,8 @@ adamw_status adamw_route_balance(adamw_router_plan* plan, const int32_t* starts,
 
 /*
  * Rows to the experts: xs[slots[t][j]] = x[t].  A slot outside [0, xs_rows) is passed
- * over; rows of xs that no slot names are left as they were.  Row strides in elements.
+ * over; rows of xs that no slot names are left as they were, and of two slots that name one
+ * row (adamw_route writes none) either may win, piece by piece.  Row strides in elements.
  */
 adamw_status adamw_route_dispatch(adamw_router_plan* plan, adamw_dtype dtype, int64_t tokens,
                                   int64_t width, const void* x, int64_t x_stride,
@@ -763,7 +765,8 @@ adamw_status adamw_route_combine(adamw_router_plan* plan, adamw_dtype dtype, int
 /*
  * dys[slots[t][j]] = weights[t][j] * dy[t],  dweights[t][j] = <dy[t], ys[slots[t][j]]> (0
  * without a slot).  dys has ys_rows rows, and may be ys (same stride); rows that no slot
- * names are left as they were.
+ * names are left as they were.  Two slots that name one row leave either's values in dys, and
+ * with dys in place of ys any of them in dweights.
  */
 adamw_status adamw_route_combine_backward(adamw_router_plan* plan, adamw_dtype dtype,
                                           int64_t tokens, int64_t width, const void* dy,

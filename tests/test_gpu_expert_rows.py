@@ -115,6 +115,8 @@ def test_no_tokens_and_refusals():
     from adamw_optimizer_step_tensor_gb300 import AdamWError
     with pytest.raises(AdamWError, match="may not be ys"):
         router.combine(x, slots, y=x)
+    with pytest.raises(AdamWError, match="may not be x"):
+        router.dispatch(x, slots, xs=x)
     with pytest.raises(AdamWError, match="may not be dy"):
         router.combine_backward(x, x.clone(), slots, torch.ones(4, 2, device="cuda"), dys=x)
     with pytest.raises(AdamWError, match="5 tokens"):

@@ -239,3 +239,60 @@ def test_a_wait_that_gives_up_is_reported_and_the_plan_is_fit_again():
 @pytest.mark.parametrize("dtype", DTYPES)
 def test_cuts_of_every_kind(shape, groups, dtype):
     check(shape, groups, dtype, silu=True)
+
+
+def test_positions_at_the_limit():
+    """2^31 - 1 positions, elements past 2^31 and 2^32.  A thread merges its 2^31 / (304 256) / 8 =
+    3450 runs one after another, each merge off by 3 u of a run's mean, below 6 for normal numbers:
+    4e-3 at most of a mean, a spread and, relative to 1, of the means of the gradient."""
+    n, length = 2, 2 ** 31 - 1
+    x = torch.empty(n, length, 1, dtype=torch.bfloat16, device="cuda").normal_(generator=torch.Generator("cuda").manual_seed(5))
+    norm = FusedGroupNorm(1, 1, n)
+    y, mean, rstd = norm.forward(x)
+    step = 1 << 27
+    for s in range(n):
+        sums = torch.zeros(2, dtype=torch.float64, device="cuda")
+        for at in range(0, length, step):
+            part = x[s, at:at + step].double()
+            sums += torch.stack([part.sum(), (part * part).sum()])
+        m = sums[0] / length
+        r = 1 / torch.sqrt(sums[1] / length - m * m + 1e-5)
+        assert abs(mean[s, 0] - m) <= 4e-3 and abs(rstd[s, 0] - r) <= 4e-3 * r
+        for at in (0, 1 << 30, length - 4096):
+            want = (x[s, at:at + 4096].double() - m) * r
+            assert ((y[s, at:at + 4096].double() - want).abs() <= 2.0 ** -8 * want.abs() + 4e-3 * (1 + want.abs())).all()
+    # of dy = 1 nothing is left: one mean off by 4e-3, the other, with the forward pass's, by 8e-3 of xhat < 6.3
+    dx, _, _ = norm.backward(torch.ones((), dtype=torch.bfloat16, device="cuda").expand(n, length, 1).contiguous(), x, None, None, mean, rstd, dx=y)
+    assert dx[:, :: 1 << 20].abs().max() <= 6e-2 and dx[:, -4096:].abs().max() <= 6e-2
+    assert norm.status() == 0
+
+
+def test_strides_past_32_bits():
+    """Every position lies more than 2^31 elements behind the one before."""
+    n, length, c = 2, 3, 64
+    pace = 2 ** 31 + 64
+    room = torch.empty(n * length * pace, dtype=torch.bfloat16, device="cuda")
+    x = room.as_strided((n, length, c), (length * pace, pace, 1))
+    dense = torch.randn(n, length, c, device="cuda").to(torch.bfloat16)
+    dy = torch.randn(n, length, c, device="cuda").to(torch.bfloat16)
+    norm = FusedGroupNorm(c, 4, n, activation="silu")
+    want = norm.forward(dense)
+    want_dx = norm.backward(dy, dense, None, None, *want[1:])
+    x.copy_(dense)
+    assert all(torch.equal(a, b) for a, b in zip(want_dx, norm.backward(dy, x, None, None, *want[1:])))
+    got = norm.forward(x, y=x)
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("shape,groups", [((900, 1, 256), 8), ((40, 6, 96), 4), ((2, 33, 2280), 3), ((7, 39, 3584), 14), ((2, 40_000, 96), 4),
+                                          ((2, 314, 3662), 2), ((3, 1, 3364), 2)])
+def test_a_mean_near_zero_keeps_its_bits(shape, groups, dtype):
+    """Whole numbers of at most 8: every sum of them is exact, so a mean is off by the rounding of a
+    quotient, or of a reciprocal and a product: 2 u of itself, whatever the kernel."""
+    n, length, c = shape
+    x = np.random.default_rng(c).integers(-8, 9, shape).astype(np.float64)
+    _, mean, rstd = FusedGroupNorm(c, groups, n).forward(tensor_of(x, dtype))
+    want = x.reshape(n, length, groups, -1).mean((1, 3))
+    assert (np.abs(wide(mean) - want) <= 2.0 ** -23 * np.abs(want)).all()
+    assert (np.abs(wide(rstd) - GN.forward(x, groups)[2]) <= 2.0 ** -16).all()
