@@ -58,7 +58,7 @@ __global__ void __launch_bounds__(kGnThreads, K == 1 ? kSmallCtasPerSm : 2) gn_f
     for (int k = 0; k < K; ++k)
       if (live && row0 + k * c.team_rows < rows) {
 #pragma unroll
-        for (int i = 0; i < kPairs; ++i) sum = add2(sum, p[k].pair(i));
+        for (int i = 0; i < kPairs; ++i) sum = add_of<N>(sum, p[k].pair(i));
       }
     const float mean = gn_team_sums(make_float2(sum.x + sum.y, 0.0f), c, s_sum, s_group).x * inv;
     float2 square = both(0.0f);
@@ -67,9 +67,8 @@ __global__ void __launch_bounds__(kGnThreads, K == 1 ? kSmallCtasPerSm : 2) gn_f
       if (live && row0 + k * c.team_rows < rows) {
 #pragma unroll
         for (int i = 0; i < kPairs; ++i) {
-          float2 d = add2(p[k].pair(i), both(-mean));
-          if constexpr (N == 1) d.y = 0.0f;
-          square = fma2(d, d, square);
+          float2 d = add_of<N>(p[k].pair(i), both(-mean));
+          square = fma_of<N>(d, d, square);
         }
       }
     const float spread = gn_team_sums(make_float2(square.x + square.y, 0.0f), c, s_sum, s_group).x;
@@ -86,8 +85,8 @@ __global__ void __launch_bounds__(kGnThreads, K == 1 ? kSmallCtasPerSm : 2) gn_f
       if (l < rows) {
 #pragma unroll
         for (int i = 0; i < kPairs; ++i) {
-          const float2 xhat = mul2(add2(p[k].pair(i), both(-mean)), both(rstd));
-          p[k].set(i, activate<T, SILU>(fma2(xhat, w[i], b[i])));
+          const float2 xhat = mul_of<N>(add_of<N>(p[k].pair(i), both(-mean)), both(rstd));
+          p[k].set(i, activate<T, N, SILU>(fma_of<N>(xhat, w[i], b[i])));
         }
         p[k].store(y + l * a.out_position);
       }
@@ -123,7 +122,7 @@ __global__ void __launch_bounds__(kGnThreads, kSmallCtasPerSm) gn_forward_lanes_
     for (int u = 0; u < U; ++u) {
       float2 t = p[u].pair(0);
 #pragma unroll
-      for (int i = 1; i < kPairs; ++i) t = add2(t, p[u].pair(i));
+      for (int i = 1; i < kPairs; ++i) t = add_of<N>(t, p[u].pair(i));
       sum[u] = t.x + t.y;
     }
     for (int o = 1; o < c.group_pieces; o *= 2)
@@ -135,9 +134,8 @@ __global__ void __launch_bounds__(kGnThreads, kSmallCtasPerSm) gn_forward_lanes_
       float2 t = both(0.0f);
 #pragma unroll
       for (int i = 0; i < kPairs; ++i) {
-        float2 d = add2(p[u].pair(i), both(-sum[u]));
-        if constexpr (N == 1) d.y = 0.0f;
-        t = fma2(d, d, t);
+        float2 d = add_of<N>(p[u].pair(i), both(-sum[u]));
+        t = fma_of<N>(d, d, t);
       }
       square[u] = t.x + t.y;
     }
@@ -155,7 +153,7 @@ __global__ void __launch_bounds__(kGnThreads, kSmallCtasPerSm) gn_forward_lanes_
       }
 #pragma unroll
       for (int i = 0; i < kPairs; ++i)
-        p[u].set(i, activate<T, SILU>(fma2(mul2(add2(p[u].pair(i), both(-mean)), both(rstd)), w[i], b[i])));
+        p[u].set(i, activate<T, N, SILU>(fma_of<N>(mul_of<N>(add_of<N>(p[u].pair(i), both(-mean)), both(rstd)), w[i], b[i])));
       p[u].store(static_cast<T*>(a.out) + sample * a.out_sample + at.channel());
     }
   }
@@ -256,8 +254,8 @@ __global__ void __launch_bounds__(kGnThreads, 3) gn_forward_cluster_kernel(const
         const P v = *reinterpret_cast<const P*>(p);
         float2 of_row = v.pair(0);
 #pragma unroll
-        for (int j = 1; j < kPairs; ++j) of_row = add2(of_row, v.pair(j));
-        t = add2(t, of_row);
+        for (int j = 1; j < kPairs; ++j) of_row = add_of<N>(of_row, v.pair(j));
+        t = add_of<N>(t, of_row);
       }
     }
     gn_block_sums<N>(c, at, make_float2(t.x + t.y, 0.0f), s_sum, s_group);
@@ -274,10 +272,9 @@ __global__ void __launch_bounds__(kGnThreads, 3) gn_forward_cluster_kernel(const
         const P v = *reinterpret_cast<const P*>(p);
 #pragma unroll
         for (int j = 0; j < kPairs; ++j) {
-          float2 d = add2(v.pair(j), both(-here));
-          if constexpr (N == 1) d.y = 0.0f;
-          off = add2(off, d);
-          t = fma2(d, d, t);
+          float2 d = add_of<N>(v.pair(j), both(-here));
+          off = add_of<N>(off, d);
+          t = fma_of<N>(d, d, t);
         }
       }
     }
@@ -312,7 +309,7 @@ __global__ void __launch_bounds__(kGnThreads, 3) gn_forward_cluster_kernel(const
       P v = *reinterpret_cast<const P*>(p);
 #pragma unroll
       for (int j = 0; j < kPairs; ++j)
-        v.set(j, activate<T, SILU>(fma2(mul2(add2(v.pair(j), both(-mean)), both(rstd)), w[j], b[j])));
+        v.set(j, activate<T, N, SILU>(fma_of<N>(mul_of<N>(add_of<N>(v.pair(j), both(-mean)), both(rstd)), w[j], b[j])));
       v.store(y);
     }
   }
@@ -392,19 +389,12 @@ __global__ void __launch_bounds__(kGnFusedThreads, kGnCtasPerSm) gn_forward_fuse
         ring.get(p);
         if (k >= ring.rows) continue;
         if (run == 0) shift = p[0].pair(0).x;
-        if constexpr (N == 1) {
-          const float x = p[0].pair(0).x, d = x - shift;
-          raw.x += x;
-          sum.x += d;
-          square.x = fmaf(d, d, square.x);
-        } else {
 #pragma unroll
-          for (int j = 0; j < kPairs; ++j) {
-            const float2 d = add2(p[0].pair(j), both(-shift));
-            raw = add2(raw, p[0].pair(j));
-            sum = add2(sum, d);
-            square = fma2(d, d, square);
-          }
+        for (int j = 0; j < kPairs; ++j) {
+          const float2 d = add_of<N>(p[0].pair(j), both(-shift));
+          raw = add_of<N>(raw, p[0].pair(j));
+          sum = add_of<N>(sum, d);
+          square = fma_of<N>(d, d, square);
         }
         if (++run == kRun / N || k == ring.rows - 1) {
           const float count = static_cast<float>(run * N), total = sum.x + sum.y, off = __fdividef(total, count);
@@ -435,15 +425,15 @@ __global__ void __launch_bounds__(kGnFusedThreads, kGnCtasPerSm) gn_forward_fuse
     float2 slope[kPairs], start[kPairs];
 #pragma unroll
     for (int j = 0; j < kPairs; ++j) {
-      slope[j] = mul2(w[j], both(rstd));
-      start[j] = fma2(slope[j], both(-mean), b[j]);
+      slope[j] = mul_of<N>(w[j], both(rstd));
+      start[j] = fma_of<N>(slope[j], both(-mean), b[j]);
     }
     const int rows = open ? ring.rows : 0;
     for (int k = 0; k < part.steps; ++k) {
       P p[1];
       ring.get(p);
 #pragma unroll
-      for (int j = 0; j < kPairs; ++j) p[0].set(j, activate<T, SILU>(fma2(p[0].pair(j), slope[j], start[j])));
+      for (int j = 0; j < kPairs; ++j) p[0].set(j, activate<T, N, SILU>(fma_of<N>(p[0].pair(j), slope[j], start[j])));
       if (k < rows) p[0].store(y);
       y += out_pace;
     }

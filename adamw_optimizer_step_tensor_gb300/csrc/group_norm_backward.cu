@@ -106,13 +106,13 @@ __global__ void __launch_bounds__(kGnThreads, K == 1 ? 3 : 2) gn_backward_small_
       if (live && row0 + k * c.team_rows < rows) {
 #pragma unroll
         for (int i = 0; i < kPairs; ++i) {
-          const float2 xhat = fma2(p[k].pair(i), both(rstd), both(start));
-          const float2 dz = through<T, SILU>(q[k].pair(i), fma2(xhat, w[i], b[i]));
-          col_b[i] = add2(col_b[i], dz);
-          col_w[i] = fma2(dz, xhat, col_w[i]);
+          const float2 xhat = fma_of<N>(p[k].pair(i), both(rstd), both(start));
+          const float2 dz = through<T, N, SILU>(q[k].pair(i), fma_of<N>(xhat, w[i], b[i]));
+          col_b[i] = add_of<N>(col_b[i], dz);
+          col_w[i] = fma_of<N>(dz, xhat, col_w[i]);
           const float2 g = mul2(dz, w[i]);
-          one = add2(one, g);
-          two = fma2(g, xhat, two);
+          one = add_of<N>(one, g);
+          two = fma_of<N>(g, xhat, two);
         }
       }
     const float2 means = mul2(gn_team_sums(N == 1 ? make_float2(one.x, two.x) : make_float2(one.x + one.y, two.x + two.y), c, s_sum, s_group),
@@ -121,8 +121,8 @@ __global__ void __launch_bounds__(kGnThreads, K == 1 ? 3 : 2) gn_backward_small_
       since = 0;
 #pragma unroll
       for (int i = 0; i < kPairs; ++i) {
-        s_column[2 * i][threadIdx.x] = add2(s_column[2 * i][threadIdx.x], col_w[i]);
-        s_column[2 * i + 1][threadIdx.x] = add2(s_column[2 * i + 1][threadIdx.x], col_b[i]);
+        s_column[2 * i][threadIdx.x] = add_of<N>(s_column[2 * i][threadIdx.x], col_w[i]);
+        s_column[2 * i + 1][threadIdx.x] = add_of<N>(s_column[2 * i + 1][threadIdx.x], col_b[i]);
         col_w[i] = col_b[i] = both(0.0f);
       }
     }
@@ -131,9 +131,9 @@ __global__ void __launch_bounds__(kGnThreads, K == 1 ? 3 : 2) gn_backward_small_
       if (live && row0 + k * c.team_rows < rows) {
 #pragma unroll
         for (int i = 0; i < kPairs; ++i) {
-          const float2 xhat = fma2(p[k].pair(i), both(rstd), both(start));
-          const float2 dz = through<T, SILU>(q[k].pair(i), fma2(xhat, w[i], b[i]));
-          p[k].set(i, mul2(both(rstd), fma2(xhat, both(means.y), fma2(dz, w[i], both(means.x)))));
+          const float2 xhat = fma_of<N>(p[k].pair(i), both(rstd), both(start));
+          const float2 dz = through<T, N, SILU>(q[k].pair(i), fma_of<N>(xhat, w[i], b[i]));
+          p[k].set(i, mul_of<N>(both(rstd), fma_of<N>(xhat, both(means.y), fma_of<N>(dz, w[i], both(means.x)))));
         }
         p[k].store(dx + k * c.team_rows * a.out_position);
       }
@@ -146,8 +146,8 @@ __global__ void __launch_bounds__(kGnThreads, K == 1 ? 3 : 2) gn_backward_small_
   let_next_kernel_start();
 #pragma unroll
   for (int i = 0; i < kPairs; ++i) {
-    s_column[2 * i][threadIdx.x] = add2(s_column[2 * i][threadIdx.x], col_w[i]);
-    s_column[2 * i + 1][threadIdx.x] = add2(s_column[2 * i + 1][threadIdx.x], col_b[i]);
+    s_column[2 * i][threadIdx.x] = add_of<N>(s_column[2 * i][threadIdx.x], col_w[i]);
+    s_column[2 * i + 1][threadIdx.x] = add_of<N>(s_column[2 * i + 1][threadIdx.x], col_b[i]);
   }
   gn_columns_out<N>(a, c, at, &s_column[0][0]);
 }
@@ -194,13 +194,13 @@ __global__ void __launch_bounds__(kGnThreads, 3) gn_backward_lanes_kernel(const 
       if (live) {
 #pragma unroll
         for (int i = 0; i < kPairs; ++i) {
-          const float2 xhat = fma2(p[u].pair(i), both(rstd[u]), both(start[u]));
-          const float2 dz = through<T, SILU>(q[u].pair(i), fma2(xhat, w[i], b[i]));
-          col_b[i] = add2(col_b[i], dz);
-          col_w[i] = fma2(dz, xhat, col_w[i]);
+          const float2 xhat = fma_of<N>(p[u].pair(i), both(rstd[u]), both(start[u]));
+          const float2 dz = through<T, N, SILU>(q[u].pair(i), fma_of<N>(xhat, w[i], b[i]));
+          col_b[i] = add_of<N>(col_b[i], dz);
+          col_w[i] = fma_of<N>(dz, xhat, col_w[i]);
           const float2 g = mul2(dz, w[i]);
-          one = add2(one, g);
-          two = fma2(g, xhat, two);
+          one = add_of<N>(one, g);
+          two = fma_of<N>(g, xhat, two);
         }
       }
       t[u] = N == 1 ? make_float2(one.x, two.x) : make_float2(one.x + one.y, two.x + two.y);
@@ -213,8 +213,8 @@ __global__ void __launch_bounds__(kGnThreads, 3) gn_backward_lanes_kernel(const 
       since = 0;
 #pragma unroll
       for (int i = 0; i < kPairs; ++i) {
-        s_column[2 * i][threadIdx.x] = add2(s_column[2 * i][threadIdx.x], col_w[i]);
-        s_column[2 * i + 1][threadIdx.x] = add2(s_column[2 * i + 1][threadIdx.x], col_b[i]);
+        s_column[2 * i][threadIdx.x] = add_of<N>(s_column[2 * i][threadIdx.x], col_w[i]);
+        s_column[2 * i + 1][threadIdx.x] = add_of<N>(s_column[2 * i + 1][threadIdx.x], col_b[i]);
         col_w[i] = col_b[i] = both(0.0f);
       }
     }
@@ -225,9 +225,9 @@ __global__ void __launch_bounds__(kGnThreads, 3) gn_backward_lanes_kernel(const 
       const float2 means = mul2(t[u], both(-inv));
 #pragma unroll
       for (int i = 0; i < kPairs; ++i) {
-        const float2 xhat = fma2(p[u].pair(i), both(rstd[u]), both(start[u]));
-        const float2 dz = through<T, SILU>(q[u].pair(i), fma2(xhat, w[i], b[i]));
-        p[u].set(i, mul2(both(rstd[u]), fma2(xhat, both(means.y), fma2(dz, w[i], both(means.x)))));
+        const float2 xhat = fma_of<N>(p[u].pair(i), both(rstd[u]), both(start[u]));
+        const float2 dz = through<T, N, SILU>(q[u].pair(i), fma_of<N>(xhat, w[i], b[i]));
+        p[u].set(i, mul_of<N>(both(rstd[u]), fma_of<N>(xhat, both(means.y), fma_of<N>(dz, w[i], both(means.x)))));
       }
       p[u].store(static_cast<T*>(a.out) + sample * a.out_sample + at.channel());
     }
@@ -235,8 +235,8 @@ __global__ void __launch_bounds__(kGnThreads, 3) gn_backward_lanes_kernel(const 
   let_next_kernel_start();
 #pragma unroll
   for (int i = 0; i < kPairs; ++i) {
-    s_column[2 * i][threadIdx.x] = add2(s_column[2 * i][threadIdx.x], col_w[i]);
-    s_column[2 * i + 1][threadIdx.x] = add2(s_column[2 * i + 1][threadIdx.x], col_b[i]);
+    s_column[2 * i][threadIdx.x] = add_of<N>(s_column[2 * i][threadIdx.x], col_w[i]);
+    s_column[2 * i + 1][threadIdx.x] = add_of<N>(s_column[2 * i + 1][threadIdx.x], col_b[i]);
   }
   gn_columns_out<N>(a, c, at, &s_column[0][0]);
 }
@@ -316,20 +316,20 @@ __global__ void __launch_bounds__(kGnThreads, 3) gn_backward_cluster_kernel(cons
         const P v = *reinterpret_cast<const P*>(p), g = *reinterpret_cast<const P*>(p + other);
 #pragma unroll
         for (int j = 0; j < kPairs; ++j) {
-          const float2 xhat = fma2(v.pair(j), both(rstd), both(start));
-          const float2 dz = through<T, SILU>(g.pair(j), fma2(xhat, w[j], b[j]));
-          col_b[j] = add2(col_b[j], dz);
-          col_w[j] = fma2(dz, xhat, col_w[j]);
+          const float2 xhat = fma_of<N>(v.pair(j), both(rstd), both(start));
+          const float2 dz = through<T, N, SILU>(g.pair(j), fma_of<N>(xhat, w[j], b[j]));
+          col_b[j] = add_of<N>(col_b[j], dz);
+          col_w[j] = fma_of<N>(dz, xhat, col_w[j]);
         }
       }
     }
     float2 one = both(0.0f), two = both(0.0f);
 #pragma unroll
     for (int j = 0; j < kPairs; ++j) {
-      one = fma2(w[j], col_b[j], one);
-      two = fma2(w[j], col_w[j], two);
-      all_w[j] = add2(all_w[j], col_w[j]);
-      all_b[j] = add2(all_b[j], col_b[j]);
+      one = fma_of<N>(w[j], col_b[j], one);
+      two = fma_of<N>(w[j], col_w[j], two);
+      all_w[j] = add_of<N>(all_w[j], col_w[j]);
+      all_b[j] = add_of<N>(all_b[j], col_b[j]);
     }
     gn_block_sums<N>(c, at, N == 1 ? make_float2(one.x, two.x) : make_float2(one.x + one.y, two.x + two.y), s_sum, s_group);
     // two sets of slots: a CTA may be a sample ahead of one that still reads
@@ -348,9 +348,9 @@ __global__ void __launch_bounds__(kGnThreads, 3) gn_backward_cluster_kernel(cons
       const P g = *reinterpret_cast<const P*>(p + other);
 #pragma unroll
       for (int j = 0; j < kPairs; ++j) {
-        const float2 xhat = fma2(v.pair(j), both(rstd), both(start));
-        const float2 dz = through<T, SILU>(g.pair(j), fma2(xhat, w[j], b[j]));
-        v.set(j, fma2(xhat, both(means.y), fma2(mul2(dz, w[j]), both(rstd), both(means.x))));
+        const float2 xhat = fma_of<N>(v.pair(j), both(rstd), both(start));
+        const float2 dz = through<T, N, SILU>(g.pair(j), fma_of<N>(xhat, w[j], b[j]));
+        v.set(j, fma_of<N>(xhat, both(means.y), fma_of<N>(mul_of<N>(dz, w[j]), both(rstd), both(means.x))));
       }
       v.store(dx);
     }
@@ -398,19 +398,19 @@ __device__ __forceinline__ void gn_backward_items(const GroupNormArgs& a, const 
         ring.get(p);                       // a dy of 0 where there is no row
 #pragma unroll
         for (int j = 0; j < kPairs; ++j) {
-          const float2 xhat = fma2(p[0].pair(j), both(rstd), both(start));
-          const float2 dz = through<T, SILU>(p[1].pair(j), fma2(xhat, w[j], b[j]));
-          col_b[j] = add2(col_b[j], dz);
-          col_w[j] = fma2(dz, xhat, col_w[j]);
+          const float2 xhat = fma_of<N>(p[0].pair(j), both(rstd), both(start));
+          const float2 dz = through<T, N, SILU>(p[1].pair(j), fma_of<N>(xhat, w[j], b[j]));
+          col_b[j] = add_of<N>(col_b[j], dz);
+          col_w[j] = fma_of<N>(dz, xhat, col_w[j]);
         }
       }
       float2 one = both(0.0f), two = both(0.0f);
 #pragma unroll
       for (int j = 0; j < kPairs; ++j) {
-        one = fma2(w[j], col_b[j], one);
-        two = fma2(w[j], col_w[j], two);
-        s_column[2 * j * kGnThreads] = add2(s_column[2 * j * kGnThreads], col_w[j]);
-        s_column[(2 * j + 1) * kGnThreads] = add2(s_column[(2 * j + 1) * kGnThreads], col_b[j]);
+        one = fma_of<N>(w[j], col_b[j], one);
+        two = fma_of<N>(w[j], col_w[j], two);
+        s_column[2 * j * kGnThreads] = add_of<N>(s_column[2 * j * kGnThreads], col_w[j]);
+        s_column[(2 * j + 1) * kGnThreads] = add_of<N>(s_column[(2 * j + 1) * kGnThreads], col_b[j]);
       }
       float2 t = N == 1 ? make_float2(one.x, two.x) : make_float2(one.x + one.y, two.x + two.y);
       if (c.by_lanes)
@@ -430,15 +430,15 @@ __device__ __forceinline__ void gn_backward_items(const GroupNormArgs& a, const 
     const int rows = open ? ring.rows : 0;
     float2 slope[kPairs];
 #pragma unroll
-    for (int j = 0; j < kPairs; ++j) slope[j] = mul2(w[j], both(rstd));
+    for (int j = 0; j < kPairs; ++j) slope[j] = mul_of<N>(w[j], both(rstd));
     for (int k = 0; k < part.steps; ++k) {
       P p[2];
       ring.get(p);
 #pragma unroll
       for (int j = 0; j < kPairs; ++j) {
-        const float2 xhat = fma2(p[0].pair(j), both(rstd), both(start));
-        const float2 dz = through<T, SILU>(p[1].pair(j), fma2(xhat, w[j], b[j]));
-        p[0].set(j, fma2(xhat, both(means.y), fma2(dz, slope[j], both(means.x))));
+        const float2 xhat = fma_of<N>(p[0].pair(j), both(rstd), both(start));
+        const float2 dz = through<T, N, SILU>(p[1].pair(j), fma_of<N>(xhat, w[j], b[j]));
+        p[0].set(j, fma_of<N>(xhat, both(means.y), fma_of<N>(dz, slope[j], both(means.x))));
       }
       if (k < rows) p[0].store(dx);
       dx += out_pace;
