@@ -222,7 +222,7 @@ __device__ __noinline__ void gn_join(const GroupNormArgs& a, const GnCut& c, con
 template <typename T, int N, bool SILU>
 __global__ void __launch_bounds__(kGnThreads, 3) gn_forward_cluster_kernel(const GroupNormArgs a, const GnCut c) {
   using P = GnPiece<T, N>;
-  constexpr int kPairs = gn_pairs<N>();
+  constexpr int kPairs = gn_pairs<N>(), kUnroll = N <= 2 ? 8 : 4, kUnrollOut = N <= 2 ? 4 : 2;
   extern __shared__ uint4 s_tile[];
   __shared__ float2 s_sum[kGnThreads], s_group[kGnTileGroups], s_slots[2][kGnClusterMax][kGnTileGroups];
   __shared__ float s_here[kGnTileGroups];
@@ -242,14 +242,14 @@ __global__ void __launch_bounds__(kGnThreads, 3) gn_forward_cluster_kernel(const
   int turn = 0;
   for (int64_t sample = blockIdx.x / c.cluster; sample < a.samples; sample += gridDim.x / c.cluster) {
     __syncthreads();                    // the sample before is done with
-    gn_fetch(reinterpret_cast<char*>(s_tile),
+    gn_fetch<P::kBytes>(reinterpret_cast<char*>(s_tile),
              reinterpret_cast<const char*>(static_cast<const T*>(a.x) + sample * a.x_sample + first * a.x_position) + at.tile0 * P::kBytes,
              rows, tile_bytes, a.x_position * static_cast<int64_t>(sizeof(T)), c.unit);
     gn_fetched();
     float2 t = both(0.0f);
     if (at.there) {
       const char* p = tile + at.row0 * tile_bytes;
-#pragma unroll 4
+#pragma unroll kUnroll
       for (int l = at.row0; l < rows; l += c.at_once, p += row_bytes) {
         const P v = *reinterpret_cast<const P*>(p);
         float2 of_row = v.pair(0);
@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(kGnThreads, 3) gn_forward_cluster_kernel(const
     t = both(0.0f);
     if (at.there) {
       const char* p = tile + at.row0 * tile_bytes;
-#pragma unroll 4
+#pragma unroll kUnroll
       for (int l = at.row0; l < rows; l += c.at_once, p += row_bytes) {
         const P v = *reinterpret_cast<const P*>(p);
 #pragma unroll
@@ -304,7 +304,7 @@ __global__ void __launch_bounds__(kGnThreads, 3) gn_forward_cluster_kernel(const
     T* y = static_cast<T*>(a.out) + sample * a.out_sample + (first + at.row0) * a.out_position + at.channel();
     const int64_t pace = c.at_once * a.out_position;
     const char* p = tile + at.row0 * tile_bytes;
-#pragma unroll 2
+#pragma unroll kUnrollOut
     for (int l = at.row0; l < rows; l += c.at_once, p += row_bytes, y += pace) {
       P v = *reinterpret_cast<const P*>(p);
 #pragma unroll
@@ -623,11 +623,12 @@ GnCut gn_cut(const GroupNormArgs& a, int piece, int most, int sms) {
   c.parts = static_cast<int32_t>(up(a.positions, c.part_rows));
   c.batch = static_cast<int32_t>(batch);
   c.ctas = c.batch * c.parts;
-  // What it takes: 13 us a batch, or 1.7 times the floor (3 and 5 times with pieces of 4 and 2
-  // bytes), and 8 us for the first statistics and the last results.
+  // What it takes: 13 us a batch, or 1.7 times the floor (3 and 14 times with pieces of 4 and 2
+  // bytes: 300 x 100 x 1000 fp16 in 8 groups, backward, takes 387 us here and 86 by clusters),
+  // and 8 us for the first statistics and the last results.
   const int bytes = piece * a.size;
   const double floor = static_cast<double>(samples) * static_cast<double>(a.positions) * a.channels * a.size * (a.dy != nullptr ? 3 : 2) / 6800.0;
-  const double work = floor * (bytes == 16 ? 1.7 : (bytes == 4 ? 3.0 : 5.0)), turns = 13000.0 * static_cast<double>(up(samples, batch));
+  const double work = floor * (bytes == 16 ? 1.7 : (bytes == 4 ? 3.0 : 14.0)), turns = 13000.0 * static_cast<double>(up(samples, batch));
   const double fused = 8000.0 + (work > turns ? work : turns);
   GnCut k = c;
   if (a.samples > 0 && cut_cluster(&k, a, piece, sms, fused)) {

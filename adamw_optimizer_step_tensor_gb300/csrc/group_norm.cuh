@@ -108,7 +108,7 @@ __device__ __forceinline__ float warp_total(float x) {
 
 // Arithmetic on pairs of elements.  A lone element (N = 1) is the first of its pair; the other
 // half is 0 and takes no instructions (112 x 3589 x 58 bf16 in 2 groups, whose pieces are single
-// elements: forward 125 -> 118 us, backward 311 -> 304).
+// elements: forward 125 us with both halves, 118 without).
 template <int N>
 __device__ __forceinline__ float2 fma_of(float2 x, float2 y, float2 z) {
   if constexpr (N == 1) return make_float2(fmaf(x.x, y.x, z.x), 0.0f);

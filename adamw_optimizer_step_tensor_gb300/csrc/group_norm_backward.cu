@@ -277,7 +277,7 @@ __device__ __noinline__ void gn_join_sums(const GroupNormArgs& a, const GnCut& c
 template <typename T, int N, bool SILU>
 __global__ void __launch_bounds__(kGnThreads, 3) gn_backward_cluster_kernel(const GroupNormArgs a, const GnCut c) {
   using P = GnPiece<T, N>;
-  constexpr int kPairs = gn_pairs<N>();
+  constexpr int kPairs = gn_pairs<N>(), kUnroll = N <= 2 ? 4 : 2;
   extern __shared__ uint4 s_tile[];
   __shared__ float2 s_sum[kGnThreads], s_group[kGnTileGroups], s_slots[2][kGnClusterMax][kGnTileGroups];
   const GnPlace<N> at(c);
@@ -297,9 +297,9 @@ __global__ void __launch_bounds__(kGnThreads, 3) gn_backward_cluster_kernel(cons
   for (int64_t sample = blockIdx.x / c.cluster; sample < a.samples; sample += gridDim.x / c.cluster) {
     __syncthreads();                    // the sample before is done with
     char* to = reinterpret_cast<char*>(s_tile);
-    gn_fetch(to, reinterpret_cast<const char*>(static_cast<const T*>(a.x) + sample * a.x_sample + first * a.x_position) + at.tile0 * P::kBytes,
+    gn_fetch<P::kBytes>(to, reinterpret_cast<const char*>(static_cast<const T*>(a.x) + sample * a.x_sample + first * a.x_position) + at.tile0 * P::kBytes,
              rows, tile_bytes, a.x_position * size, c.unit);
-    gn_fetch(to + other,
+    gn_fetch<P::kBytes>(to + other,
              reinterpret_cast<const char*>(static_cast<const T*>(a.dy) + sample * a.dy_sample + first * a.dy_position) + at.tile0 * P::kBytes,
              rows, tile_bytes, a.dy_position * size, c.unit);
     float rstd = 0.0f, start = 0.0f;
@@ -311,7 +311,7 @@ __global__ void __launch_bounds__(kGnThreads, 3) gn_backward_cluster_kernel(cons
     float2 col_w[kPairs] = {}, col_b[kPairs] = {};
     if (at.there) {
       const char* p = tile + at.row0 * tile_bytes;
-#pragma unroll 2
+#pragma unroll kUnroll
       for (int l = at.row0; l < rows; l += c.at_once, p += row_bytes) {
         const P v = *reinterpret_cast<const P*>(p), g = *reinterpret_cast<const P*>(p + other);
 #pragma unroll
@@ -342,7 +342,7 @@ __global__ void __launch_bounds__(kGnThreads, 3) gn_backward_cluster_kernel(cons
     T* dx = static_cast<T*>(a.out) + sample * a.out_sample + (first + at.row0) * a.out_position + at.channel();
     const int64_t pace = c.at_once * a.out_position;
     const char* p = tile + at.row0 * tile_bytes;
-#pragma unroll 2
+#pragma unroll kUnroll
     for (int l = at.row0; l < rows; l += c.at_once, p += row_bytes, dx += pace) {
       P v = *reinterpret_cast<const P*>(p);
       const P g = *reinterpret_cast<const P*>(p + other);

@@ -18,23 +18,45 @@ constexpr int kGnTileGroups = 64;        // groups of a tile, at most
 constexpr int kGnClusterMax = 8;
 
 // Starts the copies of this CTA's rows of a tile: `rows` rows of tile_bytes bytes, dense in
-// shared memory.  from: the first row's first byte.
+// shared memory.  from: the first row's first byte.  Asynchronous copies are of 4 bytes at least;
+// single 16-bit elements that lie on no such grid (BYTES, of a piece, and unit are 2) come by loads,
+// kAhead of them on their way (112 x 3589 x 58 bf16 in 2 groups: forward 125 us one by one, 69 with
+// 16; backward 633 and 189; with 32 the registers do not suffice).
+template <int BYTES>
 __device__ __forceinline__ void gn_fetch(char* to, const char* from, int rows, int tile_bytes, int64_t row_bytes, int unit) {
   const int per_row = tile_bytes / unit;
   int row = threadIdx.x / per_row, col = threadIdx.x - row * per_row;
   const int row_step = kGnThreads / per_row, col_step = kGnThreads - row_step * per_row;
-  while (row < rows) {
-    const char* src = from + row * row_bytes + col * unit;
-    char* dst = to + row * tile_bytes + col * unit;
-    if (unit == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
-    else if (unit == 4) asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
-    else *reinterpret_cast<uint16_t*>(dst) = *reinterpret_cast<const uint16_t*>(src);
+  const auto next = [&] {
     row += row_step;
     col += col_step;
     if (col >= per_row) {
       col -= per_row;
       ++row;
     }
+  };
+  if constexpr (BYTES == 2) {
+    constexpr int kAhead = 16;
+    while (unit == 2 && row < rows) {
+      uint16_t v[kAhead];
+      int at[kAhead];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        at[u] = row < rows ? row * tile_bytes + col * 2 : -1;
+        if (row < rows) v[u] = __ldg(reinterpret_cast<const uint16_t*>(from + row * row_bytes + col * 2));
+        next();
+      }
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u)
+        if (at[u] >= 0) *reinterpret_cast<uint16_t*>(to + at[u]) = v[u];
+    }
+  }
+  while (row < rows) {
+    const char* src = from + row * row_bytes + col * unit;
+    char* dst = to + row * tile_bytes + col * unit;
+    if (unit == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+    next();
   }
 }
 __device__ __forceinline__ void gn_fetched() {
