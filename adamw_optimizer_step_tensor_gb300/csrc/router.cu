@@ -11,7 +11,8 @@
 // warp several tokens (route_teams_kernel; groups of whole lanes): 5 and 2.5 times fewer
 // instructions a token than with a warp for each (128 and 256 experts), and it is instructions
 // that bound it.  Where 32 lanes of 16 experts do not hold the groups, or the experts, a warp
-// takes a token (route_kernel).
+// takes a token (route_kernel).  65536 x 128 bf16, 8 chosen: 24 us for the choice, 8 for the places,
+// 10 for the gradient.
 //
 // Keys are off by a few units of the scores' last bits and by the bits that the number takes
 // (none that 16-bit logits have).  A choice in which two keys that matter lie closer than that
