@@ -592,7 +592,7 @@ __device__ __noinline__ double exact_key(float z, float b, bool by_logit, bool s
   const double e = exp(softmax ? z - top : -static_cast<double>(z));
   return (softmax ? e / total : 1.0 / (1.0 + e)) + static_cast<double>(b);
 }
-// A team's sum of exponentials in 64 bits.
+// A team's sum of exponentials in 64 bits.  Called by all lanes of a warp together.
 template <typename T, int LANES>
 __device__ __noinline__ double exact_sum(const T* row, int e0, int end, int many, float top) {
   double t = 0.0;
@@ -706,6 +706,9 @@ __global__ void __launch_bounds__(32 * kTeamWarps, 1) route_teams_kernel(const R
     }
     bool sure = bias_max < INFINITY || !live;     // no scale holds an infinite bias
     double total64 = 0.0;                         // once it is needed
+    // The warp's one answer to whether it has been computed.  Its value is none: of a padded row it
+    // is 0, and the lanes that went to compute it again would leave the others at their shuffles.
+    bool have_total = false;
     best = max(best, 1u);                         // 1: none left
     if (by_group) {
       uint32_t one = best, other = second;
@@ -736,7 +739,10 @@ __global__ void __launch_bounds__(32 * kTeamWarps, 1) route_teams_kernel(const R
         sure = sure && (exact ? sizeof(T) == 2 || least >> 5 != most >> 5
                               : static_cast<float>((least >> 5) - (most >> 5)) > 2.0f * off * (summed ? 2.0f : 1.0f));
       if (__any_sync(kFull, !sure)) {
-        if (softmax && scored) total64 = exact_sum<T, LANES>(row, e0, end, V, top);
+        if (softmax && scored) {
+          total64 = exact_sum<T, LANES>(row, e0, end, V, top);
+          have_total = true;
+        }
         // again from the 64-bit keys of each lane's two best, if its third is far enough below
         uint32_t third = 0;
 #pragma unroll
@@ -802,7 +808,7 @@ __global__ void __launch_bounds__(32 * kTeamWarps, 1) route_teams_kernel(const R
     }
     sure = (__ballot_sync(kFull, sure) >> (sub * LANES) & kTeam) == kTeam;      // one answer for the team
     if (__any_sync(kFull, !sure && live)) {
-      if (softmax && bias != nullptr && total64 == 0.0) total64 = exact_sum<T, LANES>(row, e0, end, V, top);
+      if (softmax && bias != nullptr && !have_total) total64 = exact_sum<T, LANES>(row, e0, end, V, top);
       // Again from 64-bit keys: as many best as the team has lanes, each in its lane, if the one
       // after them is far enough below the last chosen.
       const bool by_logit = bias == nullptr || bad, grouped = sure_of_groups;
