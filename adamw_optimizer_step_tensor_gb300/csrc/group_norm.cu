@@ -226,6 +226,7 @@ __global__ void __launch_bounds__(kGnThreads, 3) gn_forward_cluster_kernel(const
   extern __shared__ uint4 s_tile[];
   __shared__ float2 s_sum[kGnThreads], s_group[kGnTileGroups], s_slots[2][kGnClusterMax][kGnTileGroups];
   __shared__ float s_here[kGnTileGroups];
+  gn_started(c.cluster);
   const GnPlace<N> at(c);
   const int rank = c.cluster > 1 ? static_cast<int>(cluster_rank()) : 0;
   const int first = rank * c.part_rows;
@@ -240,12 +241,14 @@ __global__ void __launch_bounds__(kGnThreads, 3) gn_forward_cluster_kernel(const
   const char* tile = reinterpret_cast<const char*>(s_tile) + (threadIdx.x % c.wide) * P::kBytes;
   const int row_bytes = c.at_once * tile_bytes;
   int turn = 0;
+  bool all_started = false;
   for (int64_t sample = blockIdx.x / c.cluster; sample < a.samples; sample += gridDim.x / c.cluster) {
     __syncthreads();                    // the sample before is done with
     gn_fetch<P::kBytes>(reinterpret_cast<char*>(s_tile),
              reinterpret_cast<const char*>(static_cast<const T*>(a.x) + sample * a.x_sample + first * a.x_position) + at.tile0 * P::kBytes,
              rows, tile_bytes, a.x_position * static_cast<int64_t>(sizeof(T)), c.unit);
     gn_fetched();
+    gn_all_started(c.cluster, &all_started);
     float2 t = both(0.0f);
     if (at.there) {
       const char* p = tile + at.row0 * tile_bytes;

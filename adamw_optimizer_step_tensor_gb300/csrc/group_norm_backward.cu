@@ -280,6 +280,7 @@ __global__ void __launch_bounds__(kGnThreads, 3) gn_backward_cluster_kernel(cons
   constexpr int kPairs = gn_pairs<N>(), kUnroll = N <= 2 ? 4 : 2;
   extern __shared__ uint4 s_tile[];
   __shared__ float2 s_sum[kGnThreads], s_group[kGnTileGroups], s_slots[2][kGnClusterMax][kGnTileGroups];
+  gn_started(c.cluster);
   const GnPlace<N> at(c);
   const int rank = c.cluster > 1 ? static_cast<int>(cluster_rank()) : 0;
   const int first = rank * c.part_rows;
@@ -294,6 +295,7 @@ __global__ void __launch_bounds__(kGnThreads, 3) gn_backward_cluster_kernel(cons
   const char* tile = reinterpret_cast<const char*>(s_tile) + (threadIdx.x % c.wide) * P::kBytes;
   const int row_bytes = c.at_once * tile_bytes;
   int turn = 0;
+  bool all_started = false;
   for (int64_t sample = blockIdx.x / c.cluster; sample < a.samples; sample += gridDim.x / c.cluster) {
     __syncthreads();                    // the sample before is done with
     char* to = reinterpret_cast<char*>(s_tile);
@@ -308,6 +310,7 @@ __global__ void __launch_bounds__(kGnThreads, 3) gn_backward_cluster_kernel(cons
       start = -__ldg(a.mean + sample * a.groups + at.group) * rstd;
     }
     gn_fetched();
+    gn_all_started(c.cluster, &all_started);
     float2 col_w[kPairs] = {}, col_b[kPairs] = {};
     if (at.there) {
       const char* p = tile + at.row0 * tile_bytes;

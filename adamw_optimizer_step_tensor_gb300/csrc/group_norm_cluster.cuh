@@ -5,7 +5,8 @@
 // its share of the positions.  The elements are copied to shared memory once, by whatever
 // pieces lie on their grid in memory; statistics and results are computed there by pieces of
 // one group.  Sums go from threads to the CTA and from there to every CTA of the cluster,
-// one exchange per sample.  Several CTAs share an SM, so that one copies while others compute.
+// one exchange per sample; before the first one all CTAs meet, since a CTA that has not started
+// yet has no shared memory to write to.  Several CTAs share an SM, so that one copies while others compute.
 #pragma once
 
 #include "cluster.cuh"
@@ -100,6 +101,15 @@ __device__ __forceinline__ void gn_block_sums(const GnCut& c, const GnPlace<N>& 
   __syncthreads();
 }
 
+// Says that this CTA has started, and waits until all of the cluster have: the one on entry,
+// the other once, before the first exchange, when the first sample's copies have hidden it.
+__device__ __forceinline__ void gn_started(int size) {
+  if (size > 1) cluster_arrive_all();
+}
+__device__ __forceinline__ void gn_all_started(int size, bool* known) {
+  if (size > 1 && !*known) cluster_wait_all();
+  *known = true;
+}
 // Hands this CTA's pairs per group to every CTA of the cluster: slots[rank][group].
 __device__ __forceinline__ void gn_exchange(int size, int rank, int groups, const float2* mine, float2 (*slots)[kGnTileGroups]) {
   for (int i = threadIdx.x; i < groups * size; i += kGnThreads) {
