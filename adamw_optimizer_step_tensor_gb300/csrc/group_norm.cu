@@ -159,6 +159,9 @@ __global__ void __launch_bounds__(kGnThreads, kSmallCtasPerSm) gn_forward_lanes_
   }
 }
 
+// A spread that roundings made negative is 0.  One that is no number stays so (fmaxf would make it 0):
+// a value that is infinite or no number has no spread about any mean.
+__device__ __forceinline__ float gn_spread(float x) { return x < 0.0f ? 0.0f : x; }
 // Joins (count, mean, spread) u to t.
 __device__ __forceinline__ float3 gn_merge_means(float3 t, float3 u) {
   const float all = t.x + u.x, share = __fdividef(u.x, all), d = u.y - t.y;
@@ -286,7 +289,7 @@ __global__ void __launch_bounds__(kGnThreads, 3) gn_forward_cluster_kernel(const
     if (threadIdx.x < at.groups) {
       const float2 v = s_group[threadIdx.x];
       const float d = v.x * mine;
-      s_group[threadIdx.x] = make_float2(s_here[threadIdx.x], fmaxf(fmaf(-d, v.x, v.y), 0.0f));
+      s_group[threadIdx.x] = make_float2(s_here[threadIdx.x], gn_spread(fmaf(-d, v.x, v.y)));
     }
     __syncthreads();
     // two sets of slots: a CTA may be a sample ahead of one that still reads
@@ -401,13 +404,13 @@ __global__ void __launch_bounds__(kGnFusedThreads, kGnCtasPerSm) gn_forward_fuse
         }
         if (++run == kRun / N || k == ring.rows - 1) {
           const float count = static_cast<float>(run * N), total = sum.x + sum.y, off = __fdividef(total, count);
-          t = gn_merge_means(t, make_float3(count, shift + off, fmaxf(fmaf(-off, total, square.x + square.y), 0.0f)));
+          t = gn_merge_means(t, make_float3(count, shift + off, gn_spread(fmaf(-off, total, square.x + square.y))));
           add_exactly(raw.x + raw.y, &whole, &rest);
           run = 0;
           raw = sum = square = both(0.0f);
         }
       }
-      t.y = whole + rest;
+      t.y = fabsf(whole) < INFINITY ? whole + rest : whole;      // the rest of an infinite sum is no number
       if (c.by_lanes)
         for (int o = 1; o < c.group_pieces; o *= 2) t = gn_merge(t, gn_from(t, o));
       float2* s = s_stat[turn.batch % 2];
