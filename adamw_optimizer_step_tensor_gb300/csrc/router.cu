@@ -1136,11 +1136,11 @@ cudaError_t launch_route(adamw_dtype dt, RouteArgs a, int sms, cudaStream_t s) {
   // else a share of every SM's, a third of a turn at least
   const Team team = team_for(a.router);
   const int turn = team.lanes > 0 ? kTeamWarps * (32 / team.lanes) : kRouteWarps;
-  const int64_t most = router_chunks(sms);
-  int64_t chunks = a.tokens <= 2 * turn && a.tokens <= 64 ? 1 : (a.tokens + turn / 3 - 1) / (turn / 3);
+  const int64_t most = router_chunks(sms), tokens = a.tokens;        // near 2^31 a sum leaves 32 bits
+  int64_t chunks = tokens <= 2 * turn && tokens <= 64 ? 1 : (tokens + turn / 3 - 1) / (turn / 3);
   if (chunks > most) chunks = most;
-  a.per_chunk = static_cast<int32_t>((a.tokens + chunks - 1) / chunks);
-  a.chunks = a.per_chunk > 0 ? (a.tokens + a.per_chunk - 1) / a.per_chunk : 1;
+  a.per_chunk = static_cast<int32_t>((tokens + chunks - 1) / chunks);
+  a.chunks = a.per_chunk > 0 ? static_cast<int32_t>((tokens + a.per_chunk - 1) / a.per_chunk) : 1;
   a.pitch = router_pitch(a.router.experts);
   a.per_group = a.router.experts / a.router.groups;
   a.group_factor = ((1 << 20) + a.per_group - 1) / a.per_group;
