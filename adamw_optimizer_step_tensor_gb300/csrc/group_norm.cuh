@@ -397,7 +397,9 @@ __device__ __forceinline__ bool gn_arrive(const GnCut& c, uint32_t* words, uint3
     const uint32_t all = static_cast<uint32_t>(c.parts) * (c.aligned ? 1 : c.tiles);
     last = before + 1 == all * (batch / kGnKept + 1);
   }
-  return __shfl_sync(kFull, static_cast<int>(last), 0) != 0;
+  last = __shfl_sync(kFull, static_cast<int>(last), 0) != 0;
+  __syncwarp();          // what the first lane has acquired the others may read: a shuffle orders no memory
+  return last;
 }
 __device__ __forceinline__ void gn_open(uint32_t* words, uint32_t batch) {
   __syncwarp();
@@ -426,6 +428,7 @@ __device__ __forceinline__ bool gn_wait_open(const GroupNormArgs& a, const uint3
     }
   }
   open = __shfl_sync(kFull, static_cast<int>(open), 0) != 0;
+  __syncwarp();          // as in gn_arrive
   if (!open) *limit_ns = 0;
   return open;
 }
@@ -436,6 +439,7 @@ __device__ __forceinline__ void gn_leave(const GroupNormArgs& a, const GnCut& c)
   if (threadIdx.x == 0) {
     __threadfence();
     last = atomicAdd(a.ticket, 1u) == gridDim.x * gridDim.y - 1;
+    __threadfence();
   }
   if (!__syncthreads_or(last)) return;
   for (int i = threadIdx.x; i < kGnWords * c.batch * (c.aligned ? c.tiles : 1); i += blockDim.x) a.words[i] = 0;
