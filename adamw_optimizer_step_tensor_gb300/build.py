@@ -23,7 +23,7 @@ SOURCES = ["capi.cpp", "qmap.cpp", "step_kernels.cu", "bulk_kernels.cu", "small_
            "aux_kernels.cu", "noalloc.cu", "mini_kernels.cu", "q4_kernels.cu", "operators_capi.cpp",
            "grad_norm.cu", "token_loss.cu", "token_loss_small.cu", "layer_norm.cu",
            "block_capi.cpp", "dropout.cu", "router.cu", "expert_rows.cu", "group_norm.cu",
-           "group_norm_backward.cu"]
+           "group_norm_backward.cu", "group_norm_cut.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

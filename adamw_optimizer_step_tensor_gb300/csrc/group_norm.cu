@@ -1,5 +1,5 @@
-// group_norm.cu -- group norm with an activation over channels-last tensors: how calls
-// are cut up, and the forward pass.
+// group_norm.cu -- group norm with an activation over channels-last tensors: the forward pass
+// (group_norm_cut.cpp: how calls are cut up).
 //
 // Statistics of the fused kernel: a thread sums x - K and its square, K the first of its
 // own values, and starts anew after kRun values.  K is one of the n values it is subtracted
@@ -15,9 +15,6 @@ namespace adamw {
 namespace {
 
 constexpr int kRun = 64;                // values of a run of sums
-constexpr int kGnTiles = 65535;         // of a grid's second axis
-constexpr int kSmallForward = 8;        // pieces a thread of the small kernel holds
-constexpr int kSmallCtasPerSm = 4;      // of the small kernels forward, on which their grid goes; backward 3
 
 template <typename T, int N, bool SILU, int K>
 __global__ void __launch_bounds__(kGnThreads, K == 1 ? kSmallCtasPerSm : 2) gn_forward_small_kernel(const GroupNormArgs a, const GnCut c) {
@@ -449,17 +446,16 @@ __global__ void __launch_bounds__(kGnFusedThreads, kGnCtasPerSm) gn_forward_fuse
 
 template <typename T, int N, bool SILU>
 cudaError_t gn_forward(const GroupNormArgs& a, int sms, cudaStream_t s) {
-  const GnCut c = gn_cut(a, N, kSmallForward, sms);
+  const GnCut c = gn_cut(a, N, sms);
   const dim3 grid(c.ctas, c.tiles);
-  if (c.cluster > 0) return gn_cluster_launch(gn_forward_cluster_kernel<T, N, SILU>, gn_cluster_bytes(a, c, N), s, a, c);
-  if (c.team_rows == 0) {
-    constexpr int kBytes = GnRing<T, N, 1, kForwardDepth>::kBytes;
-    return gn_launch(gn_forward_fused_kernel<T, N, SILU>, grid, kGnFusedThreads, kBytes, s, a, c);
+  switch (gn_kind(a, c)) {
+    case kGnCluster: return gn_cluster_launch(gn_forward_cluster_kernel<T, N, SILU>, gn_cluster_bytes(a, c, N), s, a, c);
+    case kGnFused:
+      return gn_launch(gn_forward_fused_kernel<T, N, SILU>, grid, kGnFusedThreads, GnRing<T, N, 1, kForwardDepth>::kBytes, s, a, c);
+    case kGnLanes: return gn_launch(gn_forward_lanes_kernel<T, N, SILU>, grid, kGnThreads, 0, s, a, c);
+    case kGnRow: return gn_launch(gn_forward_small_kernel<T, N, SILU, 1>, grid, kGnThreads, 0, s, a, c);
+    default: return gn_launch(gn_forward_small_kernel<T, N, SILU, kSmallForward>, grid, kGnThreads, 0, s, a, c);
   }
-  if (a.positions == 1 && c.by_lanes && c.teams == c.at_once)
-    return gn_launch(gn_forward_lanes_kernel<T, N, SILU>, grid, kGnThreads, 0, s, a, c);
-  if (a.positions <= c.team_rows) return gn_launch(gn_forward_small_kernel<T, N, SILU, 1>, grid, kGnThreads, 0, s, a, c);
-  return gn_launch(gn_forward_small_kernel<T, N, SILU, kSmallForward>, grid, kGnThreads, 0, s, a, c);
 }
 template <typename T>
 cudaError_t gn_forward_type(const GroupNormArgs& a, int sms, cudaStream_t s) {
@@ -471,214 +467,7 @@ cudaError_t gn_forward_type(const GroupNormArgs& a, int sms, cudaStream_t s) {
   return a.silu ? gn_forward<T, 1, true>(a, sms, s) : gn_forward<T, 1, false>(a, sms, s);
 }
 
-bool on_grid(const void* p, int64_t sample, int64_t position, const GroupNormArgs& a, int size, int bytes) {
-  return p == nullptr || (reinterpret_cast<uintptr_t>(p) % bytes == 0 && (a.samples < 2 || sample * size % bytes == 0) &&
-                          (a.positions < 2 || position * size % bytes == 0));
-}
-int64_t up(int64_t n, int64_t d) { return (n + d - 1) / d; }
-
-// Tiles of whole groups for the small kernels: as few as may be, but up to three more where
-// narrower ones leave fewer of the 256 threads without a piece (160 pieces: two tiles of 80,
-// three rows at once).  False where a group fits none.
-bool cut_whole(GnCut* c) {
-  const int q = c->group_pieces;
-  if (q > kGnThreads) return false;
-  const int64_t least = up(c->pieces, kGnThreads / q * q);
-  double best = 0.0;
-  for (int64_t t = least; t < least + 4 && t <= c->pieces / q; ++t) {
-    const int64_t wide = up(up(c->pieces, t), q) * q;
-    if (wide > kGnThreads) continue;
-    const int64_t tiles = up(c->pieces, wide);
-    const double use = static_cast<double>(c->pieces) / static_cast<double>(tiles * kGnThreads) * static_cast<double>(kGnThreads / wide);
-    if (use > 1.05 * best) {
-      best = use;
-      c->wide = static_cast<int32_t>(wide);
-      c->tiles = static_cast<int32_t>(tiles);
-    }
-  }
-  c->at_once = kGnThreads / c->wide;
-  return best > 0.0;
-}
-
-// Tiles of the fused kernels, narrow ones of whole groups: at least 256 bytes of a row, and
-// of those the one that leaves the fewest threads and CTAs without work.  At most `most`
-// tiles; where no such tile will do, any 256 pieces.
-void cut_narrow(GnCut* c, int piece_bytes, int64_t most, int ctas) {
-  const int q = c->group_pieces;
-  if (most > ctas) most = ctas;
-  double best = 0.0;
-  for (int wide = q; wide <= kGnThreads; wide += q) {
-    const int64_t tiles = up(c->pieces, wide);
-    if (tiles > most || (wide * piece_bytes < 256 && tiles > 1)) continue;
-    const double use = static_cast<double>(c->pieces) / static_cast<double>(tiles * kGnThreads) * (kGnThreads / wide) *
-                       static_cast<double>(ctas / tiles * tiles) / ctas;
-    if (use > 1.03 * best) {
-      best = use;
-      c->wide = wide;
-      c->tiles = static_cast<int32_t>(tiles);
-    }
-    if (tiles == 1) break;
-  }
-  c->aligned = best > 0.0;
-  if (!c->aligned) {
-    c->wide = c->pieces < kGnThreads ? c->pieces : kGnThreads;
-    c->tiles = static_cast<int32_t>(up(c->pieces, c->wide));
-  }
-  c->at_once = kGnThreads / c->wide;
-}
-
-// Tiles and clusters of the cluster kernels: of all that fit, by a model of the time that was
-// fitted to 146 measured choices of ten calls (its picks are within a quarter of the best).
-// A sample takes 3 us, 0.4 more for each CTA of a cluster, and the larger of its copies
-// (5.5 bytes/ns in all) and its instructions (8 (8 N + 60) per warp, row and tensor for pieces
-// of N), and half the smaller one.  False where nothing fits, or takes more than `limit` ns.
-bool cut_cluster(GnCut* c, const GroupNormArgs& a, int piece, int sms, double limit) {
-  const int q = c->group_pieces, tensors = a.dy != nullptr ? 2 : 1, groups = a.groups;
-  if (q > kGnThreads) return false;
-  double best = 0.0;
-  for (int m = 1; ; m = 2 * m < groups ? 2 * m : groups) {
-    const int wide = m * q;
-    if (wide > kGnThreads || m > kGnTileGroups) break;
-    const int64_t tiles = up(groups, m), tile_bytes = static_cast<int64_t>(wide) * piece * a.size;
-    const int at_once = kGnThreads / wide;
-    for (int cluster = 1; cluster <= kGnClusterMax && tiles <= kGnTiles; cluster *= 2) {
-      const int64_t rows = up(a.positions, cluster), bytes = rows * tile_bytes * tensors;
-      if (bytes > kGnClusterBytes || (cluster > 1 && rows * (cluster - 1) >= a.positions)) continue;
-      int64_t per_sm = (224 << 10) / (bytes + (12 << 10));
-      if (per_sm > 3) per_sm = 3;
-      const double slots = static_cast<double>(per_sm * sms);
-      int64_t clusters = per_sm * sms / cluster / tiles;
-      if (clusters < 1) clusters = 1;
-      if (clusters > a.samples) clusters = a.samples;
-      const double busy = static_cast<double>(clusters * cluster * tiles), waves = busy > slots ? busy / slots : 1.0;
-      const double ctas = busy < slots ? busy : slots, on_sm = ctas > sms ? ctas / sms : 1.0;
-      const double compute = static_cast<double>(up(rows, at_once) * 8 * (8 * piece + 60) * tensors) * on_sm / 7.6;
-      const double copies = static_cast<double>(bytes) * (1.0 + 1.0 / tensors) * ctas / 5500.0;
-      const double time = static_cast<double>(up(a.samples, clusters)) * waves *
-                          (3000.0 + (cluster > 1 ? 400.0 * cluster : 0.0) + (compute > copies ? compute + 0.5 * copies : copies + 0.5 * compute));
-      if (best == 0.0 || time < best) {
-        best = time;
-        c->wide = wide;
-        c->tiles = static_cast<int32_t>(tiles);
-        c->at_once = at_once;
-        c->cluster = cluster;
-        c->part_rows = static_cast<int32_t>(rows);
-        c->ctas = static_cast<int32_t>(clusters * cluster);
-      }
-    }
-    if (m == groups) break;
-  }
-  if (best > limit) best = c->cluster = 0;
-  return best > 0.0;
-}
-
-// Bytes that an item of the fused kernels reads, if there is enough for every CTA: 16 x 4096 x
-// 1024 bf16 forward 159 us with 48 KB, 73 with 96, 66 with 160, 70 with 192 (backward 130, 130,
-// 113, 122): short items leave the waits bare, long ones lose the L2.
-constexpr int64_t kItemBytes = 160 << 10;
-
 }  // namespace
-
-int gn_piece(const GroupNormArgs& a, int size) {
-  const int per = a.channels / a.groups;
-  for (int bytes = 16; bytes > size; bytes = bytes == 16 ? 4 : 0) {
-    const int n = bytes / size;
-    if (per % n == 0 && on_grid(a.x, a.x_sample, a.x_position, a, size, bytes) &&
-        on_grid(a.dy, a.dy_sample, a.dy_position, a, size, bytes) &&
-        on_grid(a.out, a.out_sample, a.out_position, a, size, bytes))
-      return n;
-  }
-  return 1;
-}
-
-GnCut gn_cut(const GroupNormArgs& a, int piece, int most, int sms) {
-  GnCut c{};
-  c.per = a.channels / a.groups;
-  c.pieces = a.channels / piece;
-  c.group_pieces = c.per / piece;
-  const bool lanes = c.group_pieces <= 32 && (c.group_pieces & (c.group_pieces - 1)) == 0;
-  if (cut_whole(&c) && a.positions <= static_cast<int64_t>(most) * c.at_once) {
-    // with samples enough for every CTA's threads, as few threads a sample as hold it;
-    // else as many as it has work for
-    const int64_t resident = static_cast<int64_t>(a.dy != nullptr ? 3 : kSmallCtasPerSm) * sms;
-    const bool many = a.samples * c.tiles >= resident * c.at_once;
-    const int64_t rows = many ? up(a.positions, most) : (a.positions < c.at_once ? a.positions : c.at_once);
-    c.by_lanes = lanes;
-    c.team_rows = static_cast<int32_t>(rows);
-    c.teams = c.at_once / c.team_rows;
-    int64_t ctas = up(a.samples, c.teams), all = resident / c.tiles;
-    if (all < 1) all = 1;
-    c.ctas = static_cast<int32_t>(ctas < all ? ctas : all);
-    return c;
-  }
-  const int64_t samples = a.samples > 0 ? a.samples : 1;
-  const int resident = kGnCtasPerSm * sms;
-  cut_narrow(&c, piece * a.size, resident, resident);
-  c.by_lanes = c.aligned && lanes;
-  // the batch whose parts come closest to an item's bytes, one part for each of a tile's CTAs
-  const int64_t ctas = resident / c.tiles > 0 ? resident / c.tiles : 1;
-  const int64_t row_bytes = static_cast<int64_t>(c.wide) * piece * a.size * (a.dy != nullptr ? 2 : 1);
-  const int64_t rows = kItemBytes / row_bytes > c.at_once ? kItemBytes / row_bytes : c.at_once;
-  int64_t batch = ctas / up(a.positions, rows);
-  if (batch < 1) batch = 1;
-  batch = up(samples, up(samples, batch));        // as many in the last one, or nearly
-  int64_t parts = ctas / batch;
-  const int64_t most_parts = up(a.positions, c.at_once);
-  if (parts > most_parts) parts = most_parts;
-  c.part_rows = static_cast<int32_t>(up(a.positions, parts));
-  c.parts = static_cast<int32_t>(up(a.positions, c.part_rows));
-  c.batch = static_cast<int32_t>(batch);
-  c.ctas = c.batch * c.parts;
-  // What it takes: 13 us a batch, or 1.7 times the floor (3 and 14 times with pieces of 4 and 2
-  // bytes: 300 x 100 x 1000 fp16 in 8 groups, backward, takes 387 us here and 86 by clusters),
-  // and 8 us for the first statistics and the last results.
-  const int bytes = piece * a.size;
-  const double floor = static_cast<double>(samples) * static_cast<double>(a.positions) * a.channels * a.size * (a.dy != nullptr ? 3 : 2) / 6800.0;
-  const double work = floor * (bytes == 16 ? 1.7 : (bytes == 4 ? 3.0 : 14.0)), turns = 13000.0 * static_cast<double>(up(samples, batch));
-  const double fused = 8000.0 + (work > turns ? work : turns);
-  GnCut k = c;
-  if (a.samples > 0 && cut_cluster(&k, a, piece, sms, fused)) {
-    k.by_lanes = lanes;
-    const int64_t step = static_cast<int64_t>(k.wide) * piece * a.size;     // bytes from tile to tile
-    k.unit = a.size;
-    for (int unit : {16, 4}) {
-      if (unit > a.size && step % unit == 0 && static_cast<int64_t>(a.channels) * a.size % unit == 0 &&
-          on_grid(a.x, a.x_sample, a.x_position, a, a.size, unit) && on_grid(a.dy, a.dy_sample, a.dy_position, a, a.size, unit)) {
-        k.unit = unit;
-        break;
-      }
-    }
-    return k;
-  }
-  return c;
-}
-
-int gn_cluster_bytes(const GroupNormArgs& a, const GnCut& c, int piece) {
-  const int bytes = c.part_rows * c.wide * piece * a.size * (a.dy != nullptr ? 2 : 1);
-  // the threads' column sums take the elements' place at the end
-  const int columns = a.dy != nullptr ? 2 * ((piece + 1) / 2) * kGnThreads * static_cast<int>(sizeof(float2)) : 0;
-  return bytes > columns ? bytes : columns;
-}
-
-GroupNormSpace group_norm_space(int32_t channels, int32_t groups, int64_t max_samples, int sms) {
-  GroupNormSpace n{};
-  const int64_t resident = static_cast<int64_t>(kGnCtasPerSm) * sms;
-  n.joined = max_samples * groups * 2;
-  n.words = kGnWords * resident;
-  // of the CTAs of a tile, the most where tiles are widest: fused ones leave statistics, all
-  // leave a row of column sums
-  const int64_t rows = (kSmallCtasPerSm > kGnCtasPerSm ? kSmallCtasPerSm : kGnCtasPerSm) * static_cast<int64_t>(sms);
-  for (int piece : {1, 2, 4, 8}) {
-    if (channels / groups % piece != 0) continue;
-    const int64_t tiles = up(channels / piece, kGnThreads);
-    const int64_t parts = resident / tiles > 1 ? resident / tiles : 1;
-    const int64_t stats = kGnKept * parts * (groups + tiles) * 2;
-    const int64_t ctas = rows / tiles > kGnClusterMax ? rows / tiles : kGnClusterMax;
-    if (stats > n.stats) n.stats = stats;
-    if (2 * ctas * channels > n.columns) n.columns = 2 * ctas * channels;
-  }
-  return n;
-}
 
 template <typename T, int N, bool SILU>
 cudaError_t gn_prepare_one() {

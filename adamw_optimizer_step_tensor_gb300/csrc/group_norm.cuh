@@ -1,5 +1,5 @@
-// group_norm.cuh -- what group norm's forward and backward passes share: how a call is
-// cut up, pieces of channels, the activation, and the order of work of the fused passes.
+// group_norm.cuh -- what group norm's forward and backward passes share: pieces of channels,
+// the activation, and the order of work of the fused passes.
 //
 // A thread keeps one piece of channels (16 bytes, 4 bytes or one element: the widest
 // that lies on its grid in every tensor and inside one group), so its group's statistics
@@ -32,34 +32,13 @@
 
 #include "async_copy.cuh"
 #include "block_ops.h"
+#include "group_norm_cut.h"
 #include "rows.cuh"
 
 namespace adamw {
 
-// How a call is cut up.
-struct GnCut {
-  int32_t pieces, wide, tiles;   // of a row; of a tile; tiles of a row
-  int32_t at_once;               // rows a CTA takes at once
-  int32_t per;                   // channels of a group
-  int32_t group_pieces;          // pieces of a group
-  int32_t by_lanes;              // a group's pieces are a power of two of neighbouring lanes
-  // small kernels
-  int32_t team_rows;             // rows of threads per sample
-  int32_t teams;                 // samples a CTA takes at once
-  // cluster kernels
-  int32_t cluster;               // CTAs that share a sample's tile; 0: other kernels
-  int32_t unit;                  // bytes of a copy
-  // fused kernels
-  int32_t aligned;               // tiles are of whole groups: each of a sample's is open by itself
-  int32_t parts;                 // of a sample
-  int32_t batch;                 // samples of a batch
-  int32_t part_rows;
-  int32_t ctas;                  // per tile; fused kernels: batch x parts
-};
-
 namespace {
 
-constexpr int kGnThreads = 256;
 constexpr int kGnWarps = kGnThreads / 32;
 constexpr int kGnFusedThreads = kGnThreads + 32;
 
@@ -352,11 +331,6 @@ struct GnRing {
   }
 };
 
-// Statistics of parts and means of samples are kept for three batches: a CTA leaves those of
-// batch j + 3 after its results of batch j + 1, whose sample was opened when all parts of
-// batch j had been joined.
-constexpr int kGnKept = 3;
-
 // Partial statistics of a part: group g, or where tiles may begin inside a group g + t for
 // tile t (each such tile adds one, so the places are distinct).
 __device__ __forceinline__ int gn_pitch(const GroupNormArgs& a, const GnCut& c) { return a.groups + (c.aligned ? 0 : c.tiles); }
@@ -382,7 +356,6 @@ struct GnLanes {
 // Words of the CTAs that share a sample (or a tile of one) of each batch: the number that
 // left their statistics, for each of the batches kept, and the batches that are open.  They
 // only grow; the last CTA to leave the kernel clears them.
-constexpr int kGnWords = kGnKept + 1;
 __device__ __forceinline__ uint32_t* gn_words(const GroupNormArgs& a, const GnCut& c, const GnPart& part) {
   return a.words + kGnWords * (c.aligned ? part.sample0 * c.tiles + blockIdx.y : part.sample0);
 }
@@ -490,16 +463,6 @@ __device__ __forceinline__ float2 gn_team_sums(float2 x, const GnCut& c, float2*
 }
 
 }  // namespace
-
-// Cuts a call up (group_norm.cu).  `most`: pieces per thread of the small kernels; 0 rows
-// of threads (team_rows) where the fused ones take it.
-GnCut gn_cut(const GroupNormArgs& a, int piece, int most, int sms);
-// Shared memory of a CTA of the cluster kernels, for its elements.
-int gn_cluster_bytes(const GroupNormArgs& a, const GnCut& c, int piece);
-constexpr int kGnClusterBytes = 208 << 10;   // of them, at most
-constexpr int kGnCtasPerSm = 2;          // of the fused kernels
-// The widest piece of the call, in elements of `size` bytes.
-int gn_piece(const GroupNormArgs& a, int size);
 
 template <typename K>
 cudaError_t gn_launch(K kernel, dim3 grid, int threads, int smem, cudaStream_t s, const GroupNormArgs& a, const GnCut& c) {

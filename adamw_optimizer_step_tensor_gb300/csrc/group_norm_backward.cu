@@ -9,7 +9,6 @@
 namespace adamw {
 namespace {
 
-constexpr int kSmallBackward = 4;       // pieces of x and of dy a thread of the small kernel holds
 constexpr int kFlush = 64;              // samples whose column sums a thread adds up before they join the rest
 
 // The CTA's column sums from its threads': s holds [2 kPairs][kGnThreads] pairs, of the weight
@@ -536,17 +535,16 @@ cudaError_t gn_columns(const GroupNormArgs& a, int rows, cudaStream_t s) {
 
 template <typename T, int N, bool SILU>
 cudaError_t gn_backward(const GroupNormArgs& a, int sms, cudaStream_t s) {
-  const GnCut c = gn_cut(a, N, kSmallBackward, sms);
+  const GnCut c = gn_cut(a, N, sms);
   const dim3 grid(c.ctas, c.tiles);
   if (a.samples > 0) {
+    const GnKind kind = gn_kind(a, c);
     const cudaError_t e =
-        c.cluster > 0 ? gn_cluster_launch(gn_backward_cluster_kernel<T, N, SILU>, gn_cluster_bytes(a, c, N), s, a, c)
-        : c.team_rows == 0 ? gn_launch(gn_backward_fused_kernel<T, N, SILU>, grid, kGnFusedThreads, gn_backward_smem<T, N>(), s, a, c)
-        : a.positions == 1 && c.by_lanes && c.teams == c.at_once
-            ? gn_launch(gn_backward_lanes_kernel<T, N, SILU>, grid, kGnThreads, 0, s, a, c)
-        : a.positions <= c.team_rows
-            ? gn_launch(gn_backward_small_kernel<T, N, SILU, 1>, grid, kGnThreads, 0, s, a, c)
-            : gn_launch(gn_backward_small_kernel<T, N, SILU, kSmallBackward>, grid, kGnThreads, 0, s, a, c);
+        kind == kGnCluster ? gn_cluster_launch(gn_backward_cluster_kernel<T, N, SILU>, gn_cluster_bytes(a, c, N), s, a, c)
+        : kind == kGnFused ? gn_launch(gn_backward_fused_kernel<T, N, SILU>, grid, kGnFusedThreads, gn_backward_smem<T, N>(), s, a, c)
+        : kind == kGnLanes ? gn_launch(gn_backward_lanes_kernel<T, N, SILU>, grid, kGnThreads, 0, s, a, c)
+        : kind == kGnRow   ? gn_launch(gn_backward_small_kernel<T, N, SILU, 1>, grid, kGnThreads, 0, s, a, c)
+                           : gn_launch(gn_backward_small_kernel<T, N, SILU, kSmallBackward>, grid, kGnThreads, 0, s, a, c);
     if (e != cudaSuccess) return e;
   }
   if (a.dweight == nullptr && a.dbias == nullptr) return cudaSuccess;

@@ -15,9 +15,6 @@
 namespace adamw {
 namespace {
 
-constexpr int kGnTileGroups = 64;        // groups of a tile, at most
-constexpr int kGnClusterMax = 8;
-
 // Starts the copies of this CTA's rows of a tile: `rows` rows of tile_bytes bytes, dense in
 // shared memory.  from: the first row's first byte.  Asynchronous copies are of 4 bytes at least;
 // single 16-bit elements that lie on no such grid (BYTES, of a piece, and unit are 2) come by loads,

@@ -1,0 +1,59 @@
+"""CPU: how the group norm's calls are cut up: rules that every cut keeps (its workspace holds what its kernel
+leaves, its CTAs are resident where they wait for one another), and the kernels that the GPU tests' sizes get."""
+
+import ctypes
+import os
+import shutil
+import subprocess
+
+import pytest
+import torch
+
+import test_gpu_group_norm_clusters as clusters
+import test_gpu_group_norm_no_numbers as no_numbers
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+CSRC = os.path.join(ROOT, "adamw_optimizer_step_tensor_gb300", "csrc")
+KINDS = ("lanes", "row", "small", "cluster", "fused")
+SIZE = {torch.float32: 4, torch.float16: 2, torch.bfloat16: 2}
+
+
+class Cut(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("kind", "piece", "tiles", "wide", "cluster", "part_rows", "parts", "batch", "aligned", "ctas")]
+
+
+@pytest.fixture(scope="module")
+def lib(tmp_path_factory):
+    cxx = shutil.which("g++") or shutil.which("c++")
+    inc = next((os.path.join(d, "include") for d in (os.environ.get("CUDA_HOME"), "/usr/local/cuda")
+                if d and os.path.exists(os.path.join(d, "include", "cuda_runtime.h"))), None)
+    if cxx is None or inc is None:
+        pytest.skip("needs a host C++ compiler and the CUDA headers")
+    so = str(tmp_path_factory.mktemp("host") / "cuts.so")
+    subprocess.run([cxx, "-std=c++17", "-O2", "-shared", "-fPIC", "-I", os.path.join(ROOT, "include"), "-I", CSRC, "-I", inc,
+                    os.path.join(CSRC, "group_norm_cut.cpp"), os.path.join(ROOT, "tests", "host", "group_norm_cuts.cpp"), "-o", so], check=True)
+    L = ctypes.CDLL(so)
+    L.group_norm_cut.restype, L.group_norm_cut.argtypes = Cut, [ctypes.c_int64] * 2 + [ctypes.c_int] * 7
+    L.group_norm_check.restype = ctypes.c_int64
+    L.group_norm_check.argtypes = [ctypes.c_uint64, ctypes.c_int64, ctypes.POINTER(ctypes.c_int64), ctypes.c_char_p, ctypes.c_int]
+    return L
+
+
+def cut(lib, shape, groups, size, backward, layout=(0, 0, False)):
+    return lib.group_norm_cut(*shape[:2], shape[2], groups, size, backward, *layout)
+
+
+@pytest.mark.parametrize("seed", range(4))
+def test_every_cut_keeps_the_rules(lib, seed):
+    kinds, why = (ctypes.c_int64 * 5)(), ctypes.create_string_buffer(400)
+    assert lib.group_norm_check(seed, 400_000, kinds, why, 400) == 0, why.value.decode()
+    assert min(kinds) > 10_000                  # of every kernel
+
+
+def test_sizes_of_the_other_tests_reach_every_kernel(lib):
+    kinds = {(KINDS[c.kind], b) for s, g in no_numbers.SHAPES for size in (2, 4) for b in (0, 1) for c in [cut(lib, s, g, size, b)]}
+    assert kinds == {(k, b) for k in KINDS for b in (0, 1)}
+    assert {cut(lib, s, g, size, 0).cluster for s, g in no_numbers.SHAPES for size in (2, 4)} >= {1, 2, 8}
+    for dtype, shapes in clusters.SHAPES.items():
+        got = {(c.cluster, c.piece, b) for s, g in shapes for b in (0, 1) for c in [cut(lib, s, g, SIZE[dtype], b)]}
+        assert got >= {(n, p, b) for n in (2, 4, 8) for p in {torch.float32: (1, 4), torch.bfloat16: (1, 2, 8)}[dtype] for b in (0, 1)}
