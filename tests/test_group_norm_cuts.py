@@ -10,6 +10,7 @@ import pytest
 import torch
 
 import test_gpu_group_norm_clusters as clusters
+import test_gpu_group_norm_layouts as layouts
 import test_gpu_group_norm_no_numbers as no_numbers
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
@@ -48,6 +49,26 @@ def test_every_cut_keeps_the_rules(lib, seed):
     kinds, why = (ctypes.c_int64 * 5)(), ctypes.create_string_buffer(400)
     assert lib.group_norm_check(seed, 400_000, kinds, why, 400) == 0, why.value.decode()
     assert min(kinds) > 10_000                  # of every kernel
+
+
+def test_sizes_of_the_layout_tests_reach_the_kernels_they_name(lib):
+    for shape, groups, names in layouts.CASES:
+        want = iter(names.split())
+        for dtype, size in layouts.DTYPES.items():
+            for backward in (0, 1):
+                name = next(want)
+                for layout in ((0, 0, False), layouts.LAYOUTS["padded"], layouts.LAYOUTS["swapped"], (8, 8, True)):
+                    assert KINDS[cut(lib, shape, groups, size, backward, layout).kind] == name, (shape, dtype, backward, layout)
+    # samples in parts: tiles of whole groups, a group over several tiles, several batches and one
+    fused = [cut(lib, s, g, size, b) for s, g, _ in layouts.CASES for size in (2, 4) for b in (0, 1)]
+    several = [(c.aligned, c.batch < s[0]) for (s, g, _), c in zip([x for x in layouts.CASES for _ in range(4)], fused) if c.kind == 4]
+    assert set(several) == {(1, False), (0, False), (0, True), (1, True)}
+
+
+def test_off_the_grid_a_piece_is_one_element(lib):
+    for shape, groups, _ in layouts.SMALL:
+        kinds = {KINDS[cut(lib, shape, groups, size, b, layouts.LAYOUTS[n]).kind] for size in (2, 4) for b in (0, 1) for n in ("odd", "shifted", "all")}
+        assert kinds <= set(KINDS) and all(cut(lib, shape, groups, 2, b, layouts.LAYOUTS["all"]).piece == 1 for b in (0, 1))
 
 
 def test_sizes_of_the_other_tests_reach_every_kernel(lib):
