@@ -116,7 +116,8 @@ class FusedRouter(_Plan):
 
     score "softmax" or "sigmoid"; with ``groups`` a token's experts are those of its
     ``top_groups`` best groups, by their largest score (group_score "max") or the sum of
-    their two largest ("top2"); ``renormalise``: a token's weights sum to ``scale``.
+    their two largest ("top2"; where one expert of a group is there, that one's);
+    ``renormalise``: a token's weights sum to ``scale``.
     """
 
     _destroy = staticmethod(_capi.adamw_router_plan_destroy)

@@ -702,7 +702,8 @@ adamw_status adamw_router_plan_destroy(adamw_router_plan* plan);
 /*
  * Routes each token by its row of logits z (float32, float16 or bfloat16 [tokens][experts]):
  *     s = softmax(z) or sigmoid(z),   key = s + bias
- *     a group's score = its largest key, or the sum of its two largest
+ *     a group's score = its largest key, or the sum of its two largest (of a group with one
+ *                       expert that is there: that one's key; with none, it is not taken)
  *     ids = the top_k largest keys of the top_groups best groups, largest first
  *     weights = scale * s[ids], or scale * s[ids] / sum of s[ids] (renormalise)
  * Equal keys and groups go to the lowest index; keys are compared as 64-bit values, and
