@@ -194,7 +194,8 @@ class FusedRouter(_Plan):
 
     def dispatch(self, x, slots, *, xs=None, stream=None):
         """xs[slots[t, j]] = x[t]: rows ordered by expert, for the experts' products.  Rows of xs that no
-        slot names are left as they were."""
+        slot names (behind the last assignment, where a token has fewer than top_k) are left as they
+        were, and are 0 in an xs that is made here, which costs a pass over it."""
         if stream is not None:
             with _on(stream):
                 return self.dispatch(x, slots, xs=xs)
@@ -202,7 +203,7 @@ class FusedRouter(_Plan):
         tokens, width = x.shape
         at = self._slots(slots, tokens)
         if xs is None:
-            xs = torch.empty((tokens * self.top_k, width), dtype=x.dtype, device=x.device)
+            xs = torch.zeros((tokens * self.top_k, width), dtype=x.dtype, device=x.device)
         out = _rows("xs", xs, x.dtype, (xs.shape[0], width), self.device)
         _capi.adamw_route_dispatch(self.plan, dtype, tokens, width, x.data_ptr(), stride, at, xs.data_ptr(), xs.shape[0],
                                    out, _stream(None))
@@ -228,7 +229,8 @@ class FusedRouter(_Plan):
 
     def combine_backward(self, dy, ys, slots, weights, *, dys=None, dweights=None, stream=None):
         """(dys, dweights): dys[slots[t, j]] = weights[t, j] dy[t], dweights[t, j] = <dy[t], ys[slots[t, j]]>.
-        dys may be ys."""
+        dys may be ys.  Rows of ys that no slot names have no gradient: those of a given dys are left as
+        they were, and are 0 in one that is made here, which costs a pass over it."""
         if stream is not None:
             with _on(stream):
                 return self.combine_backward(dy, ys, slots, weights, dys=dys, dweights=dweights)
@@ -238,7 +240,7 @@ class FusedRouter(_Plan):
         dy_stride = _rows("dy", dy, ys.dtype, (tokens, width), self.device)
         at = self._slots(slots, tokens)
         if dys is None:
-            dys = torch.empty(ys.shape, dtype=ys.dtype, device=ys.device)
+            dys = torch.zeros(ys.shape, dtype=ys.dtype, device=ys.device)
         if dweights is None:
             dweights = _empty(shape, ys)
         out = _rows("dys", dys, ys.dtype, ys.shape, self.device)
