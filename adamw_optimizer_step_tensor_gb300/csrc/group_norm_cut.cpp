@@ -62,49 +62,26 @@ void cut_narrow(GnCut* c, int piece_bytes, int64_t most, int ctas) {
   c->at_once = kGnThreads / c->wide;
 }
 
-// Tiles and clusters of the cluster kernels: of all that fit, by a model of the time that was
-// fitted to 146 measured choices of ten calls (its picks are within a quarter of the best).
-// A sample takes 3 us, 0.4 more for each CTA of a cluster, and the larger of its copies
-// (5.5 bytes/ns in all) and its instructions (8 (8 N + 60) per warp, row and tensor for pieces
-// of N), and half the smaller one.  False where nothing fits, or takes more than `limit` ns.
+// Tiles and clusters of the cluster kernels: of all that fit, the one that the model likes best.
+// False where nothing fits, or takes more than `limit` ns.
 bool cut_cluster(GnCut* c, const GroupNormArgs& a, int piece, int sms, double limit) {
-  const int q = c->group_pieces, tensors = a.dy != nullptr ? 2 : 1, groups = a.groups;
-  if (q > kGnThreads) return false;
-  double best = 0.0;
-  for (int m = 1; ; m = 2 * m < groups ? 2 * m : groups) {
-    const int wide = m * q;
-    if (wide > kGnThreads || m > kGnTileGroups) break;
-    const int64_t tiles = up(groups, m), tile_bytes = static_cast<int64_t>(wide) * piece * a.size;
-    const int at_once = kGnThreads / wide;
-    for (int cluster = 1; cluster <= kGnClusterMax && tiles <= kGnTiles; cluster *= 2) {
-      const int64_t rows = up(a.positions, cluster), bytes = rows * tile_bytes * tensors;
-      if (bytes > kGnClusterBytes || (cluster > 1 && rows * (cluster - 1) >= a.positions)) continue;
-      int64_t per_sm = (224 << 10) / (bytes + (12 << 10));
-      if (per_sm > 3) per_sm = 3;
-      const double slots = static_cast<double>(per_sm * sms);
-      int64_t clusters = per_sm * sms / cluster / tiles;
-      if (clusters < 1) clusters = 1;
-      if (clusters > a.samples) clusters = a.samples;
-      const double busy = static_cast<double>(clusters * cluster * tiles), waves = busy > slots ? busy / slots : 1.0;
-      const double ctas = busy < slots ? busy : slots, on_sm = ctas > sms ? ctas / sms : 1.0;
-      const double compute = static_cast<double>(up(rows, at_once) * 8 * (8 * piece + 60) * tensors) * on_sm / 7.6;
-      const double copies = static_cast<double>(bytes) * (1.0 + 1.0 / tensors) * ctas / 5500.0;
-      const double time = static_cast<double>(up(a.samples, clusters)) * waves *
-                          (3000.0 + (cluster > 1 ? 400.0 * cluster : 0.0) + (compute > copies ? compute + 0.5 * copies : copies + 0.5 * compute));
-      if (best == 0.0 || time < best) {
-        best = time;
-        c->wide = wide;
-        c->tiles = static_cast<int32_t>(tiles);
-        c->at_once = at_once;
-        c->cluster = cluster;
-        c->part_rows = static_cast<int32_t>(rows);
-        c->ctas = static_cast<int32_t>(clusters * cluster);
+  const int groups = a.groups;
+  GnCut best = *c;
+  double least = 0.0;
+  for (int m = 1; m <= kGnTileGroups && m * c->group_pieces <= kGnThreads; m = 2 * m < groups ? 2 * m : groups) {
+    for (int cluster = 1; cluster <= kGnClusterMax; cluster *= 2) {
+      GnCut k = *c;
+      const double time = gn_cluster_time(a, piece, sms, m, cluster, &k);
+      if (time > 0.0 && (least == 0.0 || time < least)) {
+        least = time;
+        best = k;
       }
     }
     if (m == groups) break;
   }
-  if (best > limit) best = c->cluster = 0;
-  return best > 0.0;
+  if (least == 0.0 || least > limit) return false;
+  *c = best;
+  return true;
 }
 
 // Bytes that an item of the fused kernels reads, if there is enough for every CTA: 16 x 4096 x
@@ -124,6 +101,47 @@ int gn_piece(const GroupNormArgs& a, int size) {
       return n;
   }
   return 1;
+}
+
+// A sample takes 3 us, 0.4 more for each CTA of a cluster, and the larger of its copies
+// (5.5 bytes/ns in all) and its instructions (8 (8 N + 60) per warp, row and tensor for pieces
+// of N), and half the smaller one.  Off by a factor of 1.29 over the 251 choices measured in
+// profiles/group_norm_cuts.md; what it likes best is within a quarter of the best of them (pieces of
+// one 16-bit element backward: within 1.44).
+double gn_cluster_time(const GroupNormArgs& a, int piece, int sms, int m, int cluster, GnCut* c) {
+  const int tensors = a.dy != nullptr ? 2 : 1, wide = m * c->group_pieces;
+  const int64_t tiles = up(a.groups, m), tile_bytes = static_cast<int64_t>(wide) * piece * a.size;
+  const int64_t rows = up(a.positions, cluster), bytes = rows * tile_bytes * tensors;
+  if (wide > kGnThreads || tiles > kGnTiles || bytes > kGnClusterBytes || (cluster > 1 && rows * (cluster - 1) >= a.positions)) return 0.0;
+  const int at_once = kGnThreads / wide;
+  int64_t per_sm = (224 << 10) / (bytes + (12 << 10));
+  if (per_sm > 3) per_sm = 3;
+  const double slots = static_cast<double>(per_sm * sms);
+  int64_t clusters = per_sm * sms / cluster / tiles;
+  if (clusters < 1) clusters = 1;
+  if (clusters > a.samples) clusters = a.samples;
+  const double busy = static_cast<double>(clusters * cluster * tiles), waves = busy > slots ? busy / slots : 1.0;
+  const double ctas = busy < slots ? busy : slots, on_sm = ctas > sms ? ctas / sms : 1.0;
+  const double compute = static_cast<double>(up(rows, at_once) * 8 * (8 * piece + 60) * tensors) * on_sm / 7.6;
+  const double copies = static_cast<double>(bytes) * (1.0 + 1.0 / tensors) * ctas / 5500.0;
+  c->wide = wide;
+  c->tiles = static_cast<int32_t>(tiles);
+  c->at_once = at_once;
+  c->cluster = cluster;
+  c->part_rows = static_cast<int32_t>(rows);
+  c->ctas = static_cast<int32_t>(clusters * cluster);
+  return static_cast<double>(up(a.samples, clusters)) * waves *
+         (3000.0 + (cluster > 1 ? 400.0 * cluster : 0.0) + (compute > copies ? compute + 0.5 * copies : copies + 0.5 * compute));
+}
+
+// 13 us a batch, or 1.7 times the floor (3 and 14 times with pieces of 4 and 2 bytes: 300 x 100 x 1000
+// fp16 in 8 groups, backward, takes 384 us so and 85 by clusters), and 8 us for the first statistics
+// and the last results.
+double gn_parts_time(const GroupNormArgs& a, int piece, const GnCut& c) {
+  const int bytes = piece * a.size;
+  const double floor = static_cast<double>(a.samples) * static_cast<double>(a.positions) * a.channels * a.size * (a.dy != nullptr ? 3 : 2) / 6800.0;
+  const double work = floor * (bytes == 16 ? 1.7 : (bytes == 4 ? 3.0 : 14.0)), turns = 13000.0 * static_cast<double>(up(a.samples, c.batch));
+  return 8000.0 + (work > turns ? work : turns);
 }
 
 GnCut gn_cut(const GroupNormArgs& a, int piece, int sms) {
@@ -165,15 +183,8 @@ GnCut gn_cut(const GroupNormArgs& a, int piece, int sms) {
   c.parts = static_cast<int32_t>(up(a.positions, c.part_rows));
   c.batch = static_cast<int32_t>(batch);
   c.ctas = c.batch * c.parts;
-  // What it takes: 13 us a batch, or 1.7 times the floor (3 and 14 times with pieces of 4 and 2
-  // bytes: 300 x 100 x 1000 fp16 in 8 groups, backward, takes 387 us here and 86 by clusters),
-  // and 8 us for the first statistics and the last results.
-  const int bytes = piece * a.size;
-  const double floor = static_cast<double>(samples) * static_cast<double>(a.positions) * a.channels * a.size * (a.dy != nullptr ? 3 : 2) / 6800.0;
-  const double work = floor * (bytes == 16 ? 1.7 : (bytes == 4 ? 3.0 : 14.0)), turns = 13000.0 * static_cast<double>(up(samples, batch));
-  const double fused = 8000.0 + (work > turns ? work : turns);
   GnCut k = c;
-  if (a.samples > 0 && cut_cluster(&k, a, piece, sms, fused)) {
+  if (a.samples > 0 && cut_cluster(&k, a, piece, sms, gn_parts_time(a, piece, c))) {
     k.by_lanes = lanes;
     const int64_t step = static_cast<int64_t>(k.wide) * piece * a.size;     // bytes from tile to tile
     k.unit = a.size;

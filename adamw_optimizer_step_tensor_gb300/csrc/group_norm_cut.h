@@ -49,6 +49,11 @@ constexpr int kGnWords = kGnKept + 1;
 int gn_piece(const GroupNormArgs& a, int size);
 // Cuts a call up (a.dy: the backward pass) in pieces of `piece` elements.
 GnCut gn_cut(const GroupNormArgs& a, int piece, int sms);
+// The model's time, in ns, of the cluster kernels with `m` groups a tile and `cluster` CTAs a sample,
+// and their cut (c: with its group_pieces); 0 where they do not fit.
+double gn_cluster_time(const GroupNormArgs& a, int piece, int sms, int m, int cluster, GnCut* c);
+// And of the kernels that cut samples into parts, in batches of c.batch.
+double gn_parts_time(const GroupNormArgs& a, int piece, const GnCut& c);
 // What takes a call: lone positions on neighbouring lanes; samples in a CTA's registers, one piece
 // a thread or several; samples in the shared memory of a cluster; parts of samples, read twice.
 enum GnKind { kGnLanes, kGnRow, kGnSmall, kGnCluster, kGnFused };

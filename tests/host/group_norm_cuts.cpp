@@ -87,6 +87,23 @@ Cut group_norm_cut(int64_t samples, int64_t positions, int channels, int groups,
   return {gn_kind(a, c), piece, c.tiles, c.wide, c.cluster, c.part_rows, c.parts, c.batch, c.aligned, c.ctas};
 }
 
+// The model's time in ns of the cluster kernels with m groups a tile and `cluster` CTAs a sample (0: does not fit).
+double group_norm_cluster_ns(int64_t samples, int64_t positions, int channels, int groups, int size, int backward, int m, int cluster) {
+  const GroupNormArgs a = call(samples, positions, channels, groups, size, backward != 0, 0, 0, false);
+  GnCut c{};
+  const int piece = gn_piece(a, size);
+  c.group_pieces = channels / groups / piece;
+  return gn_cluster_time(a, piece, 152, m, cluster, &c);
+}
+
+// And of the kernels for parts of samples, in batches of `batch`.
+double group_norm_parts_ns(int64_t samples, int64_t positions, int channels, int groups, int size, int backward, int batch) {
+  const GroupNormArgs a = call(samples, positions, channels, groups, size, backward != 0, 0, 0, false);
+  GnCut c{};
+  c.batch = batch;
+  return gn_parts_time(a, gn_piece(a, size), c);
+}
+
 // Cuts `n` random calls; returns how many broke a rule, and says which in `why`; `kinds` counts the kernels.
 int64_t group_norm_check(uint64_t seed, int64_t n, int64_t* kinds, char* why, int length) {
   std::mt19937_64 g(seed);

@@ -2,6 +2,7 @@
 leaves, its CTAs are resident where they wait for one another), and the kernels that the GPU tests' sizes get."""
 
 import ctypes
+import math
 import os
 import shutil
 import subprocess
@@ -35,6 +36,8 @@ def lib(tmp_path_factory):
                     os.path.join(CSRC, "group_norm_cut.cpp"), os.path.join(ROOT, "tests", "host", "group_norm_cuts.cpp"), "-o", so], check=True)
     L = ctypes.CDLL(so)
     L.group_norm_cut.restype, L.group_norm_cut.argtypes = Cut, [ctypes.c_int64] * 2 + [ctypes.c_int] * 7
+    L.group_norm_cluster_ns.restype, L.group_norm_cluster_ns.argtypes = ctypes.c_double, [ctypes.c_int64] * 2 + [ctypes.c_int] * 6
+    L.group_norm_parts_ns.restype, L.group_norm_parts_ns.argtypes = ctypes.c_double, [ctypes.c_int64] * 2 + [ctypes.c_int] * 5
     L.group_norm_check.restype = ctypes.c_int64
     L.group_norm_check.argtypes = [ctypes.c_uint64, ctypes.c_int64, ctypes.POINTER(ctypes.c_int64), ctypes.c_char_p, ctypes.c_int]
     return L
@@ -78,3 +81,30 @@ def test_sizes_of_the_other_tests_reach_every_kernel(lib):
     for dtype, shapes in clusters.SHAPES.items():
         got = {(c.cluster, c.piece, b) for s, g in shapes for b in (0, 1) for c in [cut(lib, s, g, SIZE[dtype], b)]}
         assert got >= {(n, p, b) for n in (2, 4, 8) for p in {torch.float32: (1, 4), torch.bfloat16: (1, 2, 8)}[dtype] for b in (0, 1)}
+
+
+def measured():
+    """The choices of profiles/group_norm_cuts.md: (sizes, groups, bytes of an element, backward), us of the
+    kernel for parts, and us of the clusters by (groups a tile, CTAs)."""
+    for line in open(os.path.join(ROOT, "profiles", "group_norm_cuts.md")).read().split("|---|---|---|\n")[1].splitlines():
+        call, parts, choices = line.strip("| ").split(" | ")
+        sizes, groups, kind, way = call.split(", ")
+        size = {"f32": 4, "f16": 2, "bf16": 2}[kind]
+        yield (tuple(map(int, sizes.split(" x "))), int(groups), size, int(way == "bwd")), float(parts), {
+            tuple(map(int, c.split()[0].split(","))): float(c.split()[1]) for c in choices.split("; ")}
+
+
+def test_the_models_are_as_near_to_the_measured_choices_as_they_are_said_to_be(lib):
+    off = []
+    for (shape, groups, size, back), parts, choices in measured():
+        for (m, ctas), us in choices.items():
+            ns = lib.group_norm_cluster_ns(*shape[:2], shape[2], groups, size, back, m, ctas)
+            assert ns > 0, (shape, m, ctas)
+            off.append(math.log(ns / 1e3 / us))
+        c = cut(lib, shape, groups, size, back)
+        model = lib.group_norm_parts_ns(*shape[:2], shape[2], groups, size, back, c.batch) / 1e3
+        assert 0.8 < model / parts < 3, (shape, model, parts)
+        mine = parts if KINDS[c.kind] == "fused" else choices[c.wide * c.piece * groups // shape[2], c.cluster]
+        most = 1.45 if (shape, back) == ((112, 3589, 58), 1) else 1.26
+        assert mine <= most * min(parts, *choices.values()), (shape, mine)
+    assert len(off) == 251 and math.sqrt(sum(x * x for x in off) / len(off)) < 0.26
