@@ -256,7 +256,8 @@ class FusedGroupNorm(_Plan):
 
     [samples, positions, channels], float32, float16 or bfloat16, the channels contiguous and any
     other strides; weight and bias float32 or of the elements' dtype, or None; mean and rstd
-    float32 [samples, groups].  ``max_samples`` samples per call at most.
+    float32 [samples, groups].  ``max_samples`` samples per call at most.  A group whose squared
+    distances from the mean add up to more than float32 holds has rstd 0.
     """
 
     _destroy = staticmethod(_capi.adamw_group_norm_plan_destroy)

@@ -809,7 +809,9 @@ typedef struct {
  *     z = xhat weight + bias,  y = z or z sigmoid(z)
  * weight and bias [channels], float32 or of the elements' dtype (EUNSUPPORTED
  * otherwise), may be NULL (1 and 0).  mean, rstd: float32 [samples][groups].  positions
- * 1 .. 2^31 - 1.  y may be x (same strides).
+ * 1 .. 2^31 - 1.  y may be x (same strides).  An infinite value makes its group's mean
+ * infinite and its rstd and y NaN, a NaN all three.  Sums are float32: a group whose squared
+ * distances from the mean add up to more than its range has rstd 0 (and y = the bias's).
  */
 adamw_status adamw_group_norm_forward(adamw_group_norm_plan* plan, adamw_dtype dtype,
                                       adamw_dtype weight_dtype, int64_t samples, int64_t positions,
