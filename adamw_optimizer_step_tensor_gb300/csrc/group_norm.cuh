@@ -26,7 +26,7 @@
 // do not pause where an item ends or waits.  A ninth warp takes the threads' statistics
 // over, adds them up and does all that concerns other CTAs; the eight go on at once.
 //
-// 16 x 4096 x 1024 bf16 in 32 groups: forward 65 us, backward 110 (a read and a write of each tensor
+// 16 x 4096 x 1024 bf16 in 32 groups: forward 66 us, backward 111 (a read and a write of each tensor
 // take 40 and 59): instructions bound it, and the part of the second read that the L2 has lost.
 #pragma once
 

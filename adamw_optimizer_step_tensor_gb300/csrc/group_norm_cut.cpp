@@ -66,11 +66,10 @@ void cut_narrow(GnCut* c, int piece_bytes, int64_t most, int ctas) {
 // False where nothing fits, or takes more than `limit` ns.
 bool cut_cluster(GnCut* c, const GroupNormArgs& a, int piece, int sms, double limit) {
   const int groups = a.groups;
-  GnCut best = *c;
+  GnCut best = *c, k = *c;
   double least = 0.0;
   for (int m = 1; m <= kGnTileGroups && m * c->group_pieces <= kGnThreads; m = 2 * m < groups ? 2 * m : groups) {
     for (int cluster = 1; cluster <= kGnClusterMax; cluster *= 2) {
-      GnCut k = *c;
       const double time = gn_cluster_time(a, piece, sms, m, cluster, &k);
       if (time > 0.0 && (least == 0.0 || time < least)) {
         least = time;

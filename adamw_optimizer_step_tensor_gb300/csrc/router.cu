@@ -12,7 +12,9 @@
 // instructions a token than with a warp for each (128 and 256 experts), and it is instructions
 // that bound it.  Where 32 lanes of 16 experts do not hold the groups, or the experts, a warp
 // takes a token (route_kernel).  65536 x 128 bf16, 8 chosen: 24 us for the choice, 8 for the places,
-// 10 for the gradient.
+// 10 for the gradient (27 where the whole softmax has one: it reads a row twice).  65536 x 1024: 106
+// us and 37.  All variants of the team kernel spill at the 72 registers that 28 warps leave, 44 to 332
+// bytes a thread, most with 16 experts a lane in teams of 8 and 16.
 //
 // Keys are off by a few units of the scores' last bits and by the bits that the number takes
 // (none that 16-bit logits have).  A choice in which two keys that matter lie closer than that
