@@ -104,9 +104,9 @@ int gn_piece(const GroupNormArgs& a, int size) {
 
 // A sample takes 3 us, 0.4 more for each CTA of a cluster, and the larger of its copies
 // (5.5 bytes/ns in all) and its instructions (8 (8 N + 60) per warp, row and tensor for pieces
-// of N), and half the smaller one.  Off by a factor of 1.29 over the 251 choices measured in
-// profiles/group_norm_cuts.md; what it likes best is within a quarter of the best of them (pieces of
-// one 16-bit element backward: within 1.44).
+// of N), and half the smaller one.  Off by a factor of 1.29 over the 251 choices that were measured
+// (tests/golden/group_norm_cuts.json); the choices taken by it take at most 1.26 times the best one's
+// time (pieces of one 16-bit element backward: 1.44).
 double gn_cluster_time(const GroupNormArgs& a, int piece, int sms, int m, int cluster, GnCut* c) {
   const int tensors = a.dy != nullptr ? 2 : 1, wide = m * c->group_pieces;
   const int64_t tiles = up(a.groups, m), tile_bytes = static_cast<int64_t>(wide) * piece * a.size;

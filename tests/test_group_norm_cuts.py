@@ -2,6 +2,7 @@
 leaves, its CTAs are resident where they wait for one another), and the kernels that the GPU tests' sizes get."""
 
 import ctypes
+import json
 import math
 import os
 import shutil
@@ -84,14 +85,12 @@ def test_sizes_of_the_other_tests_reach_every_kernel(lib):
 
 
 def measured():
-    """The choices of profiles/group_norm_cuts.md: (sizes, groups, bytes of an element, backward), us of the
-    kernel for parts, and us of the clusters by (groups a tile, CTAs)."""
-    for line in open(os.path.join(ROOT, "profiles", "group_norm_cuts.md")).read().split("|---|---|---|\n")[1].splitlines():
-        call, parts, choices = line.strip("| ").split(" | ")
-        sizes, groups, kind, way = call.split(", ")
-        size = {"f32": 4, "f16": 2, "bf16": 2}[kind]
-        yield (tuple(map(int, sizes.split(" x "))), int(groups), size, int(way == "bwd")), float(parts), {
-            tuple(map(int, c.split()[0].split(","))): float(c.split()[1]) for c in choices.split("; ")}
+    """The choices that were measured: (sizes, groups, bytes of an element, backward), us of the kernel for parts,
+    and us of the clusters by (groups a tile, CTAs)."""
+    with open(os.path.join(ROOT, "tests", "golden", "group_norm_cuts.json")) as f:
+        for c in json.load(f)["calls"]:
+            yield (tuple(c["sizes"]), c["groups"], {"f32": 4, "f16": 2, "bf16": 2}[c["type"]], int(c["direction"] == "bwd")), c["parts_us"], {
+                tuple(map(int, k.split(","))): us for k, us in c["clusters_us"].items()}
 
 
 def test_the_models_are_as_near_to_the_measured_choices_as_they_are_said_to_be(lib):
