@@ -12,6 +12,13 @@ pytestmark = pytest.mark.gpu
 STEP = 1 << 27
 
 
+@pytest.fixture(autouse=True)
+def give_the_memory_back():
+    """The library's plans take memory that torch's cache holds otherwise."""
+    yield
+    torch.cuda.empty_cache()
+
+
 def windows(n):
     return [at for at in (0, (1 << 31) - 8, (1 << 32) - 8, (1 << 33) + 4, (1 << 34) - 8, n - 48) if at + 48 <= n]
 

@@ -19,6 +19,13 @@ pytestmark = pytest.mark.gpu
 STEP = 1 << 27
 
 
+@pytest.fixture(autouse=True)
+def give_the_memory_back():
+    """The library's plans take memory that torch's cache holds otherwise."""
+    yield
+    torch.cuda.empty_cache()
+
+
 def test_every_position_of_the_longest_samples():
     n, length = 2, 2 ** 31 - 1
     g = torch.Generator("cuda").manual_seed(31)
